@@ -18,6 +18,11 @@ Entry points mirror the C names::
 and the indexer front end (``include/dsa_front_end.h``)::
 
     dsa_indexer_front_end(prob, d, x, wq, ww, q_idx, w_idx, ws_front, ...)
+
+and dense attention (``include/dsa_dense.h``)::
+
+    dp = DenseProblem.from_tensors(q=..., k=..., v=..., offsets=..., row_offsets=..., row_len=..., ...)
+    dsa_dense_attn(dp, out, lse, alloc_dense_workspace(dp))
 """
 from __future__ import annotations
 
@@ -47,6 +52,7 @@ DSA_INDEXER_DP4A = 1
 DSA_INDEXER_TC = 2
 DSA_FLAG_NO_RELU = 0x100
 DSA_FLAG_KV_FP8 = 0x200
+DSA_FLAG_FP16 = 0x400
 
 INDEXERS = {"auto": DSA_INDEXER_AUTO, "dp4a": DSA_INDEXER_DP4A, "tc": DSA_INDEXER_TC}
 
@@ -58,6 +64,8 @@ EXPORTS = ("dsa_version", "dsa_last_error_string", "dsa_indexer_kind", "dsa_deco
            "dsa_read_device_status", "dsa_get_device_status", "dsa_check_bounds",
            # include/dsa_front_end.h
            "dsa_front_end_workspace_size", "dsa_indexer_front_end",
+           # include/dsa_dense.h
+           "dsa_dense_workspace_size", "dsa_dense_attn",
            # include/dsa_testing.h
            "dsa_test_topk_missing_arrival", "dsa_test_attn_missing_gather",
            "dsa_test_indexer_missing_tile")
@@ -75,6 +83,17 @@ class dsa_problem(ctypes.Structure):
         ("q", ctypes.c_void_p), ("kv", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
         ("row_offsets", ctypes.c_void_p), ("row_len", ctypes.c_void_p),
         ("kv_scale", ctypes.c_void_p),
+    ]
+
+
+class dsa_dense_problem(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int32), ("B", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("D_k", ctypes.c_int32), ("D_v", ctypes.c_int32), ("L_max", ctypes.c_int32), ("rows_max", ctypes.c_int32),
+        ("L_total", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p), ("row_len", ctypes.c_void_p),
     ]
 
 
@@ -105,6 +124,9 @@ def _load() -> ctypes.CDLL:
     lib.dsa_front_end_workspace_size.restype = sz
     lib.dsa_front_end_workspace_size.argtypes = [P, ctypes.c_int32]
     W = ctypes.POINTER(dsa_affine_weights)
+    DP = ctypes.POINTER(dsa_dense_problem)
+    lib.dsa_dense_workspace_size.restype = sz
+    lib.dsa_dense_workspace_size.argtypes = [DP]
     for name, args in (
         ("dsa_index_scores", [P, vp, vp, sz, vp]),
         ("dsa_topk", [P, vp, vp, vp, vp, sz, vp]),
@@ -115,6 +137,7 @@ def _load() -> ctypes.CDLL:
         ("dsa_get_device_status", [vp, vp]),
         ("dsa_check_bounds", [P, ctypes.c_int64, ctypes.c_int64, vp, sz, vp]),
         ("dsa_indexer_front_end", [P, ctypes.c_int32, vp, W, W, vp, vp, vp, vp, vp, vp, sz, vp]),
+        ("dsa_dense_attn", [DP, vp, vp, vp, sz, vp]),
         ("dsa_test_topk_missing_arrival", [P, vp, vp, vp, vp, sz, ctypes.c_int, ctypes.c_int64, vp]),
         ("dsa_test_attn_missing_gather", [P, vp, vp, vp, vp, vp, sz, ctypes.c_int64, vp]),
         ("dsa_test_indexer_missing_tile", [P, vp, vp, sz, ctypes.c_int64, vp]),
@@ -160,10 +183,12 @@ class Problem:
     ``row_len``/``offsets`` (a device read) unless given.
     """
 
+    _struct = dsa_problem
+
     def __init__(self, **kw):
         self._keep = {}
-        s = dsa_problem()
-        for f, _ in dsa_problem._fields_:
+        s = self._struct()
+        for f, _ in self._struct._fields_:
             v = kw.get(f)
             if v is None:
                 continue
@@ -368,3 +393,105 @@ def dsa_indexer_front_end(prob: Problem, d: int, x, wq, ww, q_idx, w_idx, ws, q_
                                       ctypes.byref(ww), _ptr(q_idx), _ptr(w_idx), _ptr(q_scale),
                                       _ptr(w_scale), _ptr(proj), _ptr(ws), ws.numel(),
                                       _stream(stream)))
+
+
+# Dense attention (include/dsa_dense.h).
+
+def _head_tensor(name, t):
+    """(heads, width, token stride) of a [tokens, heads, width] tensor whose heads are packed."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [tokens, heads, width] with packed heads (a token stride is allowed)")
+    return int(t.shape[1]), int(t.shape[2]), int(t.stride(0)) if t.shape[0] > 1 else 0
+
+
+def _fp16_flag(**ts):
+    import torch
+    kinds = {t.dtype for t in ts.values()}
+    if kinds == {torch.bfloat16}:
+        return 0
+    if kinds == {torch.float16}:
+        return DSA_FLAG_FP16
+    raise ValueError(f"{', '.join(ts)} must all be bfloat16 or all float16, got {sorted(map(str, kinds))}")
+
+
+def _on_current_device(prob, *ts):
+    """The call runs on the current CUDA device: every tensor has to be there."""
+    import torch
+    for t in list(prob._keep.values()) + [t for t in ts if t is not None]:
+        if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device")
+
+
+def _check_output(name, t, shape, dtype):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _check_ints(n, **ts):
+    import torch
+    for name, t in ts.items():
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
+                              or (n.get(name) is not None and t.shape[0] != n[name])):
+            raise ValueError(f"{name} must be a contiguous int32 vector"
+                             + (f" of {n[name]} entries" if n.get(name) is not None else ""))
+
+
+class DenseProblem(Problem):
+    """Sizes plus device tensors of one dense attention call (include/dsa_dense.h).
+
+    q [R, H_q, D_k], k [L_total, H_kv, D_k] and v [L_total, H_kv, D_v] are bfloat16 or
+    float16; they may be views with a token stride (slices of a fused projection).
+    ``L_max``, ``L_total`` and ``rows_max`` are host values, read from the device
+    tensors unless given.
+    """
+
+    _struct = dsa_dense_problem
+
+    @classmethod
+    def from_tensors(cls, *, q, k, v, offsets, row_offsets, row_len, softmax_scale, L_max=None, L_total=None,
+                     rows_max=None):
+        H_q, D_k, q_stride = _head_tensor("q", q)
+        H_kv, D, k_stride = _head_tensor("k", k)
+        H_v, D_v, v_stride = _head_tensor("v", v)
+        if D != D_k or H_v != H_kv or k.shape[0] != v.shape[0]:
+            raise ValueError("q and k must have one width, k and v the same tokens and heads")
+        R = int(q.shape[0])
+        B = int(offsets.shape[0]) - 1
+        _check_ints(dict(offsets=B + 1, row_offsets=B + 1, row_len=R), offsets=offsets, row_offsets=row_offsets,
+                    row_len=row_len)
+        if L_max is None:
+            L_max = int(row_len.max().item()) if R else 0
+        if L_total is None:
+            L_total = int(offsets[-1].item())
+        if L_total > k.shape[0]:
+            raise ValueError(f"L_total={L_total} but k and v have {k.shape[0]} tokens")
+        if rows_max is None:
+            rows_max = int((row_offsets[1:] - row_offsets[:-1]).max().item()) if R else 0
+        prob = cls(R=R, B=B, H_q=H_q, H_kv=H_kv, D_k=D_k, D_v=D_v, L_max=int(L_max), rows_max=int(rows_max),
+                   L_total=int(L_total), q_stride=q_stride, k_stride=k_stride, v_stride=v_stride,
+                   softmax_scale=float(softmax_scale), flags=_fp16_flag(q=q, k=k, v=v), q=q, k=k, v=v,
+                   offsets=offsets, row_offsets=row_offsets, row_len=row_len)
+        return prob
+
+
+def dsa_dense_workspace_size(prob: DenseProblem) -> int:
+    n = _lib.dsa_dense_workspace_size(ctypes.byref(prob.c))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, _lib.dsa_last_error_string().decode())
+    return n
+
+
+def alloc_dense_workspace(prob: DenseProblem, device="cuda"):
+    import torch
+    return torch.empty(dsa_dense_workspace_size(prob), dtype=torch.uint8, device=device)
+
+
+def dsa_dense_attn(prob: DenseProblem, out, lse, ws, stream=None) -> None:
+    """out [R, H_q, D_v] in the operands' type; lse [R, H_q] float32 or None."""
+    import torch
+    c = prob.c
+    _check_output("out", out, (c.R, c.H_q, c.D_v), prob._keep["q"].dtype)
+    _check_output("lse", lse, (c.R, c.H_q), torch.float32)
+    _on_current_device(prob, out, lse, ws)
+    _check(_lib.dsa_dense_attn(ctypes.byref(c), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))

@@ -6,6 +6,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "dense.cuh"
 
 namespace dsa {
 namespace {
@@ -143,13 +144,15 @@ dsa_status make_plan(const dsa_problem* p, int need, Plan* pl) {
   return DSA_OK;
 }
 
-dsa_status check_ws(const Plan& pl, void* ws, size_t ws_bytes) {
+dsa_status check_ws(size_t need, void* ws, size_t ws_bytes) {
   if (!ws) return fail(DSA_ERR_INVALID_ARG, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(DSA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  if (ws_bytes < pl.total)
-    return fail(DSA_ERR_INVALID_ARG, "workspace %zu bytes < required %zu", ws_bytes, pl.total);
+  if (ws_bytes < need)
+    return fail(DSA_ERR_INVALID_ARG, "workspace %zu bytes < required %zu", ws_bytes, need);
   return DSA_OK;
 }
+
+dsa_status check_ws(const Plan& pl, void* ws, size_t ws_bytes) { return check_ws(pl.total, ws, ws_bytes); }
 
 dsa_status run_indexer(const dsa_problem& p, const Plan& pl, int32_t* scores, char* ws,
                        cudaStream_t st) {
@@ -426,6 +429,86 @@ dsa_status dsa_indexer_front_end(const dsa_problem* p, int32_t d, const uint16_t
   if (e != cudaSuccess) return cuda_fail(e, "clear workspace");
   e = launch_front_end(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "indexer front end");
+  return DSA_OK;
+}
+
+// ------------------------------------------------------------ dense attention
+
+namespace {
+
+struct DensePlan {
+  DenseShape shape;
+  size_t off_ml, off_part, total;
+};
+
+dsa_status dense_plan(const dsa_dense_problem* p, DensePlan* dp) {
+  if (!p) return fail(DSA_ERR_INVALID_ARG, "problem is NULL");
+  if (p->R < 0 || p->R > 65535) return fail(DSA_ERR_INVALID_ARG, "R=%d outside [0,65535]", p->R);
+  if (p->B < 1 || p->B > kMaxB) return fail(DSA_ERR_UNSUPPORTED, "B=%d outside [1,%d]", p->B, kMaxB);
+  if (p->H_q < 1 || p->H_q > 128) return fail(DSA_ERR_UNSUPPORTED, "H_q=%d outside [1,128]", p->H_q);
+  if (p->H_kv < 1 || p->H_q % p->H_kv)
+    return fail(DSA_ERR_UNSUPPORTED, "H_kv=%d does not divide H_q=%d", p->H_kv, p->H_q);
+  if (!(p->D_k == 64 && p->D_v == 64) && !((p->D_k == 128 || p->D_k == 192) && p->D_v == 128))
+    return fail(DSA_ERR_UNSUPPORTED, "(D_k, D_v)=(%d, %d) not in {(64,64), (128,128), (192,128)}", p->D_k, p->D_v);
+  if (p->L_max < 0) return fail(DSA_ERR_INVALID_ARG, "L_max=%d < 0", p->L_max);
+  if (p->rows_max < 0) return fail(DSA_ERR_INVALID_ARG, "rows_max=%d < 0", p->rows_max);
+  if (p->L_total < 0 || p->L_total >= (int64_t(1) << 31))
+    return fail(DSA_ERR_UNSUPPORTED, "L_total=%lld outside [0,2^31)", (long long)p->L_total);
+  const int64_t pack[3] = {(int64_t)p->H_q * p->D_k, (int64_t)p->H_kv * p->D_k, (int64_t)p->H_kv * p->D_v};
+  const int64_t stride[3] = {p->q_stride, p->k_stride, p->v_stride};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] && (stride[i] < pack[i] || stride[i] % 8 || stride[i] > (int64_t(1) << 31)))
+      return fail(DSA_ERR_INVALID_ARG, "%c_stride=%lld: need a multiple of 8 in [%lld, 2^31], or 0", "qkv"[i],
+                  (long long)stride[i], (long long)pack[i]);
+  if (!(p->softmax_scale > 0.f) || p->softmax_scale > 1e30f)
+    return fail(DSA_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
+  if (p->flags & ~DSA_FLAG_FP16) return fail(DSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
+  dp->shape = dense_shape(*p);
+  size_t off = 256;
+  dp->off_ml = dp->off_part = off;
+  if (dp->shape.splits > 1) {
+    const size_t parts = size_t(p->R) * p->H_q * dp->shape.splits;
+    off = align_up(off + parts * 8, 256);
+    dp->off_part = off;
+    off = align_up(off + parts * p->D_v * 4, 256);
+  }
+  dp->total = off;
+  return DSA_OK;
+}
+
+}  // namespace
+
+size_t dsa_dense_workspace_size(const dsa_dense_problem* p) {
+  g_err.clear();
+  DensePlan dp;
+  return dense_plan(p, &dp) == DSA_OK ? dp.total : 0;
+}
+
+dsa_status dsa_dense_attn(const dsa_dense_problem* p, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                          void* stream) {
+  g_err.clear();
+  DensePlan dp;
+  dsa_status s = dense_plan(p, &dp);
+  if (s != DSA_OK) return s;
+  if ((s = check_ws(dp.total, ws, ws_bytes)) != DSA_OK) return s;
+  if (p->R > 0) {
+    if (!p->offsets || !p->row_offsets || !p->row_len)
+      return fail(DSA_ERR_INVALID_ARG, "offsets/row_offsets/row_len must be set");
+    if (!p->q || !out || (p->L_total > 0 && (!p->k || !p->v)))
+      return fail(DSA_ERR_INVALID_ARG, "q/k/v/out must be set");
+  }
+  if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(out, 16))
+    return fail(DSA_ERR_INVALID_ARG, "q/k/v/out must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(p->offsets, 4) || !aligned(p->row_offsets, 4) || !aligned(p->row_len, 4))
+    return fail(DSA_ERR_INVALID_ARG, "lse/offsets/row_offsets/row_len must be 4-byte aligned");
+  char* w = static_cast<char*>(ws);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  if (e != cudaSuccess) return cuda_fail(e, "clear status");
+  if (p->R == 0) return DSA_OK;
+  e = launch_dense(*p, dp.shape, out, lse, reinterpret_cast<float*>(w + dp.off_part),
+                   reinterpret_cast<float*>(w + dp.off_ml), static_cast<uint32_t*>(ws), st);
+  if (e != cudaSuccess) return cuda_fail(e, "dense attention");
   return DSA_OK;
 }
 
