@@ -23,6 +23,12 @@ and dense attention (``include/dsa_dense.h``)::
 
     dp = DenseProblem.from_tensors(q=..., k=..., v=..., offsets=..., row_offsets=..., row_len=..., ...)
     dsa_dense_attn(dp, out, lse, alloc_dense_workspace(dp))
+
+and linear attention with a decay for each head (``include/dsa_linear.h``)::
+
+    lp = LinearProblem.from_tensors(q=..., k=..., v=..., log_decay=..., row_offsets=..., scale=...)
+    dsa_linear_attn(lp, state_in, state_out, out, alloc_linear_workspace(lp))    # prompts
+    dsa_linear_step(lp, state, state, out, ws)                                   # one token of each request
 """
 from __future__ import annotations
 
@@ -66,6 +72,8 @@ EXPORTS = ("dsa_version", "dsa_last_error_string", "dsa_indexer_kind", "dsa_deco
            "dsa_front_end_workspace_size", "dsa_indexer_front_end",
            # include/dsa_dense.h
            "dsa_dense_workspace_size", "dsa_dense_attn",
+           # include/dsa_linear.h
+           "dsa_linear_workspace_size", "dsa_linear_attn", "dsa_linear_step",
            # include/dsa_testing.h
            "dsa_test_topk_missing_arrival", "dsa_test_attn_missing_gather",
            "dsa_test_indexer_missing_tile")
@@ -94,6 +102,17 @@ class dsa_dense_problem(ctypes.Structure):
         ("v_stride", ctypes.c_int64), ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_int32),
         ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
         ("row_offsets", ctypes.c_void_p), ("row_len", ctypes.c_void_p),
+    ]
+
+
+class dsa_linear_problem(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("D_k", ctypes.c_int32),
+        ("D_v", ctypes.c_int32), ("rows_max", ctypes.c_int32), ("n_states", ctypes.c_int32),
+        ("flags", ctypes.c_int32), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("reserved0", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("log_decay", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p), ("state_idx", ctypes.c_void_p),
     ]
 
 
@@ -127,6 +146,9 @@ def _load() -> ctypes.CDLL:
     DP = ctypes.POINTER(dsa_dense_problem)
     lib.dsa_dense_workspace_size.restype = sz
     lib.dsa_dense_workspace_size.argtypes = [DP]
+    LP = ctypes.POINTER(dsa_linear_problem)
+    lib.dsa_linear_workspace_size.restype = sz
+    lib.dsa_linear_workspace_size.argtypes = [LP]
     for name, args in (
         ("dsa_index_scores", [P, vp, vp, sz, vp]),
         ("dsa_topk", [P, vp, vp, vp, vp, sz, vp]),
@@ -138,6 +160,8 @@ def _load() -> ctypes.CDLL:
         ("dsa_check_bounds", [P, ctypes.c_int64, ctypes.c_int64, vp, sz, vp]),
         ("dsa_indexer_front_end", [P, ctypes.c_int32, vp, W, W, vp, vp, vp, vp, vp, vp, sz, vp]),
         ("dsa_dense_attn", [DP, vp, vp, vp, sz, vp]),
+        ("dsa_linear_attn", [LP, vp, vp, vp, vp, sz, vp]),
+        ("dsa_linear_step", [LP, vp, vp, vp, vp, sz, vp]),
         ("dsa_test_topk_missing_arrival", [P, vp, vp, vp, vp, sz, ctypes.c_int, ctypes.c_int64, vp]),
         ("dsa_test_attn_missing_gather", [P, vp, vp, vp, vp, vp, sz, ctypes.c_int64, vp]),
         ("dsa_test_indexer_missing_tile", [P, vp, vp, sz, ctypes.c_int64, vp]),
@@ -495,3 +519,76 @@ def dsa_dense_attn(prob: DenseProblem, out, lse, ws, stream=None) -> None:
     _check_output("lse", lse, (c.R, c.H_q), torch.float32)
     _on_current_device(prob, out, lse, ws)
     _check(_lib.dsa_dense_attn(ctypes.byref(c), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# Linear attention with a decay for each head (include/dsa_linear.h).
+
+class LinearProblem(Problem):
+    """Sizes plus device tensors of one linear attention call (include/dsa_linear.h).
+
+    q, k [R, H, D_k] and v [R, H, D_v] are bfloat16 or float16 (views with a token
+    stride are fine), log_decay is float32 [H].  ``row_offsets`` is None for
+    dsa_linear_step alone: one token of each request.  ``rows_max`` is a host value,
+    read from ``row_offsets`` unless given; ``n_states`` is the number of places of
+    the state arrays (the requests, unless ``state_idx`` names places).
+    """
+
+    _struct = dsa_linear_problem
+
+    @classmethod
+    def from_tensors(cls, *, q, k, v, log_decay, row_offsets=None, scale, rows_max=None, state_idx=None,
+                     n_states=None):
+        import torch
+        H, D_k, q_stride = _head_tensor("q", q)
+        H_k, D, k_stride = _head_tensor("k", k)
+        H_v, D_v, v_stride = _head_tensor("v", v)
+        if D != D_k or H_k != H or H_v != H or not q.shape[0] == k.shape[0] == v.shape[0]:
+            raise ValueError("q, k and v must have the same tokens and heads, q and k one width")
+        if log_decay.dtype != torch.float32 or tuple(log_decay.shape) != (H,) or not log_decay.is_contiguous():
+            raise ValueError(f"log_decay must be a contiguous float32 vector of {H} entries")
+        R = int(q.shape[0])
+        B = R if row_offsets is None else int(row_offsets.shape[0]) - 1
+        _check_ints(dict(row_offsets=B + 1, state_idx=B), row_offsets=row_offsets, state_idx=state_idx)
+        if rows_max is None:
+            rows_max = 1 if row_offsets is None else int((row_offsets[1:] - row_offsets[:-1]).max().item())
+        if n_states is None:
+            if state_idx is not None:
+                raise ValueError("state_idx needs n_states")
+            n_states = B
+        return cls(R=R, B=B, H=H, D_k=D_k, D_v=D_v, rows_max=int(rows_max), n_states=int(n_states),
+                   flags=_fp16_flag(q=q, k=k, v=v), q_stride=q_stride, k_stride=k_stride, v_stride=v_stride,
+                   scale=float(scale), q=q, k=k, v=v, log_decay=log_decay, row_offsets=row_offsets,
+                   state_idx=state_idx)
+
+
+def dsa_linear_workspace_size(prob: LinearProblem) -> int:
+    n = _lib.dsa_linear_workspace_size(ctypes.byref(prob.c))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, _lib.dsa_last_error_string().decode())
+    return n
+
+
+def alloc_linear_workspace(prob: LinearProblem, device="cuda"):
+    import torch
+    return torch.empty(dsa_linear_workspace_size(prob), dtype=torch.uint8, device=device)
+
+
+def _linear_call(fn, prob, state_in, state_out, out, ws, stream):
+    import torch
+    c = prob.c
+    _check_output("out", out, (c.R, c.H, c.D_v), prob._keep["q"].dtype)
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        _check_output(name, t, (c.n_states, c.H, c.D_k, c.D_v), torch.float32)
+    _on_current_device(prob, state_in, state_out, out, ws)
+    _check(fn(ctypes.byref(c), _ptr(state_in), _ptr(state_out), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def dsa_linear_attn(prob: LinearProblem, state_in, state_out, out, ws, stream=None) -> None:
+    """Prompts.  state_in (None: zeros) and state_out (None: not wanted) are float32
+    [n_states, H, D_k, D_v], and may be one tensor; out [R, H, D_v] in the operands' type."""
+    _linear_call(_lib.dsa_linear_attn, prob, state_in, state_out, out, ws, stream)
+
+
+def dsa_linear_step(prob: LinearProblem, state_in, state_out, out, ws, stream=None) -> None:
+    """One token of each request; arguments as dsa_linear_attn."""
+    _linear_call(_lib.dsa_linear_step, prob, state_in, state_out, out, ws, stream)

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "dense.cuh"
+#include "linear.cuh"
 
 namespace dsa {
 namespace {
@@ -509,6 +510,125 @@ dsa_status dsa_dense_attn(const dsa_dense_problem* p, uint16_t* out, float* lse,
   e = launch_dense(*p, dp.shape, out, lse, reinterpret_cast<float*>(w + dp.off_part),
                    reinterpret_cast<float*>(w + dp.off_ml), static_cast<uint32_t*>(ws), st);
   if (e != cudaSuccess) return cuda_fail(e, "dense attention");
+  return DSA_OK;
+}
+
+// ------------------------------------------------------------ linear attention
+
+namespace {
+
+struct LinearPlan {
+  LinearArgs a;
+  bool split;          // a request may have several segments
+  size_t off_seg, total;
+};
+
+dsa_status linear_plan(const dsa_linear_problem* p, LinearPlan* lp) {
+  if (!p) return fail(DSA_ERR_INVALID_ARG, "problem is NULL");
+  if (p->R < 0) return fail(DSA_ERR_INVALID_ARG, "R=%d < 0", p->R);
+  if (p->B < 1 || p->B > kMaxB) return fail(DSA_ERR_UNSUPPORTED, "B=%d outside [1,%d]", p->B, kMaxB);
+  if (p->H < 1 || p->H > 256) return fail(DSA_ERR_UNSUPPORTED, "H=%d outside [1,256]", p->H);
+  if ((p->D_k != 64 && p->D_k != 128) || (p->D_v != 64 && p->D_v != 128))
+    return fail(DSA_ERR_UNSUPPORTED, "D_k=%d, D_v=%d: each must be 64 or 128", p->D_k, p->D_v);
+  if (p->rows_max < 0) return fail(DSA_ERR_INVALID_ARG, "rows_max=%d < 0", p->rows_max);
+  if (p->n_states < 0) return fail(DSA_ERR_INVALID_ARG, "n_states=%d < 0", p->n_states);
+  const int64_t pack[3] = {(int64_t)p->H * p->D_k, (int64_t)p->H * p->D_k, (int64_t)p->H * p->D_v};
+  const int64_t stride[3] = {p->q_stride, p->k_stride, p->v_stride};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] && (stride[i] < pack[i] || stride[i] % 8 || stride[i] > (int64_t(1) << 31)))
+      return fail(DSA_ERR_INVALID_ARG, "%c_stride=%lld: need a multiple of 8 in [%lld, 2^31], or 0", "qkv"[i],
+                  (long long)stride[i], (long long)pack[i]);
+  if (!(p->scale > -1e30f && p->scale < 1e30f)) return fail(DSA_ERR_INVALID_ARG, "scale must be finite");
+  if (p->flags & ~DSA_FLAG_FP16) return fail(DSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
+  if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16))
+    return fail(DSA_ERR_INVALID_ARG, "q/k/v must be 16-byte aligned");
+  if (!aligned(p->log_decay, 4) || !aligned(p->row_offsets, 4) || !aligned(p->state_idx, 4))
+    return fail(DSA_ERR_INVALID_ARG, "log_decay/row_offsets/state_idx must be 4-byte aligned");
+  LinearArgs& a = lp->a;
+  std::memset(&a, 0, sizeof a);
+  a.q = p->q; a.k = p->k; a.v = p->v;
+  a.log_decay = p->log_decay; a.row_offsets = p->row_offsets; a.state_idx = p->state_idx;
+  a.q_stride = stride[0] ? stride[0] : pack[0];
+  a.k_stride = stride[1] ? stride[1] : pack[1];
+  a.v_stride = stride[2] ? stride[2] : pack[2];
+  a.wait_ns = kDefaultWaitNs;
+  a.R = p->R; a.B = p->B; a.H = p->H; a.D_k = p->D_k; a.D_v = p->D_v; a.n_states = p->n_states;
+  a.scale = p->scale;
+  a.seg_len = linear_seg_len(*p);
+  lp->split = p->R > a.seg_len;
+  const int64_t segs = linear_segs(*p, a.seg_len);
+  if (segs * p->H > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "too many segments (%lld)", (long long)segs);
+  a.segs = (int)segs;
+  size_t off = 256;
+  lp->off_seg = off;
+  if (lp->split) off = align_up(off + size_t(segs) * p->H * p->D_k * p->D_v * 4, 256);
+  lp->total = off;
+  return DSA_OK;
+}
+
+// What both calls check of their buffers.
+dsa_status linear_buffers(const dsa_linear_problem* p, const LinearPlan& lp, const float* state_in,
+                          const float* state_out, const uint16_t* out, void* ws, size_t ws_bytes) {
+  const dsa_status s = check_ws(lp.total, ws, ws_bytes);
+  if (s != DSA_OK) return s;
+  if (!p->log_decay) return fail(DSA_ERR_INVALID_ARG, "log_decay must be set");
+  if (p->R > 0 && (!p->q || !p->k || !p->v || !out)) return fail(DSA_ERR_INVALID_ARG, "q/k/v/out must be set");
+  if (!aligned(out, 16) || !aligned(state_in, 16) || !aligned(state_out, 16))
+    return fail(DSA_ERR_INVALID_ARG, "out/state_in/state_out must be 16-byte aligned");
+  if (state_in && state_out && state_in != state_out) {
+    const char *x = reinterpret_cast<const char*>(state_in), *y = reinterpret_cast<const char*>(state_out);
+    const size_t bytes = size_t(p->n_states) * p->H * p->D_k * p->D_v * 4;
+    if (x < y + bytes && y < x + bytes)
+      return fail(DSA_ERR_INVALID_ARG, "state_in and state_out overlap without being the same");
+  }
+  return DSA_OK;
+}
+
+}  // namespace
+
+size_t dsa_linear_workspace_size(const dsa_linear_problem* p) {
+  g_err.clear();
+  LinearPlan lp;
+  return linear_plan(p, &lp) == DSA_OK ? lp.total : 0;
+}
+
+dsa_status dsa_linear_attn(const dsa_linear_problem* p, const float* state_in, float* state_out, uint16_t* out,
+                           void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  LinearPlan lp;
+  dsa_status s = linear_plan(p, &lp);
+  if (s != DSA_OK) return s;
+  if ((s = linear_buffers(p, lp, state_in, state_out, out, ws, ws_bytes)) != DSA_OK) return s;
+  if (!p->row_offsets) return fail(DSA_ERR_INVALID_ARG, "row_offsets must be set");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  if (e != cudaSuccess) return cuda_fail(e, "clear status");
+  LinearArgs& a = lp.a;
+  a.state_in = state_in; a.state_out = state_out; a.out = out;
+  a.seg_state = reinterpret_cast<float*>(static_cast<char*>(ws) + lp.off_seg);
+  a.status = static_cast<uint32_t*>(ws);
+  e = launch_linear(a, p->flags & DSA_FLAG_FP16, lp.split, st);
+  if (e != cudaSuccess) return cuda_fail(e, "linear attention");
+  return DSA_OK;
+}
+
+dsa_status dsa_linear_step(const dsa_linear_problem* p, const float* state_in, float* state_out, uint16_t* out,
+                           void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  LinearPlan lp;
+  dsa_status s = linear_plan(p, &lp);
+  if (s != DSA_OK) return s;
+  if (p->R != p->B) return fail(DSA_ERR_INVALID_ARG, "R=%d, B=%d: a step has one token of each request", p->R, p->B);
+  if ((s = linear_buffers(p, lp, state_in, state_out, out, ws, ws_bytes)) != DSA_OK) return s;
+  if (!state_out) return fail(DSA_ERR_INVALID_ARG, "state_out must be set");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  if (e != cudaSuccess) return cuda_fail(e, "clear status");
+  LinearArgs& a = lp.a;
+  a.state_in = state_in; a.state_out = state_out; a.out = out;
+  a.status = static_cast<uint32_t*>(ws);
+  e = launch_linear_step(a, p->flags & DSA_FLAG_FP16, st);
+  if (e != cudaSuccess) return cuda_fail(e, "linear attention step");
   return DSA_OK;
 }
 

@@ -1,0 +1,573 @@
+// Linear attention over whole prompts, in chunks of 128 tokens (dsa_linear_attn).
+//
+// Mathematics.  With lambda = e^{ld} the decay of a head, H the state before a
+// chunk of n tokens and i, j tokens of the chunk:
+//
+//   S_ij = q_i . k_j                              128 x 128 x D_k
+//   P_ij = scale * lambda^(i-j) S_ij  (j <= i)
+//   O    = diag(scale * lambda^(i+1)) Q H + P V   two products into one accumulator
+//   H'   = lambda^n H + sum_j lambda^(n-1-j) k_j^T v_j
+//
+// Every power has an exponent >= 0, so nothing overflows whatever the decay.
+//
+// The state stays in fp32 registers, transposed: a thread holds the D_k values of
+// one column of H (one dv).  Per chunk the tensor core adds
+//   dH^T = (V diag(lambda^(n-1-j)))^T K
+// whose A operand the same threads write into tensor memory: the decayed v, split
+// into 16-bit terms that add up to its fp32 value (bf16 three terms, fp16 two after
+// a power-of-two scaling per column), so the state loses nothing to the operands' 8
+// or 11 bits.  Q H reads H rounded to the operands' type, as P V reads P (fp16: each
+// column of H and row of P scaled by a power of two into range).
+//
+// A CTA takes one head of one request, or of one segment of a long request, and
+// walks its chunks.  Warp roles:
+//   warp 0       producer: Q, K, V tiles by TMA, two chunks in flight
+//   warp 1       issues S = Q K^T, O = Q H, O += P V
+//   warp 2       issues dH^T
+//   warp 3       none
+//   warps 4-7    "rows": a thread holds one token's row of S, P and O
+//   warps 8-11   "state": a thread holds one column of H
+//
+// Bound: reading q, k, v and writing out once.  Where requests and heads do not
+// fill the GPU, long requests are split into segments: a first launch computes
+// each segment's own end state (K and V only), then every segment starts from
+// the decayed sum of those before it.
+#include "linear.cuh"
+
+#include <cstring>
+
+#include "tc.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kC = 128;            // tokens of a chunk
+constexpr int kThreads = 384;
+constexpr int kStages = 2;
+
+// Tensor-memory columns.
+constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384;
+
+struct ChunkParams {
+  CUtensorMap tq, tk, tv;
+  LinearArgs a;
+  int state_only;
+};
+
+struct __align__(16) Shared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_ready, qh_ready, h_ready, p_ready, o_ready, o_free, v_ready, v_done, dh_ready, tail, done1, done2;
+  uint32_t tmem;
+  int abort;
+  int req, seg, nseg, first;       // request, its segment, its segments, their first index; req < 0: nothing
+  int t0, n;                       // tokens of the segment
+  int place, scratch;
+  float pw[kC + 4];                // lambda^0 .. lambda^128
+  float cs[2][128];                // fp16: scale of each column of H as Q H read it
+};
+
+template <int DK, int DV>
+__host__ __device__ constexpr uint32_t stage_bytes() {
+  return (2 * (DK / 64) + DV / 64) * kChunkBytes;
+}
+template <int DK, int DV>
+__host__ __device__ constexpr size_t smem_bytes() {
+  return kStages * stage_bytes<DK, DV>() + DV * DK * 2 + sizeof(Shared) + 1024;
+}
+
+// Segment of this CTA (warp 0).
+__device__ void locate(const LinearArgs& a, int idx, Shared* sh, int lane) {
+  if (lane == 0) sh->req = -1;
+  __syncwarp();
+  int run = 0;
+  for (int base = 0; base < a.B && run <= idx; base += 32) {
+    const int b = base + lane;
+    int t0 = 0, n = 0, v = 0;
+    if (b < a.B) {
+      const int x0 = a.row_offsets[b], x1 = a.row_offsets[b + 1];
+      t0 = min(max(x0, 0), a.R);
+      n = max(min(x1, a.R) - t0, 0);
+      v = n > a.seg_len ? (n - 1) / a.seg_len + 1 : 1;
+    }
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int first = run + incl - v;
+    if (idx >= first && idx < first + v) {
+      const int s = idx - first;
+      const int skip = s * a.seg_len;   // (below n)
+      sh->req = b;
+      sh->seg = s;
+      sh->nseg = v;
+      sh->first = first;
+      sh->t0 = t0 + skip;
+      sh->n = v == 1 ? n : min(n - skip, a.seg_len);
+    }
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// The two values of a packed pair, widened.
+template <bool F16>
+__device__ __forceinline__ float2 widen(uint32_t p) {
+  if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&p));
+  return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+}
+
+// The power of two that takes m >= 0 into [2^14, 2^15), and its inverse: values of
+// which m is the largest then fit fp16, and only those below 2^-28 of it lose
+// precision (fp16 is normal from 2^-14 on).  1 where m is 0, tiny or not finite.
+__device__ __forceinline__ float half_range(float m, float* back) {
+  const uint32_t e = (__float_as_uint(m) >> 23) & 255u;
+  if (e < 32 || e > 252) {
+    *back = 1.f;
+    return 1.f;
+  }
+  *back = __uint_as_float((e - 14) << 23);
+  return __uint_as_float((268u - e) << 23);
+}
+
+template <int DK, int DV, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr int KC = DK / 64, VC = DV / 64;
+  constexpr uint32_t kStage = stage_bytes<DK, DV>();
+  constexpr int kTerms = F16 ? 2 : 3;
+  const LinearArgs& a = p.a;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned char* Hb = smem + kStages * kStage;     // H in the operands' type, D_v rows of D_k, K-major
+  Shared* sh = reinterpret_cast<Shared*>(Hb + DV * DK * 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x % a.H;
+
+  if (warp == 0) locate(a, blockIdx.x / a.H, sh, lane);
+  __syncthreads();
+  if (sh->req < 0) return;
+  if (p.state_only && sh->seg >= sh->nseg - 1) return;   // (no segment follows)
+  const int place = state_place(a, sh->req, &sh->scratch, h == 0 && sh->seg == 0);
+  if (place < 0) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sh->full[i]), 1);
+      mbar_init(smem_u32(&sh->empty[i]), p.state_only ? 1 : 2);
+    }
+    mbar_init(smem_u32(&sh->s_ready), 1);
+    mbar_init(smem_u32(&sh->qh_ready), 1);
+    mbar_init(smem_u32(&sh->h_ready), 4);
+    mbar_init(smem_u32(&sh->p_ready), 4);
+    mbar_init(smem_u32(&sh->o_ready), 1);
+    mbar_init(smem_u32(&sh->o_free), 4);
+    mbar_init(smem_u32(&sh->v_ready), 4);
+    mbar_init(smem_u32(&sh->v_done), 1);
+    mbar_init(smem_u32(&sh->dh_ready), 1);
+    mbar_init(smem_u32(&sh->tail), 4);
+    mbar_init(smem_u32(&sh->done1), 1);
+    mbar_init(smem_u32(&sh->done2), 1);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) tmem_alloc(smem_u32(&sh->tmem), 512);
+  const float ld2 = log2_decay(a.log_decay[h]);
+  for (int i = tid; i <= kC; i += kThreads) sh->pw[i] = exp2f(ld2 * (float)i);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  const WaitCtx wc{&sh->abort, a.status, a.wait_ns};
+
+  const int n = sh->n, t0 = sh->t0, seg = sh->seg, nseg = sh->nseg;
+  const int chunks = (n + kC - 1) / kC;
+  const int last_n = n - (chunks - 1) * kC;               // tokens of the last chunk
+  const bool ragged = chunks > 0 && last_n < kC;
+  const bool final_state = p.state_only || (seg == nseg - 1 && a.state_out);
+  const int deltas = final_state ? chunks : chunks - 1;   // chunks whose dH is needed
+  auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  auto stage = [&](int c) { return smem + (c % kStages) * kStage; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int c = 0;
+      for (; c < chunks; ++c) {
+        const int s = c % kStages;
+        if (c >= kStages && !wait_bar(bar(sh->empty[s]), (c / kStages - 1) & 1, wc)) break;
+        const uint32_t b = bar(sh->full[s]), dst = smem_u32(stage(c));
+        const int y = t0 + c * kC;
+        mbar_expect_tx(b, p.state_only ? (KC + VC) * kChunkBytes : kStage);
+        if (!p.state_only)
+          for (int x = 0; x < KC; ++x) tma_load_2d(dst + x * kChunkBytes, &p.tq, h * DK + x * 64, y, b);
+        for (int x = 0; x < KC; ++x) tma_load_2d(dst + (KC + x) * kChunkBytes, &p.tk, h * DK + x * 64, y, b);
+        for (int x = 0; x < VC; ++x) tma_load_2d(dst + (2 * KC + x) * kChunkBytes, &p.tv, h * DV + x * 64, y, b);
+      }
+      for (int i = max(0, c - kStages); i < c; ++i)   // (an abort may leave copies in flight)
+        drain_bar(bar(sh->full[i % kStages]), (i / kStages) & 1, a.wait_ns);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S, Q H, P V
+    if (!p.state_only) {
+      const uint32_t id_s = idesc_16(F16, kC, kC, false, false);
+      const uint32_t id_h = idesc_16(F16, kC, DV, false, false);
+      const uint32_t id_o = idesc_16(F16, kC, DV, false, true);
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t q = smem_u32(stage(c)), k = q + KC * kChunkBytes, v = k + KC * kChunkBytes;
+        if (!wait_bar_warp(bar(sh->full[c % kStages]), (c / kStages) & 1, wc)) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int x = 0; x < KC * 4; ++x) {
+            const uint32_t at = (x >> 2) * kChunkBytes + (x & 3) * 32;
+            mma_ss(tmem + kColS, desc_kmajor(q + at), desc_kmajor(k + at), id_s, x);
+          }
+          mma_commit(bar(sh->s_ready));
+        }
+        if (!wait_bar_warp(bar(sh->h_ready), c & 1, wc)) break;
+        if (c > 0 && !wait_bar_warp(bar(sh->o_free), (c - 1) & 1, wc)) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int x = 0; x < KC * 4; ++x)
+            mma_ss(tmem + kColO, desc_kmajor(q + (x >> 2) * kChunkBytes + (x & 3) * 32),
+                   desc_kmajor(smem_u32(Hb) + (x >> 2) * (DV * 128) + (x & 3) * 32), id_h, x);
+          mma_commit(bar(sh->qh_ready));
+        }
+        if (ragged && c == chunks - 1 && !wait_bar_warp(bar(sh->tail), 0, wc)) break;
+        if (!wait_bar_warp(bar(sh->p_ready), c & 1, wc)) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            mma_ts(tmem + kColO, tmem + kColS + x * 8, desc_mnmajor(v + x * 2048, kChunkBytes), id_o, 1);
+          mma_commit(bar(sh->o_ready));
+          mma_commit(bar(sh->empty[c % kStages]));
+        }
+      }
+      if (lane == 0 && chunks > 0) {
+        mma_commit(bar(sh->done1));
+        drain_bar(bar(sh->done1), 0, a.wait_ns);
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ dH^T
+    const uint32_t id_d = idesc_16(F16, kC, DK, false, true);
+    for (int c = 0; c < deltas; ++c) {
+      const uint32_t k = smem_u32(stage(c)) + KC * kChunkBytes;
+      bool ok = true;
+      for (int half = 0; half < 2 && ok; ++half) {
+        ok = wait_bar_warp(bar(sh->v_ready), half, wc);   // (two phases per chunk)
+        if (ok && half == 0) ok = wait_bar_warp(bar(sh->full[c % kStages]), (c / kStages) & 1, wc);
+        if (ok && half == 0 && ragged && c == chunks - 1) ok = wait_bar_warp(bar(sh->tail), 0, wc);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              mma_ts(tmem + kColH, tmem + kColV + t * 32 + x * 8, desc_mnmajor(k + (half * 4 + x) * 2048, kChunkBytes),
+                     id_d, half | t | x);
+          mma_commit(half ? bar(sh->dh_ready) : bar(sh->v_done));
+          if (half) mma_commit(bar(sh->empty[c % kStages]));
+        }
+      }
+      if (!ok) break;
+    }
+    if (lane == 0 && deltas > 0) {
+      mma_commit(bar(sh->done2));
+      drain_bar(bar(sh->done2), 0, a.wait_ns);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ rows
+    const int quad = warp & 3, i = quad * 32 + lane;   // token of the chunk
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const float reach = sh->pw[i + 1] * a.scale;
+    if (!p.state_only) {
+      for (int c = 0; c < chunks; ++c) {
+        if (!wait_bar_warp(bar(sh->s_ready), c & 1, wc)) break;
+        tc_fence_after();
+        float pf = 1.f, pback = 1.f;       // fp16: the row of P brought into its range
+        if (F16) {
+          float mx = 0.f;
+          for (int x = 0; x <= quad; ++x) {
+            uint32_t s[32];
+            tmem_ld32(lanes + kColS + x * 32, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (x * 32 + y <= i) mx = fmaxf(mx, fabsf(__uint_as_float(s[y])));
+          }
+          pf = half_range(mx * a.scale, &pback);
+        }
+        const float ps = a.scale * pf;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {      // P overwrites S behind the columns already read
+          uint32_t s[32];
+          if (x <= quad) {
+            tmem_ld32(lanes + kColS + x * 32, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              const int d = i - (x * 32 + y);
+              const float p0 = d >= 0 ? __uint_as_float(s[y]) * ps * ex2(ld2 * (float)d) : 0.f;
+              const float p1 = d >= 1 ? __uint_as_float(s[y + 1]) * ps * ex2(ld2 * (float)(d - 1)) : 0.f;
+              s[y >> 1] = pack16<F16>(p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) s[y] = 0;
+          }
+          tmem_st16(lanes + kColS + x * 16, s);
+        }
+        if (!wait_bar_warp(bar(sh->qh_ready), c & 1, wc)) break;
+        tc_fence_after();
+        const float f = reach * pf;
+#pragma unroll
+        for (int x = 0; x < DV; x += 32) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kColO + x, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            o[y] = __float_as_uint(__uint_as_float(o[y]) * (F16 ? f * sh->cs[c & 1][x + y] : f));
+          tmem_st32(lanes + kColO + x, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->p_ready));
+        if (!wait_bar_warp(bar(sh->o_ready), c & 1, wc)) break;
+        tc_fence_after();
+        const bool mine = c * kC + i < n;
+        uint16_t* dst = a.out + ((int64_t)(t0 + c * kC + i) * a.H + h) * DV;
+#pragma unroll
+        for (int x = 0; x < DV; x += 32) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kColO + x, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 32; y += 2)
+            o[y >> 1] = pack16<F16>(__uint_as_float(o[y]) * pback, __uint_as_float(o[y + 1]) * pback);
+          if (mine) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              reinterpret_cast<uint4*>(dst + x)[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->o_free));
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ state
+    const int quad = warp & 3, d = quad * 32 + lane;   // column of H
+    const bool live = d < DV;                          // (a whole warp)
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int64_t head = (int64_t)DK * DV;
+    float H[DK];
+#pragma unroll
+    for (int x = 0; x < DK; ++x) H[x] = 0.f;
+    auto load = [&](const float* src) {
+#pragma unroll
+      for (int x = 0; x < DK; ++x) H[x] = src[x * DV + d];
+    };
+    auto store = [&](float* dst) {
+#pragma unroll
+      for (int x = 0; x < DK; ++x) dst[x * DV + d] = H[x];
+    };
+    float* ends = a.seg_state + ((int64_t)sh->first * a.H + h) * head;   // [segment] of this request, H heads apart
+    if (live) {
+      if (seg == 0) {
+        if (nseg > 1 && !p.state_only)
+          load(ends + (int64_t)(nseg - 1) * a.H * head);   // the first launch's copy: state_out may be state_in
+        else if (a.state_in)
+          load(a.state_in + ((int64_t)place * a.H + h) * head);
+        if (p.state_only) store(ends + (int64_t)(nseg - 1) * a.H * head);
+      } else if (!p.state_only) {
+        // lambda^(seg_len (seg - 1 - s)) E_s summed over the segments s before this one.
+        const float f = exp2f(fmaxf(ld2 * (float)a.seg_len, -300.f));
+        load(ends);
+        for (int s = 1; s < seg; ++s) {
+          const float* e = ends + (int64_t)s * a.H * head;
+#pragma unroll
+          for (int x = 0; x < DK; ++x) H[x] = fmaf(f, H[x], e[x * DV + d]);
+        }
+      }
+    }
+    bool ok = true;
+    for (int c = 0; c < chunks && ok; ++c) {
+      if (!p.state_only) {
+        // H in the operands' type, once Q H of the chunk before has read the last one.
+        if (c > 0 && !(ok = wait_bar_warp(bar(sh->qh_ready), (c - 1) & 1, wc))) break;
+        if (live) {
+          float hf = 1.f;
+          if (F16) {
+            float mx = 0.f, back;
+#pragma unroll
+            for (int x = 0; x < DK; ++x) mx = fmaxf(mx, fabsf(H[x]));
+            hf = half_range(mx, &back);
+            sh->cs[c & 1][d] = back;
+          }
+#pragma unroll
+          for (int x = 0; x < DK; x += 8) {
+            uint4 w;
+            w.x = pack16<F16>(H[x] * hf, H[x + 1] * hf);
+            w.y = pack16<F16>(H[x + 2] * hf, H[x + 3] * hf);
+            w.z = pack16<F16>(H[x + 4] * hf, H[x + 5] * hf);
+            w.w = pack16<F16>(H[x + 6] * hf, H[x + 7] * hf);
+            *reinterpret_cast<uint4*>(Hb + (x >> 6) * (DV * 128) + d * 128 + ((((x >> 3) & 7) ^ (d & 7)) << 4)) = w;
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->h_ready));
+      }
+      const bool short_chunk = ragged && c == chunks - 1;
+      if (c >= deltas && !short_chunk) break;
+      if (!(ok = wait_bar_warp(bar(sh->full[c % kStages]), (c / kStages) & 1, wc))) break;
+      if (short_chunk) {
+        // The rows behind the last token belong to the next request (or to none):
+        // zeros in K and V, whose weights are zero but times NaN would be NaN.
+        unsigned char* kv = stage(c) + KC * kChunkBytes;   // the K chunks, then the V chunks
+        for (int x = 0; x < KC + VC; ++x) {
+          uint4* w = reinterpret_cast<uint4*>(kv + x * kChunkBytes + last_n * 128);
+          for (int i = quad * 32 + lane; i < (kC - last_n) * 8; i += 128) w[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->tail));
+        if (c >= deltas) break;
+      }
+      const int m = short_chunk ? last_n : kC;
+      const unsigned char* v = stage(c) + (2 * KC + (live ? d >> 6 : 0)) * kChunkBytes + (d & 7) * 2;
+      const int piece = (d >> 3) & 7;
+      auto value = [&](int j) {
+        return to_float<F16>(*reinterpret_cast<const uint16_t*>(v + j * 128 + ((piece ^ (j & 7)) << 4)));
+      };
+      float vf = 1.f, vback = 1.f;
+      if (F16 && live) {                       // the column of V brought into fp16's range
+        float mx = 0.f;
+#pragma unroll 8
+        for (int j = 0; j < kC; ++j)
+          if (j < m) mx = fmaxf(mx, fabsf(value(j)));
+        vf = half_range(mx, &vback);
+      }
+      for (int half = 0; half < 2 && ok; ++half) {
+        if (half && !(ok = wait_bar_warp(bar(sh->v_done), c & 1, wc))) break;
+        tc_fence_after();
+        if (live) {
+          for (int g = 0; g < 4; ++g) {        // 16 tokens: 8 columns of each term
+            uint32_t w[3][8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int j = half * 64 + g * 16 + 2 * y;
+              float x0 = j < m ? value(j) * (sh->pw[max(m - 1 - j, 0)] * vf) : 0.f;
+              float x1 = j + 1 < m ? value(j + 1) * (sh->pw[max(m - 2 - j, 0)] * vf) : 0.f;
+#pragma unroll
+              for (int t = 0; t < kTerms; ++t) {
+                w[t][y] = pack16<F16>(x0, x1);
+                const float2 r = widen<F16>(w[t][y]);
+                x0 -= r.x;
+                x1 -= r.y;
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) tmem_st8(lanes + kColV + t * 32 + g * 8, w[t]);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->v_ready));
+      }
+      if (!ok || !(ok = wait_bar_warp(bar(sh->dh_ready), c & 1, wc))) break;
+      tc_fence_after();
+      if (live) {
+        const float f = sh->pw[m];
+#pragma unroll
+        for (int x = 0; x < DK; x += 32) {
+          uint32_t e[32];
+          tmem_ld32(lanes + kColH + x, e);
+          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 32; ++y) H[x + y] = fmaf(f, H[x + y], __uint_as_float(e[y]) * vback);
+        }
+      }
+    }
+    if (ok && live && final_state)
+      store(p.state_only ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+template <int DK, int DV, bool F16>
+cudaError_t launch_one(ChunkParams& p, bool split, cudaStream_t st) {
+  constexpr size_t smem = smem_bytes<DK, DV>();
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  auto kernel = linear_chunk_kernel<DK, DV, F16>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)p.a.segs * (unsigned)p.a.H;
+  if (split) {
+    p.state_only = 1;
+    kernel<<<grid, kThreads, smem, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  p.state_only = 0;
+  kernel<<<grid, kThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DK, int DV>
+cudaError_t launch_width(ChunkParams& p, bool f16, bool split, cudaStream_t st) {
+  return f16 ? launch_one<DK, DV, true>(p, split, st) : launch_one<DK, DV, false>(p, split, st);
+}
+
+}  // namespace
+
+int linear_seg_len(const dsa_linear_problem& p) {
+  constexpr int kWhole = INT32_MAX - 127;
+  const int64_t longest = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
+  const int64_t even = (int64_t)p.R * p.H / 152;   // tokens of each SM if the work were level
+  if (longest <= 1024 || longest <= even + even / 2) return kWhole;
+  int64_t len = (even + 127) / 128 * 128;
+  if (len < 512) len = 512;
+  return (int)len;
+}
+
+int64_t linear_segs(const dsa_linear_problem& p, int seg_len) { return (int64_t)p.R / seg_len + p.B; }
+
+cudaError_t launch_linear(const LinearArgs& a, bool f16, bool split, cudaStream_t st) {
+  ChunkParams p;
+  std::memset(&p, 0, sizeof p);
+  p.a = a;
+  if (a.R > 0) {   // (no tokens: only states are handed on)
+    cudaError_t e = chunk_map(&p.tq, a.q, a.R, (int64_t)a.H * a.D_k, a.q_stride);
+    if (e == cudaSuccess) e = chunk_map(&p.tk, a.k, a.R, (int64_t)a.H * a.D_k, a.k_stride);
+    if (e == cudaSuccess) e = chunk_map(&p.tv, a.v, a.R, (int64_t)a.H * a.D_v, a.v_stride);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.D_k == 64) return a.D_v == 64 ? launch_width<64, 64>(p, f16, split, st) : launch_width<64, 128>(p, f16, split, st);
+  return a.D_v == 64 ? launch_width<128, 64>(p, f16, split, st) : launch_width<128, 128>(p, f16, split, st);
+}
+
+}  // namespace dsa

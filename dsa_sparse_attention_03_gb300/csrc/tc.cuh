@@ -180,6 +180,11 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return pack_bf16(lo, hi);
 }
 
+template <bool F16>
+__device__ __forceinline__ float to_float(uint16_t x) {
+  return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
+}
+
 // [rows, cols] 16-bit values, rows `stride` values apart, in boxes of 128 rows x
 // 64 columns with the 128-byte swizzle; rows past the end read as zeros.
 inline cudaError_t chunk_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride) {
