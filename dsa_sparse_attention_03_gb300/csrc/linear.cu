@@ -62,8 +62,8 @@ struct __align__(16) Shared {
   int req, seg, nseg, first;       // request, its segment, its segments, their first index; req < 0: nothing
   int t0, n;                       // tokens of the segment
   int place, scratch;
-  float pw[kC + 4];                // lambda^0 .. lambda^128
-  float cs[2][128];                // fp16: scale of each column of H as Q H read it
+  float pw[2 * kC + 4];            // pw[128 + e] = lambda^e for e = 0 .. 128, 0 for e < 0
+  unsigned char cs[2][128];        // fp16: scale of each column of H as Q H read it (a power of two's exponent field)
 };
 
 template <int DK, int DV>
@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   }
   if (warp == 2) tmem_alloc(smem_u32(&sh->tmem), 512);
   const float ld2 = log2_decay(a.log_decay[h]);
-  for (int i = tid; i <= kC; i += kThreads) sh->pw[i] = exp2f(ld2 * (float)i);
+  for (int i = tid; i <= 2 * kC; i += kThreads) sh->pw[i] = i < kC ? 0.f : exp2f(ld2 * (float)(i - kC));
+  const float* pw = sh->pw + kC;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -277,11 +278,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         tc_fence_after();
         if (lane == 0) {
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t)
+          for (int t = 0; t < kTerms; ++t)   // the smallest terms first: the sum stays small while they are added
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              mma_ts(tmem + kColH, tmem + kColV + t * 32 + x * 8, desc_mnmajor(k + (half * 4 + x) * 2048, kChunkBytes),
-                     id_d, half | t | x);
+              mma_ts(tmem + kColH, tmem + kColV + (kTerms - 1 - t) * 32 + x * 8,
+                     desc_mnmajor(k + (half * 4 + x) * 2048, kChunkBytes), id_d, half | t | x);
           mma_commit(half ? bar(sh->dh_ready) : bar(sh->v_done));
           if (half) mma_commit(bar(sh->empty[c % kStages]));
         }
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     // ------------------------------------------------------------ rows
     const int quad = warp & 3, i = quad * 32 + lane;   // token of the chunk
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const float reach = sh->pw[i + 1] * a.scale;
+    const float reach = pw[i + 1] * a.scale;
     if (!p.state_only) {
       for (int c = 0; c < chunks; ++c) {
         if (!wait_bar_warp(bar(sh->s_ready), c & 1, wc)) break;
@@ -309,8 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             tmem_ld32(lanes + kColS + x * 32, s);
             tmem_wait_ld();
 #pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (x * 32 + y <= i) mx = fmaxf(mx, fabsf(__uint_as_float(s[y])));
+            for (int y = 0; y < 32; ++y) {
+              const float v = x * 32 + y <= i ? fabsf(__uint_as_float(s[y])) : 0.f;
+              mx = fmaxf(mx, v);
+            }
           }
           pf = half_range(mx * a.scale, &pback);
         }
@@ -318,15 +321,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
         for (int x = 0; x < 4; ++x) {      // P overwrites S behind the columns already read
           uint32_t s[32];
-          if (x <= quad) {
+          if (x < quad) {
+            // Every column lies before the row: lambda^(i-j) = lambda^(i-e) lambda^(e-j)
+            // with e the block's last column, one power per thread, one per column.
             tmem_ld32(lanes + kColS + x * 32, s);
             tmem_wait_ld();
+            const float f = ps * pw[i - (x * 32 + 31)];
+#pragma unroll
+            for (int y = 0; y < 32; y += 2)
+              s[y >> 1] = pack16<F16>(__uint_as_float(s[y]) * (f * pw[31 - y]),
+                                      __uint_as_float(s[y + 1]) * (f * pw[30 - y]));
+          } else if (x == quad) {
+            // The diagonal's block (the table is 0 where the column lies behind the row;
+            // what S holds there may be anything, so it is also replaced).
+            tmem_ld32(lanes + kColS + x * 32, s);
+            tmem_wait_ld();
+            const float* w = pw + lane;
 #pragma unroll
             for (int y = 0; y < 32; y += 2) {
-              const int d = i - (x * 32 + y);
-              const float p0 = d >= 0 ? __uint_as_float(s[y]) * ps * ex2(ld2 * (float)d) : 0.f;
-              const float p1 = d >= 1 ? __uint_as_float(s[y + 1]) * ps * ex2(ld2 * (float)(d - 1)) : 0.f;
-              s[y >> 1] = pack16<F16>(p0, p1);
+              const float s0 = y <= lane ? __uint_as_float(s[y]) : 0.f;
+              const float s1 = y + 1 <= lane ? __uint_as_float(s[y + 1]) : 0.f;
+              s[y >> 1] = pack16<F16>(s0 * (ps * w[-y]), s1 * (ps * w[-y - 1]));
             }
           } else {
 #pragma unroll
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           tmem_wait_ld();
 #pragma unroll
           for (int y = 0; y < 32; ++y)
-            o[y] = __float_as_uint(__uint_as_float(o[y]) * (F16 ? f * sh->cs[c & 1][x + y] : f));
+            o[y] = __float_as_uint(__uint_as_float(o[y]) * (F16 ? f * __uint_as_float((uint32_t)sh->cs[c & 1][x + y] << 23) : f));
           tmem_st32(lanes + kColO + x, o);
         }
         tmem_wait_st();
@@ -422,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
             for (int x = 0; x < DK; ++x) mx = fmaxf(mx, fabsf(H[x]));
             hf = half_range(mx, &back);
-            sh->cs[c & 1][d] = back;
+            sh->cs[c & 1][d] = (unsigned char)(__float_as_uint(back) >> 23);
           }
 #pragma unroll
           for (int x = 0; x < DK; x += 8) {
@@ -450,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           for (int i = quad * 32 + lane; i < (kC - last_n) * 8; i += 128) w[i] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
-        __syncwarp();
+        asm volatile("bar.sync 1, 128;" ::: "memory");   // (the state warps; the decayed v below read the zeros)
         if (lane == 0) mbar_arrive(bar(sh->tail));
         if (c >= deltas) break;
       }
@@ -460,12 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       auto value = [&](int j) {
         return to_float<F16>(*reinterpret_cast<const uint16_t*>(v + j * 128 + ((piece ^ (j & 7)) << 4)));
       };
+      const float* fade = pw + m - 1;          // fade[-j] = lambda^(m-1-j), 0 behind the last token
       float vf = 1.f, vback = 1.f;
       if (F16 && live) {                       // the column of V brought into fp16's range
         float mx = 0.f;
 #pragma unroll 8
-        for (int j = 0; j < kC; ++j)
-          if (j < m) mx = fmaxf(mx, fabsf(value(j)));
+        for (int j = 0; j < kC; ++j) mx = fmaxf(mx, fabsf(value(j)));
         vf = half_range(mx, &vback);
       }
       for (int half = 0; half < 2 && ok; ++half) {
@@ -477,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const int j = half * 64 + g * 16 + 2 * y;
-              float x0 = j < m ? value(j) * (sh->pw[max(m - 1 - j, 0)] * vf) : 0.f;
-              float x1 = j + 1 < m ? value(j + 1) * (sh->pw[max(m - 2 - j, 0)] * vf) : 0.f;
+              float x0 = value(j) * (fade[-j] * vf), x1 = value(j + 1) * (fade[-j - 1] * vf);
 #pragma unroll
               for (int t = 0; t < kTerms; ++t) {
                 w[t][y] = pack16<F16>(x0, x1);
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       if (!ok || !(ok = wait_bar_warp(bar(sh->dh_ready), c & 1, wc))) break;
       tc_fence_after();
       if (live) {
-        const float f = sh->pw[m];
+        const float f = pw[m];
 #pragma unroll
         for (int x = 0; x < DK; x += 32) {
           uint32_t e[32];
@@ -549,7 +563,10 @@ int linear_seg_len(const dsa_linear_problem& p) {
   const int64_t longest = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
   const int64_t even = (int64_t)p.R * p.H / 152;   // tokens of each SM if the work were level
   if (longest <= 1024 || longest <= even + even / 2) return kWhole;
-  int64_t len = (even + 127) / 128 * 128;
+  // As many segments per head as SMs, less the ones the requests' ends add.
+  int64_t segs = 152 / p.H - (p.B > 1 ? 1 : 0);
+  if (segs < 1) segs = 1;
+  int64_t len = ((p.R + segs - 1) / segs + 127) / 128 * 128;
   if (len < 512) len = 512;
   return (int)len;
 }
