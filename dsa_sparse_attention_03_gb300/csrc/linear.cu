@@ -20,13 +20,18 @@
 // column of H and row of P scaled by a power of two into range).
 //
 // A CTA takes one head of one request, or of one segment of a long request, and
-// walks its chunks.  Warp roles:
-//   warp 0       producer: Q, K, V tiles by TMA, two chunks in flight
-//   warp 1       issues S = Q K^T, O = Q H, O += P V
-//   warp 2       issues dH^T
-//   warp 3       none
-//   warps 4-7    "rows": a thread holds one token's row of S, P and O
-//   warps 8-11   "state": a thread holds one column of H
+// walks its chunks.  Four warpgroups, so that the chunks' steps overlap:
+//   warp 0        producer: Q, K, V tiles by TMA, two chunks in flight
+//   warp 1        issues S = Q K^T, O = Q H, O += P V
+//   warp 2        issues dH^T
+//   warps 4-7     "rows": a thread holds one token's row of S, P and O; the output
+//                 tile leaves by TMA through the shared memory of its own Q tile
+//   warps 8-11    "decay": a thread writes one column of the decayed V, a quarter
+//                 chunk (32 tokens) at a time into two buffers in turn; in a request's
+//                 last chunk they first zero the K and V rows behind the last token
+//                 (another request's: weight zero times NaN is NaN)
+//   warps 12-15   "state": a thread holds one column of H
+// Registers are dealt to the groups with setmaxnreg (56 + 120 + 104 + 232 of 4 x 128).
 //
 // Bound: reading q, k, v and writing out once.  Where requests and heads do not
 // fill the GPU, long requests are split into segments: a first launch computes
@@ -42,21 +47,23 @@ namespace dsa {
 namespace {
 
 constexpr int kC = 128;            // tokens of a chunk
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+constexpr int kQuarter = 32;       // tokens of the decayed V in one buffer
 constexpr int kStages = 2;
 
 // Tensor-memory columns.
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384;
 
 struct ChunkParams {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   LinearArgs a;
   int state_only;
 };
 
 struct __align__(16) Shared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t s_ready, qh_ready, h_ready, p_ready, o_ready, o_free, v_ready, v_done, dh_ready, tail, done1, done2;
+  uint64_t q_full[kStages], kv_full[kStages], q_empty[kStages], kv_empty[kStages];
+  uint64_t s_ready, qh_ready, h_ready, p_ready, o_ready, o_free, dh_ready, dh_free, tail, done1, done2;
+  uint64_t v_ready[2], v_free[2];
   uint32_t tmem;
   int abort;
   int req, seg, nseg, first;       // request, its segment, its segments, their first index; req < 0: nothing
@@ -64,11 +71,12 @@ struct __align__(16) Shared {
   int place, scratch;
   float pw[2 * kC + 4];            // pw[128 + e] = lambda^e for e = 0 .. 128, 0 for e < 0
   unsigned char cs[2][128];        // fp16: scale of each column of H as Q H read it (a power of two's exponent field)
+  unsigned char vs[2][128];        // fp16: the same of each column of the decayed V
 };
 
 template <int DK, int DV>
 __host__ __device__ constexpr uint32_t stage_bytes() {
-  return (2 * (DK / 64) + DV / 64) * kChunkBytes;
+  return ((DK > DV ? DK : DV) / 64 + DK / 64 + DV / 64) * kChunkBytes;   // Q (later O), K, V
 }
 template <int DK, int DV>
 __host__ __device__ constexpr size_t smem_bytes() {
@@ -110,6 +118,22 @@ __device__ void locate(const LinearArgs& a, int idx, Shared* sh, int lane) {
   }
 }
 
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -122,6 +146,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+
+__device__ __forceinline__ float exponent_value(unsigned char e) { return __uint_as_float((uint32_t)e << 23); }
+__device__ __forceinline__ unsigned char exponent_field(float x) { return (unsigned char)(__float_as_uint(x) >> 23); }
 
 // The two values of a packed pair, widened.
 template <bool F16>
@@ -145,7 +172,7 @@ __device__ __forceinline__ float half_range(float m, float* back) {
 
 template <int DK, int DV, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int KC = DK / 64, VC = DV / 64;
+  constexpr int KC = DK / 64, VC = DV / 64, QC = KC > VC ? KC : VC;
   constexpr uint32_t kStage = stage_bytes<DK, DV>();
   constexpr int kTerms = F16 ? 2 : 3;
   const LinearArgs& a = p.a;
@@ -165,8 +192,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sh->full[i]), 1);
-      mbar_init(smem_u32(&sh->empty[i]), p.state_only ? 1 : 2);
+      mbar_init(smem_u32(&sh->q_full[i]), 1);
+      mbar_init(smem_u32(&sh->kv_full[i]), 1);
+      mbar_init(smem_u32(&sh->q_empty[i]), 1);
+      mbar_init(smem_u32(&sh->kv_empty[i]), p.state_only ? 1 : 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh->v_ready[i]), 4);
+      mbar_init(smem_u32(&sh->v_free[i]), 1);
     }
     mbar_init(smem_u32(&sh->s_ready), 1);
     mbar_init(smem_u32(&sh->qh_ready), 1);
@@ -174,9 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     mbar_init(smem_u32(&sh->p_ready), 4);
     mbar_init(smem_u32(&sh->o_ready), 1);
     mbar_init(smem_u32(&sh->o_free), 4);
-    mbar_init(smem_u32(&sh->v_ready), 4);
-    mbar_init(smem_u32(&sh->v_done), 1);
     mbar_init(smem_u32(&sh->dh_ready), 1);
+    mbar_init(smem_u32(&sh->dh_free), 4);
     mbar_init(smem_u32(&sh->tail), 4);
     mbar_init(smem_u32(&sh->done1), 1);
     mbar_init(smem_u32(&sh->done2), 1);
@@ -201,34 +233,47 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const int deltas = final_state ? chunks : chunks - 1;   // chunks whose dH is needed
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   auto stage = [&](int c) { return smem + (c % kStages) * kStage; };
+  auto phase = [&](int c) { return (uint32_t)((c / kStages) & 1); };
+  const int quad = warp & 3;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int c = 0;
-      for (; c < chunks; ++c) {
-        const int s = c % kStages;
-        if (c >= kStages && !wait_bar(bar(sh->empty[s]), (c / kStages - 1) & 1, wc)) break;
-        const uint32_t b = bar(sh->full[s]), dst = smem_u32(stage(c));
-        const int y = t0 + c * kC;
-        mbar_expect_tx(b, p.state_only ? (KC + VC) * kChunkBytes : kStage);
-        if (!p.state_only)
-          for (int x = 0; x < KC; ++x) tma_load_2d(dst + x * kChunkBytes, &p.tq, h * DK + x * 64, y, b);
-        for (int x = 0; x < KC; ++x) tma_load_2d(dst + (KC + x) * kChunkBytes, &p.tk, h * DK + x * 64, y, b);
-        for (int x = 0; x < VC; ++x) tma_load_2d(dst + (2 * KC + x) * kChunkBytes, &p.tv, h * DV + x * 64, y, b);
+  if (warp < 4) {
+    regs_down<56>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        int c = 0;
+        bool q_last = false;   // chunk c's Q tile was asked for
+        for (; c < chunks; ++c) {
+          const int s = c % kStages, y = t0 + c * kC;
+          const uint32_t q = smem_u32(stage(c)), k = q + QC * kChunkBytes, v = k + KC * kChunkBytes;
+          if (c >= kStages && !wait_bar(bar(sh->kv_empty[s]), phase(c - kStages), wc)) break;
+          mbar_expect_tx(bar(sh->kv_full[s]), (KC + VC) * kChunkBytes);
+          for (int x = 0; x < KC; ++x) tma_load_2d(k + x * kChunkBytes, &p.tk, h * DK + x * 64, y, bar(sh->kv_full[s]));
+          for (int x = 0; x < VC; ++x) tma_load_2d(v + x * kChunkBytes, &p.tv, h * DV + x * 64, y, bar(sh->kv_full[s]));
+          if (p.state_only) continue;
+          if (c >= kStages && !wait_bar(bar(sh->q_empty[s]), phase(c - kStages), wc)) {
+            ++c;
+            q_last = true;     // (its K and V were asked for, its Q was not)
+            break;
+          }
+          mbar_expect_tx(bar(sh->q_full[s]), KC * kChunkBytes);
+          for (int x = 0; x < KC; ++x) tma_load_2d(q + x * kChunkBytes, &p.tq, h * DK + x * 64, y, bar(sh->q_full[s]));
+        }
+        for (int i = max(0, c - kStages); i < c; ++i) {   // (an abort may leave copies in flight)
+          drain_bar(bar(sh->kv_full[i % kStages]), phase(i), a.wait_ns);
+          if (!p.state_only && !(q_last && i == c - 1)) drain_bar(bar(sh->q_full[i % kStages]), phase(i), a.wait_ns);
+        }
       }
-      for (int i = max(0, c - kStages); i < c; ++i)   // (an abort may leave copies in flight)
-        drain_bar(bar(sh->full[i % kStages]), (i / kStages) & 1, a.wait_ns);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S, Q H, P V
-    if (!p.state_only) {
+    } else if (warp == 1 && !p.state_only) {
+      // ---------------------------------------------------------- S, Q H, P V
       const uint32_t id_s = idesc_16(F16, kC, kC, false, false);
       const uint32_t id_h = idesc_16(F16, kC, DV, false, false);
       const uint32_t id_o = idesc_16(F16, kC, DV, false, true);
       for (int c = 0; c < chunks; ++c) {
-        const uint32_t q = smem_u32(stage(c)), k = q + KC * kChunkBytes, v = k + KC * kChunkBytes;
-        if (!wait_bar_warp(bar(sh->full[c % kStages]), (c / kStages) & 1, wc)) break;
+        const int s = c % kStages;
+        const uint32_t q = smem_u32(stage(c)), k = q + QC * kChunkBytes, v = k + KC * kChunkBytes;
+        if (!wait_bar_warp(bar(sh->kv_full[s]), phase(c), wc)) break;
+        if (!wait_bar_warp(bar(sh->q_full[s]), phase(c), wc)) break;
         tc_fence_after();
         if (lane == 0) {
 #pragma unroll
@@ -256,46 +301,50 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           for (int x = 0; x < 8; ++x)
             mma_ts(tmem + kColO, tmem + kColS + x * 8, desc_mnmajor(v + x * 2048, kChunkBytes), id_o, 1);
           mma_commit(bar(sh->o_ready));
-          mma_commit(bar(sh->empty[c % kStages]));
+          mma_commit(bar(sh->kv_empty[s]));
         }
       }
       if (lane == 0 && chunks > 0) {
         mma_commit(bar(sh->done1));
         drain_bar(bar(sh->done1), 0, a.wait_ns);
       }
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ dH^T
-    const uint32_t id_d = idesc_16(F16, kC, DK, false, true);
-    for (int c = 0; c < deltas; ++c) {
-      const uint32_t k = smem_u32(stage(c)) + KC * kChunkBytes;
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- dH^T
+      const uint32_t id_d = idesc_16(F16, kC, DK, false, true);
       bool ok = true;
-      for (int half = 0; half < 2 && ok; ++half) {
-        ok = wait_bar_warp(bar(sh->v_ready), half, wc);   // (two phases per chunk)
-        if (ok && half == 0) ok = wait_bar_warp(bar(sh->full[c % kStages]), (c / kStages) & 1, wc);
-        if (ok && half == 0 && ragged && c == chunks - 1) ok = wait_bar_warp(bar(sh->tail), 0, wc);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
+      for (int c = 0; c < deltas && ok; ++c) {
+        const uint32_t k = smem_u32(stage(c)) + QC * kChunkBytes;
+        if (!(ok = wait_bar_warp(bar(sh->kv_full[c % kStages]), phase(c), wc))) break;
+        if (ragged && c == chunks - 1 && !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;
+        if (c > 0 && !(ok = wait_bar_warp(bar(sh->dh_free), (c - 1) & 1, wc))) break;
+        for (int g = 0; g < 4 && ok; ++g) {
+          const int b = g & 1;                       // quarter 4 c + g: buffer g % 2, its use 2 c + g / 2
+          if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), g >> 1, wc))) break;
+          tc_fence_after();
+          if (lane == 0) {
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t)   // the smallest terms first: the sum stays small while they are added
+            for (int t = kTerms - 1; t >= 0; --t)    // the smallest terms first: the sum stays small meanwhile
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_ts(tmem + kColH, tmem + kColV + (kTerms - 1 - t) * 32 + x * 8,
-                     desc_mnmajor(k + (half * 4 + x) * 2048, kChunkBytes), id_d, half | t | x);
-          mma_commit(half ? bar(sh->dh_ready) : bar(sh->v_done));
-          if (half) mma_commit(bar(sh->empty[c % kStages]));
+              for (int x = 0; x < 2; ++x)
+                mma_ts(tmem + kColH, tmem + kColV + b * 64 + t * 16 + x * 8,
+                       desc_mnmajor(k + (g * 2 + x) * 2048, kChunkBytes), id_d, g | (kTerms - 1 - t) | x);
+            mma_commit(bar(sh->v_free[b]));
+            if (g == 3) {
+              mma_commit(bar(sh->dh_ready));
+              mma_commit(bar(sh->kv_empty[c % kStages]));
+            }
+          }
         }
       }
-      if (!ok) break;
+      if (lane == 0 && deltas > 0) {
+        mma_commit(bar(sh->done2));
+        drain_bar(bar(sh->done2), 0, a.wait_ns);
+      }
     }
-    if (lane == 0 && deltas > 0) {
-      mma_commit(bar(sh->done2));
-      drain_bar(bar(sh->done2), 0, a.wait_ns);
-    }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ rows
-    const int quad = warp & 3, i = quad * 32 + lane;   // token of the chunk
+    regs_down<120>();
+    const int i = quad * 32 + lane;   // token of the chunk
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const float reach = pw[i + 1] * a.scale;
     if (!p.state_only) {
@@ -359,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           tmem_wait_ld();
 #pragma unroll
           for (int y = 0; y < 32; ++y)
-            o[y] = __float_as_uint(__uint_as_float(o[y]) * (F16 ? f * __uint_as_float((uint32_t)sh->cs[c & 1][x + y] << 23) : f));
+            o[y] = __float_as_uint(__uint_as_float(o[y]) * (F16 ? f * exponent_value(sh->cs[c & 1][x + y]) : f));
           tmem_st32(lanes + kColO + x, o);
         }
         tmem_wait_st();
@@ -368,7 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (lane == 0) mbar_arrive(bar(sh->p_ready));
         if (!wait_bar_warp(bar(sh->o_ready), c & 1, wc)) break;
         tc_fence_after();
-        const bool mine = c * kC + i < n;
+        // A whole chunk leaves by TMA through the shared memory of its Q tile, which
+        // no MMA reads any more; a request's last rows are stored one by one.
+        const bool whole = !(ragged && c == chunks - 1);
+        unsigned char* tile = stage(c);
         uint16_t* dst = a.out + ((int64_t)(t0 + c * kC + i) * a.H + h) * DV;
 #pragma unroll
         for (int x = 0; x < DV; x += 32) {
@@ -378,22 +430,109 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
           for (int y = 0; y < 32; y += 2)
             o[y >> 1] = pack16<F16>(__uint_as_float(o[y]) * pback, __uint_as_float(o[y + 1]) * pback);
-          if (mine) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              reinterpret_cast<uint4*>(dst + x)[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          for (int y = 0; y < 4; ++y) {
+            const uint4 w = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            if (whole)
+              *reinterpret_cast<uint4*>(tile + (x >> 6) * kChunkBytes + i * 128 +
+                                        (((((x & 63) >> 3) + y) ^ (i & 7)) << 4)) = w;
+            else if (i < last_n)
+              reinterpret_cast<uint4*>(dst + x)[y] = w;
           }
         }
         tc_fence_before();
-        __syncwarp();
+        if (whole) {
+          fence_proxy_async();
+          asm volatile("bar.sync 2, 128;" ::: "memory");   // (the row warps)
+        } else {
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive(bar(sh->o_free));
+        if (whole && warp == 4 && lane == 0) {
+          for (int x = 0; x < VC; ++x)
+            tma_store_2d(&p.to, h * DV + x * 64, t0 + c * kC, smem_u32(tile + x * kChunkBytes));
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          mbar_arrive(bar(sh->q_empty[c % kStages]));
+        }
+      }
+      if (warp == 4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ decay
+    regs_down<104>();
+    const int d = quad * 32 + lane;                    // column of V
+    const bool live = d < DV;                          // (a whole warp)
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + kColV;
+    bool ok = true;
+    for (int c = 0; c < chunks && ok; ++c) {
+      const bool short_chunk = ragged && c == chunks - 1;
+      if (c >= deltas && !short_chunk) break;
+      if (!(ok = wait_bar_warp(bar(sh->kv_full[c % kStages]), phase(c), wc))) break;
+      unsigned char* kv = stage(c) + QC * kChunkBytes;   // the K chunks, then the V chunks
+      if (short_chunk) {
+        // Zeros in K and V behind the last token.
+        for (int x = 0; x < KC + VC; ++x) {
+          uint4* w = reinterpret_cast<uint4*>(kv + x * kChunkBytes + last_n * 128);
+          for (int i = quad * 32 + lane; i < (kC - last_n) * 8; i += 128) w[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        asm volatile("bar.sync 1, 128;" ::: "memory");   // (the decay warps, who read the zeros too)
+        if (lane == 0) mbar_arrive(bar(sh->tail));
+        if (c >= deltas) break;
+      }
+      const int m = short_chunk ? last_n : kC;
+      const unsigned char* v = kv + (KC + (live ? d >> 6 : 0)) * kChunkBytes + (d & 7) * 2;
+      const int piece = (d >> 3) & 7;
+      auto value = [&](int j) {
+        return to_float<F16>(*reinterpret_cast<const uint16_t*>(v + j * 128 + ((piece ^ (j & 7)) << 4)));
+      };
+      const float* fade = pw + m - 1;          // fade[-j] = lambda^(m-1-j), 0 behind the last token
+      float vf = 1.f, vback = 1.f;
+      if (F16 && live) {                       // the column of V brought into fp16's range
+        float mx = 0.f;
+#pragma unroll 8
+        for (int j = 0; j < kC; ++j) mx = fmaxf(mx, fabsf(value(j)));
+        vf = half_range(mx, &vback);
+      }
+      for (int g = 0; g < 4; ++g) {
+        // The buffer's last use was two quarters ago.
+        if ((c > 0 || g > 1) && !(ok = wait_bar_warp(bar(sh->v_free[g & 1]), (g >> 1) ^ 1, wc))) break;
+        tc_fence_after();
+        if (live) {
+          if (F16 && g == 0) sh->vs[c & 1][d] = exponent_field(vback);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {        // 16 tokens: 8 columns of each term
+            uint32_t w[3][8];
+            const int j0 = g * kQuarter + z * 16;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int j = j0 + 2 * y;
+              float x0 = value(j) * (fade[-j] * vf), x1 = value(j + 1) * (fade[-j - 1] * vf);
+#pragma unroll
+              for (int t = 0; t < kTerms; ++t) {
+                w[t][y] = pack16<F16>(x0, x1);
+                const float2 r = widen<F16>(w[t][y]);
+                x0 -= r.x;
+                x1 -= r.y;
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) tmem_st8(lanes + (g & 1) * 64 + t * 16 + z * 8, w[t]);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->v_ready[g & 1]));
       }
     }
-  } else if (warp >= 8) {
+  } else {
     // ------------------------------------------------------------ state
-    const int quad = warp & 3, d = quad * 32 + lane;   // column of H
+    regs_up<232>();
+    const int d = quad * 32 + lane;                    // column of H
     const bool live = d < DV;                          // (a whole warp)
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + kColH;
     const int64_t head = (int64_t)DK * DV;
     float H[DK];
 #pragma unroll
@@ -421,12 +560,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         for (int s = 1; s < seg; ++s) {
           const float* e = ends + (int64_t)s * a.H * head;
 #pragma unroll
-          for (int x = 0; x < DK; ++x) H[x] = fmaf(f, H[x], e[x * DV + d]);
+          for (int x = 0; x < DK; x += 16) {
+            float t[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) t[y] = e[(x + y) * DV + d];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, H[x + y], t[y]);
+            asm volatile("" ::: "memory");   // (no more than 16 loads ahead: registers)
+          }
         }
       }
     }
     bool ok = true;
-    for (int c = 0; c < chunks && ok; ++c) {
+    for (int c = 0; c < chunks; ++c) {
       if (!p.state_only) {
         // H in the operands' type, once Q H of the chunk before has read the last one.
         if (c > 0 && !(ok = wait_bar_warp(bar(sh->qh_ready), (c - 1) & 1, wc))) break;
@@ -437,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
             for (int x = 0; x < DK; ++x) mx = fmaxf(mx, fabsf(H[x]));
             hf = half_range(mx, &back);
-            sh->cs[c & 1][d] = (unsigned char)(__float_as_uint(back) >> 23);
+            sh->cs[c & 1][d] = exponent_field(back);
           }
 #pragma unroll
           for (int x = 0; x < DK; x += 8) {
@@ -453,76 +599,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh->h_ready));
       }
-      const bool short_chunk = ragged && c == chunks - 1;
-      if (c >= deltas && !short_chunk) break;
-      if (!(ok = wait_bar_warp(bar(sh->full[c % kStages]), (c / kStages) & 1, wc))) break;
-      if (short_chunk) {
-        // The rows behind the last token belong to the next request (or to none):
-        // zeros in K and V, whose weights are zero but times NaN would be NaN.
-        unsigned char* kv = stage(c) + KC * kChunkBytes;   // the K chunks, then the V chunks
-        for (int x = 0; x < KC + VC; ++x) {
-          uint4* w = reinterpret_cast<uint4*>(kv + x * kChunkBytes + last_n * 128);
-          for (int i = quad * 32 + lane; i < (kC - last_n) * 8; i += 128) w[i] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        asm volatile("bar.sync 1, 128;" ::: "memory");   // (the state warps; the decayed v below read the zeros)
-        if (lane == 0) mbar_arrive(bar(sh->tail));
-        if (c >= deltas) break;
-      }
-      const int m = short_chunk ? last_n : kC;
-      const unsigned char* v = stage(c) + (2 * KC + (live ? d >> 6 : 0)) * kChunkBytes + (d & 7) * 2;
-      const int piece = (d >> 3) & 7;
-      auto value = [&](int j) {
-        return to_float<F16>(*reinterpret_cast<const uint16_t*>(v + j * 128 + ((piece ^ (j & 7)) << 4)));
-      };
-      const float* fade = pw + m - 1;          // fade[-j] = lambda^(m-1-j), 0 behind the last token
-      float vf = 1.f, vback = 1.f;
-      if (F16 && live) {                       // the column of V brought into fp16's range
-        float mx = 0.f;
-#pragma unroll 8
-        for (int j = 0; j < kC; ++j) mx = fmaxf(mx, fabsf(value(j)));
-        vf = half_range(mx, &vback);
-      }
-      for (int half = 0; half < 2 && ok; ++half) {
-        if (half && !(ok = wait_bar_warp(bar(sh->v_done), c & 1, wc))) break;
-        tc_fence_after();
-        if (live) {
-          for (int g = 0; g < 4; ++g) {        // 16 tokens: 8 columns of each term
-            uint32_t w[3][8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int j = half * 64 + g * 16 + 2 * y;
-              float x0 = value(j) * (fade[-j] * vf), x1 = value(j + 1) * (fade[-j - 1] * vf);
-#pragma unroll
-              for (int t = 0; t < kTerms; ++t) {
-                w[t][y] = pack16<F16>(x0, x1);
-                const float2 r = widen<F16>(w[t][y]);
-                x0 -= r.x;
-                x1 -= r.y;
-              }
-            }
-#pragma unroll
-            for (int t = 0; t < kTerms; ++t) tmem_st8(lanes + kColV + t * 32 + g * 8, w[t]);
-          }
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh->v_ready));
-      }
-      if (!ok || !(ok = wait_bar_warp(bar(sh->dh_ready), c & 1, wc))) break;
+      if (c >= deltas) break;
+      if (!(ok = wait_bar_warp(bar(sh->dh_ready), c & 1, wc))) break;
       tc_fence_after();
       if (live) {
-        const float f = pw[m];
+        const float f = pw[ragged && c == chunks - 1 ? last_n : kC];
+        const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) : 1.f;
 #pragma unroll
         for (int x = 0; x < DK; x += 32) {
           uint32_t e[32];
-          tmem_ld32(lanes + kColH + x, e);
+          tmem_ld32(lanes + x, e);
           tmem_wait_ld();
 #pragma unroll
           for (int y = 0; y < 32; ++y) H[x + y] = fmaf(f, H[x + y], __uint_as_float(e[y]) * vback);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh->dh_free));
     }
     if (ok && live && final_state)
       store(p.state_only ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
@@ -581,6 +675,7 @@ cudaError_t launch_linear(const LinearArgs& a, bool f16, bool split, cudaStream_
     cudaError_t e = chunk_map(&p.tq, a.q, a.R, (int64_t)a.H * a.D_k, a.q_stride);
     if (e == cudaSuccess) e = chunk_map(&p.tk, a.k, a.R, (int64_t)a.H * a.D_k, a.k_stride);
     if (e == cudaSuccess) e = chunk_map(&p.tv, a.v, a.R, (int64_t)a.H * a.D_v, a.v_stride);
+    if (e == cudaSuccess) e = chunk_map(&p.to, a.out, a.R, (int64_t)a.H * a.D_v, (int64_t)a.H * a.D_v);
     if (e != cudaSuccess) return e;
   }
   if (a.D_k == 64) return a.D_v == 64 ? launch_width<64, 64>(p, f16, split, st) : launch_width<64, 128>(p, f16, split, st);

@@ -42,7 +42,7 @@ struct WaitCtx {
   uint64_t limit_ns;
 };
 
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const WaitCtx& c) {
+static __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, const WaitCtx& c) {
   const uint64_t t0 = gtimer();
   for (;;) {
     if (mbar_try(bar, parity)) return true;
