@@ -62,7 +62,7 @@ struct ChunkParams {
 
 struct __align__(16) Shared {
   uint64_t q_full[kStages], kv_full[kStages], q_empty[kStages], kv_empty[kStages];
-  uint64_t s_ready, qh_ready, h_ready, p_ready, o_ready, o_free, dh_ready, dh_free, tail, done1, done2;
+  uint64_t s_ready, o_staged, qh_ready, h_ready, p_ready, o_ready, o_free, dh_ready, dh_free, tail, done1, done2;
   uint64_t v_ready[2], v_free[2];
   uint32_t tmem;
   int abort;
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       mbar_init(smem_u32(&sh->v_free[i]), 1);
     }
     mbar_init(smem_u32(&sh->s_ready), 1);
+    mbar_init(smem_u32(&sh->o_staged), 4);
     mbar_init(smem_u32(&sh->qh_ready), 1);
     mbar_init(smem_u32(&sh->h_ready), 4);
     mbar_init(smem_u32(&sh->p_ready), 4);
@@ -340,6 +341,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         mma_commit(bar(sh->done2));
         drain_bar(bar(sh->done2), 0, a.wait_ns);
       }
+    } else if (warp == 3 && !p.state_only) {
+      // ---------------------------------------------------------- output tiles
+      if (lane == 0) {
+        for (int c = 0; c < chunks - (ragged ? 1 : 0); ++c) {
+          if (!wait_bar(bar(sh->o_staged), c & 1, wc)) break;
+          for (int x = 0; x < VC; ++x)
+            tma_store_2d(&p.to, h * DV + x * 64, t0 + c * kC, smem_u32(stage(c) + x * kChunkBytes));
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          mbar_arrive(bar(sh->q_empty[c % kStages]));
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      }
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ rows
@@ -347,6 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     const int i = quad * 32 + lane;   // token of the chunk
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const float reach = pw[i + 1] * a.scale;
+    float2 column[16];                // lambda^(31-y) of a block's columns
+#pragma unroll
+    for (int y = 0; y < 16; ++y) column[y] = make_float2(pw[31 - 2 * y], pw[30 - 2 * y]);
     if (!p.state_only) {
       for (int c = 0; c < chunks; ++c) {
         if (!wait_bar_warp(bar(sh->s_ready), c & 1, wc)) break;
@@ -376,10 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             tmem_ld32(lanes + kColS + x * 32, s);
             tmem_wait_ld();
             const float f = ps * pw[i - (x * 32 + 31)];
+            const float2 f2 = make_float2(f, f);
 #pragma unroll
-            for (int y = 0; y < 32; y += 2)
-              s[y >> 1] = pack16<F16>(__uint_as_float(s[y]) * (f * pw[31 - y]),
-                                      __uint_as_float(s[y + 1]) * (f * pw[30 - y]));
+            for (int y = 0; y < 32; y += 2) {
+              const float2 v = mul2(mul2(make_float2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), f2), column[y >> 1]);
+              s[y >> 1] = pack16<F16>(v.x, v.y);
+            }
           } else if (x == quad) {
             // The diagonal's block (the table is 0 where the column lies behind the row;
             // what S holds there may be anything, so it is also replaced).
@@ -407,8 +426,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           tmem_ld32(lanes + kColO + x, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int y = 0; y < 32; ++y)
-            o[y] = __float_as_uint(__uint_as_float(o[y]) * (F16 ? f * exponent_value(sh->cs[c & 1][x + y]) : f));
+          for (int y = 0; y < 32; y += 2) {
+            float2 g = make_float2(f, f);
+            if (F16) g = mul2(g, make_float2(exponent_value(sh->cs[c & 1][x + y]), exponent_value(sh->cs[c & 1][x + y + 1])));
+            g = mul2(g, make_float2(__uint_as_float(o[y]), __uint_as_float(o[y + 1])));
+            o[y] = __float_as_uint(g.x);
+            o[y + 1] = __float_as_uint(g.y);
+          }
           tmem_st32(lanes + kColO + x, o);
         }
         tmem_wait_st();
@@ -441,22 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           }
         }
         tc_fence_before();
-        if (whole) {
-          fence_proxy_async();
-          asm volatile("bar.sync 2, 128;" ::: "memory");   // (the row warps)
-        } else {
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive(bar(sh->o_free));
-        if (whole && warp == 4 && lane == 0) {
-          for (int x = 0; x < VC; ++x)
-            tma_store_2d(&p.to, h * DV + x * 64, t0 + c * kC, smem_u32(tile + x * kChunkBytes));
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive(bar(sh->q_empty[c % kStages]));
+        if (whole) fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(sh->o_free));
+          if (whole) mbar_arrive(bar(sh->o_staged));
         }
       }
-      if (warp == 4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ decay
