@@ -384,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           pf = half_range(mx * a.scale, &pback);
         }
         const float ps = a.scale * pf;
-#pragma unroll
+        // (Rolled loops: the four groups' code has to fit the instruction cache together.)
+#pragma unroll 1
         for (int x = 0; x < 4; ++x) {      // P overwrites S behind the columns already read
           uint32_t s[32];
           if (x < quad) {
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (!wait_bar_warp(bar(sh->qh_ready), c & 1, wc)) break;
         tc_fence_after();
         const float f = reach * pf;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < DV; x += 32) {
           uint32_t o[32];
           tmem_ld32(lanes + kColO + x, o);
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         const bool whole = !(ragged && c == chunks - 1);
         unsigned char* tile = stage(c);
         uint16_t* dst = a.out + ((int64_t)(t0 + c * kC + i) * a.H + h) * DV;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < DV; x += 32) {
           uint32_t o[32];
           tmem_ld32(lanes + kColO + x, o);
@@ -510,13 +511,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         for (int j = 0; j < kC; ++j) mx = fmaxf(mx, fabsf(value(j)));
         vf = half_range(mx, &vback);
       }
+#pragma unroll 1
       for (int g = 0; g < 4; ++g) {
         // The buffer's last use was two quarters ago.
         if ((c > 0 || g > 1) && !(ok = wait_bar_warp(bar(sh->v_free[g & 1]), (g >> 1) ^ 1, wc))) break;
         tc_fence_after();
         if (live) {
           if (F16 && g == 0) sh->vs[c & 1][d] = exponent_field(vback);
-#pragma unroll
+#pragma unroll 1
           for (int z = 0; z < 2; ++z) {        // 16 tokens: 8 columns of each term
             uint32_t w[3][8];
             const int j0 = g * kQuarter + z * 16;
