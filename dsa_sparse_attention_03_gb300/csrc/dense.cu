@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
-  const WaitCtx wc{&sh->abort, a.status, a.wait_ns};
+  const WaitCtx wc(&sh->abort, a.status, a.wait_ns);
 
   // K/V tiles of this CTA: [lo, hi); row tile w takes those below its own end.
   int end[2];

@@ -24,14 +24,16 @@
 //   warp 0        producer: Q, K, V tiles by TMA, two chunks in flight
 //   warp 1        issues S = Q K^T, O = Q H, O += P V
 //   warp 2        issues dH^T
-//   warps 4-7     "rows": a thread holds one token's row of S, P and O; the output
-//                 tile leaves by TMA through the shared memory of its own Q tile
-//   warps 8-11    "decay": a thread writes one column of the decayed V, a quarter
+//   warps 4-11    "rows": two threads per token hold its row of S, P and O, one the
+//                 32-column blocks 0 and 2, the other 1 and 3
+//   warp 3        stores the output tiles by TMA, through the shared memory of
+//                 their own Q tile, which no MMA reads by then
+//   warps 12-15   "decay": a thread writes one column of the decayed V, a quarter
 //                 chunk (32 tokens) at a time into two buffers in turn; in a request's
 //                 last chunk they first zero the K and V rows behind the last token
 //                 (another request's: weight zero times NaN is NaN)
-//   warps 12-15   "state": a thread holds one column of H
-// Registers are dealt to the groups with setmaxnreg (56 + 120 + 104 + 232 of 4 x 128).
+//   warps 16-19   "state": a thread holds one column of H
+// Registers are dealt to the groups with setmaxnreg (40 + 3 x 88 + 176 of 5 x 96).
 //
 // Bound: reading q, k, v and writing out once.  Where requests and heads do not
 // fill the GPU, long requests are split into segments: a first launch computes
@@ -47,7 +49,7 @@ namespace dsa {
 namespace {
 
 constexpr int kC = 128;            // tokens of a chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kQuarter = 32;       // tokens of the decayed V in one buffer
 constexpr int kStages = 2;
 
@@ -63,13 +65,15 @@ struct ChunkParams {
 struct __align__(16) Shared {
   uint64_t q_full[kStages], kv_full[kStages], q_empty[kStages], kv_empty[kStages];
   uint64_t s_ready, o_staged, qh_ready, h_ready, p_ready, o_ready, o_free, dh_ready, dh_free, tail, done1, done2;
-  uint64_t v_ready[2], v_free[2];
+  uint64_t v_ready[2], v_free[2], pair[4];
   uint32_t tmem;
   int abort;
   int req, seg, nseg, first;       // request, its segment, its segments, their first index; req < 0: nothing
   int t0, n;                       // tokens of the segment
   int place, scratch;
-  float pw[2 * kC + 4];            // pw[128 + e] = lambda^e for e = 0 .. 128, 0 for e < 0
+  __align__(16) float pw[2 * kC + 4];            // pw[128 + e] = lambda^e for e = 0 .. 128, 0 for e < 0
+  float column[32];                // lambda^(31-y)
+  unsigned char mx[2][128];        // fp16: exponent fields of the two halves' largest |S| of each row
   unsigned char cs[2][128];        // fp16: scale of each column of H as Q H read it (a power of two's exponent field)
   unsigned char vs[2][128];        // fp16: the same of each column of the decayed V
 };
@@ -80,30 +84,31 @@ __host__ __device__ constexpr uint32_t stage_bytes() {
 }
 template <int DK, int DV>
 __host__ __device__ constexpr size_t smem_bytes() {
-  return kStages * stage_bytes<DK, DV>() + DV * DK * 2 + sizeof(Shared) + 1024;
+  return kStages * stage_bytes<DK, DV>() + DV * DK * 2 + sizeof(Shared);
 }
 
-// Segment of this CTA (warp 0).
+// Segment of this CTA (warp 0).  The requests' segments are numbered from the
+// longest request on (up to 32 requests; more keep their order), so that the
+// longest walks start first.
 __device__ void locate(const LinearArgs& a, int idx, Shared* sh, int lane) {
   if (lane == 0) sh->req = -1;
   __syncwarp();
   int run = 0;
   for (int base = 0; base < a.B && run <= idx; base += 32) {
     const int b = base + lane;
-    int t0 = 0, n = 0, v = 0;
+    int t0 = 0, n = -1, v = 0;
     if (b < a.B) {
       const int x0 = a.row_offsets[b], x1 = a.row_offsets[b + 1];
       t0 = min(max(x0, 0), a.R);
       n = max(min(x1, a.R) - t0, 0);
       v = n > a.seg_len ? (n - 1) / a.seg_len + 1 : 1;
     }
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+    int first = run, all = 0;
+    for (int o = 0; o < 32; ++o) {
+      const int on = __shfl_sync(0xffffffffu, n, o), ov = __shfl_sync(0xffffffffu, v, o);
+      all += ov;
+      if (a.B <= 32 ? on > n || (on == n && o < lane) : o < lane) first += ov;
     }
-    const int first = run + incl - v;
     if (idx >= first && idx < first + v) {
       const int s = idx - first;
       const int skip = s * a.seg_len;   // (below n)
@@ -114,7 +119,7 @@ __device__ void locate(const LinearArgs& a, int idx, Shared* sh, int lane) {
       sh->t0 = t0 + skip;
       sh->n = v == 1 ? n : min(n - skip, a.seg_len);
     }
-    run += __shfl_sync(0xffffffffu, incl, 31);
+    run += all;
   }
 }
 
@@ -138,6 +143,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -177,12 +189,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   constexpr int kTerms = F16 ? 2 : 3;
   const LinearArgs& a = p.a;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned char* smem = smem_raw;   // (1024-byte aligned: checked below)
   unsigned char* Hb = smem + kStages * kStage;     // H in the operands' type, D_v rows of D_k, K-major
   Shared* sh = reinterpret_cast<Shared*>(Hb + DV * DK * 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H;
 
+  if (smem_u32(smem_raw) & 1023) {
+    if (tid == 0) raise_status(a.status, DSA_DEVICE_CAPACITY);
+    return;
+  }
   if (warp == 0) locate(a, blockIdx.x / a.H, sh, lane);
   __syncthreads();
   if (sh->req < 0) return;
@@ -198,19 +214,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       mbar_init(smem_u32(&sh->kv_empty[i]), p.state_only ? 1 : 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh->v_ready[i]), 4);
+      mbar_init(smem_u32(&sh->v_ready[i]), DV / 32);
       mbar_init(smem_u32(&sh->v_free[i]), 1);
     }
     mbar_init(smem_u32(&sh->s_ready), 1);
-    mbar_init(smem_u32(&sh->o_staged), 4);
+    mbar_init(smem_u32(&sh->o_staged), 8);
     mbar_init(smem_u32(&sh->qh_ready), 1);
-    mbar_init(smem_u32(&sh->h_ready), 4);
-    mbar_init(smem_u32(&sh->p_ready), 4);
+    mbar_init(smem_u32(&sh->h_ready), DV / 32);
+    mbar_init(smem_u32(&sh->p_ready), 8);
     mbar_init(smem_u32(&sh->o_ready), 1);
-    mbar_init(smem_u32(&sh->o_free), 4);
+    mbar_init(smem_u32(&sh->o_free), 8);
     mbar_init(smem_u32(&sh->dh_ready), 1);
-    mbar_init(smem_u32(&sh->dh_free), 4);
-    mbar_init(smem_u32(&sh->tail), 4);
+    mbar_init(smem_u32(&sh->dh_free), DV / 32);
+    mbar_init(smem_u32(&sh->tail), DV / 32);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh->pair[i]), 2);
     mbar_init(smem_u32(&sh->done1), 1);
     mbar_init(smem_u32(&sh->done2), 1);
     sh->abort = 0;
@@ -219,12 +236,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   if (warp == 2) tmem_alloc(smem_u32(&sh->tmem), 512);
   const float ld2 = log2_decay(a.log_decay[h]);
   for (int i = tid; i <= 2 * kC; i += kThreads) sh->pw[i] = i < kC ? 0.f : exp2f(ld2 * (float)(i - kC));
+  if (tid < 32) sh->column[tid] = exp2f(ld2 * (float)(31 - tid));
   const float* pw = sh->pw + kC;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
-  const WaitCtx wc{&sh->abort, a.status, a.wait_ns};
+  const WaitCtx wc(&sh->abort, a.status, a.wait_ns);
 
   const int n = sh->n, t0 = sh->t0, seg = sh->seg, nseg = sh->nseg;
   const int chunks = (n + kC - 1) / kC;
@@ -238,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const int quad = warp & 3;
 
   if (warp < 4) {
-    regs_down<56>();
+    regs_down<40>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
@@ -270,9 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const uint32_t id_s = idesc_16(F16, kC, kC, false, false);
       const uint32_t id_h = idesc_16(F16, kC, DV, false, false);
       const uint32_t id_o = idesc_16(F16, kC, DV, false, true);
+      const uint64_t dh = desc_kmajor(smem_u32(Hb));
       for (int c = 0; c < chunks; ++c) {
         const int s = c % kStages;
         const uint32_t q = smem_u32(stage(c)), k = q + QC * kChunkBytes, v = k + KC * kChunkBytes;
+        const uint64_t dq = desc_kmajor(q), dk = desc_kmajor(k), dv = desc_mnmajor(v, kChunkBytes);
         if (!wait_bar_warp(bar(sh->kv_full[s]), phase(c), wc)) break;
         if (!wait_bar_warp(bar(sh->q_full[s]), phase(c), wc)) break;
         tc_fence_after();
@@ -280,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
           for (int x = 0; x < KC * 4; ++x) {
             const uint32_t at = (x >> 2) * kChunkBytes + (x & 3) * 32;
-            mma_ss(tmem + kColS, desc_kmajor(q + at), desc_kmajor(k + at), id_s, x);
+            mma_ss(tmem + kColS, dq + desc_step(at), dk + desc_step(at), id_s, x);
           }
           mma_commit(bar(sh->s_ready));
         }
@@ -290,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (lane == 0) {
 #pragma unroll
           for (int x = 0; x < KC * 4; ++x)
-            mma_ss(tmem + kColO, desc_kmajor(q + (x >> 2) * kChunkBytes + (x & 3) * 32),
-                   desc_kmajor(smem_u32(Hb) + (x >> 2) * (DV * 128) + (x & 3) * 32), id_h, x);
+            mma_ss(tmem + kColO, dq + desc_step((x >> 2) * kChunkBytes + (x & 3) * 32),
+                   dh + desc_step((x >> 2) * (DV * 128) + (x & 3) * 32), id_h, x);
           mma_commit(bar(sh->qh_ready));
         }
         if (ragged && c == chunks - 1 && !wait_bar_warp(bar(sh->tail), 0, wc)) break;
@@ -300,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (lane == 0) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            mma_ts(tmem + kColO, tmem + kColS + x * 8, desc_mnmajor(v + x * 2048, kChunkBytes), id_o, 1);
+            mma_ts(tmem + kColO, tmem + kColS + (x >> 1) * 32 + (x & 1) * 8, dv + desc_step(x * 2048), id_o, 1);
           mma_commit(bar(sh->o_ready));
           mma_commit(bar(sh->kv_empty[s]));
         }
@@ -314,10 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const uint32_t id_d = idesc_16(F16, kC, DK, false, true);
       bool ok = true;
       for (int c = 0; c < deltas && ok; ++c) {
-        const uint32_t k = smem_u32(stage(c)) + QC * kChunkBytes;
+        const uint64_t dk = desc_mnmajor(smem_u32(stage(c)) + QC * kChunkBytes, kChunkBytes);
         if (!(ok = wait_bar_warp(bar(sh->kv_full[c % kStages]), phase(c), wc))) break;
         if (ragged && c == chunks - 1 && !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;
         if (c > 0 && !(ok = wait_bar_warp(bar(sh->dh_free), (c - 1) & 1, wc))) break;
+#pragma unroll 1
         for (int g = 0; g < 4 && ok; ++g) {
           const int b = g & 1;                       // quarter 4 c + g: buffer g % 2, its use 2 c + g / 2
           if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), g >> 1, wc))) break;
@@ -328,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
               for (int x = 0; x < 2; ++x)
                 mma_ts(tmem + kColH, tmem + kColV + b * 64 + t * 16 + x * 8,
-                       desc_mnmajor(k + (g * 2 + x) * 2048, kChunkBytes), id_d, g | (kTerms - 1 - t) | x);
+                       dk + desc_step((g * 2 + x) * 2048), id_d, g | (kTerms - 1 - t) | x);
             mma_commit(bar(sh->v_free[b]));
             if (g == 3) {
               mma_commit(bar(sh->dh_ready));
@@ -355,130 +376,141 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
+   regs_down<88>();
+   if (warp < 12 && !p.state_only) {
     // ------------------------------------------------------------ rows
-    regs_down<120>();
-    const int i = quad * 32 + lane;   // token of the chunk
+    const int half = (warp >> 2) - 1;   // this thread's blocks of 32 columns: half, half + 2
+    const int i = quad * 32 + lane;     // token of the chunk
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const float reach = pw[i + 1] * a.scale;
-    float2 column[16];                // lambda^(31-y) of a block's columns
-#pragma unroll
-    for (int y = 0; y < 16; ++y) column[y] = make_float2(pw[31 - 2 * y], pw[30 - 2 * y]);
-    if (!p.state_only) {
-      for (int c = 0; c < chunks; ++c) {
-        if (!wait_bar_warp(bar(sh->s_ready), c & 1, wc)) break;
-        tc_fence_after();
-        float pf = 1.f, pback = 1.f;       // fp16: the row of P brought into its range
-        if (F16) {
-          float mx = 0.f;
-          for (int x = 0; x <= quad; ++x) {
-            uint32_t s[32];
-            tmem_ld32(lanes + kColS + x * 32, s);
-            tmem_wait_ld();
-#pragma unroll
-            for (int y = 0; y < 32; ++y) {
-              const float v = x * 32 + y <= i ? fabsf(__uint_as_float(s[y])) : 0.f;
-              mx = fmaxf(mx, v);
-            }
-          }
-          pf = half_range(mx * a.scale, &pback);
-        }
-        const float ps = a.scale * pf;
-        // (Rolled loops: the four groups' code has to fit the instruction cache together.)
+    uint32_t turn = 0;                  // (fp16)
+    auto pair_sync = [&]() -> bool {    // the rows' two warps meet
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh->pair[quad]));
+      const bool r = wait_bar_warp(bar(sh->pair[quad]), turn, wc);
+      turn ^= 1;
+      return r;
+    };
+    for (int c = 0; c < chunks; ++c) {
+      if (!wait_bar_warp(bar(sh->s_ready), c & 1, wc)) break;
+      tc_fence_after();
+      float pf = 1.f, pback = 1.f;       // fp16: the row of P brought into its range
+      if (F16) {
+        float mx = 0.f;
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {      // P overwrites S behind the columns already read
+        for (int x = half; x <= quad; x += 2) {
           uint32_t s[32];
-          if (x < quad) {
-            // Every column lies before the row: lambda^(i-j) = lambda^(i-e) lambda^(e-j)
-            // with e the block's last column, one power per thread, one per column.
-            tmem_ld32(lanes + kColS + x * 32, s);
-            tmem_wait_ld();
-            const float f = ps * pw[i - (x * 32 + 31)];
-            const float2 f2 = make_float2(f, f);
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              const float2 v = mul2(mul2(make_float2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), f2), column[y >> 1]);
-              s[y >> 1] = pack16<F16>(v.x, v.y);
-            }
-          } else if (x == quad) {
-            // The diagonal's block (the table is 0 where the column lies behind the row;
-            // what S holds there may be anything, so it is also replaced).
-            tmem_ld32(lanes + kColS + x * 32, s);
-            tmem_wait_ld();
-            const float* w = pw + lane;
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              const float s0 = y <= lane ? __uint_as_float(s[y]) : 0.f;
-              const float s1 = y + 1 <= lane ? __uint_as_float(s[y + 1]) : 0.f;
-              s[y >> 1] = pack16<F16>(s0 * (ps * w[-y]), s1 * (ps * w[-y - 1]));
-            }
-          } else {
-#pragma unroll
-            for (int y = 0; y < 16; ++y) s[y] = 0;
-          }
-          tmem_st16(lanes + kColS + x * 16, s);
-        }
-        if (!wait_bar_warp(bar(sh->qh_ready), c & 1, wc)) break;
-        tc_fence_after();
-        const float f = reach * pf;
-#pragma unroll 1
-        for (int x = 0; x < DV; x += 32) {
-          uint32_t o[32];
-          tmem_ld32(lanes + kColO + x, o);
+          tmem_ld32(lanes + kColS + x * 32, s);
           tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
+            const float v = x * 32 + y <= i ? fabsf(__uint_as_float(s[y])) : 0.f;
+            mx = fmaxf(mx, v);
+          }
+        }
+        sh->mx[half][i] = exponent_field(mx * fabsf(a.scale));
+        if (!pair_sync()) break;
+        pf = half_range(exponent_value(max(sh->mx[0][i], sh->mx[1][i])), &pback);
+      }
+      const float ps = a.scale * pf;
+      // (Rolled loops: the groups' code has to fit the instruction cache together.)
+#pragma unroll 1
+      for (int x = half; x < 4; x += 2) {   // P of a block goes over the first half of its S
+        uint32_t s[32];
+        if (x <= quad) {
+          tmem_ld32(lanes + kColS + x * 32, s);
+          tmem_wait_ld();
+        }
+        if (x < quad) {
+          // Every column lies before the row: lambda^(i-j) = lambda^(i-e) lambda^(e-j)
+          // with e the block's last column, one power per thread, one per column.
+          const float f = ps * pw[i - (x * 32 + 31)];
+          const float4* w = reinterpret_cast<const float4*>(sh->column);
+#pragma unroll
+          for (int y = 0; y < 32; y += 4) {
+            const float4 e = w[y >> 2];
+            const float2 u = mul2(mul2(make_float2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), make_float2(f, f)), make_float2(e.x, e.y));
+            const float2 v = mul2(mul2(make_float2(__uint_as_float(s[y + 2]), __uint_as_float(s[y + 3])), make_float2(f, f)), make_float2(e.z, e.w));
+            s[y >> 1] = pack16<F16>(u.x, u.y);
+            s[(y >> 1) + 1] = pack16<F16>(v.x, v.y);
+          }
+        } else if (x == quad) {
+          // The diagonal's block (the table is 0 where the column lies behind the row;
+          // what S holds there may be anything, so it is also replaced).
+          const float* w = pw + lane;
 #pragma unroll
           for (int y = 0; y < 32; y += 2) {
-            float2 g = make_float2(f, f);
-            if (F16) g = mul2(g, make_float2(exponent_value(sh->cs[c & 1][x + y]), exponent_value(sh->cs[c & 1][x + y + 1])));
-            g = mul2(g, make_float2(__uint_as_float(o[y]), __uint_as_float(o[y + 1])));
-            o[y] = __float_as_uint(g.x);
-            o[y + 1] = __float_as_uint(g.y);
+            const float s0 = y <= lane ? __uint_as_float(s[y]) : 0.f;
+            const float s1 = y + 1 <= lane ? __uint_as_float(s[y + 1]) : 0.f;
+            s[y >> 1] = pack16<F16>(s0 * (ps * w[-y]), s1 * (ps * w[-y - 1]));
           }
-          tmem_st32(lanes + kColO + x, o);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 16; ++y) s[y] = 0;
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh->p_ready));
-        if (!wait_bar_warp(bar(sh->o_ready), c & 1, wc)) break;
-        tc_fence_after();
-        // A whole chunk leaves by TMA through the shared memory of its Q tile, which
-        // no MMA reads any more; a request's last rows are stored one by one.
-        const bool whole = !(ragged && c == chunks - 1);
-        unsigned char* tile = stage(c);
-        uint16_t* dst = a.out + ((int64_t)(t0 + c * kC + i) * a.H + h) * DV;
+        tmem_st16(lanes + kColS + x * 32, s);
+      }
+      if (!wait_bar_warp(bar(sh->qh_ready), c & 1, wc)) break;
+      tc_fence_after();
+      const float f = reach * pf;
 #pragma unroll 1
-        for (int x = 0; x < DV; x += 32) {
-          uint32_t o[32];
-          tmem_ld32(lanes + kColO + x, o);
-          tmem_wait_ld();
+      for (int x = half * 32; x < DV; x += 64) {
+        uint32_t o[32];
+        tmem_ld32(lanes + kColO + x, o);
+        tmem_wait_ld();
 #pragma unroll
-          for (int y = 0; y < 32; y += 2)
-            o[y >> 1] = pack16<F16>(__uint_as_float(o[y]) * pback, __uint_as_float(o[y + 1]) * pback);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint4 w = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-            if (whole)
-              *reinterpret_cast<uint4*>(tile + (x >> 6) * kChunkBytes + i * 128 +
-                                        (((((x & 63) >> 3) + y) ^ (i & 7)) << 4)) = w;
-            else if (i < last_n)
-              reinterpret_cast<uint4*>(dst + x)[y] = w;
-          }
+        for (int y = 0; y < 32; y += 2) {
+          float2 g = make_float2(f, f);
+          if (F16) g = mul2(g, make_float2(exponent_value(sh->cs[c & 1][x + y]), exponent_value(sh->cs[c & 1][x + y + 1])));
+          g = mul2(g, make_float2(__uint_as_float(o[y]), __uint_as_float(o[y + 1])));
+          o[y] = __float_as_uint(g.x);
+          o[y + 1] = __float_as_uint(g.y);
         }
-        tc_fence_before();
-        if (whole) fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(sh->o_free));
-          if (whole) mbar_arrive(bar(sh->o_staged));
+        tmem_st32(lanes + kColO + x, o);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh->p_ready));
+      if (!wait_bar_warp(bar(sh->o_ready), c & 1, wc)) break;
+      tc_fence_after();
+      // A whole chunk leaves by TMA through the shared memory of its Q tile; a
+      // request's last rows are stored one by one.
+      const bool whole = !(ragged && c == chunks - 1);
+      unsigned char* tile = stage(c);
+      uint16_t* dst = a.out + ((int64_t)(t0 + c * kC + i) * a.H + h) * DV;
+#pragma unroll 1
+      for (int x = half * 32; x < DV; x += 64) {
+        uint32_t o[32];
+        tmem_ld32(lanes + kColO + x, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 32; y += 2)
+          o[y >> 1] = pack16<F16>(__uint_as_float(o[y]) * pback, __uint_as_float(o[y + 1]) * pback);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint4 w = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          if (whole)
+            *reinterpret_cast<uint4*>(tile + (x >> 6) * kChunkBytes + i * 128 + (((((x & 63) >> 3) + y) ^ (i & 7)) << 4)) = w;
+          else if (i < last_n)
+            reinterpret_cast<uint4*>(dst + x)[y] = w;
         }
       }
+      tc_fence_before();
+      if (whole) fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(sh->o_free));
+        if (whole) mbar_arrive(bar(sh->o_staged));
+      }
     }
-  } else if (warp < 12) {
+   } else if ((warp < 8 || warp >= 12) && quad * 32 < DV) {
     // ------------------------------------------------------------ decay
-    regs_down<104>();
+    // The first launch of a split call has no rows: there the first row warps take
+    // the odd quarters.
+    const int g0 = warp < 8 ? 1 : 0, gs = p.state_only ? 2 : 1;
     const int d = quad * 32 + lane;                    // column of V
-    const bool live = d < DV;                          // (a whole warp)
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + kColV;
     bool ok = true;
     for (int c = 0; c < chunks && ok; ++c) {
@@ -490,34 +522,33 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         // Zeros in K and V behind the last token.
         for (int x = 0; x < KC + VC; ++x) {
           uint4* w = reinterpret_cast<uint4*>(kv + x * kChunkBytes + last_n * 128);
-          for (int i = quad * 32 + lane; i < (kC - last_n) * 8; i += 128) w[i] = make_uint4(0, 0, 0, 0);
+          for (int i = d; i < (kC - last_n) * 8; i += DV) w[i] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
-        asm volatile("bar.sync 1, 128;" ::: "memory");   // (the decay warps, who read the zeros too)
+        __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh->tail));
-        if (c >= deltas) break;
+        if (c >= deltas || !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;   // (they read the zeros below)
       }
       const int m = short_chunk ? last_n : kC;
-      const unsigned char* v = kv + (KC + (live ? d >> 6 : 0)) * kChunkBytes + (d & 7) * 2;
+      const unsigned char* v = kv + (KC + (d >> 6)) * kChunkBytes + (d & 7) * 2;
       const int piece = (d >> 3) & 7;
       auto value = [&](int j) {
         return to_float<F16>(*reinterpret_cast<const uint16_t*>(v + j * 128 + ((piece ^ (j & 7)) << 4)));
       };
       const float* fade = pw + m - 1;          // fade[-j] = lambda^(m-1-j), 0 behind the last token
       float vf = 1.f, vback = 1.f;
-      if (F16 && live) {                       // the column of V brought into fp16's range
+      if (F16) {                               // the column of V brought into fp16's range
         float mx = 0.f;
 #pragma unroll 8
         for (int j = 0; j < kC; ++j) mx = fmaxf(mx, fabsf(value(j)));
         vf = half_range(mx, &vback);
       }
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
+      for (int g = g0; g < 4; g += gs) {
         // The buffer's last use was two quarters ago.
         if ((c > 0 || g > 1) && !(ok = wait_bar_warp(bar(sh->v_free[g & 1]), (g >> 1) ^ 1, wc))) break;
         tc_fence_after();
-        if (live) {
-          if (F16 && g == 0) sh->vs[c & 1][d] = exponent_field(vback);
+        if (F16 && g == 0) sh->vs[c & 1][d] = exponent_field(vback);
 #pragma unroll 1
           for (int z = 0; z < 2; ++z) {        // 16 tokens: 8 columns of each term
             uint32_t w[3][8];
@@ -537,18 +568,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
             for (int t = 0; t < kTerms; ++t) tmem_st8(lanes + (g & 1) * 64 + t * 16 + z * 8, w[t]);
           }
-          tmem_wait_st();
-        }
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh->v_ready[g & 1]));
       }
     }
+   }
   } else {
     // ------------------------------------------------------------ state
-    regs_up<232>();
+    regs_up<176>();
+    if (quad * 32 < DV) {
     const int d = quad * 32 + lane;                    // column of H
-    const bool live = d < DV;                          // (a whole warp)
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + kColH;
     const int64_t head = (int64_t)DK * DV;
     float H[DK];
@@ -563,28 +594,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       for (int x = 0; x < DK; ++x) dst[x * DV + d] = H[x];
     };
     float* ends = a.seg_state + ((int64_t)sh->first * a.H + h) * head;   // [segment] of this request, H heads apart
-    if (live) {
-      if (seg == 0) {
-        if (nseg > 1 && !p.state_only)
-          load(ends + (int64_t)(nseg - 1) * a.H * head);   // the first launch's copy: state_out may be state_in
-        else if (a.state_in)
-          load(a.state_in + ((int64_t)place * a.H + h) * head);
-        if (p.state_only) store(ends + (int64_t)(nseg - 1) * a.H * head);
-      } else if (!p.state_only) {
-        // lambda^(seg_len (seg - 1 - s)) E_s summed over the segments s before this one.
-        const float f = exp2f(fmaxf(ld2 * (float)a.seg_len, -300.f));
-        load(ends);
-        for (int s = 1; s < seg; ++s) {
-          const float* e = ends + (int64_t)s * a.H * head;
+    if (seg == 0) {
+      if (nseg > 1 && !p.state_only)
+        load(ends + (int64_t)(nseg - 1) * a.H * head);   // the first launch's copy: state_out may be state_in
+      else if (a.state_in)
+        load(a.state_in + ((int64_t)place * a.H + h) * head);
+      if (p.state_only) store(ends + (int64_t)(nseg - 1) * a.H * head);
+    } else if (!p.state_only) {
+      // lambda^(seg_len (seg - 1 - s)) E_s summed over the segments s before this one.
+      const float f = exp2f(fmaxf(ld2 * (float)a.seg_len, -300.f));
+      load(ends);
+      for (int s = 1; s < seg; ++s) {
+        const float* e = ends + (int64_t)s * a.H * head;
 #pragma unroll
-          for (int x = 0; x < DK; x += 16) {
-            float t[16];
+        for (int x = 0; x < DK; x += 16) {
+          float t[16];
 #pragma unroll
-            for (int y = 0; y < 16; ++y) t[y] = e[(x + y) * DV + d];
+          for (int y = 0; y < 16; ++y) t[y] = e[(x + y) * DV + d];
 #pragma unroll
-            for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, H[x + y], t[y]);
-            asm volatile("" ::: "memory");   // (no more than 16 loads ahead: registers)
-          }
+          for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, H[x + y], t[y]);
+          asm volatile("" ::: "memory");   // (no more than 16 loads ahead: registers)
         }
       }
     }
@@ -593,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       if (!p.state_only) {
         // H in the operands' type, once Q H of the chunk before has read the last one.
         if (c > 0 && !(ok = wait_bar_warp(bar(sh->qh_ready), (c - 1) & 1, wc))) break;
-        if (live) {
+        {
           float hf = 1.f;
           if (F16) {
             float mx = 0.f, back;
@@ -619,24 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       if (c >= deltas) break;
       if (!(ok = wait_bar_warp(bar(sh->dh_ready), c & 1, wc))) break;
       tc_fence_after();
-      if (live) {
+      {
         const float f = pw[ragged && c == chunks - 1 ? last_n : kC];
         const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) : 1.f;
 #pragma unroll
-        for (int x = 0; x < DK; x += 32) {
-          uint32_t e[32];
-          tmem_ld32(lanes + x, e);
+        for (int x = 0; x < DK; x += 16) {
+          uint32_t e[16];
+          tmem_ld16(lanes + x, e);
           tmem_wait_ld();
 #pragma unroll
-          for (int y = 0; y < 32; ++y) H[x + y] = fmaf(f, H[x + y], __uint_as_float(e[y]) * vback);
+          for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, H[x + y], __uint_as_float(e[y]) * vback);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh->dh_free));
     }
-    if (ok && live && final_state)
+    if (ok && final_state)
       store(p.state_only ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
+    }
   }
   tc_fence_before();
   __syncthreads();

@@ -35,29 +35,30 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 
 // What a CTA's waits share: the abort flag (shared memory), the status word and
-// the limit of each wait.
+// the limit of each wait, as a number of tries.  A try that fails has been
+// suspended for up to about 20 us, so `limit_ns` is an upper bound of the order of
+// the wait itself; counting tries instead of reading a clock keeps the loop to a
+// few instructions, of which a kernel holds dozens of copies (its code competes
+// for the instruction cache).
 struct WaitCtx {
   volatile int* abort_flag;
   uint32_t* status;
-  uint64_t limit_ns;
+  uint32_t tries;
+  __device__ WaitCtx(int* flag, uint32_t* st, uint64_t limit_ns)
+      : abort_flag(flag), status(st), tries((uint32_t)(limit_ns / 10000) + 1) {}
 };
-
-static __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, const WaitCtx& c) {
-  const uint64_t t0 = gtimer();
-  for (;;) {
-    if (mbar_try(bar, parity)) return true;
-    if (*c.abort_flag) return false;
-    if (gtimer() - t0 > c.limit_ns) {
-      *c.abort_flag = 1;
-      raise_status(c.status, DSA_DEVICE_TIMEOUT);
-      return false;
-    }
-  }
-}
 
 // Bounded wait of one thread; false once the CTA is aborting.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitCtx& c) {
-  return mbar_try(bar, parity) || wait_slow(bar, parity, c);
+  uint32_t left = c.tries;
+  while (!mbar_try(bar, parity)) {
+    if (*c.abort_flag || --left == 0) {
+      if (!*c.abort_flag) raise_status(c.status, DSA_DEVICE_TIMEOUT);
+      *c.abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
 }
 
 // The same by a whole warp, which goes on together.
@@ -90,7 +91,9 @@ __device__ __forceinline__ void tc_fence_after() {
 }
 
 // Shared-memory matrix descriptors (128-byte swizzle, 8-row groups 1024 bytes
-// apart, descriptor version 1).
+// apart, descriptor version 1).  A descriptor plus desc_step(bytes) is that of the
+// tile `bytes` further on.
+__device__ __forceinline__ constexpr uint64_t desc_step(uint32_t bytes) { return bytes >> 4; }
 __device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
          ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
