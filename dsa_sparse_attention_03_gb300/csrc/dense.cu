@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
   unsigned char* Qs = smem;
   unsigned char* ring = smem + NW * kQBytes;
   Shared* sh = reinterpret_cast<Shared*>(ring + NS * kChunkBytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   const int h = blockIdx.x % a.H_kv;
   const int split = (blockIdx.x / a.H_kv) % a.splits;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const WaitCtx wc(&sh->abort, a.status, a.wait_ns);
 
   // K/V tiles of this CTA: [lo, hi); row tile w takes those below its own end.
@@ -252,6 +252,8 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
     const uint32_t ids = idesc_16(F16, kTile, kTile, false, false);
     const uint32_t ido = idesc_16(F16, kTile, DV, false, true);
     const uint32_t ido64 = idesc_16(F16, kTile, 64, false, true);
+    const uint64_t dq = desc_kmajor(smem_u32(Qs)), dr = desc_kmajor(smem_u32(ring));
+    const uint64_t dv = desc_mnmajor(smem_u32(ring), kChunkBytes);
     auto wait_chunk = [&](int n) { return wait_bar_warp(smem_u32(&sh->full[n % NS]), (n / NS) & 1, wc); };
     // S of row tile i against K tile jj.
     auto issue_s = [&](int i, int jj) -> bool {
@@ -260,20 +262,16 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
       for (int c = 0; c < KC; ++c) {
         if (!wait_chunk(n + c)) return false;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t qa = smem_u32(Qs + i * kQBytes + c * kChunkBytes);
-          const uint32_t ka = smem_u32(ring + ((n + c) % NS) * kChunkBytes);
+        const uint64_t qa = dq + desc_step(i * kQBytes + c * kChunkBytes);
+        const uint64_t ka = dr + desc_step(((n + c) % NS) * kChunkBytes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss(tmem + i * 128, desc_kmajor(qa + kk * 32), desc_kmajor(ka + kk * 32), ids, c | kk);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss(tmem + i * 128, qa + desc_step(kk * 32), ka + desc_step(kk * 32), ids, c | kk);
       }
-      if (lane == 0) {
-        mma_commit(smem_u32(&sh->sfull[i]));
-        if (NW == 1 || i == 1 || jj >= cnt[1])
+      mma_commit(smem_u32(&sh->sfull[i]));
+      if (NW == 1 || i == 1 || jj >= cnt[1])
 #pragma unroll
-          for (int c = 0; c < KC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
-      }
+        for (int c = 0; c < KC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
       return true;
     };
     // O of row tile i += P V for V tile jj.
@@ -294,26 +292,23 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
         __syncwarp();
       }
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t od = tmem + NW * 128 + i * 128, pa = tmem + i * 128;
-        const uint32_t v0 = smem_u32(ring + (n % NS) * kChunkBytes);
-        const uint32_t v1 = smem_u32(ring + ((n + VC - 1) % NS) * kChunkBytes);
-        if (VC == 1 || v1 > v0) {
+      const uint32_t od = tmem + NW * 128 + i * 128, pa = tmem + i * 128;
+      const int s0 = n % NS, s1 = (n + VC - 1) % NS;
+      if (VC == 1 || s1 > s0) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(od, pa + kk * 8, dv + desc_step(s0 * kChunkBytes + kk * 2048), ido, jj | kk);
+      } else {   // the tile's second chunk wrapped round the ring
+#pragma unroll
+        for (int c = 0; c < VC; ++c)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(od, pa + kk * 8, desc_mnmajor(v0 + kk * 2048, kChunkBytes), ido, jj | kk);
-        } else {   // the tile's second chunk wrapped round the ring
-#pragma unroll
-          for (int c = 0; c < VC; ++c)
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(od + c * 64, pa + kk * 8, desc_mnmajor((c ? v1 : v0) + kk * 2048, kChunkBytes), ido64, jj | kk);
-        }
-        if (jj == cnt[i] - 1) mma_commit(smem_u32(&sh->ofull[i]));
-        if (NW == 1 || i == 1 || jj >= cnt[1])
-#pragma unroll
-          for (int c = 0; c < VC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
+            mma_ts(od + c * 64, pa + kk * 8, dv + desc_step((c ? s1 : s0) * kChunkBytes + kk * 2048), ido64, jj | kk);
       }
+      if (jj == cnt[i] - 1) mma_commit(smem_u32(&sh->ofull[i]));
+      if (NW == 1 || i == 1 || jj >= cnt[1])
+#pragma unroll
+        for (int c = 0; c < VC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
       return true;
     };
     bool ok = true;
@@ -324,7 +319,7 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
         if (jj < cnt[i]) ok = issue_o(i, jj);
         if (ok && jj + 1 < cnt[i]) ok = issue_s(i, jj + 1);
       }
-    if (lane == 0 && steps > 0) {   // every MMA and commit has landed
+    if (steps > 0) {   // every MMA and commit has landed
       mma_commit(smem_u32(&sh->done));
       drain_bar(smem_u32(&sh->done), 0, a.wait_ns);
     }

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   unsigned char* smem = smem_raw;   // (1024-byte aligned: checked below)
   unsigned char* Hb = smem + kStages * kStage;     // H in the operands' type, D_v rows of D_k, K-major
   Shared* sh = reinterpret_cast<Shared*>(Hb + DV * DK * 2);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int h = blockIdx.x % a.H;
 
   if (smem_u32(smem_raw) & 1023) {
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const WaitCtx wc(&sh->abort, a.status, a.wait_ns);
 
   const int n = sh->n, t0 = sh->t0, seg = sh->seg, nseg = sh->nseg;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (!wait_bar_warp(bar(sh->kv_full[s]), phase(c), wc)) break;
         if (!wait_bar_warp(bar(sh->q_full[s]), phase(c), wc)) break;
         tc_fence_after();
-        if (lane == 0) {
+        {
 #pragma unroll
           for (int x = 0; x < KC * 4; ++x) {
             const uint32_t at = (x >> 2) * kChunkBytes + (x & 3) * 32;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (!wait_bar_warp(bar(sh->h_ready), c & 1, wc)) break;
         if (c > 0 && !wait_bar_warp(bar(sh->o_free), (c - 1) & 1, wc)) break;
         tc_fence_after();
-        if (lane == 0) {
+        {
 #pragma unroll
           for (int x = 0; x < KC * 4; ++x)
             mma_ss(tmem + kColO, dq + desc_step((x >> 2) * kChunkBytes + (x & 3) * 32),
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (ragged && c == chunks - 1 && !wait_bar_warp(bar(sh->tail), 0, wc)) break;
         if (!wait_bar_warp(bar(sh->p_ready), c & 1, wc)) break;
         tc_fence_after();
-        if (lane == 0) {
+        {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             mma_ts(tmem + kColO, tmem + kColS + (x >> 1) * 32 + (x & 1) * 8, dv + desc_step(x * 2048), id_o, 1);
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           mma_commit(bar(sh->kv_empty[s]));
         }
       }
-      if (lane == 0 && chunks > 0) {
+      if (chunks > 0) {
         mma_commit(bar(sh->done1));
         drain_bar(bar(sh->done1), 0, a.wait_ns);
       }
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           const int b = g & 1;                       // quarter 4 c + g: buffer g % 2, its use 2 c + g / 2
           if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), g >> 1, wc))) break;
           tc_fence_after();
-          if (lane == 0) {
+          {
 #pragma unroll
             for (int t = kTerms - 1; t >= 0; --t)    // the smallest terms first: the sum stays small meanwhile
 #pragma unroll
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           }
         }
       }
-      if (lane == 0 && deltas > 0) {
+      if (deltas > 0) {
         mma_commit(bar(sh->done2));
         drain_bar(bar(sh->done2), 0, a.wait_ns);
       }
