@@ -193,7 +193,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -211,6 +211,7 @@ class Problem:
 
     def __init__(self, **kw):
         self._keep = {}
+        self._on = None      # device on which the tensors were found (_check_call)
         s = self._struct()
         for f, _ in self._struct._fields_:
             v = kw.get(f)
@@ -244,6 +245,7 @@ class Problem:
                    row_offsets=row_offsets, row_len=row_len, kv_scale=kv_scale)
 
     def set(self, **kw):
+        self._on = None
         for f, v in kw.items():
             if hasattr(v, "data_ptr"):
                 self._keep[f] = v
@@ -252,7 +254,7 @@ class Problem:
         return self
 
     def __getattr__(self, name):
-        if name in ("c", "_keep"):
+        if name in ("c", "_keep", "_on"):
             raise AttributeError(name)
         return getattr(self.c, name)
 
@@ -438,18 +440,27 @@ def _fp16_flag(**ts):
     raise ValueError(f"{', '.join(ts)} must all be bfloat16 or all float16, got {sorted(map(str, kinds))}")
 
 
-def _on_current_device(prob, *ts):
-    """The call runs on the current CUDA device: every tensor has to be there."""
+def _check_call(prob, outputs, ws):
+    """What a call checks of its tensors: each output (name, tensor, shape, dtype; the
+    tensor may be None) and that everything is on the current CUDA device.  The
+    problem's own tensors are looked over once, until ``set`` changes one."""
     import torch
-    for t in list(prob._keep.values()) + [t for t in ts if t is not None]:
-        if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device")
-
-
-def _check_output(name, t, shape, dtype):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else None
+    if prob._on != dev or dev is None:
+        for t in prob._keep.values():
+            if t.get_device() != dev:
+                raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device")
+        prob._on = dev
+    for name, t, shape, dtype in outputs:
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if ws.get_device() != dev:
+        raise ValueError(f"the workspace is on {ws.device}, not on the current CUDA device")
 
 
 def _check_ints(n, **ts):
@@ -515,9 +526,8 @@ def dsa_dense_attn(prob: DenseProblem, out, lse, ws, stream=None) -> None:
     """out [R, H_q, D_v] in the operands' type; lse [R, H_q] float32 or None."""
     import torch
     c = prob.c
-    _check_output("out", out, (c.R, c.H_q, c.D_v), prob._keep["q"].dtype)
-    _check_output("lse", lse, (c.R, c.H_q), torch.float32)
-    _on_current_device(prob, out, lse, ws)
+    _check_call(prob, (("out", out, (c.R, c.H_q, c.D_v), prob._keep["q"].dtype),
+                       ("lse", lse, (c.R, c.H_q), torch.float32)), ws)
     _check(_lib.dsa_dense_attn(ctypes.byref(c), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
 
 
@@ -576,10 +586,10 @@ def alloc_linear_workspace(prob: LinearProblem, device="cuda"):
 def _linear_call(fn, prob, state_in, state_out, out, ws, stream):
     import torch
     c = prob.c
-    _check_output("out", out, (c.R, c.H, c.D_v), prob._keep["q"].dtype)
-    for name, t in (("state_in", state_in), ("state_out", state_out)):
-        _check_output(name, t, (c.n_states, c.H, c.D_k, c.D_v), torch.float32)
-    _on_current_device(prob, state_in, state_out, out, ws)
+    states = (c.n_states, c.H, c.D_k, c.D_v)
+    _check_call(prob, (("out", out, (c.R, c.H, c.D_v), prob._keep["q"].dtype),
+                       ("state_in", state_in, states, torch.float32),
+                       ("state_out", state_out, states, torch.float32)), ws)
     _check(fn(ctypes.byref(c), _ptr(state_in), _ptr(state_out), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
 
 
