@@ -19,8 +19,10 @@
 //   warp 0      producer: K and V tiles by TMA, in 16 KB chunks of 64 columns
 //               through one ring, in the order the MMAs use them
 //   warp 1      issues the MMAs: S = Q K^T (both operands in shared memory) and
-//               O += P V (P in tensor memory, over the S it came from)
-//   4 NW warps  softmax: a thread holds one row of S
+//               O += P V (P in tensor memory, over the S it came from, in two
+//               halves, so that the product starts while the second is computed)
+//   warps 4..   softmax, four warps to a row tile: a thread holds one row of S
+// Registers are dealt with setmaxnreg: 56 to warps 0-3, 224 (200) to the softmax.
 // With two row tiles the tensor core works on one while the other's softmax
 // runs; with one, two CTAs share an SM and alternate.
 //
@@ -67,7 +69,7 @@ struct DenseArgs {
 
 struct __align__(16) Shared {
   uint64_t full[16], empty[16];   // ring of chunks
-  uint64_t sfull[2], pready[2], ofull[2], done;
+  uint64_t sfull[2], pready[2][2], ofull[2], done;
   uint32_t tmem;
   int abort;
   int req, tile;                  // request and its tile; req < 0: nothing to do
@@ -135,7 +137,7 @@ __device__ void locate(const DenseArgs& a, int rows_per_cta, int idx, Shared* sh
 }
 
 template <int DK, int DV, int NW, bool F16>
-__global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
+__global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     dense_attn_kernel(const __grid_constant__ DenseArgs a) {
   constexpr int NS = ring_slots<DK, DV, NW>();
   constexpr int KC = DK / 64, VC = DV / 64;
@@ -163,7 +165,8 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh->sfull[i]), 1);
-      mbar_init(smem_u32(&sh->pready[i]), 4);
+      mbar_init(smem_u32(&sh->pready[i][0]), 4);
+      mbar_init(smem_u32(&sh->pready[i][1]), 4);
       mbar_init(smem_u32(&sh->ofull[i]), 1);
     }
     mbar_init(smem_u32(&sh->done), 1);
@@ -173,14 +176,14 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
   if (warp == 1) tmem_alloc(smem_u32(&sh->tmem), kCols);
 
   // Softmax warps: warp w of a tile reads tensor-memory lanes 32 (w % 4).. .
-  const int w = (warp - 2) >> 2;                         // row tile of this warp
+  const int w = (warp >> 2) - 1;                         // row tile of this warp
   const int trow = (warp & 3) * 32 + lane;               // row in the tile
   const int packed = (sh->tile * NW + w) * kTile + trow; // packed row in the request
-  const bool valid = warp >= 2 && packed < sh->n * a.G;
+  const bool valid = warp >= 4 && packed < sh->n * a.G;
   const int row = sh->r0 + (valid ? packed / a.G : 0);
   const int head = h * a.G + (valid ? packed % a.G : 0);
   int len = 0;
-  if (warp >= 2) {
+  if (warp >= 4) {
     if (valid) {
       const int l = a.row_len[row];
       len = min(max(l, 0), sh->len);
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
     // Q, K-major and swizzled: 16-byte pieces, consecutive threads along a row.
     const int t0 = (sh->tile * NW + w) * kTile;
     constexpr int P = DK / 8;
-    for (int i = (tid - 64) & 127; i < kTile * P; i += 128) {
+    for (int i = tid & 127; i < kTile * P; i += 128) {
       const int r = i / P, x = i % P, pk = t0 + r;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (pk < sh->n * a.G)
@@ -223,7 +226,9 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
   for (int i = 0; i < 2; ++i) cnt[i] = max(min((end[i] + kTile - 1) / kTile, hi) - lo, 0);
   const int steps = hi - lo;
 
-  if (warp == 0) {
+  if (warp < 4) {
+   regs_down<56>();
+   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       int n = 0;
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
       for (int i = max(0, n - NS); i < n; ++i)   // (an abort may leave copies in flight)
         drain_bar(smem_u32(&sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
     }
-  } else if (warp == 1) {
+   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t ids = idesc_16(F16, kTile, kTile, false, false);
     const uint32_t ido = idesc_16(F16, kTile, DV, false, true);
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
     };
     // O of row tile i += P V for V tile jj.
     auto issue_o = [&](int i, int jj) -> bool {
-      if (!wait_bar_warp(smem_u32(&sh->pready[i]), jj & 1, wc)) return false;
+      if (!wait_bar_warp(smem_u32(&sh->pready[i][0]), jj & 1, wc)) return false;
       const int n = jj * (KC + VC) + KC;
 #pragma unroll
       for (int c = 0; c < VC; ++c)
@@ -291,19 +296,23 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
         fence_proxy_async();
         __syncwarp();
       }
-      tc_fence_after();
       const uint32_t od = tmem + NW * 128 + i * 128, pa = tmem + i * 128;
       const int s0 = n % NS, s1 = (n + VC - 1) % NS;
-      if (VC == 1 || s1 > s0) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(od, pa + kk * 8, dv + desc_step(s0 * kChunkBytes + kk * 2048), ido, jj | kk);
-      } else {   // the tile's second chunk wrapped round the ring
+      for (int half = 0; half < 2; ++half) {           // P comes in two halves of 64 positions
+        if (half && !wait_bar_warp(smem_u32(&sh->pready[i][1]), jj & 1, wc)) return false;
+        tc_fence_after();
+        if (VC == 1 || s1 > s0) {
 #pragma unroll
-        for (int c = 0; c < VC; ++c)
+          for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+            mma_ts(od, pa + kk * 8, dv + desc_step(s0 * kChunkBytes + kk * 2048), ido, jj | kk);
+        } else {   // the tile's second chunk wrapped round the ring
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(od + c * 64, pa + kk * 8, dv + desc_step((c ? s1 : s0) * kChunkBytes + kk * 2048), ido64, jj | kk);
+          for (int c = 0; c < VC; ++c)
+#pragma unroll
+            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+              mma_ts(od + c * 64, pa + kk * 8, dv + desc_step((c ? s1 : s0) * kChunkBytes + kk * 2048), ido64, jj | kk);
+        }
       }
       if (jj == cnt[i] - 1) mma_commit(smem_u32(&sh->ofull[i]));
       if (NW == 1 || i == 1 || jj >= cnt[1])
@@ -323,8 +332,10 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
       mma_commit(smem_u32(&sh->done));
       drain_bar(smem_u32(&sh->done), 0, a.wait_ns);
     }
+   }
   } else {
     // ------------------------------------------------------------ softmax
+    regs_up<NW == 1 ? 200 : 224>();
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t st = lane_base + w * 128, ot = lane_base + NW * 128 + w * 128;
     const bool any = __any_sync(0xffffffffu, valid);
@@ -346,13 +357,16 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
           for (int x = 0; x < 128; ++x)
             if (x >= left) v[x] = 0xff800000u;
         }
-        float t0 = __uint_as_float(v[0]), t1 = __uint_as_float(v[1]);
+        float t[4];
 #pragma unroll
-        for (int x = 2; x < 128; x += 2) {
-          t0 = fmaxf(t0, __uint_as_float(v[x]));
-          t1 = fmaxf(t1, __uint_as_float(v[x + 1]));
-        }
-        const float mn = fmaxf(m, fmaxf(t0, t1));
+        for (int x = 0; x < 4; ++x) t[x] = __uint_as_float(v[x]);
+#pragma unroll
+        for (int x = 4; x < 124; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) t[y] = max3(t[y], __uint_as_float(v[x + y]), __uint_as_float(v[x + 4 + y]));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) t[x] = fmaxf(t[x], __uint_as_float(v[124 + x]));
+        const float mn = fmaxf(max3(m, t[0], t[1]), fmaxf(t[2], t[3]));
         if (jj == 0) {
           m = mn;
         } else if (__any_sync(0xffffffffu, (mn - m) * a.c > 8.f)) {
@@ -371,23 +385,33 @@ __global__ void __launch_bounds__(64 + 128 * NW, NW == 1 ? 2 : 1)
           }
         }
         const float mc = m == -INFINITY ? 0.f : m * a.c;
-        float s0 = 0.f, s1 = 0.f;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int x = 0; x < 128; x += 2) {
-          const float p0 = ex2(fmaf(__uint_as_float(v[x]), a.c, -mc));
-          const float p1 = ex2(fmaf(__uint_as_float(v[x + 1]), a.c, -mc));
-          s0 += p0;
-          s1 += p1;
-          v[x >> 1] = pack16<F16>(p0, p1);
+        for (int half = 0; half < 2; ++half) {   // P in two halves: the first one's product starts meanwhile
+#pragma unroll
+          for (int x = half * 64; x < half * 64 + 64; x += 2) {
+            const float2 e = fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), make_float2(a.c, a.c),
+                                  make_float2(-mc, -mc));
+            const float2 p = make_float2(ex2(e.x), ex2(e.y));
+            sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], p);
+            v[x >> 1] = pack16<F16>(p.x, p.y);
+          }
+          tmem_st32(st + half * 32, v + half * 32);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->pready[w][half]));
         }
-        l += s0 + s1;
-        tmem_st32(st, v);
-        tmem_st32(st + 32, v + 32);
-        tmem_wait_st();
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh->pready[w][0]));
+          mbar_arrive(smem_u32(&sh->pready[w][1]));
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh->pready[w]));
     }
     if (mine > 0 && ok) ok = wait_bar_warp(smem_u32(&sh->ofull[w]), 0, wc);
     tc_fence_after();
@@ -483,7 +507,7 @@ cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)a.tiles * a.splits * a.H_kv;
-  kernel<<<(unsigned)grid, 64 + 128 * NW, smem, st>>>(a);
+  kernel<<<(unsigned)grid, 128 + 128 * NW, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
   const int64_t rows = (int64_t)a.R * a.H_q;
   return launch_pdl(dense_join_kernel<DV, F16>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, (const float*)a.part,
