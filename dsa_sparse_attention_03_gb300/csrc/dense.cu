@@ -18,9 +18,11 @@
 // request has more than one tile), one K/V head and a range of K/V tiles:
 //   warp 0      producer: K and V tiles by TMA, in 16 KB chunks of 64 columns
 //               through one ring, in the order the MMAs use them
-//   warp 1      issues the MMAs: S = Q K^T (both operands in shared memory) and
-//               O += P V (P in tensor memory, over the S it came from, in two
-//               halves, so that the product starts while the second is computed)
+//   warps 1..   one per row tile issues its MMAs: S = Q K^T (both operands in shared
+//               memory) and O += P V (P in tensor memory, over the S it came from, in
+//               two halves, so that the product starts while the second is computed).
+//               The tensor core takes few MMAs ahead, so an issuer that waits leaves
+//               it idle; with two, the other row tile's go on.
 //   warps 4..   softmax, four warps to a row tile: a thread holds one row of S
 // Registers are dealt with setmaxnreg: 56 to warps 0-3, 224 (200) to the softmax.
 // With two row tiles the tensor core works on one while the other's softmax
@@ -69,7 +71,7 @@ struct DenseArgs {
 
 struct __align__(16) Shared {
   uint64_t full[16], empty[16];   // ring of chunks
-  uint64_t sfull[2], pready[2][2], ofull[2], done;
+  uint64_t sfull[2], pready[2][2], ofull[2], done[2];
   uint32_t tmem;
   int abort;
   int req, tile;                  // request and its tile; req < 0: nothing to do
@@ -161,15 +163,15 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(&sh->full[i]), 1);
-      mbar_init(smem_u32(&sh->empty[i]), 1);
+      mbar_init(smem_u32(&sh->empty[i]), NW);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh->sfull[i]), 1);
       mbar_init(smem_u32(&sh->pready[i][0]), 4);
       mbar_init(smem_u32(&sh->pready[i][1]), 4);
       mbar_init(smem_u32(&sh->ofull[i]), 1);
+      mbar_init(smem_u32(&sh->done[i]), 1);
     }
-    mbar_init(smem_u32(&sh->done), 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -252,42 +254,40 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
       for (int i = max(0, n - NS); i < n; ++i)   // (an abort may leave copies in flight)
         drain_bar(smem_u32(&sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
     }
-   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+   } else if (warp <= NW) {
+    // ------------------------------------------------------------ MMA issuers
+    const int i = warp - 1, mine = i ? cnt[1] : cnt[0];
     const uint32_t ids = idesc_16(F16, kTile, kTile, false, false);
     const uint32_t ido = idesc_16(F16, kTile, DV, false, true);
     const uint32_t ido64 = idesc_16(F16, kTile, 64, false, true);
-    const uint64_t dq = desc_kmajor(smem_u32(Qs)), dr = desc_kmajor(smem_u32(ring));
+    const uint64_t dq = desc_kmajor(smem_u32(Qs)) + desc_step(i * kQBytes), dr = desc_kmajor(smem_u32(ring));
     const uint64_t dv = desc_mnmajor(smem_u32(ring), kChunkBytes);
+    const uint32_t sd = tmem + i * 128, od = tmem + NW * 128 + i * 128;
     auto wait_chunk = [&](int n) { return wait_bar_warp(smem_u32(&sh->full[n % NS]), (n / NS) & 1, wc); };
-    // S of row tile i against K tile jj.
-    auto issue_s = [&](int i, int jj) -> bool {
+    // S against K tile jj.
+    auto issue_s = [&](int jj) -> bool {
       const int n = jj * (KC + VC);
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
         if (!wait_chunk(n + c)) return false;
         tc_fence_after();
-        const uint64_t qa = dq + desc_step(i * kQBytes + c * kChunkBytes);
-        const uint64_t ka = dr + desc_step(((n + c) % NS) * kChunkBytes);
+        const uint64_t qa = dq + desc_step(c * kChunkBytes), ka = dr + desc_step(((n + c) % NS) * kChunkBytes);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss(tmem + i * 128, qa + desc_step(kk * 32), ka + desc_step(kk * 32), ids, c | kk);
+        for (int kk = 0; kk < 4; ++kk) mma_ss(sd, qa + desc_step(kk * 32), ka + desc_step(kk * 32), ids, c | kk);
       }
       mma_commit(smem_u32(&sh->sfull[i]));
-      if (NW == 1 || i == 1 || jj >= cnt[1])
 #pragma unroll
-        for (int c = 0; c < KC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
+      for (int c = 0; c < KC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
       return true;
     };
-    // O of row tile i += P V for V tile jj.
-    auto issue_o = [&](int i, int jj) -> bool {
-      if (!wait_bar_warp(smem_u32(&sh->pready[i][0]), jj & 1, wc)) return false;
+    // O += P V for V tile jj.
+    auto issue_o = [&](int jj) -> bool {
       const int n = jj * (KC + VC) + KC;
 #pragma unroll
       for (int c = 0; c < VC; ++c)
         if (!wait_chunk(n + c)) return false;
       const int rows = kv_end - (lo + jj) * kTile;
-      if (rows < kTile && (i == 0 || jj >= cnt[0])) {   // the cache's last tile, at its first use
+      if (rows < kTile) {   // the cache's last tile (each row tile's issuer writes the same zeros)
 #pragma unroll
         for (int c = 0; c < VC; ++c) {
           uint4* p = reinterpret_cast<uint4*>(ring + ((n + c) % NS) * kChunkBytes + rows * 128);
@@ -296,41 +296,41 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
         fence_proxy_async();
         __syncwarp();
       }
-      const uint32_t od = tmem + NW * 128 + i * 128, pa = tmem + i * 128;
       const int s0 = n % NS, s1 = (n + VC - 1) % NS;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {           // P comes in two halves of 64 positions
-        if (half && !wait_bar_warp(smem_u32(&sh->pready[i][1]), jj & 1, wc)) return false;
+        if (!wait_bar_warp(smem_u32(&sh->pready[i][half]), jj & 1, wc)) return false;
         tc_fence_after();
         if (VC == 1 || s1 > s0) {
 #pragma unroll
           for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-            mma_ts(od, pa + kk * 8, dv + desc_step(s0 * kChunkBytes + kk * 2048), ido, jj | kk);
+            mma_ts(od, sd + kk * 8, dv + desc_step(s0 * kChunkBytes + kk * 2048), ido, jj | kk);
         } else {   // the tile's second chunk wrapped round the ring
 #pragma unroll
           for (int c = 0; c < VC; ++c)
 #pragma unroll
             for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-              mma_ts(od + c * 64, pa + kk * 8, dv + desc_step((c ? s1 : s0) * kChunkBytes + kk * 2048), ido64, jj | kk);
+              mma_ts(od + c * 64, sd + kk * 8, dv + desc_step((c ? s1 : s0) * kChunkBytes + kk * 2048), ido64, jj | kk);
         }
       }
-      if (jj == cnt[i] - 1) mma_commit(smem_u32(&sh->ofull[i]));
-      if (NW == 1 || i == 1 || jj >= cnt[1])
+      if (jj == mine - 1) mma_commit(smem_u32(&sh->ofull[i]));
 #pragma unroll
-        for (int c = 0; c < VC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
+      for (int c = 0; c < VC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
       return true;
     };
-    bool ok = true;
-    for (int i = 0; i < NW && ok; ++i)
-      if (cnt[i] > 0) ok = issue_s(i, 0);
-    for (int jj = 0; jj < steps && ok; ++jj)
-      for (int i = 0; i < NW && ok; ++i) {
-        if (jj < cnt[i]) ok = issue_o(i, jj);
-        if (ok && jj + 1 < cnt[i]) ok = issue_s(i, jj + 1);
-      }
-    if (steps > 0) {   // every MMA and commit has landed
-      mma_commit(smem_u32(&sh->done));
-      drain_bar(smem_u32(&sh->done), 0, a.wait_ns);
+    bool ok = mine == 0 || issue_s(0);
+    for (int jj = 0; jj < mine && ok; ++jj) {
+      ok = issue_o(jj);
+      if (ok && jj + 1 < mine) ok = issue_s(jj + 1);
+    }
+    // Tiles past this row tile's last one are given back unread.
+    for (int n = mine * (KC + VC); n < steps * (KC + VC) && ok; ++n) {
+      ok = wait_chunk(n);
+      if (ok && lane == 0) mbar_arrive(smem_u32(&sh->empty[n % NS]));
+    }
+    if (mine > 0) {   // every MMA and commit has landed
+      mma_commit(smem_u32(&sh->done[i]));
+      drain_bar(smem_u32(&sh->done[i]), 0, a.wait_ns);
     }
    }
   } else {
