@@ -71,7 +71,7 @@ struct DenseArgs {
 
 struct __align__(16) Shared {
   uint64_t full[16], empty[16];   // ring of chunks
-  uint64_t sfull[2], pready[2][2], ofull[2], done[2];
+  uint64_t sfull[2], pready[2][2], ofull[2], done[2], turn[2];
   uint32_t tmem;
   int abort;
   int req, tile;                  // request and its tile; req < 0: nothing to do
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
       mbar_init(smem_u32(&sh->pready[i][1]), 4);
       mbar_init(smem_u32(&sh->ofull[i]), 1);
       mbar_init(smem_u32(&sh->done[i]), 1);
+      mbar_init(smem_u32(&sh->turn[i]), 1);
     }
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -264,6 +265,14 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     const uint64_t dv = desc_mnmajor(smem_u32(ring), kChunkBytes);
     const uint32_t sd = tmem + i * 128, od = tmem + NW * 128 + i * 128;
     auto wait_chunk = [&](int n) { return wait_bar_warp(smem_u32(&sh->full[n % NS]), (n / NS) & 1, wc); };
+    // The row tiles take turns at O += P V, S = Q K^T: one's softmax then falls
+    // into the other's MMAs, where side by side both would wait and work together.
+    auto my_turn = [&](int jj) -> bool {
+      return NW == 1 || (i == 0 && jj == 0) || wait_bar_warp(smem_u32(&sh->turn[i]), (jj + i - 1) & 1, wc);
+    };
+    auto pass_turn = [&]() {
+      if (NW == 2 && lane == 0) mbar_arrive(smem_u32(&sh->turn[i ^ 1]));
+    };
     // S against K tile jj.
     auto issue_s = [&](int jj) -> bool {
       const int n = jj * (KC + VC);
@@ -300,6 +309,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {           // P comes in two halves of 64 positions
         if (!wait_bar_warp(smem_u32(&sh->pready[i][half]), jj & 1, wc)) return false;
+        if (half == 0 && !my_turn(jj)) return false;
         tc_fence_after();
         if (VC == 1 || s1 > s0) {
 #pragma unroll
@@ -322,11 +332,16 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     for (int jj = 0; jj < mine && ok; ++jj) {
       ok = issue_o(jj);
       if (ok && jj + 1 < mine) ok = issue_s(jj + 1);
+      pass_turn();
     }
     // Tiles past this row tile's last one are given back unread.
-    for (int n = mine * (KC + VC); n < steps * (KC + VC) && ok; ++n) {
-      ok = wait_chunk(n);
-      if (ok && lane == 0) mbar_arrive(smem_u32(&sh->empty[n % NS]));
+    for (int jj = mine; jj < steps && ok; ++jj) {
+      for (int n = jj * (KC + VC); n < (jj + 1) * (KC + VC) && ok; ++n) {
+        ok = wait_chunk(n);
+        if (ok && lane == 0) mbar_arrive(smem_u32(&sh->empty[n % NS]));
+      }
+      ok = ok && my_turn(jj);
+      pass_turn();
     }
     if (mine > 0) {   // every MMA and commit has landed
       mma_commit(smem_u32(&sh->done[i]));
