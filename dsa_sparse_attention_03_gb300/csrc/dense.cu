@@ -14,15 +14,18 @@
 // tile of 128 packed rows reads each K/V tile once for all of them: whole
 // prompts and single tokens of grouped heads run the same kernel.
 //
-// A CTA takes NW tiles of 128 packed rows (NW = 2 for prompts, 1 where no
-// request has more than one tile), one K/V head and a range of K/V tiles:
-//   warp 0      producer: K and V tiles by TMA, in 16 KB chunks of 64 columns
-//               through one ring, in the order the MMAs use them
+// An item is NW tiles of 128 packed rows (NW = 2 for prompts, 1 where no request
+// has more than one tile), one K/V head and a range of K/V tiles.  CTAs are
+// persistent (one per SM with NW = 2, two with NW = 1) and take items from a
+// counter, so that an item's loads and first MMAs run under the last one's end:
+//   warp 0      producer: Q, and K and V tiles through one ring of 16 KB chunks of
+//               64 columns, in the order the MMAs use them, by TMA
 //   warps 1..   one per row tile issues its MMAs: S = Q K^T (both operands in shared
 //               memory) and O += P V (P in tensor memory, over the S it came from, in
 //               two halves, so that the product starts while the second is computed).
 //               The tensor core takes few MMAs ahead, so an issuer that waits leaves
 //               it idle; with two, the other row tile's go on.
+//   warp 3      scheduler: takes items, finds their request, positions and lengths
 //   warps 4..   softmax, four warps to a row tile: a thread holds one row of S
 // Registers are dealt with setmaxnreg: 56 to warps 0-3, 224 (200) to the softmax.
 // With two row tiles the tensor core works on one while the other's softmax
@@ -53,7 +56,7 @@ namespace {
 constexpr int kTile = 128;
 
 struct DenseArgs {
-  CUtensorMap tk, tv;
+  CUtensorMap tq, tk, tv;
   const uint16_t* q;
   const int32_t* offsets;
   const int32_t* row_offsets;
@@ -63,78 +66,124 @@ struct DenseArgs {
   float* part;      // [R * H_q, splits, D_v]
   float2* ml;       // [R * H_q, splits]: (c m, l)
   uint32_t* status;
+  uint32_t* next;   // items taken beyond the grid (zeroed with the status)
   int64_t q_stride;
   uint64_t wait_ns;
   int R, B, H_q, H_kv, G, L_total, splits, tiles;
+  int q_tma;        // Q tiles by TMA (the group divides a tile), else by the softmax warps
   float scale, c;   // c = scale * log2 e
 };
 
+struct Item {
+  int rows, r0, t0, h;   // rows = 0: no more items.  Packed rows and first row of the request; first packed row here
+  int o0, len, split;    // the request's positions
+  int lo, steps;         // K/V tiles of this part
+  int cnt[2];            // of them, those each row tile needs
+  int kv_end;            // positions past it are seen by no row of the item
+};
+
+constexpr int kEarly = 4;     // K/V tiles before an item's end at which the next one is taken
+constexpr int kBlocks = 64;   // request blocks of the lookup table
+
 struct __align__(16) Shared {
   uint64_t full[16], empty[16];   // ring of chunks
-  uint64_t sfull[2], pready[2][2], ofull[2], done[2], turn[2];
+  uint64_t sfull[2], pready[2][2], ofull[2], ofree[2], qfull[2], qempty[2], turn[2], done[2];
+  uint64_t ifull[2], ifree[2], inext;   // items
   uint32_t tmem;
   int abort;
-  int req, tile;                  // request and its tile; req < 0: nothing to do
-  int r0, n, o0, len;             // its rows and positions
-  int far[2][4];                  // largest length of each warp's rows
+  Item item[2];
+  int first[kBlocks + 1];         // row tiles before each block of requests
 };
 
 template <int DK, int DV, int NW>
 __host__ __device__ constexpr int ring_slots() {
-  constexpr int budget = (NW == 1 ? 113 : 227) * 1024 - 2048;
+  constexpr int budget = (NW == 1 ? 113 : 227) * 1024 - (int)sizeof(Shared);
   constexpr int s = (budget - NW * kTile * DK * 2) / (int)kChunkBytes;
   return s < 16 ? s : 16;
 }
 template <int DK, int DV, int NW>
 __host__ __device__ constexpr size_t smem_bytes() {
-  return (size_t)NW * kTile * DK * 2 + (size_t)ring_slots<DK, DV, NW>() * kChunkBytes + sizeof(Shared) + 1024;
+  return (size_t)NW * kTile * DK * 2 + (size_t)ring_slots<DK, DV, NW>() * kChunkBytes + sizeof(Shared);
 }
 
-// Finds the request of this CTA's row tile (warp 0).  Tiles are numbered over
-// the requests; the last ones (a causal prompt's longest) come first.
-__device__ void locate(const DenseArgs& a, int rows_per_cta, int idx, Shared* sh, int lane) {
-  auto bounds = [&](int b, int& r0, int& n) {
-    r0 = 0; n = 0;
-    if (b >= a.B) return;
-    const int x0 = a.B == 1 ? 0 : a.row_offsets[b], x1 = a.B == 1 ? a.R : a.row_offsets[b + 1];
-    r0 = min(max(x0, 0), a.R);
-    n = max(min(x1, a.R) - r0, 0);
-  };
-  int total = 0;
-  for (int base = 0; base < a.B; base += 32) {
-    int r0, n;
-    bounds(base + lane, r0, n);
-    total += __reduce_add_sync(0xffffffffu, (n * a.G + rows_per_cta - 1) / rows_per_cta);
+// Request b's rows, clamped to the call's.
+__device__ __forceinline__ void request_rows(const DenseArgs& a, int b, int& r0, int& n) {
+  const int x0 = a.B == 1 ? 0 : a.row_offsets[b], x1 = a.B == 1 ? a.R : a.row_offsets[b + 1];
+  r0 = min(max(x0, 0), a.R);
+  n = max(min(x1, a.R) - r0, 0);
+}
+
+// Item `idx` (one warp).  Row tiles are numbered over the requests; the last ones
+// (a causal prompt's longest) come first, K/V heads and parts vary fastest.
+template <int NW>
+__device__ void find_item(const DenseArgs& a, int64_t idx, Shared* sh, Item* it, int lane) {
+  const int h = (int)(idx % a.H_kv);
+  const int split = (int)(idx / a.H_kv % a.splits);
+  const int want = sh->first[kBlocks] - 1 - (int)(idx / a.H_kv / a.splits);
+  if (want < 0) {
+    if (lane == 0) it->rows = 0;
+    return;
   }
-  if (total > a.tiles && idx == 0 && lane == 0) raise_status(a.status, DSA_DEVICE_CAPACITY);
-  if (lane == 0) sh->req = -1;
-  __syncwarp();
-  const int want = total - 1 - idx;
-  if (want < 0) return;
-  int run = 0;
-  for (int base = 0; base < a.B; base += 32) {
-    int r0, n;
-    bounds(base + lane, r0, n);
-    const int v = (n * a.G + rows_per_cta - 1) / rows_per_cta;
+  // The block of requests, then the request in it.
+  const int per = (a.B + kBlocks - 1) / kBlocks;
+  const int blk = __popc(__ballot_sync(0xffffffffu, sh->first[lane + 1] <= want)) +
+                  __popc(__ballot_sync(0xffffffffu, sh->first[lane + 33] <= want));
+  int run = sh->first[blk], b = 0, r0 = 0, n = 0, tile = 0;
+  for (int base = blk * per; base < (blk + 1) * per; base += 32) {
+    int x0 = 0, xn = 0;
+    if (base + lane < (blk + 1) * per && base + lane < a.B) request_rows(a, base + lane, x0, xn);
+    const int v = (xn * a.G + NW * kTile - 1) / (NW * kTile);
     int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += t;
     }
-    const int first = run + incl - v;
-    if (want >= first && want < first + v) {
-      const int b = base + lane;
-      const int y0 = a.B == 1 ? 0 : a.offsets[b], y1 = a.B == 1 ? a.L_total : a.offsets[b + 1];
-      const int o0 = min(max(y0, 0), a.L_total);
-      sh->req = b;
-      sh->tile = want - first;
-      sh->r0 = r0;
-      sh->n = n;
-      sh->o0 = o0;
-      sh->len = max(min(y1, a.L_total) - o0, 0);
-    }
+    const int at = run + incl - v;
+    const uint32_t hit = __ballot_sync(0xffffffffu, want >= at && want < at + v);
     run += __shfl_sync(0xffffffffu, incl, 31);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = base + src;
+      r0 = __shfl_sync(0xffffffffu, x0, src);
+      n = __shfl_sync(0xffffffffu, xn, src);
+      tile = want - __shfl_sync(0xffffffffu, at, src);
+      break;
+    }
+  }
+  const int y0 = a.B == 1 ? 0 : a.offsets[b], y1 = a.B == 1 ? a.L_total : a.offsets[b + 1];
+  const int o0 = min(max(y0, 0), a.L_total);
+  const int len = max(min(y1, a.L_total) - o0, 0);
+  const int rows = n * a.G, t0 = tile * NW * kTile;
+  // The farthest position each row tile sees.
+  int end[2] = {0, 0};
+  bool bad = false;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const int x0 = t0 + w * kTile, x1 = min(x0 + kTile, rows);
+    for (int r = x0 / a.G + lane; r * a.G < x1; r += 32) {
+      const int l = a.row_len[r0 + r];
+      bad |= l < 0 || l > len;
+      end[w] = max(end[w], min(max(l, 0), len));
+    }
+    end[w] = __reduce_max_sync(0xffffffffu, end[w]);
+  }
+  if (bad && split == 0 && h == 0) raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+  if (lane == 0) {
+    const int kv_end = max(end[0], end[1]);
+    const int nt = (kv_end + kTile - 1) / kTile;
+    const int lo = (int)((int64_t)nt * split / a.splits), hi = (int)((int64_t)nt * (split + 1) / a.splits);
+    it->rows = rows;
+    it->r0 = r0;
+    it->t0 = t0;
+    it->h = h;
+    it->o0 = o0;
+    it->len = len;
+    it->split = split;
+    it->lo = lo;
+    it->steps = hi - lo;
+    for (int w = 0; w < 2; ++w) it->cnt[w] = max(min((end[w] + kTile - 1) / kTile, hi) - lo, 0);
+    it->kv_end = kv_end;
   }
 }
 
@@ -145,171 +194,213 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
   constexpr int KC = DK / 64, VC = DV / 64;
   constexpr uint32_t kQBytes = kTile * DK * 2;
   constexpr uint32_t kCols = NW * 256;      // S of each row tile, then O of each
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  constexpr int kReaders = 1 + NW + 4 * NW; // warps that read an item
+  extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* Qs = smem;
   unsigned char* ring = smem + NW * kQBytes;
   Shared* sh = reinterpret_cast<Shared*>(ring + NS * kChunkBytes);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
-  const int h = blockIdx.x % a.H_kv;
-  const int split = (blockIdx.x / a.H_kv) % a.splits;
-  const int idx = blockIdx.x / a.H_kv / a.splits;
-
-  if (warp == 0) locate(a, NW * kTile, idx, sh, lane);
-  __syncthreads();
-  if (sh->req < 0) return;
-
-  if (warp == 0 && lane == 0) {
+  if (smem_u32(smem) & 1023) {   // (the swizzle's atoms)
+    if (tid == 0) raise_status(a.status, DSA_DEVICE_CAPACITY);
+    return;
+  }
+  if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(smem_u32(&sh->full[i]), 1);
-      mbar_init(smem_u32(&sh->empty[i]), NW);
+      mbar_init(bar(sh->full[i]), 1);
+      mbar_init(bar(sh->empty[i]), NW);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh->sfull[i]), 1);
-      mbar_init(smem_u32(&sh->pready[i][0]), 4);
-      mbar_init(smem_u32(&sh->pready[i][1]), 4);
-      mbar_init(smem_u32(&sh->ofull[i]), 1);
-      mbar_init(smem_u32(&sh->done[i]), 1);
-      mbar_init(smem_u32(&sh->turn[i]), 1);
+      mbar_init(bar(sh->sfull[i]), 1);
+      mbar_init(bar(sh->pready[i][0]), 4);
+      mbar_init(bar(sh->pready[i][1]), 4);
+      mbar_init(bar(sh->ofull[i]), 1);
+      mbar_init(bar(sh->ofree[i]), 4);
+      mbar_init(bar(sh->qfull[i]), a.q_tma ? 1 : 4);
+      mbar_init(bar(sh->qempty[i]), 1);
+      mbar_init(bar(sh->turn[i]), 1);
+      mbar_init(bar(sh->done[i]), 1);
+      mbar_init(bar(sh->ifull[i]), 1);
+      mbar_init(bar(sh->ifree[i]), kReaders);
     }
+    mbar_init(bar(sh->inext), 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh->tmem), kCols);
-
-  // Softmax warps: warp w of a tile reads tensor-memory lanes 32 (w % 4).. .
-  const int w = (warp >> 2) - 1;                         // row tile of this warp
-  const int trow = (warp & 3) * 32 + lane;               // row in the tile
-  const int packed = (sh->tile * NW + w) * kTile + trow; // packed row in the request
-  const bool valid = warp >= 4 && packed < sh->n * a.G;
-  const int row = sh->r0 + (valid ? packed / a.G : 0);
-  const int head = h * a.G + (valid ? packed % a.G : 0);
-  int len = 0;
-  if (warp >= 4) {
-    if (valid) {
-      const int l = a.row_len[row];
-      len = min(max(l, 0), sh->len);
-      if (len != l && split == 0) raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+  if (warp == 2) {
+    // Row tiles before each block of requests.
+    const int per = (a.B + kBlocks - 1) / kBlocks;
+    int run = 0;
+    for (int half = 0; half < 2; ++half) {
+      const int blk = half * 32 + lane;
+      int v = 0;
+      for (int b = blk * per; b < (blk + 1) * per && b < a.B; ++b) {
+        int r0, n;
+        request_rows(a, b, r0, n);
+        v += (n * a.G + NW * kTile - 1) / (NW * kTile);
+      }
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      sh->first[blk] = run + incl - v;
+      run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const int m = __reduce_max_sync(0xffffffffu, len);
-    if (lane == 0) sh->far[w][warp & 3] = m;
-    // Q, K-major and swizzled: 16-byte pieces, consecutive threads along a row.
-    const int t0 = (sh->tile * NW + w) * kTile;
-    constexpr int P = DK / 8;
-    for (int i = tid & 127; i < kTile * P; i += 128) {
-      const int r = i / P, x = i % P, pk = t0 + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (pk < sh->n * a.G)
-        v = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(sh->r0 + pk / a.G) * a.q_stride +
-                                                 (int64_t)(h * a.G + pk % a.G) * DK) + x);
-      *reinterpret_cast<uint4*>(Qs + w * kQBytes + (x >> 3) * kChunkBytes + r * 128 + (((x & 7) ^ (r & 7)) << 4)) = v;
+    if (lane == 0) {
+      // (the launch was sized by the declared rows: later tiles come first in the
+      // numbering, so those past it are the first requests' and stay unwritten)
+      if (run > a.tiles) raise_status(a.status, DSA_DEVICE_CAPACITY);
+      sh->first[kBlocks] = run;
     }
-    fence_proxy_async();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const WaitCtx wc(&sh->abort, a.status, a.wait_ns);
-
-  // K/V tiles of this CTA: [lo, hi); row tile w takes those below its own end.
-  int end[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int* f = sh->far[i];
-    end[i] = i < NW ? max(max(f[0], f[1]), max(f[2], f[3])) : 0;
-  }
-  const int kv_end = max(end[0], end[1]);
-  const int nt = (kv_end + kTile - 1) / kTile;
-  const int lo = (int)((int64_t)nt * split / a.splits);
-  const int hi = (int)((int64_t)nt * (split + 1) / a.splits);
-  int cnt[2];                               // tiles of each row tile
-#pragma unroll
-  for (int i = 0; i < 2; ++i) cnt[i] = max(min((end[i] + kTile - 1) / kTile, hi) - lo, 0);
-  const int steps = hi - lo;
+  // Item k of this CTA; whoever has read what it needs gives the slot back.
+  auto item_wait = [&](int k) { return wait_bar_warp(bar(sh->ifull[k & 1]), (k >> 1) & 1, wc); };
+  auto item_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(sh->ifree[k & 1]));
+  };
 
   if (warp < 4) {
    regs_down<56>();
-   if (warp == 0) {
+   if (warp == 3) {
+    // ------------------------------------------------------------ scheduler
+    int64_t idx;
+    const int64_t items = (int64_t)a.tiles * a.splits * a.H_kv;
+    for (int k = 0;; ++k) {
+      // Not before the producer nears the end of the last one: an item taken early
+      // is one that no idle CTA can take.
+      if (k >= 1 && !wait_bar_warp(bar(sh->inext), (k - 1) & 1, wc)) break;
+      if (k == 0) {
+        idx = blockIdx.x;
+      } else {
+        uint32_t t = 0;
+        if (lane == 0) t = atomicAdd(a.next, 1u);
+        idx = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, t, 0);
+      }
+      if (k >= 2 && !wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc)) break;
+      Item* it = &sh->item[k & 1];
+      if (idx < items)
+        find_item<NW>(a, idx, sh, it, lane);
+      else if (lane == 0)
+        it->rows = 0;
+      __syncwarp();
+      const int rows = __shfl_sync(0xffffffffu, it->rows, 0);
+      if (lane == 0) mbar_arrive(bar(sh->ifull[k & 1]));
+      if (rows == 0) break;
+    }
+   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int n = 0;
-      bool ok = true;
-      for (int j = lo; j < hi && ok; ++j) {
-        for (int c = 0; c < KC + VC; ++c, ++n) {
-          const int s = n % NS;
-          if (n >= NS && !wait_bar(smem_u32(&sh->empty[s]), (n / NS - 1) & 1, wc)) {
-            ok = false;
-            break;
+    int n = 0, nq[2] = {0, 0};   // chunks and Q tiles asked for
+    bool ok = true;
+    for (int k = 0; ok && item_wait(k); ++k) {
+      const Item it = sh->item[k & 1];
+      item_done(k);
+      if (it.rows == 0) break;
+      if (lane == 0) {
+        if (a.q_tma) {
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            if (it.cnt[w] == 0 || !ok) continue;
+            if (nq[w] > 0 && !(ok = wait_bar(bar(sh->qempty[w]), (nq[w] - 1) & 1, wc))) continue;
+            mbar_expect_tx(bar(sh->qfull[w]), kQBytes);
+            const int row = it.r0 + (it.t0 + w * kTile) / a.G;
+            for (int c = 0; c < KC; ++c)
+              tma_load_3d(smem_u32(Qs) + w * kQBytes + c * kChunkBytes, &a.tq, c * 64, it.h * a.G, row, bar(sh->qfull[w]));
+            ++nq[w];
           }
-          const uint32_t bar = smem_u32(&sh->full[s]), dst = smem_u32(ring + s * kChunkBytes);
-          mbar_expect_tx(bar, kChunkBytes);
-          const int y = sh->o0 + j * kTile;
-          if (c < KC)
-            tma_load_2d(dst, &a.tk, h * DK + c * 64, y, bar);
-          else
-            tma_load_2d(dst, &a.tv, h * DV + (c - KC) * 64, y, bar);
+        }
+        if (it.steps == 0) mbar_arrive(bar(sh->inext));
+        for (int j = 0; j < it.steps && ok; ++j) {
+          if (j == max(it.steps - kEarly, 0)) mbar_arrive(bar(sh->inext));
+          for (int c = 0; c < KC + VC; ++c, ++n) {
+            const int s = n % NS;
+            if (n >= NS && !(ok = wait_bar(bar(sh->empty[s]), (n / NS - 1) & 1, wc))) break;
+            const uint32_t b = bar(sh->full[s]), dst = smem_u32(ring + s * kChunkBytes);
+            mbar_expect_tx(b, kChunkBytes);
+            const int y = it.o0 + (it.lo + j) * kTile;
+            if (c < KC)
+              tma_load_2d(dst, &a.tk, it.h * DK + c * 64, y, b);
+            else
+              tma_load_2d(dst, &a.tv, it.h * DV + (c - KC) * 64, y, b);
+          }
         }
       }
-      for (int i = max(0, n - NS); i < n; ++i)   // (an abort may leave copies in flight)
-        drain_bar(smem_u32(&sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+    }
+    if (lane == 0) {   // (an abort may leave copies in flight)
+      for (int i = max(0, n - NS); i < n; ++i) drain_bar(bar(sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
+      for (int w = 0; w < NW; ++w)
+        if (nq[w] > 0) drain_bar(bar(sh->qfull[w]), (nq[w] - 1) & 1, a.wait_ns);
     }
    } else if (warp <= NW) {
     // ------------------------------------------------------------ MMA issuers
-    const int i = warp - 1, mine = i ? cnt[1] : cnt[0];
+    const int i = warp - 1;
     const uint32_t ids = idesc_16(F16, kTile, kTile, false, false);
     const uint32_t ido = idesc_16(F16, kTile, DV, false, true);
     const uint32_t ido64 = idesc_16(F16, kTile, 64, false, true);
     const uint64_t dq = desc_kmajor(smem_u32(Qs)) + desc_step(i * kQBytes), dr = desc_kmajor(smem_u32(ring));
     const uint64_t dv = desc_mnmajor(smem_u32(ring), kChunkBytes);
     const uint32_t sd = tmem + i * 128, od = tmem + NW * 128 + i * 128;
-    auto wait_chunk = [&](int n) { return wait_bar_warp(smem_u32(&sh->full[n % NS]), (n / NS) & 1, wc); };
+    int n = 0;              // first chunk of the current K/V tile
+    int tiles = 0;          // S tiles issued (the softmax's count)
+    int used = 0;           // items that had tiles for this row tile
+    int turns = 0;          // turns taken
+    bool ok = true;
+    auto wait_chunk = [&](int m) { return wait_bar_warp(bar(sh->full[m % NS]), (m / NS) & 1, wc); };
     // The row tiles take turns at O += P V, S = Q K^T: one's softmax then falls
     // into the other's MMAs, where side by side both would wait and work together.
-    auto my_turn = [&](int jj) -> bool {
-      return NW == 1 || (i == 0 && jj == 0) || wait_bar_warp(smem_u32(&sh->turn[i]), (jj + i - 1) & 1, wc);
+    auto my_turn = [&]() -> bool {
+      const int t = turns++;
+      return NW == 1 || (i == 0 && t == 0) || wait_bar_warp(bar(sh->turn[i]), (t + i - 1) & 1, wc);
     };
     auto pass_turn = [&]() {
-      if (NW == 2 && lane == 0) mbar_arrive(smem_u32(&sh->turn[i ^ 1]));
+      if (NW == 2 && lane == 0) mbar_arrive(bar(sh->turn[i ^ 1]));
     };
-    // S against K tile jj.
-    auto issue_s = [&](int jj) -> bool {
-      const int n = jj * (KC + VC);
+    // S against the K tile whose first chunk is m; `last` of its item.
+    auto issue_s = [&](int m, bool last) -> bool {
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        if (!wait_chunk(n + c)) return false;
+        if (!wait_chunk(m + c)) return false;
         tc_fence_after();
-        const uint64_t qa = dq + desc_step(c * kChunkBytes), ka = dr + desc_step(((n + c) % NS) * kChunkBytes);
+        const uint64_t qa = dq + desc_step(c * kChunkBytes), ka = dr + desc_step(((m + c) % NS) * kChunkBytes);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) mma_ss(sd, qa + desc_step(kk * 32), ka + desc_step(kk * 32), ids, c | kk);
       }
-      mma_commit(smem_u32(&sh->sfull[i]));
+      mma_commit(bar(sh->sfull[i]));
 #pragma unroll
-      for (int c = 0; c < KC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
+      for (int c = 0; c < KC; ++c) mma_commit(bar(sh->empty[(m + c) % NS]));
+      if (last) mma_commit(bar(sh->qempty[i]));
       return true;
     };
-    // O += P V for V tile jj.
-    auto issue_o = [&](int jj) -> bool {
-      const int n = jj * (KC + VC) + KC;
+    // O += P V for the item's V tile jj, whose first chunk is m; `rows` of it are seen.
+    auto issue_o = [&](int jj, int m, int rows, bool last) -> bool {
 #pragma unroll
       for (int c = 0; c < VC; ++c)
-        if (!wait_chunk(n + c)) return false;
-      const int rows = kv_end - (lo + jj) * kTile;
+        if (!wait_chunk(m + c)) return false;
       if (rows < kTile) {   // the cache's last tile (each row tile's issuer writes the same zeros)
 #pragma unroll
         for (int c = 0; c < VC; ++c) {
-          uint4* p = reinterpret_cast<uint4*>(ring + ((n + c) % NS) * kChunkBytes + rows * 128);
+          uint4* p = reinterpret_cast<uint4*>(ring + ((m + c) % NS) * kChunkBytes + rows * 128);
           for (int x = lane; x < (kTile - rows) * 8; x += 32) p[x] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
         __syncwarp();
       }
-      const int s0 = n % NS, s1 = (n + VC - 1) % NS;
+      if (jj == 0 && used > 0 && !wait_bar_warp(bar(sh->ofree[i]), (used - 1) & 1, wc)) return false;
+      const int s0 = m % NS, s1 = (m + VC - 1) % NS;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {           // P comes in two halves of 64 positions
-        if (!wait_bar_warp(smem_u32(&sh->pready[i][half]), jj & 1, wc)) return false;
-        if (half == 0 && !my_turn(jj)) return false;
+        if (!wait_bar_warp(bar(sh->pready[i][half]), tiles & 1, wc)) return false;
+        if (half == 0 && !my_turn()) return false;
         tc_fence_after();
         if (VC == 1 || s1 > s0) {
 #pragma unroll
@@ -323,151 +414,188 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
               mma_ts(od + c * 64, sd + kk * 8, dv + desc_step((c ? s1 : s0) * kChunkBytes + kk * 2048), ido64, jj | kk);
         }
       }
-      if (jj == mine - 1) mma_commit(smem_u32(&sh->ofull[i]));
+      ++tiles;
+      if (last) mma_commit(bar(sh->ofull[i]));
 #pragma unroll
-      for (int c = 0; c < VC; ++c) mma_commit(smem_u32(&sh->empty[(n + c) % NS]));
+      for (int c = 0; c < VC; ++c) mma_commit(bar(sh->empty[(m + c) % NS]));
       return true;
     };
-    bool ok = mine == 0 || issue_s(0);
-    for (int jj = 0; jj < mine && ok; ++jj) {
-      ok = issue_o(jj);
-      if (ok && jj + 1 < mine) ok = issue_s(jj + 1);
-      pass_turn();
-    }
-    // Tiles past this row tile's last one are given back unread.
-    for (int jj = mine; jj < steps && ok; ++jj) {
-      for (int n = jj * (KC + VC); n < (jj + 1) * (KC + VC) && ok; ++n) {
-        ok = wait_chunk(n);
-        if (ok && lane == 0) mbar_arrive(smem_u32(&sh->empty[n % NS]));
+    for (int k = 0; ok && item_wait(k); ++k) {
+      const Item& si = sh->item[k & 1];
+      const int rows = si.rows, steps = si.steps, mine = i ? si.cnt[1] : si.cnt[0], end = si.kv_end - si.lo * kTile;
+      item_done(k);
+      if (rows == 0) break;
+      if (mine > 0) {
+        ok = wait_bar_warp(bar(sh->qfull[i]), used & 1, wc) && issue_s(n, mine == 1);
+        for (int jj = 0; jj < mine && ok; ++jj) {
+          ok = issue_o(jj, n + KC, end - jj * kTile, jj == mine - 1);
+          n += KC + VC;
+          if (ok && jj + 1 < mine) ok = issue_s(n, jj + 2 == mine);
+          pass_turn();
+        }
+        ++used;
       }
-      ok = ok && my_turn(jj);
-      pass_turn();
+      // Tiles past this row tile's last one are given back unread.
+      for (int jj = mine; jj < steps && ok; ++jj) {
+        for (int c = 0; c < KC + VC && ok; ++c, ++n) {
+          ok = wait_chunk(n);
+          if (ok && lane == 0) mbar_arrive(bar(sh->empty[n % NS]));
+        }
+        ok = ok && my_turn();
+        pass_turn();
+      }
     }
-    if (mine > 0) {   // every MMA and commit has landed
-      mma_commit(smem_u32(&sh->done[i]));
-      drain_bar(smem_u32(&sh->done[i]), 0, a.wait_ns);
-    }
+    mma_commit(bar(sh->done[i]));   // every MMA and commit has landed
+    drain_bar(bar(sh->done[i]), 0, a.wait_ns);
    }
   } else {
     // ------------------------------------------------------------ softmax
     regs_up<NW == 1 ? 200 : 224>();
+    const int w = (warp >> 2) - 1;                         // row tile of this warp
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t st = lane_base + w * 128, ot = lane_base + NW * 128 + w * 128;
-    const bool any = __any_sync(0xffffffffu, valid);
-    const int mylen = valid ? len : kv_end;      // rows of the tile that hold nothing need no mask
-    const int mine = w ? cnt[1] : cnt[0];
-    float m = -INFINITY, l = 0.f;
+    int tiles = 0, used = 0;                               // S tiles taken; items with tiles
     bool ok = true;
-    for (int jj = 0; jj < mine; ++jj) {
-      if (!(ok = wait_bar_warp(smem_u32(&sh->sfull[w]), jj & 1, wc))) break;
-      tc_fence_after();
-      if (any) {
-        uint32_t v[128];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32(st + x * 32, v + x * 32);
-        tmem_wait_ld();
-        const int left = mylen - (lo + jj) * kTile;   // columns this row sees
-        if (__any_sync(0xffffffffu, left < kTile)) {
-#pragma unroll
-          for (int x = 0; x < 128; ++x)
-            if (x >= left) v[x] = 0xff800000u;
+    for (int k = 0; ok && item_wait(k); ++k) {
+      const Item& si = sh->item[k & 1];
+      const int rows = si.rows, t0 = si.t0 + w * kTile, r0 = si.r0, h = si.h, split = si.split;
+      const int mine = w ? si.cnt[1] : si.cnt[0], lo = si.lo, kv_end = si.kv_end, reach = si.len;
+      item_done(k);
+      if (rows == 0) break;
+      const int packed = t0 + (warp & 3) * 32 + lane;      // packed row in the request
+      const bool valid = packed < rows;
+      const int row = r0 + (valid ? packed / a.G : 0);
+      const int head = h * a.G + (valid ? packed % a.G : 0);
+      const bool any = __any_sync(0xffffffffu, valid);
+      // Rows of the tile that hold nothing need no mask.
+      const int mylen = valid ? min(max(a.row_len[row], 0), reach) : kv_end;
+      if (!a.q_tma && mine > 0) {
+        // Q, K-major and swizzled: 16-byte pieces, consecutive threads along a row.
+        if (used > 0 && !(ok = wait_bar_warp(bar(sh->qempty[w]), (used - 1) & 1, wc))) break;
+        constexpr int P = DK / 8;
+        for (int x = tid & 127; x < kTile * P; x += 128) {
+          const int r = x / P, c = x % P, pk = t0 + r;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (pk < rows)
+            v = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + pk / a.G) * a.q_stride +
+                                                     (int64_t)(h * a.G + pk % a.G) * DK) + c);
+          *reinterpret_cast<uint4*>(Qs + w * kQBytes + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
         }
-        float t[4];
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->qfull[w]));
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int jj = 0; jj < mine; ++jj, ++tiles) {
+        if (!(ok = wait_bar_warp(bar(sh->sfull[w]), tiles & 1, wc))) break;
+        tc_fence_after();
+        if (any) {
+          uint32_t v[128];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) t[x] = __uint_as_float(v[x]);
+          for (int x = 0; x < 4; ++x) tmem_ld32(st + x * 32, v + x * 32);
+          tmem_wait_ld();
+          const int left = mylen - (lo + jj) * kTile;   // columns this row sees
+          if (__any_sync(0xffffffffu, left < kTile)) {
 #pragma unroll
-        for (int x = 4; x < 124; x += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) t[y] = max3(t[y], __uint_as_float(v[x + y]), __uint_as_float(v[x + 4 + y]));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) t[x] = fmaxf(t[x], __uint_as_float(v[124 + x]));
-        const float mn = fmaxf(max3(m, t[0], t[1]), fmaxf(t[2], t[3]));
-        if (jj == 0) {
-          m = mn;
-        } else if (__any_sync(0xffffffffu, (mn - m) * a.c > 8.f)) {
-          // S of this tile was issued after O += P V of the previous one, so O is still.
-          const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * a.c);
-          m = mn;
-          l *= f;
-#pragma unroll
-          for (int x = 0; x < DV; x += 32) {
-            uint32_t o[32];
-            tmem_ld32(ot + x, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-            tmem_st32(ot + x, o);
+            for (int x = 0; x < 128; ++x)
+              if (x >= left) v[x] = 0xff800000u;
           }
-        }
-        const float mc = m == -INFINITY ? 0.f : m * a.c;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float t[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {   // P in two halves: the first one's product starts meanwhile
+          for (int x = 0; x < 4; ++x) t[x] = __uint_as_float(v[x]);
 #pragma unroll
-          for (int x = half * 64; x < half * 64 + 64; x += 2) {
-            const float2 e = fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), make_float2(a.c, a.c),
-                                  make_float2(-mc, -mc));
-            const float2 p = make_float2(ex2(e.x), ex2(e.y));
-            sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], p);
-            v[x >> 1] = pack16<F16>(p.x, p.y);
+          for (int x = 4; x < 124; x += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) t[y] = max3(t[y], __uint_as_float(v[x + y]), __uint_as_float(v[x + 4 + y]));
+#pragma unroll
+          for (int x = 0; x < 4; ++x) t[x] = fmaxf(t[x], __uint_as_float(v[124 + x]));
+          const float mn = fmaxf(max3(m, t[0], t[1]), fmaxf(t[2], t[3]));
+          if (jj == 0) {
+            m = mn;
+          } else if (__any_sync(0xffffffffu, (mn - m) * a.c > 8.f)) {
+            // S of this tile was issued after O += P V of the previous one, so O is still.
+            const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * a.c);
+            m = mn;
+            l *= f;
+#pragma unroll 1
+            for (int x = 0; x < DV; x += 32) {
+              uint32_t o[32];
+              tmem_ld32(ot + x, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st32(ot + x, o);
+            }
           }
-          tmem_st32(st + half * 32, v + half * 32);
-          tmem_wait_st();
+          const float mc = m == -INFINITY ? 0.f : m * a.c;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {   // P in two halves: the first one's product starts meanwhile
+#pragma unroll
+            for (int x = half * 64; x < half * 64 + 64; x += 2) {
+              const float2 e = fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])),
+                                    make_float2(a.c, a.c), make_float2(-mc, -mc));
+              const float2 p = make_float2(ex2(e.x), ex2(e.y));
+              sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], p);
+              v[x >> 1] = pack16<F16>(p.x, p.y);
+            }
+            tmem_st32(st + half * 32, v + half * 32);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh->pready[w][half]));
+          }
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
+        } else {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh->pready[w][half]));
-        }
-        sum[0] = add2(sum[0], sum[1]);
-        l += sum[0].x + sum[0].y;
-      } else {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&sh->pready[w][0]));
-          mbar_arrive(smem_u32(&sh->pready[w][1]));
+          if (lane == 0) {
+            mbar_arrive(bar(sh->pready[w][0]));
+            mbar_arrive(bar(sh->pready[w][1]));
+          }
         }
       }
-    }
-    if (mine > 0 && ok) ok = wait_bar_warp(smem_u32(&sh->ofull[w]), 0, wc);
-    tc_fence_after();
-    if (ok && any) {
-      const int64_t rh = (int64_t)row * a.H_q + head;
-      const bool some = mine > 0 && l != 0.f;
-      if (a.splits > 1) {
-        if (valid) a.ml[rh * a.splits + split] = make_float2(m * a.c, some ? l : 0.f);
-        if (__any_sync(0xffffffffu, some)) {
-#pragma unroll
+      if (mine > 0 && ok) ok = wait_bar_warp(bar(sh->ofull[w]), used & 1, wc);
+      if (!ok) break;
+      tc_fence_after();
+      if (any) {
+        const int64_t rh = (int64_t)row * a.H_q + head;
+        const bool some = mine > 0 && l != 0.f;
+        const bool parts = a.splits > 1;
+        // Written as it is into its part, or divided by l: a row of NaN (l is NaN)
+        // keeps it, a row that sees nothing gets zeros.
+        const float inv = some ? 1.f / l : 0.f;
+        if (valid && parts) a.ml[rh * a.splits + split] = make_float2(m * a.c, some ? l : 0.f);
+        if (valid && !parts && a.lse) a.lse[rh] = some ? m * a.scale + logf(l) : -INFINITY;
+        if (!parts || __any_sync(0xffffffffu, some)) {
+#pragma unroll 1
           for (int x = 0; x < DV; x += 32) {
             uint32_t o[32];
             tmem_ld32(ot + x, o);
             tmem_wait_ld();
-            if (valid && some) {
+            if (parts) {
               uint4* dst = reinterpret_cast<uint4*>(a.part + (rh * a.splits + split) * DV + x);
+              if (valid && some)
 #pragma unroll
-              for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + rh * DV + x);
+#pragma unroll
+              for (int y = 0; y < 16; ++y)
+                o[y] = some ? pack16<F16>(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv) : 0u;
+              if (valid)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
             }
           }
         }
-      } else {
-        // A row of NaN (l is NaN) keeps it; a row that sees nothing gets zeros.
-        const bool empty = mine == 0 || l == 0.f;
-        const float inv = empty ? 0.f : 1.f / l;
-        if (valid && a.lse) a.lse[rh] = empty ? -INFINITY : m * a.scale + logf(l);
-#pragma unroll
-        for (int x = 0; x < DV; x += 32) {
-          uint32_t o[32];
-          tmem_ld32(ot + x, o);
-          tmem_wait_ld();
-          uint32_t q[16];
-#pragma unroll
-          for (int y = 0; y < 16; ++y)
-            q[y] = empty ? 0u : pack16<F16>(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
-          if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + rh * DV + x);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) dst[y] = make_uint4(q[4 * y], q[4 * y + 1], q[4 * y + 2], q[4 * y + 3]);
-          }
-        }
+      }
+      if (mine > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->ofree[w]));
+        ++used;
       }
     }
   }
@@ -521,7 +649,8 @@ cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
   auto kernel = dense_attn_kernel<DK, DV, NW, F16>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = (int64_t)a.tiles * a.splits * a.H_kv;
+  const int64_t items = (int64_t)a.tiles * a.splits * a.H_kv, slots = NW == 1 ? 304 : 152;
+  const int64_t grid = items < slots ? items : slots;
   kernel<<<(unsigned)grid, 128 + 128 * NW, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
   const int64_t rows = (int64_t)a.R * a.H_q;
@@ -546,12 +675,16 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
   int64_t tiles = p.B * ((most * G + per - 1) / per);
   tiles = tiles < p.R * G / per + p.B ? tiles : p.R * G / per + p.B;
   s.tiles = (int)tiles;
-  // Parts per row tile: enough CTAs for two waves of the resident ones, none
-  // with less than two K/V tiles.
+  // Parts per row tile.  Single tokens of several requests: eight items per
+  // resident CTA, since their lengths differ (32 requests of up to 32768 positions:
+  // 288 us with two, 268 with four, 258 with eight, 255 with sixteen); one request,
+  // whose items are alike: one each.  Prompts: two where the row tiles alone leave
+  // SMs idle.  No part has less than two K/V tiles.
   const int64_t items = tiles * p.H_kv, slots = s.nw == 1 ? 304 : 152;
   const int64_t kvt = (p.L_max + kTile - 1) / kTile;
+  const int64_t each = p.B == 1 ? 1 : (s.nw == 1 ? 8 : 2);
   int64_t splits = 1;
-  if (items > 0 && items < 2 * slots) splits = p.B == 1 ? slots / items : (2 * slots + items - 1) / items;
+  if (items > 0 && items < each * slots) splits = p.B == 1 ? slots / items : (each * slots + items - 1) / items;
   const int64_t cap = kvt / 2 < 64 ? kvt / 2 : 64;
   if (splits > cap) splits = cap;
   s.splits = splits < 1 ? 1 : (int)splits;
@@ -565,12 +698,18 @@ cudaError_t launch_dense(const dsa_dense_problem& p, const DenseShape& s, uint16
   a.q = p.q; a.offsets = p.offsets; a.row_offsets = p.row_offsets; a.row_len = p.row_len;
   a.out = out; a.lse = lse; a.part = part; a.ml = reinterpret_cast<float2*>(ml);
   a.status = status;
+  a.next = status + kBarrierWord;
   a.q_stride = p.q_stride ? p.q_stride : (int64_t)p.H_q * p.D_k;
   a.wait_ns = kDefaultWaitNs;
   a.R = p.R; a.B = p.B; a.H_q = p.H_q; a.H_kv = p.H_kv; a.G = p.H_q / p.H_kv; a.L_total = (int)p.L_total;
   a.splits = s.splits; a.tiles = s.tiles;
   a.scale = p.softmax_scale;
   a.c = (float)(p.softmax_scale * 1.4426950408889634);
+  a.q_tma = kTile % a.G == 0;
+  if (a.q_tma) {
+    const cudaError_t e = group_map(&a.tq, p.q, p.R, p.H_q, p.D_k, a.q_stride, a.G);
+    if (e != cudaSuccess) return e;
+  }
   if (p.L_total > 0) {   // (an empty cache is never read)
     cudaError_t e = chunk_map(&a.tk, p.k, p.L_total, (int64_t)p.H_kv * p.D_k, p.k_stride ? p.k_stride : (int64_t)p.H_kv * p.D_k);
     if (e == cudaSuccess)
