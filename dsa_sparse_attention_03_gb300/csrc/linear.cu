@@ -51,7 +51,8 @@ namespace {
 constexpr int kC = 128;            // tokens of a chunk
 constexpr int kThreads = 640;
 constexpr int kQuarter = 32;       // tokens of the decayed V in one buffer
-constexpr int kStages = 2;
+constexpr int kStages = 2;         // of Q, K and V; the state launch, without Q, has room for three
+constexpr int kStateStages = 3;
 
 // Tensor-memory columns.
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384;
@@ -63,7 +64,7 @@ struct ChunkParams {
 };
 
 struct __align__(16) Shared {
-  uint64_t q_full[kStages], kv_full[kStages], q_empty[kStages], kv_empty[kStages];
+  uint64_t q_full[kStages], kv_full[kStateStages], q_empty[kStages], kv_empty[kStateStages];
   uint64_t s_ready, o_staged, qh_ready, h_ready, p_ready, o_ready, o_free, dh_ready, dh_free, tail, done1, done2;
   uint64_t v_ready[2], v_free[2], pair[4];
   uint32_t tmem;
@@ -200,8 +201,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sh->q_full[i]), 1);
-      mbar_init(smem_u32(&sh->kv_full[i]), 1);
       mbar_init(smem_u32(&sh->q_empty[i]), 1);
+    }
+    for (int i = 0; i < kStateStages; ++i) {
+      mbar_init(smem_u32(&sh->kv_full[i]), 1);
       mbar_init(smem_u32(&sh->kv_empty[i]), p.state_only ? 1 : 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -242,8 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const bool final_state = p.state_only || (seg == nseg - 1 && a.state_out);
   const int deltas = final_state ? chunks : chunks - 1;   // chunks whose dH is needed
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
-  auto stage = [&](int c) { return smem + (c % kStages) * kStage; };
-  auto phase = [&](int c) { return (uint32_t)((c / kStages) & 1); };
+  const int stages = p.state_only ? kStateStages : kStages;
+  const uint32_t k_off = p.state_only ? 0 : QC * kChunkBytes;   // K in a stage, behind Q
+  const uint32_t stride = p.state_only ? (KC + VC) * kChunkBytes : kStage;
+  static_assert(kStateStages * (KC + VC) * kChunkBytes <= kStages * kStage, "the state launch's stages");
+  auto stage = [&](int c) { return smem + (c % stages) * stride; };
+  auto phase = [&](int c) { return (uint32_t)((c / stages) & 1); };
   const int quad = warp & 3;
 
   if (warp < 4) {
@@ -254,14 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         int c = 0;
         bool q_last = false;   // chunk c's Q tile was asked for
         for (; c < chunks; ++c) {
-          const int s = c % kStages, y = t0 + c * kC;
-          const uint32_t q = smem_u32(stage(c)), k = q + QC * kChunkBytes, v = k + KC * kChunkBytes;
-          if (c >= kStages && !wait_bar(bar(sh->kv_empty[s]), phase(c - kStages), wc)) break;
+          const int s = c % stages, y = t0 + c * kC;
+          const uint32_t q = smem_u32(stage(c)), k = q + k_off, v = k + KC * kChunkBytes;
+          if (c >= stages && !wait_bar(bar(sh->kv_empty[s]), phase(c - stages), wc)) break;
           mbar_expect_tx(bar(sh->kv_full[s]), (KC + VC) * kChunkBytes);
           for (int x = 0; x < KC; ++x) tma_load_2d(k + x * kChunkBytes, &p.tk, h * DK + x * 64, y, bar(sh->kv_full[s]));
           for (int x = 0; x < VC; ++x) tma_load_2d(v + x * kChunkBytes, &p.tv, h * DV + x * 64, y, bar(sh->kv_full[s]));
           if (p.state_only) continue;
-          if (c >= kStages && !wait_bar(bar(sh->q_empty[s]), phase(c - kStages), wc)) {
+          if (c >= stages && !wait_bar(bar(sh->q_empty[s]), phase(c - stages), wc)) {
             ++c;
             q_last = true;     // (its K and V were asked for, its Q was not)
             break;
@@ -269,9 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           mbar_expect_tx(bar(sh->q_full[s]), KC * kChunkBytes);
           for (int x = 0; x < KC; ++x) tma_load_2d(q + x * kChunkBytes, &p.tq, h * DK + x * 64, y, bar(sh->q_full[s]));
         }
-        for (int i = max(0, c - kStages); i < c; ++i) {   // (an abort may leave copies in flight)
-          drain_bar(bar(sh->kv_full[i % kStages]), phase(i), a.wait_ns);
-          if (!p.state_only && !(q_last && i == c - 1)) drain_bar(bar(sh->q_full[i % kStages]), phase(i), a.wait_ns);
+        for (int i = max(0, c - stages); i < c; ++i) {   // (an abort may leave copies in flight)
+          drain_bar(bar(sh->kv_full[i % stages]), phase(i), a.wait_ns);
+          if (!p.state_only && !(q_last && i == c - 1)) drain_bar(bar(sh->q_full[i % stages]), phase(i), a.wait_ns);
         }
       }
     } else if (warp == 1 && !p.state_only) {
@@ -281,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const uint32_t id_o = idesc_16(F16, kC, DV, false, true);
       const uint64_t dh = desc_kmajor(smem_u32(Hb));
       for (int c = 0; c < chunks; ++c) {
-        const int s = c % kStages;
-        const uint32_t q = smem_u32(stage(c)), k = q + QC * kChunkBytes, v = k + KC * kChunkBytes;
+        const int s = c % stages;
+        const uint32_t q = smem_u32(stage(c)), k = q + k_off, v = k + KC * kChunkBytes;
         const uint64_t dq = desc_kmajor(q), dk = desc_kmajor(k), dv = desc_mnmajor(v, kChunkBytes);
         if (!wait_bar_warp(bar(sh->kv_full[s]), phase(c), wc)) break;
         if (!wait_bar_warp(bar(sh->q_full[s]), phase(c), wc)) break;
@@ -325,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const uint32_t id_d = idesc_16(F16, kC, DK, false, true);
       bool ok = true;
       for (int c = 0; c < deltas && ok; ++c) {
-        const uint64_t dk = desc_mnmajor(smem_u32(stage(c)) + QC * kChunkBytes, kChunkBytes);
-        if (!(ok = wait_bar_warp(bar(sh->kv_full[c % kStages]), phase(c), wc))) break;
+        const uint64_t dk = desc_mnmajor(smem_u32(stage(c)) + k_off, kChunkBytes);
+        if (!(ok = wait_bar_warp(bar(sh->kv_full[c % stages]), phase(c), wc))) break;
         if (ragged && c == chunks - 1 && !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;
         if (c > 0 && !(ok = wait_bar_warp(bar(sh->dh_free), (c - 1) & 1, wc))) break;
 #pragma unroll 1
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             mma_commit(bar(sh->v_free[b]));
             if (g == 3) {
               mma_commit(bar(sh->dh_ready));
-              mma_commit(bar(sh->kv_empty[c % kStages]));
+              mma_commit(bar(sh->kv_empty[c % stages]));
             }
           }
         }
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             tma_store_2d(&p.to, h * DV + x * 64, t0 + c * kC, smem_u32(stage(c) + x * kChunkBytes));
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive(bar(sh->q_empty[c % kStages]));
+          mbar_arrive(bar(sh->q_empty[c % stages]));
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       }
@@ -507,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     for (int c = 0; c < chunks && ok; ++c) {
       const bool short_chunk = ragged && c == chunks - 1;
       if (c >= deltas && !short_chunk) break;
-      if (!(ok = wait_bar_warp(bar(sh->kv_full[c % kStages]), phase(c), wc))) break;
-      unsigned char* kv = stage(c) + QC * kChunkBytes;   // the K chunks, then the V chunks
+      if (!(ok = wait_bar_warp(bar(sh->kv_full[c % stages]), phase(c), wc))) break;
+      unsigned char* kv = stage(c) + k_off;   // the K chunks, then the V chunks
       if (short_chunk) {
         // Zeros in K and V behind the last token.
         for (int x = 0; x < KC + VC; ++x) {
@@ -690,17 +697,25 @@ cudaError_t launch_width(ChunkParams& p, bool f16, bool split, cudaStream_t st) 
 
 }  // namespace
 
+// One walk over a request's n chunks takes about 3.2 us a chunk.  Split, a request's
+// states are walked first (0.6 of that a chunk), then its segments side by side, each
+// after adding up the states before it (0.6 us for 64 KB); the second launch and
+// its start cost about 6 us.  A split is worth it where that is less and the segments
+// fill SMs that would idle.  Measured: 65536 tokens of 16 heads in nine segments
+// 303 us against 1700; 1000 tokens of 8 heads of width 64 in eight 21 us against 32.
 int linear_seg_len(const dsa_linear_problem& p) {
   constexpr int kWhole = INT32_MAX - 127;
   const int64_t longest = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
   const int64_t even = (int64_t)p.R * p.H / 152;   // tokens of each SM if the work were level
-  if (longest <= 1024 || longest <= even + even / 2) return kWhole;
-  // As many segments per head as SMs, less the ones the requests' ends add.
-  int64_t segs = 152 / p.H - (p.B > 1 ? 1 : 0);
-  if (segs < 1) segs = 1;
-  int64_t len = ((p.R + segs - 1) / segs + 127) / 128 * 128;
-  if (len < 512) len = 512;
-  return (int)len;
+  int64_t segs = 152 / p.H - (p.B - 1);            // segments that find an SM each
+  if (segs < 2) {
+    if (longest <= even + even / 2) return kWhole;
+    segs = 152 / p.H > 0 ? 152 / p.H : 1;
+  }
+  const int64_t len = ((p.R + segs - 1) / segs + 127) / 128 * 128;
+  const double n = (double)((longest + 127) / 128), m = (double)(len / 128);
+  const double sum = 0.6 * p.D_k * p.D_v / 16384;
+  return 3.2 * n > 6.0 + 1.6 * 3.2 * m + sum * n / m ? (int)len : kWhole;
 }
 
 int64_t linear_segs(const dsa_linear_problem& p, int seg_len) { return (int64_t)p.R / seg_len + p.B; }
