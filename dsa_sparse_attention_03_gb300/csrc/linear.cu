@@ -66,7 +66,7 @@ struct ChunkParams {
 struct __align__(16) Shared {
   uint64_t q_full[kStages], kv_full[kStateStages], q_empty[kStages], kv_empty[kStateStages];
   uint64_t s_ready, o_staged, qh_ready, h_ready, p_ready, o_ready, o_free, dh_ready, dh_free, tail, done1, done2;
-  uint64_t v_ready[2], v_free[2], pair[4];
+  uint64_t v_ready[4], v_free[4], pair[4];
   uint32_t tmem;
   int abort;
   int req, seg, nseg, first;       // request, its segment, its segments, their first index; req < 0: nothing
@@ -131,8 +131,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+// 16 lanes x 16 columns in the shape of four 8 x 8 blocks of 16-bit pairs: thread t
+// holds column 4 i + t % 4 of lanes t / 4 (v[2 i]) and t / 4 + 8 (v[2 i + 1]).
+__device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       mbar_init(smem_u32(&sh->kv_full[i]), 1);
       mbar_init(smem_u32(&sh->kv_empty[i]), p.state_only ? 1 : 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sh->v_ready[i]), DV / 32);
       mbar_init(smem_u32(&sh->v_free[i]), 1);
     }
@@ -245,6 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const bool final_state = p.state_only || (seg == nseg - 1 && a.state_out);
   const int deltas = final_state ? chunks : chunks - 1;   // chunks whose dH is needed
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  // Buffers of the decayed V: two, each used twice a chunk; in the state launch four
+  // (it has no S), used once.
+  const int v_bufs = p.state_only ? 4 : 2;
+  auto v_col = [&](int b) -> uint32_t { return b < 2 ? kColV + b * 64 : kColS + (b - 2) * 64; };
   const int stages = p.state_only ? kStateStages : kStages;
   const uint32_t k_off = p.state_only ? 0 : QC * kChunkBytes;   // K in a stage, behind Q
   const uint32_t stride = p.state_only ? (KC + VC) * kChunkBytes : kStage;
@@ -338,15 +344,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (c > 0 && !(ok = wait_bar_warp(bar(sh->dh_free), (c - 1) & 1, wc))) break;
 #pragma unroll 1
         for (int g = 0; g < 4 && ok; ++g) {
-          const int b = g & 1;                       // quarter 4 c + g: buffer g % 2, its use 2 c + g / 2
-          if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), g >> 1, wc))) break;
+          const int b = g & (v_bufs - 1);
+          if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), p.state_only ? c & 1 : g >> 1, wc))) break;
+          const uint32_t va = tmem + v_col(b);
           tc_fence_after();
           {
 #pragma unroll
             for (int t = kTerms - 1; t >= 0; --t)    // the smallest terms first: the sum stays small meanwhile
 #pragma unroll
               for (int x = 0; x < 2; ++x)
-                mma_ts(tmem + kColH, tmem + kColV + b * 64 + t * 16 + x * 8,
+                mma_ts(tmem + kColH, va + t * 16 + x * 8,
                        dk + desc_step((g * 2 + x) * 2048), id_d, g | (kTerms - 1 - t) | x);
             mma_commit(bar(sh->v_free[b]));
             if (g == 3) {
@@ -509,7 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     // the odd quarters.
     const int g0 = warp < 8 ? 1 : 0, gs = p.state_only ? 2 : 1;
     const int d = quad * 32 + lane;                    // column of V
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + kColV;
+    // V is read in 8 x 8 blocks transposed (ldmatrix): a thread holds, of every 8
+    // tokens, two adjacent ones (2 (lane % 4) and the next) of four columns, lane / 4
+    // + 0, 8, 16, 24, and stores them in the matching tensor-memory shape.
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int at_row = ((lane >> 4) << 3) + (lane & 7), at_piece = (lane >> 3) & 1;   // this lane's row address
     bool ok = true;
     for (int c = 0; c < chunks && ok; ++c) {
       const bool short_chunk = ragged && c == chunks - 1;
@@ -528,48 +539,81 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (c >= deltas || !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;   // (they read the zeros below)
       }
       const int m = short_chunk ? last_n : kC;
-      const unsigned char* v = kv + (KC + (d >> 6)) * kChunkBytes + (d & 7) * 2;
-      const int piece = (d >> 3) & 7;
-      auto value = [&](int j) {
-        return to_float<F16>(*reinterpret_cast<const uint16_t*>(v + j * 128 + ((piece ^ (j & 7)) << 4)));
+      // Columns quad * 32 ..: four 16-byte pieces of a row of one V chunk.
+      const uint32_t v = smem_u32(kv) + (KC + (quad >> 1)) * kChunkBytes;
+      auto blocks = [&](int j, int hh, uint32_t* r) {   // tokens j .. j + 15, columns 16 hh ..
+        const int row = j + at_row, piece = (quad & 1) * 4 + hh * 2 + at_piece;
+        ldsm_x4_t(v + row * 128 + ((piece ^ (row & 7)) << 4), r[0], r[1], r[2], r[3]);
       };
       const float* fade = pw + m - 1;          // fade[-j] = lambda^(m-1-j), 0 behind the last token
-      float vf = 1.f, vback = 1.f;
-      if (F16) {                               // the column of V brought into fp16's range
-        float mx = 0.f;
-#pragma unroll 8
-        for (int j = 0; j < kC; ++j) mx = fmaxf(mx, fabsf(value(j)));
-        vf = half_range(mx, &vback);
+      float vf[4] = {1.f, 1.f, 1.f, 1.f};
+      float vback[4];
+      if (F16) {                               // the columns of V brought into fp16's range
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+          float mx[2] = {0.f, 0.f};
+#pragma unroll 1
+          for (int j = 0; j < kC; j += 16) {
+            uint32_t r[4];
+            blocks(j, hh, r);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 x = widen<F16>(r[y]);
+              mx[y & 1] = fmaxf(mx[y & 1], fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 1));
+            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 2));
+          }
+          if (hh == 0) {
+            vf[0] = half_range(mx[0], &vback[0]);
+            vf[1] = half_range(mx[1], &vback[1]);
+          } else {
+            vf[2] = half_range(mx[0], &vback[2]);
+            vf[3] = half_range(mx[1], &vback[3]);
+          }
+        }
       }
 #pragma unroll 1
       for (int g = g0; g < 4; g += gs) {
-        // The buffer's last use was two quarters ago.
-        if ((c > 0 || g > 1) && !(ok = wait_bar_warp(bar(sh->v_free[g & 1]), (g >> 1) ^ 1, wc))) break;
+        const int b = g & (v_bufs - 1);
+        if (p.state_only ? c > 0 : (c > 0 || g > 1))   // the buffer's last use
+          if (!(ok = wait_bar_warp(bar(sh->v_free[b]), p.state_only ? (c - 1) & 1 : (g >> 1) ^ 1, wc))) break;
         tc_fence_after();
-        if (F16 && g == 0) sh->vs[c & 1][d] = exponent_field(vback);
-#pragma unroll 1
-          for (int z = 0; z < 2; ++z) {        // 16 tokens: 8 columns of each term
-            uint32_t w[3][8];
-            const int j0 = g * kQuarter + z * 16;
+        if (F16 && g == 0 && (lane & 3) == 0) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int j = j0 + 2 * y;
-              float x0 = value(j) * (fade[-j] * vf), x1 = value(j + 1) * (fade[-j - 1] * vf);
+          for (int y = 0; y < 4; ++y) sh->vs[c & 1][quad * 32 + (lane >> 2) + 8 * y] = exponent_field(vback[y]);
+        }
+        float2 fd[4];
 #pragma unroll
-              for (int t = 0; t < kTerms; ++t) {
-                w[t][y] = pack16<F16>(x0, x1);
-                const float2 r = widen<F16>(w[t][y]);
-                x0 -= r.x;
-                x1 -= r.y;
-              }
+        for (int y = 0; y < 4; ++y) {
+          const int j = g * kQuarter + 8 * y + 2 * (lane & 3);
+          fd[y] = make_float2(fade[-j], fade[-j - 1]);
+        }
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {       // 16 columns at a time
+          uint32_t r[8], w[kTerms][8];
+          blocks(g * kQuarter, hh, r);
+          blocks(g * kQuarter + 16, hh, r + 4);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            float2 x = mul2(widen<F16>(r[y]), fd[y >> 1]);
+            if (F16) x = mul2(x, make_float2(vf[hh * 2 + (y & 1)], vf[hh * 2 + (y & 1)]));
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) {
+              w[t][y] = pack16<F16>(x.x, x.y);
+              if (t + 1 < kTerms) x = fma2(widen<F16>(w[t][y]), make_float2(-1.f, -1.f), x);
             }
-#pragma unroll
-            for (int t = 0; t < kTerms; ++t) tmem_st8(lanes + (g & 1) * 64 + t * 16 + z * 8, w[t]);
           }
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) tmem_st_16x128_x4(lanes + ((uint32_t)(hh * 16) << 16) + v_col(b) + t * 16, w[t]);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh->v_ready[g & 1]));
+        if (lane == 0) mbar_arrive(bar(sh->v_ready[b]));
       }
     }
    }
