@@ -65,7 +65,8 @@ struct ChunkParams {
 
 struct __align__(16) Shared {
   uint64_t q_full[kStages], kv_full[kStateStages], q_empty[kStages], kv_empty[kStateStages];
-  uint64_t s_ready, o_staged, qh_ready, h_ready, p_ready, o_ready, o_free, dh_ready, dh_free, tail, done1, done2;
+  uint64_t s_ready, o_staged, qh_ready, h_ready, p_ready, o_ready, o_free, tail, done1, done2;
+  uint64_t dh_ready[2], dh_free[2];
   uint64_t v_ready[4], v_free[4], pair[4];
   uint32_t tmem;
   int abort;
@@ -220,8 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     mbar_init(smem_u32(&sh->p_ready), 8);
     mbar_init(smem_u32(&sh->o_ready), 1);
     mbar_init(smem_u32(&sh->o_free), 8);
-    mbar_init(smem_u32(&sh->dh_ready), 1);
-    mbar_init(smem_u32(&sh->dh_free), DV / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh->dh_ready[i]), 1);
+      mbar_init(smem_u32(&sh->dh_free[i]), DV / 32);
+    }
     mbar_init(smem_u32(&sh->tail), DV / 32);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh->pair[i]), 2);
     mbar_init(smem_u32(&sh->done1), 1);
@@ -251,6 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   // (it has no S), used once.
   const int v_bufs = p.state_only ? 4 : 2;
   auto v_col = [&](int b) -> uint32_t { return b < 2 ? kColV + b * 64 : kColS + (b - 2) * 64; };
+  // dH^T likewise: one accumulator, or two in turn (the second in O's place).
+  const int dh_bufs = p.state_only ? 2 : 1;
+  auto dh_col = [&](int c) -> uint32_t { return p.state_only && (c & 1) ? kColO : kColH; };
+  auto dh_phase = [&](int c) { return (uint32_t)(p.state_only ? (c >> 1) & 1 : c & 1); };
   const int stages = p.state_only ? kStateStages : kStages;
   const uint32_t k_off = p.state_only ? 0 : QC * kChunkBytes;   // K in a stage, behind Q
   const uint32_t stride = p.state_only ? (KC + VC) * kChunkBytes : kStage;
@@ -341,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         const uint64_t dk = desc_mnmajor(smem_u32(stage(c)) + k_off, kChunkBytes);
         if (!(ok = wait_bar_warp(bar(sh->kv_full[c % stages]), phase(c), wc))) break;
         if (ragged && c == chunks - 1 && !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;
-        if (c > 0 && !(ok = wait_bar_warp(bar(sh->dh_free), (c - 1) & 1, wc))) break;
+        const int db = c & (dh_bufs - 1);
+        if (c >= dh_bufs && !(ok = wait_bar_warp(bar(sh->dh_free[db]), dh_phase(c - dh_bufs), wc))) break;
 #pragma unroll 1
         for (int g = 0; g < 4 && ok; ++g) {
           const int b = g & (v_bufs - 1);
@@ -353,11 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             for (int t = kTerms - 1; t >= 0; --t)    // the smallest terms first: the sum stays small meanwhile
 #pragma unroll
               for (int x = 0; x < 2; ++x)
-                mma_ts(tmem + kColH, va + t * 16 + x * 8,
+                mma_ts(tmem + dh_col(c), va + t * 16 + x * 8,
                        dk + desc_step((g * 2 + x) * 2048), id_d, g | (kTerms - 1 - t) | x);
             mma_commit(bar(sh->v_free[b]));
             if (g == 3) {
-              mma_commit(bar(sh->dh_ready));
+              mma_commit(bar(sh->dh_ready[db]));
               mma_commit(bar(sh->kv_empty[c % stages]));
             }
           }
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     regs_up<176>();
     if (quad * 32 < DV) {
     const int d = quad * 32 + lane;                    // column of H
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + kColH;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const int64_t head = (int64_t)DK * DV;
     float H[DK];
 #pragma unroll
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (lane == 0) mbar_arrive(bar(sh->h_ready));
       }
       if (c >= deltas) break;
-      if (!(ok = wait_bar_warp(bar(sh->dh_ready), c & 1, wc))) break;
+      if (!(ok = wait_bar_warp(bar(sh->dh_ready[c & (dh_bufs - 1)]), dh_phase(c), wc))) break;
       tc_fence_after();
       {
         const float f = pw[ragged && c == chunks - 1 ? last_n : kC];
@@ -696,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll
         for (int x = 0; x < DK; x += 16) {
           uint32_t e[16];
-          tmem_ld16(lanes + x, e);
+          tmem_ld16(lanes + dh_col(c) + x, e);
           tmem_wait_ld();
 #pragma unroll
           for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, H[x + y], __uint_as_float(e[y]) * vback);
@@ -704,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh->dh_free));
+      if (lane == 0) mbar_arrive(bar(sh->dh_free[c & (dh_bufs - 1)]));
     }
     if (ok && final_state)
       store(p.state_only ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
