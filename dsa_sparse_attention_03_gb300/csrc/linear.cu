@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
     for (int i = 0; i < kStateStages; ++i) {
       mbar_init(smem_u32(&sh->kv_full[i]), 1);
-      mbar_init(smem_u32(&sh->kv_empty[i]), p.state_only ? 1 : 2);
+      mbar_init(smem_u32(&sh->kv_empty[i]), 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sh->v_ready[i]), DV / 32);
@@ -244,7 +244,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   const WaitCtx wc(&sh->abort, a.status, a.wait_ns);
 
   const int n = sh->n, t0 = sh->t0, seg = sh->seg, nseg = sh->nseg;
-  const int chunks = (n + kC - 1) / kC;
+  const int all = (n + kC - 1) / kC;
+  // The state launch walks a segment (whole chunks) from its end: dH of its chunk c
+  // counts with lambda^(128 c), and where that is 0 in fp32 (below 2^-150) the walk
+  // ends.  It leaves the segments' first tokens in the L2 cache, where the second
+  // launch begins.
+  const int chunks = p.state_only ? min(all, (int)fminf(151.f / (-ld2 * kC), 1e9f) + 2) : all;
+  auto token = [&](int c) { return t0 + (p.state_only ? all - 1 - c : c) * kC; };   // first token of chunk c
   const int last_n = n - (chunks - 1) * kC;               // tokens of the last chunk
   const bool ragged = chunks > 0 && last_n < kC;
   const bool final_state = p.state_only || (seg == nseg - 1 && a.state_out);
@@ -274,9 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         int c = 0;
         bool q_last = false;   // chunk c's Q tile was asked for
         for (; c < chunks; ++c) {
-          const int s = c % stages, y = t0 + c * kC;
+          const int s = c % stages, y = token(c);
           const uint32_t q = smem_u32(stage(c)), k = q + k_off, v = k + KC * kChunkBytes;
-          if (c >= stages && !wait_bar(bar(sh->kv_empty[s]), phase(c - stages), wc)) break;
+          // (the state launch's K and V are read last by dH, whose end is dh_ready)
+          if (c >= stages && !(p.state_only ? wait_bar(bar(sh->dh_ready[(c - stages) & 1]), dh_phase(c - stages), wc)
+                                            : wait_bar(bar(sh->kv_empty[s]), phase(c - stages), wc)))
+            break;
           mbar_expect_tx(bar(sh->kv_full[s]), (KC + VC) * kChunkBytes);
           for (int x = 0; x < KC; ++x) tma_load_2d(k + x * kChunkBytes, &p.tk, h * DK + x * 64, y, bar(sh->kv_full[s]));
           for (int x = 0; x < VC; ++x) tma_load_2d(v + x * kChunkBytes, &p.tv, h * DV + x * 64, y, bar(sh->kv_full[s]));
@@ -342,11 +351,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
     } else if (warp == 2) {
       // ---------------------------------------------------------- dH^T
+      // (the decayed V of a chunk is ready only after its K has landed)
       const uint32_t id_d = idesc_16(F16, kC, DK, false, true);
       bool ok = true;
       for (int c = 0; c < deltas && ok; ++c) {
         const uint64_t dk = desc_mnmajor(smem_u32(stage(c)) + k_off, kChunkBytes);
-        if (!(ok = wait_bar_warp(bar(sh->kv_full[c % stages]), phase(c), wc))) break;
         if (ragged && c == chunks - 1 && !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;
         const int db = c & (dh_bufs - 1);
         if (c >= dh_bufs && !(ok = wait_bar_warp(bar(sh->dh_free[db]), dh_phase(c - dh_bufs), wc))) break;
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             mma_commit(bar(sh->v_free[b]));
             if (g == 3) {
               mma_commit(bar(sh->dh_ready[db]));
-              mma_commit(bar(sh->kv_empty[c % stages]));
+              if (!p.state_only) mma_commit(bar(sh->kv_empty[c % stages]));
             }
           }
         }
@@ -518,11 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (whole) mbar_arrive(bar(sh->o_staged));
       }
     }
-   } else if ((warp < 8 || warp >= 12) && quad * 32 < DV) {
+   } else if ((p.state_only || warp >= 12) && quad * 32 < DV) {
     // ------------------------------------------------------------ decay
-    // The first launch of a split call has no rows: there the first row warps take
-    // the odd quarters.
-    const int g0 = warp < 8 ? 1 : 0, gs = p.state_only ? 2 : 1;
+    // Quarter g of chunk c is task 4 c + g.  The state launch has no rows: there the
+    // row warps share the tasks.
+    const int groups = p.state_only ? 3 : 1, group = p.state_only ? (warp >> 2) - 1 : 0;
     const int d = quad * 32 + lane;                    // column of V
     // V is read in 8 x 8 blocks transposed (ldmatrix): a thread holds, of every 8
     // tokens, two adjacent ones (2 (lane % 4) and the next) of four columns, lane / 4
@@ -533,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     for (int c = 0; c < chunks && ok; ++c) {
       const bool short_chunk = ragged && c == chunks - 1;
       if (c >= deltas && !short_chunk) break;
+      const int g0 = (group + 3 * groups - 4 * c % groups) % groups;   // this group's first quarter of the chunk
       if (!(ok = wait_bar_warp(bar(sh->kv_full[c % stages]), phase(c), wc))) break;
       unsigned char* kv = stage(c) + k_off;   // the K chunks, then the V chunks
       if (short_chunk) {
@@ -585,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
       }
 #pragma unroll 1
-      for (int g = g0; g < 4; g += gs) {
+      for (int g = g0; g < 4; g += groups) {
         const int b = g & (v_bufs - 1);
         if (p.state_only ? c > 0 : (c > 0 || g > 1))   // the buffer's last use
           if (!(ok = wait_bar_warp(bar(sh->v_free[b]), p.state_only ? (c - 1) & 1 : (g >> 1) ^ 1, wc))) break;
@@ -644,26 +654,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       for (int x = 0; x < DK; ++x) dst[x * DV + d] = H[x];
     };
     float* ends = a.seg_state + ((int64_t)sh->first * a.H + h) * head;   // [segment] of this request, H heads apart
-    if (seg == 0) {
-      if (nseg > 1 && !p.state_only)
-        load(ends + (int64_t)(nseg - 1) * a.H * head);   // the first launch's copy: state_out may be state_in
-      else if (a.state_in)
-        load(a.state_in + ((int64_t)place * a.H + h) * head);
-      if (p.state_only) store(ends + (int64_t)(nseg - 1) * a.H * head);
-    } else if (!p.state_only) {
-      // lambda^(seg_len (seg - 1 - s)) E_s summed over the segments s before this one.
-      const float f = exp2f(fmaxf(ld2 * (float)a.seg_len, -300.f));
-      load(ends);
-      for (int s = 1; s < seg; ++s) {
-        const float* e = ends + (int64_t)s * a.H * head;
+    const float* start = seg == 0 && a.state_in ? a.state_in + ((int64_t)place * a.H + h) * head : nullptr;
+    float* copy = ends + (int64_t)(nseg - 1) * a.H * head;   // of the start: state_out may be state_in
+    auto decay_of = [&](int segs) { return exp2f(fmaxf(ld2 * ((float)a.seg_len * (float)segs), -300.f)); };
+    if (!p.state_only) {
+      if (seg == 0) {
+        if (nseg > 1)
+          load(copy);
+        else if (start)
+          load(start);
+      } else {
+        // lambda^(seg_len (seg - 1 - s)) E_s summed over the segments s before this one.
+        load(ends + (int64_t)(seg - 1) * a.H * head);
+        for (int s = seg - 2; s >= 0; --s) {
+          const float f = decay_of(seg - 1 - s);
+          if (f == 0.f) break;
+          const float* e = ends + (int64_t)s * a.H * head;
 #pragma unroll
-        for (int x = 0; x < DK; x += 16) {
-          float t[16];
+          for (int x = 0; x < DK; x += 16) {
+            float t[16];
 #pragma unroll
-          for (int y = 0; y < 16; ++y) t[y] = e[(x + y) * DV + d];
+            for (int y = 0; y < 16; ++y) t[y] = e[(x + y) * DV + d];
 #pragma unroll
-          for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, H[x + y], t[y]);
-          asm volatile("" ::: "memory");   // (no more than 16 loads ahead: registers)
+            for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, t[y], H[x + y]);
+            asm volatile("" ::: "memory");   // (no more than 16 loads ahead: registers)
+          }
         }
       }
     }
@@ -699,20 +714,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       if (!(ok = wait_bar_warp(bar(sh->dh_ready[c & (dh_bufs - 1)]), dh_phase(c), wc))) break;
       tc_fence_after();
       {
-        const float f = pw[ragged && c == chunks - 1 ? last_n : kC];
-        const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) : 1.f;
+        // Forwards, H = lambda^n H + dH; backwards, H = H + lambda^(128 c) dH.
+        const float fh = p.state_only ? 1.f : pw[ragged && c == chunks - 1 ? last_n : kC];
+        const float fd = p.state_only ? exp2f(fmaxf(ld2 * (float)(c * kC), -300.f)) : 1.f;
+        const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) * fd : fd;
 #pragma unroll
         for (int x = 0; x < DK; x += 16) {
           uint32_t e[16];
           tmem_ld16(lanes + dh_col(c) + x, e);
           tmem_wait_ld();
 #pragma unroll
-          for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, H[x + y], __uint_as_float(e[y]) * vback);
+          for (int y = 0; y < 16; ++y) H[x + y] = fmaf(fh, H[x + y], __uint_as_float(e[y]) * vback);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh->dh_free[c & (dh_bufs - 1)]));
+    }
+    if (p.state_only && seg == 0) {
+      const float f = decay_of(1);
+#pragma unroll
+      for (int x = 0; x < DK; x += 16) {
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const float v = start ? start[(x + y) * DV + d] : 0.f;
+          copy[(x + y) * DV + d] = v;
+          H[x + y] = fmaf(f, v, H[x + y]);
+        }
+        asm volatile("" ::: "memory");
+      }
     }
     if (ok && final_state)
       store(p.state_only ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
