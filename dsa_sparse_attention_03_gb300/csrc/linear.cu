@@ -682,6 +682,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
       }
     }
+    // lambda^128: rounded to fp32 it would be off the same way with every chunk (a head
+    // that remembers 4096 tokens by 30 times that), so the walk takes its two fp32
+    // neighbours in the proportion that keeps their product on the true power.
+    // e^y = (e^(y / 8192))^8192, by a short series and 13 squarings in 64 bits.
+    const float y128 = fminf(a.log_decay[h], 0.f) * kC;
+    const double r = (double)fmaxf(y128, -110.f) * (1.0 / 8192);   // |r| < 0.0135: the series is good to 2^-52
+    double decay = 1.0 + r * (1.0 + r * (1.0 / 2) * (1.0 + r * (1.0 / 3) * (1.0 + r * (1.0 / 4) * (1.0 + r * (1.0 / 5) * (1.0 + r * (1.0 / 6))))));
+#pragma unroll 1
+    for (int x = 0; x < 13; ++x) decay *= decay;
+    if (y128 < -104.f) decay = 0.0;                           // (below fp32's range)
+    float below = pw[kC], above = below, part = 0.f, turn = 0.f;
+    if (pw[kC] <= 1.f) {                                      // (not NaN)
+      below = __double2float_rd(decay);
+      above = __double2float_ru(decay);
+      if (above > below) part = (float)((decay - (double)below) / ((double)above - (double)below));
+    }
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       if (!p.state_only) {
@@ -715,16 +731,32 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       tc_fence_after();
       {
         // Forwards, H = lambda^n H + dH; backwards, H = H + lambda^(128 c) dH.
-        const float fh = p.state_only ? 1.f : pw[ragged && c == chunks - 1 ? last_n : kC];
-        const float fd = p.state_only ? exp2f(fmaxf(ld2 * (float)(c * kC), -300.f)) : 1.f;
-        const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) * fd : fd;
+        float f;
+        if (p.state_only) {
+          f = exp2f(fmaxf(ld2 * (float)(c * kC), -300.f));
+        } else if (ragged && c == chunks - 1) {
+          f = pw[last_n];
+        } else {
+          turn += part;
+          f = turn >= 1.f ? above : below;
+          if (turn >= 1.f) turn -= 1.f;
+        }
+        const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) : 1.f;
+        const float2 f2 = p.state_only ? make_float2(f * vback, f * vback) : make_float2(f, f);
 #pragma unroll
         for (int x = 0; x < DK; x += 16) {
           uint32_t e[16];
           tmem_ld16(lanes + dh_col(c) + x, e);
           tmem_wait_ld();
 #pragma unroll
-          for (int y = 0; y < 16; ++y) H[x + y] = fmaf(fh, H[x + y], __uint_as_float(e[y]) * vback);
+          for (int y = 0; y < 16; y += 2) {
+            float2 g = make_float2(__uint_as_float(e[y]), __uint_as_float(e[y + 1]));
+            const float2 o = make_float2(H[x + y], H[x + y + 1]);
+            if (F16 && !p.state_only) g = mul2(g, make_float2(vback, vback));
+            const float2 r = p.state_only ? fma2(f2, g, o) : fma2(f2, o, g);
+            H[x + y] = r.x;
+            H[x + y + 1] = r.y;
+          }
         }
       }
       tc_fence_before();
