@@ -60,7 +60,6 @@ constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384;
 struct ChunkParams {
   CUtensorMap tq, tk, tv, to;
   LinearArgs a;
-  int state_only;
 };
 
 struct __align__(16) Shared {
@@ -177,7 +176,8 @@ __device__ __forceinline__ float half_range(float m, float* back) {
   return __uint_as_float((268u - e) << 23);
 }
 
-template <int DK, int DV, bool F16>
+// STATE: the first launch of a split call, the segments' end states alone.
+template <int DK, int DV, bool F16, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int KC = DK / 64, VC = DV / 64, QC = KC > VC ? KC : VC;
   constexpr uint32_t kStage = stage_bytes<DK, DV>();
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   if (warp == 0) locate(a, blockIdx.x / a.H, sh, lane);
   __syncthreads();
   if (sh->req < 0) return;
-  if (p.state_only && sh->seg >= sh->nseg - 1) return;   // (no segment follows)
+  if (STATE && sh->seg >= sh->nseg - 1) return;   // (no segment follows)
   const int place = state_place(a, sh->req, &sh->scratch, h == 0 && sh->seg == 0);
   if (place < 0) return;
 
@@ -249,24 +249,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   // counts with lambda^(128 c), and where that is 0 in fp32 (below 2^-150) the walk
   // ends.  It leaves the segments' first tokens in the L2 cache, where the second
   // launch begins.
-  const int chunks = p.state_only ? min(all, (int)fminf(151.f / (-ld2 * kC), 1e9f) + 2) : all;
-  auto token = [&](int c) { return t0 + (p.state_only ? all - 1 - c : c) * kC; };   // first token of chunk c
+  const int chunks = STATE ? min(all, (int)fminf(151.f / (-ld2 * kC), 1e9f) + 2) : all;
+  auto token = [&](int c) { return t0 + (STATE ? all - 1 - c : c) * kC; };   // first token of chunk c
   const int last_n = n - (chunks - 1) * kC;               // tokens of the last chunk
   const bool ragged = chunks > 0 && last_n < kC;
-  const bool final_state = p.state_only || (seg == nseg - 1 && a.state_out);
+  const bool final_state = STATE || (seg == nseg - 1 && a.state_out);
   const int deltas = final_state ? chunks : chunks - 1;   // chunks whose dH is needed
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   // Buffers of the decayed V: two, each used twice a chunk; in the state launch four
   // (it has no S), used once.
-  const int v_bufs = p.state_only ? 4 : 2;
+  const int v_bufs = STATE ? 4 : 2;
   auto v_col = [&](int b) -> uint32_t { return b < 2 ? kColV + b * 64 : kColS + (b - 2) * 64; };
   // dH^T likewise: one accumulator, or two in turn (the second in O's place).
-  const int dh_bufs = p.state_only ? 2 : 1;
-  auto dh_col = [&](int c) -> uint32_t { return p.state_only && (c & 1) ? kColO : kColH; };
-  auto dh_phase = [&](int c) { return (uint32_t)(p.state_only ? (c >> 1) & 1 : c & 1); };
-  const int stages = p.state_only ? kStateStages : kStages;
-  const uint32_t k_off = p.state_only ? 0 : QC * kChunkBytes;   // K in a stage, behind Q
-  const uint32_t stride = p.state_only ? (KC + VC) * kChunkBytes : kStage;
+  const int dh_bufs = STATE ? 2 : 1;
+  auto dh_col = [&](int c) -> uint32_t { return STATE && (c & 1) ? kColO : kColH; };
+  auto dh_phase = [&](int c) { return (uint32_t)(STATE ? (c >> 1) & 1 : c & 1); };
+  const int stages = STATE ? kStateStages : kStages;
+  const uint32_t k_off = STATE ? 0 : QC * kChunkBytes;   // K in a stage, behind Q
+  const uint32_t stride = STATE ? (KC + VC) * kChunkBytes : kStage;
   static_assert(kStateStages * (KC + VC) * kChunkBytes <= kStages * kStage, "the state launch's stages");
   auto stage = [&](int c) { return smem + (c % stages) * stride; };
   auto phase = [&](int c) { return (uint32_t)((c / stages) & 1); };
@@ -283,13 +283,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           const int s = c % stages, y = token(c);
           const uint32_t q = smem_u32(stage(c)), k = q + k_off, v = k + KC * kChunkBytes;
           // (the state launch's K and V are read last by dH, whose end is dh_ready)
-          if (c >= stages && !(p.state_only ? wait_bar(bar(sh->dh_ready[(c - stages) & 1]), dh_phase(c - stages), wc)
+          if (c >= stages && !(STATE ? wait_bar(bar(sh->dh_ready[(c - stages) & 1]), dh_phase(c - stages), wc)
                                             : wait_bar(bar(sh->kv_empty[s]), phase(c - stages), wc)))
             break;
           mbar_expect_tx(bar(sh->kv_full[s]), (KC + VC) * kChunkBytes);
           for (int x = 0; x < KC; ++x) tma_load_2d(k + x * kChunkBytes, &p.tk, h * DK + x * 64, y, bar(sh->kv_full[s]));
           for (int x = 0; x < VC; ++x) tma_load_2d(v + x * kChunkBytes, &p.tv, h * DV + x * 64, y, bar(sh->kv_full[s]));
-          if (p.state_only) continue;
+          if (STATE) continue;
           if (c >= stages && !wait_bar(bar(sh->q_empty[s]), phase(c - stages), wc)) {
             ++c;
             q_last = true;     // (its K and V were asked for, its Q was not)
@@ -300,10 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
         for (int i = max(0, c - stages); i < c; ++i) {   // (an abort may leave copies in flight)
           drain_bar(bar(sh->kv_full[i % stages]), phase(i), a.wait_ns);
-          if (!p.state_only && !(q_last && i == c - 1)) drain_bar(bar(sh->q_full[i % stages]), phase(i), a.wait_ns);
+          if (!STATE && !(q_last && i == c - 1)) drain_bar(bar(sh->q_full[i % stages]), phase(i), a.wait_ns);
         }
       }
-    } else if (warp == 1 && !p.state_only) {
+    } else if (warp == 1 && !STATE) {
       // ---------------------------------------------------------- S, Q H, P V
       const uint32_t id_s = idesc_16(F16, kC, kC, false, false);
       const uint32_t id_h = idesc_16(F16, kC, DV, false, false);
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll 1
         for (int g = 0; g < 4 && ok; ++g) {
           const int b = g & (v_bufs - 1);
-          if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), p.state_only ? c & 1 : g >> 1, wc))) break;
+          if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), STATE ? c & 1 : g >> 1, wc))) break;
           const uint32_t va = tmem + v_col(b);
           tc_fence_after();
           {
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             mma_commit(bar(sh->v_free[b]));
             if (g == 3) {
               mma_commit(bar(sh->dh_ready[db]));
-              if (!p.state_only) mma_commit(bar(sh->kv_empty[c % stages]));
+              if (!STATE) mma_commit(bar(sh->kv_empty[c % stages]));
             }
           }
         }
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         mma_commit(bar(sh->done2));
         drain_bar(bar(sh->done2), 0, a.wait_ns);
       }
-    } else if (warp == 3 && !p.state_only) {
+    } else if (warp == 3 && !STATE) {
       // ---------------------------------------------------------- output tiles
       if (lane == 0) {
         for (int c = 0; c < chunks - (ragged ? 1 : 0); ++c) {
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
   } else if (warp < 16) {
    regs_down<88>();
-   if (warp < 12 && !p.state_only) {
+   if (warp < 12 && !STATE) {
     // ------------------------------------------------------------ rows
     const int half = (warp >> 2) - 1;   // this thread's blocks of 32 columns: half, half + 2
     const int i = quad * 32 + lane;     // token of the chunk
@@ -527,11 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (whole) mbar_arrive(bar(sh->o_staged));
       }
     }
-   } else if ((p.state_only || warp >= 12) && quad * 32 < DV) {
+   } else if ((STATE || warp >= 12) && quad * 32 < DV) {
     // ------------------------------------------------------------ decay
     // Quarter g of chunk c is task 4 c + g.  The state launch has no rows: there the
     // row warps share the tasks.
-    const int groups = p.state_only ? 3 : 1, group = p.state_only ? (warp >> 2) - 1 : 0;
+    const int groups = STATE ? 3 : 1, group = STATE ? (warp >> 2) - 1 : 0;
     const int d = quad * 32 + lane;                    // column of V
     // V is read in 8 x 8 blocks transposed (ldmatrix): a thread holds, of every 8
     // tokens, two adjacent ones (2 (lane % 4) and the next) of four columns, lane / 4
@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 #pragma unroll 1
       for (int g = g0; g < 4; g += groups) {
         const int b = g & (v_bufs - 1);
-        if (p.state_only ? c > 0 : (c > 0 || g > 1))   // the buffer's last use
-          if (!(ok = wait_bar_warp(bar(sh->v_free[b]), p.state_only ? (c - 1) & 1 : (g >> 1) ^ 1, wc))) break;
+        if (STATE ? c > 0 : (c > 0 || g > 1))   // the buffer's last use
+          if (!(ok = wait_bar_warp(bar(sh->v_free[b]), STATE ? (c - 1) & 1 : (g >> 1) ^ 1, wc))) break;
         tc_fence_after();
         if (F16 && g == 0 && (lane & 3) == 0) {
 #pragma unroll
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     const float* start = seg == 0 && a.state_in ? a.state_in + ((int64_t)place * a.H + h) * head : nullptr;
     float* copy = ends + (int64_t)(nseg - 1) * a.H * head;   // of the start: state_out may be state_in
     auto decay_of = [&](int segs) { return exp2f(fmaxf(ld2 * ((float)a.seg_len * (float)segs), -300.f)); };
-    if (!p.state_only) {
+    if (!STATE) {
       if (seg == 0) {
         if (nseg > 1)
           load(copy);
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
-      if (!p.state_only) {
+      if (!STATE) {
         // H in the operands' type, once Q H of the chunk before has read the last one.
         if (c > 0 && !(ok = wait_bar_warp(bar(sh->qh_ready), (c - 1) & 1, wc))) break;
         {
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       {
         // Forwards, H = lambda^n H + dH; backwards, H = H + lambda^(128 c) dH.
         float f;
-        if (p.state_only) {
+        if (STATE) {
           f = exp2f(fmaxf(ld2 * (float)(c * kC), -300.f));
         } else if (ragged && c == chunks - 1) {
           f = pw[last_n];
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           if (turn >= 1.f) turn -= 1.f;
         }
         const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) : 1.f;
-        const float2 f2 = p.state_only ? make_float2(f * vback, f * vback) : make_float2(f, f);
+        const float2 f2 = STATE ? make_float2(f * vback, f * vback) : make_float2(f, f);
 #pragma unroll
         for (int x = 0; x < DK; x += 16) {
           uint32_t e[16];
@@ -752,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           for (int y = 0; y < 16; y += 2) {
             float2 g = make_float2(__uint_as_float(e[y]), __uint_as_float(e[y + 1]));
             const float2 o = make_float2(H[x + y], H[x + y + 1]);
-            if (F16 && !p.state_only) g = mul2(g, make_float2(vback, vback));
-            const float2 r = p.state_only ? fma2(f2, g, o) : fma2(f2, o, g);
+            if (F16 && !STATE) g = mul2(g, make_float2(vback, vback));
+            const float2 r = STATE ? fma2(f2, g, o) : fma2(f2, o, g);
             H[x + y] = r.x;
             H[x + y + 1] = r.y;
           }
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh->dh_free[c & (dh_bufs - 1)]));
     }
-    if (p.state_only && seg == 0) {
+    if (STATE && seg == 0) {
       const float f = decay_of(1);
 #pragma unroll
       for (int x = 0; x < DK; x += 16) {
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
     }
     if (ok && final_state)
-      store(p.state_only ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
+      store(STATE ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
     }
   }
   tc_fence_before();
@@ -790,16 +790,16 @@ template <int DK, int DV, bool F16>
 cudaError_t launch_one(ChunkParams& p, bool split, cudaStream_t st) {
   constexpr size_t smem = smem_bytes<DK, DV>();
   static_assert(smem <= 232448, "shared memory of one CTA");
-  auto kernel = linear_chunk_kernel<DK, DV, F16>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)p.a.segs * (unsigned)p.a.H;
+  cudaError_t e;
   if (split) {
-    p.state_only = 1;
-    kernel<<<grid, kThreads, smem, st>>>(p);
+    auto states = linear_chunk_kernel<DK, DV, F16, true>;
+    if ((e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    states<<<grid, kThreads, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  p.state_only = 0;
+  auto kernel = linear_chunk_kernel<DK, DV, F16, false>;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
   kernel<<<grid, kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
