@@ -116,10 +116,10 @@ __device__ __forceinline__ void request_rows(const DenseArgs& a, int b, int& r0,
 // Item `idx` (one warp).  Row tiles are numbered over the requests; the last ones
 // (a causal prompt's longest) come first, K/V heads and parts vary fastest.
 template <int NW>
-__device__ void find_item(const DenseArgs& a, int64_t idx, Shared* sh, Item* it, int lane) {
-  const int h = (int)(idx % a.H_kv);
-  const int split = (int)(idx / a.H_kv % a.splits);
-  const int want = sh->first[kBlocks] - 1 - (int)(idx / a.H_kv / a.splits);
+__device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it, int lane) {
+  const uint32_t hs = idx / (uint32_t)a.H_kv, ts = hs / (uint32_t)a.splits;
+  const int h = (int)(idx - hs * a.H_kv), split = (int)(hs - ts * a.splits);
+  const int want = sh->first[kBlocks] - 1 - (int)ts;
   if (want < 0) {
     if (lane == 0) it->rows = 0;
     return;
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  pdl_trigger();   // (the join, if any, may take its place; it waits for this grid's end)
   if (warp == 1) tmem_alloc(smem_u32(&sh->tmem), kCols);
   if (warp == 2) {
     // Row tiles before each block of requests.
@@ -273,8 +274,8 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
    regs_down<56>();
    if (warp == 3) {
     // ------------------------------------------------------------ scheduler
-    int64_t idx;
-    const int64_t items = (int64_t)a.tiles * a.splits * a.H_kv;
+    uint32_t idx;
+    const uint32_t items = (uint32_t)a.tiles * a.splits * a.H_kv;   // (dense_shape keeps it below 2^31)
     for (int k = 0;; ++k) {
       // Not before the producer nears the end of the last one: an item taken early
       // is one that no idle CTA can take.
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
       } else {
         uint32_t t = 0;
         if (lane == 0) t = atomicAdd(a.next, 1u);
-        idx = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, t, 0);
+        idx = gridDim.x + __shfl_sync(0xffffffffu, t, 0);
       }
       if (k >= 2 && !wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc)) break;
       Item* it = &sh->item[k & 1];
@@ -625,15 +626,16 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const float* part, cons
   constexpr int E = DV / 32;
   float acc[E] = {}, L = 0.f;
   bool any = false;
+#pragma unroll 8
   for (int i = 0; i < splits; ++i) {
     const float2 v = ml[rh * splits + i];
-    if (v.y == 0.f) continue;
-    any = true;
-    const float f = ex2(v.x - M);
-    L += f * v.y;
+    const bool seen = v.y != 0.f;   // (a part that saw nothing has no O)
+    any |= seen;
+    const float f = seen ? ex2(v.x - M) : 0.f;
+    L = fmaf(f, v.y, L);
     const float* p = part + (rh * splits + i) * DV + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, p[e], acc[e]);
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, seen ? p[e] : 0.f, acc[e]);
   }
   const float inv = any ? 1.f / L : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(out + rh * DV + lane * E);
@@ -687,6 +689,9 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
   if (items > 0 && items < each * slots) splits = p.B == 1 ? slots / items : (each * slots + items - 1) / items;
   const int64_t cap = kvt / 2 < 64 ? kvt / 2 : 64;
   if (splits > cap) splits = cap;
+  // Finer parts than one a slot only while they keep sixteen tiles.
+  const int64_t wave = items > 0 && slots / items > 1 ? slots / items : 1;
+  if (splits > wave && splits > kvt / 16) splits = wave > kvt / 16 ? wave : kvt / 16;
   s.splits = splits < 1 ? 1 : (int)splits;
   return s;
 }

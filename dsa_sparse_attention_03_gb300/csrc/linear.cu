@@ -666,18 +666,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       } else {
         // lambda^(seg_len (seg - 1 - s)) E_s summed over the segments s before this one.
         load(ends + (int64_t)(seg - 1) * a.H * head);
-        for (int s = seg - 2; s >= 0; --s) {
-          const float f = decay_of(seg - 1 - s);
-          if (f == 0.f) break;
-          const float* e = ends + (int64_t)s * a.H * head;
+        int s0 = seg - 1;                                // first segment that still counts
+        while (s0 > 0 && decay_of(seg - s0) != 0.f) --s0;
+        const int64_t step = (int64_t)a.H * head;
 #pragma unroll
-          for (int x = 0; x < DK; x += 16) {
+        for (int x = 0; x < DK; x += 16) {               // (16 values of two segments in flight)
+#pragma unroll 2
+          for (int s = seg - 2; s >= s0; --s) {
+            const float f = decay_of(seg - 1 - s);
+            const float* e = ends + s * step + x * DV + d;
             float t[16];
 #pragma unroll
-            for (int y = 0; y < 16; ++y) t[y] = e[(x + y) * DV + d];
+            for (int y = 0; y < 16; ++y) t[y] = e[y * DV];
 #pragma unroll
             for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, t[y], H[x + y]);
-            asm volatile("" ::: "memory");   // (no more than 16 loads ahead: registers)
           }
         }
       }
