@@ -76,7 +76,8 @@ EXPORTS = ("dsa_version", "dsa_last_error_string", "dsa_indexer_kind", "dsa_deco
            "dsa_linear_workspace_size", "dsa_linear_attn", "dsa_linear_step",
            # include/dsa_testing.h
            "dsa_test_topk_missing_arrival", "dsa_test_attn_missing_gather",
-           "dsa_test_indexer_missing_tile")
+           "dsa_test_indexer_missing_tile", "dsa_test_dense_missing_tile",
+           "dsa_test_linear_missing_tile")
 
 
 class dsa_problem(ctypes.Structure):
@@ -162,6 +163,8 @@ def _load() -> ctypes.CDLL:
         ("dsa_dense_attn", [DP, vp, vp, vp, sz, vp]),
         ("dsa_linear_attn", [LP, vp, vp, vp, vp, sz, vp]),
         ("dsa_linear_step", [LP, vp, vp, vp, vp, sz, vp]),
+        ("dsa_test_dense_missing_tile", [DP, vp, vp, vp, sz, ctypes.c_int64, vp]),
+        ("dsa_test_linear_missing_tile", [LP, vp, vp, vp, vp, sz, ctypes.c_int64, vp]),
         ("dsa_test_topk_missing_arrival", [P, vp, vp, vp, vp, sz, ctypes.c_int, ctypes.c_int64, vp]),
         ("dsa_test_attn_missing_gather", [P, vp, vp, vp, vp, vp, sz, ctypes.c_int64, vp]),
         ("dsa_test_indexer_missing_tile", [P, vp, vp, sz, ctypes.c_int64, vp]),
@@ -602,3 +605,15 @@ def dsa_linear_attn(prob: LinearProblem, state_in, state_out, out, ws, stream=No
 def dsa_linear_step(prob: LinearProblem, state_in, state_out, out, ws, stream=None) -> None:
     """One token of each request; arguments as dsa_linear_attn."""
     _linear_call(_lib.dsa_linear_step, prob, state_in, state_out, out, ws, stream)
+
+
+# Test hooks of these calls (include/dsa_testing.h).
+
+def dsa_test_dense_missing_tile(prob: DenseProblem, out, lse, ws, limit_ns, stream=None) -> None:
+    _check(_lib.dsa_test_dense_missing_tile(ctypes.byref(prob.c), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                            int(limit_ns), _stream(stream)))
+
+
+def dsa_test_linear_missing_tile(prob: LinearProblem, state_in, state_out, out, ws, limit_ns, stream=None) -> None:
+    _check(_lib.dsa_test_linear_missing_tile(ctypes.byref(prob.c), _ptr(state_in), _ptr(state_out), _ptr(out),
+                                             _ptr(ws), ws.numel(), int(limit_ns), _stream(stream)))

@@ -467,8 +467,7 @@ dsa_status dense_plan(const dsa_dense_problem* p, DensePlan* dp) {
   dp->shape = dense_shape(*p);
   size_t off = 256;
   dp->off_ml = dp->off_part = off;
-  if (dp->shape.splits > 1) {
-    const size_t parts = size_t(p->R) * p->H_q * dp->shape.splits;
+  if (const size_t parts = dense_parts(*p, dp->shape)) {
     off = align_up(off + parts * 8, 256);
     dp->off_part = off;
     off = align_up(off + parts * p->D_v * 4, 256);
@@ -485,9 +484,8 @@ size_t dsa_dense_workspace_size(const dsa_dense_problem* p) {
   return dense_plan(p, &dp) == DSA_OK ? dp.total : 0;
 }
 
-dsa_status dsa_dense_attn(const dsa_dense_problem* p, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
-                          void* stream) {
-  g_err.clear();
+static dsa_status run_dense(const dsa_dense_problem* p, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                            void* stream, const TestHooks* hooks) {
   DensePlan dp;
   dsa_status s = dense_plan(p, &dp);
   if (s != DSA_OK) return s;
@@ -508,9 +506,15 @@ dsa_status dsa_dense_attn(const dsa_dense_problem* p, uint16_t* out, float* lse,
   if (e != cudaSuccess) return cuda_fail(e, "clear status");
   if (p->R == 0) return DSA_OK;
   e = launch_dense(*p, dp.shape, out, lse, reinterpret_cast<float*>(w + dp.off_part),
-                   reinterpret_cast<float*>(w + dp.off_ml), static_cast<uint32_t*>(ws), st);
+                   reinterpret_cast<float*>(w + dp.off_ml), static_cast<uint32_t*>(ws), st, hooks);
   if (e != cudaSuccess) return cuda_fail(e, "dense attention");
   return DSA_OK;
+}
+
+dsa_status dsa_dense_attn(const dsa_dense_problem* p, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                          void* stream) {
+  g_err.clear();
+  return run_dense(p, out, lse, ws, ws_bytes, stream, nullptr);
 }
 
 // ------------------------------------------------------------ linear attention
@@ -592,9 +596,8 @@ size_t dsa_linear_workspace_size(const dsa_linear_problem* p) {
   return linear_plan(p, &lp) == DSA_OK ? lp.total : 0;
 }
 
-dsa_status dsa_linear_attn(const dsa_linear_problem* p, const float* state_in, float* state_out, uint16_t* out,
-                           void* ws, size_t ws_bytes, void* stream) {
-  g_err.clear();
+static dsa_status run_linear(const dsa_linear_problem* p, const float* state_in, float* state_out, uint16_t* out,
+                             void* ws, size_t ws_bytes, void* stream, const TestHooks* hooks) {
   LinearPlan lp;
   dsa_status s = linear_plan(p, &lp);
   if (s != DSA_OK) return s;
@@ -607,9 +610,19 @@ dsa_status dsa_linear_attn(const dsa_linear_problem* p, const float* state_in, f
   a.state_in = state_in; a.state_out = state_out; a.out = out;
   a.seg_state = reinterpret_cast<float*>(static_cast<char*>(ws) + lp.off_seg);
   a.status = static_cast<uint32_t*>(ws);
+  if (hooks) {
+    a.wait_ns = hooks->wait_ns;
+    a.test_no_load = hooks->tile_no_load;
+  }
   e = launch_linear(a, p->flags & DSA_FLAG_FP16, lp.split, st);
   if (e != cudaSuccess) return cuda_fail(e, "linear attention");
   return DSA_OK;
+}
+
+dsa_status dsa_linear_attn(const dsa_linear_problem* p, const float* state_in, float* state_out, uint16_t* out,
+                           void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  return run_linear(p, state_in, state_out, out, ws, ws_bytes, stream, nullptr);
 }
 
 dsa_status dsa_linear_step(const dsa_linear_problem* p, const float* state_in, float* state_out, uint16_t* out,
@@ -706,6 +719,26 @@ dsa_status dsa_test_indexer_missing_tile(const dsa_problem* p, int32_t* scores, 
                                     static_cast<cudaStream_t>(stream), &h);
   if (e != cudaSuccess) return cuda_fail(e, "indexer (tensor core)");
   return DSA_OK;
+}
+
+dsa_status dsa_test_dense_missing_tile(const dsa_dense_problem* p, uint16_t* out, float* lse, void* ws,
+                                       size_t ws_bytes, int64_t limit_ns, void* stream) {
+  g_err.clear();
+  TestHooks h;
+  const dsa_status s = check_limit(limit_ns, &h);
+  if (s != DSA_OK) return s;
+  h.tile_no_load = 1;
+  return run_dense(p, out, lse, ws, ws_bytes, stream, &h);
+}
+
+dsa_status dsa_test_linear_missing_tile(const dsa_linear_problem* p, const float* state_in, float* state_out,
+                                        uint16_t* out, void* ws, size_t ws_bytes, int64_t limit_ns, void* stream) {
+  g_err.clear();
+  TestHooks h;
+  const dsa_status s = check_limit(limit_ns, &h);
+  if (s != DSA_OK) return s;
+  h.tile_no_load = 1;
+  return run_linear(p, state_in, state_out, out, ws, ws_bytes, stream, &h);
 }
 
 dsa_status dsa_check_bounds(const dsa_problem* p, int64_t key_row0, int64_t key_rows, void* ws,

@@ -191,6 +191,7 @@ struct TestHooks {
   int topk_skip_cta = -1;              // this top-k CTA returns before its first grid barrier
   int attn_no_gather = 0;              // attention CTAs arm their first gather, issue no copy
   int indexer_no_load = 0;             // indexer CTAs arm their first key tile, issue no copy
+  int tile_no_load = 0;                // dense and linear attention CTAs: the same of their first K tile
 };
 
 // cuTensorMapEncodeTiled from the driver, looked up once through the runtime

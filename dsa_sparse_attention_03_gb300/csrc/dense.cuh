@@ -7,14 +7,19 @@
 namespace dsa {
 
 // How a problem is cut: row tiles of 128 packed rows per CTA (nw), CTAs along
-// the rows (tiles, an upper bound) and parts of the positions (splits).
+// the rows (tiles, an upper bound) and parts of the positions (splits); or, without
+// splits, the last `tail` items (row tile, K/V head) in `tail_parts` parts each.
 struct DenseShape {
-  int nw, tiles, splits;
+  int nw, tiles, splits, tail, tail_parts;
 };
 DenseShape dense_shape(const dsa_dense_problem& p);
 
-// part [R * H_q, splits, D_v] and ml [R * H_q, splits, 2] are used with splits > 1.
+// Parts that the launch leaves for its join: O [parts, D_v] in `part`, (m, l) in `ml`.
+inline size_t dense_parts(const dsa_dense_problem& p, const DenseShape& s) {
+  if (s.splits > 1) return (size_t)p.R * p.H_q * s.splits;
+  return s.tail_parts > 1 ? (size_t)s.tail * s.nw * 128 * s.tail_parts : 0;
+}
 cudaError_t launch_dense(const dsa_dense_problem& p, const DenseShape& s, uint16_t* out, float* lse, float* part,
-                         float* ml, uint32_t* status, cudaStream_t st);
+                         float* ml, uint32_t* status, cudaStream_t st, const TestHooks* hooks = nullptr);
 
 }  // namespace dsa

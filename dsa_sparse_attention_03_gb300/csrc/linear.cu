@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   // counts with lambda^(128 c), and where that is 0 in fp32 (below 2^-150) the walk
   // ends.  It leaves the segments' first tokens in the L2 cache, where the second
   // launch begins.
-  const int chunks = STATE ? min(all, (int)fminf(151.f / (-ld2 * kC), 1e9f) + 2) : all;
+  const int chunks = STATE ? min(all, (int)fminf(151.f / (fabsf(ld2) * kC), 1e9f) + 2) : all;
   auto token = [&](int c) { return t0 + (STATE ? all - 1 - c : c) * kC; };   // first token of chunk c
   const int last_n = n - (chunks - 1) * kC;               // tokens of the last chunk
   const bool ragged = chunks > 0 && last_n < kC;
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
                                             : wait_bar(bar(sh->kv_empty[s]), phase(c - stages), wc)))
             break;
           mbar_expect_tx(bar(sh->kv_full[s]), (KC + VC) * kChunkBytes);
+          if (a.test_no_load && c == 0) continue;
           for (int x = 0; x < KC; ++x) tma_load_2d(k + x * kChunkBytes, &p.tk, h * DK + x * 64, y, bar(sh->kv_full[s]));
           for (int x = 0; x < VC; ++x) tma_load_2d(v + x * kChunkBytes, &p.tv, h * DV + x * 64, y, bar(sh->kv_full[s]));
           if (STATE) continue;
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         }
         for (int i = max(0, c - stages); i < c; ++i) {   // (an abort may leave copies in flight)
           drain_bar(bar(sh->kv_full[i % stages]), phase(i), a.wait_ns);
-          if (!STATE && !(q_last && i == c - 1)) drain_bar(bar(sh->q_full[i % stages]), phase(i), a.wait_ns);
+          if (!STATE && !(q_last && i == c - 1) && !(a.test_no_load && i == 0)) drain_bar(bar(sh->q_full[i % stages]), phase(i), a.wait_ns);
         }
       }
     } else if (warp == 1 && !STATE) {

@@ -24,6 +24,7 @@ struct LinearArgs {
   int seg_len;              // tokens of a segment (a multiple of 128)
   int segs;                 // segments of the call, at most
   float scale;
+  int test_no_load;         // test hook: arm the first chunk, issue no copy
 };
 
 // Tokens of a segment: a request with more is split, its segments run on

@@ -20,6 +20,8 @@
 #define DSA_TESTING_H
 
 #include "dsa.h"
+#include "dsa_dense.h"
+#include "dsa_linear.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -58,6 +60,19 @@ DSA_API dsa_status dsa_test_attn_missing_gather(const dsa_problem* p, const int3
  */
 DSA_API dsa_status dsa_test_indexer_missing_tile(const dsa_problem* p, int32_t* scores, void* ws,
                                                  size_t ws_bytes, int64_t limit_ns, void* stream);
+
+/*
+ * dsa_dense_attn and dsa_linear_attn with every CTA arming the barrier of its first
+ * K tile but issuing no copy for it: its other roles' waits run out one after
+ * the other or stop at the abort flag, and the kernel frees its tensor memory
+ * and returns.  These kernels' waits count tries of up to about 20 us each, so
+ * `limit_ns` is an order of magnitude.
+ */
+DSA_API dsa_status dsa_test_dense_missing_tile(const dsa_dense_problem* p, uint16_t* out, float* lse, void* ws,
+                                               size_t ws_bytes, int64_t limit_ns, void* stream);
+DSA_API dsa_status dsa_test_linear_missing_tile(const dsa_linear_problem* p, const float* state_in, float* state_out,
+                                                uint16_t* out, void* ws, size_t ws_bytes, int64_t limit_ns,
+                                                void* stream);
 
 #ifdef __cplusplus
 }

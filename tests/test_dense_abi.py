@@ -59,6 +59,14 @@ def test_buffers_refused(dsa):
     assert dsa.lib().dsa_dense_workspace_size(ctypes.byref(_prob(dsa, H_kv=3).c)) == 0
 
 
+def test_hook_limit_refused(dsa):
+    p = _prob(dsa)
+    for limit in (0, -5, 10 ** 11):
+        assert dsa.lib().dsa_test_dense_missing_tile(ctypes.byref(p.c), FAKE, None, ctypes.c_void_p(FAKE), 1 << 40,
+                                                     limit, None) == 1
+        assert b"limit_ns" in dsa.lib().dsa_last_error_string()
+
+
 def test_workspace_holds_parts_only_where_the_cache_is_split(dsa):
     few = dsa.dsa_dense_workspace_size(_prob(dsa, R=1, B=1, L_max=65536, L_total=65536))
     assert few > 256 + 8 * 128 * 4

@@ -41,6 +41,22 @@ def test_split_cache(dk, dv, rows, hq, hkv, L):
     H.check(t, scale, out, lse)
 
 
+@pytest.mark.parametrize("rows,hq,hkv,L", [(2570, 16, 16, 5200), (900, 48, 16, 1900), (2600, 16, 8, 5300)])
+def test_last_wave_in_parts(rows, hq, hkv, L):
+    # A chunk behind a cache as long: more items than SMs, the last ones split and joined.
+    t = H.make([rows], [L], hq, hkv, 64, 64, seed=L)
+    out, lse, bits = H.run(t, 0.125)
+    assert bits == 0
+    keep = sorted({0, 1, 127, 128, rows // 2, rows - 1} | set(range(3, rows, 61)))
+    few = dict(t, q=t["q"][keep], row_len=t["row_len"][keep])
+    import torch
+    few["row_offsets"] = torch.tensor([0, len(keep)], dtype=torch.int32)
+    H.check(few, 0.125, out[keep], lse[keep])
+    again, _, _ = H.run(t, 0.125, rows_max=rows, ws_fill=0xC3)
+    assert again.equal(out)
+    assert torch.isfinite(out.float()).all() and not (out == 77.0).all(dim=2).any()
+
+
 @pytest.mark.parametrize("rows_max", [None, 0, 4000])
 def test_rows_max_only_changes_the_split(rows_max):
     t = H.make([2, 140, 1], [500, 140, 900], 4, 2, 128, 128, seed=9)
@@ -231,3 +247,20 @@ def test_long_offsets_pass_32_bits():
     dsa.dsa_dense_attn(p, out, None, ws)
     assert dsa.dsa_read_device_status(ws) == 0
     H.check(small, 0.09, out.cpu(), None)
+
+
+@pytest.mark.parametrize("rows,lens", [([1], [3000]), ([400, 1], [400, 900])])
+def test_a_wait_that_runs_out(rows, lens):
+    # The first K tile never lands: the call returns with the status bit, and the
+    # workspace and the context go on working.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    t = H.make(rows, lens, 4, 2, 128, 128, seed=20)
+    p, d = H.problem(t, 0.09)
+    out = torch.zeros(p.R, 4, 128, dtype=torch.bfloat16, device="cuda")
+    ws = dsa.alloc_dense_workspace(p)
+    dsa.dsa_test_dense_missing_tile(p, out, None, ws, 1_000_000)
+    assert dsa.dsa_read_device_status(ws) & dsa.DSA_DEVICE_TIMEOUT
+    dsa.dsa_dense_attn(p, out, None, ws)
+    assert dsa.dsa_read_device_status(ws) == 0
+    H.check(t, 0.09, out.cpu(), None)

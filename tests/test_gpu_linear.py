@@ -279,3 +279,30 @@ def test_prompt_then_steps(dtype):
         o, bound, S, sb = ref[b]
         assert bool(((got[b] - o).abs() <= bound).all())
         assert bool(((state[b].cpu().double() - S).abs() <= sb + sb * extra).all())
+
+
+@pytest.mark.parametrize("decay", [0.0, -1e-4, -0.7, -30.0, -float("inf")])
+def test_segments_with_every_decay(decay):
+    # The state launch ends where the decay reaches 0 in fp32: never, or at once.
+    t, s0 = H.make([2500], 1, 128, 64, seed=21, decay=decay)
+    out, state, bits = H.run(t, s0, 0.1)
+    assert bits == 0
+    H.check(t, s0, 0.1, out, state)
+
+
+@pytest.mark.parametrize("rows", [[300], [3000]])
+def test_a_wait_that_runs_out(rows):
+    # The first K and V tile never lands: the call returns with the status bit, and
+    # the workspace and the context go on working.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    t, s0 = H.make(rows, 2, 128, 128, seed=22)
+    d = H.to_device(t)
+    p = dsa.LinearProblem.from_tensors(scale=0.1, **d)
+    out = torch.zeros(rows[0], 2, 128, dtype=torch.bfloat16, device="cuda")
+    sin, sout, ws = s0.cuda(), torch.zeros(1, 2, 128, 128, device="cuda"), dsa.alloc_linear_workspace(p)
+    dsa.dsa_test_linear_missing_tile(p, sin, sout, out, ws, 1_000_000)
+    assert dsa.dsa_read_device_status(ws) & dsa.DSA_DEVICE_TIMEOUT
+    dsa.dsa_linear_attn(p, sin, sout, out, ws)
+    assert dsa.dsa_read_device_status(ws) == 0
+    H.check(t, s0, 0.1, out.cpu(), sout.cpu())
