@@ -556,6 +556,7 @@ dsa_status linear_plan(const dsa_linear_problem* p, LinearPlan* lp) {
   a.k_stride = stride[1] ? stride[1] : pack[1];
   a.v_stride = stride[2] ? stride[2] : pack[2];
   a.wait_ns = kDefaultWaitNs;
+  a.status_known = -1;
   a.R = p->R; a.B = p->B; a.H = p->H; a.D_k = p->D_k; a.D_v = p->D_v; a.n_states = p->n_states;
   a.scale = p->scale;
   a.seg_len = linear_seg_len(*p);
@@ -635,9 +636,12 @@ dsa_status dsa_linear_step(const dsa_linear_problem* p, const float* state_in, f
   if ((s = linear_buffers(p, lp, state_in, state_out, out, ws, ws_bytes)) != DSA_OK) return s;
   if (!state_out) return fail(DSA_ERR_INVALID_ARG, "state_out must be set");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
-  if (e != cudaSuccess) return cuda_fail(e, "clear status");
+  cudaError_t e;
   LinearArgs& a = lp.a;
+  // Without state_idx the status is known here, and the kernel writes it; with it,
+  // the kernel looks for bad places.
+  a.status_known = p->state_idx ? -1 : (p->n_states < p->B ? DSA_DEVICE_BAD_INDEX : 0);
+  if (p->state_idx && (e = cudaMemsetAsync(ws, 0, 256, st)) != cudaSuccess) return cuda_fail(e, "clear status");
   a.state_in = state_in; a.state_out = state_out; a.out = out;
   a.status = static_cast<uint32_t*>(ws);
   e = launch_linear_step(a, p->flags & DSA_FLAG_FP16, st);

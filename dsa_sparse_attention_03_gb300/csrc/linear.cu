@@ -196,10 +196,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   }
   if (warp == 0) locate(a, blockIdx.x / a.H, sh, lane);
   __syncthreads();
-  if (sh->req < 0) return;
-  if (STATE && sh->seg >= sh->nseg - 1) return;   // (no segment follows)
+  // The second launch of a split call starts while the first one ends; its state
+  // warps wait for it (as does every CTA before it leaves).
+  if (STATE) pdl_trigger();
+  if (sh->req < 0 || (STATE && sh->seg >= sh->nseg - 1)) {   // (nothing here; no segment follows)
+    pdl_wait();
+    return;
+  }
   const int place = state_place(a, sh->req, &sh->scratch, h == 0 && sh->seg == 0);
-  if (place < 0) return;
+  if (place < 0) {
+    pdl_wait();
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -655,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       for (int x = 0; x < DK; ++x) dst[x * DV + d] = H[x];
     };
     float* ends = a.seg_state + ((int64_t)sh->first * a.H + h) * head;   // [segment] of this request, H heads apart
+    pdl_wait();
     const float* start = seg == 0 && a.state_in ? a.state_in + ((int64_t)place * a.H + h) * head : nullptr;
     float* copy = ends + (int64_t)(nseg - 1) * a.H * head;   // of the start: state_out may be state_in
     auto decay_of = [&](int segs) { return exp2f(fmaxf(ld2 * ((float)a.seg_len * (float)segs), -300.f)); };
@@ -803,6 +812,7 @@ cudaError_t launch_one(ChunkParams& p, bool split, cudaStream_t st) {
   }
   auto kernel = linear_chunk_kernel<DK, DV, F16, false>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+  if (split) return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, st, p);
   kernel<<<grid, kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }

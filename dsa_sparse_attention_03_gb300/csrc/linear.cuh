@@ -25,6 +25,7 @@ struct LinearArgs {
   int segs;                 // segments of the call, at most
   float scale;
   int test_no_load;         // test hook: arm the first chunk, issue no copy
+  int status_known;         // the status word is this value whatever the kernel finds (-1: it is cleared before, and raised)
 };
 
 // Tokens of a segment: a request with more is split, its segments run on
@@ -42,7 +43,7 @@ cudaError_t launch_linear_step(const LinearArgs& a, bool f16, cudaStream_t st);
 static __device__ inline int state_place(const LinearArgs& a, int b, int* scratch, bool report) {
   if (!a.state_idx) {
     const int ok = b < a.n_states;
-    if (!ok && report && threadIdx.x == 0) raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+    if (!ok && report && threadIdx.x == 0 && a.status_known < 0) raise_status(a.status, DSA_DEVICE_BAD_INDEX);
     return ok ? b : -1;
   }
   const int at = a.state_idx[b];

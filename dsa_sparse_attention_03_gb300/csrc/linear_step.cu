@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
   __shared__ int twice;
   const int h = blockIdx.x % a.H, b = blockIdx.x / a.H;
   const int tid = threadIdx.x, c = tid % C4, r = tid / C4;
+  if (blockIdx.x == 0 && tid == 0 && a.status_known >= 0) *a.status = (uint32_t)a.status_known;
   const int at = state_place(a, b, &twice, h == 0);
   if (at < 0) return;
   const int64_t base = ((int64_t)at * a.H + h) * DK * DV;

@@ -306,3 +306,14 @@ def test_a_wait_that_runs_out(rows):
     dsa.dsa_linear_attn(p, sin, sout, out, ws)
     assert dsa.dsa_read_device_status(ws) == 0
     H.check(t, s0, 0.1, out.cpu(), sout.cpu())
+
+
+@pytest.mark.parametrize("step", [False, True])
+def test_fewer_places_than_requests_is_flagged(step):
+    import dsa_sparse_attention_03_gb300 as dsa
+    rows = [1] * 3 if step else [20, 30, 40]
+    t, s0 = H.make(rows, 2, 64, 64, seed=23, n_states=2)
+    out, state, bits = H.run(t, s0, 0.1, step=step, n_states=2)
+    assert bits & dsa.DSA_DEVICE_BAD_INDEX
+    ro = t["row_offsets"].tolist()
+    assert (out[ro[2]:] == 77.0).all() and not (out[:ro[2]] == 77.0).all()
