@@ -101,3 +101,25 @@ def test_binding_checks(dsa):
     for out in (mk(2, 8, 128), mk(2, 8, 64), mk(2, 8, 128, dt=h), mk(8, 2, 128).transpose(0, 1)):
         with pytest.raises((ValueError, RuntimeError, AssertionError)):
             dsa.dsa_dense_attn(p, out, None, ws)
+
+
+def test_headers_from_c(dsa, tmp_path):
+    # The new headers are C99, alone and together, and lay the structs out as the binding does.
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "h.c"
+    src.write_text('#include "dsa_linear.h"\n#include "dsa_dense.h"\n#include "dsa_testing.h"\n'
+                   "int a[sizeof(dsa_dense_problem) == %d ? 1 : -1];\nint b[sizeof(dsa_linear_problem) == %d ? 1 : -1];\n"
+                   "int main(void) { dsa_dense_problem p = {0}; return dsa_dense_workspace_size(&p) != 0; }\n"
+                   % (ctypes.sizeof(dsa.dsa_dense_problem), ctypes.sizeof(dsa.dsa_linear_problem)))
+    lib = os.path.dirname(dsa.LIB_PATH)
+    exe = str(tmp_path / "h")
+    res = subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(root, "include"), str(src),
+                          "-o", exe, "-L", lib, "-ldsa", "-Wl,-rpath," + lib], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    assert subprocess.run([exe], timeout=120).returncode == 0
