@@ -548,12 +548,27 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) t[x] = fmaxf(t[x], __uint_as_float(v[124 + x]));
           const float mn = fmaxf(max3(m, t[0], t[1]), fmaxf(t[2], t[3]));
-          if (jj == 0) {
-            m = mn;
-          } else if (__any_sync(0xffffffffu, (mn - m) * a.c > 8.f)) {
+          if (jj == 0) m = mn;
+          float mc = m == -INFINITY ? 0.f : m * a.c;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto weights = [&](int half) {
+#pragma unroll
+            for (int x = half * 64; x < half * 64 + 64; x += 2) {
+              const float2 e = fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])),
+                                    make_float2(a.c, a.c), make_float2(-mc, -mc));
+              const float2 p = make_float2(ex2(e.x), ex2(e.y));
+              sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], p);
+              v[x >> 1] = pack16<F16>(p.x, p.y);
+            }
+          };
+          // The first half's weights do not wait for the maximum: it rarely moves the
+          // scale.  Where it does, O and l are rescaled and they are computed again.
+          weights(0);
+          if (__any_sync(0xffffffffu, (mn - m) * a.c > 8.f)) {
             // S of this tile was issued after O += P V of the previous one, so O is still.
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * a.c);
             m = mn;
+            mc = m == -INFINITY ? 0.f : m * a.c;
             l *= f;
 #pragma unroll 1
             for (int x = 0; x < DV; x += 32) {
@@ -564,19 +579,18 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
               for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
               tmem_st32(ot + x, o);
             }
+            tmem_ld32(st, v);
+            tmem_ld32(st + 32, v + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 64; ++x)
+              if (x >= left) v[x] = 0xff800000u;
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            weights(0);
           }
-          const float mc = m == -INFINITY ? 0.f : m * a.c;
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {   // P in two halves: the first one's product starts meanwhile
-#pragma unroll
-            for (int x = half * 64; x < half * 64 + 64; x += 2) {
-              const float2 e = fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])),
-                                    make_float2(a.c, a.c), make_float2(-mc, -mc));
-              const float2 p = make_float2(ex2(e.x), ex2(e.y));
-              sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], p);
-              v[x >> 1] = pack16<F16>(p.x, p.y);
-            }
+            if (half) weights(1);
             tmem_st32(st + half * 32, v + half * 32);
             tmem_wait_st();
             tc_fence_before();
