@@ -465,7 +465,7 @@ dsa_status dense_plan(const dsa_dense_problem* p, DensePlan* dp) {
     return fail(DSA_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
   if (p->flags & ~DSA_FLAG_FP16) return fail(DSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
   dp->shape = dense_shape(*p);
-  size_t off = 256;
+  size_t off = kDensePartsOffset;
   dp->off_ml = dp->off_part = off;
   if (const size_t parts = dense_parts(*p, dp->shape)) {
     off = align_up(off + parts * 8, 256);
@@ -502,7 +502,7 @@ static dsa_status run_dense(const dsa_dense_problem* p, uint16_t* out, float* ls
     return fail(DSA_ERR_INVALID_ARG, "lse/offsets/row_offsets/row_len must be 4-byte aligned");
   char* w = static_cast<char*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  cudaError_t e = launch_clear_status(ws, st);
   if (e != cudaSuccess) return cuda_fail(e, "clear status");
   if (p->R == 0) return DSA_OK;
   e = launch_dense(*p, dp.shape, out, lse, reinterpret_cast<float*>(w + dp.off_part),
@@ -605,7 +605,7 @@ static dsa_status run_linear(const dsa_linear_problem* p, const float* state_in,
   if ((s = linear_buffers(p, lp, state_in, state_out, out, ws, ws_bytes)) != DSA_OK) return s;
   if (!p->row_offsets) return fail(DSA_ERR_INVALID_ARG, "row_offsets must be set");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  cudaError_t e = launch_clear_status(ws, st);
   if (e != cudaSuccess) return cuda_fail(e, "clear status");
   LinearArgs& a = lp.a;
   a.state_in = state_in; a.state_out = state_out; a.out = out;

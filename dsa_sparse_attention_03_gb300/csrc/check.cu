@@ -55,4 +55,16 @@ cudaError_t launch_check_bounds(const int8_t* k, size_t k_bytes, const int8_t* q
   return cudaGetLastError();
 }
 
+namespace {
+__global__ void clear_status_kernel(uint32_t* status) {
+  pdl_trigger();
+  status[threadIdx.x] = 0;
+}
+}  // namespace
+
+cudaError_t launch_clear_status(void* ws, cudaStream_t st) {
+  clear_status_kernel<<<1, 64, 0, st>>>(static_cast<uint32_t*>(ws));
+  return cudaGetLastError();
+}
+
 }  // namespace dsa

@@ -275,7 +275,10 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     if (lane == 0) {
       // (the launch was sized by the declared rows: later tiles come first in the
       // numbering, so those past it are the first requests' and stay unwritten)
-      if (run > a.tiles) raise_status(a.status, DSA_DEVICE_CAPACITY);
+      if (run > a.tiles) {
+        pdl_wait();
+        raise_status(a.status, DSA_DEVICE_CAPACITY);
+      }
       sh->first[kBlocks] = run;
     }
   }
@@ -295,6 +298,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
    regs_down<56>();
    if (warp == 3) {
     // ------------------------------------------------------------ scheduler
+    pdl_wait();              // (the status block and the counter are cleared)
     WaitCtx item_wc = wc;   // an item may take long: a thousand times the limit, or until another role gives up
     item_wc.tries *= 1000;
     uint32_t idx;
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
         idx = blockIdx.x;
       } else {
         uint32_t t = 0;
-        if (lane == 0) t = atomicAdd(a.next, 1u);
+        if (lane == 0 && gridDim.x < items) t = atomicAdd(a.next, 1u);
         idx = gridDim.x + __shfl_sync(0xffffffffu, t, 0);
       }
       if (k >= 2 && !wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc)) break;
@@ -716,8 +720,8 @@ cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = item_count(a), slots = NW == 1 ? 304 : 152;
   const int64_t grid = items < slots ? items : slots;
-  kernel<<<(unsigned)grid, 128 + 128 * NW, smem, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3((unsigned)grid), dim3(128 + 128 * NW), smem, st, a);
+  if (e != cudaSuccess) return e;
   int64_t rows = 0;
   if (a.splits > 1) rows = (int64_t)a.R * a.H_q;
   if (a.tail_parts > 1) rows = (int64_t)(a.tiles * a.H_kv - a.full) * NW * kTile;

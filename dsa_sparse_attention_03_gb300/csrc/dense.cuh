@@ -14,6 +14,12 @@ struct DenseShape {
 };
 DenseShape dense_shape(const dsa_dense_problem& p);
 
+// The workspace: the status block with the counter of items, the parts.  Atomics on
+// a line slow down every access within 4 KB of it (six requests of 22 rows in all:
+// 36 us with the rows just before the workspace, 22 with its parts behind the
+// counter, 19 with neither), so the parts start further on and a call whose items
+// all have a CTA leaves the counter alone.
+constexpr size_t kDensePartsOffset = 4096;
 // Parts that the launch leaves for its join: O [parts, D_v] in `part`, (m, l) in `ml`.
 inline size_t dense_parts(const dsa_dense_problem& p, const DenseShape& s) {
   if (s.splits > 1) return (size_t)p.R * p.H_q * s.splits;

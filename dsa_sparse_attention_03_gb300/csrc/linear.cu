@@ -196,8 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   }
   if (warp == 0) locate(a, blockIdx.x / a.H, sh, lane);
   __syncthreads();
-  // The second launch of a split call starts while the first one ends; its state
-  // warps wait for it (as does every CTA before it leaves).
+  // Each launch starts under the one before it (the clearing of the status block, or
+  // the state launch); its state warps wait for that one's end, as does whoever
+  // touches the status block and every CTA before it leaves.
   if (STATE) pdl_trigger();
   if (sh->req < 0 || (STATE && sh->seg >= sh->nseg - 1)) {   // (nothing here; no segment follows)
     pdl_wait();
@@ -807,14 +808,11 @@ cudaError_t launch_one(ChunkParams& p, bool split, cudaStream_t st) {
   if (split) {
     auto states = linear_chunk_kernel<DK, DV, F16, true>;
     if ((e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    states<<<grid, kThreads, smem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_pdl(states, dim3(grid), dim3(kThreads), smem, st, p)) != cudaSuccess) return e;
   }
   auto kernel = linear_chunk_kernel<DK, DV, F16, false>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-  if (split) return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, st, p);
-  kernel<<<grid, kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, st, p);
 }
 
 template <int DK, int DV>

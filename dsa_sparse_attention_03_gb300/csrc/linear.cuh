@@ -43,7 +43,10 @@ cudaError_t launch_linear_step(const LinearArgs& a, bool f16, cudaStream_t st);
 static __device__ inline int state_place(const LinearArgs& a, int b, int* scratch, bool report) {
   if (!a.state_idx) {
     const int ok = b < a.n_states;
-    if (!ok && report && threadIdx.x == 0 && a.status_known < 0) raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+    if (!ok && report && threadIdx.x == 0 && a.status_known < 0) {
+      pdl_wait();
+      raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+    }
     return ok ? b : -1;
   }
   const int at = a.state_idx[b];
@@ -55,7 +58,10 @@ static __device__ inline int state_place(const LinearArgs& a, int b, int* scratc
   if (twice) *scratch = 1;
   __syncthreads();
   if (*scratch) {
-    if (report && threadIdx.x == 0) raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+    if (report && threadIdx.x == 0) {
+      pdl_wait();
+      raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+    }
     return -1;
   }
   return at;

@@ -68,10 +68,11 @@ def test_hook_limit_refused(dsa):
 
 
 def test_workspace_holds_parts_only_where_the_cache_is_split(dsa):
+    base = dsa.dsa_dense_workspace_size(_prob(dsa, R=0))
     few = dsa.dsa_dense_workspace_size(_prob(dsa, R=1, B=1, L_max=65536, L_total=65536))
-    assert few > 256 + 8 * 128 * 4
-    assert dsa.dsa_dense_workspace_size(_prob(dsa, R=1, B=1, L_max=128, L_total=128)) == 256
-    assert dsa.dsa_dense_workspace_size(_prob(dsa, R=65535, B=1, rows_max=0, L_max=65535, L_total=65535)) == 256
+    assert few > base + 8 * 128 * 4
+    assert dsa.dsa_dense_workspace_size(_prob(dsa, R=1, B=1, L_max=128, L_total=128)) == base
+    assert dsa.dsa_dense_workspace_size(_prob(dsa, R=65535, B=1, rows_max=0, L_max=65535, L_total=65535)) == base
 
 
 def test_binding_checks(dsa):
