@@ -251,18 +251,25 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
   }
   pdl_trigger();   // (the join, if any, may take its place; it waits for this grid's end)
   if (warp == 1) tmem_alloc(smem_u32(&sh->tmem), kCols);
-  if (warp == 2) {
-    // Row tiles before each block of requests.
+  // Row tiles before each block of requests: one request to a block, or counted by
+  // all threads.
+  auto row_tiles = [&](int b) {
+    int r0, n;
+    request_rows(a, b, r0, n);
+    return (n * a.G + NW * kTile - 1) / (NW * kTile);
+  };
+  if (a.B > kBlocks) {
     const int per = (a.B + kBlocks - 1) / kBlocks;
+    if (tid <= kBlocks) sh->first[tid] = 0;
+    __syncthreads();
+    for (int b = tid; b < a.B; b += blockDim.x) atomicAdd(&sh->first[b / per], row_tiles(b));
+    __syncthreads();
+  }
+  if (warp == 2) {
     int run = 0;
     for (int half = 0; half < 2; ++half) {
       const int blk = half * 32 + lane;
-      int v = 0;
-      for (int b = blk * per; b < (blk + 1) * per && b < a.B; ++b) {
-        int r0, n;
-        request_rows(a, b, r0, n);
-        v += (n * a.G + NW * kTile - 1) / (NW * kTile);
-      }
+      const int v = a.B > kBlocks ? sh->first[blk] : (blk < a.B ? row_tiles(blk) : 0);
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

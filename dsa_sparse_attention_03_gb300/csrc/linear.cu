@@ -88,40 +88,81 @@ __host__ __device__ constexpr size_t smem_bytes() {
   return kStages * stage_bytes<DK, DV>() + DV * DK * 2 + sizeof(Shared);
 }
 
-// Segment of this CTA (warp 0).  The requests' segments are numbered from the
-// longest request on (up to 32 requests; more keep their order), so that the
-// longest walks start first.
-__device__ void locate(const LinearArgs& a, int idx, Shared* sh, int lane) {
-  if (lane == 0) sh->req = -1;
-  __syncwarp();
-  int run = 0;
-  for (int base = 0; base < a.B && run <= idx; base += 32) {
-    const int b = base + lane;
+// Request b's first token, tokens and segments, clamped to the call's.
+__device__ __forceinline__ void request(const LinearArgs& a, int b, int& t0, int& n, int& v) {
+  const int x0 = a.row_offsets[b], x1 = a.row_offsets[b + 1];
+  t0 = min(max(x0, 0), a.R);
+  n = max(min(x1, a.R) - t0, 0);
+  v = n > a.seg_len ? (n - 1) / a.seg_len + 1 : 1;
+}
+
+__device__ __forceinline__ void take_segment(const LinearArgs& a, Shared* sh, int b, int s, int first, int t0, int n, int v) {
+  const int skip = s * a.seg_len;   // (below n)
+  sh->req = b;
+  sh->seg = s;
+  sh->nseg = v;
+  sh->first = first;
+  sh->t0 = t0 + skip;
+  sh->n = v == 1 ? n : min(n - skip, a.seg_len);
+}
+
+// Segment `idx` of the call (the whole CTA; the result is there after its next
+// __syncthreads).  Up to 32 requests' segments are numbered from the longest
+// request on, so that the longest walks start first; more keep their order.
+__device__ void locate(const LinearArgs& a, int idx, Shared* sh) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) sh->req = -1;
+  __syncthreads();
+  if (a.B <= 32) {
+    if (warp > 0) return;
     int t0 = 0, n = -1, v = 0;
-    if (b < a.B) {
-      const int x0 = a.row_offsets[b], x1 = a.row_offsets[b + 1];
-      t0 = min(max(x0, 0), a.R);
-      n = max(min(x1, a.R) - t0, 0);
-      v = n > a.seg_len ? (n - 1) / a.seg_len + 1 : 1;
-    }
-    int first = run, all = 0;
-    for (int o = 0; o < 32; ++o) {
+    if (lane < a.B) request(a, lane, t0, n, v);
+    int first = 0;
+    for (int o = 0; o < a.B; ++o) {
       const int on = __shfl_sync(0xffffffffu, n, o), ov = __shfl_sync(0xffffffffu, v, o);
-      all += ov;
-      if (a.B <= 32 ? on > n || (on == n && o < lane) : o < lane) first += ov;
+      if (on > n || (on == n && o < lane)) first += ov;
     }
-    if (idx >= first && idx < first + v) {
-      const int s = idx - first;
-      const int skip = s * a.seg_len;   // (below n)
-      sh->req = b;
-      sh->seg = s;
-      sh->nseg = v;
-      sh->first = first;
-      sh->t0 = t0 + skip;
-      sh->n = v == 1 ? n : min(n - skip, a.seg_len);
-    }
-    run += all;
+    if (idx >= first && idx < first + v) take_segment(a, sh, lane, idx - first, first, t0, n, v);
+    return;
   }
+  if (a.R <= a.seg_len) {   // no request is split
+    if (tid == 0 && idx < a.B) {
+      int t0, n, v;
+      request(a, idx, t0, n, v);
+      take_segment(a, sh, idx, 0, idx, t0, n, v);
+    }
+    return;
+  }
+  // A thread counts the segments of some adjacent requests; the one whose range
+  // holds idx looks for it there.
+  const int per = (a.B + kThreads - 1) / kThreads;
+  int mine = 0;
+  for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) {
+    int t0, n, v;
+    request(a, b, t0, n, v);
+    mine += v;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  int* sums = reinterpret_cast<int*>(sh->pw);   // (the table is filled later)
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int first = incl - mine;
+  for (int w = 0; w < warp; ++w) first += sums[w];
+  if (idx >= first && idx < first + mine)
+    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) {
+      int t0, n, v;
+      request(a, b, t0, n, v);
+      if (idx < first + v) {
+        take_segment(a, sh, b, idx - first, first, t0, n, v);
+        break;
+      }
+      first += v;
+    }
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
@@ -194,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     if (tid == 0) raise_status(a.status, DSA_DEVICE_CAPACITY);
     return;
   }
-  if (warp == 0) locate(a, blockIdx.x / a.H, sh, lane);
+  locate(a, blockIdx.x / a.H, sh);
   __syncthreads();
   // Each launch starts under the one before it (the clearing of the status block, or
   // the state launch); its state warps wait for that one's end, as does whoever

@@ -15,8 +15,8 @@
  *
  * for the rows r of request b.  The mask is each row's own length, as in
  * dsa.h: a causal prompt of n rows over a request of L positions sets
- * row_len = L - n + i + 1 for its row i.  A row that sees nothing (row_len = 0)
- * gets zeros and lse = -inf.  Rows before row_offsets[0] or from row_offsets[B]
+ * row_len = L - n + i + 1 for its row i.  A row that sees nothing (row_len = 0, or
+ * every logit -inf) gets zeros and lse = -inf.  Rows before row_offsets[0] or from row_offsets[B]
  * on are not written.
  *
  * Precision: operands bf16 (or fp16 with DSA_FLAG_FP16), products and sums in

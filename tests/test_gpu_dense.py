@@ -170,10 +170,12 @@ def test_no_rows_and_empty_cache():
     assert bits == 0 and out.numel() == 0
 
 
-def test_many_requests():
-    # More requests than one warp looks up at a time, some without rows.
-    rows = [i % 3 for i in range(100)]
-    lens = [(37 * i) % 211 for i in range(100)]
+@pytest.mark.parametrize("B", [33, 64, 65, 100, 700])
+def test_many_requests(B):
+    # More requests than one warp looks up at a time, or than the lookup table has
+    # blocks, some without rows.
+    rows = [i % 3 for i in range(B)]
+    lens = [(37 * i) % 211 for i in range(B)]
     t = H.make(rows, lens, 2, 1, 64, 64, seed=12)
     out, lse, bits = H.run(t, 0.125)
     assert bits == 0

@@ -204,9 +204,11 @@ def test_rows_max_only_changes_the_split(rows_max):
     H.check(t, s0, 0.1, out, state)
 
 
-def test_many_requests():
-    rows = [(7 * i) % 40 for i in range(70)]
-    t, s0 = H.make(rows, 2, 64, 64, seed=16)
+@pytest.mark.parametrize("rows", [[(7 * i) % 40 for i in range(70)], [i % 4 for i in range(900)],
+                                  [2, 2000, 0, 1] * 9, [3] * 700 + [1900] + [1] * 20])
+def test_many_requests(rows):
+    # More than 32, without and with a long one that is split; more than threads.
+    t, s0 = H.make(rows, 1, 64, 64, seed=16)
     out, state, bits = H.run(t, s0, 0.1)
     assert bits == 0
     H.check(t, s0, 0.1, out, state)
