@@ -13,14 +13,13 @@
 // The state stays in fp32 registers, transposed: a thread holds the D_k values of
 // one column of H (one dv).  Per chunk the tensor core adds
 //   dH^T = (V diag(lambda^(n-1-j)))^T K
-// whose A operand the same threads write into tensor memory: the decayed v, split
-// into 16-bit terms that add up to its fp32 value (bf16 three terms, fp16 two after
+// whose A operand is written into tensor memory: the decayed v, split into 16-bit terms that add up to its fp32 value (bf16 three terms, fp16 two after
 // a power-of-two scaling per column), so the state loses nothing to the operands' 8
 // or 11 bits.  Q H reads H rounded to the operands' type, as P V reads P (fp16: each
 // column of H and row of P scaled by a power of two into range).
 //
 // A CTA takes one head of one request, or of one segment of a long request, and
-// walks its chunks.  Four warpgroups, so that the chunks' steps overlap:
+// walks its chunks.  Five warpgroups, so that the chunks' steps overlap:
 //   warp 0        producer: Q, K, V tiles by TMA, two chunks in flight
 //   warp 1        issues S = Q K^T, O = Q H, O += P V
 //   warp 2        issues dH^T
@@ -28,17 +27,24 @@
 //                 32-column blocks 0 and 2, the other 1 and 3
 //   warp 3        stores the output tiles by TMA, through the shared memory of
 //                 their own Q tile, which no MMA reads by then
-//   warps 12-15   "decay": a thread writes one column of the decayed V, a quarter
-//                 chunk (32 tokens) at a time into two buffers in turn; in a request's
+//   warps 12-15   "decay": they write the decayed V, a quarter chunk (32 tokens) at a
+//                 time into two buffers in turn; in a request's
 //                 last chunk they first zero the K and V rows behind the last token
 //                 (another request's: weight zero times NaN is NaN)
 //   warps 16-19   "state": a thread holds one column of H
 // Registers are dealt to the groups with setmaxnreg (40 + 3 x 88 + 176 of 5 x 96).
 //
-// Bound: reading q, k, v and writing out once.  Where requests and heads do not
-// fill the GPU, long requests are split into segments: a first launch computes
-// each segment's own end state (K and V only), then every segment starts from
-// the decayed sum of those before it.
+// The groups' code together has to fit the instruction cache: unrolling the loops
+// over column blocks cost more than they saved (65536 tokens: 432 us unrolled, 357
+// rolled), as did out-of-place copies of the waits and of the MMA operands.
+//
+// Bound: reading q, k, v and writing out once.  With every SM at work a chunk of
+// 96 + 32 KB takes about 5600 cycles, 6.1 TB/s: 12 ragged prompts of 32 heads take
+// 110 us against 86 us for their bytes, the rest being the longest prompt's walk.
+// Where requests and heads do not fill the GPU, long requests are split into
+// segments: a first launch computes each segment's own end state (K and V only),
+// then every segment starts from the decayed sum of those before it (65536 tokens of
+// 16 heads: 262 us in nine segments, 1167 us in one walk; 159 us for its bytes).
 #include "linear.cuh"
 
 #include <cstring>
@@ -867,8 +873,9 @@ cudaError_t launch_width(ChunkParams& p, bool f16, bool split, cudaStream_t st) 
 // states are walked first (0.6 of that a chunk), then its segments side by side, each
 // after adding up the states before it (0.6 us for 64 KB); the second launch and
 // its start cost about 6 us.  A split is worth it where that is less and the segments
-// fill SMs that would idle.  Measured: 65536 tokens of 16 heads in nine segments
-// 303 us against 1700; 1000 tokens of 8 heads of width 64 in eight 21 us against 32.
+// fill SMs that would idle.  Measured: 65536 tokens of 16 heads 262 us in nine segments
+// against 1167 in one; 1000 tokens (with four shorter requests) of 8 heads of width
+// 64 18.5 us in eight against 31.8.
 int linear_seg_len(const dsa_linear_problem& p) {
   constexpr int kWhole = INT32_MAX - 127;
   const int64_t longest = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
