@@ -430,6 +430,8 @@ def _head_tensor(name, t):
     """(heads, width, token stride) of a [tokens, heads, width] tensor whose heads are packed."""
     if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
         raise ValueError(f"{name} must be [tokens, heads, width] with packed heads (a token stride is allowed)")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1] * t.shape[2]:   # (expanded: stride 0 means packed in the struct)
+        raise ValueError(f"{name}'s tokens overlap (stride {t.stride(0)} for {t.shape[1]} heads of {t.shape[2]})")
     return int(t.shape[1]), int(t.shape[2]), int(t.stride(0)) if t.shape[0] > 1 else 0
 
 

@@ -453,8 +453,8 @@ dsa_status dense_plan(const dsa_dense_problem* p, DensePlan* dp) {
     return fail(DSA_ERR_UNSUPPORTED, "(D_k, D_v)=(%d, %d) not in {(64,64), (128,128), (192,128)}", p->D_k, p->D_v);
   if (p->L_max < 0) return fail(DSA_ERR_INVALID_ARG, "L_max=%d < 0", p->L_max);
   if (p->rows_max < 0) return fail(DSA_ERR_INVALID_ARG, "rows_max=%d < 0", p->rows_max);
-  if (p->L_total < 0 || p->L_total >= (int64_t(1) << 31))
-    return fail(DSA_ERR_UNSUPPORTED, "L_total=%lld outside [0,2^31)", (long long)p->L_total);
+  if (p->L_total < 0 || p->L_total > (int64_t(1) << 31) - 256)   // (positions are rounded up to tiles in 32 bits)
+    return fail(DSA_ERR_UNSUPPORTED, "L_total=%lld outside [0,2^31-256]", (long long)p->L_total);
   const int64_t pack[3] = {(int64_t)p->H_q * p->D_k, (int64_t)p->H_kv * p->D_k, (int64_t)p->H_kv * p->D_v};
   const int64_t stride[3] = {p->q_stride, p->k_stride, p->v_stride};
   for (int i = 0; i < 3; ++i)

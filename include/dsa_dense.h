@@ -51,8 +51,8 @@ extern "C" {
  *   rows_max >= the most query rows of one request; 0 = not known (R is taken).
  *            It decides how the work is split, and bounds the launch: a batch
  *            with more rows in a request raises DSA_DEVICE_CAPACITY, and the
- *            rows past the launch are not written.
- *   L_total  offsets[B] (rows of k and v)                        L_total < 2^31
+ *            outputs of rows past the launch are then unspecified.
+ *   L_total  offsets[B] (rows of k and v)                        L_total <= 2^31 - 256
  *   q_stride, k_stride, v_stride  elements from one row (token) to the next; 0 =
  *            packed (H_q * D_k, H_kv * D_k, H_kv * D_v).  Multiples of 8, at least
  *            the packed width: q, k and v may be views of one fused projection.
@@ -81,7 +81,8 @@ typedef struct dsa_dense_problem {
 DSA_API size_t dsa_dense_workspace_size(const dsa_dense_problem* p);
 
 /*
- * Writes out [R, H_q, D_v] (16-byte aligned) and, if non-NULL, lse [R, H_q].
+ * Writes out [R, H_q, D_v] (16-byte aligned) and, if non-NULL, lse [R, H_q];
+ * neither may overlap an input.
  * ws: at least dsa_dense_workspace_size(p) bytes, 256-byte aligned; the call
  * clears its status word first (dsa_read_device_status reads it).  A kernel that
  * clears it, the attention's, and where the cache is split over the grid one that

@@ -35,6 +35,11 @@
  * to the operands' type for their matrix products (fp16: scaled into its range by
  * powers of two), sums are fp32, and the output is rounded once.  dsa_linear_step
  * computes in fp32 throughout.  Results do not depend on timing.
+ *
+ * A token's k may be anything for the tokens before it, but its v has to be finite:
+ * in the chunked form a NaN or infinity there reaches the outputs of its chunk's
+ * earlier tokens too (a weight of zero times NaN is NaN).  Rows of other requests, or
+ * of none, never reach a request, whatever they hold.
  */
 #ifndef DSA_LINEAR_H
 #define DSA_LINEAR_H
@@ -85,7 +90,8 @@ typedef struct dsa_linear_problem {
 DSA_API size_t dsa_linear_workspace_size(const dsa_linear_problem* p);
 
 /*
- * Prompts.  Writes out [R, H, D_v] (16-byte aligned) and, if non-NULL, state_out.
+ * Prompts.  Writes out [R, H, D_v] (16-byte aligned; it may not overlap an input)
+ * and, if non-NULL, state_out.
  * A request without tokens hands its state on.  Rows outside every request are
  * not written.  ws: at least dsa_linear_workspace_size(p) bytes, 256-byte
  * aligned; its status word is cleared first.  A kernel that clears it, and one, or

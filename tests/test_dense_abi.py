@@ -124,3 +124,32 @@ def test_headers_from_c(dsa, tmp_path):
                           "-o", exe, "-L", lib, "-ldsa", "-Wl,-rpath," + lib], capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
     assert subprocess.run([exe], timeout=120).returncode == 0
+
+
+def test_expanded_tokens_are_refused(dsa):
+    # A token stride of 0 (expand) would read as "packed" and run past the storage.
+    import torch
+    i = lambda *a: torch.tensor(a, dtype=torch.int32)
+    one = torch.zeros(1, 2, 128, dtype=torch.bfloat16)
+    ok = dict(q=one.expand(2, 2, 128).contiguous(), k=one.expand(30, 2, 128).contiguous(),
+              v=one.expand(30, 2, 128).contiguous(), offsets=i(0, 30), row_offsets=i(0, 2), row_len=i(29, 30),
+              softmax_scale=0.1)
+    dsa.DenseProblem.from_tensors(**ok)
+    wide = torch.zeros(30 * 256 + 256, dtype=torch.bfloat16)
+    for bad in (dict(k=one.expand(30, 2, 128)), dict(q=one.expand(2, 2, 128)), dict(v=one.expand(30, 2, 128)),
+                dict(k=wide.as_strided((30, 2, 128), (128, 128, 1)))):
+        with pytest.raises(ValueError, match="overlap"):
+            dsa.DenseProblem.from_tensors(**dict(ok, **bad))
+    ln = dict(q=ok["k"], k=ok["k"], v=ok["v"], log_decay=torch.zeros(2), row_offsets=i(0, 30), scale=0.1)
+    dsa.LinearProblem.from_tensors(**ln)
+    for name in "qkv":
+        with pytest.raises(ValueError, match="overlap"):
+            dsa.LinearProblem.from_tensors(**dict(ln, **{name: one.expand(30, 2, 128)}))
+
+
+def test_longest_cache(dsa):
+    # Positions are rounded up to whole tiles in 32 bits.
+    top = (1 << 31) - 256
+    assert dsa.dsa_dense_workspace_size(_prob(dsa, L_total=top)) > 0
+    assert _call(dsa, _prob(dsa, L_total=top + 1)) == 2
+    assert b"L_total" in dsa.lib().dsa_last_error_string()
