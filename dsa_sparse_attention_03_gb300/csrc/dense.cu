@@ -123,7 +123,7 @@ __host__ __device__ __forceinline__ uint32_t item_count(const DenseArgs& a) {   
 
 // Request b's rows, clamped to the call's.
 __device__ __forceinline__ void request_rows(const DenseArgs& a, int b, int& r0, int& n) {
-  const int x0 = a.B == 1 ? 0 : a.row_offsets[b], x1 = a.B == 1 ? a.R : a.row_offsets[b + 1];
+  const int x0 = a.row_offsets[b], x1 = a.row_offsets[b + 1];
   r0 = min(max(x0, 0), a.R);
   n = max(min(x1, a.R) - r0, 0);
 }
@@ -175,7 +175,7 @@ __device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it
       break;
     }
   }
-  const int y0 = a.B == 1 ? 0 : a.offsets[b], y1 = a.B == 1 ? a.L_total : a.offsets[b + 1];
+  const int y0 = a.offsets[b], y1 = a.offsets[b + 1];
   const int o0 = min(max(y0, 0), a.L_total);
   const int len = max(min(y1, a.L_total) - o0, 0);
   const int rows = n * a.G, t0 = tile * NW * kTile;
@@ -684,16 +684,20 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__
   if (a.tail_parts > 1) {
     splits = a.tail_parts;
     const uint32_t q = (uint32_t)(at / row_tile), id = a.full + q, ts = id / (uint32_t)a.H_kv;
-    if (id >= (uint32_t)a.tiles * a.H_kv) return;
-    const int64_t packed = (int64_t)(a.tiles - 1 - ts) * row_tile + (at - (int64_t)q * row_tile);
-    if (packed >= (int64_t)a.R * a.G) return;
-    rh = packed / a.G * a.H_q + (int64_t)(id - ts * a.H_kv) * a.G + packed % a.G;
+    int r0, n;
+    request_rows(a, 0, r0, n);
+    const int tiles = (n * a.G + row_tile - 1) / row_tile;   // (numbered from the last one, as the items are)
+    if (ts >= (uint32_t)tiles) return;
+    const int64_t packed = (int64_t)(tiles - 1 - ts) * row_tile + (at - (int64_t)q * row_tile);
+    if (packed >= (int64_t)n * a.G) return;
+    rh = (r0 + packed / a.G) * a.H_q + (int64_t)(id - ts * a.H_kv) * a.G + packed % a.G;
   } else if (rh >= (int64_t)a.R * a.H_q) {
     return;
   }
   const int row = (int)(rh / a.H_q);
+  const bool ours = row >= a.row_offsets[0] && row < a.row_offsets[a.B];
   pdl_wait();
-  if (a.B > 1 && (row < a.row_offsets[0] || row >= a.row_offsets[a.B])) return;
+  if (!ours) return;
   const float2* ml = a.ml + at * splits;
   float M = -INFINITY;
   for (int i = lane; i < splits; i += 32) {

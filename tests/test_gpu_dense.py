@@ -150,6 +150,25 @@ def test_rows_behind_the_last_request_stay(rows):
     assert (out[-5:] == 77.0).all() and (lse[-5:] == 77.0).all()
 
 
+@pytest.mark.parametrize("rows,L,hq,hkv,front", [
+    (1, 700, 4, 1, 0), (3, 5000, 4, 1, 0), (3, 700, 4, 1, 2), (200, 300, 4, 4, 0), (200, 300, 4, 4, 3),
+    (300, 700, 80, 80, 3),       # more items than SMs, the last ones in parts
+])
+def test_rows_around_a_single_request_stay(rows, L, hq, hkv, front):
+    # One request takes part of the call's rows, as the padded batch of a captured graph has it.
+    t = H.make([rows], [L], hq, hkv, 64, 64, seed=12, extra_rows=8)
+    t["row_len"][rows:] = L            # a length that would be computed
+    if front:
+        for x in ("q", "row_len"):
+            t[x] = t[x].roll(front, 0)
+        t["row_offsets"] += front
+    out, lse, bits = H.run(t, 0.125)
+    assert bits == 0
+    H.check(t, 0.125, out, lse, rows=slice(front, front + rows))
+    for x in (out, lse):
+        assert (x[:front] == 77.0).all() and (x[front + rows:] == 77.0).all()
+
+
 def test_length_beyond_the_request_is_clamped_and_flagged():
     import dsa_sparse_attention_03_gb300 as dsa
     t = H.make([1, 2], [100, 200], 2, 1, 128, 128, seed=11)
