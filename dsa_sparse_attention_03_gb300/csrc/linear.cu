@@ -13,8 +13,9 @@
 // The state stays in fp32 registers, transposed: a thread holds the D_k values of
 // one column of H (one dv).  Per chunk the tensor core adds
 //   dH^T = (V diag(lambda^(n-1-j)))^T K
-// whose A operand is written into tensor memory: the decayed v, split into 16-bit terms that add up to its fp32 value (bf16 three terms, fp16 two after
-// a power-of-two scaling per column), so the state loses nothing to the operands' 8
+// whose A operand is written into tensor memory: the decayed v, split into 16-bit
+// terms that add up to its fp32 value (bf16 three terms, fp16 two after a
+// power-of-two scaling per column), so the state loses nothing to the operands' 8
 // or 11 bits.  Q H reads H rounded to the operands' type, as P V reads P (fp16: each
 // column of H and row of P scaled by a power of two into range).
 //
@@ -28,9 +29,9 @@
 //   warp 3        stores the output tiles by TMA, through the shared memory of
 //                 their own Q tile, which no MMA reads by then
 //   warps 12-15   "decay": they write the decayed V, a quarter chunk (32 tokens) at a
-//                 time into two buffers in turn; in a request's
-//                 last chunk they first zero the K and V rows behind the last token
-//                 (another request's: weight zero times NaN is NaN)
+//                 time into two buffers in turn; in a request's last chunk they
+//                 first zero the K and V rows behind the last token (another
+//                 request's: weight zero times NaN is NaN)
 //   warps 16-19   "state": a thread holds one column of H
 // Registers are dealt to the groups with setmaxnreg (40 + 3 x 88 + 176 of 5 x 96).
 //
