@@ -128,10 +128,33 @@ __device__ __forceinline__ void request_rows(const DenseArgs& a, int b, int& r0,
   n = max(min(x1, a.R) - r0, 0);
 }
 
+// Request b's positions, clamped to the call's.
+__device__ __forceinline__ void request_cache(const DenseArgs& a, int b, int& o0, int& len) {
+  const int y0 = a.offsets[b], y1 = a.offsets[b + 1];
+  o0 = min(max(y0, 0), a.L_total);
+  len = max(min(y1, a.L_total) - o0, 0);
+}
+
+// Up to kBlocks requests, held by the scheduler's lanes (lane, lane + 32): between
+// items, dependent loads are what the next one's first MMA waits for.
+struct Requests {
+  int r0[2], n[2], o0[2], len[2];
+  __device__ __forceinline__ void load(const DenseArgs& a, int lane) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      r0[x] = n[x] = o0[x] = len[x] = 0;
+      const int b = lane + 32 * x;
+      if (a.B > kBlocks || b >= a.B) continue;
+      request_rows(a, b, r0[x], n[x]);
+      request_cache(a, b, o0[x], len[x]);
+    }
+  }
+};
+
 // Item `idx` (one warp).  Row tiles are numbered over the requests; the last ones
 // (a causal prompt's longest) come first, K/V heads and parts vary fastest.
 template <int NW>
-__device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it, int lane) {
+__device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it, int lane, const Requests& rq) {
   int parts = a.splits, split = 0, slot = -1;
   if (a.tail_parts > 1 && idx >= (uint32_t)a.full) {
     const uint32_t j = idx - a.full, q = j / (uint32_t)a.tail_parts;
@@ -152,43 +175,55 @@ __device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it
   const int per = (a.B + kBlocks - 1) / kBlocks;
   const int blk = __popc(__ballot_sync(0xffffffffu, sh->first[lane + 1] <= want)) +
                   __popc(__ballot_sync(0xffffffffu, sh->first[lane + 33] <= want));
-  int run = sh->first[blk], b = 0, r0 = 0, n = 0, tile = 0;
-  for (int base = blk * per; base < (blk + 1) * per; base += 32) {
-    int x0 = 0, xn = 0;
-    if (base + lane < (blk + 1) * per && base + lane < a.B) request_rows(a, base + lane, x0, xn);
-    const int v = (xn * a.G + NW * kTile - 1) / (NW * kTile);
-    int incl = v;
+  int run = sh->first[blk], r0 = 0, n = 0, tile = 0, o0 = 0, len = 0;
+  if (per == 1) {
+    tile = want - run;
+    r0 = __shfl_sync(0xffffffffu, blk < 32 ? rq.r0[0] : rq.r0[1], blk & 31);
+    n = __shfl_sync(0xffffffffu, blk < 32 ? rq.n[0] : rq.n[1], blk & 31);
+    o0 = __shfl_sync(0xffffffffu, blk < 32 ? rq.o0[0] : rq.o0[1], blk & 31);
+    len = __shfl_sync(0xffffffffu, blk < 32 ? rq.len[0] : rq.len[1], blk & 31);
+  } else {
+    int b = 0;
+    for (int base = blk * per; base < (blk + 1) * per; base += 32) {
+      int x0 = 0, xn = 0;
+      if (base + lane < (blk + 1) * per && base + lane < a.B) request_rows(a, base + lane, x0, xn);
+      const int v = (xn * a.G + NW * kTile - 1) / (NW * kTile);
+      int incl = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const int at = run + incl - v;
+      const uint32_t hit = __ballot_sync(0xffffffffu, want >= at && want < at + v);
+      run += __shfl_sync(0xffffffffu, incl, 31);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        b = base + src;
+        r0 = __shfl_sync(0xffffffffu, x0, src);
+        n = __shfl_sync(0xffffffffu, xn, src);
+        tile = want - __shfl_sync(0xffffffffu, at, src);
+        break;
+      }
     }
-    const int at = run + incl - v;
-    const uint32_t hit = __ballot_sync(0xffffffffu, want >= at && want < at + v);
-    run += __shfl_sync(0xffffffffu, incl, 31);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      b = base + src;
-      r0 = __shfl_sync(0xffffffffu, x0, src);
-      n = __shfl_sync(0xffffffffu, xn, src);
-      tile = want - __shfl_sync(0xffffffffu, at, src);
-      break;
-    }
+    request_cache(a, b, o0, len);
   }
-  const int y0 = a.offsets[b], y1 = a.offsets[b + 1];
-  const int o0 = min(max(y0, 0), a.L_total);
-  const int len = max(min(y1, a.L_total) - o0, 0);
   const int rows = n * a.G, t0 = tile * NW * kTile;
-  // The farthest position each row tile sees.
-  int end[2] = {0, 0};
+  // The farthest position each row tile sees: at most 128 lengths each, loaded together.
+  int end[2] = {0, 0}, l[NW][kTile / 32];
   bool bad = false;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const int x0 = t0 + w * kTile, x1 = min(x0 + kTile, rows);
-    for (int r = x0 / a.G + lane; r * a.G < x1; r += 32) {
-      const int l = a.row_len[r0 + r];
-      bad |= l < 0 || l > len;
-      end[w] = max(end[w], min(max(l, 0), len));
+    const int x0 = t0 + w * kTile, x1 = min(x0 + kTile, rows), first = x0 / a.G + lane;
+#pragma unroll
+    for (int u = 0; u < kTile / 32; ++u) l[w][u] = (first + 32 * u) * a.G < x1 ? a.row_len[r0 + first + 32 * u] : 0;
+  }
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+#pragma unroll
+    for (int u = 0; u < kTile / 32; ++u) {
+      bad |= l[w][u] < 0 || l[w][u] > len;
+      end[w] = max(end[w], min(max(l[w][u], 0), len));
     }
     end[w] = __reduce_max_sync(0xffffffffu, end[w]);
   }
@@ -294,6 +329,8 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
       sh->first[kBlocks] = run;
     }
   }
+  Requests rq;
+  if (warp == 3) rq.load(a, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -329,7 +366,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
       if (k >= 2 && !wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc)) break;
       Item* it = &sh->item[k & 1];
       if (idx < items)
-        find_item<NW>(a, idx, sh, it, lane);
+        find_item<NW>(a, idx, sh, it, lane, rq);
       else if (lane == 0)
         it->rows = 0;
       __syncwarp();
