@@ -248,6 +248,26 @@ __device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it
   }
 }
 
+// Lane i of four adjacent ones holds four 16-byte pieces of row i; afterwards piece i of
+// the four rows.
+__device__ __forceinline__ void exchange4(uint32_t* p, int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & bit) continue;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t &lo = p[4 * k + y], &hi = p[4 * (k | bit) + y];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+        lo = up ? got : lo;
+        hi = up ? hi : got;
+      }
+    }
+  }
+}
+
 template <int DK, int DV, int NW, bool F16>
 __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     dense_attn_kernel(const __grid_constant__ DenseArgs a) {
@@ -671,6 +691,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
         // Written as it is into its part, or divided by l: a row of NaN (l is NaN)
         // keeps it, a row that sees nothing gets zeros.
         const float inv = some ? 1.f / l : 0.f;
+        const int at_row = valid ? (int)rh : -1;   // (below 2^23: 65535 rows of 128 heads)
         if (valid && parts > 1) a.ml[at] = make_float2(m * a.c, some ? l : 0.f);
         if (valid && parts == 1 && a.lse) a.lse[rh] = some ? m * a.scale + logf(l) : -INFINITY;
         if (parts == 1 || __any_sync(0xffffffffu, some)) {
@@ -685,13 +706,19 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
 #pragma unroll
                 for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
             } else {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + rh * DV + x);
 #pragma unroll
               for (int y = 0; y < 16; ++y)
                 o[y] = some ? pack16<F16>(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv) : 0u;
-              if (valid)
+              // Four lanes exchange their rows' 16-byte pieces, so that a store writes 64
+              // bytes of a row: 8 rows to an instruction rather than 32.
+              exchange4(o, lane);
+              uint16_t* dst = a.out + x + (lane & 3) * 8;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+              for (int y = 0; y < 4; ++y) {
+                const int to = __shfl_sync(0xffffffffu, at_row, (lane & 28) + y);
+                if (to >= 0)
+                  *reinterpret_cast<uint4*>(dst + (int64_t)to * DV) = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+              }
             }
           }
         }
