@@ -414,11 +414,14 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
           ++q;
         };
         load_q(0);
-        if (NW == 2) load_q(1);
         if (it.steps == 0) mbar_arrive(bar(sh->inext));
         for (int j = 0; j < it.steps && ok; ++j) {
           if (j == max(it.steps - kEarly, 0)) mbar_arrive(bar(sh->inext));
           for (int c = 0; c < KC + VC; ++c, ++n) {
+            if (NW == 2 && j == 0 && c == KC) {   // (row tile 0 starts with what is asked for by now)
+              load_q(1);
+              if (!ok) break;
+            }
             const int s = n % NS;
             if (n >= NS && !(ok = wait_bar(bar(sh->empty[s]), (n / NS - 1) & 1, wc))) break;
             const uint32_t b = bar(sh->full[s]), dst = smem_u32(ring + s * kChunkBytes);
