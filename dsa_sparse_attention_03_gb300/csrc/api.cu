@@ -502,7 +502,8 @@ static dsa_status run_dense(const dsa_dense_problem* p, uint16_t* out, float* ls
     return fail(DSA_ERR_INVALID_ARG, "lse/offsets/row_offsets/row_len must be 4-byte aligned");
   char* w = static_cast<char*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_clear_status(ws, st);
+  cudaError_t e = cudaSuccess;
+  if (p->R == 0 || dense_cleared(*p, dp.shape)) e = launch_clear_status(ws, st);
   if (e != cudaSuccess) return cuda_fail(e, "clear status");
   if (p->R == 0) return DSA_OK;
   e = launch_dense(*p, dp.shape, out, lse, reinterpret_cast<float*>(w + dp.off_part),

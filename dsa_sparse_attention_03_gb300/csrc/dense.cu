@@ -72,6 +72,7 @@ struct DenseArgs {
   float2* ml;       // the same without D_v: (c m, l)
   uint32_t* status;
   uint32_t* next;   // items taken beyond the grid (zeroed with the status)
+  uint32_t* bits;   // status bits of each CTA, joined with the parts; or null: the status is cleared before, and raised
   int64_t q_stride;
   uint64_t wait_ns;
   int R, B, H_q, H_kv, G, L_total, splits, tiles;
@@ -100,6 +101,7 @@ struct __align__(16) Shared {
   uint64_t ifull[2], ifree[2], inext;   // items
   uint32_t tmem;
   int abort;
+  uint32_t bits;                  // status bits, where the join collects them
   volatile int steps[2];          // K/V tiles that each row tile's issuer is through with
   Item item[2];
   int first[kBlocks + 1];         // row tiles before each block of requests
@@ -154,7 +156,8 @@ struct Requests {
 // Item `idx` (one warp).  Row tiles are numbered over the requests; the last ones
 // (a causal prompt's longest) come first, K/V heads and parts vary fastest.
 template <int NW>
-__device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it, int lane, const Requests& rq) {
+__device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it, int lane, const Requests& rq,
+                          uint32_t* status) {
   int parts = a.splits, split = 0, slot = -1;
   if (a.tail_parts > 1 && idx >= (uint32_t)a.full) {
     const uint32_t j = idx - a.full, q = j / (uint32_t)a.tail_parts;
@@ -227,7 +230,7 @@ __device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it
     }
     end[w] = __reduce_max_sync(0xffffffffu, end[w]);
   }
-  if (bad && split == 0 && h == 0) raise_status(a.status, DSA_DEVICE_BAD_INDEX);
+  if (bad && split == 0 && h == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
   if (lane == 0) {
     const int kv_end = max(end[0], end[1]);
     const int nt = (kv_end + kTile - 1) / kTile;
@@ -284,7 +287,12 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
   if (smem_u32(smem) & 1023) {   // (the swizzle's atoms)
-    if (tid == 0) raise_status(a.status, DSA_DEVICE_CAPACITY);
+    if (tid == 0) {
+      if (a.bits)
+        a.bits[blockIdx.x] = DSA_DEVICE_CAPACITY;
+      else
+        raise_status(a.status, DSA_DEVICE_CAPACITY);
+    }
     return;
   }
   if (tid == 0) {
@@ -306,6 +314,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     }
     mbar_init(bar(sh->inext), 1);
     sh->abort = 0;
+    sh->bits = 0;
     sh->steps[0] = sh->steps[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -339,15 +348,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
       sh->first[blk] = run + incl - v;
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) {
-      // (the launch was sized by the declared rows: later tiles come first in the
-      // numbering, so those past it are the first requests' and stay unwritten)
-      if (run > a.tiles) {
-        pdl_wait();
-        raise_status(a.status, DSA_DEVICE_CAPACITY);
-      }
-      sh->first[kBlocks] = run;
-    }
+    if (lane == 0) sh->first[kBlocks] = run;
   }
   Requests rq;
   if (warp == 3) rq.load(a, lane);
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0);
-  const WaitCtx wc(&sh->abort, a.status, a.wait_ns);
+  uint32_t* const status = a.bits ? &sh->bits : a.status;
+  const WaitCtx wc(&sh->abort, status, a.wait_ns);
   // Item k of this CTA; whoever has read what it needs gives the slot back.
   auto item_wait = [&](int k) { return wait_bar_warp(bar(sh->ifull[k & 1]), (k >> 1) & 1, wc); };
   auto item_done = [&](int k) {
@@ -368,6 +370,9 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
    if (warp == 3) {
     // ------------------------------------------------------------ scheduler
     pdl_wait();              // (the status block and the counter are cleared)
+    // The launch was sized by the declared rows: later tiles come first in the
+    // numbering, so those past it are the first requests' and are not computed.
+    if (lane == 0 && sh->first[kBlocks] > a.tiles) raise_status(status, DSA_DEVICE_CAPACITY);
     WaitCtx item_wc = wc;   // an item may take long: a thousand times the limit, or until another role gives up
     item_wc.tries *= 1000;
     uint32_t idx;
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
       if (k >= 2 && !wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc)) break;
       Item* it = &sh->item[k & 1];
       if (idx < items)
-        find_item<NW>(a, idx, sh, it, lane, rq);
+        find_item<NW>(a, idx, sh, it, lane, rq, status);
       else if (lane == 0)
         it->rows = 0;
       __syncwarp();
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
         if (!t0) t0 = gtimer();
         if (*wc.abort_flag) return false;
         if (gtimer() - t0 > a.wait_ns) {
-          raise_status(a.status, DSA_DEVICE_TIMEOUT);
+          raise_status(status, DSA_DEVICE_TIMEOUT);
           *wc.abort_flag = 1;
           return false;
         }
@@ -738,12 +743,13 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kCols);
+  if (tid == 0 && a.bits) a.bits[blockIdx.x] = sh->bits;
 }
 
 // Joins the parts of each (row, head): one warp each.  Split calls have parts of
 // every (row, head); the tail of others of its own rows (one request).
 template <int DV, bool F16>
-__global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__ DenseArgs a, int row_tile) {
+__global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__ DenseArgs a, int row_tile, int ctas) {
   const int lane = threadIdx.x & 31;
   const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   int splits = a.splits;
@@ -764,6 +770,12 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__
   const int row = (int)(rh / a.H_q);
   const bool ours = row >= a.row_offsets[0] && row < a.row_offsets[a.B];
   pdl_wait();
+  if (a.bits && at == 0) {
+    uint32_t bits = 0;
+    for (int i = lane; i < ctas; i += 32) bits |= a.bits[i];
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0) *a.status = bits;
+  }
   if (!ours) return;
   const float2* ml = a.ml + at * splits;
   float M = -INFINITY;
@@ -801,15 +813,20 @@ cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
   auto kernel = dense_attn_kernel<DK, DV, NW, F16>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t items = item_count(a), slots = NW == 1 ? 304 : 152;
+  const int64_t items = item_count(a), slots = dense_slots(NW);
   const int64_t grid = items < slots ? items : slots;
-  e = launch_pdl(kernel, dim3((unsigned)grid), dim3(128 + 128 * NW), smem, st, a);
+  if (a.bits) {   // (nothing of this call comes before it, so it waits for all that the stream holds)
+    kernel<<<dim3((unsigned)grid), dim3(128 + 128 * NW), smem, st>>>(a);
+    e = cudaGetLastError();
+  } else {
+    e = launch_pdl(kernel, dim3((unsigned)grid), dim3(128 + 128 * NW), smem, st, a);
+  }
   if (e != cudaSuccess) return e;
   int64_t rows = 0;
   if (a.splits > 1) rows = (int64_t)a.R * a.H_q;
   if (a.tail_parts > 1) rows = (int64_t)(a.tiles * a.H_kv - a.full) * NW * kTile;
   if (rows == 0) return cudaSuccess;
-  return launch_pdl(dense_join_kernel<DV, F16>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, a, NW * kTile);
+  return launch_pdl(dense_join_kernel<DV, F16>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, a, NW * kTile, (int)grid);
 }
 
 template <int DK, int DV>
@@ -834,7 +851,7 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
   // 288 us with two, 268 with four, 258 with eight, 255 with sixteen); one request,
   // whose items are alike: one each.  Prompts: two where the row tiles alone leave
   // SMs idle.  No part has less than two K/V tiles.
-  const int64_t items = tiles * p.H_kv, slots = s.nw == 1 ? 304 : 152;
+  const int64_t items = tiles * p.H_kv, slots = dense_slots(s.nw);
   const int64_t kvt = (p.L_max + kTile - 1) / kTile;
   const int64_t each = p.B == 1 ? 1 : (s.nw == 1 ? 8 : 2);
   int64_t splits = 1;
@@ -865,6 +882,7 @@ cudaError_t launch_dense(const dsa_dense_problem& p, const DenseShape& s, uint16
   a.out = out; a.lse = lse; a.part = part; a.ml = reinterpret_cast<float2*>(ml);
   a.status = status;
   a.next = status + kBarrierWord;
+  a.bits = dense_cleared(p, s) ? nullptr : status + kDenseBits;
   a.q_stride = p.q_stride ? p.q_stride : (int64_t)p.H_q * p.D_k;
   a.wait_ns = hooks ? hooks->wait_ns : kDefaultWaitNs;
   a.test_no_load = hooks ? hooks->tile_no_load : 0;

@@ -20,6 +20,16 @@ DenseShape dense_shape(const dsa_dense_problem& p);
 // counter, 19 with neither), so the parts start further on and a call whose items
 // all have a CTA leaves the counter alone.
 constexpr size_t kDensePartsOffset = 4096;
+// CTAs that the GPU holds at once.
+constexpr int dense_slots(int nw) { return nw == 1 ? 304 : 152; }
+// Whether the status block is cleared before the attention kernel.  Not where the cache
+// is split and every item has a CTA: the CTAs leave their bits in words from here on
+// and the join writes the status (one token 16.4 us with the clearing kernel, TIME without).
+constexpr int kDenseBits = 64;
+static_assert((kDenseBits + dense_slots(1)) * 4 <= kDensePartsOffset, "status words of the CTAs");
+inline bool dense_cleared(const dsa_dense_problem& p, const DenseShape& s) {
+  return s.splits == 1 || (int64_t)s.tiles * s.splits * p.H_kv > dense_slots(s.nw);
+}
 // Parts that the launch leaves for its join: O [parts, D_v] in `part`, (m, l) in `ml`.
 inline size_t dense_parts(const dsa_dense_problem& p, const DenseShape& s) {
   if (s.splits > 1) return (size_t)p.R * p.H_q * s.splits;
