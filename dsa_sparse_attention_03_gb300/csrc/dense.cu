@@ -19,7 +19,8 @@
 // persistent (one per SM with NW = 2, two with NW = 1) and take items from a
 // counter, so that an item's loads and first MMAs run under the last one's end:
 //   warp 0      producer: Q, and K and V tiles through one ring of 16 KB chunks of
-//               64 columns, in the order the MMAs use them, by TMA
+//               64 columns, in the order the MMAs use them, by TMA (the second row
+//               tile's Q behind the first K tile: the first one starts meanwhile)
 //   warps 1..   one per row tile issues its MMAs: S = Q K^T (both operands in shared
 //               memory) and O += P V (P in tensor memory, over the S it came from, in
 //               two halves, so that the product starts while the second is computed).
@@ -33,11 +34,14 @@
 //
 // Bounds.  Prompts: the tensor core's rate, 2 (D_k + D_v) flops per visible
 // pair and head; measured 1.58 PFLOP/s for 16384 tokens of 16 heads over 2
-// (697 us, 83% of the cuBLAS rate), where a tile's softmax and the hand-overs
-// between it and the MMAs are what the other row tile does not cover.  Width 192
-// fills shared memory with Q, so that its ring holds only 1.6 tiles: 1.0 PFLOP/s on
-// ragged prompts of up to 2048 tokens.  Single tokens: reading K and V once; 6.1 TB/s
-// for 32 requests of up to 32768 positions (259 us, 90% of the copy rate).
+// (694 us, 84% of the cuBLAS burst rate and 93% of the sustained one), where a tile's
+// softmax and the hand-overs between it and the MMAs are what the other row tile does
+// not cover.  Short prompts: an item's start and end cost about 4 us of loads, fill and
+// epilogue, so ragged prompts of up to 2048 tokens and width 192, whose Q leaves
+// the ring only 1.6 tiles, reach 1.06 PFLOP/s (234 us).  Two threads to a row of S,
+// with its maximum exchanged through shared memory, halve the softmax's work per
+// thread but took longer (837 us for the 16384 tokens).  Single tokens: reading K and V
+// once; 6.1 TB/s for 32 requests of up to 32768 positions (256 us, 91% of the copy rate).
 //
 // Split cache.  Where the row tiles do not fill the grid, each is computed by
 // several CTAs over parts of its positions; they leave (m, l, O) in the
@@ -92,7 +96,6 @@ struct Item {
   int kv_end;            // positions past it are seen by no row of the item
 };
 
-constexpr int kEarly = 4;     // K/V tiles before an item's end at which the next one is taken
 constexpr int kBlocks = 64;   // request blocks of the lookup table
 
 struct __align__(16) Shared {
@@ -401,6 +404,10 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     }
    } else if (warp == 0) {
     // ------------------------------------------------------------ producer
+    // K/V tiles before an item's end at which the next one is taken: looking it up takes
+    // 2000 to 4000 cycles, and a longer lead takes it from a CTA that would be free (32
+    // single tokens 254 us with two, 257 with four, 258 with six; prompts alike).
+    constexpr int early = NW == 1 ? 2 : 4;
     int n = 0, nq[2] = {0, 0};   // chunks and Q tiles asked for
     bool ok = true;
     for (int k = 0; ok && item_wait(k); ++k) {
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
         load_q(0);
         if (it.steps == 0) mbar_arrive(bar(sh->inext));
         for (int j = 0; j < it.steps && ok; ++j) {
-          if (j == max(it.steps - kEarly, 0)) mbar_arrive(bar(sh->inext));
+          if (j == max(it.steps - early, 0)) mbar_arrive(bar(sh->inext));
           for (int c = 0; c < KC + VC; ++c, ++n) {
             if (NW == 2 && j == 0 && c == KC) {   // (row tile 0 starts with what is asked for by now)
               load_q(1);
