@@ -57,14 +57,14 @@ cudaError_t launch_check_bounds(const int8_t* k, size_t k_bytes, const int8_t* q
 
 namespace {
 __global__ void clear_status_kernel(uint32_t* status) {
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();   // (behind the wait: the next kernel reads the call's inputs at once)
   status[threadIdx.x] = 0;
 }
 }  // namespace
 
 cudaError_t launch_clear_status(void* ws, cudaStream_t st) {
-  clear_status_kernel<<<1, 64, 0, st>>>(static_cast<uint32_t*>(ws));
-  return cudaGetLastError();
+  return launch_pdl(clear_status_kernel, dim3(1), dim3(64), 0, st, static_cast<uint32_t*>(ws));
 }
 
 }  // namespace dsa

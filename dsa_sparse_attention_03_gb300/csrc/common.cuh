@@ -264,9 +264,9 @@ struct FrontArgs {
 cudaError_t launch_front_end(FrontArgs a, cudaStream_t st);
 
 // Clears the 256-byte status block as a kernel (check.cu) after which a kernel
-// launched with launch_pdl may start at once: it has only to wait (pdl_wait)
-// before it touches the block.  A memset in its place costs its own time and a
-// gap before the kernel.
+// launched with launch_pdl may start at once and read the call's inputs: it has
+// only to wait (pdl_wait) before it touches the block.  A memset in its place costs
+// its own time and a gap before the kernel.
 cudaError_t launch_clear_status(void* ws, cudaStream_t st);
 
 // Declared-bound check (check.cu): int8 bytes of k and q (16-byte multiples)

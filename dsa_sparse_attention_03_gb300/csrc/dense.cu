@@ -321,8 +321,9 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
     sh->steps[0] = sh->steps[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_trigger();   // (the join, if any, may take its place; it waits for this grid's end)
   if (warp == 1) tmem_alloc(smem_u32(&sh->tmem), kCols);
+  if (a.bits) pdl_wait();   // (the call's first kernel: its inputs may only just be written)
+  pdl_trigger();   // (the join, if any, may take its place; it waits for this grid's end)
   // Row tiles before each block of requests: one request to a block, or counted by
   // all threads.
   auto row_tiles = [&](int b) {
@@ -761,22 +762,21 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__
   const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   int splits = a.splits;
   int64_t rh = at;
+  bool ours = true;
   if (a.tail_parts > 1) {
     splits = a.tail_parts;
     const uint32_t q = (uint32_t)(at / row_tile), id = a.full + q, ts = id / (uint32_t)a.H_kv;
     int r0, n;
     request_rows(a, 0, r0, n);
     const int tiles = (n * a.G + row_tile - 1) / row_tile;   // (numbered from the last one, as the items are)
-    if (ts >= (uint32_t)tiles) return;
-    const int64_t packed = (int64_t)(tiles - 1 - ts) * row_tile + (at - (int64_t)q * row_tile);
-    if (packed >= (int64_t)n * a.G) return;
+    const int64_t packed = ((int64_t)tiles - 1 - ts) * row_tile + (at - (int64_t)q * row_tile);
+    ours = id < (uint32_t)a.tiles * a.H_kv && packed >= 0 && packed < (int64_t)n * a.G;
     rh = (r0 + packed / a.G) * a.H_q + (int64_t)(id - ts * a.H_kv) * a.G + packed % a.G;
-  } else if (rh >= (int64_t)a.R * a.H_q) {
-    return;
+  } else {
+    const int64_t row = at / a.H_q;
+    ours = row < a.R && row >= a.row_offsets[0] && row < a.row_offsets[a.B];
   }
-  const int row = (int)(rh / a.H_q);
-  const bool ours = row >= a.row_offsets[0] && row < a.row_offsets[a.B];
-  pdl_wait();
+  pdl_wait();   // (by every thread: whoever waits for this grid's end waits for the parts' too)
   if (a.bits && at == 0) {
     uint32_t bits = 0;
     for (int i = lane; i < ctas; i += 32) bits |= a.bits[i];
@@ -822,12 +822,7 @@ cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = item_count(a), slots = dense_slots(NW);
   const int64_t grid = items < slots ? items : slots;
-  if (a.bits) {   // (nothing of this call comes before it, so it waits for all that the stream holds)
-    kernel<<<dim3((unsigned)grid), dim3(128 + 128 * NW), smem, st>>>(a);
-    e = cudaGetLastError();
-  } else {
-    e = launch_pdl(kernel, dim3((unsigned)grid), dim3(128 + 128 * NW), smem, st, a);
-  }
+  e = launch_pdl(kernel, dim3((unsigned)grid), dim3(128 + 128 * NW), smem, st, a);
   if (e != cudaSuccess) return e;
   int64_t rows = 0;
   if (a.splits > 1) rows = (int64_t)a.R * a.H_q;

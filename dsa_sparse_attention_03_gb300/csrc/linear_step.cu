@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
   __shared__ int twice;
   const int h = blockIdx.x % a.H, b = blockIdx.x / a.H;
   const int tid = threadIdx.x, c = tid % C4, r = tid / C4;
+  pdl_wait();
   if (blockIdx.x == 0 && tid == 0 && a.status_known >= 0) *a.status = (uint32_t)a.status_known;
   const int at = state_place(a, b, &twice, h == 0);
   if (at < 0) return;
@@ -82,11 +83,8 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
 template <int DK, int DV>
 cudaError_t launch_one(const LinearArgs& a, bool f16, cudaStream_t st) {
   const unsigned grid = (unsigned)a.B * (unsigned)a.H;
-  if (f16)
-    linear_step_kernel<DK, DV, true><<<grid, kThreads, 0, st>>>(a);
-  else
-    linear_step_kernel<DK, DV, false><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return f16 ? launch_pdl(linear_step_kernel<DK, DV, true>, dim3(grid), dim3(kThreads), 0, st, a)
+             : launch_pdl(linear_step_kernel<DK, DV, false>, dim3(grid), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace

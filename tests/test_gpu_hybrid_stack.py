@@ -117,3 +117,70 @@ def test_dense_equals_sparse_over_every_position(R):
     out, _, bound, _ = DH.reference(t, 1 / math.sqrt(Dk))
     assert bool(((a.view(torch.bfloat16).cpu().double() - b.cpu().double()).abs() <= 2 * bound).all())
     assert bool(((la - lb).abs() <= 2e-3).all())
+
+
+@pytest.mark.parametrize("case", ["tokens", "rows", "prompt", "short rows", "short prompts", "split prompt", "step"])
+def test_inputs_written_just_before(case):
+    # Each call's first kernel may be resident before what precedes it in the stream has
+    # ended: a large copy and this library's own kernels right before, their outputs
+    # and the offsets among the inputs, and the last call's workspace and output reused.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    g = torch.Generator().manual_seed(4)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    big = torch.empty(1 << 27, dtype=torch.uint8, device="cuda")      # 40 us of writing
+    rnd = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()
+    if case in ("tokens", "rows", "prompt", "short rows"):
+        R, L = {"tokens": (1, 3000), "rows": (400, 700), "prompt": (900, 900), "short rows": (130, 200)}[case]
+        src = [[rnd(R, 8, 64), rnd(L, 2, 64), rnd(L, 2, 64),
+                i32(*[max(0, L - R + i + 1 - 7 * v) for i in range(R)]), i32(0, L - v), i32(0, R)] for v in range(3)]
+        use = [x.clone() for x in src[0]]
+        q, k, v, rl, off, ro = use
+        prob = dsa.DenseProblem.from_tensors(q=q, k=k, v=v, offsets=off, row_offsets=ro, row_len=rl, L_total=L,
+                                             L_max=L, softmax_scale=0.125)
+        out, ws = torch.empty(R, 8, 64, dtype=torch.bfloat16, device="cuda"), dsa.alloc_dense_workspace(prob)
+        call = lambda: dsa.dsa_dense_attn(prob, out, None, ws)
+        outs = [out]
+    else:
+        rows = {"short prompts": [150, 20, 300], "split prompt": [6000], "step": [1] * 5}[case]
+        R, H_ = sum(rows), 4
+        pre = [0] + list(np.cumsum(rows))
+        src = [[rnd(R, H_, 64), rnd(R, H_, 64), rnd(R, H_, 64), -torch.rand(H_, generator=g).cuda() * 0.01,
+                i32(*[max(0, x - v) for x in pre]), torch.randn(len(rows), H_, 64, 64, generator=g).cuda()] for v in range(3)]
+        use = [x.clone() for x in src[0]]
+        q, k, v, ld, ro, s0 = use
+        prob = dsa.LinearProblem.from_tensors(q=q, k=k, v=v, log_decay=ld, row_offsets=None if case == "step" else ro,
+                                              scale=0.125, rows_max=max(rows))
+        out, s1 = torch.empty(R, H_, 64, dtype=torch.bfloat16, device="cuda"), torch.empty_like(s0)
+        ws = dsa.alloc_linear_workspace(prob)
+        fn = dsa.dsa_linear_step if case == "step" else dsa.dsa_linear_attn
+        call = lambda: fn(prob, s0, s1, out, ws)
+        outs = [out, s1]
+    want = []
+    for v in range(3):                                   # one at a time
+        for a, b in zip(use, src[v]):
+            a.copy_(b)
+        for o in outs:
+            o.fill_(0)
+        torch.cuda.synchronize()
+        call()
+        torch.cuda.synchronize()
+        assert dsa.dsa_read_device_status(ws) == 0
+        want.append([o.clone() for o in outs])
+    assert not want[0][0].equal(want[1][0])
+    got = []
+    for rep in range(6):                                 # back to back
+        big.fill_(rep)
+        for a, b in zip(use, src[rep % 3]):
+            a.copy_(b)
+        for o in outs:
+            o.fill_(0)
+        call()
+        got.append([o.clone() for o in outs])
+        call()                                           # once more into the same output: what a reader finds is whole
+        got.append([o.clone() for o in outs])
+    torch.cuda.synchronize()
+    for n, x in enumerate(got):
+        for a, b in zip(x, want[n // 2 % 3]):
+            assert a.equal(b), (n, case)
+    assert dsa.dsa_read_device_status(ws) == 0
