@@ -41,7 +41,7 @@
 // the ring only 1.6 tiles, reach 1.06 PFLOP/s (234 us).  Two threads to a row of S,
 // with its maximum exchanged through shared memory, halve the softmax's work per
 // thread but took longer (837 us for the 16384 tokens).  Single tokens: reading K and V
-// once; 6.1 TB/s for 32 requests of up to 32768 positions (256 us, 91% of the copy rate).
+// once; 6.2 TB/s for 32 requests of up to 32768 positions (255 us, 91% of the copy rate).
 //
 // Split cache.  Where the row tiles do not fill the grid, each is computed by
 // several CTAs over parts of its positions; they leave (m, l, O) in the

@@ -41,7 +41,7 @@
 //
 // Bound: reading q, k, v and writing out once.  With every SM at work a chunk of
 // 96 + 32 KB takes about 5600 cycles, 6.1 TB/s: 12 ragged prompts of 32 heads take
-// 110 us against 86 us for their bytes, the rest being the longest prompt's walk.
+// 109 us against 86 us for their bytes, the rest being the longest prompt's walk.
 // Where requests and heads do not fill the GPU, long requests are split into
 // segments: a first launch computes each segment's own end state (K and V only),
 // then every segment starts from the decayed sum of those before it (65536 tokens of
@@ -876,7 +876,7 @@ cudaError_t launch_width(ChunkParams& p, bool f16, bool split, cudaStream_t st) 
 // its start cost about 6 us.  A split is worth it where that is less and the segments
 // fill SMs that would idle.  Measured: 65536 tokens of 16 heads 262 us in nine segments
 // against 1167 in one; 1000 tokens (with four shorter requests) of 8 heads of width
-// 64 18.5 us in eight against 31.8.
+// 64 18.5 us in eight against 31.8 (16.6 since the call starts under what precedes it).
 int linear_seg_len(const dsa_linear_problem& p) {
   constexpr int kWhole = INT32_MAX - 127;
   const int64_t longest = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;

@@ -7,8 +7,8 @@
 // threads per request and head, a thread holding 4 adjacent columns of every
 // (256 / (D_v / 4))-th row, with all its loads issued before the first use.  The
 // output's partial sums over rows meet in shared memory, in a fixed order.
-// Measured: 96 requests of 64 heads of 128 x 128, 119.5 us for 812 MB, 6.79 TB/s (the
-// copy rate); one request 3.6 us in a graph.
+// Measured: 96 requests of 64 heads of 128 x 128, 117 to 119 us for 812 MB, 6.8 to 6.9
+// TB/s (the copy rate); one request 2.9 us in a graph.
 #include "linear.cuh"
 #include "tc.cuh"
 

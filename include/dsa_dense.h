@@ -84,9 +84,9 @@ DSA_API size_t dsa_dense_workspace_size(const dsa_dense_problem* p);
  * Writes out [R, H_q, D_v] (16-byte aligned) and, if non-NULL, lse [R, H_q];
  * neither may overlap an input.
  * ws: at least dsa_dense_workspace_size(p) bytes, 256-byte aligned; the call
- * clears its status word first (dsa_read_device_status reads it).  A kernel that
- * clears it, the attention's, and where the cache is split over the grid one that
- * joins the parts; asynchronous on
+ * sets its status word (dsa_read_device_status reads it).  The attention's kernel,
+ * where the cache is split over the grid one that joins the parts, and before them
+ * one that clears the status where the join does not collect it; asynchronous on
  * `stream`, no host synchronisation, capturable in a CUDA graph.  Calls that
  * may overlap need workspaces of their own.  Host validation failures return
  * non-zero and enqueue nothing.
