@@ -257,7 +257,7 @@ class Problem:
         return self
 
     def __getattr__(self, name):
-        if name in ("c", "_keep", "_on"):
+        if name in ("c", "_keep", "_on", "_expect"):
             raise AttributeError(name)
         return getattr(self.c, name)
 
@@ -450,7 +450,10 @@ def _check_call(prob, outputs, ws):
     tensor may be None) and that everything is on the current CUDA device.  The
     problem's own tensors are looked over once, until ``set`` changes one."""
     import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else None
+    if prob._on is not None:       # (CUDA is up)
+        dev = torch._C._cuda_getDevice()
+    else:
+        dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else None
     if prob._on != dev or dev is None:
         for t in prob._keep.values():
             if t.get_device() != dev:
@@ -466,6 +469,7 @@ def _check_call(prob, outputs, ws):
             raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
     if ws.get_device() != dev:
         raise ValueError(f"the workspace is on {ws.device}, not on the current CUDA device")
+    return dev
 
 
 def _check_ints(n, **ts):
@@ -530,10 +534,14 @@ def alloc_dense_workspace(prob: DenseProblem, device="cuda"):
 def dsa_dense_attn(prob: DenseProblem, out, lse, ws, stream=None) -> None:
     """out [R, H_q, D_v] in the operands' type; lse [R, H_q] float32 or None."""
     import torch
-    c = prob.c
-    _check_call(prob, (("out", out, (c.R, c.H_q, c.D_v), prob._keep["q"].dtype),
-                       ("lse", lse, (c.R, c.H_q), torch.float32)), ws)
-    _check(_lib.dsa_dense_attn(ctypes.byref(c), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    if prob._on is None:           # (new, or changed)
+        c = prob.c
+        prob._expect = (ctypes.byref(c), (c.R, c.H_q, c.D_v), prob._keep["q"].dtype, (c.R, c.H_q))
+    ref, shape, dtype, rows = prob._expect
+    dev = _check_call(prob, (("out", out, shape, dtype), ("lse", lse, rows, torch.float32)), ws)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    _check(_lib.dsa_dense_attn(ref, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 # Linear attention with a decay for each head (include/dsa_linear.h).
@@ -590,12 +598,15 @@ def alloc_linear_workspace(prob: LinearProblem, device="cuda"):
 
 def _linear_call(fn, prob, state_in, state_out, out, ws, stream):
     import torch
-    c = prob.c
-    states = (c.n_states, c.H, c.D_k, c.D_v)
-    _check_call(prob, (("out", out, (c.R, c.H, c.D_v), prob._keep["q"].dtype),
-                       ("state_in", state_in, states, torch.float32),
-                       ("state_out", state_out, states, torch.float32)), ws)
-    _check(fn(ctypes.byref(c), _ptr(state_in), _ptr(state_out), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    if prob._on is None:           # (new, or changed)
+        c = prob.c
+        prob._expect = (ctypes.byref(c), (c.R, c.H, c.D_v), prob._keep["q"].dtype, (c.n_states, c.H, c.D_k, c.D_v))
+    ref, shape, dtype, states = prob._expect
+    dev = _check_call(prob, (("out", out, shape, dtype), ("state_in", state_in, states, torch.float32),
+                             ("state_out", state_out, states, torch.float32)), ws)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    _check(fn(ref, _ptr(state_in), _ptr(state_out), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def dsa_linear_attn(prob: LinearProblem, state_in, state_out, out, ws, stream=None) -> None:

@@ -169,12 +169,19 @@ def test_inputs_written_just_before(case):
         want.append([o.clone() for o in outs])
     assert not want[0][0].equal(want[1][0])
     got = []
-    for rep in range(6):                                 # back to back
-        big.fill_(rep)
-        for a, b in zip(use, src[rep % 3]):
-            a.copy_(b)
+    side = torch.cuda.Stream()
+    for rep in range(12):                                # back to back, every other time written on another stream
+        here = torch.cuda.current_stream()
         for o in outs:
             o.fill_(0)
+        if rep % 2:
+            side.wait_stream(here)
+        with torch.cuda.stream(side if rep % 2 else here):
+            big.fill_(rep)
+            for a, b in zip(use, src[rep % 3]):
+                a.copy_(b)
+        if rep % 2:
+            here.wait_stream(side)
         call()
         got.append([o.clone() for o in outs])
         call()                                           # once more into the same output: what a reader finds is whole
