@@ -565,9 +565,11 @@ dsa_status linear_plan(const dsa_linear_problem* p, LinearPlan* lp) {
   const int64_t segs = linear_segs(*p, a.seg_len);
   if (segs * p->H > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "too many segments (%lld)", (long long)segs);
   a.segs = (int)segs;
+  const int64_t split_segs = lp->split ? linear_split_segs(*p, a.seg_len) : 0;
+  a.split_segs = (int)(split_segs < segs ? split_segs : segs);
   size_t off = 256;
   lp->off_seg = off;
-  if (lp->split) off = align_up(off + size_t(segs) * p->H * p->D_k * p->D_v * 4, 256);
+  if (lp->split) off = align_up(off + size_t(a.split_segs) * p->H * p->D_k * p->D_v * 4, 256);
   lp->total = off;
   return DSA_OK;
 }

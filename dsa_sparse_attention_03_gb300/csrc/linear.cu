@@ -48,6 +48,7 @@
 // 16 heads: 262 us in nine segments, 1167 us in one walk; 159 us for its bytes).
 #include "linear.cuh"
 
+#include <algorithm>
 #include <cstring>
 
 #include "tc.cuh"
@@ -114,9 +115,10 @@ __device__ __forceinline__ void take_segment(const LinearArgs& a, Shared* sh, in
 }
 
 // Segment `idx` of the call (the whole CTA; the result is there after its next
-// __syncthreads).  Up to 32 requests' segments are numbered from the longest
-// request on, so that the longest walks start first; more keep their order.
+// __syncthreads).  Split requests' segments come first, so that only these need end
+// states; up to 32 requests from the longest on, so that the longest walks start first.
 __device__ void locate(const LinearArgs& a, int idx, Shared* sh) {
+  int* sums = reinterpret_cast<int*>(sh->pw);   // (the table is filled later)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) sh->req = -1;
   __syncthreads();
@@ -140,36 +142,49 @@ __device__ void locate(const LinearArgs& a, int idx, Shared* sh) {
     }
     return;
   }
-  // A thread counts the segments of some adjacent requests; the one whose range
-  // holds idx looks for it there.
+  // A thread counts some adjacent requests' segments, those of split requests and the
+  // others; the one whose range holds idx looks for it there.
   const int per = (a.B + kThreads - 1) / kThreads;
-  int mine = 0;
+  int mine[2] = {0, 0}, incl[2], first[2] = {0, 0}, split = 0;
   for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) {
     int t0, n, v;
     request(a, b, t0, n, v);
-    mine += v;
+    if (v == 1)
+      ++mine[1];
+    else
+      mine[0] += v;
   }
-  int incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
-  }
-  int* sums = reinterpret_cast<int*>(sh->pw);   // (the table is filled later)
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  int first = incl - mine;
-  for (int w = 0; w < warp; ++w) first += sums[w];
-  if (idx >= first && idx < first + mine)
-    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) {
-      int t0, n, v;
-      request(a, b, t0, n, v);
-      if (idx < first + v) {
-        take_segment(a, sh, b, idx - first, first, t0, n, v);
-        break;
-      }
-      first += v;
+  for (int x = 0; x < 2; ++x) {
+    incl[x] = mine[x];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl[x], o);
+      if (lane >= o) incl[x] += t;
     }
+    if (lane == 31) sums[warp * 2 + x] = incl[x];
+  }
+  __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) {
+    split += sums[w * 2];
+    if (w < warp) {
+      first[0] += sums[w * 2];
+      first[1] += sums[w * 2 + 1];
+    }
+  }
+  const bool one = idx >= split;
+  int at = one ? split + first[1] + incl[1] - mine[1] : first[0] + incl[0] - mine[0];
+  if (idx < at || idx >= at + (one ? mine[1] : mine[0])) return;
+  for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) {
+    int t0, n, v;
+    request(a, b, t0, n, v);
+    if ((v == 1) != one) continue;
+    if (idx < at + v) {
+      take_segment(a, sh, b, idx - at, at, t0, n, v);
+      return;
+    }
+    at += v;
+  }
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
@@ -250,6 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   if (STATE) pdl_trigger();
   if (sh->req < 0 || (STATE && sh->seg >= sh->nseg - 1)) {   // (nothing here; no segment follows)
     pdl_wait();
+    return;
+  }
+  if (sh->nseg > 1 && sh->first + sh->nseg > a.split_segs) {   // (offsets that overlap: more than the workspace holds)
+    pdl_wait();
+    if (tid == 0) raise_status(a.status, DSA_DEVICE_CAPACITY);
     return;
   }
   const int place = state_place(a, sh->req, &sh->scratch, h == 0 && sh->seg == 0);
@@ -713,35 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     };
     float* ends = a.seg_state + ((int64_t)sh->first * a.H + h) * head;   // [segment] of this request, H heads apart
     pdl_wait();
-    const float* start = seg == 0 && a.state_in ? a.state_in + ((int64_t)place * a.H + h) * head : nullptr;
-    float* copy = ends + (int64_t)(nseg - 1) * a.H * head;   // of the start: state_out may be state_in
-    auto decay_of = [&](int segs) { return exp2f(fmaxf(ld2 * ((float)a.seg_len * (float)segs), -300.f)); };
     if (!STATE) {
-      if (seg == 0) {
-        if (nseg > 1)
-          load(copy);
-        else if (start)
-          load(start);
-      } else {
-        // lambda^(seg_len (seg - 1 - s)) E_s summed over the segments s before this one.
-        load(ends + (int64_t)(seg - 1) * a.H * head);
-        int s0 = seg - 1;                                // first segment that still counts
-        while (s0 > 0 && decay_of(seg - s0) != 0.f) --s0;
-        const int64_t step = (int64_t)a.H * head;
-#pragma unroll
-        for (int x = 0; x < DK; x += 16) {               // (16 values of two segments in flight)
-#pragma unroll 2
-          for (int s = seg - 2; s >= s0; --s) {
-            const float f = decay_of(seg - 1 - s);
-            const float* e = ends + s * step + x * DV + d;
-            float t[16];
-#pragma unroll
-            for (int y = 0; y < 16; ++y) t[y] = e[y * DV];
-#pragma unroll
-            for (int y = 0; y < 16; ++y) H[x + y] = fmaf(f, t[y], H[x + y]);
-          }
-        }
-      }
+      // Segment s of a split request starts from what the scan left for it.
+      const float* start = a.state_in ? a.state_in + ((int64_t)place * a.H + h) * head : nullptr;
+      if (nseg > 1) start = ends + (int64_t)(seg > 0 ? seg - 1 : nseg - 1) * a.H * head;
+      if (start && (seg > 0 || a.state_in)) load(start);
     }
     // lambda^128: rounded to fp32 it would be off the same way with every chunk (a head
     // that remembers 4096 tokens by 30 times that), so the walk takes its two fp32
@@ -824,19 +820,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh->dh_free[c & (dh_bufs - 1)]));
     }
-    if (STATE && seg == 0) {
-      const float f = decay_of(1);
-#pragma unroll
-      for (int x = 0; x < DK; x += 16) {
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const float v = start ? start[(x + y) * DV + d] : 0.f;
-          copy[(x + y) * DV + d] = v;
-          H[x + y] = fmaf(f, v, H[x + y]);
-        }
-        asm volatile("" ::: "memory");
-      }
-    }
     if (ok && final_state)
       store(STATE ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
     }
@@ -845,6 +828,85 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// Between the two launches of a split call.  E_s the end state that segment s has on
+// its own, each segment starts with
+//   P_0 = the request's state,  P_{s+1} = lambda^seg_len P_s + E_s.
+// P_{s+1} is written over E_s, and P_0 behind them (state_out may be state_in).  One CTA
+// for 256 elements of a split request's head: a thread walks the segments with one
+// element, 16 loads in flight.
+constexpr int kScanThreads = 256;
+__global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearArgs a) {
+  __shared__ int req, segs, first, scratch, sums[kScanThreads / 32][2];
+  const int head = a.D_k * a.D_v, parts = head / kScanThreads;
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % a.H, k = blockIdx.x / parts / a.H;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  // The k-th split request in the order of the segments (locate).
+  if (tid == 0) req = -1;
+  __syncthreads();
+  if (a.B <= 32) {
+    if (warp == 0) {
+      int t0, n = -1, v = 0;
+      if (lane < a.B) request(a, lane, t0, n, v);
+      int rank = 0, at = 0;
+      for (int o = 0; o < a.B; ++o) {
+        const int on = __shfl_sync(0xffffffffu, n, o), ov = __shfl_sync(0xffffffffu, v, o);
+        if (on > n || (on == n && o < lane)) {
+          ++rank;
+          at += ov;
+        }
+      }
+      if (rank == k && v > 1) req = lane, segs = v, first = at;
+    }
+  } else {
+    const int per = (a.B + kScanThreads - 1) / kScanThreads;
+    int mine[2] = {0, 0}, incl[2];   // split requests, their segments
+    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) {
+      int t0, n, v;
+      request(a, b, t0, n, v);
+      if (v > 1) ++mine[0], mine[1] += v;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      incl[x] = mine[x];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl[x], o);
+        if (lane >= o) incl[x] += t;
+      }
+      if (lane == 31) sums[warp][x] = incl[x];
+    }
+    __syncthreads();
+    int rank = incl[0] - mine[0], at = incl[1] - mine[1];
+    for (int w = 0; w < warp; ++w) rank += sums[w][0], at += sums[w][1];
+    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) {
+      int t0, n, v;
+      request(a, b, t0, n, v);
+      if (v == 1) continue;
+      if (rank == k) req = b, segs = v, first = at;
+      ++rank, at += v;
+    }
+  }
+  __syncthreads();
+  const float f = exp2f(fmaxf(log2_decay(a.log_decay[h]) * (float)a.seg_len, -300.f));
+  const int place = req >= 0 && first + segs <= a.split_segs ? state_place(a, req, &scratch, false) : -1;
+  pdl_wait();
+  if (place < 0) return;
+  const int64_t step = (int64_t)a.H * head;
+  float* p = a.seg_state + ((int64_t)first * a.H + h) * head + part * kScanThreads + tid;
+  float x = 0.f;
+  if (a.state_in) p[(segs - 1) * step] = x = a.state_in[((int64_t)place * a.H + h) * head + part * kScanThreads + tid];
+  if (f == 0.f) return;              // (whatever the states before hold)
+  for (int s = 0; s < segs - 1; s += 16) {
+    float e[16];
+#pragma unroll
+    for (int y = 0; y < 16; ++y) e[y] = s + y < segs - 1 ? p[(s + y) * step] : 0.f;
+#pragma unroll
+    for (int y = 0; y < 16; ++y)
+      if (s + y < segs - 1) p[(s + y) * step] = x = fmaf(f, x, e[y]);
+  }
 }
 
 template <int DK, int DV, bool F16>
@@ -856,7 +918,12 @@ cudaError_t launch_one(ChunkParams& p, bool split, cudaStream_t st) {
   if (split) {
     auto states = linear_chunk_kernel<DK, DV, F16, true>;
     if ((e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    if ((e = launch_pdl(states, dim3(grid), dim3(kThreads), smem, st, p)) != cudaSuccess) return e;
+    const unsigned heads = (unsigned)p.a.split_segs * (unsigned)p.a.H;
+    if ((e = launch_pdl(states, dim3(heads), dim3(kThreads), smem, st, p)) != cudaSuccess) return e;
+    const unsigned requests = (unsigned)std::min(p.a.B, p.a.R / p.a.seg_len);   // that are split, at most
+    if ((e = launch_pdl(linear_scan_kernel, dim3(requests * p.a.H * (DK * DV / kScanThreads)), dim3(kScanThreads), 0, st, p.a)) !=
+        cudaSuccess)
+      return e;
   }
   auto kernel = linear_chunk_kernel<DK, DV, F16, false>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
@@ -888,8 +955,7 @@ int linear_seg_len(const dsa_linear_problem& p) {
   }
   const int64_t len = ((p.R + segs - 1) / segs + 127) / 128 * 128;
   const double n = (double)((longest + 127) / 128), m = (double)(len / 128);
-  const double sum = 0.6 * p.D_k * p.D_v / 16384;
-  return 3.2 * n > 6.0 + 1.6 * 3.2 * m + sum * n / m ? (int)len : kWhole;
+  return 3.2 * n > 9.0 + 1.6 * 3.2 * m ? (int)len : kWhole;
 }
 
 int64_t linear_segs(const dsa_linear_problem& p, int seg_len) { return (int64_t)p.R / seg_len + p.B; }

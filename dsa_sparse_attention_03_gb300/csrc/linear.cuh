@@ -16,13 +16,13 @@ struct LinearArgs {
   const float* state_in;    // or null
   float* state_out;         // or null
   uint16_t* out;
-  float* seg_state;         // workspace [segs, H, D_k, D_v]: each segment's end state
+  float* seg_state;         // workspace [split_segs, H, D_k, D_v]: each segment's end state
   uint32_t* status;
   int64_t q_stride, k_stride, v_stride;
   uint64_t wait_ns;
   int R, B, H, D_k, D_v, n_states;
   int seg_len;              // tokens of a segment (a multiple of 128)
-  int segs;                 // segments of the call, at most
+  int segs, split_segs;     // segments of the call, at most, and those of split requests
   float scale;
   int test_no_load;         // test hook: arm the first chunk, issue no copy
   int status_known;         // the status word is this value whatever the kernel finds (-1: it is cleared before, and raised)
@@ -33,6 +33,8 @@ struct LinearArgs {
 int linear_seg_len(const dsa_linear_problem& p);
 // Segments of the call, at most.
 int64_t linear_segs(const dsa_linear_problem& p, int seg_len);
+// Those of split requests: one of n > seg_len tokens has less than 2 n / seg_len.
+inline int64_t linear_split_segs(const dsa_linear_problem& p, int seg_len) { return 2 * (int64_t)p.R / seg_len; }
 
 cudaError_t launch_linear(const LinearArgs& a, bool f16, bool split, cudaStream_t st);
 cudaError_t launch_linear_step(const LinearArgs& a, bool f16, cudaStream_t st);
