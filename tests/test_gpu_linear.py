@@ -319,3 +319,52 @@ def test_fewer_places_than_requests_is_flagged(step):
     assert bits & dsa.DSA_DEVICE_BAD_INDEX
     ro = t["row_offsets"].tolist()
     assert (out[ro[2]:] == 77.0).all() and not (out[:ro[2]] == 77.0).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_segments_of_many_requests(in_place, dtype):
+    # Long and short requests in turn, more than a warp looks up; the long ones are split,
+    # one of them and a short one are unused, and the states' places are in another order.
+    import torch
+    rows = [0, 900, 5, 2000, 1, 1300] + [3] * 30 + [1100, 0, 700]
+    B = len(rows)
+    places = [(7 * b + 3) % 41 for b in range(B)]
+    places[5] = places[8] = -1
+    t, s0 = H.make(rows, 2, 64, 128, dtype=dtype, seed=31, n_states=41)
+    out, state, bits = H.run(t, s0, 0.1, places=places, in_place=in_place, n_states=41)
+    assert bits == 0
+    ro = t["row_offsets"].tolist()
+    for b, at in enumerate(places):
+        if at < 0:
+            assert (out[ro[b]:ro[b + 1]] == 77.0).all()
+            continue
+        one = {x: t[x][ro[b]:ro[b + 1]] if x in "qkv" else t[x] for x in t}
+        one["row_offsets"] = torch.tensor([0, rows[b]], dtype=torch.int32)
+        H.check(one, s0[at][None], 0.1, out[ro[b]:ro[b + 1]], state[at][None])
+    untouched = s0 if in_place else torch.full_like(s0, 77.0)
+    for i in set(range(41)) - set(places):
+        assert state[i].equal(untouched[i])
+
+
+@pytest.mark.parametrize("state", [False, True])
+def test_many_segments_of_one_head(state):
+    # One head on the whole GPU: more segments than the scan loads at a time.
+    t, s0 = H.make([20000], 1, 64, 64, seed=32, state=state, decay=-3e-4)
+    out, s1, bits = H.run(t, s0, 0.1, in_place=state)
+    assert bits == 0
+    H.check(t, s0, 0.1, out, s1)
+
+
+def test_offsets_that_overlap_are_flagged():
+    # Three requests over the same rows: more segments than the workspace has end states
+    # for.  Those that do not fit are skipped.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    t, s0 = H.make([3000], 1, 64, 64, seed=33, n_states=5)
+    one = dict(t)
+    t["row_offsets"] = torch.tensor([0, 3000, 0, 3000, 0, 3000], dtype=torch.int32)
+    out, state, bits = H.run(t, s0, 0.1)
+    assert bits == dsa.DSA_DEVICE_CAPACITY
+    H.check(one, s0[:1], 0.1, out, state[:1])
+    assert (state[2] == 77.0).all() and (state[4] == 77.0).all()
