@@ -43,9 +43,12 @@
 // 96 + 32 KB takes about 5600 cycles, 6.1 TB/s: 12 ragged prompts of 32 heads take
 // 109 us against 86 us for their bytes, the rest being the longest prompt's walk.
 // Where requests and heads do not fill the GPU, long requests are split into
-// segments: a first launch computes each segment's own end state (K and V only),
-// then every segment starts from the decayed sum of those before it (65536 tokens of
-// 16 heads: 262 us in nine segments, 1167 us in one walk; 159 us for its bytes).
+// segments: a first launch computes each segment's own end state (K and V only), a
+// scan adds them up to each segment's start, and a second launch walks the segments
+// side by side (65536 tokens of 16 heads: 243 us in nine segments, 1171 us in one walk;
+// 159 us for its bytes, 238 with K and V read twice).  Adding up the states before it in
+// each segment's own CTA, one warpgroup's loads at a time, took 20 us more, and as much
+// again for the first segment's state.
 #include "linear.cuh"
 
 #include <algorithm>
@@ -937,25 +940,26 @@ cudaError_t launch_width(ChunkParams& p, bool f16, bool split, cudaStream_t st) 
 
 }  // namespace
 
-// One walk over a request's n chunks takes about 3.2 us a chunk.  Split, a request's
-// states are walked first (0.6 of that a chunk), then its segments side by side, each
-// after adding up the states before it (0.6 us for 64 KB); the second launch and
-// its start cost about 6 us.  A split is worth it where that is less and the segments
-// fill SMs that would idle.  Measured: 65536 tokens of 16 heads 262 us in nine segments
-// against 1167 in one; 1000 tokens (with four shorter requests) of 8 heads of width
-// 64 18.5 us in eight against 31.8 (16.6 since the call starts under what precedes it).
+// One walk over a request's n chunks takes about 7 + 2.4 n us.  Split into segments of m
+// chunks, the states' launch, the scan and the outputs' launch take about 19 + 4.2 m, if
+// the segments fill SMs that would idle.  Measured, one walk against segments: 65536
+// tokens of 16 heads 1171 us, 243 in nine; 4096 of 32 heads 82, 53 in four; of 64 heads
+// 85, 90 in two; 1024 of 16 heads 26, 21 in eight; 512 of them 16, 20 in four.
+// Where requests and heads alone fill the GPU, only a request that is still walked when
+// the others are done is split (20000 tokens and 39 of 200, 8 heads: 370 and 105; with
+// 299 of 100, 16 heads, 391 and 421); a short one costs its start and end, 3 chunks.
 int linear_seg_len(const dsa_linear_problem& p) {
   constexpr int kWhole = INT32_MAX - 127;
   const int64_t longest = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
-  const int64_t even = (int64_t)p.R * p.H / 152;   // tokens of each SM if the work were level
+  const double n = (double)((longest + 127) / 128);
   int64_t segs = 152 / p.H - (p.B - 1);            // segments that find an SM each
   if (segs < 2) {
-    if (longest <= even + even / 2) return kWhole;
+    const double even = ((double)p.R / kC + 3.5 * p.B) * p.H / 152;   // chunks of each SM if the work were level
+    if (n <= 1.5 * even) return kWhole;
     segs = 152 / p.H > 0 ? 152 / p.H : 1;
   }
   const int64_t len = ((p.R + segs - 1) / segs + 127) / 128 * 128;
-  const double n = (double)((longest + 127) / 128), m = (double)(len / 128);
-  return 3.2 * n > 9.0 + 1.6 * 3.2 * m ? (int)len : kWhole;
+  return 2.4 * n > 12.0 + 4.2 * (double)(len / 128) ? (int)len : kWhole;
 }
 
 int64_t linear_segs(const dsa_linear_problem& p, int seg_len) { return (int64_t)p.R / seg_len + p.B; }

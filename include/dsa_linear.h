@@ -95,7 +95,7 @@ DSA_API size_t dsa_linear_workspace_size(const dsa_linear_problem* p);
  * A request without tokens hands its state on.  Rows outside every request are
  * not written.  ws: at least dsa_linear_workspace_size(p) bytes, 256-byte
  * aligned; its status word is cleared first.  A kernel that clears it, and one, or
- * two where long requests are split; asynchronous, capturable, no host
+ * three where long requests are split; asynchronous, capturable, no host
  * synchronisation.  Calls that may overlap need workspaces of their own.
  */
 DSA_API dsa_status dsa_linear_attn(const dsa_linear_problem* p, const float* state_in, float* state_out,
