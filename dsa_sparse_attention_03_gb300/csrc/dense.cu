@@ -41,7 +41,8 @@
 // the ring only 1.6 tiles, reach 1.06 PFLOP/s (234 us).  Two threads to a row of S,
 // with its maximum exchanged through shared memory, halve the softmax's work per
 // thread but took longer (837 us for the 16384 tokens).  Single tokens: reading K and V
-// once; 6.2 TB/s for 32 requests of up to 32768 positions (255 us, 91% of the copy rate).
+// once; 6.2 TB/s for 32 requests of up to 32768 positions (255 us, 91% of the copy rate),
+// eight of 32768 at the copy rate.
 //
 // Split cache.  Where the row tiles do not fill the grid, each is computed by
 // several CTAs over parts of its positions; they leave (m, l, O) in the
@@ -848,28 +849,38 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
   int64_t tiles = p.B * ((most * G + per - 1) / per);
   tiles = tiles < p.R * G / per + p.B ? tiles : p.R * G / per + p.B;
   s.tiles = (int)tiles;
-  // Parts per row tile.  Single tokens of several requests: eight items per
-  // resident CTA, since their lengths differ (32 requests of up to 32768 positions:
-  // 288 us with two, 268 with four, 258 with eight, 255 with sixteen); one request,
-  // whose items are alike: one each.  Prompts: two where the row tiles alone leave
-  // SMs idle.  No part has less than two K/V tiles.
+  // Parts per row tile, of at least four K/V tiles (512 rows over 512 positions, 32 heads
+  // over 8: 13.6 us in one part, 20.2 in two; 64 rows over 4096: 20.8 in eight, 30.5 in
+  // sixteen): the parts' way through memory and the join have to pay.  Single tokens'
+  // parts are small: 512 positions in two (9.8 us, 11.0 in one).
   const int64_t items = tiles * p.H_kv, slots = dense_slots(s.nw);
   const int64_t kvt = (p.L_max + kTile - 1) / kTile;
-  const int64_t each = p.B == 1 ? 1 : (s.nw == 1 ? 8 : 2);
+  const int64_t cap = s.nw == 1 && kvt >= 4 && kvt < 8 ? 2 : (kvt / 4 < 64 ? kvt / 4 : 64);
+  // Items of one length as far as the host can tell: one to an SM, or one to a slot
+  // where that leaves them eight tiles (single tokens of 64 heads over 8: one request
+  // over 32768 positions 36 us in 19 parts, 43 in 38; eight 158 in four, 180 in sixteen).
+  const bool even = p.B == 1 || 4 * p.L_total >= 3 * (int64_t)p.B * p.L_max;
   int64_t splits = 1;
-  if (items > 0 && items < each * slots) splits = p.B == 1 ? slots / items : (each * slots + items - 1) / items;
-  const int64_t cap = kvt / 2 < 64 ? kvt / 2 : 64;
+  if (items > 0 && items <= 152 && even) {
+    splits = kvt >= 8 * (slots / items) ? slots / items : 152 / items;
+  } else if (items > 0 && p.B > 1) {
+    // Others, single tokens: eight items per slot, since their lengths differ (32
+    // requests of up to 32768 positions: 288 us with two, 268 with four, 258 with eight,
+    // 255 with sixteen).  Prompts: two where the row tiles alone leave SMs idle.
+    const int64_t each = s.nw == 1 ? 8 : 2;
+    if (items < each * slots) splits = (each * slots + items - 1) / items;
+    // Finer parts than one a slot only while they keep sixteen tiles.
+    const int64_t wave = slots / items > 1 ? slots / items : 1;
+    if (splits > wave && splits > kvt / 16) splits = wave > kvt / 16 ? wave : kvt / 16;
+  }
   if (splits > cap) splits = cap;
-  // Finer parts than one a slot only while they keep sixteen tiles.
-  const int64_t wave = items > 0 && slots / items > 1 ? slots / items : 1;
-  if (splits > wave && splits > kvt / 16) splits = wave > kvt / 16 ? wave : kvt / 16;
   s.splits = splits < 1 ? 1 : (int)splits;
   // One request whose row tiles all see about as much (a chunk behind a long
   // cache): the last, partly filled wave's items in parts, so that it is shorter
   // (2048 rows over 10240 positions, 512 items: 466 us without, 441 with).
   s.tail = s.tail_parts = 0;
   const int64_t rest = items % slots;
-  if (s.nw == 2 && p.B == 1 && items > slots && rest > 0 && rest <= slots / 2 && 2 * ((int64_t)p.L_max - p.R) >= p.L_max) {
+  if (s.splits == 1 && s.nw == 2 && p.B == 1 && items > slots && rest > 0 && rest <= slots / 2 && 2 * ((int64_t)p.L_max - p.R) >= p.L_max) {
     s.tail = (int)rest;
     s.tail_parts = (int)(slots / rest < 4 ? slots / rest : 4);
   }

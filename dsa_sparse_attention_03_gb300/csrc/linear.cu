@@ -41,14 +41,14 @@
 //
 // Bound: reading q, k, v and writing out once.  With every SM at work a chunk of
 // 96 + 32 KB takes about 5600 cycles, 6.1 TB/s: 12 ragged prompts of 32 heads take
-// 109 us against 86 us for their bytes, the rest being the longest prompt's walk.
+// 107 us against 86 us for their bytes, the rest being the longest prompt's walk.
 // Where requests and heads do not fill the GPU, long requests are split into
 // segments: a first launch computes each segment's own end state (K and V only), a
 // scan adds them up to each segment's start, and a second launch walks the segments
-// side by side (65536 tokens of 16 heads: 243 us in nine segments, 1171 us in one walk;
-// 159 us for its bytes, 238 with K and V read twice).  Adding up the states before it in
-// each segment's own CTA, one warpgroup's loads at a time, took 20 us more, and as much
-// again for the first segment's state.
+// side by side (65536 tokens of 16 heads: 262 us in nine segments, 1171 us in one walk;
+// 159 us for its bytes, 238 with K and V read twice).  With each segment's CTA adding up
+// the states before it, one warpgroup's loads at a time, 4096 tokens of 16 heads that go
+// on from a state took 63 us, with the scan 33.
 #include "linear.cuh"
 
 #include <algorithm>
