@@ -103,7 +103,8 @@ DSA_API dsa_status dsa_linear_attn(const dsa_linear_problem* p, const float* sta
 
 /*
  * Single tokens: one for each request (R == B).  Both state_in (or NULL) and
- * state_out as above; state_out must be set.  One kernel.
+ * state_out as above; state_out must be set.  One kernel (with state_idx, after a
+ * memset of the status).
  */
 DSA_API dsa_status dsa_linear_step(const dsa_linear_problem* p, const float* state_in, float* state_out,
                                    uint16_t* out, void* ws, size_t ws_bytes, void* stream);
