@@ -41,8 +41,7 @@
 // the ring only 1.6 tiles, reach 1.06 PFLOP/s (234 us).  Two threads to a row of S,
 // with its maximum exchanged through shared memory, halve the softmax's work per
 // thread but took longer (837 us for the 16384 tokens).  Single tokens: reading K and V
-// once; 6.2 TB/s for 32 requests of up to 32768 positions (255 us, 91% of the copy rate),
-// eight of 32768 at the copy rate.
+// once; 6.2 TB/s for 32 requests of up to 32768 positions (255 us, 91% of the copy rate).
 //
 // Split cache.  Where the row tiles do not fill the grid, each is computed by
 // several CTAs over parts of its positions; they leave (m, l, O) in the
@@ -856,10 +855,12 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
   const int64_t items = tiles * p.H_kv, slots = dense_slots(s.nw);
   const int64_t kvt = (p.L_max + kTile - 1) / kTile;
   const int64_t cap = s.nw == 1 && kvt >= 4 && kvt < 8 ? 2 : (kvt / 4 < 64 ? kvt / 4 : 64);
-  // Items of one length as far as the host can tell: one to an SM, or one to a slot
-  // where that leaves them eight tiles (single tokens of 64 heads over 8: one request
-  // over 32768 positions 36 us in 19 parts, 43 in 38; eight 158 in four, 180 in sixteen).
-  const bool even = p.B == 1 || 4 * p.L_total >= 3 * (int64_t)p.B * p.L_max;
+  // Items of one length: one to an SM, or one to a slot where that leaves them eight
+  // tiles (one token of 64 heads over 8 and 32768 positions: 35 us in 19 parts, 43 in
+  // 38).  So are one request's, and prompts that fill a packed cache; single tokens of
+  // several requests may not be, whatever the host knows of a cache laid out by capacity.
+  const int64_t full = (int64_t)p.B * p.L_max;
+  const bool even = p.B == 1 || (s.nw == 2 && p.L_total <= full && 4 * p.L_total >= 3 * full);
   int64_t splits = 1;
   if (items > 0 && items <= 152 && even) {
     splits = kvt >= 8 * (slots / items) ? slots / items : 152 / items;
@@ -869,9 +870,11 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
     // 255 with sixteen).  Prompts: two where the row tiles alone leave SMs idle.
     const int64_t each = s.nw == 1 ? 8 : 2;
     if (items < each * slots) splits = (each * slots + items - 1) / items;
-    // Finer parts than one a slot only while they keep sixteen tiles.
-    const int64_t wave = slots / items > 1 ? slots / items : 1;
-    if (splits > wave && splits > kvt / 16) splits = wave > kvt / 16 ? wave : kvt / 16;
+    // Finer parts than one a slot only of sixteen tiles, and from 8192 positions on (one
+    // of 32768 positions and seven of 500: 50 us, 69 with parts of 32 tiles; eight of
+    // 32768: 179 and 166; 64 of 4096: 158 in one part, 168 in two).
+    const int64_t wave = slots / items > 1 ? slots / items : 1, fine = kvt >= 64 ? kvt / 16 : 1;
+    if (splits > wave && splits > fine) splits = wave > fine ? wave : fine;
   }
   if (splits > cap) splits = cap;
   s.splits = splits < 1 ? 1 : (int)splits;
