@@ -54,6 +54,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "linear_protocol.h"
 #include "tc.cuh"
 
 namespace dsa {
@@ -62,8 +63,8 @@ namespace {
 constexpr int kC = 128;            // tokens of a chunk
 constexpr int kThreads = 640;
 constexpr int kQuarter = 32;       // tokens of the decayed V in one buffer
-constexpr int kStages = 2;         // of Q, K and V; the state launch, without Q, has room for three
-constexpr int kStateStages = 3;
+constexpr int kStages = ChunkPipe<false>::stages;        // of Q, K and V; the state launch, without Q,
+constexpr int kStateStages = ChunkPipe<true>::stages;    // has room for three
 
 // Tensor-memory columns.
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384;
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   constexpr int KC = DK / 64, VC = DV / 64, QC = KC > VC ? KC : VC;
   constexpr uint32_t kStage = stage_bytes<DK, DV>();
   constexpr int kTerms = F16 ? 2 : 3;
+  using Pipe = ChunkPipe<STATE>;
   const LinearArgs& a = p.a;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw;   // (1024-byte aligned: checked below)
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     }
     for (int i = 0; i < kStateStages; ++i) {
       mbar_init(smem_u32(&sh->kv_full[i]), 1);
-      mbar_init(smem_u32(&sh->kv_empty[i]), 2);
+      mbar_init(smem_u32(&sh->kv_empty[i]), Pipe::kv_releases);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sh->v_ready[i]), DV / 32);
@@ -338,18 +340,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   // Buffers of the decayed V: two, each used twice a chunk; in the state launch four
   // (it has no S), used once.
-  const int v_bufs = STATE ? 4 : 2;
   auto v_col = [&](int b) -> uint32_t { return b < 2 ? kColV + b * 64 : kColS + (b - 2) * 64; };
   // dH^T likewise: one accumulator, or two in turn (the second in O's place).
-  const int dh_bufs = STATE ? 2 : 1;
-  auto dh_col = [&](int c) -> uint32_t { return STATE && (c & 1) ? kColO : kColH; };
-  auto dh_phase = [&](int c) { return (uint32_t)(STATE ? (c >> 1) & 1 : c & 1); };
-  const int stages = STATE ? kStateStages : kStages;
+  auto dh_col = [&](int c) -> uint32_t { return Pipe::dh(c) ? kColO : kColH; };
   const uint32_t k_off = STATE ? 0 : QC * kChunkBytes;   // K in a stage, behind Q
   const uint32_t stride = STATE ? (KC + VC) * kChunkBytes : kStage;
   static_assert(kStateStages * (KC + VC) * kChunkBytes <= kStages * kStage, "the state launch's stages");
-  auto stage = [&](int c) { return smem + (c % stages) * stride; };
-  auto phase = [&](int c) { return (uint32_t)((c / stages) & 1); };
+  constexpr int stages = Pipe::stages;
+  auto stage = [&](int c) { return smem + Pipe::stage(c) * stride; };
+  auto phase = [&](int c) { return Pipe::stage_phase(c); };
   const int quad = warp & 3;
 
   if (warp < 4) {
@@ -360,12 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         int c = 0;
         bool q_last = false;   // chunk c's Q tile was asked for
         for (; c < chunks; ++c) {
-          const int s = c % stages, y = token(c);
+          const int s = Pipe::stage(c), y = token(c);
           const uint32_t q = smem_u32(stage(c)), k = q + k_off, v = k + KC * kChunkBytes;
-          // (the state launch's K and V are read last by dH, whose end is dh_ready)
-          if (c >= stages && !(STATE ? wait_bar(bar(sh->dh_ready[(c - stages) & 1]), dh_phase(c - stages), wc)
-                                            : wait_bar(bar(sh->kv_empty[s]), phase(c - stages), wc)))
-            break;
+          if (c >= stages && !wait_bar(bar(sh->kv_empty[s]), phase(c - stages), wc)) break;
           mbar_expect_tx(bar(sh->kv_full[s]), (KC + VC) * kChunkBytes);
           if (a.test_no_load && c == 0) continue;
           for (int x = 0; x < KC; ++x) tma_load_2d(k + x * kChunkBytes, &p.tk, h * DK + x * 64, y, bar(sh->kv_full[s]));
@@ -391,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const uint32_t id_o = idesc_16(F16, kC, DV, false, true);
       const uint64_t dh = desc_kmajor(smem_u32(Hb));
       for (int c = 0; c < chunks; ++c) {
-        const int s = c % stages;
+        const int s = Pipe::stage(c);
         const uint32_t q = smem_u32(stage(c)), k = q + k_off, v = k + KC * kChunkBytes;
         const uint64_t dq = desc_kmajor(q), dk = desc_kmajor(k), dv = desc_mnmajor(v, kChunkBytes);
         if (!wait_bar_warp(bar(sh->kv_full[s]), phase(c), wc)) break;
@@ -438,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       for (int c = 0; c < deltas && ok; ++c) {
         const uint64_t dk = desc_mnmajor(smem_u32(stage(c)) + k_off, kChunkBytes);
         if (ragged && c == chunks - 1 && !(ok = wait_bar_warp(bar(sh->tail), 0, wc))) break;
-        const int db = c & (dh_bufs - 1);
-        if (c >= dh_bufs && !(ok = wait_bar_warp(bar(sh->dh_free[db]), dh_phase(c - dh_bufs), wc))) break;
+        const int db = Pipe::dh(c);
+        if (c >= Pipe::dh_bufs && !(ok = wait_bar_warp(bar(sh->dh_free[db]), Pipe::dh_phase(c - Pipe::dh_bufs), wc))) break;
 #pragma unroll 1
         for (int g = 0; g < 4 && ok; ++g) {
-          const int b = g & (v_bufs - 1);
-          if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), STATE ? c & 1 : g >> 1, wc))) break;
+          const int b = Pipe::v(g);
+          if (!(ok = wait_bar_warp(bar(sh->v_ready[b]), Pipe::v_phase(c, g), wc))) break;
           const uint32_t va = tmem + v_col(b);
           tc_fence_after();
           {
@@ -456,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             mma_commit(bar(sh->v_free[b]));
             if (g == 3) {
               mma_commit(bar(sh->dh_ready[db]));
-              if (!STATE) mma_commit(bar(sh->kv_empty[c % stages]));
+              mma_commit(bar(sh->kv_empty[Pipe::stage(c)]));
             }
           }
         }
@@ -474,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             tma_store_2d(&p.to, h * DV + x * 64, t0 + c * kC, smem_u32(stage(c) + x * kChunkBytes));
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive(bar(sh->q_empty[c % stages]));
+          mbar_arrive(bar(sh->q_empty[Pipe::stage(c)]));
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       }
@@ -624,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const bool short_chunk = ragged && c == chunks - 1;
       if (c >= deltas && !short_chunk) break;
       const int g0 = (group + 3 * groups - 4 * c % groups) % groups;   // this group's first quarter of the chunk
-      if (!(ok = wait_bar_warp(bar(sh->kv_full[c % stages]), phase(c), wc))) break;
+      if (!(ok = wait_bar_warp(bar(sh->kv_full[Pipe::stage(c)]), phase(c), wc))) break;
       unsigned char* kv = stage(c) + k_off;   // the K chunks, then the V chunks
       if (short_chunk) {
         // Zeros in K and V behind the last token.
@@ -677,9 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
 #pragma unroll 1
       for (int g = g0; g < 4; g += groups) {
-        const int b = g & (v_bufs - 1);
-        if (STATE ? c > 0 : (c > 0 || g > 1))   // the buffer's last use
-          if (!(ok = wait_bar_warp(bar(sh->v_free[b]), STATE ? (c - 1) & 1 : (g >> 1) ^ 1, wc))) break;
+        const int b = Pipe::v(g);
+        if (!Pipe::v_first(c, g) && !(ok = wait_bar_warp(bar(sh->v_free[b]), Pipe::v_phase_before(c, g), wc))) break;
         tc_fence_after();
         if (F16 && g == 0 && (lane & 3) == 0) {
 #pragma unroll
@@ -787,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (lane == 0) mbar_arrive(bar(sh->h_ready));
       }
       if (c >= deltas) break;
-      if (!(ok = wait_bar_warp(bar(sh->dh_ready[c & (dh_bufs - 1)]), dh_phase(c), wc))) break;
+      if (!(ok = wait_bar_warp(bar(sh->dh_ready[Pipe::dh(c)]), Pipe::dh_phase(c), wc))) break;
       tc_fence_after();
       {
         // Forwards, H = lambda^n H + dH; backwards, H = H + lambda^(128 c) dH.
@@ -821,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh->dh_free[c & (dh_bufs - 1)]));
+      if (lane == 0) mbar_arrive(bar(sh->dh_free[Pipe::dh(c)]));
     }
     if (ok && final_state)
       store(STATE ? ends + (int64_t)seg * a.H * head : a.state_out + ((int64_t)place * a.H + h) * head);
