@@ -88,7 +88,7 @@ struct __align__(16) Shared {
   float column[32];                // lambda^(31-y)
   unsigned char mx[2][128];        // fp16: exponent fields of the two halves' largest |S| of each row
   unsigned char cs[2][128];        // fp16: scale of each column of H as Q H read it (a power of two's exponent field)
-  unsigned char vs[2][128];        // fp16: the same of each column of the decayed V
+  unsigned char vs[ChunkPipe<true>::scale_slots][128];   // fp16: the same of each column of the decayed V
 };
 
 template <int DK, int DV>
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         tc_fence_after();
         if (F16 && g == 0 && (lane & 3) == 0) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) sh->vs[c & 1][quad * 32 + (lane >> 2) + 8 * y] = exponent_field(vback[y]);
+          for (int y = 0; y < 4; ++y) sh->vs[Pipe::scale(c)][quad * 32 + (lane >> 2) + 8 * y] = exponent_field(vback[y]);
         }
         float2 fd[4];
 #pragma unroll
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           f = turn >= 1.f ? above : below;
           if (turn >= 1.f) turn -= 1.f;
         }
-        const float vback = F16 ? exponent_value(sh->vs[c & 1][d]) : 1.f;
+        const float vback = F16 ? exponent_value(sh->vs[Pipe::scale(c)][d]) : 1.f;
         const float2 f2 = STATE ? make_float2(f * vback, f * vback) : make_float2(f, f);
 #pragma unroll
         for (int x = 0; x < DK; x += 16) {

@@ -28,11 +28,16 @@ struct ChunkPipe {
   // where there are outputs that of P V.  One barrier for each stage, whose next phase
   // needs the producer's own load.
   static constexpr int kv_releases = STATE ? 1 : 2;
+  // Slots of the scales of the decayed V's columns (fp16).  Chunk c's are written once the
+  // first product of chunk c - 1 is through, which waited for the state warps to be through
+  // with chunk c - 1 - dh_bufs: they may still read those of the dh_bufs chunks before c.
+  static constexpr int scale_slots = STATE ? 4 : 2;
 
   DSA_PIPE_FN int stage(int c) { return (int)((unsigned)c % stages); }
   DSA_PIPE_FN uint32_t stage_phase(int c) { return (unsigned)c / stages & 1u; }
   DSA_PIPE_FN int dh(int c) { return (int)((unsigned)c % dh_bufs); }
   DSA_PIPE_FN uint32_t dh_phase(int c) { return (unsigned)c / dh_bufs & 1u; }
+  DSA_PIPE_FN int scale(int c) { return (int)((unsigned)c % scale_slots); }
   DSA_PIPE_FN int v(int g) { return (int)((unsigned)g % v_bufs); }
   DSA_PIPE_FN bool v_first(int c, int g) { return c == 0 && g < v_bufs; }   // the buffer's first use
   // Phase of use (c, g), and of the buffer's use before it.

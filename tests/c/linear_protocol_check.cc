@@ -116,8 +116,9 @@ Found explore(const Model& m, size_t* states) {
 }
 
 // The launch of the segments' end states.  `by_dh`: stages given back by the barriers of dH
-// instead of their own, which chunk c + 2 completes again without the producer.
-Model state_launch(int chunks, bool by_dh) {
+// instead of their own, which chunk c + 2 completes again without the producer.  `slots`
+// of the scales.
+Model state_launch(int chunks, bool by_dh, int slots = dsa::ChunkPipe<true>::scale_slots) {
   using P = dsa::ChunkPipe<true>;
   Model m;
   int full[P::stages], empty[P::stages], v_ready[P::v_bufs], v_free[P::v_bufs], dh_ready[P::dh_bufs], dh_free[P::dh_bufs];
@@ -125,12 +126,15 @@ Model state_launch(int chunks, bool by_dh) {
   for (int i = 0; i < P::stages; ++i) full[i] = m.bar(1), empty[i] = m.bar(P::kv_releases), kv[i] = m.buffer();
   for (int i = 0; i < P::v_bufs; ++i) v_ready[i] = m.bar(1), v_free[i] = m.bar(1), vt[i] = m.buffer();
   for (int i = 0; i < P::dh_bufs; ++i) dh_ready[i] = m.bar(1), dh_free[i] = m.bar(1), dh[i] = m.buffer();
+  std::vector<int> scale(slots);
+  for (int& i : scale) i = m.buffer();
   const int producer = m.role(), issuer = m.role(), tensor = m.role(), state = m.role();
   int land[P::stages], decay[3];
   for (int& r : land) r = m.role();
   for (int& r : decay) r = m.role();
   for (int c = 0; c < chunks; ++c) {
     const int s = P::stage(c), d = P::dh(c);
+    const int scaled = scale[slots == P::scale_slots ? P::scale(c) : c % slots];
     Step& load = m.add(producer);
     if (c >= P::stages) {
       const int last = c - P::stages;
@@ -153,6 +157,7 @@ Model state_launch(int chunks, bool by_dh) {
       if (!P::v_first(c, g)) w.bar = v_free[b], w.parity = P::v_phase_before(c, g);
       w.reads = {{kv[s], c}};
       w.writes = {{vt[b], 4 * c + g}};
+      if (g == 0) w.writes.push_back({scaled, c});
       w.arrives = {v_ready[b]};
       Step& issue = m.add(issuer);
       issue.bar = v_ready[b], issue.parity = P::v_phase(c, g);
@@ -166,7 +171,7 @@ Model state_launch(int chunks, bool by_dh) {
     Step& r = m.add(state);
     r.bar = dh_ready[d], r.parity = P::dh_phase(c);
     Step& takes = m.add(state);
-    takes.reads = {{dh[d], c}};
+    takes.reads = {{dh[d], c}, {scaled, c}};
     takes.arrives = {dh_free[d]};
   }
   return m;
@@ -190,6 +195,7 @@ void expect(const char* what, const Model& m, Found want) {
 int main() {
   expect("states' launch", state_launch(7, false), kFine);
   expect("states' launch, stages given back by the barriers of dH", state_launch(7, true), kStuck);
+  expect("states' launch, two slots of scales", state_launch(7, false, 2), kWrongRead);
   if (!failed) std::printf("all ok\n");
   return failed != 0;
 }
