@@ -76,7 +76,8 @@ struct ChunkParams {
 
 struct __align__(16) Shared {
   uint64_t q_full[kStages], kv_full[kStateStages], q_empty[kStages], kv_empty[kStateStages];
-  uint64_t s_ready, o_staged, qh_ready, h_ready, p_ready, o_ready, o_free, tail, done1, done2;
+  uint64_t o_staged[ChunkPipe<false>::o_tiles];
+  uint64_t s_ready, qh_ready, h_ready, p_ready, o_ready, o_free, tail, done1, done2;
   uint64_t dh_ready[2], dh_free[2];
   uint64_t v_ready[4], v_free[4], pair[4];
   uint32_t tmem;
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       mbar_init(smem_u32(&sh->v_free[i]), 1);
     }
     mbar_init(smem_u32(&sh->s_ready), 1);
-    mbar_init(smem_u32(&sh->o_staged), 8);
+    for (int i = 0; i < ChunkPipe<false>::o_tiles; ++i) mbar_init(smem_u32(&sh->o_staged[i]), 8);
     mbar_init(smem_u32(&sh->qh_ready), 1);
     mbar_init(smem_u32(&sh->h_ready), DV / 32);
     mbar_init(smem_u32(&sh->p_ready), 8);
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       // ---------------------------------------------------------- output tiles
       if (lane == 0) {
         for (int c = 0; c < chunks - (ragged ? 1 : 0); ++c) {
-          if (!wait_bar(bar(sh->o_staged), c & 1, wc)) break;
+          if (!wait_bar(bar(sh->o_staged[Pipe::stage(c)]), phase(c), wc)) break;
           for (int x = 0; x < VC; ++x)
             tma_store_2d(&p.to, h * DV + x * 64, t0 + c * kC, smem_u32(stage(c) + x * kChunkBytes));
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(sh->o_free));
-        if (whole) mbar_arrive(bar(sh->o_staged));
+        if (whole) mbar_arrive(bar(sh->o_staged[Pipe::stage(c)]));
       }
     }
    } else if ((STATE || warp >= 12) && quad * 32 < DV) {

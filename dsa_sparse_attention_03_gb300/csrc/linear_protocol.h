@@ -28,6 +28,9 @@ struct ChunkPipe {
   // where there are outputs that of P V.  One barrier for each stage, whose next phase
   // needs the producer's own load.
   static constexpr int kv_releases = STATE ? 1 : 2;
+  // Barriers for the output tiles that wait for their store, one for each stage whose Q
+  // tile they lie in: the next tile there needs the stage that the store gives back.
+  static constexpr int o_tiles = STATE ? 0 : stages;
   // Slots of the scales of the decayed V's columns (fp16).  Chunk c's are written once the
   // first product of chunk c - 1 is through, which waited for the state warps to be through
   // with chunk c - 1 - dh_bufs: they may still read those of the dh_bufs chunks before c.

@@ -177,6 +177,96 @@ Model state_launch(int chunks, bool by_dh, int slots = dsa::ChunkPipe<true>::sca
   return m;
 }
 
+// The launch of the outputs.  `tiles` barriers for the staged output tiles, in turn.
+Model output_launch(int chunks, int tiles) {
+  using P = dsa::ChunkPipe<false>;
+  constexpr int kStaged = 100;   // an output tile over chunk c's Q holds kStaged + c
+  Model m;
+  int kv_full[P::stages], kv_empty[P::stages], q_full[P::stages], q_empty[P::stages], kv[P::stages], q[P::stages];
+  int v_ready[P::v_bufs], v_free[P::v_bufs], vt[P::v_bufs], scale[P::scale_slots];
+  for (int i = 0; i < P::stages; ++i) {
+    kv_full[i] = m.bar(1), kv_empty[i] = m.bar(P::kv_releases), q_full[i] = m.bar(1), q_empty[i] = m.bar(1);
+    kv[i] = m.buffer(), q[i] = m.buffer();
+  }
+  for (int i = 0; i < P::v_bufs; ++i) v_ready[i] = m.bar(1), v_free[i] = m.bar(1), vt[i] = m.buffer();
+  for (int& i : scale) i = m.buffer();
+  std::vector<int> staged(tiles);
+  for (int& i : staged) i = m.bar(1);
+  const int s_ready = m.bar(1), qh_ready = m.bar(1), h_ready = m.bar(1), p_ready = m.bar(1), o_ready = m.bar(1);
+  const int o_free = m.bar(1), dh_ready = m.bar(1), dh_free = m.bar(1);
+  const int sp = m.buffer(), o = m.buffer(), hb = m.buffer(), dh = m.buffer();   // S and P, O, H, dH
+  const int producer = m.role(), out = m.role(), out_tensor = m.role(), delta = m.role(), delta_tensor = m.role();
+  const int rows = m.role(), decay = m.role(), state = m.role(), store = m.role();
+  int kv_land[P::stages], q_land[P::stages];
+  for (int i = 0; i < P::stages; ++i) kv_land[i] = m.role(), q_land[i] = m.role();
+  auto wait = [&](int r, int bar, uint32_t parity) -> Step& {
+    Step& s = m.add(r);
+    s.bar = bar, s.parity = parity;
+    return s;
+  };
+  auto follows = [&](int r, int other) -> Step& {   // behind what `other` has done so far
+    Step& s = m.add(r);
+    s.role = other, s.behind = m.at(other);
+    return s;
+  };
+  for (int c = 0; c < chunks; ++c) {
+    const int s = P::stage(c), last = c - P::stages;
+    const uint32_t odd = (uint32_t)c & 1u;
+    Step& k_load = m.add(producer);
+    if (c >= P::stages) k_load.bar = kv_empty[s], k_load.parity = P::stage_phase(last);
+    k_load.writes = {{kv[s], c}};
+    follows(kv_land[s], producer).arrives = {kv_full[s]};
+    Step& q_load = m.add(producer);
+    if (c >= P::stages) q_load.bar = q_empty[s], q_load.parity = P::stage_phase(last);
+    q_load.writes = {{q[s], c}};
+    follows(q_land[s], producer).arrives = {q_full[s]};
+
+    wait(out, kv_full[s], P::stage_phase(c));
+    wait(out, q_full[s], P::stage_phase(c));
+    Step& ends_s = follows(out_tensor, out);
+    ends_s.reads = {{kv[s], c}, {q[s], c}}, ends_s.writes = {{sp, c}}, ends_s.arrives = {s_ready};
+    wait(out, h_ready, odd);
+    if (c > 0) wait(out, o_free, odd ^ 1u);
+    Step& ends_h = follows(out_tensor, out);
+    ends_h.reads = {{q[s], c}, {hb, c}}, ends_h.writes = {{o, c}}, ends_h.arrives = {qh_ready};
+    wait(out, p_ready, odd);
+    Step& ends_p = follows(out_tensor, out);
+    ends_p.reads = {{kv[s], c}, {sp, kStaged + c}, {o, kStaged + c}};
+    ends_p.writes = {{o, c}}, ends_p.arrives = {o_ready, kv_empty[s]};
+
+    wait(rows, s_ready, odd).reads = {{sp, c}};
+    Step& p = wait(rows, qh_ready, odd);
+    p.reads = {{o, c}}, p.writes = {{sp, kStaged + c}, {o, kStaged + c}}, p.arrives = {p_ready};
+    Step& tile = wait(rows, o_ready, odd);
+    tile.reads = {{o, c}}, tile.writes = {{q[s], kStaged + c}};
+    tile.arrives = {o_free, staged[c % tiles]};
+    wait(store, staged[c % tiles], (uint32_t)(c / tiles) & 1u);
+    Step& stored = m.add(store);
+    stored.reads = {{q[s], kStaged + c}}, stored.arrives = {q_empty[s]};
+
+    if (c > 0) wait(delta, dh_free, P::dh_phase(c - 1));
+    for (int g = 0; g < 4; ++g) {
+      const int b = P::v(g);
+      if (g == 0) wait(decay, kv_full[s], P::stage_phase(c));
+      Step& w = m.add(decay);
+      if (!P::v_first(c, g)) w.bar = v_free[b], w.parity = P::v_phase_before(c, g);
+      w.reads = {{kv[s], c}}, w.writes = {{vt[b], 4 * c + g}}, w.arrives = {v_ready[b]};
+      if (g == 0) w.writes.push_back({scale[P::scale(c)], c});
+      wait(delta, v_ready[b], P::v_phase(c, g));
+      Step& ends = follows(delta_tensor, delta);
+      ends.reads = {{kv[s], c}, {vt[b], 4 * c + g}}, ends.writes = {{dh, g < 3 ? 254 : c}}, ends.arrives = {v_free[b]};
+      if (g == 3) ends.arrives.insert(ends.arrives.end(), {dh_ready, kv_empty[s]});
+    }
+    Step& h = m.add(state);
+    if (c > 0) h.bar = qh_ready, h.parity = odd ^ 1u;
+    h.writes = {{hb, c}}, h.arrives = {h_ready};
+    wait(state, dh_ready, P::dh_phase(c));
+    Step& takes = m.add(state);
+    takes.reads = {{dh, c}, {scale[P::scale(c)], c}}, takes.arrives = {dh_free};
+  }
+  return m;
+}
+
 int failed = 0;
 void expect(const char* what, const Model& m, Found want) {
   if (m.roles.size() + m.buffers > kMax) {
@@ -196,6 +286,8 @@ int main() {
   expect("states' launch", state_launch(7, false), kFine);
   expect("states' launch, stages given back by the barriers of dH", state_launch(7, true), kStuck);
   expect("states' launch, two slots of scales", state_launch(7, false, 2), kWrongRead);
+  expect("outputs' launch", output_launch(5, dsa::ChunkPipe<false>::o_tiles), kFine);
+  expect("outputs' launch, one barrier for the staged output tiles", output_launch(5, 1), kStuck);
   if (!failed) std::printf("all ok\n");
   return failed != 0;
 }
