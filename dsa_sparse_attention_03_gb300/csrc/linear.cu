@@ -232,11 +232,13 @@ __device__ __forceinline__ float2 widen(uint32_t p) {
 }
 
 // The power of two that takes m >= 0 into [2^14, 2^15), and its inverse: values of
-// which m is the largest then fit fp16, and only those below 2^-28 of it lose
-// precision (fp16 is normal from 2^-14 on).  1 where m is 0, tiny or not finite.
+// which m is the largest then fit fp16.  Rounded to it, those below 2^-28 of m (fp16 is
+// normal from 2^-14 on) are off by 2^-39 m; split into two terms, those from 2^-17 of m on
+// keep 22 bits and those below are off by 2^-39 m.  1 where m is 0, below 2^-112 or not
+// finite.
 __device__ __forceinline__ float half_range(float m, float* back) {
   const uint32_t e = (__float_as_uint(m) >> 23) & 255u;
-  if (e < 32 || e > 252) {
+  if (e < 15 || e > 252) {
     *back = 1.f;
     return 1.f;
   }
@@ -644,32 +646,34 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
       const float* fade = pw + m - 1;          // fade[-j] = lambda^(m-1-j), 0 behind the last token
       float vf[4] = {1.f, 1.f, 1.f, 1.f};
       float vback[4];
-      if (F16) {                               // the columns of V brought into fp16's range
+      if (F16) {
+        // The columns of the decayed V brought into fp16's range.  (Of V as it is, an early
+        // token that a fast head has forgotten would push those that count out of it.)
+        float mx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {
-          float mx[2] = {0.f, 0.f};
-#pragma unroll 1
-          for (int j = 0; j < kC; j += 16) {
+        for (int j = 0; j < kC; j += 16) {
+          float2 fd[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int at = j + 8 * y + 2 * (lane & 3);
+            fd[y] = make_float2(fade[-at], fade[-at - 1]);
+          }
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
             uint32_t r[4];
             blocks(j, hh, r);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const float2 x = widen<F16>(r[y]);
-              mx[y & 1] = fmaxf(mx[y & 1], fmaxf(fabsf(x.x), fabsf(x.y)));
+              const float2 x = mul2(widen<F16>(r[y]), fd[y >> 1]);
+              mx[hh * 2 + (y & 1)] = max3(mx[hh * 2 + (y & 1)], fabsf(x.x), fabsf(x.y));
             }
           }
+        }
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 1));
-            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 2));
-          }
-          if (hh == 0) {
-            vf[0] = half_range(mx[0], &vback[0]);
-            vf[1] = half_range(mx[1], &vback[1]);
-          } else {
-            vf[2] = half_range(mx[0], &vback[2]);
-            vf[3] = half_range(mx[1], &vback[3]);
-          }
+        for (int y = 0; y < 4; ++y) {
+          mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 1));
+          mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 2));
+          vf[y] = half_range(mx[y], &vback[y]);
         }
       }
 #pragma unroll 1

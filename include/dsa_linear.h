@@ -30,7 +30,9 @@
  *
  * Precision: q, k, v bf16 (or fp16 with DSA_FLAG_FP16).  The state is held,
  * updated and returned in fp32: in the chunked form each decayed v is split into
- * 16-bit terms that together keep 24 bits (bf16: three) or 22 (fp16: two).  The
+ * 16-bit terms that together keep 24 bits (bf16: three) or 22 (fp16: two, scaled for
+ * each column and chunk: 22 bits of what is at least 2^-17 of the column's largest
+ * decayed v there, 2^-39 of the latter below).  The
  * decayed products (q . k) and the state that a chunk's queries read are rounded
  * to the operands' type for their matrix products (fp16: scaled into its range by
  * powers of two), sums are fp32, and the output is rounded once.  dsa_linear_step

@@ -45,3 +45,47 @@ def test_segments_with_columns_that_change_by_chunk(dk, dv, with_state):
     chunks = -(-n // H.C)
     assert bool((err <= A * 2.0 ** -23 * (48 + 4 * chunks) + 1e-37).all()), (err / A).max()
     assert torch.isfinite(out.float()).all()
+
+
+def two_terms(t, b=0):
+    """What the fp16 operands of the state's update cost, per value of S: sum over chunks c
+    of lam^(tokens behind c) 2^-39 M sum_j |k_j|, M the largest lam^(m-1-j) |v_j| of a column
+    in the chunk.
+
+    A decayed value x is split into two fp16 terms after a scaling by a power of two that takes
+    M into [2^14, 2^15).  The first is off by at most 2^-11 |x|, which the second holds to
+    2^-11 of itself, or to half of fp16's smallest step, 2^-25, where it is below
+    2^-14: 2^-22 |x| (22 bits, in the harness's bound) or 2^-25 <= 2^-39 M.
+    """
+    import torch
+    lo, hi = t["row_offsets"][b:b + 2].tolist()
+    k, v = t["k"][lo:hi].double().abs(), t["v"][lo:hi].double().abs()
+    lam = torch.exp(t["log_decay"].double().clamp(max=0.0))
+    n = hi - lo
+    extra = torch.zeros(k.shape[1], k.shape[2], v.shape[2], dtype=torch.float64)
+    for c in range(0, n, H.C):
+        m = min(H.C, n - c)
+        w = lam[None] ** torch.arange(m - 1, -1, -1)[:, None]
+        M = (w[..., None] * v[c:c + m]).amax(dim=0)
+        extra += (lam ** (n - c - m))[:, None, None] * 2.0 ** -39 * k[c:c + m].sum(dim=0)[..., None] * M[:, None]
+    return extra
+
+
+@pytest.mark.parametrize("dk,dv", W)
+@pytest.mark.parametrize("n,heads", [(300, 2), (2000, 38)])
+def test_an_early_outlier_that_is_forgotten(dk, dv, n, heads):
+    # The first token of every chunk has the largest fp16 values, the others are about 2^-26 of
+    # them, and fast heads forget it within the chunk: the others are the state, and enter it
+    # with as many bits as ever.  In one walk (300 tokens) and in segments of four chunks.
+    import torch
+    t, s0 = H.make([n], heads, dk, dv, "fp16", seed=43, amp=1e-3)
+    t["k"] = torch.randn(n, heads, dk, generator=torch.Generator().manual_seed(44)).half()
+    t["v"][::H.C] = torch.where(t["v"][::H.C] < 0, -6e4, 6e4).half()
+    t["log_decay"] = torch.linspace(-1.5, -0.2, heads)
+    out, state, bits = H.run(t, s0, 0.1)
+    assert bits == 0
+    S, A = end_state(t, s0)
+    err = (state[0].double() - S).abs()
+    chunks = -(-n // H.C)
+    bound = A * 2.0 ** -23 * (48 + 4 * chunks) + two_terms(t) + 1e-37
+    assert bool((err <= bound).all()), f"state off by {(err / bound).max():.3g} x its bound"
