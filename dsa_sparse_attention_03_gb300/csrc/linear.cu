@@ -87,7 +87,7 @@ struct __align__(16) Shared {
   int place, scratch;
   __align__(16) float pw[2 * kC + 4];            // pw[128 + e] = lambda^e for e = 0 .. 128, 0 for e < 0
   float column[32];                // lambda^(31-y)
-  unsigned char mx[2][128];        // fp16: exponent fields of the two halves' largest |S| of each row
+  unsigned char mx[2][128];        // fp16: exponent fields of the two halves' largest weight of each row
   unsigned char cs[2][128];        // fp16: scale of each column of H as Q H read it (a power of two's exponent field)
   unsigned char vs[ChunkPipe<true>::scale_slots][128];   // fp16: the same of each column of the decayed V
 };
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     const int half = (warp >> 2) - 1;   // this thread's blocks of 32 columns: half, half + 2
     const int i = quad * 32 + lane;     // token of the chunk
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const float reach = pw[i + 1] * a.scale;
+    const float reach = F16 ? pw[i + 1] : pw[i + 1] * a.scale;
     uint32_t turn = 0;                  // (fp16)
     auto pair_sync = [&]() -> bool {    // the rows' two warps meet
       __syncwarp();
@@ -497,7 +497,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     for (int c = 0; c < chunks; ++c) {
       if (!wait_bar_warp(bar(sh->s_ready), c & 1, wc)) break;
       tc_fence_after();
-      float pf = 1.f, pback = 1.f;       // fp16: the row of P brought into its range
+      // The weights of a block of S, over it: S_ij lambda^(i-j) times f0.
+      auto weigh = [&](int x, uint32_t* s, float f0) {
+        if (x < quad) {
+          // Every column lies before the row: lambda^(i-j) = lambda^(i-e) lambda^(e-j)
+          // with e the block's last column, one power per thread, one per column.
+          const float f = f0 * pw[i - (x * 32 + 31)];
+          const float4* w = reinterpret_cast<const float4*>(sh->column);
+#pragma unroll
+          for (int y = 0; y < 32; y += 4) {
+            const float4 e = w[y >> 2];
+            const float2 u = mul2(mul2(make_float2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), make_float2(f, f)), make_float2(e.x, e.y));
+            const float2 v = mul2(mul2(make_float2(__uint_as_float(s[y + 2]), __uint_as_float(s[y + 3])), make_float2(f, f)), make_float2(e.z, e.w));
+            s[y] = __float_as_uint(u.x);
+            s[y + 1] = __float_as_uint(u.y);
+            s[y + 2] = __float_as_uint(v.x);
+            s[y + 3] = __float_as_uint(v.y);
+          }
+        } else {
+          // The diagonal's block (the table is 0 where the column lies behind the row;
+          // what S holds there may be anything, so it is also replaced).
+          const float* w = pw + lane;
+#pragma unroll
+          for (int y = 0; y < 32; ++y) s[y] = __float_as_uint((y <= lane ? __uint_as_float(s[y]) : 0.f) * (f0 * w[-y]));
+        }
+      };
+      // fp16: the weights go back over S in fp32, and the row is brought into fp16's range
+      // by the largest of them.  (By the largest of S, an early key that a fast head has
+      // forgotten would push the weights that count out of it.)  The scale waits for the output.
+      float pf = 1.f, pback = 1.f;
       if (F16) {
         float mx = 0.f;
 #pragma unroll 1
@@ -505,17 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           uint32_t s[32];
           tmem_ld32(lanes + kColS + x * 32, s);
           tmem_wait_ld();
+          weigh(x, s, 1.f);
 #pragma unroll
-          for (int y = 0; y < 32; ++y) {
-            const float v = x * 32 + y <= i ? fabsf(__uint_as_float(s[y])) : 0.f;
-            mx = fmaxf(mx, v);
-          }
+          for (int y = 0; y < 32; y += 2) mx = max3(mx, fabsf(__uint_as_float(s[y])), fabsf(__uint_as_float(s[y + 1])));
+          tmem_st32(lanes + kColS + x * 32, s);
         }
-        sh->mx[half][i] = exponent_field(mx * fabsf(a.scale));
+        tmem_wait_st();
+        sh->mx[half][i] = exponent_field(mx);
         if (!pair_sync()) break;
         pf = half_range(exponent_value(max(sh->mx[0][i], sh->mx[1][i])), &pback);
+        pback *= a.scale;
       }
-      const float ps = a.scale * pf;
       // (Rolled loops: the groups' code has to fit the instruction cache together.)
 #pragma unroll 1
       for (int x = half; x < 4; x += 2) {   // P of a block goes over the first half of its S
@@ -523,30 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         if (x <= quad) {
           tmem_ld32(lanes + kColS + x * 32, s);
           tmem_wait_ld();
-        }
-        if (x < quad) {
-          // Every column lies before the row: lambda^(i-j) = lambda^(i-e) lambda^(e-j)
-          // with e the block's last column, one power per thread, one per column.
-          const float f = ps * pw[i - (x * 32 + 31)];
-          const float4* w = reinterpret_cast<const float4*>(sh->column);
+          if (!F16) weigh(x, s, a.scale);
 #pragma unroll
-          for (int y = 0; y < 32; y += 4) {
-            const float4 e = w[y >> 2];
-            const float2 u = mul2(mul2(make_float2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), make_float2(f, f)), make_float2(e.x, e.y));
-            const float2 v = mul2(mul2(make_float2(__uint_as_float(s[y + 2]), __uint_as_float(s[y + 3])), make_float2(f, f)), make_float2(e.z, e.w));
-            s[y >> 1] = pack16<F16>(u.x, u.y);
-            s[(y >> 1) + 1] = pack16<F16>(v.x, v.y);
-          }
-        } else if (x == quad) {
-          // The diagonal's block (the table is 0 where the column lies behind the row;
-          // what S holds there may be anything, so it is also replaced).
-          const float* w = pw + lane;
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            const float s0 = y <= lane ? __uint_as_float(s[y]) : 0.f;
-            const float s1 = y + 1 <= lane ? __uint_as_float(s[y + 1]) : 0.f;
-            s[y >> 1] = pack16<F16>(s0 * (ps * w[-y]), s1 * (ps * w[-y - 1]));
-          }
+          for (int y = 0; y < 32; y += 2)
+            s[y >> 1] = pack16<F16>(__uint_as_float(s[y]) * pf, __uint_as_float(s[y + 1]) * pf);
         } else {
 #pragma unroll
           for (int y = 0; y < 16; ++y) s[y] = 0;

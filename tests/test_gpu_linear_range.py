@@ -89,3 +89,57 @@ def test_an_early_outlier_that_is_forgotten(dk, dv, n, heads):
     chunks = -(-n // H.C)
     bound = A * 2.0 ** -23 * (48 + 4 * chunks) + two_terms(t) + 1e-37
     assert bool((err <= bound).all()), f"state off by {(err / bound).max():.3g} x its bound"
+
+
+def output_bound(t, s0, scale, out):
+    """How far an fp16 output may be off (one request): the harness's bound with the two terms
+    of fp16's range taken from what is rounded.  A row of P = lam^(i-j) q_i . k_j and a
+    column of the state are scaled so that their largest lies in [2^14, 2^15), and rounded to
+    11 bits (u of each), or by half of fp16's smallest step, 2^-25 <= 2^-39 of the largest."""
+    import torch
+    u, C = 2.0 ** -11, H.C
+    q, k, v = (t[x].double() for x in "qkv")
+    lam = torch.exp(t["log_decay"].double().clamp(max=0.0))
+    n = q.shape[0]
+    S = s0[0].double() if s0 is not None else torch.zeros(*q.shape[1:], v.shape[2], dtype=torch.float64)
+    bound = 1.01 * u * out.abs() + 2.0 ** -25
+    for c in range(0, n, C):
+        m, x = min(C, n - c), slice(c, min(c + C, n))
+        w = torch.arange(m)[:, None] - torch.arange(m)[None]
+        D = torch.where(w >= 0, lam[:, None, None] ** w.clamp(min=0), torch.zeros((), dtype=torch.float64))
+        s = D * torch.einsum("ihd,jhd->hij", q[x], k[x]).abs()
+        sa = D * torch.einsum("ihd,jhd->hij", q[x].abs(), k[x].abs())
+        low = 2.0 ** -39 * s.amax(dim=2, keepdim=True) * (w >= 0)
+        bound[x] += abs(scale) * torch.einsum("hij,jhe->ihe", 1.01 * u * s + 2.0 ** -17 * sa + low, v[x].abs())
+        reach = lam[None] ** (torch.arange(m)[:, None] + 1)
+        col = 1.01 * (u + 2.0 ** -15) * S.abs() + 2.0 ** -39 * S.abs().amax(dim=1, keepdim=True)
+        bound[x] += abs(scale) * reach[..., None] * torch.einsum("ihd,hde->ihe", q[x].abs(), col)
+        dec = lam[:, None] ** (m - 1 - torch.arange(m))[None]
+        S = lam[:, None, None] ** m * S + torch.einsum("hj,jhd,jhe->hde", dec, k[x], v[x])
+    return bound
+
+
+@pytest.mark.parametrize("dk,dv", W)
+@pytest.mark.parametrize("scale", [100.0, -3e4, 1e-25])
+@pytest.mark.parametrize("with_state", [False, True])
+def test_an_early_key_that_is_forgotten(dk, dv, scale, with_state):
+    # The first key of every chunk is about 2^31 times the others, and the heads forget it in a few
+    # tokens to a few dozen: later rows' weights are the others', in full precision.  Some keys are zero,
+    # so that a row's largest weight may lie anywhere.
+    import torch
+    n, heads = 300, 6
+    t, s0 = H.make([n], heads, dk, dv, "fp16", seed=45, state=with_state)
+    g = torch.Generator().manual_seed(46)
+    t["k"] = (torch.randn(n, heads, dk, generator=g) * 2e-5).half()
+    t["k"][::H.C] = torch.where(t["k"][::H.C] < 0, -6e4, 6e4).half()
+    t["k"][torch.rand(n, generator=g) < 0.3] = 0.0
+    if s0 is not None:
+        s0 = s0 * 1e-4
+    t["log_decay"] = torch.tensor([-20.0, -3.0, -1.5, -1.0, -0.7, -0.5])
+    out, state, bits = H.run(t, s0, scale)
+    assert bits == 0
+    ref = H.reference(t, s0, scale)[0][0]
+    fits = ref.abs() < 6e4                         # (behind an outlier, outputs overflow fp16)
+    bound = output_bound(t, s0, scale, ref)
+    err = (out.double() - ref).abs()
+    assert bool((err <= bound)[fits].all()), f"output off by {(err / bound)[fits].max():.3g} x its bound"
