@@ -5,9 +5,11 @@
 //   m' = max(m, max_t s_t),  p_t = 2^(c s_t - c m'),
 //   l = l 2^(c m - c m') + sum p_t,   O = O 2^(c m - c m') + P V,
 // and out = O / l, lse = scale * m + ln l.  m only has to be near the maximum:
-// O and l are rescaled when the maximum has grown by more than 2^8 (p <= 256
-// then, exact enough in 16 bits whose precision is relative), which after a
-// row's first tiles hardly ever happens.
+// O and l are rescaled when the maximum has grown by more than 2^8, which after a
+// row's first tiles hardly ever happens.  bf16 holds p as exactly whatever its size.
+// fp16 does not: there p is 2^7 times as large (at most 2^15; its range ends at 2^16),
+// so that weights down to 2^-21 of the largest keep their 11 bits and smaller ones are off by
+// 2^-32 of it.  A tail of 10^5 positions 2^-25 below the peak counts (it vanished without).
 //
 // Rows.  The G = H_q / H_kv query heads of one K/V head and the rows of one
 // request are packed into one axis (packed row = row * G + head in group), so a
@@ -63,6 +65,9 @@ namespace dsa {
 namespace {
 
 constexpr int kTile = 128;
+// The softmax weights are held as 2^lift of them.
+template <bool F16>
+constexpr float kLift = F16 ? 7.f : 0.f;
 
 struct DenseArgs {
   CUtensorMap tq, tk, tv;
@@ -73,7 +78,7 @@ struct DenseArgs {
   uint16_t* out;
   float* lse;
   float* part;      // [R * H_q, splits, D_v] (tail: [rows of the tail's tiles, tail_parts, D_v])
-  float2* ml;       // the same without D_v: (c m, l)
+  float2* ml;       // the same without D_v: (c m - lift, l)
   uint32_t* status;
   uint32_t* next;   // items taken beyond the grid (zeroed with the status)
   uint32_t* bits;   // status bits of each CTA, joined with the parts; or null: the status is cleared before, and raised
@@ -638,7 +643,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
           for (int x = 0; x < 4; ++x) t[x] = fmaxf(t[x], __uint_as_float(v[124 + x]));
           const float mn = fmaxf(max3(m, t[0], t[1]), fmaxf(t[2], t[3]));
           if (jj == 0) m = mn;
-          float mc = m == -INFINITY ? 0.f : m * a.c;
+          float mc = m == -INFINITY ? 0.f : fmaf(m, a.c, -kLift<F16>);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           auto weights = [&](int half) {
 #pragma unroll
@@ -657,7 +662,7 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
             // S of this tile was issued after O += P V of the previous one, so O is still.
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * a.c);
             m = mn;
-            mc = m == -INFINITY ? 0.f : m * a.c;
+            mc = m == -INFINITY ? 0.f : fmaf(m, a.c, -kLift<F16>);
             l *= f;
 #pragma unroll 1
             for (int x = 0; x < DV; x += 32) {
@@ -708,8 +713,8 @@ __global__ void __launch_bounds__(128 + 128 * NW, NW == 1 ? 2 : 1)
         // keeps it, a row that sees nothing gets zeros.
         const float inv = some ? 1.f / l : 0.f;
         const int at_row = valid ? (int)rh : -1;   // (below 2^23: 65535 rows of 128 heads)
-        if (valid && parts > 1) a.ml[at] = make_float2(m * a.c, some ? l : 0.f);
-        if (valid && parts == 1 && a.lse) a.lse[rh] = some ? m * a.scale + logf(l) : -INFINITY;
+        if (valid && parts > 1) a.ml[at] = make_float2(fmaf(m, a.c, -kLift<F16>), some ? l : 0.f);
+        if (valid && parts == 1 && a.lse) a.lse[rh] = some ? m * a.scale + logf(F16 ? l * 0x1p-7f : l) : -INFINITY;
         if (parts == 1 || __any_sync(0xffffffffu, some)) {
 #pragma unroll 1
           for (int x = 0; x < DV; x += 32) {

@@ -21,7 +21,8 @@
  *
  * Precision: operands bf16 (or fp16 with DSA_FLAG_FP16), products and sums in
  * fp32, softmax statistics in fp32, the softmax weights rounded to the
- * operands' type for their product with V, the output rounded once to the
+ * operands' type for their product with V (fp16: those below 2^-21 of a row's largest
+ * to multiples of 2^-31 of it), the output rounded once to the
  * operands' type.  Results do not depend on timing.
  *
  * What a masked position holds does not matter where no row of the call's tile
