@@ -875,10 +875,17 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
     // 255 with sixteen).  Prompts: two where the row tiles alone leave SMs idle.
     const int64_t each = s.nw == 1 ? 8 : 2;
     if (items < each * slots) splits = (each * slots + items - 1) / items;
-    // Finer parts than one a slot only of sixteen tiles, and from 8192 positions on (one
-    // of 32768 positions and seven of 500: 50 us, 69 with parts of 32 tiles; eight of
-    // 32768: 179 and 166; 64 of 4096: 158 in one part, 168 in two).
-    const int64_t wave = slots / items > 1 ? slots / items : 1, fine = kvt >= 64 ? kvt / 16 : 1;
+    // Finer parts than one a slot only of sixteen tiles, and from 5000 positions on.  The
+    // host does not know whether the lengths are alike: parts cost where they are, and
+    // where they are not one request is walked when the others are done.  Single tokens
+    // of 64 heads over 8, in one part and with this rule (us):
+    //   longest                                 4096      5000      6144      8000
+    //   64 requests, all of it                158 169   196 207   231 246   301 318
+    //   64, spread from 64 on                  74  68    84  76    92  74   113  88
+    //   32, one of it and 31 of 100            47  40    57  45    66  41    85  49
+    // (one of 32768 and seven of 500: 50, and 69 with parts of 32 tiles; eight of 32768: 179
+    // and 166).
+    const int64_t wave = slots / items > 1 ? slots / items : 1, fine = kvt >= 40 ? kvt / 16 : 1;
     if (splits > wave && splits > fine) splits = wave > fine ? wave : fine;
   }
   if (splits > cap) splits = cap;

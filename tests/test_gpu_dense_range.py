@@ -1,5 +1,5 @@
-"""Dense attention in fp16 on the GPU where most of what counts has small weights, against the
-definition in 64 bits."""
+"""Dense attention on the GPU where most of what counts has small weights (fp16), and where one
+request is much longer than the others, against the definition in 64 bits."""
 import pytest
 
 import dense_harness as H
@@ -91,3 +91,13 @@ def test_a_long_context_with_one_peak():
         err = (out.cpu().double() - o).abs()
         assert bool((err <= bound).all()), f"output off by {(err / bound).max():.3g} x its bound (split {split})"
         assert bool(((lse.cpu().double() - l).abs() <= lb).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_one_long_request_among_short_ones(dtype):
+    # More items than the GPU has slots for, of which the long request's are cut.
+    rows, lens = [1] * 40, [100, 6000] + [(13 * i) % 90 for i in range(38)]
+    t = H.make(rows, lens, 64, 8, 128, 128, dtype, seed=53)
+    out, lse, bits = H.run(t, 0.09)
+    assert bits == 0
+    H.check(t, 0.09, out, lse)
