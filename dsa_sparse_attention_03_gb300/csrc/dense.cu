@@ -847,7 +847,9 @@ cudaError_t launch_width(const DenseArgs& a, int nw, bool f16, cudaStream_t st) 
 DenseShape dense_shape(const dsa_dense_problem& p) {
   DenseShape s;
   const int64_t G = p.H_q / p.H_kv;
-  const int64_t most = p.rows_max > 0 ? p.rows_max : p.R;
+  // The declared bounds may lie above what the call can hold.
+  const int64_t most = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
+  const int64_t longest = p.L_max < p.L_total ? p.L_max : p.L_total;
   s.nw = most * G <= kTile ? 1 : 2;
   const int64_t per = (int64_t)s.nw * kTile;
   int64_t tiles = p.B * ((most * G + per - 1) / per);
@@ -858,13 +860,13 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
   // sixteen): the parts' way through memory and the join have to pay.  Single tokens'
   // parts are small: 512 positions in two (9.8 us, 11.0 in one).
   const int64_t items = tiles * p.H_kv, slots = dense_slots(s.nw);
-  const int64_t kvt = (p.L_max + kTile - 1) / kTile;
+  const int64_t kvt = (longest + kTile - 1) / kTile;
   const int64_t cap = s.nw == 1 && kvt >= 4 && kvt < 8 ? 2 : (kvt / 4 < 64 ? kvt / 4 : 64);
   // Items of one length: one to an SM, or one to a slot where that leaves them eight
   // tiles (one token of 64 heads over 8 and 32768 positions: 35 us in 19 parts, 43 in
   // 38).  So are one request's, and prompts that fill a packed cache; single tokens of
   // several requests may not be, whatever the host knows of a cache laid out by capacity.
-  const int64_t full = (int64_t)p.B * p.L_max;
+  const int64_t full = p.B * longest;
   const bool even = p.B == 1 || (s.nw == 2 && p.L_total <= full && 4 * p.L_total >= 3 * full);
   int64_t splits = 1;
   if (items > 0 && items <= 152 && even) {
@@ -895,7 +897,7 @@ DenseShape dense_shape(const dsa_dense_problem& p) {
   // (2048 rows over 10240 positions, 512 items: 466 us without, 441 with).
   s.tail = s.tail_parts = 0;
   const int64_t rest = items % slots;
-  if (s.splits == 1 && s.nw == 2 && p.B == 1 && items > slots && rest > 0 && rest <= slots / 2 && 2 * ((int64_t)p.L_max - p.R) >= p.L_max) {
+  if (s.splits == 1 && s.nw == 2 && p.B == 1 && items > slots && rest > 0 && rest <= slots / 2 && 2 * (longest - p.R) >= longest) {
     s.tail = (int)rest;
     s.tail_parts = (int)(slots / rest < 4 ? slots / rest : 4);
   }

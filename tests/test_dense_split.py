@@ -33,3 +33,16 @@ def test_ragged_single_tokens_below_8192_positions_are_split(dsa, longest, reque
 
 def test_single_tokens_that_are_not_split(dsa):
     assert parts(dsa, R=64, B=64, L_max=4096, L_total=64 * 4096) == 1
+
+
+def test_declared_bounds_above_what_the_call_holds(dsa):
+    # L_max and rows_max are upper bounds: the largest int32 (2^31 tiles of positions past 32
+    # bits) cuts the work as the true values do.
+    top = (1 << 31) - 1
+    for kw in (dict(R=1, B=1, L_total=32768), dict(R=32, B=32, L_total=8000), dict(R=700, B=1, rows_max=0, L_total=700),
+               dict(R=4, B=2, H_q=8, H_kv=8, rows_max=2, L_total=20000)):
+        n = parts(dsa, L_max=kw["L_total"], **kw)
+        assert parts(dsa, L_max=top, **kw) == n
+        if kw.get("rows_max") != 0:
+            assert parts(dsa, **dict(kw, L_max=top, rows_max=kw["R"])) == parts(dsa, **dict(kw, L_max=top, rows_max=top))
+    assert parts(dsa, R=1, B=1, L_total=32768, L_max=top) > 10
