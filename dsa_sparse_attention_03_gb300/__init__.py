@@ -215,6 +215,7 @@ class Problem:
     def __init__(self, **kw):
         self._keep = {}
         self._on = None      # device on which the tensors were found (_check_call)
+        self._fits = False   # whether the tensors were found to fit the sizes (_check_fits)
         s = self._struct()
         for f, _ in self._struct._fields_:
             v = kw.get(f)
@@ -248,7 +249,9 @@ class Problem:
                    row_offsets=row_offsets, row_len=row_len, kv_scale=kv_scale)
 
     def set(self, **kw):
+        """Changes fields: sizes, or tensors in the place of the problem's."""
         self._on = None
+        self._fits = False
         for f, v in kw.items():
             if hasattr(v, "data_ptr"):
                 self._keep[f] = v
@@ -257,7 +260,7 @@ class Problem:
         return self
 
     def __getattr__(self, name):
-        if name in ("c", "_keep", "_on", "_expect"):
+        if name in ("c", "_keep", "_on", "_fits", "_expect"):
             raise AttributeError(name)
         return getattr(self.c, name)
 
@@ -481,6 +484,34 @@ def _check_ints(n, **ts):
                              + (f" of {n[name]} entries" if n.get(name) is not None else ""))
 
 
+def _check_fits(prob, heads, ints, fixed=()):
+    """The problem's tensors against its sizes, which ``set`` may have changed apart: q, k and
+    v (name: heads, width, token stride, tokens at least), vectors of int32 (name: entries at least)
+    and others (name, dtype, shape)."""
+    if prob._fits:
+        return
+    for name, (h, d, stride, n) in heads.items():
+        t = prob._keep[name]
+        got = _head_tensor(name, t)
+        if got[:2] != (h, d) or t.shape[0] < n or (n > 1 and got[2] != (stride or h * d)):
+            raise ValueError(f"{name} of shape {tuple(t.shape)} and token stride {t.stride(0)} does not fit the problem: "
+                             f"{n} tokens of {h} heads of {d}, stride {stride or h * d}")
+    if _fp16_flag(**{x: prob._keep[x] for x in heads}) != prob.c.flags & DSA_FLAG_FP16:
+        raise ValueError(f"{', '.join(heads)} are not of the problem's type")
+    for name, n in ints.items():
+        t = prob._keep.get(name)
+        if t is None or getattr(prob.c, name) is None:
+            continue
+        _check_ints({}, **{name: t})
+        if t.shape[0] < n:
+            raise ValueError(f"{name} has {t.shape[0]} entries, the problem needs {n}")
+    for name, dtype, shape in fixed:
+        t = prob._keep[name]
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    prob._fits = True
+
+
 class DenseProblem(Problem):
     """Sizes plus device tensors of one dense attention call (include/dsa_dense.h).
 
@@ -516,6 +547,7 @@ class DenseProblem(Problem):
                    L_total=int(L_total), q_stride=q_stride, k_stride=k_stride, v_stride=v_stride,
                    softmax_scale=float(softmax_scale), flags=_fp16_flag(q=q, k=k, v=v), q=q, k=k, v=v,
                    offsets=offsets, row_offsets=row_offsets, row_len=row_len)
+        prob._fits = True
         return prob
 
 
@@ -536,6 +568,9 @@ def dsa_dense_attn(prob: DenseProblem, out, lse, ws, stream=None) -> None:
     import torch
     if prob._on is None:           # (new, or changed)
         c = prob.c
+        _check_fits(prob, dict(q=(c.H_q, c.D_k, c.q_stride, c.R), k=(c.H_kv, c.D_k, c.k_stride, c.L_total),
+                               v=(c.H_kv, c.D_v, c.v_stride, c.L_total)),
+                    dict(offsets=c.B + 1, row_offsets=c.B + 1, row_len=c.R))
         prob._expect = (ctypes.byref(c), (c.R, c.H_q, c.D_v), prob._keep["q"].dtype, (c.R, c.H_q))
     ref, shape, dtype, rows = prob._expect
     dev = _check_call(prob, (("out", out, shape, dtype), ("lse", lse, rows, torch.float32)), ws)
@@ -578,10 +613,12 @@ class LinearProblem(Problem):
             if state_idx is not None:
                 raise ValueError("state_idx needs n_states")
             n_states = B
-        return cls(R=R, B=B, H=H, D_k=D_k, D_v=D_v, rows_max=int(rows_max), n_states=int(n_states),
+        prob = cls(R=R, B=B, H=H, D_k=D_k, D_v=D_v, rows_max=int(rows_max), n_states=int(n_states),
                    flags=_fp16_flag(q=q, k=k, v=v), q_stride=q_stride, k_stride=k_stride, v_stride=v_stride,
                    scale=float(scale), q=q, k=k, v=v, log_decay=log_decay, row_offsets=row_offsets,
                    state_idx=state_idx)
+        prob._fits = True
+        return prob
 
 
 def dsa_linear_workspace_size(prob: LinearProblem) -> int:
@@ -600,6 +637,9 @@ def _linear_call(fn, prob, state_in, state_out, out, ws, stream):
     import torch
     if prob._on is None:           # (new, or changed)
         c = prob.c
+        _check_fits(prob, dict(q=(c.H, c.D_k, c.q_stride, c.R), k=(c.H, c.D_k, c.k_stride, c.R),
+                               v=(c.H, c.D_v, c.v_stride, c.R)),
+                    dict(row_offsets=c.B + 1, state_idx=c.B), (("log_decay", torch.float32, (c.H,)),))
         prob._expect = (ctypes.byref(c), (c.R, c.H, c.D_v), prob._keep["q"].dtype, (c.n_states, c.H, c.D_k, c.D_v))
     ref, shape, dtype, states = prob._expect
     dev = _check_call(prob, (("out", out, shape, dtype), ("state_in", state_in, states, torch.float32),
