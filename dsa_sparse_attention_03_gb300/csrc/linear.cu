@@ -82,9 +82,9 @@ struct __align__(16) Shared {
   uint64_t v_ready[4], v_free[4], pair[4];
   uint32_t tmem;
   int abort;
+  int place, scratch;              // (here: the next four, 16-byte aligned, were loaded as one and spilled)
   int req, seg, nseg, first;       // request, its segment, its segments, their first index; req < 0: nothing
   int t0, n;                       // tokens of the segment
-  int place, scratch;
   __align__(16) float pw[2 * kC + 4];            // pw[128 + e] = lambda^e for e = 0 .. 128, 0 for e < 0
   float column[32];                // lambda^(31-y)
   unsigned char mx[2][128];        // fp16: exponent fields of the two halves' largest weight of each row
