@@ -2,12 +2,15 @@
  * libdsa dense attention: softmax attention over every visible position of a
  * packed K/V cache, with grouped heads.
  *
- * A DSA layer attends densely while a row sees no more positions than its
- * top-k ("ds4 PR #964 issue #118", page 2: the full-attention regime at short
- * contexts), and a hybrid stack has layers that always do.  dsa_dense_attn is
- * that step for whole prompts, chunks of prompts and single tokens: the same
- * packed batch as dsa_sparse_attn, without a selection, over K and V caches of
- * H_kv heads.  Query head h reads K/V head h / (H_q / H_kv).
+ * The operator of layers that attend to everything they see, for whole prompts,
+ * chunks of prompts and single tokens: the same packed batch as dsa_sparse_attn,
+ * without a selection, over K and V caches of H_kv heads.  Query head h reads K/V
+ * head h / (H_q / H_kv).  A DSA layer, too, attends densely while a row sees no more
+ * positions than its top-k ("ds4 PR #964 issue #118", page 2: the full-attention
+ * regime at short contexts): this call serves it where its K and V are stored by
+ * head, in the widths below.  Over the latent cache of dsa.h (one head of up to 576
+ * columns, or FP8 rows), which it refuses, that regime is dsa_sparse_attn with every
+ * position selected.
  *
  *   s[r,h,t]  = softmax_scale * q[r,h,:] . k[offsets[b] + t, h / G, :]    t < row_len[r]
  *   out[r,h]  = sum_t softmax_t(s[r,h,:])[t] * v[offsets[b] + t, h / G, :]
@@ -25,10 +28,11 @@
  * to multiples of 2^-31 of it), the output rounded once to the
  * operands' type.  Results do not depend on timing.
  *
- * What a masked position holds does not matter where no row of the call's tile
- * sees it (past the largest row_len of the rows computed together, or another
- * request's).  A position that some rows of a prompt see and others mask must
- * hold finite V values: a weight of zero times infinity or NaN is NaN.
+ * A masked position's k may be anything.  Its v may be anything too where no row of the
+ * request sees it (past the request's largest row_len, or another request's): it
+ * reaches no output.  A v that some rows of a request see has to be finite, or any
+ * output of that request may be NaN, those of rows that mask it among them: a
+ * weight of zero times infinity or NaN is NaN.
  */
 #ifndef DSA_DENSE_H
 #define DSA_DENSE_H

@@ -1,11 +1,12 @@
 /*
  * libdsa linear attention with a decay for each head.
  *
- * The stack a DSA layer belongs to is a hybrid one: most of its layers are
- * linear-attention layers ("GLM-5.3-Flash-Alis-MLX-4bit", page 3), which keep a
- * fixed-size state per request and head in place of a cache.  This is that
- * family's basic operator, with one decay per head, over the same packed batch
- * of query rows as dsa.h.  For the tokens t = 1, 2, .. of a request:
+ * Linear attention keeps a fixed-size state per request and head in place of a cache.
+ * This is its form with one fixed decay per head, over the same packed batch of query
+ * rows as dsa.h.  It is not the operator of the stack that a DSA layer belongs to: that
+ * one's linear layers ("GLM-5.3-Flash-Alis-MLX-4bit", page 3) are KDA, with a gate for
+ * each token and channel and a delta rule, and are not computed here.  For the
+ * tokens t = 1, 2, .. of a request:
  *
  *   S_t[h] = exp(log_decay[h]) * S_{t-1}[h] + k_t[h]^T v_t[h]      S: fp32 [D_k, D_v]
  *   o_t[h] = scale * q_t[h] S_t[h]
@@ -38,9 +39,9 @@
  * powers of two), sums are fp32, and the output is rounded once.  dsa_linear_step
  * computes in fp32 throughout.  Results do not depend on timing.
  *
- * A token's k may be anything for the tokens before it, but its v has to be finite:
- * in the chunked form a NaN or infinity there reaches the outputs of its chunk's
- * earlier tokens too (a weight of zero times NaN is NaN).  Rows of other requests, or
+ * A token's q and k may be anything for the tokens before it, but its v has to be
+ * finite: otherwise any output of dsa_linear_attn for its request may be NaN, those of earlier
+ * tokens among them (a weight of zero times NaN is NaN).  Rows of other requests, or
  * of none, never reach a request, whatever they hold.
  */
 #ifndef DSA_LINEAR_H
