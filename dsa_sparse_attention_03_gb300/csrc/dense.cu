@@ -36,14 +36,14 @@
 //
 // Bounds.  Prompts: the tensor core's rate, 2 (D_k + D_v) flops per visible
 // pair and head; measured 1.58 PFLOP/s for 16384 tokens of 16 heads over 2
-// (694 us, 84% of the cuBLAS burst rate and 93% of the sustained one), where a tile's
+// (693 us, 84% of the cuBLAS burst rate and 93% of the sustained one), where a tile's
 // softmax and the hand-overs between it and the MMAs are what the other row tile does
 // not cover.  Short prompts: an item's start and end cost about 4 us of loads, fill and
 // epilogue, so ragged prompts of up to 2048 tokens and width 192, whose Q leaves
 // the ring only 1.6 tiles, reach 1.06 PFLOP/s (234 us).  Two threads to a row of S,
 // with its maximum exchanged through shared memory, halve the softmax's work per
 // thread but took longer (837 us for the 16384 tokens).  Single tokens: reading K and V
-// once; 6.2 TB/s for 32 requests of up to 32768 positions (255 us, 91% of the copy rate).
+// once; 6.2 TB/s for 32 requests of up to 32768 positions (256 us, 91% of the copy rate).
 //
 // Split cache.  Where the row tiles do not fill the grid, each is computed by
 // several CTAs over parts of its positions; they leave (m, l, O) in the

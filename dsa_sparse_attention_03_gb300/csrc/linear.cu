@@ -41,14 +41,17 @@
 //
 // Bound: reading q, k, v and writing out once.  With every SM at work a chunk of
 // 96 + 32 KB takes about 5600 cycles, 6.1 TB/s: 12 ragged prompts of 32 heads take
-// 107 us against 86 us for their bytes, the rest being the longest prompt's walk.
+// 106 us against 86 us for their bytes, the rest being the longest prompt's walk (fp16
+// 119 us: a second pass over S and one over V for the largest values).
 // Where requests and heads do not fill the GPU, long requests are split into
 // segments: a first launch computes each segment's own end state (K and V only), a
 // scan adds them up to each segment's start, and a second launch walks the segments
-// side by side (65536 tokens of 16 heads: 262 us in nine segments, 1171 us in one walk;
+// side by side.  65536 tokens of 16 heads, launches back to back on three sets of inputs in
+// turn: 244 us in nine segments, 1146 us in one walk (258 us as one call among others;
 // 159 us for its bytes, 238 with K and V read twice).  With each segment's CTA adding up
-// the states before it, one warpgroup's loads at a time, 4096 tokens of 16 heads that go
-// on from a state took 63 us, with the scan 33.
+// the states before it, one warpgroup's loads at a time, instead of the scan, 4096 tokens of
+// 16 heads that go on from a state took almost twice as long (63 us, with the scan 33, both
+// with inputs in L2; 37 on inputs in turn).
 #include "linear.cuh"
 
 #include <algorithm>
@@ -951,12 +954,17 @@ cudaError_t launch_width(ChunkParams& p, bool f16, bool split, cudaStream_t st) 
 
 // One walk over a request's n chunks takes about 7 + 2.4 n us.  Split into segments of m
 // chunks, the states' launch, the scan and the outputs' launch take about 19 + 4.2 m, if
-// the segments fill SMs that would idle.  Measured, one walk against segments: 65536
-// tokens of 16 heads 1171 us, 243 in nine; 4096 of 32 heads 82, 53 in four; of 64 heads
-// 85, 90 in two; 1024 of 16 heads 26, 21 in eight; 512 of them 16, 20 in four.
+// the segments fill SMs that would idle.  Measured (width 128, bf16, launches back to back on
+// three sets of inputs in turn; us), one walk and segments:
+//   tokens x heads   65536 x 16   4096 x 16   4096 x 32   1024 x 16   4096 x 64   512 x 16
+//                    1146  244     80   37     85   55     26   22     85   92     16   20
 // Where requests and heads alone fill the GPU, only a request that is still walked when
-// the others are done is split (20000 tokens and 39 of 200, 8 heads: 370 and 105; with
-// 299 of 100, 16 heads, 391 and 421); a short one costs its start and end, 3 chunks.
+// the others are done is split: n above 1.5 times the chunks of each SM if the work were
+// level, in which a request counts its tokens and 3.5 chunks (3 for its start and end, half
+// a one for its last, partly filled one).  One request and 100 of 200 tokens:
+//   tokens x heads   4096 x 16  8192 x 16  24576 x 32  12288 x 16  16384 x 16  24576 x 16
+//   n / level           0.56       1.06       1.30        1.51        1.91        2.60
+//                     143  198   177  215   486  490    249  228    321  238    464  262
 int linear_seg_len(const dsa_linear_problem& p) {
   constexpr int kWhole = INT32_MAX - 127;
   const int64_t longest = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
