@@ -29,6 +29,17 @@ and linear attention with a decay for each head (``include/dsa_linear.h``)::
     lp = LinearProblem.from_tensors(q=..., k=..., v=..., log_decay=..., row_offsets=..., scale=...)
     dsa_linear_attn(lp, state_in, state_out, out, alloc_linear_workspace(lp))    # prompts
     dsa_linear_step(lp, state, state, out, ws)                                   # one token of each request
+
+and norms with the position rotation (``include/dsa_rope.h``) and the paged cache held in
+4 bits (``include/dsa_kv4.h``)::
+
+    qk = QKProblem.from_tensors(q=..., k=..., v=..., positions=..., inv_freq=..., q_weight=..., k_weight=..., ...)
+    dsa_qk_norm_rope(qk, q_out, k_out)
+    cache = KV4Cache.from_tensors(pages=alloc_kv4_pages(...), table=..., page_size=64, D_k=128, D_v=128)
+    dsa_kv4_append(cache, qk, q_out, alloc_kv4_workspace())
+    kp = KV4Problem.from_tensors(cache=cache, q=q_out, row_offsets=..., row_len=..., softmax_scale=...)
+    dsa_kv4_attn(kp, out, lse, alloc_kv4_workspace(kp))
+    dsa_kv4_read(cache, row_offsets, positions, k_out, v_out, ws)
 """
 from __future__ import annotations
 
@@ -59,6 +70,7 @@ DSA_INDEXER_TC = 2
 DSA_FLAG_NO_RELU = 0x100
 DSA_FLAG_KV_FP8 = 0x200
 DSA_FLAG_FP16 = 0x400
+DSA_FLAG_ROPE_ADJACENT = 0x800
 
 INDEXERS = {"auto": DSA_INDEXER_AUTO, "dp4a": DSA_INDEXER_DP4A, "tc": DSA_INDEXER_TC}
 
@@ -74,10 +86,13 @@ EXPORTS = ("dsa_version", "dsa_last_error_string", "dsa_indexer_kind", "dsa_deco
            "dsa_dense_workspace_size", "dsa_dense_attn",
            # include/dsa_linear.h
            "dsa_linear_workspace_size", "dsa_linear_attn", "dsa_linear_step",
+           # include/dsa_rope.h, include/dsa_kv4.h
+           "dsa_qk_norm_rope", "dsa_kv4_block_bytes", "dsa_kv4_append", "dsa_kv4_read", "dsa_kv4_workspace_size",
+           "dsa_kv4_attn",
            # include/dsa_testing.h
            "dsa_test_topk_missing_arrival", "dsa_test_attn_missing_gather",
            "dsa_test_indexer_missing_tile", "dsa_test_dense_missing_tile",
-           "dsa_test_linear_missing_tile")
+           "dsa_test_linear_missing_tile", "dsa_test_kv4_missing_stage")
 
 
 class dsa_problem(ctypes.Structure):
@@ -117,6 +132,33 @@ class dsa_linear_problem(ctypes.Structure):
     ]
 
 
+class dsa_qk_problem(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int32), ("B", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("D_k", ctypes.c_int32), ("D_v", ctypes.c_int32), ("rot", ctypes.c_int32), ("rot_first", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("flags", ctypes.c_int32), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+    ]
+
+
+class dsa_kv4_cache(ctypes.Structure):
+    _fields_ = [
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("D_k", ctypes.c_int32),
+        ("D_v", ctypes.c_int32), ("B", ctypes.c_int32), ("table_cols", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+        ("pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+    ]
+
+
+class dsa_kv4_problem(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int32), ("H_q", ctypes.c_int32), ("L_max", ctypes.c_int32), ("rows_max", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p), ("row_len", ctypes.c_void_p),
+    ]
+
+
 class dsa_affine_weights(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("biases", ctypes.c_void_p)]
 
@@ -150,6 +192,11 @@ def _load() -> ctypes.CDLL:
     LP = ctypes.POINTER(dsa_linear_problem)
     lib.dsa_linear_workspace_size.restype = sz
     lib.dsa_linear_workspace_size.argtypes = [LP]
+    QP, CP, KP = (ctypes.POINTER(x) for x in (dsa_qk_problem, dsa_kv4_cache, dsa_kv4_problem))
+    lib.dsa_kv4_block_bytes.restype = sz
+    lib.dsa_kv4_block_bytes.argtypes = [ctypes.c_int32] * 3
+    lib.dsa_kv4_workspace_size.restype = sz
+    lib.dsa_kv4_workspace_size.argtypes = [CP, KP]
     for name, args in (
         ("dsa_index_scores", [P, vp, vp, sz, vp]),
         ("dsa_topk", [P, vp, vp, vp, vp, sz, vp]),
@@ -163,6 +210,11 @@ def _load() -> ctypes.CDLL:
         ("dsa_dense_attn", [DP, vp, vp, vp, sz, vp]),
         ("dsa_linear_attn", [LP, vp, vp, vp, vp, sz, vp]),
         ("dsa_linear_step", [LP, vp, vp, vp, vp, sz, vp]),
+        ("dsa_qk_norm_rope", [QP, vp, vp, vp]),
+        ("dsa_kv4_append", [CP, QP, vp, vp, sz, vp]),
+        ("dsa_kv4_read", [CP, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, vp, vp, sz, vp]),
+        ("dsa_kv4_attn", [CP, KP, vp, vp, vp, sz, vp]),
+        ("dsa_test_kv4_missing_stage", [CP, KP, vp, vp, vp, sz, ctypes.c_int64, vp]),
         ("dsa_test_dense_missing_tile", [DP, vp, vp, vp, sz, ctypes.c_int64, vp]),
         ("dsa_test_linear_missing_tile", [LP, vp, vp, vp, vp, sz, ctypes.c_int64, vp]),
         ("dsa_test_topk_missing_arrival", [P, vp, vp, vp, vp, sz, ctypes.c_int, ctypes.c_int64, vp]),
@@ -448,10 +500,9 @@ def _fp16_flag(**ts):
     raise ValueError(f"{', '.join(ts)} must all be bfloat16 or all float16, got {sorted(map(str, kinds))}")
 
 
-def _check_call(prob, outputs, ws):
-    """What a call checks of its tensors: each output (name, tensor, shape, dtype; the
-    tensor may be None) and that everything is on the current CUDA device.  The
-    problem's own tensors are looked over once, until ``set`` changes one."""
+def _check_device(prob):
+    """The current CUDA device, on which the problem's own tensors have to be: they are
+    looked over once, until ``set`` changes one."""
     import torch
     if prob._on is not None:       # (CUDA is up)
         dev = torch._C._cuda_getDevice()
@@ -462,6 +513,18 @@ def _check_call(prob, outputs, ws):
             if t.get_device() != dev:
                 raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device")
         prob._on = dev
+    return dev
+
+
+def _check_call(prob, outputs, ws):
+    """What a call checks of its tensors: each output (name, tensor, shape, dtype; the
+    tensor may be None) and that everything is on the current CUDA device."""
+    dev = _check_device(prob)
+    _check_outputs(dev, outputs, ws)
+    return dev
+
+
+def _check_outputs(dev, outputs, ws):
     for name, t, shape, dtype in outputs:
         if t is None:
             continue
@@ -470,9 +533,8 @@ def _check_call(prob, outputs, ws):
                              f"got {t.dtype} {tuple(t.shape)}")
         if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    if ws.get_device() != dev:
+    if ws is not None and ws.get_device() != dev:
         raise ValueError(f"the workspace is on {ws.device}, not on the current CUDA device")
-    return dev
 
 
 def _check_ints(n, **ts):
@@ -660,7 +722,252 @@ def dsa_linear_step(prob: LinearProblem, state_in, state_out, out, ws, stream=No
     _linear_call(_lib.dsa_linear_step, prob, state_in, state_out, out, ws, stream)
 
 
+# Norms and the position rotation (include/dsa_rope.h), the 4-bit cache (include/dsa_kv4.h).
+
+class QKProblem(Problem):
+    """Sizes plus device tensors of dsa_qk_norm_rope and dsa_kv4_append (include/dsa_rope.h).
+
+    q [R, H_q, D_k], k [R, H_kv, D_k] and v [R, H_kv, D_v] (any may be None; dsa_kv4_append
+    needs k, v and ``row_offsets``) are bfloat16 or float16 and may be views with a token stride.
+    ``inv_freq`` is float64 [rot / 2], radians a position (None: no rotation), of the columns
+    from ``rot_first`` on; ``interleaved`` pairs adjacent columns, otherwise halves.
+    ``q_weight`` and ``k_weight`` [D_k] are the norms' weights in the operands' type (None: not
+    normed).  A negative position skips its row.
+    """
+
+    _struct = dsa_qk_problem
+
+    @classmethod
+    def from_tensors(cls, *, q=None, k=None, v=None, positions, inv_freq=None, rot_first=0, interleaved=False,
+                     q_weight=None, k_weight=None, eps=1e-6, row_offsets=None):
+        heads = {n: t for n, t in (("q", q), ("k", k), ("v", v)) if t is not None}
+        if q is None and k is None:
+            raise ValueError("q or k must be given")
+        size = {n: _head_tensor(n, t) for n, t in heads.items()}
+        R = int(next(iter(heads.values())).shape[0])
+        D_k = size["q" if q is not None else "k"][1]
+        H_kv = size["k"][0] if k is not None else 0
+        if any(t.shape[0] != R for t in heads.values()):
+            raise ValueError(f"{', '.join(heads)} must have the same tokens")
+        if k is not None and size["k"][1] != D_k or v is not None and (k is None or size["v"][0] != H_kv):
+            raise ValueError("q and k must have one width, k and v the same heads")
+        rot = 0 if inv_freq is None else 2 * int(inv_freq.shape[0])
+        flags = _fp16_flag(**heads) | (DSA_FLAG_ROPE_ADJACENT if interleaved else 0)
+        prob = cls(R=R, B=0 if row_offsets is None else int(row_offsets.shape[0]) - 1, H_q=size["q"][0] if q is not None else 0,
+                   H_kv=H_kv, D_k=D_k, D_v=size["v"][1] if v is not None else 0, rot=rot, rot_first=int(rot_first),
+                   eps=float(eps), flags=flags, **{n + "_stride": s[2] for n, s in size.items()}, **heads,
+                   positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, row_offsets=row_offsets)
+        prob._look()
+        return prob
+
+    def _look(self):
+        """The tensors against the sizes (see _check_fits)."""
+        import torch
+        c, keep = self.c, self._keep
+        heads = {n: s for n, s in (("q", (c.H_q, c.D_k, c.q_stride, c.R)), ("k", (c.H_kv, c.D_k, c.k_stride, c.R)),
+                                   ("v", (c.H_kv, c.D_v, c.v_stride, c.R))) if getattr(c, n) is not None}
+        dtype = keep[next(iter(heads))].dtype if heads else None
+        fixed = [(n, d, s) for n, d, s in (("q_weight", dtype, (c.D_k,)), ("k_weight", dtype, (c.D_k,)),
+                                           ("inv_freq", torch.float64, (c.rot // 2,))) if getattr(c, n) is not None]
+        _check_fits(self, heads, dict(positions=c.R, row_offsets=c.B + 1), fixed)
+        self._expect = (ctypes.byref(c), dtype)
+
+    def _output(self, name, t, dev):
+        """Checks an output: packed, or the input itself."""
+        c = self.c
+        ptr = getattr(c, name)
+        if ptr is None:
+            return None
+        shape = (c.R, c.H_q if name == "q" else c.H_kv, c.D_k)
+        if t is None:
+            raise ValueError(f"{name}_out must be given where {name} is")
+        if t.data_ptr() == ptr and c.R > 0:
+            x = self._keep[name]
+            if t.shape != x.shape or t.stride() != x.stride() or t.dtype != x.dtype:
+                raise ValueError(f"{name}_out begins where {name} does, but is not the same tensor")
+        else:
+            _check_outputs(dev, ((name + "_out", t, shape, self._expect[1]),), None)
+        return t.data_ptr()
+
+
+def dsa_qk_norm_rope(prob: QKProblem, q_out, k_out, stream=None) -> None:
+    """q_out [R, H_q, D_k] and k_out [R, H_kv, D_k], packed, or q and k themselves; None
+    where the problem has no q (k)."""
+    import torch
+    if prob._on is None:
+        prob._look()
+    dev = _check_device(prob)
+    q, k = prob._output("q", q_out, dev), prob._output("k", k_out, dev)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    _check(_lib.dsa_qk_norm_rope(prob._expect[0], q, k, _stream(stream)))
+
+
+def dsa_kv4_block_bytes(D_k: int, D_v: int, page_size: int) -> int:
+    """Bytes of one page of one K/V head."""
+    n = _lib.dsa_kv4_block_bytes(int(D_k), int(D_v), int(page_size))
+    if n == 0:
+        raise DsaError(DSA_ERR_UNSUPPORTED, f"no 4-bit cache of D_k={D_k}, D_v={D_v}, page_size={page_size}")
+    return n
+
+
+def alloc_kv4_pages(n_pages, H_kv, D_k, D_v, page_size, device="cuda"):
+    """A pool of pages (not cleared)."""
+    import torch
+    return torch.empty(n_pages, H_kv, dsa_kv4_block_bytes(D_k, D_v, page_size), dtype=torch.uint8, device=device)
+
+
+class KV4Cache(Problem):
+    """A pool of pages and the table of its requests (include/dsa_kv4.h): ``pages`` uint8 [n_pages,
+    H_kv, block], ``table`` int32 [B, pages of a request]."""
+
+    _struct = dsa_kv4_cache
+    revision = 0     # of the fields: a problem looks the cache over again when it has changed
+
+    def set(self, **kw):
+        self.revision += 1
+        return super().set(**kw)
+
+    @classmethod
+    def from_tensors(cls, *, pages, table, page_size, D_k, D_v):
+        if pages.dim() != 3 or table.dim() != 2:
+            raise ValueError("pages must be [n_pages, H_kv, block] and table [B, pages of a request]")
+        cache = cls(n_pages=int(pages.shape[0]), page_size=int(page_size), H_kv=int(pages.shape[1]), D_k=int(D_k),
+                    D_v=int(D_v), B=int(table.shape[0]), table_cols=int(table.shape[1]), pages=pages, table=table)
+        cache._look()
+        return cache
+
+    def _look(self):
+        import torch
+        c, keep = self.c, self._keep
+        block = dsa_kv4_block_bytes(c.D_k, c.D_v, c.page_size)
+        for name, dtype, shape in (("pages", torch.uint8, (c.n_pages, c.H_kv, block)),
+                                   ("table", torch.int32, (c.B, c.table_cols))):
+            t = keep[name]
+            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+        self._expect = (ctypes.byref(c),)
+
+
+def _check_cache(cache):
+    """Looks the cache's tensors over; the current device."""
+    if cache._on is None:
+        cache._look()
+    return _check_device(cache)
+
+
+def dsa_kv4_append(cache: KV4Cache, prob: QKProblem, q_out, ws, stream=None) -> None:
+    """Rows into the cache; q_out as in dsa_qk_norm_rope (None where the problem has no q)."""
+    import torch
+    if prob._on is None:
+        prob._look()
+    dev = _check_cache(cache)
+    _check_device(prob)
+    q = prob._output("q", q_out, dev)
+    _check_outputs(dev, (), ws)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    _check(_lib.dsa_kv4_append(cache._expect[0], prob._expect[0], q, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def dsa_kv4_read(cache: KV4Cache, row_offsets, positions, k_out, v_out, ws, stream=None) -> None:
+    """k_out [R, H_kv, D_k] and v_out [R, H_kv, D_v] (either may be None), bfloat16 or float16: what the
+    cache holds at positions[r] of row r's request."""
+    import torch
+    c, dev = cache.c, _check_cache(cache)
+    _check_ints(dict(row_offsets=c.B + 1), row_offsets=row_offsets, positions=positions)
+    R = int(positions.shape[0])
+    outs = {n: t for n, t in (("k_out", k_out), ("v_out", v_out)) if t is not None}
+    flags = _fp16_flag(**outs) if outs else 0
+    dtype = torch.float16 if flags else torch.bfloat16
+    _check_outputs(dev, (("k_out", k_out, (R, c.H_kv, c.D_k), dtype), ("v_out", v_out, (R, c.H_kv, c.D_v), dtype),
+                         ("row_offsets", row_offsets, (c.B + 1,), torch.int32), ("positions", positions, (R,), torch.int32)), ws)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    _check(_lib.dsa_kv4_read(cache._expect[0], R, _ptr(row_offsets), _ptr(positions), flags, _ptr(k_out), _ptr(v_out), _ptr(ws),
+                             ws.numel(), _stream(stream)))
+
+
+class KV4Problem(Problem):
+    """Sizes plus device tensors of one attention call over a KV4Cache (include/dsa_kv4.h).
+
+    q [R, H_q, D_k] is bfloat16 or float16 and may be a view with a token stride.  ``L_max`` and
+    ``rows_max`` are host values, read from the device tensors unless given.
+    """
+
+    _struct = dsa_kv4_problem
+
+    @classmethod
+    def from_tensors(cls, *, cache, q, row_offsets, row_len, softmax_scale, L_max=None, rows_max=None):
+        H_q, D, stride = _head_tensor("q", q)
+        R = int(q.shape[0])
+        _check_ints(dict(row_offsets=cache.c.B + 1, row_len=R), row_offsets=row_offsets, row_len=row_len)
+        if L_max is None:
+            L_max = int(row_len.max().item()) if R else 0
+        if rows_max is None:
+            rows_max = int((row_offsets[1:] - row_offsets[:-1]).max().item()) if R else 0
+        prob = cls(R=R, H_q=H_q, L_max=int(L_max), rows_max=int(rows_max), softmax_scale=float(softmax_scale),
+                   flags=_fp16_flag(q=q), q_stride=stride, q=q, row_offsets=row_offsets, row_len=row_len)
+        prob._keep_cache = cache
+        if D != cache.c.D_k:
+            raise ValueError(f"q is {D} wide, the cache's keys {cache.c.D_k}")
+        prob._look()
+        return prob
+
+    def _look(self):
+        c, cache = self.c, self._keep_cache.c
+        self._fits = False
+        _check_fits(self, dict(q=(c.H_q, cache.D_k, c.q_stride, c.R)), dict(row_offsets=cache.B + 1, row_len=c.R))
+        self._revision = self._keep_cache.revision
+        self._expect = (ctypes.byref(c), (c.R, c.H_q, cache.D_v), self._keep["q"].dtype, (c.R, c.H_q))
+
+    def __getattr__(self, name):
+        if name in ("_keep_cache", "_revision"):
+            raise AttributeError(name)
+        return Problem.__getattr__(self, name)
+
+
+def dsa_kv4_workspace_size(prob: KV4Problem) -> int:
+    n = _lib.dsa_kv4_workspace_size(ctypes.byref(prob._keep_cache.c), ctypes.byref(prob.c))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, _lib.dsa_last_error_string().decode())
+    return n
+
+
+def alloc_kv4_workspace(prob: Optional[KV4Problem] = None, device="cuda"):
+    """For dsa_kv4_attn on ``prob``; without one, for dsa_kv4_append and dsa_kv4_read."""
+    import torch
+    return torch.empty(256 if prob is None else dsa_kv4_workspace_size(prob), dtype=torch.uint8, device=device)
+
+
+def _kv4_call(prob, out, lse, ws):
+    import torch
+    cache = prob._keep_cache
+    if prob._on is None or prob._revision != cache.revision:
+        cache._look()
+        prob._look()
+    ref, shape, dtype, rows = prob._expect
+    dev = _check_cache(cache)
+    _check_call(prob, (("out", out, shape, dtype), ("lse", lse, rows, torch.float32)), ws)
+    return cache._expect[0], ref, dev
+
+
+def dsa_kv4_attn(prob: KV4Problem, out, lse, ws, stream=None) -> None:
+    """out [R, H_q, D_v] in the queries' type; lse [R, H_q] float32 or None."""
+    import torch
+    cache, ref, dev = _kv4_call(prob, out, lse, ws)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    _check(_lib.dsa_kv4_attn(cache, ref, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
 # Test hooks of these calls (include/dsa_testing.h).
+
+def dsa_test_kv4_missing_stage(prob: KV4Problem, out, lse, ws, limit_ns, stream=None) -> None:
+    cache, ref, _ = _kv4_call(prob, out, lse, ws)
+    _check(_lib.dsa_test_kv4_missing_stage(cache, ref, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), int(limit_ns),
+                                           _stream(stream)))
+
 
 def dsa_test_dense_missing_tile(prob: DenseProblem, out, lse, ws, limit_ns, stream=None) -> None:
     _check(_lib.dsa_test_dense_missing_tile(ctypes.byref(prob.c), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),

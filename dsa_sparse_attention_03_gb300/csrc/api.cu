@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "dense.cuh"
+#include "kv4.cuh"
 #include "linear.cuh"
 
 namespace dsa {
@@ -652,6 +653,219 @@ dsa_status dsa_linear_step(const dsa_linear_problem* p, const float* state_in, f
   return DSA_OK;
 }
 
+// --------------------------------------------- norms, rotation and the 4-bit cache
+
+namespace {
+
+// What dsa_qk_norm_rope and dsa_kv4_append check alike; q or k may be absent.
+dsa_status turn_plan(const dsa_qk_problem* p, const uint16_t* q_out, const uint16_t* k_out, TurnArgs* t) {
+  if (!p) return fail(DSA_ERR_INVALID_ARG, "problem is NULL");
+  if (p->R < 0 || p->R > 65535) return fail(DSA_ERR_INVALID_ARG, "R=%d outside [0,65535]", p->R);
+  if ((p->q && p->H_q < 1) || p->H_q < 0 || p->H_q > 128) return fail(DSA_ERR_UNSUPPORTED, "H_q=%d outside [1,128]", p->H_q);
+  if ((p->k && p->H_kv < 1) || p->H_kv < 0 || p->H_kv > 128)
+    return fail(DSA_ERR_UNSUPPORTED, "H_kv=%d outside [1,128]", p->H_kv);
+  if (p->D_k != 64 && p->D_k != 128 && p->D_k != 192 && p->D_k != 256)
+    return fail(DSA_ERR_UNSUPPORTED, "D_k=%d not in {64,128,192,256}", p->D_k);
+  if (p->rot < 0 || p->rot % 8 || p->rot > p->D_k)
+    return fail(DSA_ERR_UNSUPPORTED, "rot=%d: need a multiple of 8 in [0,D_k]", p->rot);
+  if (p->rot_first < 0 || p->rot_first % 4 || p->rot_first > p->D_k - p->rot)
+    return fail(DSA_ERR_UNSUPPORTED, "rot_first=%d: need a multiple of 4 in [0,D_k-rot]", p->rot_first);
+  if (!(p->eps >= 0.f && p->eps < 1e30f)) return fail(DSA_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (p->flags & ~(DSA_FLAG_FP16 | DSA_FLAG_ROPE_ADJACENT)) return fail(DSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
+  const int64_t pack[3] = {(int64_t)p->H_q * p->D_k, (int64_t)p->H_kv * p->D_k, (int64_t)p->H_kv * p->D_v};
+  const int64_t stride[3] = {p->q_stride, p->k_stride, p->v_stride};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] && (stride[i] < pack[i] || stride[i] % 8 || stride[i] > (int64_t(1) << 31)))
+      return fail(DSA_ERR_INVALID_ARG, "%c_stride=%lld: need a multiple of 8 in [%lld, 2^31], or 0", "qkv"[i],
+                  (long long)stride[i], (long long)pack[i]);
+  if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->q_weight, 16) || !aligned(p->k_weight, 16) ||
+      !aligned(q_out, 16) || !aligned(k_out, 16))
+    return fail(DSA_ERR_INVALID_ARG, "q/k/v, their weights and outputs must be 16-byte aligned");
+  if (!aligned(p->inv_freq, 8) || !aligned(p->positions, 4) || !aligned(p->row_offsets, 4))
+    return fail(DSA_ERR_INVALID_ARG, "inv_freq must be 8-byte aligned, positions and row_offsets 4-byte");
+  if (p->R > 0) {
+    if (!p->positions) return fail(DSA_ERR_INVALID_ARG, "positions must be set");
+    if (p->rot > 0 && !p->inv_freq) return fail(DSA_ERR_INVALID_ARG, "inv_freq must be set where columns rotate");
+    if (p->q && !q_out) return fail(DSA_ERR_INVALID_ARG, "q_out must be set where q is");
+  }
+  TurnArgs& a = *t;
+  std::memset(&a, 0, sizeof a);
+  a.q = p->q; a.k = p->k; a.v = p->v;
+  a.q_weight = p->q ? p->q_weight : nullptr;
+  a.k_weight = p->k ? p->k_weight : nullptr;
+  a.inv_freq = p->inv_freq; a.positions = p->positions; a.row_offsets = p->row_offsets;
+  a.q_out = const_cast<uint16_t*>(q_out);
+  a.k_out = const_cast<uint16_t*>(k_out);
+  a.q_stride = stride[0] ? stride[0] : pack[0];
+  a.k_stride = stride[1] ? stride[1] : pack[1];
+  a.v_stride = stride[2] ? stride[2] : pack[2];
+  a.q_out_stride = q_out == p->q ? a.q_stride : pack[0];
+  a.k_out_stride = k_out == p->k ? a.k_stride : pack[1];
+  a.eps = p->eps;
+  a.R = p->R; a.B = p->B;
+  a.H_q = p->q ? p->H_q : 0;
+  a.H_kv = p->k ? p->H_kv : 0;
+  a.rot = p->rot; a.first = p->rot_first;
+  a.adjacent = (p->flags & DSA_FLAG_ROPE_ADJACENT) != 0;
+  return DSA_OK;
+}
+
+bool kv4_widths(int D_k, int D_v) {
+  return (D_k == 64 && D_v == 64) || ((D_k == 128 || D_k == 192) && D_v == 128);
+}
+bool kv4_page(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
+
+dsa_status cache_plan(const dsa_kv4_cache* c, CacheArgs* a) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "cache is NULL");
+  if (!kv4_widths(c->D_k, c->D_v))
+    return fail(DSA_ERR_UNSUPPORTED, "(D_k, D_v)=(%d, %d) not in {(64,64), (128,128), (192,128)}", c->D_k, c->D_v);
+  if (!kv4_page(c->page_size)) return fail(DSA_ERR_UNSUPPORTED, "page_size=%d not in {16,32,64,128}", c->page_size);
+  if (c->n_pages < 1) return fail(DSA_ERR_INVALID_ARG, "n_pages=%d < 1", c->n_pages);
+  if (c->H_kv < 1 || c->H_kv > 128) return fail(DSA_ERR_UNSUPPORTED, "H_kv=%d outside [1,128]", c->H_kv);
+  if (c->B < 1 || c->B > kMaxB) return fail(DSA_ERR_UNSUPPORTED, "B=%d outside [1,%d]", c->B, kMaxB);
+  if (c->table_cols < 1 || (int64_t)c->table_cols * c->page_size >= (int64_t(1) << 31) - 256)
+    return fail(DSA_ERR_UNSUPPORTED, "table_cols=%d: need at least one, and less than 2^31 - 256 positions", c->table_cols);
+  if (!c->pages || !aligned(c->pages, 16)) return fail(DSA_ERR_INVALID_ARG, "pages must be set and 16-byte aligned");
+  if (!c->table || !aligned(c->table, 4)) return fail(DSA_ERR_INVALID_ARG, "table must be set and 4-byte aligned");
+  a->pages = c->pages; a->table = c->table;
+  a->n_pages = c->n_pages; a->H_kv = c->H_kv; a->B = c->B; a->cols = c->table_cols;
+  a->ps = c->page_size;
+  a->ps_log2 = c->page_size == 16 ? 4 : (c->page_size == 32 ? 5 : (c->page_size == 64 ? 6 : 7));
+  a->block = (uint32_t)dsa_kv4_block_bytes(c->D_k, c->D_v, c->page_size);
+  return DSA_OK;
+}
+
+struct Kv4Plan {
+  CacheArgs cache;
+  Kv4Shape shape;
+  size_t off_ml, off_part, total;
+};
+
+dsa_status kv4_plan(const dsa_kv4_cache* c, const dsa_kv4_problem* p, Kv4Plan* kp) {
+  const dsa_status s = cache_plan(c, &kp->cache);
+  if (s != DSA_OK) return s;
+  if (!p) return fail(DSA_ERR_INVALID_ARG, "problem is NULL");
+  if (p->R < 0 || p->R > 65535) return fail(DSA_ERR_INVALID_ARG, "R=%d outside [0,65535]", p->R);
+  if (p->H_q < 1 || p->H_q > 128) return fail(DSA_ERR_UNSUPPORTED, "H_q=%d outside [1,128]", p->H_q);
+  if (p->H_q % c->H_kv) return fail(DSA_ERR_UNSUPPORTED, "H_kv=%d does not divide H_q=%d", c->H_kv, p->H_q);
+  if (p->L_max < 0) return fail(DSA_ERR_INVALID_ARG, "L_max=%d < 0", p->L_max);
+  if (p->rows_max < 0) return fail(DSA_ERR_INVALID_ARG, "rows_max=%d < 0", p->rows_max);
+  const int64_t pack = (int64_t)p->H_q * c->D_k;
+  if (p->q_stride && (p->q_stride < pack || p->q_stride % 8 || p->q_stride > (int64_t(1) << 31)))
+    return fail(DSA_ERR_INVALID_ARG, "q_stride=%lld: need a multiple of 8 in [%lld, 2^31], or 0", (long long)p->q_stride,
+                (long long)pack);
+  if (!(p->softmax_scale > 0.f) || p->softmax_scale > 1e30f)
+    return fail(DSA_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
+  if (p->flags & ~DSA_FLAG_FP16) return fail(DSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
+  kp->shape = kv4_shape(*c, *p);
+  size_t off = kKv4PartsOffset;
+  kp->off_ml = off;
+  const size_t parts = kv4_parts(kp->shape);
+  off = align_up(off + parts * 8, 256);
+  kp->off_part = off;
+  off = align_up(off + parts * c->D_v * 4, 256);
+  kp->total = off;
+  return DSA_OK;
+}
+
+}  // namespace
+
+dsa_status dsa_qk_norm_rope(const dsa_qk_problem* p, uint16_t* q_out, uint16_t* k_out, void* stream) {
+  g_err.clear();
+  TurnArgs a;
+  const dsa_status s = turn_plan(p, q_out, k_out, &a);
+  if (s != DSA_OK) return s;
+  if (p->R > 0 && p->k && !k_out) return fail(DSA_ERR_INVALID_ARG, "k_out must be set where k is");
+  const cudaError_t e = launch_qk_norm_rope(a, p->D_k, p->flags & DSA_FLAG_FP16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "norm and rotation");
+  return DSA_OK;
+}
+
+size_t dsa_kv4_block_bytes(int32_t D_k, int32_t D_v, int32_t page_size) {
+  if (!kv4_widths(D_k, D_v) || !kv4_page(page_size)) return 0;
+  return (size_t)page_size * (D_k + D_v) / 32 * 17;
+}
+
+dsa_status dsa_kv4_append(const dsa_kv4_cache* c, const dsa_qk_problem* p, uint16_t* q_out, void* ws, size_t ws_bytes,
+                          void* stream) {
+  g_err.clear();
+  CacheArgs ca;
+  TurnArgs a;
+  dsa_status s = cache_plan(c, &ca);
+  if (s != DSA_OK) return s;
+  if ((s = turn_plan(p, q_out, nullptr, &a)) != DSA_OK) return s;
+  if ((s = check_ws(256, ws, ws_bytes)) != DSA_OK) return s;
+  if (p->D_k != c->D_k || p->D_v != c->D_v || p->H_kv != c->H_kv || p->B != c->B)
+    return fail(DSA_ERR_INVALID_ARG, "H_kv=%d, D_k=%d, D_v=%d, B=%d are not the cache's %d, %d, %d, %d", p->H_kv, p->D_k,
+                p->D_v, p->B, c->H_kv, c->D_k, c->D_v, c->B);
+  if (p->R > 0 && (!p->k || !p->v || !p->row_offsets)) return fail(DSA_ERR_INVALID_ARG, "k/v/row_offsets must be set");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_clear_status(ws, st);
+  if (e != cudaSuccess) return cuda_fail(e, "clear status");
+  if (p->R == 0) return DSA_OK;
+  e = launch_kv4_append(a, ca, c->D_k, c->D_v, p->flags & DSA_FLAG_FP16, static_cast<uint32_t*>(ws), st);
+  if (e != cudaSuccess) return cuda_fail(e, "append to the 4-bit cache");
+  return DSA_OK;
+}
+
+dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t* row_offsets, const int32_t* positions, int32_t flags,
+                        uint16_t* k_out, uint16_t* v_out, void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  CacheArgs ca;
+  dsa_status s = cache_plan(c, &ca);
+  if (s != DSA_OK) return s;
+  if ((s = check_ws(256, ws, ws_bytes)) != DSA_OK) return s;
+  if (R < 0) return fail(DSA_ERR_INVALID_ARG, "R=%d < 0", R);
+  if (flags & ~DSA_FLAG_FP16) return fail(DSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", flags);
+  if (R > 0 && (!row_offsets || !positions)) return fail(DSA_ERR_INVALID_ARG, "row_offsets and positions must be set");
+  if (!aligned(row_offsets, 4) || !aligned(positions, 4))
+    return fail(DSA_ERR_INVALID_ARG, "row_offsets and positions must be 4-byte aligned");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(DSA_ERR_INVALID_ARG, "k_out/v_out must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_clear_status(ws, st);
+  if (e != cudaSuccess) return cuda_fail(e, "clear status");
+  if (R == 0 || (!k_out && !v_out)) return DSA_OK;
+  e = launch_kv4_read(ca, R, row_offsets, positions, c->D_k, c->D_v, flags & DSA_FLAG_FP16, k_out, v_out,
+                      static_cast<uint32_t*>(ws), st);
+  if (e != cudaSuccess) return cuda_fail(e, "read of the 4-bit cache");
+  return DSA_OK;
+}
+
+size_t dsa_kv4_workspace_size(const dsa_kv4_cache* c, const dsa_kv4_problem* p) {
+  g_err.clear();
+  Kv4Plan kp;
+  return kv4_plan(c, p, &kp) == DSA_OK ? kp.total : 0;
+}
+
+static dsa_status run_kv4(const dsa_kv4_cache* c, const dsa_kv4_problem* p, uint16_t* out, float* lse, void* ws,
+                          size_t ws_bytes, void* stream, const TestHooks* hooks) {
+  Kv4Plan kp;
+  dsa_status s = kv4_plan(c, p, &kp);
+  if (s != DSA_OK) return s;
+  if ((s = check_ws(kp.total, ws, ws_bytes)) != DSA_OK) return s;
+  if (p->R > 0 && (!p->row_offsets || !p->row_len || !p->q || !out))
+    return fail(DSA_ERR_INVALID_ARG, "q/out/row_offsets/row_len must be set");
+  if (!aligned(p->q, 16) || !aligned(out, 16)) return fail(DSA_ERR_INVALID_ARG, "q/out must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(p->row_offsets, 4) || !aligned(p->row_len, 4))
+    return fail(DSA_ERR_INVALID_ARG, "lse/row_offsets/row_len must be 4-byte aligned");
+  char* w = static_cast<char*>(ws);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (p->R == 0 || !kp.shape.join) e = launch_clear_status(ws, st);   // (else the join sets it)
+  if (e != cudaSuccess) return cuda_fail(e, "clear status");
+  if (p->R == 0) return DSA_OK;
+  e = launch_kv4_attn(*c, kp.cache, *p, kp.shape, out, lse, w, reinterpret_cast<float*>(w + kp.off_ml),
+                      reinterpret_cast<float*>(w + kp.off_part), st, hooks);
+  if (e != cudaSuccess) return cuda_fail(e, "attention over the 4-bit cache");
+  return DSA_OK;
+}
+
+dsa_status dsa_kv4_attn(const dsa_kv4_cache* c, const dsa_kv4_problem* p, uint16_t* out, float* lse, void* ws,
+                        size_t ws_bytes, void* stream) {
+  g_err.clear();
+  return run_kv4(c, p, out, lse, ws, ws_bytes, stream, nullptr);
+}
+
 // ------------------------------------------------------------------ test hooks
 
 static dsa_status check_limit(int64_t limit_ns, TestHooks* h) {
@@ -736,6 +950,16 @@ dsa_status dsa_test_dense_missing_tile(const dsa_dense_problem* p, uint16_t* out
   if (s != DSA_OK) return s;
   h.tile_no_load = 1;
   return run_dense(p, out, lse, ws, ws_bytes, stream, &h);
+}
+
+dsa_status dsa_test_kv4_missing_stage(const dsa_kv4_cache* c, const dsa_kv4_problem* p, uint16_t* out, float* lse, void* ws,
+                                      size_t ws_bytes, int64_t limit_ns, void* stream) {
+  g_err.clear();
+  TestHooks h;
+  const dsa_status s = check_limit(limit_ns, &h);
+  if (s != DSA_OK) return s;
+  h.tile_no_load = 1;
+  return run_kv4(c, p, out, lse, ws, ws_bytes, stream, &h);
 }
 
 dsa_status dsa_test_linear_missing_tile(const dsa_linear_problem* p, const float* state_in, float* state_out,

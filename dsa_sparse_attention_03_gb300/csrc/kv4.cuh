@@ -1,0 +1,90 @@
+// Launchers of the norm, rotation and 4-bit cache kernels (rope.cu, kv4_cache.cu, kv4_attn.cu),
+// used by api.cu, and what those units share.
+#pragma once
+
+#include "common.cuh"
+#include "dsa_kv4.h"
+
+namespace dsa {
+
+// What turns a head: dsa_qk_problem with its strides filled in.
+struct TurnArgs {
+  const uint16_t *q, *k, *v;
+  const uint16_t *q_weight, *k_weight;
+  const double* inv_freq;
+  const int32_t *positions, *row_offsets;
+  uint16_t *q_out, *k_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  float eps;
+  int R, B, H_q, H_kv, rot, first, adjacent;   // H_q (H_kv) = 0: no q (k)
+  int chunks;                                  // CTAs to a row
+};
+
+struct CacheArgs {
+  uint8_t* pages;
+  const int32_t* table;
+  int n_pages, H_kv, B, cols;
+  int ps, ps_log2;
+  uint32_t block;      // bytes of one page of one head
+};
+
+cudaError_t launch_qk_norm_rope(TurnArgs a, int D, bool f16, cudaStream_t st);
+cudaError_t launch_kv4_append(TurnArgs a, const CacheArgs& c, int D_k, int D_v, bool f16, uint32_t* status, cudaStream_t st);
+cudaError_t launch_kv4_read(const CacheArgs& c, int R, const int32_t* row_offsets, const int32_t* positions, int D_k, int D_v,
+                            bool f16, uint16_t* k_out, uint16_t* v_out, uint32_t* status, cudaStream_t st);
+
+// The attention's workspace: the status block, a word of status bits for each CTA, what the
+// join has to know of each CTA's last item, then the parts.
+constexpr int kKv4Slots = 304;                 // CTAs that the GPU holds at once
+constexpr int kKv4Bits = 64;                   // (words of the status block)
+constexpr size_t kKv4DescOffset = 2048;
+constexpr size_t kKv4PartsOffset = 16384;
+struct Kv4Join {                               // an item that CTA i begins and others end
+  int32_t row0, packed, first, head;           // first row and packed rows of the request; first packed row; K/V head
+  int32_t parts, pad[3];                       // parts in the workspace, 0: none
+};
+static_assert(kKv4DescOffset + kKv4Slots * sizeof(Kv4Join) <= kKv4PartsOffset, "workspace map");
+static_assert((kKv4Bits + kKv4Slots) * 4 <= kKv4DescOffset, "status words of the CTAs");
+
+// How a call is cut: packed rows of a row block, CTAs, and whether items may be split.
+struct Kv4Shape {
+  int rows, grid;
+  bool join;
+};
+Kv4Shape kv4_shape(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
+inline size_t kv4_parts(const Kv4Shape& s) { return s.join ? (size_t)2 * s.grid * s.rows : 0; }
+cudaError_t launch_kv4_attn(const dsa_kv4_cache& c, const CacheArgs& ca, const dsa_kv4_problem& p, const Kv4Shape& s,
+                            uint16_t* out, float* lse, char* ws, float* ml, float* part, cudaStream_t st,
+                            const TestHooks* hooks = nullptr);
+
+#ifdef __CUDACC__
+// The request of row `row` (one warp): the last b with row_offsets[b] <= row, or -1.
+// Each round narrows the range 32 times: one for up to 31 requests, three for 4096.
+__device__ __forceinline__ int find_request(const int32_t* row_offsets, int B, int row, int lane) {
+  int base = 0, len = B + 1;
+  while (len > 0) {
+    const int step = (len + 31) / 32, at = base + (lane + 1) * step - 1;
+    const bool le = at < base + len && row_offsets[at] <= row;
+    const int n = __popc(__ballot_sync(0xffffffffu, le));
+    if (step == 1) {
+      base += n;
+      break;
+    }
+    const int end = base + len;
+    base += n * step;
+    len = min(step, end - base);
+  }
+  return base >= 1 && base <= B ? base - 1 : -1;
+}
+
+// Byte of the pool where position `pos` of request b begins its page for head 0, or -1.
+__device__ __forceinline__ int64_t find_page(const CacheArgs& c, int b, int pos) {
+  const int col = pos >> c.ps_log2;
+  if (b < 0 || col >= c.cols) return -1;
+  const int page = c.table[(int64_t)b * c.cols + col];
+  if (page < 0 || page >= c.n_pages) return -1;
+  return (int64_t)page * c.H_kv * c.block;
+}
+#endif
+
+}  // namespace dsa

@@ -1,0 +1,741 @@
+// Attention over the 4-bit cache, few rows of a request at a time (dsa_kv4_attn).
+//
+// Mathematics.  K[t] = s_g (u - 8) for the codes u of group g of 64 columns, so
+//   q . K[t] = sum_g s_g[t] (sum_d q_d u_d - 8 sum_d q_d),
+// and with weights p_t = 2^(c q.K[t] - m):
+//   sum_t p_t V[t] = sum_t (p_t s_g[t]) u - 8 sum_t (p_t s_g[t])      for the columns of group g.
+// The codes go into the products as they are: four bits with zeros around them are the fp16
+// number u 2^-24, and four bits higher up u 2^-20, so a pair of codes becomes a pair of operands
+// by one AND, without a conversion.  K's scales are applied to the logits, V's to the weights,
+// both in fp32.  A query row is scaled by a power of two to fp16's upper range first (every bit
+// of a bf16 query within 2^-25 of the row's largest is kept); the columns whose codes come
+// 2^4 too high get a sixteenth of it.  The products are exact, their sums fp32.
+//
+// Softmax in one pass, base 2: the maximum m only has to be near the row's: O and l are rescaled
+// when it has grown by more than 2^8.  Weights are held as 2^7 of them, and times V's scales
+// relative to a power of two not below any scale so far, so that fp16 holds them to 11 bits
+// down to 2^-21 of the largest.
+//
+// What bounds it.  Per position and K/V head (D_k + D_v) 17 / 32 bytes have to be read: 136 for
+// 128 + 128, at 45 GB/s for an SM one every 5.7 cycles.  The tensor core has little to do
+// (8 to 16 rows), but every code passes through a register: 5 instructions for 8 codes of K, 6 for
+// V, 16 mma.sync a 16 positions.  Dequantised tiles in shared memory for tcgen05 would
+// cost the same extraction, a store and two reads of 16-bit operands; registers are what
+// mma.sync takes and tcgen05 does not.
+//
+// A CTA takes 128 positions of one K/V head at a time (a stage: whole page blocks, one bulk
+// copy each, through a ring) and eight warps 16 positions each, every warp with its own maximum,
+// sum and O; they are joined when an item ends.  Each lane holds 32-bit words of codes in the
+// layout of the products' fragments: rows of K are positions, and rows of V columns, so V needs two
+// positions' codes side by side (one byte permutation for 4 pairs).
+//
+// Work.  Items (request, block of packed rows, K/V head) are laid end to end in stages
+// and cut into equal shares, one for each CTA, so ragged requests keep all SMs
+// busy to the end.  An item cut by a share's end leaves its parts (m, l, O) in the workspace
+// and kv4_join_kernel joins them, always in the same order.
+//
+// All waits are bounded; on expiry the CTA stops and drains its copies.
+#include "kv4.cuh"
+
+#include <cstring>
+
+#include "tc.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kStage = 128;      // positions
+constexpr int kWarps = 8;        // that compute; one more loads
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kBlock = 8;        // packed rows of a product's column block
+
+struct Args {
+  CacheArgs c;
+  const uint16_t* q;
+  const int32_t* row_offsets;
+  const int32_t* row_len;
+  uint16_t* out;
+  float* lse;
+  float* part;        // [2 grid, rows, D_v]
+  float2* ml;         // [2 grid, rows]: (m - 7, l)
+  Kv4Join* join;      // or null: no item is split
+  uint32_t* status;
+  uint32_t* bits;     // status bits of each CTA, for the join; or null: the status is cleared before, and raised
+  int64_t q_stride;
+  uint64_t wait_ns;
+  int R, H_q, G, L_max;
+  int test_no_load;
+  float c2;           // softmax_scale * log2 e
+};
+
+struct Item {
+  int row0, packed, first, h, b;   // packed = 0: no more items
+  int len;                         // positions that the request's rows see at most
+  int stage, stages;               // the range of stages of this CTA
+  int slot;                        // part of the workspace, or -1: the whole item
+};
+
+struct __align__(16) Shared {
+  uint64_t full[8], empty[8];
+  uint64_t ifull[2], ifree[2];
+  int abort;
+  uint32_t bits;
+  uint32_t pages[8];            // pages of each stage that the pool has
+  Item item[2];
+  int64_t units[kWarps + 1];    // of each warp's requests
+  float m[kWarps][2 * kBlock], l[kWarps][2 * kBlock];
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 block of 16-bit values, lane i holding row i / 4, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void lds2(uint32_t addr, uint32_t& x, uint32_t& y) {
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t addr) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr));
+  return x;
+}
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr));
+  return __uint_as_float((uint32_t)x << 16);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A barrier of the computing warps that tells whether any of them says yes.
+__device__ __forceinline__ bool consumers_any(bool x) {
+  uint32_t y;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(y) : "r"((uint32_t)x), "n"(32 * kWarps) : "memory");
+  return y != 0;
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+// Request b's rows, clamped to the call's.
+__device__ __forceinline__ void request_rows(const Args& a, int b, int& r0, int& n) {
+  const int x0 = a.row_offsets[b], x1 = a.row_offsets[b + 1];
+  r0 = min(max(x0, 0), a.R);
+  n = max(min(x1, a.R) - r0, 0);
+}
+
+// Rows and farthest visible position of the request that each lane names (b < B, or none), by a
+// whole warp: requests of more than eight rows are read by all lanes together.
+__device__ __forceinline__ void request_info(const Args& a, int b, int reach, int lane, int& r0, int& n, int& len, bool& bad) {
+  r0 = n = len = 0;
+  if (b >= 0 && b < a.c.B) request_rows(a, b, r0, n);
+  auto see = [&](int l) {
+    bad |= l < 0 || l > reach;
+    return min(max(l, 0), reach);
+  };
+  if (n <= 8)
+    for (int i = 0; i < n; ++i) len = max(len, see(a.row_len[r0 + i]));
+  uint32_t big = __ballot_sync(0xffffffffu, n > 8);
+  while (big) {
+    const int src = __ffs(big) - 1;
+    big &= big - 1;
+    const int x0 = __shfl_sync(0xffffffffu, r0, src), xn = __shfl_sync(0xffffffffu, n, src);
+    int m = 0;
+    for (int i = lane; i < xn; i += 32) m = max(m, see(a.row_len[x0 + i]));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == src) len = m;
+  }
+}
+
+__device__ __forceinline__ int blocks_of(const Args& a, int n, int rows) { return (n * a.G + rows - 1) / rows; }
+__device__ __forceinline__ int stages_of(int len) { return max((len + kStage - 1) / kStage, 1); }
+
+
+template <int DK, int DV>
+constexpr uint32_t kStageBytes = kStage * (DK + DV) * 17 / 32;
+template <int DK, int DV, int NB>
+__host__ __device__ constexpr int ring_stages() {
+  constexpr int rest = (NB == 1 ? 113 : 227) * 1024 - (int)sizeof(Shared) - kWarps * kBlock * DV * 4;
+  constexpr int s = rest / (int)kStageBytes<DK, DV>;
+  return s < 8 ? s : 8;
+}
+template <int DK, int DV, int NB>
+__host__ __device__ constexpr size_t smem_bytes() {
+  return (size_t)ring_stages<DK, DV, NB>() * kStageBytes<DK, DV> + kWarps * kBlock * DV * 4 + sizeof(Shared);
+}
+
+template <int DK, int DV, int NB, bool F16>
+__global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(const __grid_constant__ Args a) {
+  constexpr int GK = DK / 64, GV = DV / 64, ROWS = NB * kBlock, NS = ring_stages<DK, DV, NB>();
+  constexpr uint32_t kBytes = kStageBytes<DK, DV>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* sums = reinterpret_cast<float*>(smem + NS * kBytes);        // [warps, 8, DV]
+  Shared* sh = reinterpret_cast<Shared*>(sums + kWarps * kBlock * DV);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  const int reach = (int)min((int64_t)a.L_max, (int64_t)a.c.cols << a.c.ps_log2);
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(sh->full[i]), 1);
+      mbar_init(bar(sh->empty[i]), kWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(sh->ifull[i]), 1);
+      mbar_init(bar(sh->ifree[i]), kWarps);
+    }
+    sh->abort = 0;
+    sh->bits = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();      // (the inputs may only just be written; the status block is cleared)
+  pdl_trigger();
+  // Units (an item's stages, at least one) of all requests: each warp adds up those of a run.
+  const int per = (a.c.B + kWarps) / (kWarps + 1);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int base = 0; base < per; base += 32) {
+    int r0, n, len;
+    request_info(a, base + lane < per ? warp * per + base + lane : -1, reach, lane, r0, n, len, bad);
+    mine += (int64_t)blocks_of(a, n, ROWS) * a.c.H_kv * stages_of(len);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sh->units[warp] = mine;
+  __syncthreads();
+  uint32_t* const status = a.bits ? &sh->bits : a.status;
+  if (__any_sync(0xffffffffu, bad) && blockIdx.x == 0 && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
+  const WaitCtx wc(&sh->abort, status, a.wait_ns);
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    int64_t total = 0;
+    for (int w = 0; w <= kWarps; ++w) total += sh->units[w];
+    const int64_t shares = min(total, (int64_t)gridDim.x);
+    const int64_t lo = blockIdx.x < shares ? total * blockIdx.x / shares : 0;
+    int64_t left = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares - lo : 0;
+    int n = 0, k = 0;             // stages and items handed over
+    bool ok = true;
+    Kv4Join join = {};
+    if (left > 0) {
+      // The request where the share begins: its warp's run, then 32 at a time.
+      int64_t u = lo;             // units from here to the share's beginning
+      int w = 0;
+      while (u >= sh->units[w]) u -= sh->units[w++];
+      int base = w * per, x = 0, r0, rows, len;
+      for (;; base += 32) {
+        request_info(a, base + lane, reach, lane, r0, rows, len, bad);
+        const int64_t units = (int64_t)blocks_of(a, rows, ROWS) * a.c.H_kv * stages_of(len);
+        int64_t incl = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += t;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, u < incl);
+        if (hit) {
+          x = __ffs(hit) - 1;
+          u -= __shfl_sync(0xffffffffu, incl - units, x);
+          break;
+        }
+        u -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+      int64_t at = lo;            // units before the next piece
+      while (left > 0 && ok) {
+        if (x == 32) {
+          base += 32;
+          x = 0;
+          request_info(a, base + lane, reach, lane, r0, rows, len, bad);
+        }
+        const int xr = __shfl_sync(0xffffffffu, r0, x), xn = __shfl_sync(0xffffffffu, rows, x);
+        const int xl = __shfl_sync(0xffffffffu, len, x);
+        const int st = stages_of(xl);
+        const int64_t units = (int64_t)blocks_of(a, xn, ROWS) * a.c.H_kv * st;
+        if (u >= units) {         // (the request is through, or has no rows)
+          u = 0;
+          ++x;
+          continue;
+        }
+        const int64_t idx = u / st;
+        const int s0 = (int)(u - idx * st), rb = (int)(idx / a.c.H_kv), h = (int)(idx - (int64_t)rb * a.c.H_kv);
+        const int cnt = (int)min((int64_t)(st - s0), left);
+        const bool whole = cnt == st;
+        if (k >= 2 && !(ok = wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc))) break;
+        if (lane == 0) {
+          sh->item[k & 1] = Item{xr, xn * a.G, rb * ROWS, h, base + x, xl, s0, xl > 0 ? cnt : 0,
+                                 whole ? -1 : 2 * (int)blockIdx.x + (s0 == 0)};
+          mbar_arrive(bar(sh->ifull[k & 1]));
+        }
+        ++k;
+        if (!whole && s0 == 0) {  // the item's other parts: as many shares as begin before its end
+          int64_t i = blockIdx.x + 1;
+          while (total * i / shares < at + st) ++i;
+          join = Kv4Join{xr, xn * a.G, rb * ROWS, h, (int)(i - blockIdx.x), {0, 0, 0}};
+        }
+        if (xl > 0) {
+          // Pages: 32 entries of the table at a time, the next ones loaded ahead.
+          const int npp = kStage >> a.c.ps_log2, ends = (xl + a.c.ps - 1) >> a.c.ps_log2;
+          const int32_t* row = a.c.table + (int64_t)(base + x) * a.c.cols;
+          int first = s0 * npp;   // of `cur`
+          auto entry = [&](int i) { return i < ends ? row[i] : -1; };
+          int cur = entry(first + lane), nxt = entry(first + 32 + lane);
+          for (int j = 0; j < cnt; ++j, ++n) {
+            const int pg = (s0 + j) * npp;
+            if (pg - first == 32) {
+              first = pg;
+              cur = nxt;
+              nxt = entry(first + 32 + lane);
+            }
+            const int id = __shfl_sync(0xffffffffu, cur, (pg - first + lane) & 31);
+            const bool need = lane < npp && pg + lane < ends, have = need && id >= 0 && id < a.c.n_pages;
+            if (__any_sync(0xffffffffu, need && !have) && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
+            const uint32_t mask = __ballot_sync(0xffffffffu, have);
+            const int s = n % NS;
+            if (n >= NS && !(ok = wait_bar_warp(bar(sh->empty[s]), (n / NS - 1) & 1, wc))) break;
+            if (lane == 0) {
+              sh->pages[s] = mask;
+              mbar_expect_tx(bar(sh->full[s]), __popc(mask) * a.c.block);
+            }
+            __syncwarp();
+            if (have && !(a.test_no_load && n == 0))
+              bulk_row(smem_u32(smem) + s * kBytes + lane * a.c.block,
+                       a.c.pages + ((int64_t)id * a.c.H_kv + h) * a.c.block, a.c.block, bar(sh->full[s]));
+          }
+        }
+        u += cnt;
+        at += cnt;
+        left -= cnt;
+      }
+    }
+    if (ok && k >= 2) ok = wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc);
+    if (lane == 0) {
+      if (ok) {
+        sh->item[k & 1].packed = 0;
+        mbar_arrive(bar(sh->ifull[k & 1]));
+      }
+      if (a.join) a.join[blockIdx.x] = join;
+      for (int i = max(0, n - NS); i < n; ++i) drain_bar(bar(sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ products and softmax
+    const int i = lane >> 2, j = lane & 3;
+    // Row i of a fragment is position tau(i) of eight: so that the four positions 2 j (and the
+    // four 2 j + 1) whose V a load takes, and the first four rows of K, lie in different banks.
+    auto tau = [](int x) { return x ^ (x >> 2); };
+    const int t0 = tau(i), v0 = tau(2 * j), v1 = tau(2 * j + 1);
+    const int ps = a.c.ps, page = (16 * warp) >> a.c.ps_log2, o = (16 * warp) & (ps - 1);
+    const uint32_t vcodes = ps * (DK / 2), kscales = ps * ((DK + DV) / 2), vscales = kscales + ps * (DK / 32);
+    const uint32_t page_at = page * a.c.block;
+    int n = 0;
+    for (int k = 0;; ++k) {
+      bool ok = wait_bar_warp(bar(sh->ifull[k & 1]), (k >> 1) & 1, wc);
+      Item it;
+      it.packed = 0;
+      if (ok) it = sh->item[k & 1];
+      const bool last = it.packed == 0;
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(bar(sh->ifree[k & 1]));
+      uint32_t qf[GK][NB][4][2];
+      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], sp[GV][NB][4], oo[GV][NB][4][4], vinv = 0x1p126f;
+      int see[NB][2];
+      if (!last) {
+        // The queries, scaled to fp16's upper range by a power of two for each row.
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int pk = it.first + nb * kBlock + i;
+          const bool valid = pk < it.packed;
+          const uint16_t* q = a.q + (int64_t)(it.row0 + (valid ? pk / a.G : 0)) * a.q_stride +
+                              (int64_t)(it.h * a.G + (valid ? pk % a.G : 0)) * DK + 16 * j;
+          uint4 w[GK][2];
+#pragma unroll
+          for (int g = 0; g < GK; ++g)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              w[g][x] = valid ? *reinterpret_cast<const uint4*>(q + 64 * g + 8 * x) : make_uint4(0, 0, 0, 0);
+          auto value = [&](int g, int c) {   // column 64 g + 16 j + c
+            const uint4 v = w[g][c >> 3];
+            const uint32_t y = (c & 7) < 2 ? v.x : (c & 7) < 4 ? v.y : (c & 7) < 6 ? v.z : v.w;
+            return to_float<F16>((uint16_t)(c & 1 ? y >> 16 : y));
+          };
+          uint32_t top = 0;
+#pragma unroll
+          for (int g = 0; g < GK; ++g)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(value(g, c)) & 0x7f800000u);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^(14 - exponent of the row's largest)
+          const float up = top ? __uint_as_float(min((268u << 23) - top, 254u << 23)) : 1.f;
+#pragma unroll
+          for (int g = 0; g < GK; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int c = 8 * (y >> 1) + 2 * (y & 1);
+              const __half2 lo = __floats2half2_rn(value(g, c) * up, value(g, c + 4) * up);
+              const __half2 hi = __floats2half2_rn(value(g, c + 1) * (up * 0.0625f), value(g, c + 5) * (up * 0.0625f));
+              qf[g][nb][y][0] = *reinterpret_cast<const uint32_t*>(&lo);
+              qf[g][nb][y][1] = *reinterpret_cast<const uint32_t*>(&hi);
+              const float2 fl = __half22float2(lo), fh = __half22float2(hi);
+              sum += fl.x + fl.y + 16.f * (fh.x + fh.y);
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) qc[g][nb][x] = -0x1p-21f * __shfl_sync(0xffffffffu, sum, 4 * (2 * j + x));
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            factor[nb][x] = a.c2 * (0x1p24f / __shfl_sync(0xffffffffu, up, 4 * (2 * j + x)));
+            const int r = it.first + nb * kBlock + 2 * j + x;
+            see[nb][x] = r < it.packed ? min(max(a.row_len[it.row0 + r / a.G], 0), reach) : it.len;
+            mm[nb][x] = -1e30f;
+            l[nb][x] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < GV; ++g)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              sp[g][nb][x] = 0.f;
+#pragma unroll
+              for (int t = 0; t < 4; ++t) oo[g][nb][t][x] = 0.f;
+            }
+        int least = see[0][0];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) least = min(least, min(see[nb][0], see[nb][1]));
+        least = __reduce_min_sync(0xffffffffu, least);
+        for (int st = 0; st < it.stages; ++st, ++n) {
+          const int s = n % NS;
+          if (!(ok = wait_bar_warp(bar(sh->full[s]), (n / NS) & 1, wc))) break;
+          const int pos = (it.stage + st) * kStage + 16 * warp;     // the warp's first position
+          if (pos < it.len && (sh->pages[s] >> page & 1u)) {
+            const uint32_t blk = smem_u32(smem) + s * kBytes + page_at;
+            float acc[GK][NB][4];
+#pragma unroll
+            for (int g = 0; g < GK; ++g) {
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                acc[g][nb][0] = acc[g][nb][2] = qc[g][nb][0];
+                acc[g][nb][1] = acc[g][nb][3] = qc[g][nb][1];
+              }
+              const uint32_t at = blk + (g * ps + o + t0) * 32 + 8 * j;
+              uint32_t x[2], y[2];
+              lds2(at, x[0], x[1]);
+              lds2(at + 256, y[0], y[1]);
+#pragma unroll
+              for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const uint32_t a0 = x[w] >> (8 * z) & 0x000f000fu, a2 = x[w] >> (8 * z) & 0x00f000f0u;
+                  const uint32_t a1 = y[w] >> (8 * z) & 0x000f000fu, a3 = y[w] >> (8 * z) & 0x00f000f0u;
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb)
+                    mma_f16(acc[g][nb], a0, a1, a2, a3, qf[g][nb][2 * w + z][0], qf[g][nb][2 * w + z][1]);
+                }
+            }
+            // Logits in base 2: columns 2 j, 2 j + 1 of positions tau(i) and 8 + tau(i).
+            float ks[GK][2], vs[GV][2];
+#pragma unroll
+            for (int g = 0; g < GK; ++g)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) ks[g][x] = lds_bf16(blk + kscales + (g * ps + o + t0 + 8 * x) * 2);
+            bool up = false;
+#pragma unroll
+            for (int g = 0; g < GV; ++g)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                vs[g][x] = lds_bf16(blk + vscales + (g * ps + o + t0 + 8 * x) * 2);
+                if (pos + t0 + 8 * x >= it.len) vs[g][x] = 0.f;   // (what lies there may be anything)
+                up |= vs[g][x] * vinv > 1.f;
+              }
+            float p[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                float v = 0.f;
+#pragma unroll
+                for (int g = 0; g < GK; ++g) v = fmaf(ks[g][x >> 1], acc[g][nb][x], v);
+                v *= factor[nb][x & 1];
+                if (pos + 16 > least && pos + t0 + 8 * (x >> 1) >= see[nb][x & 1]) v = -INFINITY;
+                p[nb][x] = v;
+                up |= v > mm[nb][x & 1] + 15.f;
+              }
+            if (__any_sync(0xffffffffu, up)) {
+              // A row's maximum has grown by more than 2^8, or a scale is above all so far.
+              float big = 0.f;
+#pragma unroll
+              for (int g = 0; g < GV; ++g) big = fmaxf(big, fmaxf(vs[g][0], vs[g][1]));
+              const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23;   // 2^(e - 127) <= it
+              const float vnew = fminf(vinv, __uint_as_float((e < 252u ? 253u - e : 1u) << 23)), vf = vnew / vinv;
+              vinv = vnew;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                float f[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  float m = fmaxf(p[nb][x], p[nb][x + 2]);
+#pragma unroll
+                  for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+                  m = fmaxf(mm[nb][x], m - 7.f);
+                  f[x] = ex2(mm[nb][x] - m);
+                  mm[nb][x] = m;
+                  l[nb][x] *= f[x];
+                  f[x] *= vf;
+                }
+#pragma unroll
+                for (int g = 0; g < GV; ++g)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    sp[g][nb][x] *= f[x & 1];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) oo[g][nb][t][x] *= f[x & 1];
+                  }
+              }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                p[nb][x] = ex2(p[nb][x] - mm[nb][x & 1]);
+                l[nb][x & 1] += p[nb][x];
+              }
+#pragma unroll
+            for (int g = 0; g < GV; ++g) {
+              const float s0 = vs[g][0] * vinv, s1 = vs[g][1] * vinv;
+              uint32_t b0[NB], b1[NB];
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                b0[nb] = transposed(half2_bits(p[nb][0] * s0, p[nb][1] * s0));
+                b1[nb] = transposed(half2_bits(p[nb][2] * s1, p[nb][3] * s1));
+                mma_f16(sp[g][nb], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b0[nb], b1[nb]);
+              }
+              const uint32_t at = blk + vcodes + (g * ps + o) * 32 + 4 * i;
+              const uint32_t x0 = lds1(at + v0 * 32), x1 = lds1(at + v1 * 32);
+              const uint32_t y0 = lds1(at + v0 * 32 + 256), y1 = lds1(at + v1 * 32 + 256);
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const uint32_t x = __byte_perm(x0, x1, w ? 0x7632 : 0x5410), y = __byte_perm(y0, y1, w ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const uint32_t a0 = x >> (8 * z) & 0x000f000fu, a1 = x >> (8 * z) & 0x00f000f0u;
+                  const uint32_t a2 = y >> (8 * z) & 0x000f000fu, a3 = y >> (8 * z) & 0x00f000f0u;
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb) mma_f16(oo[g][nb][2 * w + z], a0, a1, a2, a3, b0[nb], b1[nb]);
+                }
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sh->empty[s]));
+        }
+        // The warps' sums are joined.
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int z = 4; z < 32; z <<= 1) l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], z);
+            if (i == 0) {
+              sh->m[warp][nb * kBlock + 2 * j + x] = mm[nb][x];
+              sh->l[warp][nb * kBlock + 2 * j + x] = l[nb][x];
+            }
+          }
+      }
+      if (consumers_any(!ok || last)) break;
+      auto joined = [&](int r, float& m, float& sum) {
+        m = -INFINITY;
+        sum = 0.f;
+        bool any = false;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (sh->l[w][r] != 0.f) {
+            m = fmaxf(m, sh->m[w][r]);
+            any = true;
+          }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (sh->l[w][r] != 0.f) sum = fmaf(ex2(sh->m[w][r] - m), sh->l[w][r], sum);
+        return any;
+      };
+      const float back = 1.f / vinv;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float m, sum, f[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          joined(nb * kBlock + 2 * j + x, m, sum);
+          f[x] = l[nb][x] != 0.f ? ex2(mm[nb][x] - m) * back : 0.f;
+        }
+        const bool any = joined(nb * kBlock + warp, m, sum);   // the row that this warp writes
+        // Rows of DV floats in pieces of four, their order turned by the row: no two of eight
+        // lanes that store together share banks.
+        const int turn = (j & 1) | (j & 2) << 1;
+#pragma unroll
+        for (int g = 0; g < GV; ++g)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float sub = 8.f * sp[g][nb][x];
+              float4 v;
+              v.x = (oo[g][nb][2 * t][x] * 0x1p24f - sub) * f[x];
+              v.y = (oo[g][nb][2 * t][x + 2] * 0x1p20f - sub) * f[x];
+              v.z = (oo[g][nb][2 * t + 1][x] * 0x1p24f - sub) * f[x];
+              v.w = (oo[g][nb][2 * t + 1][x + 2] * 0x1p20f - sub) * f[x];
+              if (l[nb][x] == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+              reinterpret_cast<float4*>(sums + (warp * kBlock + 2 * j + x) * DV)[(16 * g + 2 * i + t) ^ turn] = v;
+            }
+        consumers_sync();
+        const int pk = it.first + nb * kBlock + warp;
+        if (pk < it.packed && lane < DV / 4) {
+          const int turned = lane ^ ((warp >> 1 & 1) | (warp >> 1 & 2) << 1);
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float4 y = reinterpret_cast<const float4*>(sums + (w * kBlock + warp) * DV)[turned];
+            v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+          }
+          if (it.slot < 0) {
+            const int64_t rh = (int64_t)(it.row0 + pk / a.G) * a.H_q + it.h * a.G + pk % a.G;
+            const float inv = any ? 1.f / sum : 0.f;
+            *reinterpret_cast<uint2*>(a.out + rh * DV + 4 * lane) =
+                any ? make_uint2(pack16<F16>(v.x * inv, v.y * inv), pack16<F16>(v.z * inv, v.w * inv)) : make_uint2(0, 0);
+            if (a.lse && lane == 0) a.lse[rh] = any ? (m + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+          } else {
+            const int64_t at = (int64_t)it.slot * ROWS + nb * kBlock + warp;
+            reinterpret_cast<float4*>(a.part + at * DV)[lane] = v;
+            if (lane == 0) a.ml[at] = make_float2(m, any ? sum : 0.f);
+          }
+        }
+        if (nb + 1 < NB) consumers_sync();
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && a.bits) a.bits[blockIdx.x] = sh->bits;
+}
+
+// Joins the parts of the items that CTA i of the attention began and others ended: a warp to a row.
+template <int DV, bool F16>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ Args a, int rows, int ctas) {
+  const int lane = threadIdx.x & 31, per = rows / kBlock;
+  const int i = blockIdx.x / per, r = (blockIdx.x - i * per) * kBlock + (threadIdx.x >> 5);
+  pdl_wait();   // (by every thread: whoever waits for this grid's end waits for the parts' too)
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    uint32_t bits = 0;
+    for (int x = lane; x < ctas; x += 32) bits |= a.bits[x];
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0) *a.status = bits;
+  }
+  const Kv4Join jn = a.join[i];
+  const int pk = jn.first + r;
+  if (jn.parts == 0 || pk >= jn.packed) return;
+  auto slot = [&](int x) { return (int64_t)(x == 0 ? 2 * i + 1 : 2 * (i + x)) * rows + r; };
+  float M = -INFINITY;
+  for (int x = lane; x < jn.parts; x += 32) {
+    const float2 v = a.ml[slot(x)];
+    if (v.y != 0.f) M = fmaxf(M, v.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int E = DV / 32;
+  float acc[E] = {}, L = 0.f;
+  bool any = false;
+#pragma unroll 8
+  for (int x = 0; x < jn.parts; ++x) {
+    const float2 v = a.ml[slot(x)];
+    const bool seen = v.y != 0.f;
+    any |= seen;
+    const float f = seen ? ex2(v.x - M) : 0.f;
+    L = fmaf(f, v.y, L);
+    const float* p = a.part + slot(x) * DV + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, p[e], acc[e]);
+  }
+  const float inv = any ? 1.f / L : 0.f;
+  const int64_t rh = (int64_t)(jn.row0 + pk / a.G) * a.H_q + jn.head * a.G + pk % a.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + rh * DV + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = any ? pack16<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
+  if (a.lse && lane == 0) a.lse[rh] = any ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
+}
+
+template <int DK, int DV, int NB, bool F16>
+cudaError_t launch_one(const Args& a, int grid, cudaStream_t st) {
+  constexpr size_t smem = smem_bytes<DK, DV, NB>();
+  static_assert(smem <= 232448 && ring_stages<DK, DV, NB>() >= 2, "shared memory of one CTA");
+  auto kernel = kv4_attn_kernel<DK, DV, NB, F16>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, st, a);
+  if (e != cudaSuccess || !a.join) return e;
+  return launch_pdl(kv4_join_kernel<DV, F16>, dim3((unsigned)(grid * NB)), dim3(256), 0, st, a, NB * kBlock, grid);
+}
+
+template <int DK, int DV>
+cudaError_t launch_width(const Args& a, int rows, bool f16, int grid, cudaStream_t st) {
+  if (rows == kBlock) return f16 ? launch_one<DK, DV, 1, true>(a, grid, st) : launch_one<DK, DV, 1, false>(a, grid, st);
+  return f16 ? launch_one<DK, DV, 2, true>(a, grid, st) : launch_one<DK, DV, 2, false>(a, grid, st);
+}
+
+}  // namespace
+
+Kv4Shape kv4_shape(const dsa_kv4_cache& c, const dsa_kv4_problem& p) {
+  Kv4Shape s;
+  const int64_t G = p.H_q / c.H_kv, most = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
+  const int64_t held = (int64_t)c.page_size * c.table_cols, longest = p.L_max < held ? p.L_max : held;
+  s.rows = most * G <= kBlock ? kBlock : 2 * kBlock;
+  // No more CTAs than there can be stages.
+  int64_t blocks = c.B * ((most * G + s.rows - 1) / s.rows);
+  if (blocks > p.R * G / s.rows + c.B) blocks = p.R * G / s.rows + c.B;
+  const int64_t stages = longest > kStage ? (longest + kStage - 1) / kStage : 1;
+  const int64_t slots = s.rows == kBlock ? kKv4Slots : kKv4Slots / 2;
+  const int64_t items = blocks * c.H_kv;
+  s.grid = (int)(items >= slots || items * stages >= slots ? slots : items * stages);
+  if (s.grid < 1) s.grid = 1;
+  s.join = stages > 1;
+  return s;
+}
+
+cudaError_t launch_kv4_attn(const dsa_kv4_cache& c, const CacheArgs& ca, const dsa_kv4_problem& p, const Kv4Shape& s,
+                            uint16_t* out, float* lse, char* ws, float* ml, float* part, cudaStream_t st,
+                            const TestHooks* hooks) {
+  Args a;
+  std::memset(&a, 0, sizeof a);
+  a.c = ca;
+  a.q = p.q; a.row_offsets = p.row_offsets; a.row_len = p.row_len;
+  a.out = out; a.lse = lse; a.part = part; a.ml = reinterpret_cast<float2*>(ml);
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  if (s.join) {
+    a.join = reinterpret_cast<Kv4Join*>(ws + kKv4DescOffset);
+    a.bits = a.status + kKv4Bits;
+  }
+  a.q_stride = p.q_stride ? p.q_stride : (int64_t)p.H_q * c.D_k;
+  a.wait_ns = hooks ? hooks->wait_ns : kDefaultWaitNs;
+  a.test_no_load = hooks ? hooks->tile_no_load : 0;
+  a.R = p.R; a.H_q = p.H_q; a.G = p.H_q / c.H_kv; a.L_max = p.L_max;
+  a.c2 = (float)(p.softmax_scale * 1.4426950408889634);
+  const bool f16 = p.flags & DSA_FLAG_FP16;
+  if (c.D_k == 64) return launch_width<64, 64>(a, s.rows, f16, s.grid, st);
+  if (c.D_k == 128) return launch_width<128, 128>(a, s.rows, f16, s.grid, st);
+  return launch_width<192, 128>(a, s.rows, f16, s.grid, st);
+}
+
+}  // namespace dsa

@@ -22,6 +22,7 @@
 #include "dsa.h"
 #include "dsa_dense.h"
 #include "dsa_linear.h"
+#include "dsa_kv4.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -73,6 +74,9 @@ DSA_API dsa_status dsa_test_dense_missing_tile(const dsa_dense_problem* p, uint1
 DSA_API dsa_status dsa_test_linear_missing_tile(const dsa_linear_problem* p, const float* state_in, float* state_out,
                                                 uint16_t* out, void* ws, size_t ws_bytes, int64_t limit_ns,
                                                 void* stream);
+/* dsa_kv4_attn, every CTA arming the barrier of its first stage but issuing no copy for it. */
+DSA_API dsa_status dsa_test_kv4_missing_stage(const dsa_kv4_cache* c, const dsa_kv4_problem* p, uint16_t* out, float* lse,
+                                              void* ws, size_t ws_bytes, int64_t limit_ns, void* stream);
 
 #ifdef __cplusplus
 }
