@@ -12,7 +12,8 @@ namespace dsa {
 struct DenseShape {
   int nw, tiles, splits, tail, tail_parts;
 };
-DenseShape dense_shape(const dsa_dense_problem& p);
+// nw: 0, or the row tiles of an item where the caller wants a kernel that has them.
+DenseShape dense_shape(const dsa_dense_problem& p, int nw = 0);
 
 // The workspace: the status block with the counter of items, the parts.  Atomics on
 // a line slow down every access within 4 KB of it (six requests of 22 rows in all:

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dense.cuh"
 #include "dsa_kv4.h"
 
 namespace dsa {
@@ -52,6 +53,13 @@ struct Kv4Shape {
   bool join;
 };
 Kv4Shape kv4_shape(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
+// The kernel for many rows (kv4_tile.cu): its problem as dense attention's, and the launch.
+dsa_dense_problem kv4_dense(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
+cudaError_t launch_kv4_tile(const dsa_kv4_cache& c, const CacheArgs& ca, const dsa_kv4_problem& p, const DenseShape& s,
+                            uint16_t* out, float* lse, float* part, float* ml, uint32_t* status, cudaStream_t st,
+                            const TestHooks* hooks = nullptr);
+// Whether a call goes to that kernel.
+bool kv4_many_rows(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
 inline size_t kv4_parts(const Kv4Shape& s) { return s.join ? (size_t)2 * s.grid * s.rows : 0; }
 cudaError_t launch_kv4_attn(const dsa_kv4_cache& c, const CacheArgs& ca, const dsa_kv4_problem& p, const Kv4Shape& s,
                             uint16_t* out, float* lse, char* ws, float* ml, float* part, cudaStream_t st,

@@ -697,6 +697,11 @@ cudaError_t launch_width(const Args& a, int rows, bool f16, int grid, cudaStream
 
 }  // namespace
 
+bool kv4_many_rows(const dsa_kv4_cache& c, const dsa_kv4_problem& p) {
+  const int64_t most = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
+  return most * (p.H_q / c.H_kv) > 64;
+}
+
 Kv4Shape kv4_shape(const dsa_kv4_cache& c, const dsa_kv4_problem& p) {
   Kv4Shape s;
   const int64_t G = p.H_q / c.H_kv, most = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
