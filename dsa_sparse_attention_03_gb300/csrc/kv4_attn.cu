@@ -37,6 +37,7 @@
 // All waits are bounded; on expiry the CTA stops and drains its copies.
 #include "kv4.cuh"
 
+#include <climits>
 #include <cstring>
 
 #include "tc.cuh"
@@ -167,13 +168,13 @@ template <int DK, int DV>
 constexpr uint32_t kStageBytes = kStage * (DK + DV) * 17 / 32;
 template <int DK, int DV, int NB>
 __host__ __device__ constexpr int ring_stages() {
-  constexpr int rest = (NB == 1 ? 113 : 227) * 1024 - (int)sizeof(Shared) - kWarps * kBlock * DV * 4;
+  constexpr int rest = (NB == 1 ? 113 : 227) * 1024 - (int)sizeof(Shared) - kWarps / 2 * kBlock * DV * 4;
   constexpr int s = rest / (int)kStageBytes<DK, DV>;
-  return s < 8 ? s : 8;
+  return s < 8 ? s / 2 * 2 : 8;   // (even: a stage's place belongs to one half of the warps)
 }
 template <int DK, int DV, int NB>
 __host__ __device__ constexpr size_t smem_bytes() {
-  return (size_t)ring_stages<DK, DV, NB>() * kStageBytes<DK, DV> + kWarps * kBlock * DV * 4 + sizeof(Shared);
+  return (size_t)ring_stages<DK, DV, NB>() * kStageBytes<DK, DV> + kWarps / 2 * kBlock * DV * 4 + sizeof(Shared);
 }
 
 template <int DK, int DV, int NB, bool F16>
@@ -181,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   constexpr int GK = DK / 64, GV = DV / 64, ROWS = NB * kBlock, NS = ring_stages<DK, DV, NB>();
   constexpr uint32_t kBytes = kStageBytes<DK, DV>;
   extern __shared__ __align__(128) unsigned char smem[];
-  float* sums = reinterpret_cast<float*>(smem + NS * kBytes);        // [warps, 8, DV]
-  Shared* sh = reinterpret_cast<Shared*>(sums + kWarps * kBlock * DV);
+  float* sums = reinterpret_cast<float*>(smem + NS * kBytes);        // [4, 8, DV]
+  Shared* sh = reinterpret_cast<Shared*>(sums + kWarps / 2 * kBlock * DV);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   const int reach = (int)min((int64_t)a.L_max, (int64_t)a.c.cols << a.c.ps_log2);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(sh->full[i]), 1);
-      mbar_init(bar(sh->empty[i]), kWarps);
+      mbar_init(bar(sh->empty[i]), kWarps / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(sh->ifull[i]), 1);
@@ -331,14 +332,27 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   } else {
     // ------------------------------------------------------------ products and softmax
     const int i = lane >> 2, j = lane & 3;
-    // Row i of a fragment is position tau(i) of eight: so that the four positions 2 j (and the
-    // four 2 j + 1) whose V a load takes, and the first four rows of K, lie in different banks.
-    auto tau = [](int x) { return x ^ (x >> 2); };
-    const int t0 = tau(i), v0 = tau(2 * j), v1 = tau(2 * j + 1);
-    const int ps = a.c.ps, page = (16 * warp) >> a.c.ps_log2, o = (16 * warp) & (ps - 1);
-    const uint32_t vcodes = ps * (DK / 2), kscales = ps * ((DK + DV) / 2), vscales = kscales + ps * (DK / 32);
-    const uint32_t page_at = page * a.c.block;
-    int n = 0;
+    // Rows i and 8 + i of a fragment are a pair of positions, 2 sigma(i) and the next one, in this
+    // order or the other: one load brings both scales, and the first four rows of K that a
+    // load takes lie in different banks.
+    auto sigma = [](int x) { return x ^ (x >> 1 & 1); };
+    const int pair = 2 * sigma(i), ta = pair + (i & 1), tb = pair + (~i & 1);
+    const uint32_t sel_a = i & 1 ? 0x3244 : 0x1044, sel_b = i & 1 ? 0x1044 : 0x3244;   // its bf16 scale as fp32
+    // Row of V that this lane names for ldmatrix: matrix lane / 8 is rows 0.. or 8.. and half a group's codes.
+    const int vr = lane & 7, vrow = 2 * sigma(vr) + ((vr ^ lane >> 3) & 1);
+    const int ps = a.c.ps, p0 = 32 * (warp & 3), p1 = p0 + 16;      // the warp's positions in a stage: two tiles
+    uint32_t blk[2] = {(p0 >> a.c.ps_log2) * a.c.block, (p1 >> a.c.ps_log2) * a.c.block};
+    const int o[2] = {p0 & (ps - 1), p1 & (ps - 1)};
+    const uint32_t pages = 1u << (p0 >> a.c.ps_log2) | 1u << (p1 >> a.c.ps_log2);
+    uint32_t k_at[2], s_at[2], v_at[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      k_at[t] = smem_u32(smem) + blk[t] + (o[t] + ta) * 32 + 8 * j;
+      s_at[t] = smem_u32(smem) + blk[t] + ps * ((DK + DV) / 2) + (o[t] + pair) * 2;
+      v_at[t] = smem_u32(smem) + blk[t] + ps * (DK / 2) + (o[t] + vrow) * 32 + (lane >> 4) * 16;
+    }
+    const uint32_t tab = (tb - ta) * 32;
+    int n0 = 0;                  // stages of earlier items
     for (int k = 0;; ++k) {
       bool ok = wait_bar_warp(bar(sh->ifull[k & 1]), (k >> 1) & 1, wc);
       Item it;
@@ -348,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(bar(sh->ifree[k & 1]));
       uint32_t qf[GK][NB][4][2];
-      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], sp[GV][NB][4], oo[GV][NB][4][4], vinv = 0x1p126f;
+      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], sp[GV][NB][4], oo[GV][NB][4][4], vinv = 1.f;
       int see[NB][2];
       if (!last) {
         // The queries, scaled to fp16's upper range by a power of two for each row.
@@ -401,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
             factor[nb][x] = a.c2 * (0x1p24f / __shfl_sync(0xffffffffu, up, 4 * (2 * j + x)));
             const int r = it.first + nb * kBlock + 2 * j + x;
             see[nb][x] = r < it.packed ? min(max(a.row_len[it.row0 + r / a.G], 0), reach) : it.len;
-            mm[nb][x] = -1e30f;
+            mm[nb][x] = 0.f;
             l[nb][x] = 0.f;
           }
         }
@@ -419,131 +433,170 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) least = min(least, min(see[nb][0], see[nb][1]));
         least = __reduce_min_sync(0xffffffffu, least);
-        for (int st = 0; st < it.stages; ++st, ++n) {
+        bool first = true;         // no positions so far
+        // Every other stage is this warp's.
+        int pos = it.stage * kStage + p0 + ((n0 ^ (warp >> 2)) & 1) * kStage;   // the warp's first position
+        for (int n = n0 + ((n0 ^ (warp >> 2)) & 1); n < n0 + it.stages; n += 2, pos += 2 * kStage) {
           const int s = n % NS;
           if (!(ok = wait_bar_warp(bar(sh->full[s]), (n / NS) & 1, wc))) break;
-          const int pos = (it.stage + st) * kStage + 16 * warp;     // the warp's first position
-          if (pos < it.len && (sh->pages[s] >> page & 1u)) {
-            const uint32_t blk = smem_u32(smem) + s * kBytes + page_at;
-            float acc[GK][NB][4];
+          const uint32_t have = sh->pages[s] & pages;
+          if (pos < it.len && have) {
+            const uint32_t ring = s * kBytes;
+            float e[2][NB][4], vs[2][GV][2];
 #pragma unroll
-            for (int g = 0; g < GK; ++g) {
+            for (int t = 0; t < 2; ++t) {
+              float acc[GK][NB][4];
+              const uint32_t ka = ring + k_at[t], sa = ring + s_at[t];
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                acc[g][nb][0] = acc[g][nb][2] = qc[g][nb][0];
-                acc[g][nb][1] = acc[g][nb][3] = qc[g][nb][1];
+              for (int g = 0; g < GK; ++g) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  acc[g][nb][0] = acc[g][nb][2] = qc[g][nb][0];
+                  acc[g][nb][1] = acc[g][nb][3] = qc[g][nb][1];
+                }
+                const uint32_t at = ka + g * ps * 32;
+                uint32_t x[2], y[2];
+                lds2(at, x[0], x[1]);
+                lds2(at + tab, y[0], y[1]);
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    const uint32_t a0 = x[w] >> (8 * z) & 0x000f000fu, a2 = x[w] >> (8 * z) & 0x00f000f0u;
+                    const uint32_t a1 = y[w] >> (8 * z) & 0x000f000fu, a3 = y[w] >> (8 * z) & 0x00f000f0u;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                      mma_f16(acc[g][nb], a0, a1, a2, a3, qf[g][nb][2 * w + z][0], qf[g][nb][2 * w + z][1]);
+                  }
               }
-              const uint32_t at = blk + (g * ps + o + t0) * 32 + 8 * j;
-              uint32_t x[2], y[2];
-              lds2(at, x[0], x[1]);
-              lds2(at + 256, y[0], y[1]);
+              // Logits in base 2, less m: columns 2 j, 2 j + 1 of positions ta and tb.
 #pragma unroll
-              for (int w = 0; w < 2; ++w)
+              for (int g = 0; g < GK; ++g) {
+                const uint32_t w = lds1(sa + g * ps * 2);
+                const float k0 = __uint_as_float(__byte_perm(w, 0, sel_a)), k1 = __uint_as_float(__byte_perm(w, 0, sel_b));
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const uint32_t a0 = x[w] >> (8 * z) & 0x000f000fu, a2 = x[w] >> (8 * z) & 0x00f000f0u;
-                  const uint32_t a1 = y[w] >> (8 * z) & 0x000f000fu, a3 = y[w] >> (8 * z) & 0x00f000f0u;
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                  for (int nb = 0; nb < NB; ++nb)
-                    mma_f16(acc[g][nb], a0, a1, a2, a3, qf[g][nb][2 * w + z][0], qf[g][nb][2 * w + z][1]);
+                  for (int x = 0; x < 4; ++x)
+                    e[t][nb][x] = g == 0 ? (x < 2 ? k0 : k1) * acc[g][nb][x] : fmaf(x < 2 ? k0 : k1, acc[g][nb][x], e[t][nb][x]);
+              }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) e[t][nb][x] = fmaf(e[t][nb][x], factor[nb][x & 1], -mm[nb][x & 1]);
+#pragma unroll
+              for (int g = 0; g < GV; ++g) {
+                const uint32_t w = lds1(sa + (GK + g) * ps * 2);
+                vs[t][g][0] = __uint_as_float(__byte_perm(w, 0, sel_a)) * vinv;
+                vs[t][g][1] = __uint_as_float(__byte_perm(w, 0, sel_b)) * vinv;
+              }
+            }
+            if (pos + 32 > least || have != pages) {
+              // Positions that a row does not see, or whose page the pool does not have.
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int at = have >> ((t ? p1 : p0) >> a.c.ps_log2) & 1u ? pos + 16 * t + (x ? tb : ta) : INT_MAX;
+#pragma unroll
+                  for (int g = 0; g < GV; ++g)
+                    if (at >= it.len) vs[t][g][x] = 0.f;   // (what lies there may be anything)
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb) {
+                    if (at >= see[nb][0]) e[t][nb][2 * x] = -INFINITY;
+                    if (at >= see[nb][1]) e[t][nb][2 * x + 1] = -INFINITY;
+                  }
                 }
             }
-            // Logits in base 2: columns 2 j, 2 j + 1 of positions tau(i) and 8 + tau(i).
-            float ks[GK][2], vs[GV][2];
+            float top = -INFINITY, big = 0.f;
 #pragma unroll
-            for (int g = 0; g < GK; ++g)
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-              for (int x = 0; x < 2; ++x) ks[g][x] = lds_bf16(blk + kscales + (g * ps + o + t0 + 8 * x) * 2);
-            bool up = false;
+              for (int nb = 0; nb < NB; ++nb) top = max3(max3(e[t][nb][0], e[t][nb][1], top), e[t][nb][2], e[t][nb][3]);
 #pragma unroll
-            for (int g = 0; g < GV; ++g)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                vs[g][x] = lds_bf16(blk + vscales + (g * ps + o + t0 + 8 * x) * 2);
-                if (pos + t0 + 8 * x >= it.len) vs[g][x] = 0.f;   // (what lies there may be anything)
-                up |= vs[g][x] * vinv > 1.f;
-              }
-            float p[NB][4];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                float v = 0.f;
-#pragma unroll
-                for (int g = 0; g < GK; ++g) v = fmaf(ks[g][x >> 1], acc[g][nb][x], v);
-                v *= factor[nb][x & 1];
-                if (pos + 16 > least && pos + t0 + 8 * (x >> 1) >= see[nb][x & 1]) v = -INFINITY;
-                p[nb][x] = v;
-                up |= v > mm[nb][x & 1] + 15.f;
-              }
-            if (__any_sync(0xffffffffu, up)) {
+              for (int g = 0; g < GV; ++g) big = max3(vs[t][g][0], vs[t][g][1], big);
+            }
+            if (__any_sync(0xffffffffu, first || top > 15.f || big > 1.f)) {
               // A row's maximum has grown by more than 2^8, or a scale is above all so far.
-              float big = 0.f;
+              const uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23;   // 2^(x - 127) <= it
+              const float vf0 = __uint_as_float((x < 252u ? 253u - x : 1u) << 23);             // half its inverse, about
+              const float vf = first ? vf0 : fminf(vf0, 1.f);
+              vinv *= vf;
 #pragma unroll
-              for (int g = 0; g < GV; ++g) big = fmaxf(big, fmaxf(vs[g][0], vs[g][1]));
-              const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23;   // 2^(e - 127) <= it
-              const float vnew = fminf(vinv, __uint_as_float((e < 252u ? 253u - e : 1u) << 23)), vf = vnew / vinv;
-              vinv = vnew;
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int g = 0; g < GV; ++g) {
+                  vs[t][g][0] *= vf;
+                  vs[t][g][1] *= vf;
+                }
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 float f[2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  float m = fmaxf(p[nb][x], p[nb][x + 2]);
+                for (int y = 0; y < 2; ++y) {
+                  float m = max3(e[0][nb][y], e[0][nb][y + 2], fmaxf(e[1][nb][y], e[1][nb][y + 2]));
 #pragma unroll
                   for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-                  m = fmaxf(mm[nb][x], m - 7.f);
-                  f[x] = ex2(mm[nb][x] - m);
-                  mm[nb][x] = m;
-                  l[nb][x] *= f[x];
-                  f[x] *= vf;
-                }
+                  // (a row that sees none of the first positions sees none of this item's)
+                  m = first ? (m == -INFINITY ? 0.f : m - 7.f) : fmaxf(m - 7.f, 0.f);
+                  f[y] = first ? 1.f : ex2(-m);
+                  mm[nb][y] += m;
+                  l[nb][y] *= f[y];
+                  f[y] *= vf;
 #pragma unroll
-                for (int g = 0; g < GV; ++g)
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    sp[g][nb][x] *= f[x & 1];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) oo[g][nb][t][x] *= f[x & 1];
+                  for (int t = 0; t < 2; ++t) {
+                    e[t][nb][y] -= m;
+                    e[t][nb][y + 2] -= m;
                   }
+                }
+                if (!first)
+#pragma unroll
+                  for (int g = 0; g < GV; ++g)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                      sp[g][nb][y] *= f[y & 1];
+#pragma unroll
+                      for (int t = 0; t < 4; ++t) oo[g][nb][t][y] *= f[y & 1];
+                    }
               }
+              first = false;
             }
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                p[nb][x] = ex2(p[nb][x] - mm[nb][x & 1]);
-                l[nb][x & 1] += p[nb][x];
-              }
+              for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int g = 0; g < GV; ++g) {
-              const float s0 = vs[g][0] * vinv, s1 = vs[g][1] * vinv;
-              uint32_t b0[NB], b1[NB];
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                b0[nb] = transposed(half2_bits(p[nb][0] * s0, p[nb][1] * s0));
-                b1[nb] = transposed(half2_bits(p[nb][2] * s1, p[nb][3] * s1));
-                mma_f16(sp[g][nb], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b0[nb], b1[nb]);
-              }
-              const uint32_t at = blk + vcodes + (g * ps + o) * 32 + 4 * i;
-              const uint32_t x0 = lds1(at + v0 * 32), x1 = lds1(at + v1 * 32);
-              const uint32_t y0 = lds1(at + v0 * 32 + 256), y1 = lds1(at + v1 * 32 + 256);
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const uint32_t x = __byte_perm(x0, x1, w ? 0x7632 : 0x5410), y = __byte_perm(y0, y1, w ? 0x7632 : 0x5410);
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const uint32_t a0 = x >> (8 * z) & 0x000f000fu, a1 = x >> (8 * z) & 0x00f000f0u;
-                  const uint32_t a2 = y >> (8 * z) & 0x000f000fu, a3 = y >> (8 * z) & 0x00f000f0u;
-#pragma unroll
-                  for (int nb = 0; nb < NB; ++nb) mma_f16(oo[g][nb][2 * w + z], a0, a1, a2, a3, b0[nb], b1[nb]);
+                for (int x = 0; x < 4; ++x) {
+                  e[t][nb][x] = ex2(e[t][nb][x]);
+                  l[nb][x & 1] += e[t][nb][x];
                 }
+#pragma unroll
+              for (int g = 0; g < GV; ++g) {
+                uint32_t b0[NB], b1[NB], v[4];
+                ldsm_x4_t(ring + v_at[t] + g * ps * 32, v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  b0[nb] = transposed(half2_bits(e[t][nb][0] * vs[t][g][0], e[t][nb][1] * vs[t][g][0]));
+                  b1[nb] = transposed(half2_bits(e[t][nb][2] * vs[t][g][1], e[t][nb][3] * vs[t][g][1]));
+                  mma_f16(sp[g][nb], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b0[nb], b1[nb]);
+                }
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    const uint32_t x = v[2 * w] >> (8 * z), y = v[2 * w + 1] >> (8 * z);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                      mma_f16(oo[g][nb][2 * w + z], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, b0[nb],
+                              b1[nb]);
+                  }
               }
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sh->empty[s]));
         }
+        n0 += it.stages;
         // The warps' sums are joined.
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -583,32 +636,57 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           f[x] = l[nb][x] != 0.f ? ex2(mm[nb][x] - m) * back : 0.f;
         }
         const bool any = joined(nb * kBlock + warp, m, sum);   // the row that this warp writes
-        // Rows of DV floats in pieces of four, their order turned by the row: no two of eight
-        // lanes that store together share banks.
-        const int turn = (j & 1) | (j & 2) << 1;
+        // Columns 64 g + 32 w + 4 i .. of rows 2 j and 2 j + 1, in the common scale.
+        float4 v[GV][2][2];
 #pragma unroll
         for (int g = 0; g < GV; ++g)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const float sub = 8.f * sp[g][nb][x];
-              float4 v;
-              v.x = (oo[g][nb][2 * t][x] * 0x1p24f - sub) * f[x];
-              v.y = (oo[g][nb][2 * t][x + 2] * 0x1p20f - sub) * f[x];
-              v.z = (oo[g][nb][2 * t + 1][x] * 0x1p24f - sub) * f[x];
-              v.w = (oo[g][nb][2 * t + 1][x + 2] * 0x1p20f - sub) * f[x];
-              if (l[nb][x] == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-              reinterpret_cast<float4*>(sums + (warp * kBlock + 2 * j + x) * DV)[(16 * g + 2 * i + t) ^ turn] = v;
+              float4& y = v[g][w][x];
+              y.x = (oo[g][nb][2 * w][x] * 0x1p24f - sub) * f[x];
+              y.y = (oo[g][nb][2 * w][x + 2] * 0x1p20f - sub) * f[x];
+              y.z = (oo[g][nb][2 * w + 1][x] * 0x1p24f - sub) * f[x];
+              y.w = (oo[g][nb][2 * w + 1][x + 2] * 0x1p20f - sub) * f[x];
+              if (l[nb][x] == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
             }
+        // The upper four warps hand theirs to the lower four, lane to lane; these lay down
+        // rows of DV floats in pieces of four, their order turned by the row (no two of eight
+        // lanes that store together share banks), and each warp adds up one row.
+        float4* mine = reinterpret_cast<float4*>(sums) + (warp & 3) * GV * 4 * 32;
+        if (warp >= 4) {
+#pragma unroll
+          for (int g = 0; g < GV; ++g)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mine[(g * 4 + w) * 32 + lane] = v[g][w >> 1][w & 1];
+        }
+        consumers_sync();
+        if (warp < 4) {
+#pragma unroll
+          for (int g = 0; g < GV; ++g)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float4 y = mine[(g * 4 + w) * 32 + lane];
+              float4& x = v[g][w >> 1][w & 1];
+              x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+            }
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < GV; ++g)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) mine[(2 * j + x) * (DV / 4) + ((16 * g + 8 * w + i) ^ 2 * j)] = v[g][w][x];
+        }
         consumers_sync();
         const int pk = it.first + nb * kBlock + warp;
         if (pk < it.packed && lane < DV / 4) {
-          const int turned = lane ^ ((warp >> 1 & 1) | (warp >> 1 & 2) << 1);
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float4 y = reinterpret_cast<const float4*>(sums + (w * kBlock + warp) * DV)[turned];
+          for (int w = 0; w < 4; ++w) {
+            const float4 y = reinterpret_cast<const float4*>(sums)[(w * kBlock + warp) * (DV / 4) + (lane ^ (warp & 6))];
             v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
           }
           if (it.slot < 0) {
@@ -631,11 +709,18 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   if (tid == 0 && a.bits) a.bits[blockIdx.x] = sh->bits;
 }
 
-// Joins the parts of the items that CTA i of the attention began and others ended: a warp to a row.
+// Joins the parts of the items that CTA i of the attention began and others ended: four warps to
+// a row, each a quarter of the parts with up to eight of them in flight (one warp to a row walked
+// its parts at one load's latency each: 21 us for 32 parts).
+constexpr int kJoinRows = 2;   // of a CTA
+
 template <int DV, bool F16>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ Args a, int rows, int ctas) {
-  const int lane = threadIdx.x & 31, per = rows / kBlock;
-  const int i = blockIdx.x / per, r = (blockIdx.x - i * per) * kBlock + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_constant__ Args a, int rows, int ctas) {
+  constexpr int E = DV / 32;
+  __shared__ float2 ml[kJoinRows][4];
+  __shared__ float sums[kJoinRows][4][DV];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp & 3, per = rows / kJoinRows;
+  const int i = blockIdx.x / per, r = (blockIdx.x - i * per) * kJoinRows + (warp >> 2);
   pdl_wait();   // (by every thread: whoever waits for this grid's end waits for the parts' too)
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x < 32) {
@@ -646,28 +731,68 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
   }
   const Kv4Join jn = a.join[i];
   const int pk = jn.first + r;
-  if (jn.parts == 0 || pk >= jn.packed) return;
-  auto slot = [&](int x) { return (int64_t)(x == 0 ? 2 * i + 1 : 2 * (i + x)) * rows + r; };
-  float M = -INFINITY;
-  for (int x = lane; x < jn.parts; x += 32) {
-    const float2 v = a.ml[slot(x)];
-    if (v.y != 0.f) M = fmaxf(M, v.x);
+  if (jn.parts == 0) return;
+  auto slot = [&](int x) { return (x == 0 ? 2 * i + 1 : 2 * (i + x)) * rows + r; };
+  float M = -INFINITY, L = 0.f, acc[E] = {};
+  if (pk < jn.packed) {
+    for (int x = w + 4 * lane; x < jn.parts; x += 128) {
+      const float2 v = a.ml[slot(x)];
+      if (v.y != 0.f) M = fmaxf(M, v.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int base = w; base < jn.parts; base += 128) {
+      const int x = base + 4 * lane;
+      float f = 0.f;
+      if (x < jn.parts) {
+        const float2 v = a.ml[slot(x)];
+        f = v.y != 0.f ? ex2(v.x - M) : 0.f;   // (a part that saw nothing counts nothing)
+        L = fmaf(f, v.y, L);
+      }
+      const int n = min((jn.parts - base + 3) / 4, 32);
+      for (int y = 0; y < n; y += 8) {
+        float v[8][E];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float* p = a.part + (int64_t)slot(base + 4 * min(y + z, n - 1)) * DV + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[z][e] = p[e];
+        }
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float g = __shfl_sync(0xffffffffu, f, (y + z) & 31);
+          if (y + z < n)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(g, v[z][e], acc[e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) ml[warp >> 2][w] = make_float2(M, L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[warp >> 2][w][lane * E + e] = acc[e];
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  constexpr int E = DV / 32;
-  float acc[E] = {}, L = 0.f;
+  __syncthreads();
+  if (w != 0 || pk >= jn.packed) return;
+  M = -INFINITY;
   bool any = false;
-#pragma unroll 8
-  for (int x = 0; x < jn.parts; ++x) {
-    const float2 v = a.ml[slot(x)];
-    const bool seen = v.y != 0.f;
-    any |= seen;
-    const float f = seen ? ex2(v.x - M) : 0.f;
-    L = fmaf(f, v.y, L);
-    const float* p = a.part + slot(x) * DV + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, p[e], acc[e]);
+  for (int x = 0; x < 4; ++x)
+    if (ml[warp >> 2][x].y != 0.f) {
+      M = fmaxf(M, ml[warp >> 2][x].x);
+      any = true;
+    }
+  L = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const float2 v = ml[warp >> 2][x];
+    const float f = v.y != 0.f ? ex2(v.x - M) : 0.f;
+    L = fmaf(f, v.y, L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, sums[warp >> 2][x][lane * E + e], acc[e]);
   }
   const float inv = any ? 1.f / L : 0.f;
   const int64_t rh = (int64_t)(jn.row0 + pk / a.G) * a.H_q + jn.head * a.G + pk % a.G;
@@ -686,7 +811,8 @@ cudaError_t launch_one(const Args& a, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, st, a);
   if (e != cudaSuccess || !a.join) return e;
-  return launch_pdl(kv4_join_kernel<DV, F16>, dim3((unsigned)(grid * NB)), dim3(256), 0, st, a, NB * kBlock, grid);
+  return launch_pdl(kv4_join_kernel<DV, F16>, dim3((unsigned)(grid * NB * kBlock / kJoinRows)), dim3(128 * kJoinRows), 0, st, a,
+                    NB * kBlock, grid);
 }
 
 template <int DK, int DV>
