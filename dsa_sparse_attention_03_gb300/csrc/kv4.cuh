@@ -18,8 +18,12 @@ struct TurnArgs {
   int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
   float eps;
   int R, B, H_q, H_kv, rot, first, adjacent;   // H_q (H_kv) = 0: no q (k)
-  int chunks;                                  // CTAs to a row
+  int q_runs, k_runs, v_runs;                  // runs of 2^run_log2 heads that a row's q, k and v are cut into
+  int run_log2, rows_log2, split;              // rows of a CTA; or CTAs of a row, each `units` runs of it
+  int units;
 };
+// Sets the last ones: `at_once` heads fit a warp, a run has up to `most` (powers of two).
+void deal_heads(TurnArgs& t, int at_once, int most, int H_k, int H_v);
 
 struct CacheArgs {
   uint8_t* pages;

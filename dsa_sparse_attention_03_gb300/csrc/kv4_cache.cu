@@ -9,8 +9,8 @@
 //
 // Borders.  A key that was normed or rotated is off by some 2^-20 in fp32, so near the border
 // between two codes (or two scales) fp32 cannot tell which one exact arithmetic gives.  Each
-// value carries a bound of its error; where a border lies within it, the value is computed
-// again in fp64 (about one head in 600).  What the cache holds then does not depend on how
+// head has a bound of its values' errors; where a border lies within it, the value is computed
+// again in fp64 (about one head in 150).  What the cache holds then does not depend on how
 // sums were ordered.  Values that are neither normed nor rotated are quantised exactly: x has at
 // most 11 significant bits and a scale 4, so the fp32 quotient is a half only where the real
 // one is.
@@ -28,16 +28,21 @@ constexpr int kThreads = 256;
 // A normed and rotated value's error in fp32, relative to its own and its partner's
 // magnitudes: in units of 2^-24, the sum of squares over a head 13 (8 in a lane, 5 between
 // lanes) and its mean and eps 2, of which the root halves to 7.5, the root 4 (2 ulp), two
-// products 2, sine or cosine 4 (the angle's conversion and 2 ulp), the rotation 2: 19.5.
+// products 2, sine or cosine 4, the rotation 2: 19.5.
 constexpr float kTurnErr = 20.f * 0x1p-24f;
 
-// x >= 0 to four significant bits, ties to even; below 2^-126: 0.
-__device__ __forceinline__ float four_bits(float x) {
-  if (x < 0x1p-126f) return x >= 0x1.fp-127f ? 0x1p-126f : 0.f;
-  const uint32_t u = __float_as_uint(x);
-  if (u >= 0x7f800000u) return __uint_as_float(0x7fc00000u);   // (a group that is not finite)
-  return __uint_as_float((u + 0x7ffffu + ((u >> 20) & 1u)) & ~0xfffffu);
+// max / 7 to four significant bits, ties to even; below 2^-126: 0.  From the product with the rounded
+// 1 / 7, whose first four bits may be one too few; on which side of the border above them max / 7
+// lies is then told exactly, by seven times the border (five significant bits).
+__device__ __forceinline__ float group_scale(float top) {
+  const uint32_t base = __float_as_uint(top * (1.f / 7.f)) & ~0xfffffu;
+  const float border = 7.f * __uint_as_float(base | 0x80000u);
+  const bool up = top > border || (top == border && (base >> 20 & 1u));
+  float scale = __uint_as_float(up ? base + 0x100000u : base);
+  if (top < 0x1.cp-124f) scale = top >= 0x1.b2p-124f ? 0x1p-126f : 0.f;      // 7, and 7 * 31 / 32, times 2^-126
+  return top <= 3.4028234e38f ? scale : __uint_as_float(0x7fc00000u);        // (a group that is not finite)
 }
+// x >= 0 to four significant bits, in the same way.
 __device__ __forceinline__ double four_bits(double x) {
   if (x < 0x1p-126) return x >= 0x1.fp-127 ? 0x1p-126 : 0.0;
   const uint64_t u = (uint64_t)__double_as_longlong(x);
@@ -45,190 +50,332 @@ __device__ __forceinline__ double four_bits(double x) {
   return __longlong_as_double((long long)((u + 0xffffffffffffull + ((u >> 49) & 1ull)) & ~0x1ffffffffffffull));
 }
 
-// Eight columns from 8 * j on of the head `x` points at, normed and rotated in fp64: those of
-// `mask`.  By a whole warp (the sum of squares takes all the head's lanes).
+// A code, x / scale to the nearest whole number and 8, in the low bits of 12582920 + x / scale (1.5 * 2^23 + 8:
+// fp32 there holds whole numbers, and the sum is rounded to the nearest, ties to even).
+constexpr float kCode = 12582920.f;
+__device__ __forceinline__ float code(float x, float inv) { return fmaf(x, inv, kCode); }
+// The same for x of at most 11 significant bits and a scale of four, ties included: the quotient lies on a
+// half or at least 2^-13 off one, so x times the rounded inverse, itself rounded to multiples of 2^-14
+// (768 is 1.5 * 2^9), is a half exactly where it has to be.
+__device__ __forceinline__ float code_exactly(float x, float inv) { return __fadd_rn(fmaf(x, inv, 768.f), kCode - 768.f); }
+
+// Codes of four columns, 16 bits (with what lies above them).
+__device__ __forceinline__ uint32_t pack_codes(const float* c) {
+  return __float_as_uint(c[0]) - 0x4b400000u + ((__float_as_uint(c[1]) - 0x4b400000u) << 4) +
+         ((__float_as_uint(c[2]) - 0x4b400000u) << 8) + ((__float_as_uint(c[3]) - 0x4b400000u) << 12);
+}
+
+// The scale's inverse within 2^-23 of it (scales are at most 2^126); 0 where there is none.
+__device__ __forceinline__ float inverse(float scale) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(scale));
+  return scale > 0.f ? y : 0.f;
+}
+
+// The larger; a NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ double max_nan(double a, double b) { return fmax(a, b); }
+
+// Largest of the lanes' values for each group of 64 columns: va of the group that holds l.a, vb of l.b's.
+// Returned are this lane's two groups' (x: l.a's, y: l.b's) and the head's.
+template <int D, typename T>
+__device__ __forceinline__ T group_max(const HeadLane& l, T va, T vb, T& x, T& y) {
+  T all = 0;
+#pragma unroll
+  for (int g = 0; g < D / 64; ++g) {
+    const bool a = l.a >= 0 && l.a / 64 == g, b = l.b >= 0 && l.b / 64 == g;
+    T m = max_nan(a ? va : T(0), b ? vb : T(0));
+#pragma unroll
+    for (int o = kHeadLanes<D> / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (a) x = m;
+    if (b) y = m;
+    all = max_nan(all, m);
+  }
+  return all;
+}
+
+// A key's eight columns of this lane, four from l.a and four from l.b: their codes, 16 bits each, and
+// their groups' scales.
+struct Held {
+  uint32_t codes[2];
+  float scale[2];
+};
+
+// Whether fp32 leaves a scale open: the border above its four bits lies within the errors.
+__device__ __forceinline__ bool open_scale(float top, float e) {
+  const float m = top * (1.f / 7.f), border = __uint_as_float((__float_as_uint(m) & ~0xfffffu) | 0x80000u);
+  return fabsf(m - border) <= fmaf(m, 0x1p-22f, e * (1.f / 7.f));   // (2^-22: the product's own rounding)
+}
+// A quotient nearer to a half than that may be rounded wrongly (2^-18: its own and the inverse's
+// roundings, of at most 7.5, and the bound's).
+__device__ __forceinline__ float open_code(float e, float inv) { return 0.5f - 0x1p-18f - e * inv; }
+
+// Whether the 64 columns that hold column d have any that is normed or rotated: the others come as they are,
+// and their scale is exact (one bf16 maximum in sixteen lies on a border).
+__device__ __forceinline__ bool group_turned(const TurnArgs& t, int d) {
+  const int g = d & ~63;
+  return t.k_weight || (t.rot > 0 && t.first < g + 64 && t.first + t.rot > g);
+}
+
+// The same with what fp32 leaves open computed in fp64 from the head at `x` (null: the lane has none):
+// the largest values of a group whose scale is open, then the columns next to a border.  Whole warp.
 template <int D, bool F16>
-__device__ __noinline__ void turn_exactly(const TurnArgs& t, const uint16_t* x, int pos, int j, uint32_t mask, double* y) {
+__device__ __noinline__ Held hold_exactly(const TurnArgs& t, const float2* cs, const uint16_t* x, int pos, int lane) {
+  const HeadLane l = head_lane<D>(t, lane % kHeadLanes<D>);
+  const bool live = x && l.a >= 0, turned = t.k_weight || l.f >= 0;
+  float y[8];
+  unpack4<F16>(live ? load4(x, l.a) : make_uint2(0, 0), y);
+  unpack4<F16>(live ? load4(x, l.b) : make_uint2(0, 0), y + 4);
   double r = 1.0;
   if (t.k_weight) {
     double s = 0.0;
-    if (x && j < D / 8)
-      for (int i = 0; i < 8; ++i) {
-        const double v = to_float<F16>(x[8 * j + i]);
-        s = fma(v, v, s);
-      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fma((double)y[i], (double)y[i], s);
     for (int o = kHeadLanes<D> / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    r = 1.0 / sqrt(s / D + (double)t.eps);
+    r = 1.0 / sqrt(s * (1.0 / D) + (double)t.eps);   // (D = 192: 1 / D is off by 2^-54 of it)
   }
-  if (!x || j >= D / 8) mask = 0;
-  auto at = [&](int d) {
+  turn_head<D>(t, t.k_weight != nullptr, l, lane_turn<F16>(cs, t.k_weight, l), y);
+  auto value = [&](int d) {
     const double v = to_float<F16>(x[d]);
     return t.k_weight ? v * r * (double)to_float<F16>(t.k_weight[d]) : v;
   };
-  for (int i = 0; i < 8; ++i) {
-    if (!(mask >> i & 1u)) continue;
-    const int d = 8 * j + i, c = d - t.first;
-    double v = at(d);
-    if (c >= 0 && c < t.rot) {
-      const int half = t.rot / 2;
-      const bool second = t.adjacent ? c & 1 : c >= half;
-      const int f = t.adjacent ? c >> 1 : (second ? c - half : c);
-      const double p = at(t.adjacent ? t.first + (c ^ 1) : t.first + (second ? c - half : c + half));
-      double sn, cs;
-      sincospi((double)(int64_t)(turn_fraction(t.inv_freq[f]) * (uint64_t)(int64_t)pos) * 0x1p-63, &sn, &cs);
-      v = second ? v * cs + p * sn : v * cs - p * sn;
+  auto exactly = [&](int i) {
+    const int d = i < 4 ? l.a + i : l.b + i - 4, c = d - t.first;
+    if (c < 0 || c >= t.rot) return value(d);
+    const int half = t.rot / 2;
+    const bool second = t.adjacent ? c & 1 : c >= half;
+    const int f = t.adjacent ? c >> 1 : (second ? c - half : c);
+    const double v = value(d), p = value(t.first + (t.adjacent ? c ^ 1 : (second ? c - half : c + half)));
+    const double2 cs = cos_sin_exactly(turn_fraction(t.inv_freq[f]) * (uint64_t)(int64_t)pos);
+    return second ? v * cs.x + p * cs.y : v * cs.x - p * cs.y;
+  };
+  auto four = [&](const float* v) { return max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))); };
+  float top[2] = {0.f, 0.f}, scale[2];
+  const float all = group_max<D>(l, four(y), four(y + 4), top[0], top[1]);
+  const bool exact = !t.k_weight && t.rot == 0;
+  const float e = exact ? 0.f : 2.f * kTurnErr * all;
+  double most[2] = {0.0, 0.0}, most_of[2] = {0.0, 0.0};
+  bool open[2];
+  for (int v = 0; v < 2; ++v) {
+    scale[v] = group_scale(top[v]);
+    open[v] = scale[v] == scale[v] && group_turned(t, v ? l.b : l.a) && open_scale(top[v], e);
+    if (!open[v] || !live) continue;
+    for (int i = 4 * v; i < 4 * v + 4; ++i)
+      if (fabsf(y[i]) >= top[v] - 2.f * e) most[v] = fmax(most[v], fabs(exactly(i)));
+  }
+  // (an open group is open for all its lanes)
+  group_max<D>(l, most[0], most[1], most_of[0], most_of[1]);
+  Held h;
+  for (int v = 0; v < 2; ++v) {
+    if (open[v]) scale[v] = (float)four_bits(most_of[v] / 7.0);
+    const float inv = inverse(scale[v]), border = open_code(turned ? e : 0.f, inv);
+    float c[4];
+    for (int i = 0; i < 4; ++i) {
+      const float x = y[4 * v + i];
+      c[i] = turned ? code(x, inv) : code_exactly(x, inv);
+      if (turned && live && fabsf(fmaf(x, inv, kCode - c[i])) > border && scale[v] > 0.f)
+        c[i] = kCode + (float)rint(exactly(4 * v + i) / (double)scale[v]);
     }
-    y[i] = v;
+    h.codes[v] = pack_codes(c);
+    h.scale[v] = scale[v];
+  }
+  return h;
+}
+
+// The same in fp32; false where that leaves something open.  x: normed and rotated.  Whole warp.
+template <int D>
+__device__ __forceinline__ bool hold_key(const TurnArgs& t, const float* x, const HeadLane& l, Held& h) {
+  auto four = [&](const float* v) { return max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))); };
+  float top[2] = {0.f, 0.f};
+  const float all = group_max<D>(l, four(x), four(x + 4), top[0], top[1]);
+  // A pair's magnitudes before the rotation add up to at most twice the larger one after it.  Columns that
+  // are neither normed nor rotated come as they are.
+  const bool exact = !t.k_weight && t.rot == 0, turned = t.k_weight || l.f >= 0;
+  const float e = exact ? 0.f : 2.f * kTurnErr * all;
+  bool open = false;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float scale = group_scale(top[v]), inv = inverse(scale);
+    open |= group_turned(t, v ? l.b : l.a) && open_scale(top[v], e);
+    float c[4], d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = code(x[4 * v + i], inv);
+      d[i] = fabsf(fmaf(x[4 * v + i], inv, kCode - c[i]));
+    }
+    if (turned) {
+      open |= max3(d[0], d[1], fmaxf(d[2], d[3])) > open_code(e, inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = code_exactly(x[4 * v + i], inv);
+    }
+    h.codes[v] = pack_codes(c);
+    h.scale[v] = scale;
+  }
+  return !open;
+}
+
+// A lane's part of a key into its head's block.
+template <int DK, int DV>
+__device__ __forceinline__ void put_key(const CacheArgs& c, uint8_t* to, int place, const HeadLane& l, const Held& held) {
+  const uint32_t ta = (l.a >> 6) * c.ps + place, tb = (l.b >> 6) * c.ps + place, scales = c.ps * ((DK + DV) / 2);
+  *reinterpret_cast<uint16_t*>(to + ta * 32 + (l.a & 63) / 2) = (uint16_t)held.codes[0];
+  *reinterpret_cast<uint16_t*>(to + tb * 32 + (l.b & 63) / 2) = (uint16_t)held.codes[1];
+  if ((l.a & 63) == 0) *reinterpret_cast<uint16_t*>(to + scales + ta * 2) = (uint16_t)(__float_as_uint(held.scale[0]) >> 16);
+  if ((l.b & 63) == 0) *reinterpret_cast<uint16_t*>(to + scales + tb * 2) = (uint16_t)(__float_as_uint(held.scale[1]) >> 16);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// What fp32 left open: rows of the CTA (i << 8) and first heads of a round.
+struct Open {
+  int n;
+  uint16_t at[kTurnRows * 128];
+};
+
+// A run of one row's keys into its page, by one warp.
+template <int DK, int DV, bool F16>
+__device__ __forceinline__ void append_keys(const TurnArgs& t, const CacheArgs& c, const float2* cs, Open& open, int64_t page,
+                                            int row, int i, int run, int lane) {
+  const int place = t.positions[row] & (c.ps - 1);
+  constexpr int L = kHeadLanes<DK>, S = 32 / L;
+  int h0, h1;
+  run_heads(t, c.H_kv, run, h0, h1);
+  const int sub = lane / L;
+  const HeadLane l = head_lane<DK>(t, lane % L);
+  const uint16_t* src = t.k + row * t.k_stride + (h0 + sub) * DK;
+  uint8_t* dst = c.pages + page + (uint32_t)(h0 + sub) * c.block;
+  const LaneTurn turns = lane_turn<F16>(cs, t.k_weight, l);
+  const int rounds = (h1 - h0 + S - 1) / S;
+  for (int first = 0; first < rounds; first += 4) {
+    uint2 v[4][2];             // (four rounds' loads under way together)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const bool live = h0 + (first + y) * S + sub < h1;
+      v[y][0] = live ? load4(src + (first + y) * S * DK, l.a) : make_uint2(0, 0);
+      v[y][1] = live ? load4(src + (first + y) * S * DK, l.b) : make_uint2(0, 0);
+    }
+#pragma unroll 1
+    for (int n = first; n < min(first + 4, rounds); ++n) {
+      const bool live = h0 + n * S + sub < h1 && l.a >= 0;
+      float x[8];
+      unpack4<F16>(v[0][0], x);
+      unpack4<F16>(v[0][1], x + 4);
+#pragma unroll
+      for (int y = 1; y < 4; ++y) {
+        v[y - 1][0] = v[y][0];
+        v[y - 1][1] = v[y][1];
+      }
+      turn_head<DK>(t, t.k_weight != nullptr, l, turns, x);
+      Held held;
+      if (__any_sync(0xffffffffu, !hold_key<DK>(t, x, l, held) && live) && lane == 0)
+        open.at[atomicAdd(&open.n, 1)] = (uint16_t)(i << 8 | (h0 + n * S));
+      if (live) put_key<DK, DV>(c, dst + n * S * c.block, place, l, held);
+    }
   }
 }
 
-// Eight columns of a head to a word of codes and their group's scale.  `off`: bounds of x's
-// errors (all 0: exact).  `head`, `pos`: what turn_exactly needs, head null where the lane
-// has none.  Whole warp; a group is eight adjacent lanes.
-template <int D, bool F16, bool Turned>
-__device__ __forceinline__ uint32_t quantise(const TurnArgs& t, const float* x, const float* off, const uint16_t* head,
-                                             int pos, int j, float* scale_out) {
-  uint32_t top = 0;   // (as bits: a NaN is then above all)
+// A run of one row's values: eight columns to a lane, eight lanes to a group.
+template <int DK, int DV, bool F16>
+__device__ __forceinline__ void append_values(const TurnArgs& t, const CacheArgs& c, int64_t page, int row, int run, int lane) {
+  const int place = t.positions[row] & (c.ps - 1);
+  constexpr int L = DV / 8, S = 32 / L, U = 4;
+  int h0, h1;
+  run_heads(t, c.H_kv, run, h0, h1);
+  const int sub = lane / L, j = lane % L;
+  const uint32_t at = (j >> 3) * c.ps + place;
+  const uint16_t* src = t.v + row * t.v_stride + (h0 + sub) * DV + 8 * j;
+  uint8_t* dst = c.pages + page + (uint32_t)(h0 + sub) * c.block;
+  const uint32_t to = c.ps * (DK / 2) + at * 32 + (j & 7) * 4, scales = c.ps * ((DK + DV) / 2 + DK / 32) + at * 2;
+  for (int base = h0; base < h1; base += U * S) {
+    uint4 v[U];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float amax = __uint_as_float(top);
-  float scale = four_bits(__fdiv_rn(amax, 7.f));
-  uint32_t near = 0;   // columns next to a border
-  bool wide = false;   // the scale itself may be another one
-  if (Turned) {
-    float e = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e = fmaxf(e, off[i]);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
-    e *= kTurnErr;
-    // (2^-22: the quotient's own rounding)
-    wide = e > 0.f && four_bits((amax - e) * (1.f - 0x1p-22f) / 7.f) != four_bits((amax + e) * (1.f + 0x1p-22f) / 7.f);
-    if (!(scale == scale)) wide = false;
-  }
-  const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
-  int code[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = scale > 0.f ? __fdiv_rn(x[i], scale) : 0.f;
-    const float n = rintf(q);
-    code[i] = (int)n;
-    // (2^-21: the quotient's rounding, at most 2^-22, and what off * inv itself is off by)
-    if (Turned && off[i] > 0.f && fabsf(q - n) > 0.5f - 0x1p-21f - off[i] * kTurnErr * inv) near |= 1u << i;
-  }
-  if (Turned && __any_sync(0xffffffffu, near | (uint32_t)wide)) {
-    double y[8];
-    turn_exactly<D, F16>(t, head, pos, j, wide ? 0xffu : near, y);
-    double s = scale;
-    double m = 0.0;
-    if (wide && head && j < D / 8)
-      for (int i = 0; i < 8; ++i) m = fmax(m, fabs(y[i]));
-    for (int o = 4; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (wide) {
-      s = four_bits(m / 7.0);
-      scale = (float)s;
-      near = 0xffu;
+    for (int u = 0; u < U; ++u) {
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (base + u * S + sub < h1) v[u] = *reinterpret_cast<const uint4*>(src + u * S * DV);
     }
-    if (head && j < D / 8)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (near >> i & 1u) code[i] = s > 0.0 ? (int)rint(y[i] / s) : 0;
+    for (int u = 0; u < U; ++u) {
+      if (base + u * S >= h1) break;
+      float x[8];
+      unpack4<F16>(make_uint2(v[u].x, v[u].y), x);
+      unpack4<F16>(make_uint2(v[u].z, v[u].w), x + 4);
+      float top = max_nan(max_nan(max_nan(fabsf(x[0]), fabsf(x[1])), max_nan(fabsf(x[2]), fabsf(x[3]))),
+                          max_nan(max_nan(fabsf(x[4]), fabsf(x[5])), max_nan(fabsf(x[6]), fabsf(x[7]))));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float scale = group_scale(top), inv = inverse(scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = code_exactly(x[i], inv);
+      if (base + u * S + sub < h1) {
+        *reinterpret_cast<uint32_t*>(dst + to) = pack_codes(x) + (pack_codes(x + 4) << 16);
+        if ((j & 7) == 0) *reinterpret_cast<uint16_t*>(dst + scales) = (uint16_t)(__float_as_uint(scale) >> 16);
+      }
+      dst += S * c.block;
+    }
+    src += U * S * DV;
   }
-  *scale_out = scale;
-  uint32_t word = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) word |= ((uint32_t)(code[i] + 8) & 15u) << (4 * i);
-  return word;
 }
 
 template <int DK, int DV, bool F16>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const TurnArgs t, const CacheArgs c, uint32_t* status) {
-  constexpr int L = kHeadLanes<DK>, S = kThreads / L;
-  __shared__ float2 cs[128];
-  __shared__ __align__(16) float2 ys[S][DK];      // a key's values and their error bounds
-  const int tid = threadIdx.x, lane = tid & 31, j = tid % L, slot = tid / L;
-  const int row = blockIdx.x / t.chunks, chunk = blockIdx.x - row * t.chunks;
-  const int tasks = t.H_q + 2 * c.H_kv;           // heads of q, then of k, then of v
-  const int x0 = (int)((int64_t)tasks * chunk / t.chunks), x1 = (int)((int64_t)tasks * (chunk + 1) / t.chunks);
-  const HeadLane l = head_lane<DK>(t, j);
+__global__ void __launch_bounds__(kTurnThreads, 4) kv4_append_kernel(const __grid_constant__ TurnArgs t, const __grid_constant__ CacheArgs c, uint32_t* status) {
+  __shared__ RowTurns cs;
+  __shared__ int64_t pages[kTurnRows];             // a row's page; -1: outside the pool, -2: the row is skipped
+  __shared__ Open open;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, runs = t.q_runs + t.k_runs + t.v_runs;
+  int row0, u0, u1;
+  cta_units(t, runs, row0, u0, u1);
   pdl_trigger();
-  const int pos = t.positions[row];
-  const int b = find_request(t.row_offsets, t.B, row, lane);
-  if (pos < 0 || b < 0) return;
-  const int64_t page = find_page(c, b, pos);
-  const int place = pos & (c.ps - 1);
-  if (page < 0 && chunk == 0 && tid == 0) {
-    pdl_wait();                                   // (the status block is cleared)
-    raise_status(status, DSA_DEVICE_BAD_INDEX);
+  // The rows' keys and values on their way to L2 while pages and angles are looked up.
+  for (int i = warp; i >> t.rows_log2 == 0 && row0 + i < t.R; i += kTurnThreads / 32) {
+    const uint16_t *k = t.k + (row0 + i) * t.k_stride, *v = t.v + (row0 + i) * t.v_stride;
+    for (int x = lane; x < c.H_kv * (DK / 64); x += 32) prefetch_l2(k + 64 * x);
+    for (int x = lane; x < c.H_kv * (DV / 64); x += 32) prefetch_l2(v + 64 * x);
   }
-  if (tid < t.rot / 2) cs[tid] = turn(turn_fraction(t.inv_freq[tid]), pos);
+  if (threadIdx.x == 0) open.n = 0;
+  if (warp >> t.rows_log2 == 0) {
+    int64_t page = -2;
+    if (row0 + warp < t.R) {
+      const int pos = t.positions[row0 + warp], b = find_request(t.row_offsets, t.B, row0 + warp, lane);
+      if (pos >= 0 && b >= 0) page = find_page(c, b, pos);
+    }
+    if (lane == 0) {
+      pages[warp] = page;
+      if (page == -1 && u0 == 0) {
+        pdl_wait();                                // (the status block is cleared)
+        raise_status(status, DSA_DEVICE_BAD_INDEX);
+      }
+    }
+  }
+  row_turns(t, cs, row0);
   __syncthreads();
-  float2 f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = l.f >= 0 ? cs[l.f + i] : make_float2(1.f, 0.f);
-  for (int base = x0; base < x1; base += S) {
-    const int x = base + slot;
-    const bool is_q = x < t.H_q, is_k = !is_q && x < t.H_q + c.H_kv, live = x < x1;
-    // Heads of q and k.
-    if (base < t.H_q + c.H_kv) {                  // (the same for a whole CTA)
-      const int h = is_q ? x : x - t.H_q;
-      const uint16_t* src = is_q ? t.q + row * t.q_stride + (int64_t)h * DK : t.k + row * t.k_stride + (int64_t)h * DK;
-      const bool mine = live && (is_q || is_k);
-      float y[8], off[8];
-      unpack4<F16>(mine ? load4(src, l.a) : make_uint2(0, 0), y);
-      unpack4<F16>(mine ? load4(src, l.b) : make_uint2(0, 0), y + 4);
-      turn_head<DK, F16, true>(t, is_q ? t.q_weight : t.k_weight, l, f, y, off);
-      if (mine && is_q && l.a >= 0) {
-        uint16_t* p = t.q_out + row * t.q_out_stride + (int64_t)h * DK;
-        *reinterpret_cast<uint2*>(p + l.a) = make_uint2(pack16<F16>(y[0], y[1]), pack16<F16>(y[2], y[3]));
-        *reinterpret_cast<uint2*>(p + l.b) = make_uint2(pack16<F16>(y[4], y[5]), pack16<F16>(y[6], y[7]));
-      }
-      if (l.a >= 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ys[slot][l.a + i] = make_float2(y[i], off[i]);
-          ys[slot][l.b + i] = make_float2(y[4 + i], off[4 + i]);
-        }
-      }
-      __syncwarp();
-      float off8[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 v = j < DK / 8 ? ys[slot][8 * j + i] : make_float2(0.f, 0.f);
-        y[i] = is_k ? v.x : 0.f;
-        off8[i] = is_k ? v.y : 0.f;
-      }
-      __syncwarp();
-      float scale;
-      const uint32_t word = quantise<DK, F16, true>(t, y, off8, live && is_k ? src : nullptr, pos, j, &scale);
-      if (live && is_k && page >= 0 && j < DK / 8) {
-        uint8_t* p = c.pages + page + (int64_t)h * c.block;
-        const uint32_t at = (j >> 3) * c.ps + place;
-        *reinterpret_cast<uint32_t*>(p + at * 32 + (j & 7) * 4) = word;
-        if ((j & 7) == 0)
-          *reinterpret_cast<uint16_t*>(p + c.ps * ((DK + DV) / 2) + at * 2) = (uint16_t)(__float_as_uint(scale) >> 16);
-      }
+  for (int u = u0 + warp; u < u1; u += kTurnThreads / 32) {
+    const int run = u >> t.rows_log2, i = u - (run << t.rows_log2), row = row0 + i;
+    const int64_t page = pages[i];
+    if (page == -2) continue;
+    if (run < t.q_runs) {
+      int h0, h1;
+      run_heads(t, t.H_q, run, h0, h1);
+      turn_row<DK, F16>(t, t.q_weight, cs[i], t.q + row * t.q_stride, t.q_out + row * t.q_out_stride, h0, h1, lane);
+    } else if (page >= 0) {
+      if (run < t.q_runs + t.k_runs)
+        append_keys<DK, DV, F16>(t, c, cs[i], open, page, row, i, run - t.q_runs, lane);
+      else
+        append_values<DK, DV, F16>(t, c, page, row, run - t.q_runs - t.k_runs, lane);
     }
-    // Heads of v: eight columns to a lane.
-    if (base + S > t.H_q + c.H_kv) {              // (the same for a whole CTA)
-      const int h = x - t.H_q - c.H_kv;
-      const bool mine = live && h >= 0 && j < DV / 8;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (mine) w = *reinterpret_cast<const uint4*>(t.v + row * t.v_stride + (int64_t)h * DV + 8 * j);
-      float y[8], scale;
-      unpack4<F16>(make_uint2(w.x, w.y), y);
-      unpack4<F16>(make_uint2(w.z, w.w), y + 4);
-      const uint32_t word = quantise<DV, F16, false>(t, y, nullptr, nullptr, 0, j, &scale);
-      if (mine && page >= 0) {
-        uint8_t* p = c.pages + page + (int64_t)h * c.block;
-        const uint32_t at = (j >> 3) * c.ps + place;
-        *reinterpret_cast<uint32_t*>(p + c.ps * (DK / 2) + at * 32 + (j & 7) * 4) = word;
-        if ((j & 7) == 0)
-          *reinterpret_cast<uint16_t*>(p + c.ps * ((DK + DV) / 2 + DK / 32) + at * 2) = (uint16_t)(__float_as_uint(scale) >> 16);
-      }
-    }
+  }
+  __syncthreads();                                 // (the keys that are written again are written by then)
+  for (int x = warp; x < open.n; x += kTurnThreads / 32) {
+    constexpr int L = kHeadLanes<DK>;
+    const int i = open.at[x] >> 8, row = row0 + i, h = (open.at[x] & 255) + lane / L, pos = t.positions[row];
+    const HeadLane l = head_lane<DK>(t, lane % L);
+    const bool live = h < c.H_kv && l.a >= 0;
+    const Held held = hold_exactly<DK, F16>(t, cs[i], live ? t.k + row * t.k_stride + h * DK : nullptr, pos, lane);
+    if (live) put_key<DK, DV>(c, c.pages + pages[i] + (uint32_t)h * c.block, pos & (c.ps - 1), l, held);
   }
 }
 
@@ -255,18 +402,25 @@ __device__ __forceinline__ uint4 dequantise(uint32_t w, uint16_t scale) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-constexpr int kReadRows = 16;   // rows of a CTA
+template <int N>
+struct Width {
+  static constexpr int value = N;
+};
+
+// A warp takes 128 words (32 bits of codes) of a row's K or V at a time, four loads to a lane; a CTA `rows`
+// rows, of which eight warps share the pieces.
+constexpr int kReadRows = 16;   // at most
 
 template <int DK, int DV, bool F16>
 __global__ void __launch_bounds__(kThreads)
-    kv4_read_kernel(const CacheArgs c, int R, const int32_t* row_offsets, const int32_t* positions, uint16_t* k_out,
+    kv4_read_kernel(const CacheArgs c, int R, int rows, const int32_t* row_offsets, const int32_t* positions, uint16_t* k_out,
                     uint16_t* v_out, uint32_t* status) {
   __shared__ int64_t pages[kReadRows];
   __shared__ int places[kReadRows];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t row0 = (int64_t)blockIdx.x * kReadRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row0 = (int64_t)blockIdx.x * rows;
   pdl_trigger();
-  for (int i = warp; i < kReadRows; i += kThreads / 32) {
+  for (int i = warp; i < rows; i += kThreads / 32) {
     const int64_t row = row0 + i;
     int64_t page = -1;
     int pos = -1;
@@ -287,42 +441,63 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   __syncthreads();
-  constexpr int WK = DK / 8, WV = DV / 8;      // words of a head
-  auto half = [&](uint16_t* out, int W, uint32_t codes, uint32_t scales) {
+  auto piece = [&](auto width, uint16_t* out, uint32_t codes, uint32_t scales, int i, int first) {
+    constexpr int W = decltype(width)::value / 8;    // words of a head
     const int per = c.H_kv * W;
-    for (int x = tid; x < kReadRows * per; x += kThreads) {
-      const int i = x / per, y = x - i * per, h = y / W, j = y - h * W;
-      const int64_t page = pages[i];
-      if (page < 0) continue;
-      const uint8_t* p = c.pages + page + (int64_t)h * c.block;
-      const uint32_t at = (j >> 3) * c.ps + places[i];
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p + codes + at * 32 + (j & 7) * 4);
-      const uint16_t s = *reinterpret_cast<const uint16_t*>(p + scales + at * 2);
-      *reinterpret_cast<uint4*>(out + ((row0 + i) * per + y) * 8) = dequantise<F16>(w, s);
+    const int64_t page = pages[i];
+    if (page < 0) return;
+    const uint8_t* p = c.pages + page;
+    const uint32_t at = places[i];
+    uint4* to = reinterpret_cast<uint4*>(out) + (row0 + i) * per;
+    uint32_t w[4];
+    uint16_t s[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t x = min(first + 32 * u + lane, per - 1), h = x / W, j = x - h * W;
+      const uint32_t n = (j >> 3) * c.ps + at, blk = h * c.block;
+      w[u] = *reinterpret_cast<const uint32_t*>(p + (blk + codes + n * 32 + (j & 7) * 4));
+      s[u] = *reinterpret_cast<const uint16_t*>(p + (blk + scales + n * 2));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = first + 32 * u + lane;
+      if (x < per) to[x] = dequantise<F16>(w[u], s[u]);
     }
   };
-  if (k_out) half(k_out, WK, 0, c.ps * ((DK + DV) / 2));
-  if (v_out) half(v_out, WV, c.ps * (DK / 2), c.ps * ((DK + DV) / 2 + DK / 32));
+  const int nk = k_out ? (c.H_kv * (DK / 8) + 127) / 128 : 0, nv = v_out ? (c.H_kv * (DV / 8) + 127) / 128 : 0;
+  int i = warp % rows, y = warp / rows;              // (a piece of every row, then the next)
+  for (; y < nk + nv;) {
+    if (y < nk)
+      piece(Width<DK>(), k_out, 0, c.ps * ((DK + DV) / 2), i, 128 * y);
+    else
+      piece(Width<DV>(), v_out, c.ps * (DK / 2), c.ps * ((DK + DV) / 2 + DK / 32), i, 128 * (y - nk));
+    i += kThreads / 32;
+    while (i >= rows) {
+      i -= rows;
+      ++y;
+    }
+  }
 }
 
 template <int DK, int DV>
 cudaError_t launch_append_width(TurnArgs t, const CacheArgs& c, bool f16, uint32_t* status, cudaStream_t st) {
-  constexpr int S = kThreads / kHeadLanes<DK>;
-  // CTAs to a row: heads one after the other where the rows fill the GPU, else spread.
-  const int tasks = t.H_q + 2 * c.H_kv, most = (tasks + S - 1) / S;
-  t.chunks = 1;
-  while (t.chunks < most && (int64_t)t.R * t.chunks < 608) ++t.chunks;
-  const dim3 grid((unsigned)((int64_t)t.R * t.chunks));
-  return f16 ? launch_pdl(kv4_append_kernel<DK, DV, true>, grid, dim3(kThreads), 0, st, t, c, status)
-             : launch_pdl(kv4_append_kernel<DK, DV, false>, grid, dim3(kThreads), 0, st, t, c, status);
+  deal_heads(t, 32 / kHeadLanes<DK>, 8, c.H_kv, c.H_kv);
+  const dim3 grid((unsigned)((t.R + (1 << t.rows_log2) - 1) >> t.rows_log2), (unsigned)t.split);
+  return f16 ? launch_pdl(kv4_append_kernel<DK, DV, true>, grid, dim3(kTurnThreads), 0, st, t, c, status)
+             : launch_pdl(kv4_append_kernel<DK, DV, false>, grid, dim3(kTurnThreads), 0, st, t, c, status);
 }
 
 template <int DK, int DV>
 cudaError_t launch_read_width(const CacheArgs& c, int R, const int32_t* row_offsets, const int32_t* positions, bool f16,
                               uint16_t* k_out, uint16_t* v_out, uint32_t* status, cudaStream_t st) {
-  const dim3 grid((unsigned)(((int64_t)R + kReadRows - 1) / kReadRows));
-  return f16 ? launch_pdl(kv4_read_kernel<DK, DV, true>, grid, dim3(kThreads), 0, st, c, R, row_offsets, positions, k_out, v_out, status)
-             : launch_pdl(kv4_read_kernel<DK, DV, false>, grid, dim3(kThreads), 0, st, c, R, row_offsets, positions, k_out, v_out, status);
+  // Rows to a CTA: up to sixteen where that leaves two CTAs an SM or more.
+  int rows = 1;
+  while (rows < kReadRows && R / (2 * rows) >= 304) rows *= 2;
+  const dim3 grid((unsigned)(((int64_t)R + rows - 1) / rows));
+  return f16 ? launch_pdl(kv4_read_kernel<DK, DV, true>, grid, dim3(kThreads), 0, st, c, R, rows, row_offsets, positions, k_out,
+                          v_out, status)
+             : launch_pdl(kv4_read_kernel<DK, DV, false>, grid, dim3(kThreads), 0, st, c, R, rows, row_offsets, positions, k_out,
+                          v_out, status);
 }
 
 }  // namespace

@@ -3,9 +3,9 @@
 //   y = x w / sqrt(mean x^2 + eps), then pairs of columns turned by position * inv_freq.
 //
 // Every element is read once and written once (4 bytes against about ten operations), so
-// what bounds the kernel is HBM, or for few rows latency.  A CTA takes one row and some of
-// its heads: the row's angles are the same for all heads, so its cos and sin are computed
-// once, by as many threads as there are frequencies, while the heads' loads are under way.  A
+// what bounds the kernel is HBM, or for few rows latency.  A CTA takes four rows, whose
+// angles' cos and sin its threads work out first, one each (by every warp for itself they were
+// 40% of its instructions), and its warps runs of a row's heads, with the norm's weights in registers.  A
 // head is held by 8 to 32 lanes with both columns of a pair in one lane (rope.cuh), so the
 // rotation needs no exchange and the norm three to five shuffles.
 #include "rope.cuh"
@@ -13,72 +13,61 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 256;
-
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const TurnArgs t) {
-  constexpr int L = kHeadLanes<D>, S = kThreads / L, U = 4;   // lanes to a head, heads at a time, in flight
-  __shared__ float2 cs[128];
-  const int tid = threadIdx.x, j = tid % L, slot = tid / L;
-  const int row = blockIdx.x / t.chunks, chunk = blockIdx.x - row * t.chunks;
-  const int heads = t.H_q + t.H_kv;
-  const int h0 = (int)((int64_t)heads * chunk / t.chunks), h1 = (int)((int64_t)heads * (chunk + 1) / t.chunks);
-  const HeadLane l = head_lane<D>(t, j);
+__global__ void __launch_bounds__(kTurnThreads) qk_norm_rope_kernel(const __grid_constant__ TurnArgs t) {
+  __shared__ RowTurns cs;
+  const int lane = threadIdx.x & 31, runs = t.q_runs + t.k_runs;
+  int row0, u0, u1;
+  cta_units(t, runs, row0, u0, u1);
   pdl_wait();
   pdl_trigger();
-  const int pos = t.positions[row];
-  float2 c[4];
-  for (int base = h0; base < h1; base += U * S) {
-    uint2 v[U][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int x = base + u * S + slot;
-      const uint16_t* p = x < t.H_q ? t.q + row * t.q_stride + (int64_t)x * D
-                                    : t.k + row * t.k_stride + (int64_t)(x - t.H_q) * D;
-      v[u][0] = x < h1 ? load4(p, l.a) : make_uint2(0, 0);
-      v[u][1] = x < h1 ? load4(p, l.b) : make_uint2(0, 0);
-    }
-    if (base == h0) {
-      if (pos < 0) return;
-      if (tid < t.rot / 2) cs[tid] = turn(turn_fraction(t.inv_freq[tid]), pos);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = l.f >= 0 ? cs[l.f + i] : make_float2(1.f, 0.f);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (base + u * S >= h1) break;   // (the same for a whole CTA)
-      const int x = base + u * S + slot;
-      const bool is_q = x < t.H_q;
-      float y[8];
-      unpack4<F16>(v[u][0], y);
-      unpack4<F16>(v[u][1], y + 4);
-      turn_head<D, F16, false>(t, is_q ? t.q_weight : t.k_weight, l, c, y, nullptr);
-      if (x < h1 && l.a >= 0) {
-        uint16_t* p = is_q ? t.q_out + row * t.q_out_stride + (int64_t)x * D
-                           : t.k_out + row * t.k_out_stride + (int64_t)(x - t.H_q) * D;
-        *reinterpret_cast<uint2*>(p + l.a) = make_uint2(pack16<F16>(y[0], y[1]), pack16<F16>(y[2], y[3]));
-        *reinterpret_cast<uint2*>(p + l.b) = make_uint2(pack16<F16>(y[4], y[5]), pack16<F16>(y[6], y[7]));
-      }
-    }
+  row_turns(t, cs, row0);
+  __syncthreads();
+  for (int u = u0 + (threadIdx.x >> 5); u < u1; u += kTurnThreads / 32) {
+    const int c = u >> t.rows_log2, i = u - (c << t.rows_log2), row = row0 + i;
+    if (row >= t.R || t.positions[row] < 0) continue;
+    const bool is_q = c < t.q_runs;
+    int h0, h1;
+    run_heads(t, is_q ? t.H_q : t.H_kv, is_q ? c : c - t.q_runs, h0, h1);
+    turn_row<D, F16>(t, is_q ? t.q_weight : t.k_weight, cs[i], is_q ? t.q + row * t.q_stride : t.k + row * t.k_stride,
+                     is_q ? t.q_out + row * t.q_out_stride : t.k_out + row * t.k_out_stride, h0, h1, lane);
   }
 }
 
 template <int D>
 cudaError_t launch_width(TurnArgs t, bool f16, cudaStream_t st) {
-  // CTAs to a row: as many as keep four heads in flight a thread; few rows are spread
-  // further, one head a thread, to fill the GPU.
-  constexpr int S = kThreads / kHeadLanes<D>;
-  const int heads = t.H_q + t.H_kv;
-  const int most = (heads + S - 1) / S, least = (heads + 4 * S - 1) / (4 * S);
-  t.chunks = least;
-  while (t.chunks < most && (int64_t)t.R * t.chunks < 608) ++t.chunks;
-  const dim3 grid((unsigned)((int64_t)t.R * t.chunks));
-  return f16 ? launch_pdl(qk_norm_rope_kernel<D, true>, grid, dim3(kThreads), 0, st, t)
-             : launch_pdl(qk_norm_rope_kernel<D, false>, grid, dim3(kThreads), 0, st, t);
+  deal_heads(t, 32 / kHeadLanes<D>, 8, t.H_kv, 0);
+  const dim3 grid((unsigned)((t.R + (1 << t.rows_log2) - 1) >> t.rows_log2), (unsigned)t.split);
+  return f16 ? launch_pdl(qk_norm_rope_kernel<D, true>, grid, dim3(kTurnThreads), 0, st, t)
+             : launch_pdl(qk_norm_rope_kernel<D, false>, grid, dim3(kTurnThreads), 0, st, t);
 }
 
 }  // namespace
+
+// Many rows: up to eight to a CTA, whose angles its threads work out together, and `most` heads to a
+// run.  Few rows: a row's heads over several CTAs, as few to a warp as fit it, as long as that
+// leaves every CTA's warps a run.
+void deal_heads(TurnArgs& t, int at_once, int most, int H_k, int H_v) {
+  int runs = 0;
+  auto cut = [&](int log2) {
+    const int heads = 1 << log2;
+    t.run_log2 = log2;
+    t.q_runs = (t.H_q + heads - 1) / heads;
+    t.k_runs = (H_k + heads - 1) / heads;
+    t.v_runs = (H_v + heads - 1) / heads;
+    runs = t.q_runs + t.k_runs + t.v_runs;
+  };
+  int log2 = 0, least = 0;
+  while (1 << log2 < most || 1 << log2 < at_once) ++log2;
+  while (1 << least < at_once) ++least;
+  cut(log2);
+  while (log2 > least && (int64_t)t.R * runs < 9728) cut(--log2);
+  t.rows_log2 = t.R >= 8 * 608 ? 3 : t.R >= 4 * 608 ? 2 : t.R >= 2 * 608 ? 1 : 0;
+  t.split = 1;
+  if (t.rows_log2 == 0)
+    while (t.split < (runs + 7) / 8 && (int64_t)t.R * (t.split + 1) <= 1216) ++t.split;
+  t.units = ((runs << t.rows_log2) + t.split - 1) / t.split;
+}
 
 cudaError_t launch_qk_norm_rope(TurnArgs a, int D, bool f16, cudaStream_t st) {
   if (a.R == 0 || a.H_q + a.H_kv == 0) return cudaSuccess;

@@ -24,18 +24,45 @@ __device__ __forceinline__ float head_sum(float x) {
 }
 
 // inv_freq in turns a position, as a 64-bit fraction: position times it, modulo 2^64, is the
-// angle's fraction of a turn without any loss, whatever the position.
+// angle's fraction of a turn without any loss, whatever the position.  In whole numbers (the
+// fp64 unit does two operations a cycle and SM: 9601 rows took 104 us for it): inv_freq is
+// M 2^E, and 1 / (2 pi) is C 2^-66 within 2^-67, so the fraction is M C 2^(E - 2) modulo 2^64.
 __device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
-  const double t = inv_freq * 0.15915494309189533577;   // 1 / (2 pi)
-  return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
+  const uint64_t u = (uint64_t)__double_as_longlong(inv_freq);
+  const int e = (int)(u >> 52 & 0x7ff);
+  const uint64_t m = (u & 0xfffffffffffffull) | (e ? 1ull << 52 : 0), C = 0xa2f9836e4e44152aull;   // 2^66 / (2 pi)
+  const uint64_t hi = __umul64hi(m, C), lo = m * C;
+  const int right = 1077 - (e ? e : 1);   // 2 - E
+  uint64_t f = 0;
+  if (right >= 64)
+    f = right < 128 ? hi >> (right - 64) : 0;
+  else if (right > 0)
+    f = hi << (64 - right) | lo >> right;
+  else if (right > -64)
+    f = lo << -right;
+  return u >> 63 ? 0 - f : f;
 }
 
-// (cos, sin) of pos * inv_freq.  The angle is in half turns within [-1, 1), off by at most
-// 2^-25 from the conversion.
-__device__ __forceinline__ float2 turn(uint64_t fraction, int pos) {
-  const uint64_t phase = fraction * (uint64_t)(int64_t)pos;
-  float2 cs;
-  sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &cs.y, &cs.x);
+// (cos, sin) of `fraction` 2^-64 turns: quarter turns exactly, the rest, at most an eighth, by the Taylor
+// series up to y^9 and y^10 (what is left out is below 2^-25), off by at most 4 * 2^-24 in all.
+__device__ __forceinline__ float2 cos_sin(uint64_t fraction) {
+  const uint32_t p = (uint32_t)(fraction >> 32), q = (p + 0x20000000u) >> 30;
+  const float y = (float)(int32_t)(p - (q << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float z = y * y;
+  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f), c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  s = fmaf(z, s, 8.3333333e-3f);
+  c = fmaf(z, c, -1.3888889e-3f);
+  s = fmaf(z, s, -1.6666667e-1f);
+  c = fmaf(z, c, 4.1666667e-2f);
+  s = fmaf(z * y, s, y);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.f);
+  const float a = q & 1 ? s : c, b = q & 1 ? c : s;                           // cos, sin up to their signs
+  return make_float2((q + 1) & 2 ? -a : a, q & 2 ? -b : b);
+}
+__device__ __forceinline__ double2 cos_sin_exactly(uint64_t fraction) {
+  double2 cs;
+  sincospi((double)(int64_t)fraction * 0x1p-63, &cs.y, &cs.x);
   return cs;
 }
 
@@ -71,38 +98,62 @@ __device__ __forceinline__ uint2 load4(const uint16_t* row, int col) {
   return col < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2*>(row + col);
 }
 
-// The head's eight columns of this lane, x[0..3] from l.a and x[4..7] from l.b, normed and
-// rotated in place.  cs: cos and sin of the lane's four frequencies.  Returns through `off`, where
-// wanted, what each value's error is relative to: its own and its partner's magnitudes
-// before the rotation; 0 for values that come as they are (see kv4_cache.cu).
-template <int D, bool F16, bool Off>
-__device__ __forceinline__ void turn_head(const TurnArgs& t, const uint16_t* weight, const HeadLane& l, const float2* cs,
-                                          float* x, float* off) {
-  // A warp may hold heads of q and of k, of which one alone is normed: all its lanes sum.
-  float sum = 0.f;
-  if (t.q_weight || t.k_weight) {
+// The angles' cos and sin of a CTA's rows, worked out once for all heads and columns.
+constexpr int kTurnRows = 8, kTurnThreads = 256;
+typedef float2 RowTurns[kTurnRows][128];
+__device__ __forceinline__ void row_turns(const TurnArgs& t, RowTurns& cs, int row0) {
+  for (int i = threadIdx.x >> 6; i >> t.rows_log2 == 0 && row0 + i < t.R; i += kTurnThreads / 64)
+    for (int f = threadIdx.x & 63; f < t.rot / 2; f += 64)
+      cs[i][f] = cos_sin(turn_fraction(t.inv_freq[f]) * (uint64_t)(int64_t)t.positions[row0 + i]);
+}
+// The units (a run of heads, a row of the CTA's) that this CTA's warps share: run u >> rows_log2 of row
+// u & mask, so that each warp gets runs of every kind.
+__device__ __forceinline__ void cta_units(const TurnArgs& t, int runs, int& row0, int& u0, int& u1) {
+  row0 = blockIdx.x << t.rows_log2;
+  u0 = blockIdx.y * t.units;
+  u1 = min(u0 + t.units, runs << t.rows_log2);
+}
+__device__ __forceinline__ void run_heads(const TurnArgs& t, int n, int run, int& h0, int& h1) {
+  h0 = run << t.run_log2;
+  h1 = min(h0 + (1 << t.run_log2), n);
+}
+
+// What a lane keeps of its columns: cos and sin of its frequencies, the norm's weights.
+struct LaneTurn {
+  float2 cs[4];
+  float w[8];
+};
+template <bool F16>
+__device__ __forceinline__ LaneTurn lane_turn(const float2* cs, const uint16_t* weight, const HeadLane& l) {
+  LaneTurn x;
+  if (l.f >= 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-    sum = head_sum<D>(sum);
+    for (int i = 0; i < 4; ++i) x.cs[i] = cs[l.f + i];
   }
   if (weight) {
-    const float r = rsqrtf(fmaf(sum, 1.f / D, t.eps));
-    float w[8];
-    unpack4<F16>(load4(weight, l.a), w);
-    unpack4<F16>(load4(weight, l.b), w + 4);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+    unpack4<F16>(load4(weight, l.a), x.w);
+    unpack4<F16>(load4(weight, l.b), x.w + 4);
   }
-  if (Off) {
+  return x;
+}
+
+// The head's eight columns of this lane, x[0..3] from l.a and x[4..7] from l.b, normed and rotated in
+// place.  By whole warps; `norm` is the same for all heads of a warp.
+template <int D>
+__device__ __forceinline__ void turn_head(const TurnArgs& t, bool norm, const HeadLane& l, const LaneTurn& y, float* x) {
+  if (norm) {
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) off[i] = weight ? fabsf(x[i]) : 0.f;
+    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+    const float r = rsqrtf(fmaf(head_sum<D>(sum), 1.f / D, t.eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= r * y.w[i];
   }
   if (l.f < 0) return;
   auto pair = [&](int i, int a, int b) {
     const float u = x[a], v = x[b];
-    x[a] = u * cs[i].x - v * cs[i].y;
-    x[b] = v * cs[i].x + u * cs[i].y;
-    if (Off) off[a] = off[b] = fabsf(u) + fabsf(v);
+    x[a] = u * y.cs[i].x - v * y.cs[i].y;
+    x[b] = v * y.cs[i].x + u * y.cs[i].y;
   };
   if (t.adjacent) {
 #pragma unroll
@@ -110,6 +161,42 @@ __device__ __forceinline__ void turn_head(const TurnArgs& t, const uint16_t* wei
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) pair(i, i, i + 4);
+  }
+}
+
+// Heads h0 .. h1 - 1 of one row, by one warp, 32 / kHeadLanes at a time: `src` to `dst`, which may be the
+// same.  Loads of four rounds are under way together.
+template <int D, bool F16>
+__device__ __forceinline__ void turn_row(const TurnArgs& t, const uint16_t* weight, const float2* cs, const uint16_t* src,
+                                         uint16_t* dst, int h0, int h1, int lane) {
+  constexpr int L = kHeadLanes<D>, S = 32 / L, U = 4;
+  const int sub = lane / L;
+  const HeadLane l = head_lane<D>(t, lane % L);
+  LaneTurn y;
+  for (int base = h0; base < h1; base += U * S) {
+    uint2 v[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = base + u * S + sub;
+      const uint16_t* p = src + (int64_t)h * D;
+      v[u][0] = h < h1 ? load4(p, l.a) : make_uint2(0, 0);
+      v[u][1] = h < h1 ? load4(p, l.b) : make_uint2(0, 0);
+    }
+    if (base == h0) y = lane_turn<F16>(cs, weight, l);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (base + u * S >= h1) break;
+      const int h = base + u * S + sub;
+      float x[8];
+      unpack4<F16>(v[u][0], x);
+      unpack4<F16>(v[u][1], x + 4);
+      turn_head<D>(t, weight != nullptr, l, y, x);
+      if (h < h1 && l.a >= 0) {
+        uint16_t* p = dst + (int64_t)h * D;
+        *reinterpret_cast<uint2*>(p + l.a) = make_uint2(pack16<F16>(x[0], x[1]), pack16<F16>(x[2], x[3]));
+        *reinterpret_cast<uint2*>(p + l.b) = make_uint2(pack16<F16>(x[4], x[5]), pack16<F16>(x[6], x[7]));
+      }
+    }
   }
 }
 
