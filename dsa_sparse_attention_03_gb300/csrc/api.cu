@@ -739,8 +739,7 @@ struct Kv4Plan {
   CacheArgs cache;
   bool many;           // rows: the kernel of dense attention
   Kv4Shape shape;
-  DenseShape dense;
-  bool cleared;        // the status is cleared before the attention
+  Kv4Tile tile;
   size_t off_ml, off_part, total;
 };
 
@@ -760,19 +759,14 @@ dsa_status kv4_plan(const dsa_kv4_cache* c, const dsa_kv4_problem* p, Kv4Plan* k
   if (!(p->softmax_scale > 0.f) || p->softmax_scale > 1e30f)
     return fail(DSA_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
   if (p->flags & ~DSA_FLAG_FP16) return fail(DSA_ERR_INVALID_ARG, "unknown flag bits 0x%x", p->flags);
-  size_t off, parts;
   if ((kp->many = kv4_many_rows(*c, *p))) {
-    const dsa_dense_problem d = kv4_dense(*c, *p);
-    kp->dense = dense_shape(d, 2);
-    kp->cleared = dense_cleared(d, kp->dense);
-    parts = dense_parts(d, kp->dense);
-    off = kDensePartsOffset;
-  } else {
-    kp->shape = kv4_shape(*c, *p);
-    kp->cleared = !kp->shape.join;
-    parts = kv4_parts(kp->shape);
-    off = kKv4PartsOffset;
+    kp->tile = kv4_tile(*c, *p);
+    kp->total = kp->tile.total;
+    return DSA_OK;
   }
+  kp->shape = kv4_shape(*c, *p);
+  size_t off = kKv4PartsOffset;
+  const size_t parts = kv4_parts(kp->shape);
   kp->off_ml = off;
   off = align_up(off + parts * 8, 256);
   kp->off_part = off;
@@ -864,12 +858,12 @@ static dsa_status run_kv4(const dsa_kv4_cache* c, const dsa_kv4_problem* p, uint
   char* w = static_cast<char*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (p->R == 0 || kp.cleared) e = launch_clear_status(ws, st);   // (else the join sets it)
+  if (p->R == 0 || (!kp.many && !kp.shape.join)) e = launch_clear_status(ws, st);   // (else the join or the launch sets it)
   if (e != cudaSuccess) return cuda_fail(e, "clear status");
   if (p->R == 0) return DSA_OK;
-  float *ml = reinterpret_cast<float*>(w + kp.off_ml), *part = reinterpret_cast<float*>(w + kp.off_part);
-  e = kp.many ? launch_kv4_tile(*c, kp.cache, *p, kp.dense, out, lse, part, ml, static_cast<uint32_t*>(ws), st, hooks)
-              : launch_kv4_attn(*c, kp.cache, *p, kp.shape, out, lse, w, ml, part, st, hooks);
+  e = kp.many ? launch_kv4_tile(*c, kp.cache, *p, kp.tile, out, lse, w, st, hooks)
+              : launch_kv4_attn(*c, kp.cache, *p, kp.shape, out, lse, w, reinterpret_cast<float*>(w + kp.off_ml),
+                                reinterpret_cast<float*>(w + kp.off_part), st, hooks);
   if (e != cudaSuccess) return cuda_fail(e, "attention over the 4-bit cache");
   return DSA_OK;
 }

@@ -9,7 +9,7 @@ template <int DK, int DV, int NW, bool F16>
 cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
   constexpr size_t smem = smem_bytes<DK, DV, NW>();
   static_assert(smem <= 232448, "shared memory of one CTA");
-  auto kernel = dense_attn_kernel<DK, DV, NW, F16, false>;
+  auto kernel = dense_attn_kernel<DK, DV, NW, F16, kPacked>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t items = item_count(a), slots = dense_slots(NW);

@@ -61,12 +61,16 @@
 
 #include "dense.cuh"
 #include "kv4.cuh"
+#include "kv4_widen.cuh"
 #include "tc.cuh"
 
 namespace dsa {
 namespace {
 
 constexpr int kTile = 128;
+// Where K and V come from: a packed 16-bit cache; pages in 4 bits, widened by the kernel itself; a
+// copy in 16 bits that was made of such pages, request b's positions from b * reach on.
+enum CacheKind { kPacked, kPages, kCopied };
 // The softmax weights are held as 2^lift of them.
 template <bool F16>
 constexpr float kLift = F16 ? 7.f : 0.f;
@@ -91,18 +95,20 @@ struct DenseArgs {
   int test_no_load;       // test hook: arm the first chunk, issue no copy (Q4: do not hand it over)
   int q_tma;        // Q tiles by TMA (the group divides a tile), else by the softmax warps
   float scale, c;   // c = scale * log2 e
-  CacheArgs kv4;    // Q4: the pool of pages in place of tk, tv and offsets
-  int reach;        // Q4: positions that a row sees at most
+  CacheArgs kv4;        // pages: the pool, in place of tk, tv and offsets
+  int reach;            // pages: positions that a row sees at most
+  const int32_t* gone;  // copy: whether a page that a request's rows see is outside the pool
 };
 
 struct Item {
   int rows, r0, t0, h;   // rows = 0: no more items.  Packed rows and first row of the request; first packed row here
-  int o0, len;           // the request's positions (Q4: o0 is the request)
+  int o0, len;           // the request's positions (pages: o0 is the request)
   int split, parts;      // part of the item's positions
   int slot;              // its rows among the tail's, or -1
   int lo, steps;         // K/V tiles of this part
   int cnt[2];            // of them, those each row tile needs
   int kv_end;            // positions past it are seen by no row of the item
+  int gone;              // copy: some of its pages are outside the pool
 };
 
 constexpr int kBlocks = 64;   // request blocks of the lookup table
@@ -117,7 +123,7 @@ struct __align__(16) Shared {
   volatile int steps[2];          // K/V tiles that each row tile's issuer is through with
   Item item[2];
   int first[kBlocks + 1];         // row tiles before each block of requests
-  uint32_t there[16];             // Q4: of each K/V tile, a byte for every 32 positions: bits of 16 whose page the pool has
+  uint32_t there[16];             // pages: of each K/V tile, a byte for every 32 positions: bits of 16 whose page the pool has
 };
 
 template <int DK, int DV, int NW>
@@ -144,10 +150,10 @@ __device__ __forceinline__ void request_rows(const DenseArgs& a, int b, int& r0,
 }
 
 // Request b's positions, clamped to the call's.
-template <bool Q4>
+template <CacheKind Kind>
 __device__ __forceinline__ void request_cache(const DenseArgs& a, int b, int& o0, int& len) {
-  if (Q4) {
-    o0 = b;
+  if (Kind != kPacked) {
+    o0 = Kind == kPages ? b : b * a.reach;
     len = a.reach;
     return;
   }
@@ -158,7 +164,7 @@ __device__ __forceinline__ void request_cache(const DenseArgs& a, int b, int& o0
 
 // Up to kBlocks requests, held by the scheduler's lanes (lane, lane + 32): between
 // items, dependent loads are what the next one's first MMA waits for.
-template <bool Q4>
+template <CacheKind Kind>
 struct Requests {
   int r0[2], n[2], o0[2], len[2];
   __device__ __forceinline__ void load(const DenseArgs& a, int lane) {
@@ -168,15 +174,15 @@ struct Requests {
       const int b = lane + 32 * x;
       if (a.B > kBlocks || b >= a.B) continue;
       request_rows(a, b, r0[x], n[x]);
-      request_cache<Q4>(a, b, o0[x], len[x]);
+      request_cache<Kind>(a, b, o0[x], len[x]);
     }
   }
 };
 
 // Item `idx` (one warp).  Row tiles are numbered over the requests; the last ones
 // (a causal prompt's longest) come first, K/V heads and parts vary fastest.
-template <int NW, bool Q4>
-__device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it, int lane, const Requests<Q4>& rq,
+template <int NW, CacheKind Kind>
+__device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it, int lane, const Requests<Kind>& rq,
                           uint32_t* status) {
   int parts = a.splits, split = 0, slot = -1;
   if (a.tail_parts > 1 && idx >= (uint32_t)a.full) {
@@ -229,7 +235,7 @@ __device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it
         break;
       }
     }
-    request_cache<Q4>(a, b, o0, len);
+    request_cache<Kind>(a, b, o0, len);
   }
   const int rows = n * a.G, t0 = tile * NW * kTile;
   // The farthest position each row tile sees: at most 128 lengths each, loaded together.
@@ -268,37 +274,20 @@ __device__ void find_item(const DenseArgs& a, uint32_t idx, Shared* sh, Item* it
     it->steps = hi - lo;
     for (int w = 0; w < 2; ++w) it->cnt[w] = max(min((end[w] + kTile - 1) / kTile, hi) - lo, 0);
     it->kv_end = kv_end;
+    if (Kind == kCopied) it->gone = a.gone[o0 / max(a.reach, 1)];
   }
 }
 
-// Eight 4-bit codes times their scale (bf16 bits) in 16 bits, in order.  bf16: 128 + code by byte
-// permutations, then one packed multiply-add, (128 + code) s - 136 s: exact, since 136 s has 8
-// significant bits.  fp16: 1024 + code, minus 1032, times s: the last step alone may round.
-template <bool F16>
-__device__ __forceinline__ void widen8(uint32_t w, uint32_t scale, uint32_t* o) {
-  const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
-  const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);   // codes 0..3, 4..7
-  constexpr uint32_t top = F16 ? 0x64646464u : 0x43434343u;
-  uint32_t u[4] = {__byte_perm(lo, top, 0x4140), __byte_perm(lo, top, 0x4342), __byte_perm(hi, top, 0x4140),
-                   __byte_perm(hi, top, 0x4342)};
-  if (F16) {
-    const float s = __uint_as_float(scale << 16);
-    const __half2 s2 = __floats2half2_rn(s, s), zero = __floats2half2_rn(-1032.f, -1032.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 v = __hmul2(__hadd2(*reinterpret_cast<__half2*>(&u[i]), zero), s2);
-      o[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-  } else {
-    uint32_t sb = scale * 0x10001u;
-    const __nv_bfloat162 s2 = *reinterpret_cast<__nv_bfloat162*>(&sb);
-    const __nv_bfloat162 zero = __hmul2(s2, __floats2bfloat162_rn(-136.f, -136.f));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&u[i]), s2, zero);
-      o[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+// Which sixteens of the 128 positions from `pos` on lie in pages that the pool has, for a copy whose
+// request begins at o0.
+static __device__ __noinline__ uint32_t pages_there(const DenseArgs& a, int o0, int pos, int end) {
+  const int32_t* table = a.kv4.table + (int64_t)(o0 / a.reach) * a.kv4.cols;
+  uint32_t there = 0;
+  for (int x = 0; x < 8; ++x) {
+    const int id = pos + 16 * x < end ? table[(pos + 16 * x) >> a.kv4.ps_log2] : 0;
+    there |= (uint32_t)(id >= 0 && id < a.kv4.n_pages) << x;
   }
+  return there;
 }
 
 // Lane i of four adjacent ones holds four 16-byte pieces of row i; afterwards piece i of
@@ -321,13 +310,15 @@ __device__ __forceinline__ void exchange4(uint32_t* p, int lane) {
   }
 }
 
-// Threads of a CTA: four warps of roles, Q4's four converting warps, four of softmax for each row tile.
-template <int NW, bool Q4>
-constexpr int kDenseThreads = 128 + (Q4 ? 128 : 0) + 128 * NW;
+// Threads of a CTA: four warps of roles, four that widen pages, four of softmax for each row tile.
+template <int NW, CacheKind Kind>
+constexpr int kDenseThreads = 128 + (Kind == kPages ? 128 : 0) + 128 * NW;
 
-template <int DK, int DV, int NW, bool F16, bool Q4>
-__global__ void __launch_bounds__(kDenseThreads<NW, Q4>, NW == 1 && !Q4 ? 2 : 1)
+template <int DK, int DV, int NW, bool F16, CacheKind Kind>
+__global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
     dense_attn_kernel(const __grid_constant__ DenseArgs a) {
+  constexpr bool Q4 = Kind == kPages;       // four bits in, K and V tiles made here
+  static_assert(!Q4 || NW == 2, "registers of the widening warps");
   constexpr int NS = ring_slots<DK, DV, NW>();
   constexpr int KC = DK / 64, VC = DV / 64;
   constexpr uint32_t kQBytes = kTile * DK * 2;
@@ -406,7 +397,7 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Q4>, NW == 1 && !Q4 ? 2 : 1)
     }
     if (lane == 0) sh->first[kBlocks] = run;
   }
-  Requests<Q4> rq;
+  Requests<Kind> rq;
   if (warp == 3) rq.load(a, lane);
   tc_fence_before();
   __syncthreads();
@@ -447,7 +438,7 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Q4>, NW == 1 && !Q4 ? 2 : 1)
       if (k >= 2 && !wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc)) break;
       Item* it = &sh->item[k & 1];
       if (idx < items)
-        find_item<NW, Q4>(a, idx, sh, it, lane, rq, status);
+        find_item<NW, Kind>(a, idx, sh, it, lane, rq, status);
       else if (lane == 0)
         it->rows = 0;
       __syncwarp();
@@ -744,6 +735,7 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Q4>, NW == 1 && !Q4 ? 2 : 1)
       const Item& si = sh->item[k & 1];
       const int rows = si.rows, t0 = si.t0 + w * kTile, r0 = si.r0, h = si.h, split = si.split, parts = si.parts, slot = si.slot;
       const int mine = w ? si.cnt[1] : si.cnt[0], lo = si.lo, kv_end = si.kv_end, reach = si.len, steps = si.steps;
+      const int o0 = si.o0, gone = Kind == kCopied ? si.gone : 0;
       item_done(k);
       if (rows == 0) break;
       const int packed = t0 + (warp & 3) * 32 + lane;      // packed row in the request
@@ -772,6 +764,7 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Q4>, NW == 1 && !Q4 ? 2 : 1)
       float m = -INFINITY, l = 0.f;
       for (int jj = 0; jj < mine; ++jj, ++tiles) {
         const int tiles_all = before + jj;
+        uint32_t there = 0xffu;                            // copy: of 16 positions each
         if (!(ok = wait_bar_warp(bar(sh->sfull[w]), tiles & 1, wc))) break;
         tc_fence_after();
         if (any) {
@@ -790,6 +783,12 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Q4>, NW == 1 && !Q4 ? 2 : 1)
 #pragma unroll
             for (int x = 0; x < 128; ++x)
               if (!(there >> (x / 32 * 8 + x / 16 % 2) & 1u)) v[x] = 0xff800000u;
+          }
+          if (Kind == kCopied && gone) {
+            there = pages_there(a, o0, (lo + jj) * kTile, kv_end);
+#pragma unroll
+            for (int x = 0; x < 128; ++x)
+              if (!(there >> (x / 16) & 1u)) v[x] = 0xff800000u;
           }
           float t[4];
 #pragma unroll
@@ -837,7 +836,9 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Q4>, NW == 1 && !Q4 ? 2 : 1)
             tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 64; ++x)
-              if (x >= left || (Q4 && !(sh->there[tiles_all & 15] >> (x / 32 * 8 + x / 16 % 2) & 1u))) v[x] = 0xff800000u;
+              if (x >= left || (Q4 && !(sh->there[tiles_all & 15] >> (x / 32 * 8 + x / 16 % 2) & 1u)) ||
+                  (Kind == kCopied && !(there >> (x / 16) & 1u)))
+                v[x] = 0xff800000u;
             sum[0] = sum[1] = make_float2(0.f, 0.f);
             weights(0);
           }

@@ -57,11 +57,24 @@ struct Kv4Shape {
   bool join;
 };
 Kv4Shape kv4_shape(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
-// The kernel for many rows (kv4_tile.cu): its problem as dense attention's, and the launch.
+// The kernel for many rows (kv4_tile.cu): its problem as dense attention's, how it is cut, its
+// workspace and the launch.
+struct Kv4Tile {
+  DenseShape shape;
+  bool copied;           // the pages are widened into the workspace first
+  size_t off_ml, off_part, off_gone, off_k, off_v, total;
+};
+constexpr int kCopyRows = 1024;                      // packed rows of a request
+constexpr size_t kCopyBytes = size_t(1) << 33;
 dsa_dense_problem kv4_dense(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
-cudaError_t launch_kv4_tile(const dsa_kv4_cache& c, const CacheArgs& ca, const dsa_kv4_problem& p, const DenseShape& s,
-                            uint16_t* out, float* lse, float* part, float* ml, uint32_t* status, cudaStream_t st,
-                            const TestHooks* hooks = nullptr);
+Kv4Tile kv4_tile(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
+cudaError_t launch_kv4_tile(const dsa_kv4_cache& c, const CacheArgs& ca, const dsa_kv4_problem& p, const Kv4Tile& s,
+                            uint16_t* out, float* lse, char* ws, cudaStream_t st, const TestHooks* hooks = nullptr);
+// Clears the status block and widens the pages that rows see, request b's positions to rows b * reach on
+// of k and v; gone [B], lens [B]: scratch (kv4_cache.cu).
+cudaError_t launch_kv4_copy(const CacheArgs& c, int R, int reach, const int32_t* row_offsets, const int32_t* row_len, int D_k,
+                            int D_v, bool f16, uint16_t* k, uint16_t* v, int32_t* gone, int32_t* lens, uint32_t* status,
+                            cudaStream_t st);
 // Whether a call goes to that kernel.
 bool kv4_many_rows(const dsa_kv4_cache& c, const dsa_kv4_problem& p);
 inline size_t kv4_parts(const Kv4Shape& s) { return s.join ? (size_t)2 * s.grid * s.rows : 0; }

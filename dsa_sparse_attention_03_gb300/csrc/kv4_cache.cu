@@ -15,10 +15,11 @@
 // most 11 significant bits and a scale 4, so the fp32 quotient is a half only where the real
 // one is.
 //
-// Read.  code * scale, one 32-bit word of codes to 16 bytes; in bf16 by packed products
-// that are exact.
+// Read.  code * scale, 8 bytes of codes of a lane to 32 bytes of values, by packed products that
+// are exact in bf16 (kv4_widen.cuh).
 //
 // Both move each byte once and are bound by HBM, or by latency for few rows.
+#include "kv4_widen.cuh"
 #include "rope.cuh"
 
 namespace dsa {
@@ -379,27 +380,15 @@ __global__ void __launch_bounds__(kTurnThreads, 4) kv4_append_kernel(const __gri
   }
 }
 
-// Eight codes times their scale, in 16 bits.
-template <bool F16>
-__device__ __forceinline__ uint4 dequantise(uint32_t w, uint16_t scale) {
-  uint32_t o[4];
-  if (F16) {
-    const float s = __uint_as_float((uint32_t)scale << 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = pack16<true>((float)((int)(w >> (8 * i) & 15u) - 8) * s, (float)((int)(w >> (8 * i + 4) & 15u) - 8) * s);
-  } else {
-    const __nv_bfloat162 s = __halves2bfloat162(__ushort_as_bfloat16(scale), __ushort_as_bfloat16(scale));
-    const __nv_bfloat162 zero = __floats2bfloat162_rn(-136.f, -136.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = w >> (8 * i);
-      uint32_t u = (b & 15u) | ((b & 0xf0u) << 12) | 0x43004300u;   // 128 + code, twice
-      const __nv_bfloat162 v = __hmul2(__hadd2(*reinterpret_cast<__nv_bfloat162*>(&u), zero), s);
-      o[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+// 32 bytes; in halves where the caller's buffer is aligned to 16 alone.
+__device__ __forceinline__ void store8(uint16_t* p, const uint32_t* v) {
+  if (reinterpret_cast<uintptr_t>(p) & 31) {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
 }
 
 template <int N>
@@ -407,9 +396,52 @@ struct Width {
   static constexpr int value = N;
 };
 
-// A warp takes 128 words (32 bits of codes) of a row's K or V at a time, four loads to a lane; a CTA `rows`
-// rows, of which eight warps share the pieces.
-constexpr int kReadRows = 16;   // at most
+// A row is read in rounds: 32 lanes of 16 columns each (8 bytes of codes, 32 of values), the keys' rounds, then
+// the values'.
+template <int D>
+__device__ __forceinline__ int read_rounds(int heads) { return (heads * (D / 16) + 31) / 32; }
+
+// Four rounds from `first` on of one row, by one warp, their loads under way together.  page: the byte of
+// the pool where it begins (-1: nothing is read or written; -2: zeros are written).  ko, vo: the row's places.
+template <int DK, int DV, bool F16>
+__device__ __forceinline__ void read_row(const CacheArgs& c, int64_t page, uint32_t place, uint16_t* ko, uint16_t* vo, int nk, int nv,
+                                         int first, int lane) {
+  if (page == -1) return;
+  const uint8_t* p = c.pages + page;
+  uint2 w[4];
+  uint32_t s[4];
+  uint16_t* to[4];
+  auto look = [&](auto width, int round, uint32_t codes, uint32_t scales, uint16_t* out, int u) {
+    constexpr int N = decltype(width)::value / 16;        // pieces of a head
+    const uint32_t x = round * 32 + lane, h = x / N, j = x - h * N;
+    if (h >= (uint32_t)c.H_kv) return;
+    to[u] = out + x * 16;
+    if (page < 0) return;
+    const uint32_t blk = h * c.block, n = (j >> 2) * c.ps + place;
+    w[u] = *reinterpret_cast<const uint2*>(p + (blk + codes + n * 32 + (j & 3) * 8));
+    s[u] = *reinterpret_cast<const uint16_t*>(p + (blk + scales + n * 2));
+  };
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    w[u] = make_uint2(0, 0);
+    s[u] = 0;
+    to[u] = nullptr;
+    const int round = first + u;
+    if (round < nk)
+      look(Width<DK>(), round, 0, c.ps * ((DK + DV) / 2), ko, u);
+    else if (round < nk + nv)
+      look(Width<DV>(), round - nk, c.ps * (DK / 2), c.ps * ((DK + DV) / 2 + DK / 32), vo, u);
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t o[8];
+    widen8<F16>(w[u].x, s[u], o);
+    widen8<F16>(w[u].y, s[u], o + 4);
+    if (to[u]) store8(to[u], o);
+  }
+}
+
+constexpr int kReadRows = 16;   // rows of a CTA, at most
 
 template <int DK, int DV, bool F16>
 __global__ void __launch_bounds__(kThreads)
@@ -441,42 +473,65 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   __syncthreads();
-  auto piece = [&](auto width, uint16_t* out, uint32_t codes, uint32_t scales, int i, int first) {
-    constexpr int W = decltype(width)::value / 8;    // words of a head
-    const int per = c.H_kv * W;
-    const int64_t page = pages[i];
-    if (page < 0) return;
-    const uint8_t* p = c.pages + page;
-    const uint32_t at = places[i];
-    uint4* to = reinterpret_cast<uint4*>(out) + (row0 + i) * per;
-    uint32_t w[4];
-    uint16_t s[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t x = min(first + 32 * u + lane, per - 1), h = x / W, j = x - h * W;
-      const uint32_t n = (j >> 3) * c.ps + at, blk = h * c.block;
-      w[u] = *reinterpret_cast<const uint32_t*>(p + (blk + codes + n * 32 + (j & 7) * 4));
-      s[u] = *reinterpret_cast<const uint16_t*>(p + (blk + scales + n * 2));
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int x = first + 32 * u + lane;
-      if (x < per) to[x] = dequantise<F16>(w[u], s[u]);
-    }
-  };
-  const int nk = k_out ? (c.H_kv * (DK / 8) + 127) / 128 : 0, nv = v_out ? (c.H_kv * (DV / 8) + 127) / 128 : 0;
-  int i = warp % rows, y = warp / rows;              // (a piece of every row, then the next)
-  for (; y < nk + nv;) {
-    if (y < nk)
-      piece(Width<DK>(), k_out, 0, c.ps * ((DK + DV) / 2), i, 128 * y);
-    else
-      piece(Width<DV>(), v_out, c.ps * (DK / 2), c.ps * ((DK + DV) / 2 + DK / 32), i, 128 * (y - nk));
-    i += kThreads / 32;
+  const int nk = k_out ? read_rounds<DK>(c.H_kv) : 0, nv = v_out ? read_rounds<DV>(c.H_kv) : 0;
+  int i = warp, first = 0;                           // (four rounds of every row, then the next)
+  for (;;) {
     while (i >= rows) {
       i -= rows;
-      ++y;
+      first += 4;
     }
+    if (first >= nk + nv) break;
+    read_row<DK, DV, F16>(c, pages[i], places[i], k_out + (row0 + i) * c.H_kv * DK, v_out + (row0 + i) * c.H_kv * DV, nk, nv, first,
+                          lane);
+    i += kThreads / 32;
   }
+}
+
+// Clears the status block (64 words) and counts how far each request's rows see: a CTA to a request.
+__global__ void __launch_bounds__(kThreads)
+    kv4_lens_kernel(int R, int reach, const int32_t* row_offsets, const int32_t* row_len, int32_t* gone, int32_t* lens,
+                    uint32_t* status) {
+  __shared__ int most[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x, r0 = min(max(row_offsets[b], 0), R), r1 = min(row_offsets[b + 1], R);
+  if (b == 0 && threadIdx.x < 64) status[threadIdx.x] = 0;
+  int m = 0;
+  for (int r = r0 + threadIdx.x; r < r1; r += kThreads) m = max(m, min(row_len[r], reach));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) m = max(m, most[w]);
+    lens[b] = m;
+    gone[b] = 0;
+  }
+}
+
+// Sixteen positions of a request, which lie in one page, to the copy.
+template <int DK, int DV, bool F16>
+__global__ void __launch_bounds__(kThreads, 4)
+    kv4_copy_kernel(const CacheArgs c, int reach, int blocks, uint16_t* k, uint16_t* v, int32_t* gone, const int32_t* lens,
+                    uint32_t* status) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x / blocks, pos = (blockIdx.x - b * blocks) * 16;
+  pdl_wait();
+  pdl_trigger();
+  const int n = min(lens[b] - pos, 16);
+  if (n <= 0) return;
+  int64_t page = find_page(c, b, pos);
+  if (page < 0) {
+    if (threadIdx.x == 0) {
+      raise_status(status, DSA_DEVICE_BAD_INDEX);
+      gone[b] = 1;
+    }
+    page = -2;
+  }
+  const int64_t row0 = (int64_t)b * reach + pos;
+  const int nk = read_rounds<DK>(c.H_kv), nv = read_rounds<DV>(c.H_kv);
+  for (int i = warp; i < n; i += kThreads / 32)
+    for (int first = 0; first < nk + nv; first += 4)
+      read_row<DK, DV, F16>(c, page, (pos + i) & (c.ps - 1), k + (row0 + i) * c.H_kv * DK, v + (row0 + i) * c.H_kv * DV, nk, nv,
+                            first, lane);
 }
 
 template <int DK, int DV>
@@ -500,6 +555,15 @@ cudaError_t launch_read_width(const CacheArgs& c, int R, const int32_t* row_offs
                           v_out, status);
 }
 
+template <int DK, int DV>
+cudaError_t launch_copy_width(const CacheArgs& c, int reach, bool f16, uint16_t* k, uint16_t* v, int32_t* gone,
+                              const int32_t* lens, uint32_t* status, cudaStream_t st) {
+  const int blocks = (reach + 15) / 16;
+  const dim3 grid((unsigned)(c.B * blocks));
+  return f16 ? launch_pdl(kv4_copy_kernel<DK, DV, true>, grid, dim3(kThreads), 0, st, c, reach, blocks, k, v, gone, lens, status)
+             : launch_pdl(kv4_copy_kernel<DK, DV, false>, grid, dim3(kThreads), 0, st, c, reach, blocks, k, v, gone, lens, status);
+}
+
 }  // namespace
 
 cudaError_t launch_kv4_append(TurnArgs a, const CacheArgs& c, int D_k, int D_v, bool f16, uint32_t* status, cudaStream_t st) {
@@ -515,6 +579,18 @@ cudaError_t launch_kv4_read(const CacheArgs& c, int R, const int32_t* row_offset
   if (D_k == 64) return launch_read_width<64, 64>(c, R, row_offsets, positions, f16, k_out, v_out, status, st);
   if (D_k == 128) return launch_read_width<128, 128>(c, R, row_offsets, positions, f16, k_out, v_out, status, st);
   return launch_read_width<192, 128>(c, R, row_offsets, positions, f16, k_out, v_out, status, st);
+}
+
+cudaError_t launch_kv4_copy(const CacheArgs& c, int R, int reach, const int32_t* row_offsets, const int32_t* row_len, int D_k,
+                            int D_v, bool f16, uint16_t* k, uint16_t* v, int32_t* gone, int32_t* lens, uint32_t* status,
+                            cudaStream_t st) {
+  (void)D_v;
+  const cudaError_t e = launch_pdl(kv4_lens_kernel, dim3((unsigned)c.B), dim3(kThreads), 0, st, R, reach, row_offsets, row_len,
+                                   gone, lens, status);
+  if (e != cudaSuccess) return e;
+  if (D_k == 64) return launch_copy_width<64, 64>(c, reach, f16, k, v, gone, lens, status, st);
+  if (D_k == 128) return launch_copy_width<128, 128>(c, reach, f16, k, v, gone, lens, status, st);
+  return launch_copy_width<192, 128>(c, reach, f16, k, v, gone, lens, status, st);
 }
 
 }  // namespace dsa

@@ -335,3 +335,145 @@ def test_missing_stage_is_bounded(rows):
     dsa.dsa_kv4_attn(prob, out, None, ws)
     assert dsa.dsa_read_device_status(ws) == 0
     H.check(t, 0.09, out.cpu(), None)
+
+
+# Many rows of a request: the pages are widened into the workspace first.
+
+def _few(t, keep):
+    """The problem's rows `keep` (of one or several requests, ascending) alone."""
+    import torch
+    ro = t["row_offsets"].tolist()
+    n = [sum(1 for r in keep if a <= r < b) for a, b in zip(ro, ro[1:])]
+    return dict(t, q=t["q"][keep], row_len=t["row_len"][keep], row_offsets=H.prefix(n))
+
+
+def _sample(rows, step=37):
+    out, r = [], 0
+    for n in rows:
+        out += sorted({r, r + n - 1, r + n // 2} | set(range(r + 2, r + n, step)))
+        r += n
+    return out
+
+
+@pytest.mark.parametrize("dk,dv", W)
+@pytest.mark.parametrize("dt,ps,rows,lens,hq,hkv", [
+    ("bf16", 64, [1030], [1030], 2, 2),                      # a prompt of one head to a K/V head
+    ("fp16", 16, [300, 1, 513, 0, 7], [300, 900, 1500, 40, 7], 8, 2),
+    ("bf16", 128, [400], [2500], 3, 1),                      # a group that does not divide a row tile
+])
+def test_copied(dk, dv, dt, ps, rows, lens, hq, hkv):
+    t = H.make(rows, lens, hq, hkv, dk, dv, ps, dt, seed=dk + ps)
+    scale = 1 / math.sqrt(dk)
+    out, lse, bits = H.run(t, scale)
+    assert bits == 0
+    keep = _sample(rows)
+    H.check(_few(t, keep), scale, out[keep], lse[keep])
+    again, _, _ = H.run(t, scale, ws_fill=0xC3)
+    assert again.equal(out)
+
+
+def test_copied_and_not_agree():
+    # The three kernels on one problem: few rows at a time, widened by the way, widened first.
+    t = H.make([600, 2], [900, 40], 4, 2, 128, 128, 32, seed=40)
+    outs = [H.run(t, 0.09, rows_max=n)[0].double() for n in (1, 300, 600)]
+    ref, _, bound, _ = H.reference(_few(t, _sample([600, 2])), 0.09)
+    for out in outs:
+        assert bool(((out[_sample([600, 2])] - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_copied_any_row_len_and_places_no_row_sees(dt):
+    import torch
+    g = torch.Generator().manual_seed(41)
+    rows, lens, ps = [700, 560], [900, 640], 64
+    rl = [int(torch.randint(0, L - 60, (1,), generator=g)) * (i % 5 != 1) for n, L in zip(rows, lens) for i in range(n)]
+    t = H.make(rows, lens, 4, 2, 128, 128, ps, dt, seed=41, row_len=rl)
+    dirty = dict(t, pages=t["pages"].clone(), table=t["table"].clone())
+    seen = torch.zeros(t["pages"].shape[0], ps, dtype=torch.bool)
+    for b, (n, a) in enumerate(zip(rows, (0, rows[0]))):
+        far = max(rl[a:a + n])
+        for x in range(far):
+            seen[t["table"][b, x // ps], x % ps] = True
+        dirty["table"][b, -(-far // ps):] = -9
+    _, _, ks, vs = H.parts(dirty["pages"], 128, 128, ps)
+    ks.masked_fill_(~seen[:, None, None], float("inf"))
+    vs.masked_fill_(~seen[:, None, None], float("nan"))
+    out, lse, bits = H.run(dirty, 0.1)
+    assert bits == 0 and not out[t["row_len"] == 0].any()
+    keep = _sample(rows)
+    H.check(_few(t, keep), 0.1, out[keep], lse[keep])
+
+
+def test_copied_bad_pages_are_masked_and_flagged():
+    import dsa_sparse_attention_03_gb300 as dsa
+    rows = [600, 520]
+    t = H.make(rows, [900, 600], 4, 2, 128, 128, 32, seed=42)
+    t["table"][0, 3] = -5
+    t["table"][0, 20] = t["pages"].shape[0]
+    out, lse, bits = H.run(t, 0.09)
+    assert bits & dsa.DSA_DEVICE_BAD_INDEX
+    keep = _sample(rows)
+    H.check(_few(t, keep), 0.09, out[keep], lse[keep])
+    t["table"][1] = -1
+    out, lse, bits = H.run(t, 0.09)
+    assert bits & dsa.DSA_DEVICE_BAD_INDEX and not out[600:].any() and (lse[600:] == -math.inf).all()
+    H.check(_few(t, keep), 0.09, out[keep], lse[keep])
+
+
+def test_copied_row_len_outside_and_rows_outside():
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    t = H.make([560, 540], [640, 640], 4, 2, 64, 64, 64, seed=43, extra_rows=3)
+    t["row_offsets"] += 2
+    t["row_len"] = torch.cat([t["row_len"][-2:], t["row_len"][:-2]])
+    t["row_len"][5], t["row_len"][9] = -4, 5000
+    out, lse, bits = H.run(t, 0.1, L_max=700)
+    assert bits & dsa.DSA_DEVICE_BAD_INDEX
+    assert (out[:2] == 77).all() and (out[1102:] == 77).all() and (lse[1102:] == 77).all()
+    good = dict(t, row_len=t["row_len"].clamp(0, 640))
+    keep = [2 + x for x in _sample([560, 540])] + [5, 9]
+    keep = sorted(set(keep))
+    few = dict(good, q=t["q"][keep], row_len=good["row_len"][keep],
+               row_offsets=H.prefix([sum(r < 562 for r in keep), sum(r >= 562 for r in keep)]))
+    H.check(few, 0.1, out[keep], lse[keep])
+
+
+def test_copied_captured():
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    rows, lens = [600, 1], [700, 2000]
+    t, other = (H.make(rows, lens, 4, 2, 128, 128, 64, seed=44 + i) for i in range(2))
+    prob = H.problem(t, 0.09)
+    out = torch.zeros(601, 4, 128, dtype=torch.bfloat16, device="cuda")
+    ws = dsa.alloc_kv4_workspace(prob)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        dsa.dsa_kv4_attn(prob, out, None, ws)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        dsa.dsa_kv4_attn(prob, out, None, ws)
+    prob._keep["q"].copy_(other["q"])
+    prob._keep_cache._keep["pages"].copy_(other["pages"])
+    prob._keep_cache._keep["table"].copy_(other["table"])
+    out.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    want, _, _ = H.run(other, 0.09)
+    assert dsa.dsa_read_device_status(ws) == 0 and out.cpu().equal(want)
+
+
+def test_copied_missing_tile_is_bounded():
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    t = H.make([600], [2000], 4, 2, 128, 128, 64, seed=46)
+    prob = H.problem(t, 0.09)
+    out = torch.zeros(600, 4, 128, dtype=torch.bfloat16, device="cuda")
+    ws = dsa.alloc_kv4_workspace(prob)
+    dsa.dsa_test_kv4_missing_stage(prob, out, None, ws, 20_000_000)
+    assert dsa.dsa_read_device_status(ws) & dsa.DSA_DEVICE_TIMEOUT
+    dsa.dsa_kv4_attn(prob, out, None, ws)
+    assert dsa.dsa_read_device_status(ws) == 0
+    keep = _sample([600])
+    H.check(_few(t, keep), 0.09, out.cpu()[keep], None)

@@ -267,6 +267,21 @@ def test_read_is_exact(dk, dv, dt, ps):
     assert ko.cpu().equal(K[page, pos.long() % ps].to(ty)) and vo.cpu().equal(V[page, pos.long() % ps].to(ty))
 
 
+def test_read_into_a_view_and_one_of_the_two():
+    # Outputs that begin 16 bytes off a multiple of 32.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    t = H.make([0], [70], 2, 2, 128, 128, 32, seed=6)
+    cache = dsa.KV4Cache.from_tensors(pages=t["pages"].cuda(), table=t["table"].cuda(), page_size=32, D_k=128, D_v=128)
+    flat = torch.full((8 + 70 * 256 + 8,), 55.0, dtype=torch.bfloat16, device="cuda")
+    vo = flat[8:-8].view(70, 2, 128)
+    pos, ro, ws = torch.arange(70, dtype=torch.int32), H.prefix([70]).cuda(), dsa.alloc_kv4_workspace()
+    dsa.dsa_kv4_read(cache, ro, pos.cuda(), None, vo, ws)
+    _, V = H.values(t["pages"], 128, 128, 32)
+    assert vo.cpu().double().equal(V[t["table"][0, pos.long() // 32].long(), pos.long() % 32])
+    assert (flat[:8] == 55).all() and (flat[-8:] == 55).all()
+
+
 def test_pool_beyond_32_bits():
     import torch
     import dsa_sparse_attention_03_gb300 as dsa
