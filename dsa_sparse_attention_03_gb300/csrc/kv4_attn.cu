@@ -70,10 +70,11 @@ struct Args {
 };
 
 struct Item {
-  int row0, packed, first, h, b;   // packed = 0: no more items
+  int row0, packed, first, h;      // packed = 0: no more items
   int len;                         // positions that the request's rows see at most
   int stage, stages;               // the range of stages of this CTA
   int slot;                        // part of the workspace, or -1: the whole item
+  int see[2 * kBlock];             // positions that each packed row of the block sees
 };
 
 struct __align__(16) Shared {
@@ -166,15 +167,17 @@ __device__ __forceinline__ int stages_of(int len) { return max((len + kStage - 1
 
 template <int DK, int DV>
 constexpr uint32_t kStageBytes = kStage * (DK + DV) * 17 / 32;
+// Beside the ring: the queries of two items, the warps' sums and Shared.
+template <int DK, int DV, int NB>
+constexpr int kFixedBytes = 2 * NB * kBlock * DK * 2 + kWarps / 2 * kBlock * DV * 4 + (int)sizeof(Shared);
 template <int DK, int DV, int NB>
 __host__ __device__ constexpr int ring_stages() {
-  constexpr int rest = (NB == 1 ? 113 : 227) * 1024 - (int)sizeof(Shared) - kWarps / 2 * kBlock * DV * 4;
-  constexpr int s = rest / (int)kStageBytes<DK, DV>;
+  constexpr int s = ((NB == 1 ? 113 : 227) * 1024 - kFixedBytes<DK, DV, NB>) / (int)kStageBytes<DK, DV>;
   return s < 8 ? s / 2 * 2 : 8;   // (even: a stage's place belongs to one half of the warps)
 }
 template <int DK, int DV, int NB>
 __host__ __device__ constexpr size_t smem_bytes() {
-  return (size_t)ring_stages<DK, DV, NB>() * kStageBytes<DK, DV> + kWarps / 2 * kBlock * DV * 4 + sizeof(Shared);
+  return (size_t)ring_stages<DK, DV, NB>() * kStageBytes<DK, DV> + kFixedBytes<DK, DV, NB>;
 }
 
 template <int DK, int DV, int NB, bool F16>
@@ -182,7 +185,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   constexpr int GK = DK / 64, GV = DV / 64, ROWS = NB * kBlock, NS = ring_stages<DK, DV, NB>();
   constexpr uint32_t kBytes = kStageBytes<DK, DV>;
   extern __shared__ __align__(128) unsigned char smem[];
-  float* sums = reinterpret_cast<float*>(smem + NS * kBytes);        // [4, 8, DV]
+  constexpr uint32_t kQBytes = ROWS * DK * 2;
+  unsigned char* qs = smem + NS * kBytes;                            // [2, ROWS, DK]
+  float* sums = reinterpret_cast<float*>(qs + 2 * kQBytes);          // [4, 8, DV]
   Shared* sh = reinterpret_cast<Shared*>(sums + kWarps / 2 * kBlock * DV);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
@@ -224,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
     // ------------------------------------------------------------ producer
     int64_t total = 0;
     for (int w = 0; w <= kWarps; ++w) total += sh->units[w];
-    const int64_t shares = min(total, (int64_t)gridDim.x);
+    // (at least two stages to a share: the two halves of the warps take one each)
+    const int64_t shares = min((total + 1) / 2, (int64_t)gridDim.x);
     const int64_t lo = blockIdx.x < shares ? total * blockIdx.x / shares : 0;
     int64_t left = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares - lo : 0;
     int n = 0, k = 0;             // stages and items handed over
@@ -274,11 +280,28 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         const int cnt = (int)min((int64_t)(st - s0), left);
         const bool whole = cnt == st;
         if (k >= 2 && !(ok = wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc))) break;
+        // The item, with its rows' queries copied beside it.
+        const int pk = rb * ROWS + lane;
+        const bool row = lane < ROWS && pk < xn * a.G;
+        const uint32_t rows_here = __popc(__ballot_sync(0xffffffffu, row));
+        Item* it = &sh->item[k & 1];
+        if (lane < ROWS) it->see[lane] = row ? min(max(a.row_len[xr + pk / a.G], 0), reach) : xl;
         if (lane == 0) {
-          sh->item[k & 1] = Item{xr, xn * a.G, rb * ROWS, h, base + x, xl, s0, xl > 0 ? cnt : 0,
-                                 whole ? -1 : 2 * (int)blockIdx.x + (s0 == 0)};
-          mbar_arrive(bar(sh->ifull[k & 1]));
+          it->row0 = xr;
+          it->packed = xn * a.G;
+          it->first = rb * ROWS;
+          it->h = h;
+          it->len = xl;
+          it->stage = s0;
+          it->stages = xl > 0 ? cnt : 0;
+          it->slot = whole ? -1 : 2 * (int)blockIdx.x + (s0 == 0);
         }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(bar(sh->ifull[k & 1]), rows_here * DK * 2);
+        __syncwarp();
+        if (row)
+          bulk_row(smem_u32(qs) + (k & 1) * kQBytes + lane * DK * 2,
+                   a.q + (int64_t)(xr + pk / a.G) * a.q_stride + (int64_t)(h * a.G + pk % a.G) * DK, DK * 2, bar(sh->ifull[k & 1]));
         ++k;
         if (!whole && s0 == 0) {  // the item's other parts: as many shares as begin before its end
           int64_t i = blockIdx.x + 1;
@@ -328,6 +351,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
       }
       if (a.join) a.join[blockIdx.x] = join;
       for (int i = max(0, n - NS); i < n; ++i) drain_bar(bar(sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
+      // (An abort may leave queries in flight.  Otherwise they have been waited for, and the last item's
+      // arrival may be a later phase of the same barrier.)
+      for (int i = max(0, k - 2); i < k && !ok; ++i) drain_bar(bar(sh->ifull[i & 1]), (i >> 1) & 1, a.wait_ns);
     }
   } else {
     // ------------------------------------------------------------ products and softmax
@@ -355,12 +381,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
     int n0 = 0;                  // stages of earlier items
     for (int k = 0;; ++k) {
       bool ok = wait_bar_warp(bar(sh->ifull[k & 1]), (k >> 1) & 1, wc);
-      Item it;
+      struct {
+        int row0, packed, first, h, len, stage, stages, slot;
+      } it;
       it.packed = 0;
-      if (ok) it = sh->item[k & 1];
+      const Item& si = sh->item[k & 1];
+      if (ok) it = {si.row0, si.packed, si.first, si.h, si.len, si.stage, si.stages, si.slot};
       const bool last = it.packed == 0;
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(bar(sh->ifree[k & 1]));
       uint32_t qf[GK][NB][4][2];
       float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], sp[GV][NB][4], oo[GV][NB][4][4], vinv = 1.f;
       int see[NB][2];
@@ -370,14 +397,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         for (int nb = 0; nb < NB; ++nb) {
           const int pk = it.first + nb * kBlock + i;
           const bool valid = pk < it.packed;
-          const uint16_t* q = a.q + (int64_t)(it.row0 + (valid ? pk / a.G : 0)) * a.q_stride +
-                              (int64_t)(it.h * a.G + (valid ? pk % a.G : 0)) * DK + 16 * j;
+          const unsigned char* q = qs + (k & 1) * kQBytes + (nb * kBlock + i) * DK * 2 + 32 * j;
           uint4 w[GK][2];
 #pragma unroll
           for (int g = 0; g < GK; ++g)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              w[g][x] = valid ? *reinterpret_cast<const uint4*>(q + 64 * g + 8 * x) : make_uint4(0, 0, 0, 0);
+              w[g][x] = valid ? *reinterpret_cast<const uint4*>(q + 128 * g + 16 * x) : make_uint4(0, 0, 0, 0);
           auto value = [&](int g, int c) {   // column 64 g + 16 j + c
             const uint4 v = w[g][c >> 3];
             const uint32_t y = (c & 7) < 2 ? v.x : (c & 7) < 4 ? v.y : (c & 7) < 6 ? v.z : v.w;
@@ -413,8 +439,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             factor[nb][x] = a.c2 * (0x1p24f / __shfl_sync(0xffffffffu, up, 4 * (2 * j + x)));
-            const int r = it.first + nb * kBlock + 2 * j + x;
-            see[nb][x] = r < it.packed ? min(max(a.row_len[it.row0 + r / a.G], 0), reach) : it.len;
+            see[nb][x] = si.see[nb * kBlock + 2 * j + x];
             mm[nb][x] = 0.f;
             l[nb][x] = 0.f;
           }
@@ -433,6 +458,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) least = min(least, min(see[nb][0], see[nb][1]));
         least = __reduce_min_sync(0xffffffffu, least);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->ifree[k & 1]));   // (the item and its queries are read)
         bool first = true;         // no positions so far
         // Every other stage is this warp's.
         int pos = it.stage * kStage + p0 + ((n0 ^ (warp >> 2)) & 1) * kStage;   // the warp's first position
