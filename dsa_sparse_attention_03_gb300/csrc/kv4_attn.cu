@@ -49,6 +49,7 @@ constexpr int kStage = 128;      // positions
 constexpr int kWarps = 8;        // that compute; one more loads
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kBlock = 8;        // packed rows of a product's column block
+constexpr int kItems = 3;        // handed over at once
 
 struct Args {
   CacheArgs c;
@@ -64,7 +65,7 @@ struct Args {
   uint32_t* bits;     // status bits of each CTA, for the join; or null: the status is cleared before, and raised
   int64_t q_stride;
   uint64_t wait_ns;
-  int R, H_q, G, L_max;
+  int R, H_q, G, L_max, f16;
   int test_no_load;
   float c2;           // softmax_scale * log2 e
 };
@@ -74,16 +75,19 @@ struct Item {
   int len;                         // positions that the request's rows see at most
   int stage, stages;               // the range of stages of this CTA
   int slot;                        // part of the workspace, or -1: the whole item
-  int see[2 * kBlock];             // positions that each packed row of the block sees
+  // Of each packed row of the block: positions it sees, what a sum of its products is to be multiplied
+  // with, and the sums that 8 less in every code makes.
+  int see[2 * kBlock];
+  float factor[2 * kBlock], less[3][2 * kBlock];
 };
 
 struct __align__(16) Shared {
   uint64_t full[8], empty[8];
-  uint64_t ifull[2], ifree[2];
+  uint64_t ifull[kItems], ifree[kItems];
   int abort;
   uint32_t bits;
   uint32_t pages[8];            // pages of each stage that the pool has
-  Item item[2];
+  Item item[kItems];
   int64_t units[kWarps + 1];    // of each warp's requests
   float m[kWarps][2 * kBlock], l[kWarps][2 * kBlock];
 };
@@ -94,6 +98,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from accumulators that two columns share.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 // An 8 x 8 block of 16-bit values, lane i holding row i / 4, transposed.
@@ -167,9 +180,9 @@ __device__ __forceinline__ int stages_of(int len) { return max((len + kStage - 1
 
 template <int DK, int DV>
 constexpr uint32_t kStageBytes = kStage * (DK + DV) * 17 / 32;
-// Beside the ring: the queries of two items, the warps' sums and Shared.
+// Beside the ring: the queries of the items, the warps' sums and Shared.
 template <int DK, int DV, int NB>
-constexpr int kFixedBytes = 2 * NB * kBlock * DK * 2 + kWarps / 2 * kBlock * DV * 4 + (int)sizeof(Shared);
+constexpr int kFixedBytes = kItems * NB * kBlock * DK * 2 + kWarps / 2 * kBlock * DV * 4 + (int)sizeof(Shared);
 template <int DK, int DV, int NB>
 __host__ __device__ constexpr int ring_stages() {
   constexpr int s = ((NB == 1 ? 113 : 227) * 1024 - kFixedBytes<DK, DV, NB>) / (int)kStageBytes<DK, DV>;
@@ -180,25 +193,27 @@ __host__ __device__ constexpr size_t smem_bytes() {
   return (size_t)ring_stages<DK, DV, NB>() * kStageBytes<DK, DV> + kFixedBytes<DK, DV, NB>;
 }
 
-template <int DK, int DV, int NB, bool F16>
+template <int DK, int DV, int NB, int PS>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(const __grid_constant__ Args a) {
   constexpr int GK = DK / 64, GV = DV / 64, ROWS = NB * kBlock, NS = ring_stages<DK, DV, NB>();
   constexpr uint32_t kBytes = kStageBytes<DK, DV>;
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr uint32_t kQBytes = ROWS * DK * 2;
-  unsigned char* qs = smem + NS * kBytes;                            // [2, ROWS, DK]
-  float* sums = reinterpret_cast<float*>(qs + 2 * kQBytes);          // [4, 8, DV]
+  unsigned char* qs = smem + NS * kBytes;                            // [items, ROWS, DK]
+  float* sums = reinterpret_cast<float*>(qs + kItems * kQBytes);          // [4, 8, DV]
   Shared* sh = reinterpret_cast<Shared*>(sums + kWarps / 2 * kBlock * DV);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
-  const int reach = (int)min((int64_t)a.L_max, (int64_t)a.c.cols << a.c.ps_log2);
+  const int reach = (int)min((int64_t)a.L_max, (int64_t)a.c.cols * PS);
+  constexpr uint32_t kPage = PS * (DK + DV) * 17 / 32;
+  constexpr int npp = kStage / PS;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(sh->full[i]), 1);
       mbar_init(bar(sh->empty[i]), kWarps / 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kItems; ++i) {
       mbar_init(bar(sh->ifull[i]), 1);
       mbar_init(bar(sh->ifree[i]), kWarps);
     }
@@ -279,13 +294,66 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         const int s0 = (int)(u - idx * st), rb = (int)(idx / a.c.H_kv), h = (int)(idx - (int64_t)rb * a.c.H_kv);
         const int cnt = (int)min((int64_t)(st - s0), left);
         const bool whole = cnt == st;
-        if (k >= 2 && !(ok = wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc))) break;
-        // The item, with its rows' queries copied beside it.
-        const int pk = rb * ROWS + lane;
-        const bool row = lane < ROWS && pk < xn * a.G;
-        const uint32_t rows_here = __popc(__ballot_sync(0xffffffffu, row));
-        Item* it = &sh->item[k & 1];
-        if (lane < ROWS) it->see[lane] = row ? min(max(a.row_len[xr + pk / a.G], 0), reach) : xl;
+        if (k >= kItems && !(ok = wait_bar_warp(bar(sh->ifree[k % kItems]), (k / kItems - 1) & 1, wc))) break;
+        // The item, with its rows' queries as the products take them: scaled to fp16's upper range by a power
+        // of two for each row, in the layout of the fragments (lane 4 i + j: row i, columns 16 j ..).
+        Item* it = &sh->item[k % kItems];
+        const int row = rb * ROWS + lane;
+        const bool live = lane < ROWS && row < xn * a.G;
+        const int sees = live ? a.row_len[xr + row / a.G] : 0;
+        {
+          const int i = lane >> 2, j = lane & 3;
+          uint4 w[NB][GK][2];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int pk = rb * ROWS + nb * kBlock + i;
+            const bool valid = pk < xn * a.G;
+            const uint16_t* q = a.q + (int64_t)(xr + (valid ? pk / a.G : 0)) * a.q_stride +
+                                (int64_t)(h * a.G + (valid ? pk % a.G : 0)) * DK + 16 * j;
+#pragma unroll
+            for (int g = 0; g < GK; ++g)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                w[nb][g][x] = valid ? *reinterpret_cast<const uint4*>(q + 64 * g + 8 * x) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            auto value = [&](int g, int c) {   // column 64 g + 16 j + c
+              const uint4 v = w[nb][g][c >> 3];
+              const uint32_t y = (c & 7) < 2 ? v.x : (c & 7) < 4 ? v.y : (c & 7) < 6 ? v.z : v.w;
+              const uint16_t z = (uint16_t)(c & 1 ? y >> 16 : y);
+              return a.f16 ? to_float<true>(z) : to_float<false>(z);
+            };
+            uint32_t top = 0;
+#pragma unroll
+            for (int g = 0; g < GK; ++g)
+#pragma unroll
+              for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(value(g, c)) & 0x7f800000u);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(14 - exponent of the row's largest)
+            const float up = top ? __uint_as_float(min((268u << 23) - top, 254u << 23)) : 1.f;
+#pragma unroll
+            for (int g = 0; g < GK; ++g) {
+              float sum = 0.f;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int c = 8 * (y >> 1) + 2 * (y & 1);
+                const __half2 lo = __floats2half2_rn(value(g, c) * up, value(g, c + 4) * up);
+                const __half2 hi = __floats2half2_rn(value(g, c + 1) * (up * 0.0625f), value(g, c + 5) * (up * 0.0625f));
+                reinterpret_cast<uint2*>(qs + k % kItems * kQBytes)[((g * NB + nb) * 4 + y) * 32 + lane] =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                const float2 fl = __half22float2(lo), fh = __half22float2(hi);
+                sum += fl.x + fl.y + 16.f * (fh.x + fh.y);
+              }
+              sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+              sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+              if (j == 0) it->less[g][nb * kBlock + i] = -0x1p-21f * sum;
+            }
+            if (j == 0) it->factor[nb * kBlock + i] = a.c2 * (0x1p24f / up);
+          }
+        }
+        if (lane < ROWS) it->see[lane] = live ? min(max(sees, 0), reach) : xl;
         if (lane == 0) {
           it->row0 = xr;
           it->packed = xn * a.G;
@@ -297,11 +365,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           it->slot = whole ? -1 : 2 * (int)blockIdx.x + (s0 == 0);
         }
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(bar(sh->ifull[k & 1]), rows_here * DK * 2);
-        __syncwarp();
-        if (row)
-          bulk_row(smem_u32(qs) + (k & 1) * kQBytes + lane * DK * 2,
-                   a.q + (int64_t)(xr + pk / a.G) * a.q_stride + (int64_t)(h * a.G + pk % a.G) * DK, DK * 2, bar(sh->ifull[k & 1]));
+        if (lane == 0) mbar_arrive(bar(sh->ifull[k % kItems]));
         ++k;
         if (!whole && s0 == 0) {  // the item's other parts: as many shares as begin before its end
           int64_t i = blockIdx.x + 1;
@@ -310,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         }
         if (xl > 0) {
           // Pages: 32 entries of the table at a time, the next ones loaded ahead.
-          const int npp = kStage >> a.c.ps_log2, ends = (xl + a.c.ps - 1) >> a.c.ps_log2;
+          const int ends = (xl + PS - 1) / PS;
           const int32_t* row = a.c.table + (int64_t)(base + x) * a.c.cols;
           int first = s0 * npp;   // of `cur`
           auto entry = [&](int i) { return i < ends ? row[i] : -1; };
@@ -343,17 +407,14 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         left -= cnt;
       }
     }
-    if (ok && k >= 2) ok = wait_bar_warp(bar(sh->ifree[k & 1]), ((k >> 1) - 1) & 1, wc);
+    if (ok && k >= kItems) ok = wait_bar_warp(bar(sh->ifree[k % kItems]), (k / kItems - 1) & 1, wc);
     if (lane == 0) {
       if (ok) {
-        sh->item[k & 1].packed = 0;
-        mbar_arrive(bar(sh->ifull[k & 1]));
+        sh->item[k % kItems].packed = 0;
+        mbar_arrive(bar(sh->ifull[k % kItems]));
       }
       if (a.join) a.join[blockIdx.x] = join;
       for (int i = max(0, n - NS); i < n; ++i) drain_bar(bar(sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
-      // (An abort may leave queries in flight.  Otherwise they have been waited for, and the last item's
-      // arrival may be a later phase of the same barrier.)
-      for (int i = max(0, k - 2); i < k && !ok; ++i) drain_bar(bar(sh->ifull[i & 1]), (i >> 1) & 1, a.wait_ns);
     }
   } else {
     // ------------------------------------------------------------ products and softmax
@@ -366,84 +427,41 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
     const uint32_t sel_a = i & 1 ? 0x3244 : 0x1044, sel_b = i & 1 ? 0x1044 : 0x3244;   // its bf16 scale as fp32
     // Row of V that this lane names for ldmatrix: matrix lane / 8 is rows 0.. or 8.. and half a group's codes.
     const int vr = lane & 7, vrow = 2 * sigma(vr) + ((vr ^ lane >> 3) & 1);
-    const int ps = a.c.ps, p0 = 32 * (warp & 3), p1 = p0 + 16;      // the warp's positions in a stage: two tiles
-    uint32_t blk[2] = {(p0 >> a.c.ps_log2) * a.c.block, (p1 >> a.c.ps_log2) * a.c.block};
-    const int o[2] = {p0 & (ps - 1), p1 & (ps - 1)};
-    const uint32_t pages = 1u << (p0 >> a.c.ps_log2) | 1u << (p1 >> a.c.ps_log2);
-    uint32_t k_at[2], s_at[2], v_at[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      k_at[t] = smem_u32(smem) + blk[t] + (o[t] + ta) * 32 + 8 * j;
-      s_at[t] = smem_u32(smem) + blk[t] + ps * ((DK + DV) / 2) + (o[t] + pair) * 2;
-      v_at[t] = smem_u32(smem) + blk[t] + ps * (DK / 2) + (o[t] + vrow) * 32 + (lane >> 4) * 16;
-    }
+    // The warp's 32 positions of a stage: two tiles, in one page or two.
+    constexpr uint32_t kTileCodes = PS == 16 ? kPage : 512, kTileScales = PS == 16 ? kPage : 32;
+    const int p0 = 32 * (warp & 3);
+    const uint32_t pages = (PS == 16 ? 3u : 1u) << (p0 / PS);
+    const uint32_t blk = smem_u32(smem) + p0 / PS * kPage, o = p0 % PS;
+    const uint32_t k_at = blk + (o + ta) * 32 + 8 * j;
+    const uint32_t s_at = blk + PS * ((DK + DV) / 2) + (o + pair) * 2;
+    const uint32_t v_at = blk + PS * (DK / 2) + (o + vrow) * 32 + (lane >> 4) * 16;
     const uint32_t tab = (tb - ta) * 32;
     int n0 = 0;                  // stages of earlier items
     for (int k = 0;; ++k) {
-      bool ok = wait_bar_warp(bar(sh->ifull[k & 1]), (k >> 1) & 1, wc);
+      bool ok = wait_bar_warp(bar(sh->ifull[k % kItems]), (k / kItems) & 1, wc);
       struct {
         int row0, packed, first, h, len, stage, stages, slot;
       } it;
       it.packed = 0;
-      const Item& si = sh->item[k & 1];
+      const Item& si = sh->item[k % kItems];
       if (ok) it = {si.row0, si.packed, si.first, si.h, si.len, si.stage, si.stages, si.slot};
       const bool last = it.packed == 0;
-      uint32_t qf[GK][NB][4][2];
       float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], sp[GV][NB][4], oo[GV][NB][4][4], vinv = 1.f;
       int see[NB][2];
+      const uint32_t qf = smem_u32(qs) + k % kItems * kQBytes + lane * 8;
       if (!last) {
-        // The queries, scaled to fp16's upper range by a power of two for each row.
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int pk = it.first + nb * kBlock + i;
-          const bool valid = pk < it.packed;
-          const unsigned char* q = qs + (k & 1) * kQBytes + (nb * kBlock + i) * DK * 2 + 32 * j;
-          uint4 w[GK][2];
-#pragma unroll
-          for (int g = 0; g < GK; ++g)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              w[g][x] = valid ? *reinterpret_cast<const uint4*>(q + 128 * g + 16 * x) : make_uint4(0, 0, 0, 0);
-          auto value = [&](int g, int c) {   // column 64 g + 16 j + c
-            const uint4 v = w[g][c >> 3];
-            const uint32_t y = (c & 7) < 2 ? v.x : (c & 7) < 4 ? v.y : (c & 7) < 6 ? v.z : v.w;
-            return to_float<F16>((uint16_t)(c & 1 ? y >> 16 : y));
-          };
-          uint32_t top = 0;
-#pragma unroll
-          for (int g = 0; g < GK; ++g)
-#pragma unroll
-            for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(value(g, c)) & 0x7f800000u);
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^(14 - exponent of the row's largest)
-          const float up = top ? __uint_as_float(min((268u << 23) - top, 254u << 23)) : 1.f;
-#pragma unroll
-          for (int g = 0; g < GK; ++g) {
-            float sum = 0.f;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int c = 8 * (y >> 1) + 2 * (y & 1);
-              const __half2 lo = __floats2half2_rn(value(g, c) * up, value(g, c + 4) * up);
-              const __half2 hi = __floats2half2_rn(value(g, c + 1) * (up * 0.0625f), value(g, c + 5) * (up * 0.0625f));
-              qf[g][nb][y][0] = *reinterpret_cast<const uint32_t*>(&lo);
-              qf[g][nb][y][1] = *reinterpret_cast<const uint32_t*>(&hi);
-              const float2 fl = __half22float2(lo), fh = __half22float2(hi);
-              sum += fl.x + fl.y + 16.f * (fh.x + fh.y);
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) qc[g][nb][x] = -0x1p-21f * __shfl_sync(0xffffffffu, sum, 4 * (2 * j + x));
-          }
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            factor[nb][x] = a.c2 * (0x1p24f / __shfl_sync(0xffffffffu, up, 4 * (2 * j + x)));
-            see[nb][x] = si.see[nb * kBlock + 2 * j + x];
+            const int r = nb * kBlock + 2 * j + x;
+            see[nb][x] = si.see[r];
+            factor[nb][x] = si.factor[r];
+#pragma unroll
+            for (int g = 0; g < GK; ++g) qc[g][nb][x] = si.less[g][r];
             mm[nb][x] = 0.f;
             l[nb][x] = 0.f;
           }
-        }
 #pragma unroll
         for (int g = 0; g < GV; ++g)
 #pragma unroll
@@ -458,8 +476,6 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) least = min(least, min(see[nb][0], see[nb][1]));
         least = __reduce_min_sync(0xffffffffu, least);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh->ifree[k & 1]));   // (the item and its queries are read)
         bool first = true;         // no positions so far
         // Every other stage is this warp's.
         int pos = it.stage * kStage + p0 + ((n0 ^ (warp >> 2)) & 1) * kStage;   // the warp's first position
@@ -471,49 +487,56 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
             const uint32_t ring = s * kBytes;
             float e[2][NB][4], vs[2][GV][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              float acc[GK][NB][4];
-              const uint32_t ka = ring + k_at[t], sa = ring + s_at[t];
+            for (int g = 0; g < GK; ++g) {
+              float acc[2][NB][4];
+              uint32_t x[2][2], y[2][2];
 #pragma unroll
-              for (int g = 0; g < GK; ++g) {
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                  acc[g][nb][0] = acc[g][nb][2] = qc[g][nb][0];
-                  acc[g][nb][1] = acc[g][nb][3] = qc[g][nb][1];
-                }
-                const uint32_t at = ka + g * ps * 32;
-                uint32_t x[2], y[2];
-                lds2(at, x[0], x[1]);
-                lds2(at + tab, y[0], y[1]);
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    const uint32_t a0 = x[w] >> (8 * z) & 0x000f000fu, a2 = x[w] >> (8 * z) & 0x00f000f0u;
-                    const uint32_t a1 = y[w] >> (8 * z) & 0x000f000fu, a3 = y[w] >> (8 * z) & 0x00f000f0u;
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                      mma_f16(acc[g][nb], a0, a1, a2, a3, qf[g][nb][2 * w + z][0], qf[g][nb][2 * w + z][1]);
-                  }
+              for (int t = 0; t < 2; ++t) {
+                const uint32_t at = ring + k_at + t * kTileCodes + g * PS * 32;
+                lds2(at, x[t][0], x[t][1]);
+                lds2(at + tab, y[t][0], y[t][1]);
               }
-              // Logits in base 2, less m: columns 2 j, 2 j + 1 of positions ta and tb.
 #pragma unroll
-              for (int g = 0; g < GK; ++g) {
-                const uint32_t w = lds1(sa + g * ps * 2);
+              for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  uint32_t b[NB][2];
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb) lds2(qf + ((g * NB + nb) * 4 + 2 * w + z) * 256, b[nb][0], b[nb][1]);
+#pragma unroll
+                  for (int t = 0; t < 2; ++t) {
+                    const uint32_t a0 = x[t][w] >> (8 * z) & 0x000f000fu, a2 = x[t][w] >> (8 * z) & 0x00f000f0u;
+                    const uint32_t a1 = y[t][w] >> (8 * z) & 0x000f000fu, a3 = y[t][w] >> (8 * z) & 0x00f000f0u;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                      if (w + z == 0)
+                        mma_f16(acc[t][nb], a0, a1, a2, a3, b[nb][0], b[nb][1], qc[g][nb][0], qc[g][nb][1]);
+                      else
+                        mma_f16(acc[t][nb], a0, a1, a2, a3, b[nb][0], b[nb][1]);
+                    }
+                  }
+                }
+              // Logits in base 2: columns 2 j, 2 j + 1 of positions ta and tb.
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const uint32_t w = lds1(ring + s_at + t * kTileScales + g * PS * 2);
                 const float k0 = __uint_as_float(__byte_perm(w, 0, sel_a)), k1 = __uint_as_float(__byte_perm(w, 0, sel_b));
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    e[t][nb][x] = g == 0 ? (x < 2 ? k0 : k1) * acc[g][nb][x] : fmaf(x < 2 ? k0 : k1, acc[g][nb][x], e[t][nb][x]);
+                  for (int z = 0; z < 4; ++z)
+                    e[t][nb][z] = g == 0 ? (z < 2 ? k0 : k1) * acc[t][nb][z] : fmaf(z < 2 ? k0 : k1, acc[t][nb][z], e[t][nb][z]);
               }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) e[t][nb][x] = fmaf(e[t][nb][x], factor[nb][x & 1], -mm[nb][x & 1]);
 #pragma unroll
               for (int g = 0; g < GV; ++g) {
-                const uint32_t w = lds1(sa + (GK + g) * ps * 2);
+                const uint32_t w = lds1(ring + s_at + t * kTileScales + (GK + g) * PS * 2);
                 vs[t][g][0] = __uint_as_float(__byte_perm(w, 0, sel_a)) * vinv;
                 vs[t][g][1] = __uint_as_float(__byte_perm(w, 0, sel_b)) * vinv;
               }
@@ -524,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
               for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const int at = have >> ((t ? p1 : p0) >> a.c.ps_log2) & 1u ? pos + 16 * t + (x ? tb : ta) : INT_MAX;
+                  const int at = have >> ((p0 + 16 * t) / PS) & 1u ? pos + 16 * t + (x ? tb : ta) : INT_MAX;
 #pragma unroll
                   for (int g = 0; g < GV; ++g)
                     if (at >= it.len) vs[t][g][x] = 0.f;   // (what lies there may be anything)
@@ -600,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
               for (int g = 0; g < GV; ++g) {
                 uint32_t b0[NB], b1[NB], v[4];
-                ldsm_x4_t(ring + v_at[t] + g * ps * 32, v[0], v[1], v[2], v[3]);
+                ldsm_x4_t(ring + v_at + t * kTileCodes + g * PS * 32, v[0], v[1], v[2], v[3]);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                   b0[nb] = transposed(half2_bits(e[t][nb][0] * vs[t][g][0], e[t][nb][1] * vs[t][g][0]));
@@ -624,6 +647,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           if (lane == 0) mbar_arrive(bar(sh->empty[s]));
         }
         n0 += it.stages;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->ifree[k % kItems]));   // (the item and its queries are read)
         // The warps' sums are joined.
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -719,8 +744,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           if (it.slot < 0) {
             const int64_t rh = (int64_t)(it.row0 + pk / a.G) * a.H_q + it.h * a.G + pk % a.G;
             const float inv = any ? 1.f / sum : 0.f;
+            auto pack = [&](float x, float y) { return a.f16 ? pack16<true>(x, y) : pack16<false>(x, y); };
             *reinterpret_cast<uint2*>(a.out + rh * DV + 4 * lane) =
-                any ? make_uint2(pack16<F16>(v.x * inv, v.y * inv), pack16<F16>(v.z * inv, v.w * inv)) : make_uint2(0, 0);
+                any ? make_uint2(pack(v.x * inv, v.y * inv), pack(v.z * inv, v.w * inv)) : make_uint2(0, 0);
             if (a.lse && lane == 0) a.lse[rh] = any ? (m + log2f(sum)) * 0.693147180559945309f : -INFINITY;
           } else {
             const int64_t at = (int64_t)it.slot * ROWS + nb * kBlock + warp;
@@ -829,23 +855,33 @@ __global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_
   if (a.lse && lane == 0) a.lse[rh] = any ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
 }
 
-template <int DK, int DV, int NB, bool F16>
+template <int DK, int DV, int NB, int PS>
 cudaError_t launch_one(const Args& a, int grid, cudaStream_t st) {
   constexpr size_t smem = smem_bytes<DK, DV, NB>();
   static_assert(smem <= 232448 && ring_stages<DK, DV, NB>() >= 2, "shared memory of one CTA");
-  auto kernel = kv4_attn_kernel<DK, DV, NB, F16>;
+  auto kernel = kv4_attn_kernel<DK, DV, NB, PS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, st, a);
   if (e != cudaSuccess || !a.join) return e;
-  return launch_pdl(kv4_join_kernel<DV, F16>, dim3((unsigned)(grid * NB * kBlock / kJoinRows)), dim3(128 * kJoinRows), 0, st, a,
-                    NB * kBlock, grid);
+  const dim3 joins((unsigned)(grid * NB * kBlock / kJoinRows)), threads(128 * kJoinRows);
+  return a.f16 ? launch_pdl(kv4_join_kernel<DV, true>, joins, threads, 0, st, a, NB * kBlock, grid)
+               : launch_pdl(kv4_join_kernel<DV, false>, joins, threads, 0, st, a, NB * kBlock, grid);
+}
+
+template <int DK, int DV, int NB>
+cudaError_t launch_page(const Args& a, int grid, cudaStream_t st) {
+  switch (a.c.ps) {
+    case 16: return launch_one<DK, DV, NB, 16>(a, grid, st);
+    case 32: return launch_one<DK, DV, NB, 32>(a, grid, st);
+    case 64: return launch_one<DK, DV, NB, 64>(a, grid, st);
+    default: return launch_one<DK, DV, NB, 128>(a, grid, st);
+  }
 }
 
 template <int DK, int DV>
-cudaError_t launch_width(const Args& a, int rows, bool f16, int grid, cudaStream_t st) {
-  if (rows == kBlock) return f16 ? launch_one<DK, DV, 1, true>(a, grid, st) : launch_one<DK, DV, 1, false>(a, grid, st);
-  return f16 ? launch_one<DK, DV, 2, true>(a, grid, st) : launch_one<DK, DV, 2, false>(a, grid, st);
+cudaError_t launch_width(const Args& a, int rows, int grid, cudaStream_t st) {
+  return rows == kBlock ? launch_page<DK, DV, 1>(a, grid, st) : launch_page<DK, DV, 2>(a, grid, st);
 }
 
 }  // namespace
@@ -890,10 +926,10 @@ cudaError_t launch_kv4_attn(const dsa_kv4_cache& c, const CacheArgs& ca, const d
   a.test_no_load = hooks ? hooks->tile_no_load : 0;
   a.R = p.R; a.H_q = p.H_q; a.G = p.H_q / c.H_kv; a.L_max = p.L_max;
   a.c2 = (float)(p.softmax_scale * 1.4426950408889634);
-  const bool f16 = p.flags & DSA_FLAG_FP16;
-  if (c.D_k == 64) return launch_width<64, 64>(a, s.rows, f16, s.grid, st);
-  if (c.D_k == 128) return launch_width<128, 128>(a, s.rows, f16, s.grid, st);
-  return launch_width<192, 128>(a, s.rows, f16, s.grid, st);
+  a.f16 = (p.flags & DSA_FLAG_FP16) != 0;
+  if (c.D_k == 64) return launch_width<64, 64>(a, s.rows, s.grid, st);
+  if (c.D_k == 128) return launch_width<128, 128>(a, s.rows, s.grid, st);
+  return launch_width<192, 128>(a, s.rows, s.grid, st);
 }
 
 }  // namespace dsa
