@@ -174,6 +174,11 @@ __device__ __forceinline__ void request_info(const Args& a, int b, int reach, in
   }
 }
 
+// x / y of what hardly ever passes 32 bits, x >= 0, y > 0.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return x < (int64_t(1) << 32) && y < (int64_t(1) << 32) ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 __device__ __forceinline__ int blocks_of(const Args& a, int n, int rows) { return (n * a.G + rows - 1) / rows; }
 __device__ __forceinline__ int stages_of(int len) { return max((len + kStage - 1) / kStage, 1); }
 
@@ -221,45 +226,65 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
     sh->bits = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncthreads();
   pdl_wait();      // (the inputs may only just be written; the status block is cleared)
   pdl_trigger();
-  // Units (an item's stages, at least one) of all requests: each warp adds up those of a run.
+  // Units (an item's stages, at least one) of all requests: each warp adds up those of a run.  Up to
+  // 32 requests are the loading warp's lanes.
   const int per = (a.c.B + kWarps) / (kWarps + 1);
-  int64_t mine = 0;
+  const bool few = a.c.B <= 32;
   bool bad = false;
-  for (int base = 0; base < per; base += 32) {
-    int r0, n, len;
-    request_info(a, base + lane < per ? warp * per + base + lane : -1, reach, lane, r0, n, len, bad);
-    mine += (int64_t)blocks_of(a, n, ROWS) * a.c.H_kv * stages_of(len);
-  }
+  auto units_of = [&](int n, int len) { return (int64_t)blocks_of(a, n, ROWS) * a.c.H_kv * stages_of(len); };
+  if (!few) {
+    int64_t mine = 0;
+    for (int base = 0; base < per; base += 32) {
+      int r0, n, len;
+      request_info(a, base + lane < per ? warp * per + base + lane : -1, reach, lane, r0, n, len, bad);
+      mine += units_of(n, len);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh->units[warp] = mine;
-  __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sh->units[warp] = mine;
+    __syncthreads();
+  }
   uint32_t* const status = a.bits ? &sh->bits : a.status;
-  if (__any_sync(0xffffffffu, bad) && blockIdx.x == 0 && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
+  auto raise_bad = [&]() {
+    if (__any_sync(0xffffffffu, bad) && blockIdx.x == 0 && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
+  };
+  if (!few) raise_bad();
   const WaitCtx wc(&sh->abort, status, a.wait_ns);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
+    int base = 0, x = 0, r0 = 0, rows = 0, len = 0;    // 32 requests from `base` on, of which x is the next piece's
     int64_t total = 0;
-    for (int w = 0; w <= kWarps; ++w) total += sh->units[w];
+    if (few) {
+      request_info(a, lane, reach, lane, r0, rows, len, bad);
+      raise_bad();
+      total = units_of(rows, len);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    } else {
+      for (int w = 0; w <= kWarps; ++w) total += sh->units[w];
+    }
     // (at least two stages to a share: the two halves of the warps take one each)
     const int64_t shares = min((total + 1) / 2, (int64_t)gridDim.x);
-    const int64_t lo = blockIdx.x < shares ? total * blockIdx.x / shares : 0;
-    int64_t left = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares - lo : 0;
+    const int64_t lo = blockIdx.x < shares ? quotient(total * blockIdx.x, shares) : 0;
+    int64_t left = blockIdx.x < shares ? quotient(total * (blockIdx.x + 1), shares) - lo : 0;
     int n = 0, k = 0;             // stages and items handed over
     bool ok = true;
     Kv4Join join = {};
     if (left > 0) {
       // The request where the share begins: its warp's run, then 32 at a time.
       int64_t u = lo;             // units from here to the share's beginning
-      int w = 0;
-      while (u >= sh->units[w]) u -= sh->units[w++];
-      int base = w * per, x = 0, r0, rows, len;
-      for (;; base += 32) {
+      if (!few) {
+        int w = 0;
+        while (u >= sh->units[w]) u -= sh->units[w++];
+        base = w * per;
         request_info(a, base + lane, reach, lane, r0, rows, len, bad);
-        const int64_t units = (int64_t)blocks_of(a, rows, ROWS) * a.c.H_kv * stages_of(len);
+      }
+      for (;;) {
+        const int64_t units = units_of(rows, len);
         int64_t incl = units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -273,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           break;
         }
         u -= __shfl_sync(0xffffffffu, incl, 31);
+        base += 32;
+        request_info(a, base + lane, reach, lane, r0, rows, len, bad);
       }
       int64_t at = lo;            // units before the next piece
       while (left > 0 && ok) {
@@ -284,74 +311,104 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         const int xr = __shfl_sync(0xffffffffu, r0, x), xn = __shfl_sync(0xffffffffu, rows, x);
         const int xl = __shfl_sync(0xffffffffu, len, x);
         const int st = stages_of(xl);
-        const int64_t units = (int64_t)blocks_of(a, xn, ROWS) * a.c.H_kv * st;
-        if (u >= units) {         // (the request is through, or has no rows)
+        if (u >= units_of(xn, xl)) {   // (the request is through, or has no rows)
           u = 0;
           ++x;
           continue;
         }
-        const int64_t idx = u / st;
-        const int s0 = (int)(u - idx * st), rb = (int)(idx / a.c.H_kv), h = (int)(idx - (int64_t)rb * a.c.H_kv);
-        const int cnt = (int)min((int64_t)(st - s0), left);
+        const int64_t idx = quotient(u, st);
+        const int s0 = (int)(u - idx * st), rb = (int)idx / a.c.H_kv, h = (int)idx - rb * a.c.H_kv;   // (below 2^23: 65535 rows of 128 heads)
+        const int cnt = (int)min((int64_t)(st - s0), left), load = xl > 0 ? cnt : 0;
         const bool whole = cnt == st;
+        // What the piece reads first, asked for together.  Pages: 32 entries of the table at a time, the
+        // next ones ahead.
+        const int ends = (xl + PS - 1) / PS;
+        const int32_t* table = a.c.table + (int64_t)(base + x) * a.c.cols;
+        auto entry = [&](int i) { return i < ends ? table[i] : -1; };
+        int first = s0 * npp;     // of `cur`
+        int cur = entry(first + lane), nxt = entry(first + 32 + lane);
+        const int row = rb * ROWS + lane;
+        const bool live = lane < ROWS && row < xn * a.G;
+        const int sees = live ? a.row_len[xr + row / a.G] : 0;
+        const int i = lane >> 2, j = lane & 3;
+        uint4 w[NB][GK][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int pk = rb * ROWS + nb * kBlock + i;
+          const bool valid = pk < xn * a.G;
+          const uint16_t* q = a.q + (int64_t)(xr + (valid ? pk / a.G : 0)) * a.q_stride +
+                              (int64_t)(h * a.G + (valid ? pk % a.G : 0)) * DK + 16 * j;
+#pragma unroll
+          for (int g = 0; g < GK; ++g)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              w[nb][g][y] = valid ? *reinterpret_cast<const uint4*>(q + 64 * g + 8 * y) : make_uint4(0, 0, 0, 0);
+        }
+        // Stage z of the piece on its way.
+        auto issue = [&](int z) {
+          const int pg = (s0 + z) * npp;
+          if (pg - first == 32) {
+            first = pg;
+            cur = nxt;
+            nxt = entry(first + 32 + lane);
+          }
+          const int id = __shfl_sync(0xffffffffu, cur, (pg - first + lane) & 31);
+          const bool need = lane < npp && pg + lane < ends, have = need && id >= 0 && id < a.c.n_pages;
+          if (__any_sync(0xffffffffu, need && !have) && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
+          const uint32_t mask = __ballot_sync(0xffffffffu, have);
+          const int s = n % NS;
+          if (n >= NS && !wait_bar_warp(bar(sh->empty[s]), (n / NS - 1) & 1, wc)) return false;
+          if (lane == 0) {
+            sh->pages[s] = mask;
+            mbar_expect_tx(bar(sh->full[s]), __popc(mask) * kPage);
+          }
+          __syncwarp();
+          if (have && !(a.test_no_load && n == 0))
+            bulk_row(smem_u32(smem) + s * kBytes + lane * kPage, a.c.pages + ((int64_t)id * a.c.H_kv + h) * kPage, kPage,
+                     bar(sh->full[s]));
+          ++n;
+          return true;
+        };
+        if (load > 0 && !(ok = issue(0))) break;
         if (k >= kItems && !(ok = wait_bar_warp(bar(sh->ifree[k % kItems]), (k / kItems - 1) & 1, wc))) break;
         // The item, with its rows' queries as the products take them: scaled to fp16's upper range by a power
         // of two for each row, in the layout of the fragments (lane 4 i + j: row i, columns 16 j ..).
         Item* it = &sh->item[k % kItems];
-        const int row = rb * ROWS + lane;
-        const bool live = lane < ROWS && row < xn * a.G;
-        const int sees = live ? a.row_len[xr + row / a.G] : 0;
-        {
-          const int i = lane >> 2, j = lane & 3;
-          uint4 w[NB][GK][2];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const int pk = rb * ROWS + nb * kBlock + i;
-            const bool valid = pk < xn * a.G;
-            const uint16_t* q = a.q + (int64_t)(xr + (valid ? pk / a.G : 0)) * a.q_stride +
-                                (int64_t)(h * a.G + (valid ? pk % a.G : 0)) * DK + 16 * j;
+        for (int nb = 0; nb < NB; ++nb) {
+          auto value = [&](int g, int c) {   // column 64 g + 16 j + c
+            const uint4 v = w[nb][g][c >> 3];
+            const uint32_t y = (c & 7) < 2 ? v.x : (c & 7) < 4 ? v.y : (c & 7) < 6 ? v.z : v.w;
+            const uint16_t z = (uint16_t)(c & 1 ? y >> 16 : y);
+            return a.f16 ? to_float<true>(z) : to_float<false>(z);
+          };
+          uint32_t top = 0;
 #pragma unroll
-            for (int g = 0; g < GK; ++g)
+          for (int g = 0; g < GK; ++g)
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
-                w[nb][g][x] = valid ? *reinterpret_cast<const uint4*>(q + 64 * g + 8 * x) : make_uint4(0, 0, 0, 0);
-          }
+            for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(value(g, c)) & 0x7f800000u);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^(14 - exponent of the row's largest)
+          const float up = top ? __uint_as_float(min((268u << 23) - top, 254u << 23)) : 1.f;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            auto value = [&](int g, int c) {   // column 64 g + 16 j + c
-              const uint4 v = w[nb][g][c >> 3];
-              const uint32_t y = (c & 7) < 2 ? v.x : (c & 7) < 4 ? v.y : (c & 7) < 6 ? v.z : v.w;
-              const uint16_t z = (uint16_t)(c & 1 ? y >> 16 : y);
-              return a.f16 ? to_float<true>(z) : to_float<false>(z);
-            };
-            uint32_t top = 0;
+          for (int g = 0; g < GK; ++g) {
+            float sum = 0.f;
 #pragma unroll
-            for (int g = 0; g < GK; ++g)
-#pragma unroll
-              for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(value(g, c)) & 0x7f800000u);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^(14 - exponent of the row's largest)
-            const float up = top ? __uint_as_float(min((268u << 23) - top, 254u << 23)) : 1.f;
-#pragma unroll
-            for (int g = 0; g < GK; ++g) {
-              float sum = 0.f;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int c = 8 * (y >> 1) + 2 * (y & 1);
-                const __half2 lo = __floats2half2_rn(value(g, c) * up, value(g, c + 4) * up);
-                const __half2 hi = __floats2half2_rn(value(g, c + 1) * (up * 0.0625f), value(g, c + 5) * (up * 0.0625f));
-                reinterpret_cast<uint2*>(qs + k % kItems * kQBytes)[((g * NB + nb) * 4 + y) * 32 + lane] =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                const float2 fl = __half22float2(lo), fh = __half22float2(hi);
-                sum += fl.x + fl.y + 16.f * (fh.x + fh.y);
-              }
-              sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-              sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-              if (j == 0) it->less[g][nb * kBlock + i] = -0x1p-21f * sum;
+            for (int y = 0; y < 4; ++y) {
+              const int c = 8 * (y >> 1) + 2 * (y & 1);
+              const __half2 lo = __floats2half2_rn(value(g, c) * up, value(g, c + 4) * up);
+              const __half2 hi = __floats2half2_rn(value(g, c + 1) * (up * 0.0625f), value(g, c + 5) * (up * 0.0625f));
+              reinterpret_cast<uint2*>(qs + k % kItems * kQBytes)[((g * NB + nb) * 4 + y) * 32 + lane] =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+              const float2 fl = __half22float2(lo), fh = __half22float2(hi);
+              sum += fl.x + fl.y + 16.f * (fh.x + fh.y);
             }
-            if (j == 0) it->factor[nb * kBlock + i] = a.c2 * (0x1p24f / up);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (j == 0) it->less[g][nb * kBlock + i] = -0x1p-21f * sum;
           }
+          if (j == 0) it->factor[nb * kBlock + i] = a.c2 * (0x1p24f / up);
         }
         if (lane < ROWS) it->see[lane] = live ? min(max(sees, 0), reach) : xl;
         if (lane == 0) {
@@ -361,47 +418,15 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           it->h = h;
           it->len = xl;
           it->stage = s0;
-          it->stages = xl > 0 ? cnt : 0;
+          it->stages = load;
           it->slot = whole ? -1 : 2 * (int)blockIdx.x + (s0 == 0);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh->ifull[k % kItems]));
         ++k;
-        if (!whole && s0 == 0) {  // the item's other parts: as many shares as begin before its end
-          int64_t i = blockIdx.x + 1;
-          while (total * i / shares < at + st) ++i;
-          join = Kv4Join{xr, xn * a.G, rb * ROWS, h, (int)(i - blockIdx.x), {0, 0, 0}};
-        }
-        if (xl > 0) {
-          // Pages: 32 entries of the table at a time, the next ones loaded ahead.
-          const int ends = (xl + PS - 1) / PS;
-          const int32_t* row = a.c.table + (int64_t)(base + x) * a.c.cols;
-          int first = s0 * npp;   // of `cur`
-          auto entry = [&](int i) { return i < ends ? row[i] : -1; };
-          int cur = entry(first + lane), nxt = entry(first + 32 + lane);
-          for (int j = 0; j < cnt; ++j, ++n) {
-            const int pg = (s0 + j) * npp;
-            if (pg - first == 32) {
-              first = pg;
-              cur = nxt;
-              nxt = entry(first + 32 + lane);
-            }
-            const int id = __shfl_sync(0xffffffffu, cur, (pg - first + lane) & 31);
-            const bool need = lane < npp && pg + lane < ends, have = need && id >= 0 && id < a.c.n_pages;
-            if (__any_sync(0xffffffffu, need && !have) && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
-            const uint32_t mask = __ballot_sync(0xffffffffu, have);
-            const int s = n % NS;
-            if (n >= NS && !(ok = wait_bar_warp(bar(sh->empty[s]), (n / NS - 1) & 1, wc))) break;
-            if (lane == 0) {
-              sh->pages[s] = mask;
-              mbar_expect_tx(bar(sh->full[s]), __popc(mask) * a.c.block);
-            }
-            __syncwarp();
-            if (have && !(a.test_no_load && n == 0))
-              bulk_row(smem_u32(smem) + s * kBytes + lane * a.c.block,
-                       a.c.pages + ((int64_t)id * a.c.H_kv + h) * a.c.block, a.c.block, bar(sh->full[s]));
-          }
-        }
+        for (int z = 1; z < load && ok; ++z) ok = issue(z);
+        if (!whole && s0 == 0)    // the item's other parts: as many shares as begin before its end
+          join = Kv4Join{xr, xn * a.G, rb * ROWS, h, (int)(quotient((at + st) * shares + total - 1, total) - blockIdx.x), {0, 0, 0}};
         u += cnt;
         at += cnt;
         left -= cnt;
@@ -782,14 +807,16 @@ __global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_
     bits = __reduce_or_sync(0xffffffffu, bits);
     if (lane == 0) *a.status = bits;
   }
+  auto slot = [&](int x) { return (x == 0 ? 2 * i + 1 : 2 * (i + x)) * rows + r; };
   const Kv4Join jn = a.join[i];
+  // (asked for beside the item, whether it has that many parts or not)
+  const float2 early = i + w + 4 * lane < ctas ? a.ml[slot(w + 4 * lane)] : make_float2(0.f, 0.f);
   const int pk = jn.first + r;
   if (jn.parts == 0) return;
-  auto slot = [&](int x) { return (x == 0 ? 2 * i + 1 : 2 * (i + x)) * rows + r; };
   float M = -INFINITY, L = 0.f, acc[E] = {};
   if (pk < jn.packed) {
     for (int x = w + 4 * lane; x < jn.parts; x += 128) {
-      const float2 v = a.ml[slot(x)];
+      const float2 v = x < 128 ? early : a.ml[slot(x)];
       if (v.y != 0.f) M = fmaxf(M, v.x);
     }
 #pragma unroll
@@ -798,7 +825,7 @@ __global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_
       const int x = base + 4 * lane;
       float f = 0.f;
       if (x < jn.parts) {
-        const float2 v = a.ml[slot(x)];
+        const float2 v = x < 128 ? early : a.ml[slot(x)];
         f = v.y != 0.f ? ex2(v.x - M) : 0.f;   // (a part that saw nothing counts nothing)
         L = fmaf(f, v.y, L);
       }
