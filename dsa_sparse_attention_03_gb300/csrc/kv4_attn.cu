@@ -325,8 +325,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         const int ends = (xl + PS - 1) / PS;
         const int32_t* table = a.c.table + (int64_t)(base + x) * a.c.cols;
         auto entry = [&](int i) { return i < ends ? table[i] : -1; };
-        int first = s0 * npp;     // of `cur`
-        int cur = entry(first + lane), nxt = entry(first + 32 + lane);
+        int next = entry(s0 * npp + lane);
         const int row = rb * ROWS + lane;
         const bool live = lane < ROWS && row < xn * a.G;
         const int sees = live ? a.row_len[xr + row / a.G] : 0;
@@ -344,18 +343,23 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
             for (int y = 0; y < 2; ++y)
               w[nb][g][y] = valid ? *reinterpret_cast<const uint4*>(q + 64 * g + 8 * y) : make_uint4(0, 0, 0, 0);
         }
-        // Stage z of the piece on its way.
+        // Stage z of the piece on its way.  A lane holds a page of the 32 / npp stages' from `window` on; the
+        // loop over stages has one warp's time beside eight that compute, so it holds little else.
+        constexpr int kWindow = 32 / npp;
+        const uint8_t* src = nullptr;
+        uint32_t have = 0;
         auto issue = [&](int z) {
-          const int pg = (s0 + z) * npp;
-          if (pg - first == 32) {
-            first = pg;
-            cur = nxt;
-            nxt = entry(first + 32 + lane);
+          const int y = z % kWindow;
+          if (y == 0) {
+            const int at = (s0 + z) * npp + lane, id = next;
+            next = entry(at + 32);
+            const bool there = at < ends && id >= 0 && id < a.c.n_pages;
+            have = __ballot_sync(0xffffffffu, there);
+            if (__any_sync(0xffffffffu, at < ends && at < (s0 + load) * npp && !there) && lane == 0)
+              raise_status(status, DSA_DEVICE_BAD_INDEX);
+            src = a.c.pages + ((int64_t)id * a.c.H_kv + h) * kPage;
           }
-          const int id = __shfl_sync(0xffffffffu, cur, (pg - first + lane) & 31);
-          const bool need = lane < npp && pg + lane < ends, have = need && id >= 0 && id < a.c.n_pages;
-          if (__any_sync(0xffffffffu, need && !have) && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
-          const uint32_t mask = __ballot_sync(0xffffffffu, have);
+          const uint32_t mask = have >> (y * npp) & ((1u << npp) - 1u);
           const int s = n % NS;
           if (n >= NS && !wait_bar_warp(bar(sh->empty[s]), (n / NS - 1) & 1, wc)) return false;
           if (lane == 0) {
@@ -363,9 +367,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
             mbar_expect_tx(bar(sh->full[s]), __popc(mask) * kPage);
           }
           __syncwarp();
-          if (have && !(a.test_no_load && n == 0))
-            bulk_row(smem_u32(smem) + s * kBytes + lane * kPage, a.c.pages + ((int64_t)id * a.c.H_kv + h) * kPage, kPage,
-                     bar(sh->full[s]));
+          if (lane / npp == y && (have >> lane & 1u) && !(a.test_no_load && n == 0))
+            bulk_row(smem_u32(smem) + s * kBytes + lane % npp * kPage, src, kPage, bar(sh->full[s]));
           ++n;
           return true;
         };
@@ -566,6 +569,15 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                 vs[t][g][1] = __uint_as_float(__byte_perm(w, 0, sel_b)) * vinv;
               }
             }
+            // V's codes, after which the stage's place is given back: it is loaded again under the rest.
+            uint32_t v[2][GV][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int g = 0; g < GV; ++g)
+                ldsm_x4_t(ring + v_at + t * kTileCodes + g * PS * 32, v[t][g][0], v[t][g][1], v[t][g][2], v[t][g][3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh->empty[s]));
             if (pos + 32 > least || have != pages) {
               // Positions that a row does not see, or whose page the pool does not have.
 #pragma unroll
@@ -647,8 +659,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                 }
 #pragma unroll
               for (int g = 0; g < GV; ++g) {
-                uint32_t b0[NB], b1[NB], v[4];
-                ldsm_x4_t(ring + v_at + t * kTileCodes + g * PS * 32, v[0], v[1], v[2], v[3]);
+                uint32_t b0[NB], b1[NB];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                   b0[nb] = transposed(half2_bits(e[t][nb][0] * vs[t][g][0], e[t][nb][1] * vs[t][g][0]));
@@ -659,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                 for (int w = 0; w < 2; ++w)
 #pragma unroll
                   for (int z = 0; z < 2; ++z) {
-                    const uint32_t x = v[2 * w] >> (8 * z), y = v[2 * w + 1] >> (8 * z);
+                    const uint32_t x = v[t][g][2 * w] >> (8 * z), y = v[t][g][2 * w + 1] >> (8 * z);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
                       mma_f16(oo[g][nb][2 * w + z], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, b0[nb],
@@ -667,9 +678,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                   }
               }
             }
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh->empty[s]));
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(sh->empty[s]));
         }
         n0 += it.stages;
         __syncwarp();
