@@ -50,6 +50,10 @@ constexpr int kWarps = 8;        // that compute; one more loads
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kBlock = 8;        // packed rows of a product's column block
 constexpr int kItems = 3;        // handed over at once
+// An item's start and the joining of its warps' sums take a CTA about as long as four stages, and its
+// share of the work counts them (32 ragged tokens: 101 us with shares of stages alone, 90 with a cost of two
+// stages, 88 with three, 87 with four, 89 with six; width 64: 67, 60, 54, 52, 52).
+constexpr int kItemCost = 4;
 
 struct Args {
   CacheArgs c;
@@ -229,12 +233,12 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   __syncthreads();
   pdl_wait();      // (the inputs may only just be written; the status block is cleared)
   pdl_trigger();
-  // Units (an item's stages, at least one) of all requests: each warp adds up those of a run.  Up to
+  // Units (an item's cost, then its stages, at least one) of all requests: each warp adds up those of a run.  Up to
   // 32 requests are the loading warp's lanes.
   const int per = (a.c.B + kWarps) / (kWarps + 1);
   const bool few = a.c.B <= 32;
   bool bad = false;
-  auto units_of = [&](int n, int len) { return (int64_t)blocks_of(a, n, ROWS) * a.c.H_kv * stages_of(len); };
+  auto units_of = [&](int n, int len) { return (int64_t)blocks_of(a, n, ROWS) * a.c.H_kv * (kItemCost + stages_of(len)); };
   if (!few) {
     int64_t mine = 0;
     for (int base = 0; base < per; base += 32) {
@@ -316,9 +320,16 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           ++x;
           continue;
         }
-        const int64_t idx = quotient(u, st);
-        const int s0 = (int)(u - idx * st), rb = (int)idx / a.c.H_kv, h = (int)idx - rb * a.c.H_kv;   // (below 2^23: 65535 rows of 128 heads)
-        const int cnt = (int)min((int64_t)(st - s0), left), load = xl > 0 ? cnt : 0;
+        const int64_t idx = quotient(u, st + kItemCost);
+        const int u0 = (int)(u - idx * (st + kItemCost)), rb = (int)idx / a.c.H_kv, h = (int)idx - rb * a.c.H_kv;   // (below 2^23: 65535 rows of 128 heads)
+        const int take = (int)min((int64_t)(st + kItemCost - u0), left);
+        const int s0 = max(u0 - kItemCost, 0), cnt = u0 + take - kItemCost - s0;   // its stages
+        const int64_t end = at - u0 + st + kItemCost;                              // the item's last unit and one
+        u += take;
+        at += take;
+        left -= take;
+        if (cnt <= 0) continue;   // (nothing but the item's cost)
+        const int load = xl > 0 ? cnt : 0;
         const bool whole = cnt == st;
         // What the piece reads first, asked for together.  Pages: 32 entries of the table at a time, the
         // next ones ahead.
@@ -429,10 +440,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         ++k;
         for (int z = 1; z < load && ok; ++z) ok = issue(z);
         if (!whole && s0 == 0)    // the item's other parts: as many shares as begin before its end
-          join = Kv4Join{xr, xn * a.G, rb * ROWS, h, (int)(quotient((at + st) * shares + total - 1, total) - blockIdx.x), {0, 0, 0}};
-        u += cnt;
-        at += cnt;
-        left -= cnt;
+          join = Kv4Join{xr, xn * a.G, rb * ROWS, h, (int)(quotient(end * shares + total - 1, total) - blockIdx.x), {0, 0, 0}};
       }
     }
     if (ok && k >= kItems) ok = wait_bar_warp(bar(sh->ifree[k % kItems]), (k / kItems - 1) & 1, wc);
@@ -700,31 +708,27 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           }
       }
       if (consumers_any(!ok || last)) break;
-      auto joined = [&](int r, float& m, float& sum) {
-        m = -INFINITY;
-        sum = 0.f;
-        bool any = false;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          if (sh->l[w][r] != 0.f) {
-            m = fmaxf(m, sh->m[w][r]);
-            any = true;
-          }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          if (sh->l[w][r] != 0.f) sum = fmaf(ex2(sh->m[w][r] - m), sh->l[w][r], sum);
-        return any;
-      };
       const float back = 1.f / vinv;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float m, sum, f[2];
+        // The common maximum and sum of row lane % 8, over the warps lane / 8 and 4 + lane / 8.
+        const int r = nb * kBlock + (lane & 7), wa = lane >> 3, wb = wa + 4;
+        const float la = sh->l[wa][r], lb = sh->l[wb][r], ma = la != 0.f ? sh->m[wa][r] : -INFINITY,
+                    mb = lb != 0.f ? sh->m[wb][r] : -INFINITY;
+        float most = fmaxf(ma, mb);
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+        float all = (la != 0.f ? ex2(ma - most) * la : 0.f) + (lb != 0.f ? ex2(mb - most) * lb : 0.f);
+        all += __shfl_xor_sync(0xffffffffu, all, 8);
+        all += __shfl_xor_sync(0xffffffffu, all, 16);
+        float f[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          joined(nb * kBlock + 2 * j + x, m, sum);
-          f[x] = l[nb][x] != 0.f ? ex2(mm[nb][x] - m) * back : 0.f;
+          const float to = __shfl_sync(0xffffffffu, most, 2 * j + x);
+          f[x] = l[nb][x] != 0.f ? ex2(mm[nb][x] - to) * back : 0.f;
         }
-        const bool any = joined(nb * kBlock + warp, m, sum);   // the row that this warp writes
+        const float m = __shfl_sync(0xffffffffu, most, warp), sum = __shfl_sync(0xffffffffu, all, warp);   // the row that this warp writes
+        const bool any = sum != 0.f;
         // Columns 64 g + 32 w + 4 i .. of rows 2 j and 2 j + 1, in the common scale.
         float4 v[GV][2][2];
 #pragma unroll
