@@ -770,24 +770,23 @@ class QKProblem(Problem):
         fixed = [(n, d, s) for n, d, s in (("q_weight", dtype, (c.D_k,)), ("k_weight", dtype, (c.D_k,)),
                                            ("inv_freq", torch.float64, (c.rot // 2,))) if getattr(c, n) is not None]
         _check_fits(self, heads, dict(positions=c.R, row_offsets=c.B + 1), fixed)
-        self._expect = (ctypes.byref(c), dtype)
+        self._expect = (ctypes.byref(c), dtype, {"q": (c.q, (c.R, c.H_q, c.D_k)), "k": (c.k, (c.R, c.H_kv, c.D_k))})
 
     def _output(self, name, t, dev):
         """Checks an output: packed, or the input itself."""
-        c = self.c
-        ptr = getattr(c, name)
+        ptr, shape = self._expect[2][name]
         if ptr is None:
             return None
-        shape = (c.R, c.H_q if name == "q" else c.H_kv, c.D_k)
         if t is None:
             raise ValueError(f"{name}_out must be given where {name} is")
-        if t.data_ptr() == ptr and c.R > 0:
+        at = t.data_ptr()
+        if at == ptr and shape[0] > 0:
             x = self._keep[name]
             if t.shape != x.shape or t.stride() != x.stride() or t.dtype != x.dtype:
                 raise ValueError(f"{name}_out begins where {name} does, but is not the same tensor")
         else:
             _check_outputs(dev, ((name + "_out", t, shape, self._expect[1]),), None)
-        return t.data_ptr()
+        return at
 
 
 def dsa_qk_norm_rope(prob: QKProblem, q_out, k_out, stream=None) -> None:
@@ -846,7 +845,7 @@ class KV4Cache(Problem):
             t = keep[name]
             if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-        self._expect = (ctypes.byref(c),)
+        self._expect = (ctypes.byref(c), c.B + 1, c.H_kv, c.D_k, c.D_v)
 
 
 def _check_cache(cache):
@@ -874,17 +873,18 @@ def dsa_kv4_read(cache: KV4Cache, row_offsets, positions, k_out, v_out, ws, stre
     """k_out [R, H_kv, D_k] and v_out [R, H_kv, D_v] (either may be None), bfloat16 or float16: what the
     cache holds at positions[r] of row r's request."""
     import torch
-    c, dev = cache.c, _check_cache(cache)
-    _check_ints(dict(row_offsets=c.B + 1), row_offsets=row_offsets, positions=positions)
-    R = int(positions.shape[0])
-    outs = {n: t for n, t in (("k_out", k_out), ("v_out", v_out)) if t is not None}
-    flags = _fp16_flag(**outs) if outs else 0
-    dtype = torch.float16 if flags else torch.bfloat16
-    _check_outputs(dev, (("k_out", k_out, (R, c.H_kv, c.D_k), dtype), ("v_out", v_out, (R, c.H_kv, c.D_v), dtype),
-                         ("row_offsets", row_offsets, (c.B + 1,), torch.int32), ("positions", positions, (R,), torch.int32)), ws)
+    dev = _check_cache(cache)
+    ref, n, H_kv, D_k, D_v = cache._expect
+    R = positions.shape[0]
+    dtype = torch.bfloat16 if k_out is None and v_out is None else (v_out if k_out is None else k_out).dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"k_out and v_out must be bfloat16 or float16, got {dtype}")
+    flags = DSA_FLAG_FP16 if dtype is torch.float16 else 0
+    _check_outputs(dev, (("k_out", k_out, (R, H_kv, D_k), dtype), ("v_out", v_out, (R, H_kv, D_v), dtype),
+                         ("row_offsets", row_offsets, (n,), torch.int32), ("positions", positions, (R,), torch.int32)), ws)
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
-    _check(_lib.dsa_kv4_read(cache._expect[0], R, _ptr(row_offsets), _ptr(positions), flags, _ptr(k_out), _ptr(v_out), _ptr(ws),
+    _check(_lib.dsa_kv4_read(ref, R, _ptr(row_offsets), _ptr(positions), flags, _ptr(k_out), _ptr(v_out), _ptr(ws),
                              ws.numel(), _stream(stream)))
 
 
