@@ -18,21 +18,36 @@
 //
 // What bounds it.  Per position and K/V head (D_k + D_v) 17 / 32 bytes have to be read: 136 for
 // 128 + 128, at 45 GB/s for an SM one every 5.7 cycles.  The tensor core has little to do
-// (8 to 16 rows), but every code passes through a register: 5 instructions for 8 codes of K, 6 for
-// V, 16 mma.sync a 16 positions.  Dequantised tiles in shared memory for tcgen05 would
-// cost the same extraction, a store and two reads of 16-bit operands; registers are what
-// mma.sync takes and tcgen05 does not.
+// (8 to 16 rows), but every code passes through a register: 5 instructions for 8 codes,
+// 18 mma.sync for 16 positions, 245 instructions in all with the softmax.  Dequantised tiles in shared
+// memory for tcgen05 would cost the same extraction, a store and two reads of 16-bit
+// operands; registers are what mma.sync takes and tcgen05 does not.  Measured: one token of 64
+// heads over 8 and 307200 positions 65 us, 5.1 TB/s with the start (5 us until the first stage
+// is there) and the join; half the issue slots and half of the ALU's are taken.  32 ragged tokens of
+// up to 32768 positions 80 us in pages of 64 (5.3 TB/s), 87 in pages of 16, whose copies are 2 KB
+// each.  One token over 4096 positions 11.6 us: a chain of launch, lengths, table, first pages, two
+// tiles of 32 positions, and the join.
 //
 // A CTA takes 128 positions of one K/V head at a time (a stage: whole page blocks, one bulk
-// copy each, through a ring) and eight warps 16 positions each, every warp with its own maximum,
-// sum and O; they are joined when an item ends.  Each lane holds 32-bit words of codes in the
-// layout of the products' fragments: rows of K are positions, and rows of V columns, so V needs two
-// positions' codes side by side (one byte permutation for 4 pairs).
+// copy each, through a ring).  Four of its eight warps take a stage, 32 positions each, the other
+// four the next one; every warp has its own maximum, sum and O, which are joined when an item
+// ends.  Each lane holds 32-bit words of codes in the layout of the products' fragments: rows of K
+// are positions, and rows of V columns, so V needs two positions' codes side by side, which is
+// how ldmatrix transposes 16-bit units of four codes.  A stage's place in the ring is given back
+// before the softmax, with V's codes in registers.
+//
+// A ninth warp loads.  It shares its scheduler with the others, so its loop over stages is kept
+// short (lookups a window of 32 table entries at a time); it also lays out an item's queries for
+// the products, which by each warp for itself took registers that spilled.
 //
 // Work.  Items (request, block of packed rows, K/V head) are laid end to end in stages
 // and cut into equal shares, one for each CTA, so ragged requests keep all SMs
 // busy to the end.  An item cut by a share's end leaves its parts (m, l, O) in the workspace
 // and kv4_join_kernel joins them, always in the same order.
+//
+// Tried and taken out: pages prefetched into L2 behind the ring (307200 positions 68 -> 71 to 90 us);
+// parts of one stage (one token over 4096 positions 14.7 -> 13.0 without: half the warps idled);
+// one warp to a row of the join (21 us for 32 parts).
 //
 // All waits are bounded; on expiry the CTA stops and drains its copies.
 #include "kv4.cuh"

@@ -2,14 +2,20 @@
 // dense_kernel.cuh in one of two ways.
 //
 // Few row tiles: the kernel with four warps that turn pages into its K and V tiles in the place of
-// the copies.  Many: each K/V tile would be widened once for every pair of row tiles (at 0.6 us
-// of an SM), so kv4_copy_kernel widens the pages once into the workspace and the kernel reads
-// that.
+// the copies.  Their registers come from the softmax warps (192 instead of 224).  A converting warp's
+// thread holds one position and 64 of its columns at a time: 32 bytes of codes and a scale, loaded
+// two chunks ahead, become 128 bytes in the swizzled layout that the products read.  That takes 1250
+// cycles a chunk and bounds the kernel (2.4 to 2.6 us a tile of 128 positions against 1.75 with a
+// 16-bit cache); four chunks ahead made it slower (a 2048-row chunk 579 -> 656 us: its code competes
+// for the instruction cache).
 //
-// A converting warp's thread holds one position and 64 of its columns at a time: 32 bytes of
-// codes and a scale, loaded two chunks ahead, become 128 bytes in the swizzled layout that
-// the products read.  A scale has 4 significant bits, so code * scale is exact in the
-// operands' type and the products are those of the values that the cache stands for.
+// Many: each K/V tile would be widened once for every pair of row tiles, so kv4_copy_kernel widens
+// the pages once into the workspace and the kernel reads that (a 2048-row chunk over 10240
+// positions 579 -> 405 us, 14 of them the copy; eight prompts of up to 2048 tokens, one K/V head to
+// a query head, 370 -> 315, 68 of them the copy).
+//
+// A scale has 4 significant bits, so code * scale is exact in bf16 (in fp16 within its range) and the
+// products are those of the values that the cache stands for.
 #include "dense_kernel.cuh"
 
 namespace dsa {

@@ -7,7 +7,8 @@ namespace dsa {
 
 // Eight 4-bit codes times their scale (bf16 bits) in 16 bits, in order.  bf16: 128 + code by byte
 // permutations, then one packed multiply-add, (128 + code) s - 136 s: exact, since 136 s has 8
-// significant bits.  fp16: 1024 + code, minus 1032, times s: the last step alone may round.
+// significant bits; a scale from 2^120 on, where 136 s would leave the range, is taken 2^-8 of and the
+// values 2^8 times.  fp16: 1024 + code, minus 1032, times s: the last step alone may round.
 template <bool F16>
 __device__ __forceinline__ void widen8(uint32_t w, uint32_t scale, uint32_t* o) {
   const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
@@ -24,12 +25,14 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t scale, uint32_t* o) 
       o[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   } else {
-    uint32_t sb = scale * 0x10001u;
+    const bool huge = scale >= 0x7b80u && scale < 0x7f80u;
+    uint32_t sb = (huge ? scale - 0x400u : scale) * 0x10001u;
     const __nv_bfloat162 s2 = *reinterpret_cast<__nv_bfloat162*>(&sb);
     const __nv_bfloat162 zero = __hmul2(s2, __floats2bfloat162_rn(-136.f, -136.f));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&u[i]), s2, zero);
+      __nv_bfloat162 v = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&u[i]), s2, zero);
+      if (huge) v = __hmul2(v, __floats2bfloat162_rn(256.f, 256.f));
       o[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }

@@ -3,11 +3,14 @@
 //   y = x w / sqrt(mean x^2 + eps), then pairs of columns turned by position * inv_freq.
 //
 // Every element is read once and written once (4 bytes against about ten operations), so
-// what bounds the kernel is HBM, or for few rows latency.  A CTA takes four rows, whose
+// what bounds the kernel is HBM, or for few rows latency.  A CTA takes up to eight rows, whose
 // angles' cos and sin its threads work out first, one each (by every warp for itself they were
 // 40% of its instructions), and its warps runs of a row's heads, with the norm's weights in registers.  A
 // head is held by 8 to 32 lanes with both columns of a pair in one lane (rope.cuh), so the
 // rotation needs no exchange and the norm three to five shuffles.
+//
+// Measured: 9601 rows of 64 + 8 heads of 128 out of a fused projection 62.5 us, 5.7 TB/s (83% of the
+// copy rate; 61% of the issue slots are taken); one row 2.3 us in a graph.
 #include "rope.cuh"
 
 namespace dsa {

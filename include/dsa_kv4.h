@@ -62,8 +62,8 @@ DSA_API size_t dsa_kv4_block_bytes(int32_t D_k, int32_t D_v, int32_t page_size);
  * p->D_k, p->H_kv and p->B are the cache's; p->D_v as well.  Rows of a negative position
  * and rows outside row_offsets are skipped.  A position past the table, or a page outside
  * the pool, is skipped (its query is written all the same) and raises DSA_DEVICE_BAD_INDEX.
- * Positions of one call name different places: of two rows for one place, which one is
- * held is not specified.
+ * Positions of one call name different places: what a place holds that two rows are for is
+ * not specified.
  * ws: at least 256 bytes, 256-byte aligned; its status word is set by the call
  * (dsa_read_device_status).  Two kernels, asynchronous on `stream`, no host
  * synchronisation, capturable in a CUDA graph.  Calls that may overlap need workspaces of
@@ -77,7 +77,8 @@ DSA_API dsa_status dsa_kv4_append(const dsa_kv4_cache* c, const dsa_qk_problem* 
  * aligned) get the values that positions[r] of row r's request holds, in bf16, or in fp16 with
  * flags = DSA_FLAG_FP16 (exact in bf16; rounded once in fp16).  row_offsets [B + 1] are the
  * rows of the cache's B requests; R <= 2^31 - 1.  Skipped rows (as above) are left as they
- * were.  For prompts that attend over a cached prefix with dsa_dense_attn.
+ * were.  In fp16 a scale has to be below 2^16 (a pool written from fp16 has no larger ones).  For
+ * prompts that attend over a cached prefix with dsa_dense_attn.
  */
 DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t* row_offsets, const int32_t* positions,
                                 int32_t flags, uint16_t* k_out, uint16_t* v_out, void* ws, size_t ws_bytes, void* stream);
@@ -96,8 +97,9 @@ DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t
  *   R        query rows                                         0 <= R <= 65535
  *   H_q      query heads, a multiple of the cache's H_kv         1 <= H_q <= 128
  *   L_max    >= max(row_len)
- *   rows_max >= the most query rows of one request; 0 = not known (R is taken).  It
- *            decides which kernel runs; outputs do not depend on it but for rounding.
+ *   rows_max  the most query rows of one request, as far as known; 0 = not known (R is
+ *            taken).  It decides which kernel runs (outputs do not depend on it but for rounding)
+ *            and with it the workspace: below.
  *   q_stride elements from one row to the next; 0 = packed; a multiple of 8
  *   flags    DSA_FLAG_FP16
  *   q        [R, H_q, D_k], 16-byte aligned
@@ -106,11 +108,16 @@ DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t
  *            DSA_DEVICE_BAD_INDEX; so does a page outside the pool, whose positions are
  *            then as if masked.
  *
- * Precision: products with the codes are exact and summed in fp32; the softmax statistics are
+ * Kernels, by the packed rows of a request, rows_max * G: up to 64 a few rows at a time with the
+ * codes as they are, more in tiles of 128 whose K and V are widened to 16 bits, from 1024 on
+ * with the pages widened once into the workspace, where that takes at most 8 GB there.
+ *
+ * Precision: products with K are exact and summed in fp32; the softmax statistics are
  * fp32; a softmax weight is rounded once, to the operands' type or finer, for its product with
- * V; the output once.  Results do not depend on timing.  What lies at positions that no row
- * of a request sees may be anything.  A scale that some rows of a request see has to be
- * finite, or any output of that request may be NaN.
+ * V; the output once.  Results do not depend on timing.  Range: |q| below 2^115; sums over
+ * positions of 2^15 |v| below 2^128 (weights are held as up to 2^15 of them).  What lies at positions
+ * that no row of a request sees may be anything.  A scale that some rows of a request see has to
+ * be finite (with fp16 queries below 2^16), or any output of that request may be NaN.
  */
 typedef struct dsa_kv4_problem {
   int32_t R, H_q, L_max, rows_max;
@@ -123,7 +130,8 @@ typedef struct dsa_kv4_problem {
 } dsa_kv4_problem;
 
 /* Workspace bytes of dsa_kv4_attn (host only; 0 if the problem is invalid:
- * dsa_last_error_string() says why). */
+ * dsa_last_error_string() says why): some megabytes, or with 1024 packed rows or more
+ * B * L_max * H_kv * (D_k + D_v) * 2 bytes beside them. */
 DSA_API size_t dsa_kv4_workspace_size(const dsa_kv4_cache* c, const dsa_kv4_problem* p);
 
 /*

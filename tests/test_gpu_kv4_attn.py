@@ -477,3 +477,19 @@ def test_copied_missing_tile_is_bounded():
     assert dsa.dsa_read_device_status(ws) == 0
     keep = _sample([600])
     H.check(_few(t, keep), 0.09, out.cpu()[keep], None)
+
+
+@pytest.mark.parametrize("rows", [1, 150, 600])
+def test_values_near_the_end_of_the_range(rows):
+    # K's scales of 2^121: 136 of them are beyond bf16, the values are not.  V's of 2^89: the sums of weights (held as up
+    # to 2^15 of them) times values have to stay in fp32, 2^15 * 700 * 7 * 2^89 = 2^116.3; with 2^121 as well they
+    # would be 2^148.
+    t = H.make([rows], [700], 2, 1, 64, 64, 64, seed=47)
+    _, _, ks, vs = H.parts(t["pages"], 64, 64, 64)
+    vs.copy_((vs.float() * 2.0 ** 90).bfloat16())
+    ks.copy_((ks.float() * 2.0 ** 122).bfloat16())
+    t["q"] = (t["q"].float() * 2.0 ** -122).bfloat16()
+    out, lse, bits = H.run(t, 0.125)
+    keep = _sample([rows])
+    assert bits == 0
+    H.check(_few(t, keep), 0.125, out[keep], lse[keep])

@@ -282,6 +282,18 @@ def test_read_into_a_view_and_one_of_the_two():
     assert (flat[:8] == 55).all() and (flat[-8:] == 55).all()
 
 
+@pytest.mark.parametrize("e", [-124, -60, 0, 60, 119, 123])
+def test_read_of_all_magnitudes(e):
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    g = torch.Generator().manual_seed(7)
+    x = (torch.rand(9, 2, 128, generator=g, dtype=torch.float64) * 2 - 1).mul(2.0 ** e * 14).bfloat16()
+    a = _append([9], [0], 0, 2, 128, 128, 16, rot=0, norm=False, x=(x, x.flip(2)))
+    ko, vo = (torch.zeros(9, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dsa.dsa_kv4_read(a["cache"], a["ro"].cuda(), a["pos"].cuda(), ko, vo, a["ws"])
+    assert ko.cpu().double().equal(H.held(x)) and vo.cpu().double().equal(H.held(x.flip(2)))
+
+
 def test_pool_beyond_32_bits():
     import torch
     import dsa_sparse_attention_03_gb300 as dsa
