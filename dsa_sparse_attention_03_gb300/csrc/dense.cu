@@ -7,7 +7,7 @@ namespace {
 
 template <int DK, int DV, int NW, bool F16>
 cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
-  constexpr size_t smem = smem_bytes<DK, DV, NW>();
+  constexpr size_t smem = smem_bytes<DK, DV, NW, kPacked>();
   static_assert(smem <= 232448, "shared memory of one CTA");
   auto kernel = dense_attn_kernel<DK, DV, NW, F16, kPacked>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -123,18 +123,24 @@ struct __align__(16) Shared {
   volatile int steps[2];          // K/V tiles that each row tile's issuer is through with
   Item item[2];
   int first[kBlocks + 1];         // row tiles before each block of requests
+  uint64_t rfull[2], rempty[2];   // pages: tiles as they come, 4 bits
+  uint32_t rpages[2];             // of these, the pages that the pool has
   uint32_t there[16];             // pages: of each K/V tile, a byte for every 32 positions: bits of 16 whose page the pool has
 };
 
-template <int DK, int DV, int NW>
+// A K/V tile in 4 bits: its pages' blocks.
+template <int DK, int DV>
+constexpr uint32_t kRawBytes = kTile * (DK + DV) / 32 * 17;
+template <int DK, int DV, int NW, CacheKind Kind>
 __host__ __device__ constexpr int ring_slots() {
-  constexpr int budget = (NW == 1 ? 113 : 227) * 1024 - (int)sizeof(Shared);
+  constexpr int budget = (NW == 1 ? 113 : 227) * 1024 - (int)sizeof(Shared) - (Kind == kPages ? 2 * (int)kRawBytes<DK, DV> : 0);
   constexpr int s = (budget - NW * kTile * DK * 2) / (int)kChunkBytes;
   return s < 16 ? s : 16;
 }
-template <int DK, int DV, int NW>
+template <int DK, int DV, int NW, CacheKind Kind>
 __host__ __device__ constexpr size_t smem_bytes() {
-  return (size_t)NW * kTile * DK * 2 + (size_t)ring_slots<DK, DV, NW>() * kChunkBytes + sizeof(Shared);
+  return (size_t)NW * kTile * DK * 2 + (size_t)ring_slots<DK, DV, NW, Kind>() * kChunkBytes +
+         (Kind == kPages ? 2 * kRawBytes<DK, DV> : 0) + sizeof(Shared);
 }
 
 __host__ __device__ __forceinline__ uint32_t item_count(const DenseArgs& a) {   // (below 2^31: dense_shape)
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
     dense_attn_kernel(const __grid_constant__ DenseArgs a) {
   constexpr bool Q4 = Kind == kPages;       // four bits in, K and V tiles made here
   static_assert(!Q4 || NW == 2, "registers of the widening warps");
-  constexpr int NS = ring_slots<DK, DV, NW>();
+  constexpr int NS = ring_slots<DK, DV, NW, Kind>();
   constexpr int KC = DK / 64, VC = DV / 64;
   constexpr uint32_t kQBytes = kTile * DK * 2;
   constexpr uint32_t kCols = NW * 256;      // S of each row tile, then O of each
@@ -328,7 +334,8 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* Qs = smem;
   unsigned char* ring = smem + NW * kQBytes;
-  Shared* sh = reinterpret_cast<Shared*>(ring + NS * kChunkBytes);
+  unsigned char* raw = ring + NS * kChunkBytes;
+  Shared* sh = reinterpret_cast<Shared*>(raw + (Q4 ? 2 * kRawBytes<DK, DV> : 0));
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
@@ -357,6 +364,8 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
       mbar_init(bar(sh->done[i]), 1);
       mbar_init(bar(sh->ifull[i]), 1);
       mbar_init(bar(sh->ifree[i]), kReaders);
+      mbar_init(bar(sh->rfull[i]), 1);
+      mbar_init(bar(sh->rempty[i]), 4);
     }
     mbar_init(bar(sh->inext), 1);
     sh->abort = 0;
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
     // 2000 to 4000 cycles, and a longer lead takes it from a CTA that would be free (32
     // single tokens 254 us with two, 257 with four, 258 with six; prompts alike).
     constexpr int early = NW == 1 ? 2 : 4;
-    int n = 0, nq[2] = {0, 0};   // chunks and Q tiles asked for
+    int n = 0, nq[2] = {0, 0};   // chunks (pages: tiles) and Q tiles asked for
     bool ok = true;
     for (int k = 0; ok && item_wait(k); ++k) {
       const Item it = sh->item[k & 1];
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
           ++q;
         };
         load_q(0);
-        if (Q4) load_q(1);   // (K and V are the converting warps')
+        if (Q4) load_q(1);
         if (!Q4 && it.steps == 0) mbar_arrive(bar(sh->inext));
         for (int j = 0; !Q4 && j < it.steps && ok; ++j) {
           if (j == max(it.steps - early, 0)) mbar_arrive(bar(sh->inext));
@@ -493,9 +502,41 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
         }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      if (Q4 && ok) {
+        // Tiles as their pages hold them, for the warps that widen them.  A lane holds a page of the 32's
+        // window of the table.
+        const int npp = kTile >> a.kv4.ps_log2, win = 32 / npp, ends = (it.kv_end + a.kv4.ps - 1) >> a.kv4.ps_log2;
+        const int32_t* table = a.kv4.table + (int64_t)it.o0 * a.kv4.cols;
+        auto entry = [&](int i) { return i < ends ? table[i] : -1; };
+        int next = entry(it.lo * npp + lane);
+        uint32_t have = 0;
+        const uint8_t* src = nullptr;
+        for (int j = 0; j < it.steps; ++j, ++n) {
+          const int y = j & (win - 1), s = n & 1;
+          if (y == 0) {
+            const int at = (it.lo + j) * npp + lane, id = next;
+            next = entry(at + 32);
+            const bool there = at < ends && id >= 0 && id < a.kv4.n_pages;
+            have = __ballot_sync(0xffffffffu, there);
+            if (__any_sync(0xffffffffu, at < ends && at < (it.lo + it.steps) * npp && !there) && lane == 0)
+              raise_status(status, DSA_DEVICE_BAD_INDEX);
+            src = a.kv4.pages + ((int64_t)id * a.kv4.H_kv + it.h) * a.kv4.block;
+          }
+          const uint32_t mask = have >> (y * npp) & ((1u << npp) - 1u);
+          if (n >= 2 && !(ok = wait_bar_warp(bar(sh->rempty[s]), ((n >> 1) - 1) & 1, wc))) break;
+          if (lane == 0) {
+            sh->rpages[s] = mask;
+            mbar_expect_tx(bar(sh->rfull[s]), __popc(mask) * a.kv4.block);
+          }
+          __syncwarp();
+          if (lane / npp == y && (have >> lane & 1u) && !(a.test_no_load && n == 0))
+            bulk_row(smem_u32(raw) + s * kRawBytes<DK, DV> + lane % npp * a.kv4.block, src, a.kv4.block, bar(sh->rfull[s]));
+        }
+      }
     }
     if (lane == 0) {   // (an abort may leave copies in flight)
-      for (int i = max(0, n - NS); i < n; ++i) drain_bar(bar(sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
+      for (int i = max(0, n - 2); Q4 && i < n; ++i) drain_bar(bar(sh->rfull[i & 1]), (i >> 1) & 1, a.wait_ns);
+      for (int i = max(0, n - NS); !Q4 && i < n; ++i) drain_bar(bar(sh->full[i % NS]), (i / NS) & 1, a.wait_ns);
       for (int w = 0; w < NW; ++w)
         if (nq[w] > 0) drain_bar(bar(sh->qfull[w]), (nq[w] - 1) & 1, a.wait_ns);
     }
@@ -621,106 +662,59 @@ __global__ void __launch_bounds__(kDenseThreads<NW, Kind>, NW == 1 ? 2 : 1)
    }
   } else if (Q4 && warp < kSoftmax) {
     // ------------------------------------------------------------ converters
-    // A thread holds a position: 64 columns of K or V (32 bytes of codes) at a time, two
-    // chunks ahead in registers, become 128 bytes of a ring chunk.
+    // A thread holds a position: 64 columns of K or V at a time (32 bytes of codes) become 128 bytes of
+    // a ring chunk.
     regs_down<72>();
-    const int r = tid & 127;
-    const int ps = a.kv4.ps, kscales = ps * ((DK + DV) / 2);
+    const int r = tid & 127, ps = a.kv4.ps, page = r >> a.kv4.ps_log2;
+    const unsigned char* mine = raw + page * a.kv4.block + (r & (ps - 1)) * 32;
+    const int scales = ps * ((DK + DV) / 2) - (r & (ps - 1)) * 30;    // (from `mine` on)
     int n = 0, tiles = 0;       // chunks handed over, K/V tiles begun
     bool ok = true;
     for (int k = 0; ok && item_wait(k); ++k) {
       const Item& si = sh->item[k & 1];
-      const int rows = si.rows, steps = si.steps, lo = si.lo, kv_end = si.kv_end, h = si.h;
-      const int32_t* table = a.kv4.table + (int64_t)si.o0 * a.kv4.cols;
+      const int rows = si.rows, steps = si.steps, lo = si.lo, kv_end = si.kv_end;
       item_done(k);
       if (rows == 0) break;
-      if (steps == 0) {
-        if (tid == 128) mbar_arrive(bar(sh->inext));
-        continue;
-      }
+      if (steps == 0 && tid == 128) mbar_arrive(bar(sh->inext));
       constexpr int C = KC + VC, early = 4;
-      const int chunks = steps * C;
-      // Page of this thread's position in tile j, asked for a tile ahead; -1: not seen, -2: not in the pool.
-      auto entry = [&](int j) {
-        const int pos = (lo + j) * kTile + r;
-        if (j >= steps || pos >= kv_end) return -1;
-        const int id = table[pos >> a.kv4.ps_log2];
-        return id >= 0 && id < a.kv4.n_pages ? id : -2;
-      };
-      struct Raw {
-        uint4 lo, hi;
-        uint32_t scale;
-      };
-      int page = entry(0), next = entry(1), lt = 0, lc = 0;   // tile and chunk of the next load
-      auto load = [&](Raw& x) {
-        x.lo = x.hi = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-        x.scale = 0;
-        if (lt < steps) {
-          if (page >= 0) {
-            const uint8_t* blk = a.kv4.pages + ((int64_t)page * a.kv4.H_kv + h) * a.kv4.block;
-            const int at = lc * ps + (((lo + lt) * kTile + r) & (ps - 1));   // (K's groups, then V's, for codes and scales alike)
-            x.lo = *reinterpret_cast<const uint4*>(blk + at * 32);
-            x.hi = *reinterpret_cast<const uint4*>(blk + at * 32 + 16);
-            x.scale = *reinterpret_cast<const uint16_t*>(blk + kscales + at * 2);
+      for (int j = 0; j < steps && ok; ++j, ++tiles) {
+        if (j == max(steps - early, 0) && tid == 128) mbar_arrive(bar(sh->inext));
+        const int s = tiles & 1;
+        if (!(ok = wait_bar_warp(bar(sh->rfull[s]), (tiles >> 1) & 1, wc))) break;
+        const bool seen = (lo + j) * kTile + r < kv_end, have = sh->rpages[s] >> page & 1u;
+        const uint32_t gone = __ballot_sync(0xffffffffu, seen && !have);
+        if (lane == 0)
+          reinterpret_cast<volatile uint8_t*>(&sh->there[tiles & 15])[warp & 3] = (gone & 0xffffu ? 0 : 1) | (gone >> 16 ? 0 : 2);
+        const unsigned char* src = mine + s * kRawBytes<DK, DV>;
+#pragma unroll 1
+        for (int c = 0; c < C; ++c, ++n) {
+          // (what no row sees, or no page holds, is zero: 8 codes of 8, and no scale)
+          uint4 x0 = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u), x1 = x0;
+          uint32_t scale = 0;
+          if (seen && have) {
+            x0 = *reinterpret_cast<const uint4*>(src + c * ps * 32);
+            x1 = *reinterpret_cast<const uint4*>(src + c * ps * 32 + 16);
+            scale = *reinterpret_cast<const uint16_t*>(src + scales + c * ps * 2);
           }
-          if (++lc == C) {
-            lc = 0;
-            ++lt;
-            page = next;
-            next = entry(lt + 1);
+          if (c == C - 1) {     // (the tile is read)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh->rempty[s]));
           }
-        }
-      };
-      int j = 0, c = 0;           // tile and chunk being converted
-      bool bad = false;
-      auto convert = [&](const Raw& x, int state) {
-        if (c == 0) {             // (before the chunk is handed over)
-          if (j == max(steps - early, 0) && tid == 128) mbar_arrive(bar(sh->inext));
-          const uint32_t gone = __ballot_sync(0xffffffffu, state == -2);
-          if (lane == 0)
-            reinterpret_cast<volatile uint8_t*>(&sh->there[tiles & 15])[warp & 3] = (gone & 0xffffu ? 0 : 1) | (gone >> 16 ? 0 : 2);
-          bad |= state == -2;
-          ++tiles;
-        }
-        const int s = n % NS;
-        if (n >= NS && !wait_bar_warp(bar(sh->empty[s]), (n / NS - 1) & 1, wc)) {
-          ok = false;
-          return;
-        }
-        unsigned char* dst = ring + s * kChunkBytes + r * 128;
-        const uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
+          const int slot = n % NS;
+          if (n >= NS && !(ok = wait_bar_warp(bar(sh->empty[slot]), (n / NS - 1) & 1, wc))) break;
+          unsigned char* dst = ring + slot * kChunkBytes + r * 128;
+          const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          uint32_t o[4];
-          widen8<F16>(w[y], x.scale, o);
-          *reinterpret_cast<uint4*>(dst + ((y ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0 && !(a.test_no_load && n == 0)) mbar_arrive(bar(sh->full[s]));
-        ++n;
-        if (++c == C) {
-          c = 0;
-          ++j;
-        }
-      };
-      // (The state of a tile's page, known when its first chunk was loaded, kept for its conversion.)
-      Raw x0, x1;
-      int s0 = page;
-      load(x0);
-      int s1 = page;
-      load(x1);
-      for (int m = 0; m < chunks && ok; m += 2) {
-        convert(x0, s0);
-        s0 = page;
-        load(x0);
-        if (m + 1 < chunks && ok) {
-          convert(x1, s1);
-          s1 = page;
-          load(x1);
+          for (int y = 0; y < 8; ++y) {
+            uint32_t o[4];
+            widen8<F16>(w[y], scale, o);
+            *reinterpret_cast<uint4*>(dst + ((y ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sh->full[slot]));
         }
       }
-      if (__any_sync(0xffffffffu, bad) && lane == 0) raise_status(status, DSA_DEVICE_BAD_INDEX);
     }
   } else {
     // ------------------------------------------------------------ softmax

@@ -2,17 +2,19 @@
 // dense_kernel.cuh in one of two ways.
 //
 // Few row tiles: the kernel with four warps that turn pages into its K and V tiles in the place of
-// the copies.  Their registers come from the softmax warps (192 instead of 224).  A converting warp's
-// thread holds one position and 64 of its columns at a time: 32 bytes of codes and a scale, loaded
-// two chunks ahead, become 128 bytes in the swizzled layout that the products read.  That takes 1250
-// cycles a chunk and bounds the kernel (2.4 to 2.6 us a tile of 128 positions against 1.75 with a
-// 16-bit cache); four chunks ahead made it slower (a 2048-row chunk 579 -> 656 us: its code competes
-// for the instruction cache).
+// the copies.  Their registers come from the softmax warps (192 instead of 224).  The loading warp
+// brings a tile's page blocks as they are (two tiles ahead, by bulk copies), and a converting warp's
+// thread turns one position and 64 of its columns at a time, 32 bytes of codes and a scale, into 128
+// bytes in the swizzled layout that the products read.  The converting warps bound the kernel: a tile of
+// 128 positions takes about 1.9 us against 1.75 with a 16-bit cache (16 rows of 64 heads over 8
+// and 307200 positions 247 us; eight prompts of up to 2048 tokens, width 192, 285, with a 16-bit
+// cache 218).  With the codes loaded into registers, two chunks ahead, a chunk took them 1250
+// cycles (357 and 370 us); four chunks ahead were slower still, the code competing for the
+// instruction cache.
 //
 // Many: each K/V tile would be widened once for every pair of row tiles, so kv4_copy_kernel widens
 // the pages once into the workspace and the kernel reads that (a 2048-row chunk over 10240
-// positions 579 -> 405 us, 14 of them the copy; eight prompts of up to 2048 tokens, one K/V head to
-// a query head, 370 -> 315, 68 of them the copy).
+// positions 518 -> 405 us, 14 of them the copy).
 //
 // A scale has 4 significant bits, so code * scale is exact in bf16 (in fp16 within its range) and the
 // products are those of the values that the cache stands for.
@@ -23,7 +25,7 @@ namespace {
 
 template <int DK, int DV, bool F16, CacheKind Kind>
 cudaError_t launch_one(const DenseArgs& a, cudaStream_t st) {
-  constexpr size_t smem = smem_bytes<DK, DV, 2>();
+  constexpr size_t smem = smem_bytes<DK, DV, 2, Kind>();
   static_assert(smem <= 232448, "shared memory of one CTA");
   auto kernel = dense_attn_kernel<DK, DV, 2, F16, Kind>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -118,7 +120,8 @@ Kv4Tile kv4_tile(const dsa_kv4_cache& c, const dsa_kv4_problem& p) {
   off = up(off + parts * c.D_v * 4);
   const int64_t most = p.rows_max > 0 && p.rows_max < p.R ? p.rows_max : p.R;
   const size_t positions = (size_t)d.L_total;
-  s.copied = most * (p.H_q / c.H_kv) >= kCopyRows && d.L_max > 0 && positions <= (size_t(1) << 31) - 256 &&
+  const int64_t packed = most * (p.H_q / c.H_kv), hidden = d.L_max > 0 ? packed * (most < d.L_max ? most : d.L_max) / (2 * (int64_t)d.L_max) : 0;
+  s.copied = packed - hidden >= kCopyRows && d.L_max > 0 && positions <= (size_t(1) << 31) - 256 &&
              positions * c.H_kv * (c.D_k + c.D_v) * 2 <= kCopyBytes;
   s.off_gone = s.off_k = s.off_v = off;
   if (s.copied) {

@@ -109,8 +109,9 @@ DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t
  *            then as if masked.
  *
  * Kernels, by the packed rows of a request, rows_max * G: up to 64 a few rows at a time with the
- * codes as they are, more in tiles of 128 whose K and V are widened to 16 bits, from 1024 on
- * with the pages widened once into the workspace, where that takes at most 8 GB there.
+ * codes as they are, more in tiles of 128 whose K and V are widened to 16 bits, from 2304 on (of
+ * which a whole prompt's count half) with the pages widened once into the workspace, where that
+ * takes at most 8 GB there.
  *
  * Precision: products with K are exact and summed in fp32; the softmax statistics are
  * fp32; a softmax weight is rounded once, to the operands' type or finer, for its product with
@@ -130,8 +131,8 @@ typedef struct dsa_kv4_problem {
 } dsa_kv4_problem;
 
 /* Workspace bytes of dsa_kv4_attn (host only; 0 if the problem is invalid:
- * dsa_last_error_string() says why): some megabytes, or with 1024 packed rows or more
- * B * L_max * H_kv * (D_k + D_v) * 2 bytes beside them. */
+ * dsa_last_error_string() says why): some megabytes, or with 2304 packed rows or more
+ * (see above) B * L_max * H_kv * (D_k + D_v) * 2 bytes beside them. */
 DSA_API size_t dsa_kv4_workspace_size(const dsa_kv4_cache* c, const dsa_kv4_problem* p);
 
 /*

@@ -347,6 +347,13 @@ def _few(t, keep):
     return dict(t, q=t["q"][keep], row_len=t["row_len"][keep], row_offsets=H.prefix(n))
 
 
+def _is_copied(t, scale):
+    # (told by the workspace, which holds K and V in 16 bits then)
+    import dsa_sparse_attention_03_gb300 as dsa
+    prob = H.problem(t, scale)
+    return dsa.dsa_kv4_workspace_size(prob) >= len(t["table"]) * prob.L_max * t["pages"].shape[1] * (t["dk"] + t["dv"]) * 2
+
+
 def _sample(rows, step=37):
     out, r = [], 0
     for n in rows:
@@ -357,13 +364,14 @@ def _sample(rows, step=37):
 
 @pytest.mark.parametrize("dk,dv", W)
 @pytest.mark.parametrize("dt,ps,rows,lens,hq,hkv", [
-    ("bf16", 64, [1030], [1030], 2, 2),                      # a prompt of one head to a K/V head
-    ("fp16", 16, [300, 1, 513, 0, 7], [300, 900, 1500, 40, 7], 8, 2),
-    ("bf16", 128, [400], [2500], 3, 1),                      # a group that does not divide a row tile
+    ("bf16", 64, [1030], [1030], 8, 1),
+    ("fp16", 16, [300, 1, 513, 0, 7], [300, 900, 1500, 40, 7], 16, 2),
+    ("bf16", 128, [400], [2500], 7, 1),                      # a group that does not divide a row tile
 ])
 def test_copied(dk, dv, dt, ps, rows, lens, hq, hkv):
     t = H.make(rows, lens, hq, hkv, dk, dv, ps, dt, seed=dk + ps)
     scale = 1 / math.sqrt(dk)
+    assert _is_copied(t, scale)
     out, lse, bits = H.run(t, scale)
     assert bits == 0
     keep = _sample(rows)
@@ -374,7 +382,8 @@ def test_copied(dk, dv, dt, ps, rows, lens, hq, hkv):
 
 def test_copied_and_not_agree():
     # The three kernels on one problem: few rows at a time, widened by the way, widened first.
-    t = H.make([600, 2], [900, 40], 4, 2, 128, 128, 32, seed=40)
+    t = H.make([600, 2], [900, 40], 16, 2, 128, 128, 32, seed=40)
+    assert _is_copied(t, 0.09)
     outs = [H.run(t, 0.09, rows_max=n)[0].double() for n in (1, 300, 600)]
     ref, _, bound, _ = H.reference(_few(t, _sample([600, 2])), 0.09)
     for out in outs:
@@ -387,7 +396,8 @@ def test_copied_any_row_len_and_places_no_row_sees(dt):
     g = torch.Generator().manual_seed(41)
     rows, lens, ps = [700, 560], [900, 640], 64
     rl = [int(torch.randint(0, L - 60, (1,), generator=g)) * (i % 5 != 1) for n, L in zip(rows, lens) for i in range(n)]
-    t = H.make(rows, lens, 4, 2, 128, 128, ps, dt, seed=41, row_len=rl)
+    t = H.make(rows, lens, 16, 2, 128, 128, ps, dt, seed=41, row_len=rl)
+    assert _is_copied(t, 0.1)
     dirty = dict(t, pages=t["pages"].clone(), table=t["table"].clone())
     seen = torch.zeros(t["pages"].shape[0], ps, dtype=torch.bool)
     for b, (n, a) in enumerate(zip(rows, (0, rows[0]))):
@@ -407,7 +417,8 @@ def test_copied_any_row_len_and_places_no_row_sees(dt):
 def test_copied_bad_pages_are_masked_and_flagged():
     import dsa_sparse_attention_03_gb300 as dsa
     rows = [600, 520]
-    t = H.make(rows, [900, 600], 4, 2, 128, 128, 32, seed=42)
+    t = H.make(rows, [900, 600], 16, 2, 128, 128, 32, seed=42)
+    assert _is_copied(t, 0.09)
     t["table"][0, 3] = -5
     t["table"][0, 20] = t["pages"].shape[0]
     out, lse, bits = H.run(t, 0.09)
@@ -423,7 +434,8 @@ def test_copied_bad_pages_are_masked_and_flagged():
 def test_copied_row_len_outside_and_rows_outside():
     import torch
     import dsa_sparse_attention_03_gb300 as dsa
-    t = H.make([560, 540], [640, 640], 4, 2, 64, 64, 64, seed=43, extra_rows=3)
+    t = H.make([560, 540], [640, 640], 16, 2, 64, 64, 64, seed=43, extra_rows=3)
+    assert _is_copied(t, 0.1)
     t["row_offsets"] += 2
     t["row_len"] = torch.cat([t["row_len"][-2:], t["row_len"][:-2]])
     t["row_len"][5], t["row_len"][9] = -4, 5000
@@ -442,9 +454,10 @@ def test_copied_captured():
     import torch
     import dsa_sparse_attention_03_gb300 as dsa
     rows, lens = [600, 1], [700, 2000]
-    t, other = (H.make(rows, lens, 4, 2, 128, 128, 64, seed=44 + i) for i in range(2))
+    t, other = (H.make(rows, lens, 16, 2, 128, 128, 64, seed=44 + i) for i in range(2))
+    assert _is_copied(t, 0.09)
     prob = H.problem(t, 0.09)
-    out = torch.zeros(601, 4, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(601, 16, 128, dtype=torch.bfloat16, device="cuda")
     ws = dsa.alloc_kv4_workspace(prob)
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
@@ -467,9 +480,10 @@ def test_copied_captured():
 def test_copied_missing_tile_is_bounded():
     import torch
     import dsa_sparse_attention_03_gb300 as dsa
-    t = H.make([600], [2000], 4, 2, 128, 128, 64, seed=46)
+    t = H.make([600], [2000], 16, 2, 128, 128, 64, seed=46)
+    assert _is_copied(t, 0.09)
     prob = H.problem(t, 0.09)
-    out = torch.zeros(600, 4, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(600, 16, 128, dtype=torch.bfloat16, device="cuda")
     ws = dsa.alloc_kv4_workspace(prob)
     dsa.dsa_test_kv4_missing_stage(prob, out, None, ws, 20_000_000)
     assert dsa.dsa_read_device_status(ws) & dsa.DSA_DEVICE_TIMEOUT
@@ -484,7 +498,8 @@ def test_values_near_the_end_of_the_range(rows):
     # K's scales of 2^121: 136 of them are beyond bf16, the values are not.  V's of 2^89: the sums of weights (held as up
     # to 2^15 of them) times values have to stay in fp32, 2^15 * 700 * 7 * 2^89 = 2^116.3; with 2^121 as well they
     # would be 2^148.
-    t = H.make([rows], [700], 2, 1, 64, 64, 64, seed=47)
+    t = H.make([rows], [700], 16, 2, 64, 64, 64, seed=47)
+    assert _is_copied(t, 0.125) == (rows == 600)
     _, _, ks, vs = H.parts(t["pages"], 64, 64, 64)
     vs.copy_((vs.float() * 2.0 ** 90).bfloat16())
     ks.copy_((ks.float() * 2.0 ** 122).bfloat16())
