@@ -22,11 +22,13 @@
 // 18 mma.sync for 16 positions, 245 instructions in all with the softmax.  Dequantised tiles in shared
 // memory for tcgen05 would cost the same extraction, a store and two reads of 16-bit
 // operands; registers are what mma.sync takes and tcgen05 does not.  Measured: one token of 64
-// heads over 8 and 307200 positions 65 us, 5.1 TB/s with the start (5 us until the first stage
-// is there) and the join; half the issue slots and half of the ALU's are taken.  32 ragged tokens of
-// up to 32768 positions 80 us in pages of 64 (5.3 TB/s), 87 in pages of 16, whose copies are 2 KB
-// each.  One token over 4096 positions 11.6 us: a chain of launch, lengths, table, first pages, two
-// tiles of 32 positions, and the join.
+// heads over 8 and 307200 positions 61.5 us, 5.4 TB/s with the start (3.6 us until the first stage is
+// there), CTAs that get less of HBM than others and end 6 us after the middle one, and the join (3
+// us); twice as many positions take another 50, the copy rate.  32 ragged tokens of up to 32768
+// positions 79.5 us in pages of 64 (5.3 TB/s), 83.5 in pages of 16, whose copies are 2 KB each.  One
+// token over 4096 positions 10.7 us: a chain of launch, lengths (0.7), the share's place in the batch
+// (0.8), table and first pages (1.5), two tiles of 32 positions (1 to 2), the warps' sums and parts
+// (1.2), the next launch (0.7) and the join.
 //
 // A CTA takes 128 positions of one K/V head at a time (a stage: whole page blocks, one bulk
 // copy each, through a ring).  Four of its eight warps take a stage, 32 positions each, the other
@@ -47,7 +49,7 @@
 //
 // Tried and taken out: pages prefetched into L2 behind the ring (307200 positions 68 -> 71 to 90 us);
 // parts of one stage (one token over 4096 positions 14.7 -> 13.0 without: half the warps idled);
-// one warp to a row of the join (21 us for 32 parts).
+// one warp to a row of the join (21 us for 32 parts); pages marked as the first to leave L2 (no change).
 //
 // All waits are bounded; on expiry the CTA stops and drains its copies.
 #include "kv4.cuh"
@@ -87,6 +89,7 @@ struct Args {
   int R, H_q, G, L_max, f16;
   int test_no_load;
   float c2;           // softmax_scale * log2 e
+  float inv_G;
 };
 
 struct Item {
@@ -171,15 +174,22 @@ __device__ __forceinline__ void request_rows(const Args& a, int b, int& r0, int&
 }
 
 // Rows and farthest visible position of the request that each lane names (b < B, or none), by a
-// whole warp: requests of more than eight rows are read by all lanes together.
+// whole warp: requests of more than eight rows are read by all lanes together.  Row b's length is
+// asked for beside the offsets: of a batch of single tokens it is the one.
 __device__ __forceinline__ void request_info(const Args& a, int b, int reach, int lane, int& r0, int& n, int& len, bool& bad) {
   r0 = n = len = 0;
-  if (b >= 0 && b < a.c.B) request_rows(a, b, r0, n);
+  int guess = 0;
+  if (b >= 0 && b < a.c.B) {
+    if (b < a.R) guess = a.row_len[b];
+    request_rows(a, b, r0, n);
+  }
   auto see = [&](int l) {
     bad |= l < 0 || l > reach;
     return min(max(l, 0), reach);
   };
-  if (n <= 8)
+  if (n == 1 && r0 == b)
+    len = see(guess);
+  else if (n <= 8)
     for (int i = 0; i < n; ++i) len = max(len, see(a.row_len[r0 + i]));
   uint32_t big = __ballot_sync(0xffffffffu, n > 8);
   while (big) {
@@ -193,9 +203,19 @@ __device__ __forceinline__ void request_info(const Args& a, int b, int reach, in
   }
 }
 
-// x / y of what hardly ever passes 32 bits, x >= 0, y > 0.
+// x / y of what hardly ever passes 22 bits, x >= 0, y > 0: by the approximate inverse, off by less than one then.  (The
+// divisions of the loading warp stand between the launch and the first load.)
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  return x < (int64_t(1) << 32) && y < (int64_t(1) << 32) ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+  if (x >= 1 << 22 || y >= 1 << 22) return x / y;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"((float)(int)y));
+  const int q = (int)((float)(int)x * inv), rest = (int)x - q * (int)y;
+  return q + (rest >= (int)y) - (rest < 0);
+}
+// pk / G (pk below 2^23, and the inverse within 2^-24 of it).
+__device__ __forceinline__ int row_of(const Args& a, int pk) {
+  const int q = (int)((float)pk * a.inv_G), rest = pk - q * a.G;
+  return q + (rest >= a.G) - (rest < 0);
 }
 
 __device__ __forceinline__ int blocks_of(const Args& a, int n, int rows) { return (n * a.G + rows - 1) / rows; }
@@ -276,20 +296,30 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
     int base = 0, x = 0, r0 = 0, rows = 0, len = 0;    // 32 requests from `base` on, of which x is the next piece's
-    int64_t total = 0;
+    int64_t total = 0, units = 0, incl = 0;            // a lane's request's, and those up to it
+    auto add_up = [&]() {
+      units = units_of(rows, len);
+      incl = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+    };
     if (few) {
       request_info(a, lane, reach, lane, r0, rows, len, bad);
       raise_bad();
-      total = units_of(rows, len);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      add_up();
+      total = __shfl_sync(0xffffffffu, incl, 31);
     } else {
       for (int w = 0; w <= kWarps; ++w) total += sh->units[w];
     }
-    // (at least two stages to a share: the two halves of the warps take one each)
+    // (at least two stages to a share: the two halves of the warps take one each; the first `more`
+    // shares have one unit more than the others)
     const int64_t shares = min((total + 1) / 2, (int64_t)gridDim.x);
-    const int64_t lo = blockIdx.x < shares ? quotient(total * blockIdx.x, shares) : 0;
-    int64_t left = blockIdx.x < shares ? quotient(total * (blockIdx.x + 1), shares) - lo : 0;
+    const int64_t per_share = shares > 0 ? quotient(total, shares) : 0, more = total - per_share * shares;
+    const int64_t lo = per_share * blockIdx.x + min((int64_t)blockIdx.x, more);
+    int64_t left = blockIdx.x < shares ? per_share + (blockIdx.x < more) : 0;
     int n = 0, k = 0;             // stages and items handed over
     bool ok = true;
     Kv4Join join = {};
@@ -301,15 +331,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         while (u >= sh->units[w]) u -= sh->units[w++];
         base = w * per;
         request_info(a, base + lane, reach, lane, r0, rows, len, bad);
+        add_up();
       }
       for (;;) {
-        const int64_t units = units_of(rows, len);
-        int64_t incl = units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += t;
-        }
         const uint32_t hit = __ballot_sync(0xffffffffu, u < incl);
         if (hit) {
           x = __ffs(hit) - 1;
@@ -319,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         u -= __shfl_sync(0xffffffffu, incl, 31);
         base += 32;
         request_info(a, base + lane, reach, lane, r0, rows, len, bad);
+        add_up();
       }
       int64_t at = lo;            // units before the next piece
       while (left > 0 && ok) {
@@ -336,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           continue;
         }
         const int64_t idx = quotient(u, st + kItemCost);
-        const int u0 = (int)(u - idx * (st + kItemCost)), rb = (int)idx / a.c.H_kv, h = (int)idx - rb * a.c.H_kv;   // (below 2^23: 65535 rows of 128 heads)
+        const int u0 = (int)(u - idx * (st + kItemCost)), rb = (int)quotient(idx, a.c.H_kv), h = (int)idx - rb * a.c.H_kv;   // (below 2^23: 65535 rows of 128 heads)
         const int take = (int)min((int64_t)(st + kItemCost - u0), left);
         const int s0 = max(u0 - kItemCost, 0), cnt = u0 + take - kItemCost - s0;   // its stages
         const int64_t end = at - u0 + st + kItemCost;                              // the item's last unit and one
@@ -354,15 +379,15 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         int next = entry(s0 * npp + lane);
         const int row = rb * ROWS + lane;
         const bool live = lane < ROWS && row < xn * a.G;
-        const int sees = live ? a.row_len[xr + row / a.G] : 0;
+        const int sees = live ? a.row_len[xr + row_of(a, row)] : 0;
         const int i = lane >> 2, j = lane & 3;
         uint4 w[NB][GK][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int pk = rb * ROWS + nb * kBlock + i;
           const bool valid = pk < xn * a.G;
-          const uint16_t* q = a.q + (int64_t)(xr + (valid ? pk / a.G : 0)) * a.q_stride +
-                              (int64_t)(h * a.G + (valid ? pk % a.G : 0)) * DK + 16 * j;
+          const int to = valid ? row_of(a, pk) : 0;
+          const uint16_t* q = a.q + (int64_t)(xr + to) * a.q_stride + (int64_t)(h * a.G + (valid ? pk - to * a.G : 0)) * DK + 16 * j;
 #pragma unroll
           for (int g = 0; g < GK; ++g)
 #pragma unroll
@@ -454,8 +479,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
         if (lane == 0) mbar_arrive(bar(sh->ifull[k % kItems]));
         ++k;
         for (int z = 1; z < load && ok; ++z) ok = issue(z);
-        if (!whole && s0 == 0)    // the item's other parts: as many shares as begin before its end
-          join = Kv4Join{xr, xn * a.G, rb * ROWS, h, (int)(quotient(end * shares + total - 1, total) - blockIdx.x), {0, 0, 0}};
+        if (!whole && s0 == 0) {  // the item's other parts: as many shares as begin before its end
+          const int64_t longer = more * (per_share + 1);
+          const int64_t begun = end <= longer ? quotient(end + per_share, per_share + 1) : more + quotient(end - longer + per_share - 1, per_share);
+          join = Kv4Join{xr, xn * a.G, rb * ROWS, h, (int)(begun - blockIdx.x), {0, 0, 0}};
+        }
       }
     }
     if (ok && k >= kItems) ok = wait_bar_warp(bar(sh->ifree[k % kItems]), (k / kItems - 1) & 1, wc);
@@ -798,7 +826,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
             v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
           }
           if (it.slot < 0) {
-            const int64_t rh = (int64_t)(it.row0 + pk / a.G) * a.H_q + it.h * a.G + pk % a.G;
+            const int to = row_of(a, pk);
+            const int64_t rh = (int64_t)(it.row0 + to) * a.H_q + it.h * a.G + pk - to * a.G;
             const float inv = any ? 1.f / sum : 0.f;
             auto pack = [&](float x, float y) { return a.f16 ? pack16<true>(x, y) : pack16<false>(x, y); };
             *reinterpret_cast<uint2*>(a.out + rh * DV + 4 * lane) =
@@ -819,9 +848,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 }
 
 // Joins the parts of the items that CTA i of the attention began and others ended: four warps to
-// a row, each a quarter of the parts with up to eight of them in flight (one warp to a row walked
-// its parts at one load's latency each: 21 us for 32 parts).
+// a row, each a quarter of the parts with up to ten of them in flight (one warp to a row walked
+// its parts at one load's latency each: 21 us for 32 parts; with eight in flight 307200 positions
+// took 0.7 us longer, with twelve one token over 4096 0.5).
 constexpr int kJoinRows = 2;   // of a CTA
+constexpr int kJoinLoads = 10;
 
 template <int DV, bool F16>
 __global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_constant__ Args a, int rows, int ctas) {
@@ -846,6 +877,17 @@ __global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_
   if (jn.parts == 0) return;
   float M = -INFINITY, L = 0.f, acc[E] = {};
   if (pk < jn.packed) {
+    // The first of its parts, under way while the maxima are compared.
+    float v[kJoinLoads][E];
+    auto load = [&](int first, int n) {
+#pragma unroll
+      for (int z = 0; z < kJoinLoads; ++z) {
+        const float* p = a.part + (int64_t)slot(first + 4 * min(z, n - 1)) * DV + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[z][e] = p[e];
+      }
+    };
+    if (w < jn.parts) load(w, (jn.parts - w + 3) / 4);
     for (int x = w + 4 * lane; x < jn.parts; x += 128) {
       const float2 v = x < 128 ? early : a.ml[slot(x)];
       if (v.y != 0.f) M = fmaxf(M, v.x);
@@ -861,16 +903,10 @@ __global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_
         L = fmaf(f, v.y, L);
       }
       const int n = min((jn.parts - base + 3) / 4, 32);
-      for (int y = 0; y < n; y += 8) {
-        float v[8][E];
+      for (int y = 0; y < n; y += kJoinLoads) {
+        if (base != w || y > 0) load(base + 4 * y, n - y);
 #pragma unroll
-        for (int z = 0; z < 8; ++z) {
-          const float* p = a.part + (int64_t)slot(base + 4 * min(y + z, n - 1)) * DV + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[z][e] = p[e];
-        }
-#pragma unroll
-        for (int z = 0; z < 8; ++z) {
+        for (int z = 0; z < kJoinLoads; ++z) {
           const float g = __shfl_sync(0xffffffffu, f, (y + z) & 31);
           if (y + z < n)
 #pragma unroll
@@ -906,7 +942,8 @@ __global__ void __launch_bounds__(128 * kJoinRows) kv4_join_kernel(const __grid_
     for (int e = 0; e < E; ++e) acc[e] = fmaf(f, sums[warp >> 2][x][lane * E + e], acc[e]);
   }
   const float inv = any ? 1.f / L : 0.f;
-  const int64_t rh = (int64_t)(jn.row0 + pk / a.G) * a.H_q + jn.head * a.G + pk % a.G;
+  const int to = row_of(a, pk);
+  const int64_t rh = (int64_t)(jn.row0 + to) * a.H_q + jn.head * a.G + pk - to * a.G;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + rh * DV + lane * E);
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) dst[e] = any ? pack16<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
@@ -985,6 +1022,7 @@ cudaError_t launch_kv4_attn(const dsa_kv4_cache& c, const CacheArgs& ca, const d
   a.wait_ns = hooks ? hooks->wait_ns : kDefaultWaitNs;
   a.test_no_load = hooks ? hooks->tile_no_load : 0;
   a.R = p.R; a.H_q = p.H_q; a.G = p.H_q / c.H_kv; a.L_max = p.L_max;
+  a.inv_G = 1.f / (float)a.G;
   a.c2 = (float)(p.softmax_scale * 1.4426950408889634);
   a.f16 = (p.flags & DSA_FLAG_FP16) != 0;
   if (c.D_k == 64) return launch_width<64, 64>(a, s.rows, s.grid, st);
