@@ -9,18 +9,19 @@
 //
 // Borders.  A key that was normed or rotated is off by some 2^-20 in fp32, so near the border
 // between two codes (or two scales) fp32 cannot tell which one exact arithmetic gives.  Each
-// head has a bound of its values' errors; where a border lies within it, the value is computed
-// again in fp64 (about one head in 150), at the end of the CTA's work, so that the common path
-// keeps its registers.  What the cache holds then does not depend on how sums were ordered.  Values
+// head has a bound of its values' errors; where a border lies within it (one head in 200), each value's own
+// bound is looked at, and where that leaves it open (one head in 500) the value is computed again in
+// fp64, after the warp's run of heads, so that the common path keeps its registers.  What the
+// cache holds then does not depend on how sums were ordered.  Values
 // that are neither normed nor rotated are quantised exactly: x has at most 11 significant bits
 // and a scale 4, so a quotient is a half or well off one.
 //
 // Read.  code * scale, 8 bytes of codes of a lane to 32 bytes of values, by packed products that
 // are exact in bf16 (kv4_widen.cuh).
 //
-// Both move each byte once.  Measured: 9601 rows of 8 + 8 heads of 128 appended in 35 us (1.4 TB/s:
-// 22 million warp instructions, 45% of the issue slots; the quantising of keys, 225 instructions
-// for two heads, is most of it), a prefix of 10240 positions read in 13 us (4 TB/s; a wave of CTAs
+// Both move each byte once.  Measured: 9601 rows of 8 + 8 heads of 128 appended in 32 us (1.6 TB/s:
+// 22 million warp instructions, half of the issue slots; the quantising of keys, 225 instructions
+// for two heads, is most of it; 5 us are the last heads computed again), a prefix of 10240 positions read in 13 us (4 TB/s; a wave of CTAs
 // that look up, load and write in step), 8000 positions of 64 heads of 192 + 128 in 71 us
 // (5.9 TB/s).  Prefetching the rows into L2 at the start gained 1 us.
 #include "kv4_widen.cuh"
@@ -38,21 +39,17 @@ constexpr float kTurnErr = 20.f * 0x1p-24f;
 
 // max / 7 to four significant bits, ties to even; below 2^-126: 0.  From the product with the rounded
 // 1 / 7, whose first four bits may be one too few; on which side of the border above them max / 7
-// lies is then told exactly, by seven times the border (five significant bits).
-__device__ __forceinline__ float group_scale(float top) {
+// lies is then told exactly, by seven times the border (five significant bits).  `exact`: the same
+// maximum, or what fp64 makes of it (the four bits may then also be one too many, just below max / 7's
+// own: no border lies between).
+template <typename T>
+__device__ __forceinline__ float group_scale(float top, T exact) {
   const uint32_t base = __float_as_uint(top * (1.f / 7.f)) & ~0xfffffu;
-  const float border = 7.f * __uint_as_float(base | 0x80000u);
-  const bool up = top > border || (top == border && (base >> 20 & 1u));
+  const T border = 7.f * __uint_as_float(base | 0x80000u);
+  const bool up = exact > border || (exact == border && (base >> 20 & 1u));
   float scale = __uint_as_float(up ? base + 0x100000u : base);
-  if (top < 0x1.cp-124f) scale = top >= 0x1.b2p-124f ? 0x1p-126f : 0.f;      // 7, and 7 * 31 / 32, times 2^-126
+  if (top < 0x1.cp-124f) scale = exact >= T(0x1.b2p-124) ? 0x1p-126f : 0.f;  // 7, and 7 * 31 / 32, times 2^-126
   return top <= 3.4028234e38f ? scale : __uint_as_float(0x7fc00000u);        // (a group that is not finite)
-}
-// x >= 0 to four significant bits, in the same way.
-__device__ __forceinline__ double four_bits(double x) {
-  if (x < 0x1p-126) return x >= 0x1.fp-127 ? 0x1p-126 : 0.0;
-  const uint64_t u = (uint64_t)__double_as_longlong(x);
-  if (u >= 0x7ff0000000000000ull) return __longlong_as_double(0x7ff8000000000000ll);
-  return __longlong_as_double((long long)((u + 0xffffffffffffull + ((u >> 49) & 1ull)) & ~0x1ffffffffffffull));
 }
 
 // A code, x / scale to the nearest whole number and 8, in the low bits of 12582920 + x / scale (1.5 * 2^23 + 8:
@@ -126,8 +123,28 @@ __device__ __forceinline__ bool group_turned(const TurnArgs& t, int d) {
   return t.k_weight || (t.rot > 0 && t.first < g + 64 && t.first + t.rot > g);
 }
 
+// Column d of the head at `x`, normed by the factor r and rotated, in fp64.
+template <bool F16>
+__device__ __noinline__ double turned_exactly(const TurnArgs& t, const uint16_t* x, double r, int pos, int d) {
+  auto value = [&](int d) {
+    const double v = to_float<F16>(x[d]);
+    return t.k_weight ? v * (double)to_float<F16>(t.k_weight[d]) : v;
+  };
+  const int c = d - t.first;
+  if (c < 0 || c >= t.rot) return value(d) * r;
+  const int half = t.rot / 2;
+  const bool second = t.adjacent ? c & 1 : c >= half;
+  const int f = t.adjacent ? c >> 1 : (second ? c - half : c);
+  const double v = value(d), p = value(t.first + (t.adjacent ? c ^ 1 : (second ? c - half : c + half)));
+  const double2 cs = cos_sin_exactly(turn_fraction(t.inv_freq[f]) * (uint64_t)(int64_t)pos);
+  return (second ? v * cs.x + p * cs.y : v * cs.x - p * cs.y) * r;
+}
+
 // The same with what fp32 leaves open computed in fp64 from the head at `x` (null: the lane has none):
 // the largest values of a group whose scale is open, then the columns next to a border.  Whole warp.
+// It runs seldom, so its time is that of its code's way into the SM and of a chain of fp64 operations, two a cycle
+// and SM: as few of them as may be, and no division, square root or library function (with those a head
+// took 7 us, and 9601 rows 35).
 template <int D, bool F16>
 __device__ __noinline__ Held hold_exactly(const TurnArgs& t, const float2* cs, const uint16_t* x, int pos, int lane) {
   const HeadLane l = head_lane<D>(t, lane % kHeadLanes<D>);
@@ -137,27 +154,28 @@ __device__ __noinline__ Held hold_exactly(const TurnArgs& t, const float2* cs, c
   unpack4<F16>(live ? load4(x, l.b) : make_uint2(0, 0), y + 4);
   double r = 1.0;
   if (t.k_weight) {
-    double s = 0.0;
+    // (squares of 11 bits are exact in fp32, and so is what each sum is off by: low holds these)
+    float high = 0.f, low = 0.f;
+    auto add = [&](float x) {
+      const float sum = high + x, part = sum - high;
+      low += (high - (sum - part)) + (x - part);
+      high = sum;
+    };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fma((double)y[i], (double)y[i], s);
-    for (int o = kHeadLanes<D> / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    r = 1.0 / sqrt(s * (1.0 / D) + (double)t.eps);   // (D = 192: 1 / D is off by 2^-54 of it)
+    for (int i = 0; i < 8; ++i) add(y[i] * y[i]);
+#pragma unroll
+    for (int o = kHeadLanes<D> / 2; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(0xffffffffu, high, o);
+      low += __shfl_xor_sync(0xffffffffu, low, o);
+      add(x);
+    }
+    const double s = fma((double)high + (double)low, 1.0 / D, (double)t.eps);   // (D = 192: 1 / D is off by 2^-54 of it)
+    // s r^2 = 1 - e: r / sqrt(1 - e), and e is below 2^-21.
+    r = (double)rsqrtf((float)s);
+    const double e = fma(-s * r, r, 1.0);
+    r = fma(r * e, fma(0.375, e, 0.5), r);
   }
   turn_head<D>(t, t.k_weight != nullptr, l, lane_turn<F16>(cs, t.k_weight, l), y);
-  auto value = [&](int d) {
-    const double v = to_float<F16>(x[d]);
-    return t.k_weight ? v * r * (double)to_float<F16>(t.k_weight[d]) : v;
-  };
-  auto exactly = [&](int i) {
-    const int d = i < 4 ? l.a + i : l.b + i - 4, c = d - t.first;
-    if (c < 0 || c >= t.rot) return value(d);
-    const int half = t.rot / 2;
-    const bool second = t.adjacent ? c & 1 : c >= half;
-    const int f = t.adjacent ? c >> 1 : (second ? c - half : c);
-    const double v = value(d), p = value(t.first + (t.adjacent ? c ^ 1 : (second ? c - half : c + half)));
-    const double2 cs = cos_sin_exactly(turn_fraction(t.inv_freq[f]) * (uint64_t)(int64_t)pos);
-    return second ? v * cs.x + p * cs.y : v * cs.x - p * cs.y;
-  };
   auto four = [&](const float* v) { return max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))); };
   float top[2] = {0.f, 0.f}, scale[2];
   const float all = group_max<D>(l, four(y), four(y + 4), top[0], top[1]);
@@ -165,28 +183,55 @@ __device__ __noinline__ Held hold_exactly(const TurnArgs& t, const float2* cs, c
   const float e = exact ? 0.f : 2.f * kTurnErr * all;
   double most[2] = {0.0, 0.0}, most_of[2] = {0.0, 0.0};
   bool open[2];
+#pragma unroll
   for (int v = 0; v < 2; ++v) {
-    scale[v] = group_scale(top[v]);
+    scale[v] = group_scale(top[v], top[v]);
     open[v] = scale[v] == scale[v] && group_turned(t, v ? l.b : l.a) && open_scale(top[v], e);
-    if (!open[v] || !live) continue;
-    for (int i = 4 * v; i < 4 * v + 4; ++i)
-      if (fabsf(y[i]) >= top[v] - 2.f * e) most[v] = fmax(most[v], fabs(exactly(i)));
   }
-  // (an open group is open for all its lanes)
-  group_max<D>(l, most[0], most[1], most_of[0], most_of[1]);
-  Held h;
-  for (int v = 0; v < 2; ++v) {
-    if (open[v]) scale[v] = (float)four_bits(most_of[v] / 7.0);
-    const float inv = inverse(scale[v]), border = open_code(turned ? e : 0.f, inv);
-    float c[4];
-    for (int i = 0; i < 4; ++i) {
-      const float x = y[4 * v + i];
-      c[i] = turned ? code(x, inv) : code_exactly(x, inv);
-      if (turned && live && fabsf(fmaf(x, inv, kCode - c[i])) > border && scale[v] > 0.f)
-        c[i] = kCode + (float)rint(exactly(4 * v + i) / (double)scale[v]);
+  if (__any_sync(0xffffffffu, open[0] || open[1])) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int v = i >> 2;
+      if ((v ? open[1] : open[0]) && live && fabsf(y[i]) >= (v ? top[1] : top[0]) - 2.f * e) {
+        const double x0 = fabs(turned_exactly<F16>(t, x, r, pos, (v ? l.b : l.a) + (i & 3)));
+        most[v] = fmax(most[v], x0);
+      }
     }
-    h.codes[v] = pack_codes(c);
+    // (an open group is open for all its lanes)
+    group_max<D>(l, most[0], most[1], most_of[0], most_of[1]);
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      if (open[v]) scale[v] = group_scale(top[v], most_of[v]);
+  }
+  Held h;
+  uint32_t left = 0;                                 // columns next to a border
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float inv = inverse(scale[v]), border = open_code(e, inv);
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = y[4 * v + i];
+      c[i] = turned ? code(x0, inv) : code_exactly(x0, inv);
+      if (turned && live && fabsf(fmaf(x0, inv, kCode - c[i])) > border && scale[v] > 0.f) left |= 1u << (4 * v + i);
+    }
+    h.codes[v] = pack_codes(c) & 0xffffu;
     h.scale[v] = scale[v];
+  }
+  while (__any_sync(0xffffffffu, left)) {
+    if (left) {
+      // fp32's code is at most one off: what it leaves of the value, against half a scale.
+      const int i = __ffs(left) - 1, at = 4 * (i & 3);
+      left &= left - 1;
+      const uint32_t codes = i < 4 ? h.codes[0] : h.codes[1];
+      const int k = (int)(codes >> at & 15u) - 8;
+      const float sc = i < 4 ? scale[0] : scale[1];
+      const double half = 0.5 * (double)sc;
+      const double rest = fma((double)-k, (double)sc, turned_exactly<F16>(t, x, r, pos, (i < 4 ? l.a : l.b) + (i & 3)));
+      const int up = (rest > half || (rest == half && (k & 1))) - (rest < -half || (rest == -half && (k & 1)));
+      if (i < 4) h.codes[0] += up << at;
+      else h.codes[1] += up << at;
+    }
   }
   return h;
 }
@@ -204,7 +249,7 @@ __device__ __forceinline__ bool hold_key(const TurnArgs& t, const float* x, cons
   bool open = false;
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
-    const float scale = group_scale(top[v]), inv = inverse(scale);
+    const float scale = group_scale(top[v], top[v]), inv = inverse(scale);
     open |= group_turned(t, v ? l.b : l.a) && open_scale(top[v], e);
     float c[4], d[4];
 #pragma unroll
@@ -224,6 +269,30 @@ __device__ __forceinline__ bool hold_key(const TurnArgs& t, const float* x, cons
   return !open;
 }
 
+// What hold_key leaves open with a bound for the whole head, looked at with each value's own: 19.5 units times
+// the magnitudes of its pair before the rotation, which add up to at most sqrt 2 times those after it.
+template <int D>
+__device__ __noinline__ bool still_open(const TurnArgs& t, float4 xa, float4 xb, HeadLane l, float2 scale) {
+  const float x[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+  auto four = [&](const float* v) { return max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))); };
+  float top[2] = {0.f, 0.f};
+  const float e = 2.f * kTurnErr * group_max<D>(l, four(x), four(x + 4), top[0], top[1]);
+  bool open = false;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float inv = inverse(v ? scale.y : scale.x);
+    open |= group_turned(t, v ? l.b : l.a) && open_scale(top[v], e);
+    if (!t.k_weight && l.f < 0) continue;
+#pragma unroll
+    for (int i = 4 * v; i < 4 * v + 4; ++i) {
+      const float pair = fabsf(x[i]) + fabsf(t.adjacent ? x[i ^ 1] : x[i ^ 4]);
+      const float own = l.f >= 0 ? 1.42f * kTurnErr * pair : kTurnErr * fabsf(x[i]);
+      open |= fabsf(fmaf(x[i], inv, kCode - code(x[i], inv))) > open_code(own, inv);
+    }
+  }
+  return open;
+}
+
 // A lane's part of a key into its head's block.
 template <int DK, int DV>
 __device__ __forceinline__ void put_key(const CacheArgs& c, uint8_t* to, int place, const HeadLane& l, const Held& held) {
@@ -236,17 +305,11 @@ __device__ __forceinline__ void put_key(const CacheArgs& c, uint8_t* to, int pla
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// What fp32 left open: rows of the CTA (i << 8) and first heads of a round.
-struct Open {
-  int n;
-  uint16_t at[kTurnRows * 128];
-};
-
 // A run of one row's keys into its page, by one warp.
 template <int DK, int DV, bool F16>
-__device__ __forceinline__ void append_keys(const TurnArgs& t, const CacheArgs& c, const float2* cs, Open& open, int64_t page,
-                                            int row, int i, int run, int lane) {
-  const int place = t.positions[row] & (c.ps - 1);
+__device__ __forceinline__ void append_keys(const TurnArgs& t, const CacheArgs& c, const float2* cs, int64_t page, int row,
+                                            int run, int lane) {
+  const int pos = t.positions[row], place = pos & (c.ps - 1);
   constexpr int L = kHeadLanes<DK>, S = 32 / L;
   int h0, h1;
   run_heads(t, c.H_kv, run, h0, h1);
@@ -255,7 +318,8 @@ __device__ __forceinline__ void append_keys(const TurnArgs& t, const CacheArgs& 
   const uint16_t* src = t.k + row * t.k_stride + (h0 + sub) * DK;
   uint8_t* dst = c.pages + page + (uint32_t)(h0 + sub) * c.block;
   const LaneTurn turns = lane_turn<F16>(cs, t.k_weight, l);
-  const int rounds = (h1 - h0 + S - 1) / S;
+  const int rounds = (h1 - h0 + S - 1) / S;     // (at most 8)
+  uint32_t opens = 0;          // rounds that fp32 left open
   for (int first = 0; first < rounds; first += 4) {
     uint2 v[4][2];             // (four rounds' loads under way together)
 #pragma unroll
@@ -277,10 +341,18 @@ __device__ __forceinline__ void append_keys(const TurnArgs& t, const CacheArgs& 
       }
       turn_head<DK>(t, t.k_weight != nullptr, l, turns, x);
       Held held;
-      if (__any_sync(0xffffffffu, !hold_key<DK>(t, x, l, held) && live) && lane == 0)
-        open.at[atomicAdd(&open.n, 1)] = (uint16_t)(i << 8 | (h0 + n * S));
+      if (__any_sync(0xffffffffu, !hold_key<DK>(t, x, l, held) && live) &&
+          __any_sync(0xffffffffu, still_open<DK>(t, make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), l,
+                                                 make_float2(held.scale[0], held.scale[1])) && live))
+        opens |= 1u << n;
       if (live) put_key<DK, DV>(c, dst + n * S * c.block, place, l, held);
     }
+  }
+  for (; opens; opens &= opens - 1) {
+    const int n = __ffs(opens) - 1;
+    const bool live = h0 + n * S + sub < h1 && l.a >= 0;
+    const Held held = hold_exactly<DK, F16>(t, cs, live ? src + n * S * DK : nullptr, pos, lane);
+    if (live) put_key<DK, DV>(c, dst + n * S * c.block, place, l, held);
   }
 }
 
@@ -313,7 +385,7 @@ __device__ __forceinline__ void append_values(const TurnArgs& t, const CacheArgs
                           max_nan(max_nan(fabsf(x[4]), fabsf(x[5])), max_nan(fabsf(x[6]), fabsf(x[7]))));
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float scale = group_scale(top), inv = inverse(scale);
+      const float scale = group_scale(top, top), inv = inverse(scale);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = code_exactly(x[i], inv);
       if (base + u * S + sub < h1) {
@@ -330,7 +402,7 @@ template <int DK, int DV, bool F16>
 __global__ void __launch_bounds__(kTurnThreads, 4) kv4_append_kernel(const __grid_constant__ TurnArgs t, const __grid_constant__ CacheArgs c, uint32_t* status) {
   __shared__ RowTurns cs;
   __shared__ int64_t pages[kTurnRows];             // a row's page; -1: outside the pool, -2: the row is skipped
-  __shared__ Open open;
+  __shared__ int next;                             // unit that the next warp to be through takes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, runs = t.q_runs + t.k_runs + t.v_runs;
   int row0, u0, u1;
   cta_units(t, runs, row0, u0, u1);
@@ -341,7 +413,7 @@ __global__ void __launch_bounds__(kTurnThreads, 4) kv4_append_kernel(const __gri
     for (int x = lane; x < c.H_kv * (DK / 64); x += 32) prefetch_l2(k + 64 * x);
     for (int x = lane; x < c.H_kv * (DV / 64); x += 32) prefetch_l2(v + 64 * x);
   }
-  if (threadIdx.x == 0) open.n = 0;
+  if (threadIdx.x == 0) next = u0 + kTurnThreads / 32;
   if (warp >> t.rows_log2 == 0) {
     int64_t page = -2;
     if (row0 + warp < t.R) {
@@ -358,7 +430,8 @@ __global__ void __launch_bounds__(kTurnThreads, 4) kv4_append_kernel(const __gri
   }
   row_turns(t, cs, row0);
   __syncthreads();
-  for (int u = u0 + warp; u < u1; u += kTurnThreads / 32) {
+  // Keys come before values, and a warp that has to look at a head again leaves the rest to the others.
+  for (int u = u0 + warp; u < u1; u = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(&next, 1) : 0, 0)) {
     const int run = u >> t.rows_log2, i = u - (run << t.rows_log2), row = row0 + i;
     const int64_t page = pages[i];
     if (page == -2) continue;
@@ -368,19 +441,10 @@ __global__ void __launch_bounds__(kTurnThreads, 4) kv4_append_kernel(const __gri
       turn_row<DK, F16>(t, t.q_weight, cs[i], t.q + row * t.q_stride, t.q_out + row * t.q_out_stride, h0, h1, lane);
     } else if (page >= 0) {
       if (run < t.q_runs + t.k_runs)
-        append_keys<DK, DV, F16>(t, c, cs[i], open, page, row, i, run - t.q_runs, lane);
+        append_keys<DK, DV, F16>(t, c, cs[i], page, row, run - t.q_runs, lane);
       else
         append_values<DK, DV, F16>(t, c, page, row, run - t.q_runs - t.k_runs, lane);
     }
-  }
-  __syncthreads();                                 // (the keys that are written again are written by then)
-  for (int x = warp; x < open.n; x += kTurnThreads / 32) {
-    constexpr int L = kHeadLanes<DK>;
-    const int i = open.at[x] >> 8, row = row0 + i, h = (open.at[x] & 255) + lane / L, pos = t.positions[row];
-    const HeadLane l = head_lane<DK>(t, lane % L);
-    const bool live = h < c.H_kv && l.a >= 0;
-    const Held held = hold_exactly<DK, F16>(t, cs[i], live ? t.k + row * t.k_stride + h * DK : nullptr, pos, lane);
-    if (live) put_key<DK, DV>(c, c.pages + pages[i] + (uint32_t)h * c.block, pos & (c.ps - 1), l, held);
   }
   if (threadIdx.x == 0) pdl_wait();                // (whoever waits for this grid's end waits for its predecessors' too)
 }

@@ -60,10 +60,24 @@ __device__ __forceinline__ float2 cos_sin(uint64_t fraction) {
   const float a = q & 1 ? s : c, b = q & 1 ? c : s;                           // cos, sin up to their signs
   return make_float2((q + 1) & 2 ? -a : a, q & 2 ? -b : b);
 }
+// The same in fp64 by the series up to y^17 and y^16, below 2^-50 off (a library function's code is longer, and this is
+// code that an SM runs once).
 __device__ __forceinline__ double2 cos_sin_exactly(uint64_t fraction) {
-  double2 cs;
-  sincospi((double)(int64_t)fraction * 0x1p-63, &cs.y, &cs.x);
-  return cs;
+  const uint32_t q = (uint32_t)((fraction + (1ull << 61)) >> 62);
+  const double y = (double)(int64_t)(fraction - ((uint64_t)q << 62)) * 3.40612158008655459e-19;   // 2 pi / 2^64
+  const double z = -y * y;
+  // (over (2 i + 1)! and (2 i)!)
+  constexpr double over[9] = {1.0, 1.0 / 2, 1.0 / 24, 1.0 / 720, 1.0 / 40320, 1.0 / 3628800, 1.0 / 479001600, 1.0 / 87178291200.0,
+                              1.0 / 20922789888000.0};
+  double s = over[8] / 17, c = over[8];
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    s = fma(z, s, over[i] / (2 * i + 1));
+    c = fma(z, c, over[i]);
+  }
+  s *= y;
+  const double a = q & 1 ? s : c, b = q & 1 ? c : s;
+  return make_double2((q + 1) & 2 ? -a : a, q & 2 ? -b : b);
 }
 
 struct HeadLane {
