@@ -807,7 +807,8 @@ dsa_status dsa_kv4_append(const dsa_kv4_cache* c, const dsa_qk_problem* p, uint1
                 p->D_v, p->B, c->H_kv, c->D_k, c->D_v, c->B);
   if (p->R > 0 && (!p->k || !p->v || !p->row_offsets)) return fail(DSA_ERR_INVALID_ARG, "k/v/row_offsets must be set");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_clear_status(ws, st);
+  cudaError_t e = cudaSuccess;
+  if (!kv4_sets_status(p->R)) e = launch_clear_status(ws, st);
   if (e != cudaSuccess) return cuda_fail(e, "clear status");
   if (p->R == 0) return DSA_OK;
   e = launch_kv4_append(a, ca, c->D_k, c->D_v, p->flags & DSA_FLAG_FP16, static_cast<uint32_t*>(ws), st);
@@ -829,9 +830,11 @@ dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t* row_of
     return fail(DSA_ERR_INVALID_ARG, "row_offsets and positions must be 4-byte aligned");
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(DSA_ERR_INVALID_ARG, "k_out/v_out must be 16-byte aligned");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_clear_status(ws, st);
+  cudaError_t e = cudaSuccess;
+  const bool nothing = R == 0 || (!k_out && !v_out);
+  if (nothing || !kv4_sets_status(R)) e = launch_clear_status(ws, st);
   if (e != cudaSuccess) return cuda_fail(e, "clear status");
-  if (R == 0 || (!k_out && !v_out)) return DSA_OK;
+  if (nothing) return DSA_OK;
   e = launch_kv4_read(ca, R, row_offsets, positions, c->D_k, c->D_v, flags & DSA_FLAG_FP16, k_out, v_out,
                       static_cast<uint32_t*>(ws), st);
   if (e != cudaSuccess) return cuda_fail(e, "read of the 4-bit cache");

@@ -34,6 +34,8 @@ struct CacheArgs {
 };
 
 cudaError_t launch_qk_norm_rope(TurnArgs a, int D, bool f16, cudaStream_t st);
+// Whether the next two set the status block for that many rows; they need it cleared where not.
+bool kv4_sets_status(int R);
 cudaError_t launch_kv4_append(TurnArgs a, const CacheArgs& c, int D_k, int D_v, bool f16, uint32_t* status, cudaStream_t st);
 cudaError_t launch_kv4_read(const CacheArgs& c, int R, const int32_t* row_offsets, const int32_t* positions, int D_k, int D_v,
                             bool f16, uint16_t* k_out, uint16_t* v_out, uint32_t* status, cudaStream_t st);

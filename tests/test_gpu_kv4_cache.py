@@ -230,6 +230,28 @@ def test_skipped_rows_and_bad_places():
     assert (ko[[0, 1, 2, 6]] == 55).all() and not (ko[[3, 4]] == 55).any()
 
 
+@pytest.mark.parametrize("rows", [[1], [200, 0, 56], [1] * 300, [257, 255], [300, 213], [1] * 600])
+def test_status_is_each_calls_own(rows):
+    # (up to 512 rows the call's kernel sets the status, above a launch before clears it)
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    T = sum(rows)
+    a = _append(rows, [3] * len(rows), 1, 1, 64, 64, 16, seed=11)
+    assert a["bits"] == 0
+    ko = torch.empty(T, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for at in sorted({0, T // 2, T - 1}):
+        pos = a["pos"].clone()
+        for value, bits in ((16 * a["table"].shape[1], dsa.DSA_DEVICE_BAD_INDEX), (-1, 0)):
+            pos[at] = value
+            for call in ("append", "read"):
+                a["ws"].fill_(-1 if a["ws"].dtype != torch.uint8 else 255)
+                if call == "append":
+                    dsa.dsa_kv4_append(a["cache"], a["prob"].set(positions=pos.cuda()), a["q_out"], a["ws"])
+                else:
+                    dsa.dsa_kv4_read(a["cache"], a["ro"].cuda(), pos.cuda(), ko, None, a["ws"])
+                assert dsa.dsa_read_device_status(a["ws"]) == bits, (call, at, value)
+
+
 def test_rows_outside_the_requests():
     import torch
     import dsa_sparse_attention_03_gb300 as dsa
