@@ -65,7 +65,7 @@ DSA_API size_t dsa_kv4_block_bytes(int32_t D_k, int32_t D_v, int32_t page_size);
  * Positions of one call name different places: what a place holds that two rows are for is
  * not specified.
  * ws: at least 256 bytes, 256-byte aligned; its status word is set by the call
- * (dsa_read_device_status).  Two kernels, asynchronous on `stream`, no host
+ * (dsa_read_device_status).  One kernel (two from 513 rows on), asynchronous on `stream`, no host
  * synchronisation, capturable in a CUDA graph.  Calls that may overlap need workspaces of
  * their own.  Host validation failures return non-zero and enqueue nothing.
  */
