@@ -21,7 +21,7 @@
 //
 // Both move each byte once.  Measured: 9601 rows of 8 + 8 heads of 128 appended in 32 us (1.6 TB/s:
 // 22 million warp instructions, half of the issue slots; the quantising of keys, 225 instructions
-// for two heads, is most of it; 5 us are the last heads computed again), a prefix of 10240 positions read in 13 us (4 TB/s; a wave of CTAs
+// for two heads, is most of it; 5 us are the last heads computed again), a prefix of 10240 positions read in 13 us (4.1 TB/s; a wave of CTAs
 // that look up, load and write in step), 8000 positions of 64 heads of 192 + 128 in 71 us
 // (5.9 TB/s).  Prefetching the rows into L2 at the start gained 1 us.
 #include "kv4_widen.cuh"
@@ -557,24 +557,28 @@ __global__ void __launch_bounds__(kThreads)
     set_status(c, R, row_offsets, positions, status);
     return;
   }
-  for (int i = warp; i < rows; i += kThreads / 32) {
-    const int64_t row = row0 + i;
-    int64_t page = -1;
-    int pos = -1;
-    if (row < R) {
-      pos = positions[row];
-      const int b = find_request(row_offsets, c.B, (int)row, lane);
-      if (pos >= 0 && b >= 0) {
-        page = find_page(c, b, pos);
-        if (page < 0 && lane == 0 && !own) {
-          pdl_wait();
-          raise_status(status, DSA_DEVICE_BAD_INDEX);
-        }
-      }
+  // (a warp's two rows are looked up together)
+  constexpr int kWarps = kThreads / 32, kOfWarp = kReadRows / kWarps;
+  int pos[kOfWarp], b[kOfWarp];
+#pragma unroll
+  for (int u = 0; u < kOfWarp; ++u) {
+    const int i = warp + u * kWarps;
+    pos[u] = i < rows && row0 + i < R ? positions[row0 + i] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kOfWarp; ++u) b[u] = pos[u] >= 0 ? find_request(row_offsets, c.B, (int)row0 + warp + u * kWarps, lane) : -1;
+#pragma unroll
+  for (int u = 0; u < kOfWarp; ++u) {
+    const int i = warp + u * kWarps;
+    const bool asked = pos[u] >= 0 && b[u] >= 0;
+    const int64_t page = asked ? find_page(c, b[u], pos[u]) : -1;
+    if (asked && page < 0 && lane == 0 && !own) {
+      pdl_wait();
+      raise_status(status, DSA_DEVICE_BAD_INDEX);
     }
-    if (lane == 0) {
+    if (lane == 0 && i < rows) {
       pages[i] = page;
-      places[i] = pos & (c.ps - 1);
+      places[i] = pos[u] & (c.ps - 1);
     }
   }
   __syncthreads();
