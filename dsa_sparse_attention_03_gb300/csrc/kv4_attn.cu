@@ -6,14 +6,17 @@
 //   sum_t p_t V[t] = sum_t (p_t s_g[t]) u - 8 sum_t (p_t s_g[t])      for the columns of group g.
 // The codes go into the products as they are: four bits with zeros around them are the fp16
 // number u 2^-24, and four bits higher up u 2^-20, so a pair of codes becomes a pair of operands
-// by one AND, without a conversion.  K's scales are applied to the logits, V's to the weights,
+// by one AND, without a conversion.  (The tensor core cuts the addends of a sum 24 bits or so below the
+// largest exponent, which for these operands is 2^-14's whatever the code.  K's codes are shifted up by
+// two bits for that: a logit is then off by a tenth, at 1% of the time; lse of one position in
+// fp16 1.2e-6 -> 1.4e-7 of its size.)  K's scales are applied to the logits, V's to the weights,
 // both in fp32.  A query row is scaled by a power of two to fp16's upper range first (every bit
 // of a bf16 query within 2^-25 of the row's largest is kept); the columns whose codes come
 // 2^4 too high get a sixteenth of it.  The products are exact, their sums fp32.
 //
 // Softmax in one pass, base 2: the maximum m only has to be near the row's: O and l are rescaled
-// when it has grown by more than 2^8.  Weights are held as 2^7 of them, and times V's scales
-// relative to a power of two not below any scale so far, so that fp16 holds them to 11 bits
+// when it has grown by more than 2^8.  For their product with V weights are held times V's scales
+// relative to a power of two that leaves these below 2^7, so that fp16 holds them to 11 bits
 // down to 2^-21 of the largest.
 //
 // What bounds it.  Per position and K/V head (D_k + D_v) 17 / 32 bytes have to be read: 136 for
@@ -22,11 +25,11 @@
 // 18 mma.sync for 16 positions, 245 instructions in all with the softmax.  Dequantised tiles in shared
 // memory for tcgen05 would cost the same extraction, a store and two reads of 16-bit
 // operands; registers are what mma.sync takes and tcgen05 does not.  Measured: one token of 64
-// heads over 8 and 307200 positions 61.5 us, 5.4 TB/s with the start (3.6 us until the first stage is
+// heads over 8 and 307200 positions 62 us, 5.4 TB/s with the start (3.6 us until the first stage is
 // there), CTAs that get less of HBM than others and end 6 us after the middle one, and the join (3
 // us); twice as many positions take another 50, the copy rate.  32 ragged tokens of up to 32768
-// positions 79.5 us in pages of 64 (5.3 TB/s), 83.5 in pages of 16, whose copies are 2 KB each.  One
-// token over 4096 positions 10.7 us: a chain of launch, lengths (0.7), the share's place in the batch
+// positions 81 us in pages of 64 (5.2 TB/s), 84.5 in pages of 16, whose copies are 2 KB each.  One
+// token over 4096 positions 10.8 us: a chain of launch, lengths (0.7), the share's place in the batch
 // (0.8), table and first pages (1.5), two tiles of 32 positions (1 to 2), the warps' sums and parts
 // (1.2), the next launch (0.7) and the join.
 //
@@ -80,7 +83,7 @@ struct Args {
   uint16_t* out;
   float* lse;
   float* part;        // [2 grid, rows, D_v]
-  float2* ml;         // [2 grid, rows]: (m - 7, l)
+  float2* ml;         // [2 grid, rows]: (m, l)
   Kv4Join* join;      // or null: no item is split
   uint32_t* status;
   uint32_t* bits;     // status bits of each CTA, for the join; or null: the status is cleared before, and raised
@@ -460,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (j == 0) it->less[g][nb * kBlock + i] = -0x1p-21f * sum;
+            if (j == 0) it->less[g][nb * kBlock + i] = -0x1p-19f * sum;
           }
-          if (j == 0) it->factor[nb * kBlock + i] = a.c2 * (0x1p24f / up);
+          if (j == 0) it->factor[nb * kBlock + i] = a.c2 * (0x1p22f / up);
         }
         if (lane < ROWS) it->see[lane] = live ? min(max(sees, 0), reach) : xl;
         if (lane == 0) {
@@ -584,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                   for (int nb = 0; nb < NB; ++nb) lds2(qf + ((g * NB + nb) * 4 + 2 * w + z) * 256, b[nb][0], b[nb][1]);
 #pragma unroll
                   for (int t = 0; t < 2; ++t) {
-                    const uint32_t a0 = x[t][w] >> (8 * z) & 0x000f000fu, a2 = x[t][w] >> (8 * z) & 0x00f000f0u;
-                    const uint32_t a1 = y[t][w] >> (8 * z) & 0x000f000fu, a3 = y[t][w] >> (8 * z) & 0x00f000f0u;
+                    const uint32_t xs = z ? x[t][w] >> 6 : x[t][w] << 2, ys = z ? y[t][w] >> 6 : y[t][w] << 2;
+                    const uint32_t a0 = xs & 0x003c003cu, a2 = xs & 0x03c003c0u, a1 = ys & 0x003c003cu, a3 = ys & 0x03c003c0u;
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                       if (w + z == 0)
@@ -654,10 +657,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
               for (int g = 0; g < GV; ++g) big = max3(vs[t][g][0], vs[t][g][1], big);
             }
-            if (__any_sync(0xffffffffu, first || top > 15.f || big > 1.f)) {
+            if (__any_sync(0xffffffffu, first || top > 8.f || big > 128.f)) {
               // A row's maximum has grown by more than 2^8, or a scale is above all so far.
               const uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23;   // 2^(x - 127) <= it
-              const float vf0 = __uint_as_float((x < 252u ? 253u - x : 1u) << 23);             // half its inverse, about
+              const float vf0 = __uint_as_float(min(260u - x, 253u) << 23);                    // 2^6 of its inverse, about
               const float vf = first ? vf0 : fminf(vf0, 1.f);
               vinv *= vf;
 #pragma unroll
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
                   for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
                   // (a row that sees none of the first positions sees none of this item's)
-                  m = first ? (m == -INFINITY ? 0.f : m - 7.f) : fmaxf(m - 7.f, 0.f);
+                  m = first ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
                   f[y] = first ? 1.f : ex2(-m);
                   mm[nb][y] += m;
                   l[nb][y] *= f[y];
