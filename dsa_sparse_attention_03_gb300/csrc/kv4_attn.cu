@@ -3,7 +3,8 @@
 // Mathematics.  K[t] = s_g (u - 8) for the codes u of group g of 64 columns, so
 //   q . K[t] = sum_g s_g[t] (sum_d q_d u_d - 8 sum_d q_d),
 // and with weights p_t = 2^(c q.K[t] - m):
-//   sum_t p_t V[t] = sum_t (p_t s_g[t]) u - 8 sum_t (p_t s_g[t])      for the columns of group g.
+//   sum_t p_t V[t] = sum_t (p_t s_g[t]) u - 8 sum_t (p_t s_g[t])      for the columns of group g,
+// the second part taken off after every 32 positions (a product of the weights with ones).
 // The codes go into the products as they are: four bits with zeros around them are the fp16
 // number u 2^-24, and four bits higher up u 2^-20, so a pair of codes becomes a pair of operands
 // by one AND, without a conversion.  (The tensor core cuts the addends of a sum 24 bits or so below the
@@ -28,7 +29,7 @@
 // heads over 8 and 307200 positions 62 us, 5.4 TB/s with the start (3.6 us until the first stage is
 // there), CTAs that get less of HBM than others and end 6 us after the middle one, and the join (3
 // us); twice as many positions take another 50, the copy rate.  32 ragged tokens of up to 32768
-// positions 81 us in pages of 64 (5.2 TB/s), 84.5 in pages of 16, whose copies are 2 KB each.  One
+// positions 81 us in pages of 64 (5.2 TB/s), 85.5 in pages of 16, whose copies are 2 KB each.  One
 // token over 4096 positions 10.8 us: a chain of launch, lengths (0.7), the share's place in the batch
 // (0.8), table and first pages (1.5), two tiles of 32 positions (1 to 2), the warps' sums and parts
 // (1.2), the next launch (0.7) and the join.
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
       const Item& si = sh->item[k % kItems];
       if (ok) it = {si.row0, si.packed, si.first, si.h, si.len, si.stage, si.stages, si.slot};
       const bool last = it.packed == 0;
-      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], sp[GV][NB][4], oo[GV][NB][4][4], vinv = 1.f;
+      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], oo[GV][NB][4][4], vinv = 1.f;
       int see[NB][2];
       const uint32_t qf = smem_u32(qs) + k % kItems * kQBytes + lane * 8;
       if (!last) {
@@ -549,11 +550,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              sp[g][nb][x] = 0.f;
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
               for (int t = 0; t < 4; ++t) oo[g][nb][t][x] = 0.f;
-            }
         int least = see[0][0];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) least = min(least, min(see[nb][0], see[nb][1]));
@@ -694,14 +693,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
                   for (int g = 0; g < GV; ++g)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                      sp[g][nb][y] *= f[y & 1];
+                    for (int y = 0; y < 4; ++y)
 #pragma unroll
                       for (int t = 0; t < 4; ++t) oo[g][nb][t][y] *= f[y & 1];
-                    }
               }
               first = false;
             }
+            float sp[GV][NB][4];       // sums of the weights that go to the groups of V
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -718,7 +716,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                 for (int nb = 0; nb < NB; ++nb) {
                   b0[nb] = transposed(half2_bits(e[t][nb][0] * vs[t][g][0], e[t][nb][1] * vs[t][g][0]));
                   b1[nb] = transposed(half2_bits(e[t][nb][2] * vs[t][g][1], e[t][nb][3] * vs[t][g][1]));
-                  mma_f16(sp[g][nb], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b0[nb], b1[nb]);
+                  if (t == 0)
+                    mma_f16(sp[g][nb], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b0[nb], b1[nb], 0.f, 0.f);
+                  else
+                    mma_f16(sp[g][nb], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b0[nb], b1[nb]);
                 }
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
@@ -732,6 +733,18 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                   }
               }
             }
+            // The 8 less in every code, at once: a sum that grew with it would lose its low bits (one token over 307200
+            // positions in fp16 9.3e-4 off, 3.5e-4 this way at the same time; by a product with -8 before each other
+            // one 3.4e-4, 66 us instead of 62).
+#pragma unroll
+            for (int g = 0; g < GV; ++g)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    oo[g][nb][w][x] = fmaf(sp[g][nb][x & 1], x < 2 ? -0x1p-21f : -0x1p-17f, oo[g][nb][w][x]);
           } else {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(sh->empty[s]));
@@ -783,12 +796,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const float sub = 8.f * sp[g][nb][x];
               float4& y = v[g][w][x];
-              y.x = (oo[g][nb][2 * w][x] * 0x1p24f - sub) * f[x];
-              y.y = (oo[g][nb][2 * w][x + 2] * 0x1p20f - sub) * f[x];
-              y.z = (oo[g][nb][2 * w + 1][x] * 0x1p24f - sub) * f[x];
-              y.w = (oo[g][nb][2 * w + 1][x + 2] * 0x1p20f - sub) * f[x];
+              y.x = oo[g][nb][2 * w][x] * 0x1p24f * f[x];
+              y.y = oo[g][nb][2 * w][x + 2] * 0x1p20f * f[x];
+              y.z = oo[g][nb][2 * w + 1][x] * 0x1p24f * f[x];
+              y.w = oo[g][nb][2 * w + 1][x + 2] * 0x1p20f * f[x];
               if (l[nb][x] == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         // The upper four warps hand theirs to the lower four, lane to lane; these lay down
