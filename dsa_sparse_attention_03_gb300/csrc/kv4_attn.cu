@@ -22,8 +22,8 @@
 //
 // What bounds it.  Per position and K/V head (D_k + D_v) 17 / 32 bytes have to be read: 136 for
 // 128 + 128, at 45 GB/s for an SM one every 5.7 cycles.  The tensor core has little to do
-// (8 to 16 rows), but every code passes through a register: 5 instructions for 8 codes,
-// 18 mma.sync for 16 positions, 245 instructions in all with the softmax.  Dequantised tiles in shared
+// (8 to 16 rows), but every code passes through a register: 5 or 6 instructions for 8
+// codes, 18 mma.sync for 16 positions, 260 instructions in all with the softmax.  Dequantised tiles in shared
 // memory for tcgen05 would cost the same extraction, a store and two reads of 16-bit
 // operands; registers are what mma.sync takes and tcgen05 does not.  Measured: one token of 64
 // heads over 8 and 307200 positions 62 us, 5.4 TB/s with the start (3.6 us until the first stage is
