@@ -275,20 +275,23 @@ template <int D>
 __device__ __noinline__ bool still_open(const TurnArgs& t, float4 xa, float4 xb, HeadLane l, float2 scale) {
   const float x[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
   auto four = [&](const float* v) { return max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))); };
-  float top[2] = {0.f, 0.f};
-  const float e = 2.f * kTurnErr * group_max<D>(l, four(x), four(x + 4), top[0], top[1]);
+  float own[8], top[2] = {0.f, 0.f}, e[2] = {0.f, 0.f};
+  const bool turned = t.k_weight || l.f >= 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float pair = fabsf(x[i]) + fabsf(t.adjacent ? x[i ^ 1] : x[i ^ 4]);
+    own[i] = l.f >= 0 ? 1.42f * kTurnErr * pair : (turned ? kTurnErr * fabsf(x[i]) : 0.f);
+  }
+  group_max<D>(l, four(x), four(x + 4), top[0], top[1]);
+  group_max<D>(l, four(own), four(own + 4), e[0], e[1]);
   bool open = false;
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
     const float inv = inverse(v ? scale.y : scale.x);
-    open |= group_turned(t, v ? l.b : l.a) && open_scale(top[v], e);
-    if (!t.k_weight && l.f < 0) continue;
+    open |= group_turned(t, v ? l.b : l.a) && top[v] > 0.f && open_scale(top[v], e[v]);   // (nothing in it: no scale)
+    if (!turned) continue;
 #pragma unroll
-    for (int i = 4 * v; i < 4 * v + 4; ++i) {
-      const float pair = fabsf(x[i]) + fabsf(t.adjacent ? x[i ^ 1] : x[i ^ 4]);
-      const float own = l.f >= 0 ? 1.42f * kTurnErr * pair : kTurnErr * fabsf(x[i]);
-      open |= fabsf(fmaf(x[i], inv, kCode - code(x[i], inv))) > open_code(own, inv);
-    }
+    for (int i = 4 * v; i < 4 * v + 4; ++i) open |= fabsf(fmaf(x[i], inv, kCode - code(x[i], inv))) > open_code(own[i], inv);
   }
   return open;
 }

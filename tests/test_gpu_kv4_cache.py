@@ -179,6 +179,21 @@ def test_borders_fall_where_exact_arithmetic_puts_them():
     assert a["bits"] == 0 and got.equal(a["want"])
 
 
+@pytest.mark.parametrize("c", [dict(), dict(rot=64), dict(rot=0), dict(adjacent=True), dict(norm=False)])
+def test_keys_with_columns_far_above_the_others(c):
+    # (a few columns 30 to 3000 times the others, a group of zeros, heads of zeros)
+    import torch
+    g = torch.Generator().manual_seed(21)
+    k, v = torch.randn(1500, 4, 128, generator=g), torch.randn(1500, 4, 128, generator=g)
+    k[:, 0, 5] *= 30
+    k[:, 1, 70] *= 300
+    k[:, 2, 100] *= 3000
+    k[:, 3, 64:] = 0
+    k[::3, 3] = 0
+    a = _append([1500], [0], 0, 4, 128, 128, 64, seed=22, x=(k, v), **c)
+    assert a["bits"] == 0 and a["cache"]._keep["pages"].cpu().equal(a["want"])
+
+
 def test_values_that_need_no_turn_are_exact_ties_included():
     # Halves of a scale: ties go to the even code.  Zeros, one value alone, tiny and huge groups.
     import torch
