@@ -508,3 +508,18 @@ def test_values_near_the_end_of_the_range(rows):
     keep = _sample([rows])
     assert bits == 0
     H.check(_few(t, keep), 0.125, out[keep], lse[keep])
+
+
+@pytest.mark.parametrize("B", [31, 32, 33, 65, 290])
+@pytest.mark.parametrize("hq,hkv,most", [(8, 1, 1), (4, 2, 5), (2, 2, 20)])
+def test_many_requests_are_found(B, hq, hkv, most):
+    # Rows that are not their requests' numbers, requests without rows, contexts of nothing to some thousand positions.
+    import random
+    r = random.Random(B * 100 + most)
+    lens = [r.choice([0, 1, 17, 128, 129, r.randint(1, 3000)]) for _ in range(B)]
+    rows = [min(r.randint(0, most), x) if x else r.choice([0, 1]) for x in lens]
+    t = H.make(rows, lens, hq, hkv, 64, 64, 16, seed=B)
+    scale = 0.125
+    out, lse, bits = H.run(t, scale)
+    assert bits == 0
+    H.check(t, scale, out, lse)
