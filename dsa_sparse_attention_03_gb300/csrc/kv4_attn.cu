@@ -18,7 +18,8 @@
 // Softmax in one pass, base 2: the maximum m only has to be near the row's: O and l are rescaled
 // when it has grown by more than 2^8.  For their product with V weights are held times V's scales
 // relative to a power of two that leaves these below 2^7, so that fp16 holds them to 11 bits
-// down to 2^-21 of the largest.
+// down to 2^-21 of the largest.  The power follows the scales as they are, before they are multiplied by it (V
+// may begin with zeros, and what comes next may have any scale), and it only falls.
 //
 // What bounds it.  Per position and K/V head (D_k + D_v) 17 / 32 bytes have to be read: 136 for
 // 128 + 128, at 45 GB/s for an SM one every 5.7 cycles.  The tensor core has little to do
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
       const Item& si = sh->item[k % kItems];
       if (ok) it = {si.row0, si.packed, si.first, si.h, si.len, si.stage, si.stages, si.slot};
       const bool last = it.packed == 0;
-      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], oo[GV][NB][4][4], vinv = 1.f;
+      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], oo[GV][NB][4][4], vinv = 0x1p126f;   // (no scale so far)
       int see[NB][2];
       const uint32_t qf = smem_u32(qs) + k % kItems * kQBytes + lane * 8;
       if (!last) {
@@ -618,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
               for (int g = 0; g < GV; ++g) {
                 const uint32_t w = lds1(ring + s_at + t * kTileScales + (GK + g) * PS * 2);
-                vs[t][g][0] = __uint_as_float(__byte_perm(w, 0, sel_a)) * vinv;
-                vs[t][g][1] = __uint_as_float(__byte_perm(w, 0, sel_b)) * vinv;
+                vs[t][g][0] = __uint_as_float(__byte_perm(w, 0, sel_a));
+                vs[t][g][1] = __uint_as_float(__byte_perm(w, 0, sel_b));
               }
             }
             // V's codes, after which the stage's place is given back: it is loaded again under the rest.
@@ -656,19 +657,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
               for (int g = 0; g < GV; ++g) big = max3(vs[t][g][0], vs[t][g][1], big);
             }
-            if (__any_sync(0xffffffffu, first || top > 8.f || big > 128.f)) {
+            if (__any_sync(0xffffffffu, first || top > 8.f || big * vinv > 128.f)) {
               // A row's maximum has grown by more than 2^8, or a scale is above all so far.
               const uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23;   // 2^(x - 127) <= it
-              const float vf0 = __uint_as_float(min(260u - x, 253u) << 23);                    // 2^6 of its inverse, about
-              const float vf = first ? vf0 : fminf(vf0, 1.f);
-              vinv *= vf;
-#pragma unroll
-              for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int g = 0; g < GV; ++g) {
-                  vs[t][g][0] *= vf;
-                  vs[t][g][1] *= vf;
-                }
+              const float to = fminf(vinv, __uint_as_float(min(260u - x, 253u) << 23));        // 2^6 of its inverse, about
+              // What O is to be multiplied with: to / vinv, or nothing where that is below 2^-126.
+              const float vf = __uint_as_float((uint32_t)max(__float_as_int(to) - __float_as_int(vinv) + (127 << 23), 0));
+              vinv = to;
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 float f[2];
@@ -699,6 +694,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
               }
               first = false;
             }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int g = 0; g < GV; ++g) {
+                vs[t][g][0] *= vinv;
+                vs[t][g][1] *= vinv;
+              }
             float sp[GV][NB][4];       // sums of the weights that go to the groups of V
 #pragma unroll
             for (int t = 0; t < 2; ++t) {

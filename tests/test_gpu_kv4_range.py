@@ -1,0 +1,82 @@
+"""Attention over the 4-bit cache with values far apart, against the definition in 64 bits: cleared places
+before others, groups of columns and positions of very different sizes, the ends of the types' ranges."""
+import math
+
+import pytest
+
+import kv4_harness as H
+
+pytestmark = pytest.mark.gpu
+
+
+def _scale_places(t, factors):
+    """Multiplies V's scales at position x of request b by factors[b][x] (powers of two or 0)."""
+    import torch
+    vs = H.parts(t["pages"], t["dk"], t["dv"], t["ps"])[3]
+    f = torch.ones(vs.shape[0], t["ps"], dtype=torch.float64)
+    for b, fb in enumerate(factors):
+        x = torch.arange(len(fb))
+        f[t["table"][b, x // t["ps"]].long(), x % t["ps"]] = torch.as_tensor(fb, dtype=torch.float64)
+    vs.copy_((vs.double() * f[:, None, None, :]).bfloat16())
+
+
+def _cleared(L, where, before, after):
+    """Factors of L positions: `before` at the first ones or in blocks of two stages out of three, else `after`."""
+    import torch
+    x = torch.arange(L)
+    first = (x // 128) % 3 != 2 if where == "blocks" else x < where
+    return torch.where(first, torch.tensor(before, dtype=torch.float64), torch.tensor(after, dtype=torch.float64))
+
+
+def _rows(t, keep):
+    """The problem's rows `keep` (ascending) alone."""
+    ro = t["row_offsets"].tolist()
+    n = [sum(1 for r in keep if a <= r < b) for a, b in zip(ro, ro[1:])]
+    return dict(t, q=t["q"][keep], row_len=t["row_len"][keep], row_offsets=H.prefix(n))
+
+
+@pytest.mark.parametrize("after", [1.0, 2.0 ** 4, 2.0 ** 10, 2.0 ** 80])
+@pytest.mark.parametrize("where", [32, 128, 300, "blocks"])
+@pytest.mark.parametrize("rows,lens,heads,ps", [
+    ([1] * 24, [900] * 24, (32, 16), 64),                   # items of several stages, each taken whole
+    ([1], [40000], (16, 8), 16),                            # one request cut into the CTAs' shares
+    ([2, 1] * 14, [700, 1100] * 14, (64, 16), 128),         # a few rows each
+    ([4, 1, 3] * 8, [1200, 400, 600] * 8, (32, 16), 32),
+])
+def test_cleared_places_come_first(rows, lens, heads, ps, where, after):
+    # V of the first positions is zero (padded tokens, cleared places): what follows may have any scale.
+    t = H.make(rows, lens, *heads, 64, 64, ps, seed=60)
+    _scale_places(t, [_cleared(L, where, 0.0, after) for L in lens])
+    out, lse, bits = H.run(t, 0.09)
+    assert bits == 0
+    H.check(t, 0.09, out, lse)
+
+
+@pytest.mark.parametrize("before,after", [(2.0 ** -122, 1.0), (2.0 ** -100, 2.0 ** 22), (2.0 ** -100, 2.0 ** 80), (2.0 ** -60, 2.0 ** 66)])
+@pytest.mark.parametrize("rows,lens,dk,dv", [([1] * 24, [900] * 24, 64, 64), ([3, 1] * 10, [900, 1000] * 10, 192, 128)])
+def test_tiny_places_come_first(rows, lens, dk, dv, before, after):
+    t = H.make(rows, lens, 32, 16, dk, dv, 64, seed=61)
+    _scale_places(t, [_cleared(L, 200, before, after) for L in lens])
+    out, lse, bits = H.run(t, 0.1)
+    assert bits == 0
+    H.check(t, 0.1, out, lse)
+
+
+@pytest.mark.parametrize("rows_max", [1, 100, 600])
+@pytest.mark.parametrize("after", [2.0 ** 4, 2.0 ** 80])
+def test_cleared_places_whatever_the_kernel(rows_max, after):
+    # Few rows at a time, widened by the way, widened first.
+    t = H.make([600], [900], 16, 2, 128, 128, 32, seed=62)
+    _scale_places(t, [_cleared(900, 300, 0.0, after)])
+    out, lse, bits = H.run(t, 0.09, rows_max=rows_max)
+    assert bits == 0
+    keep = [0, 1, 130, 255, 256, 400, 599]
+    H.check(_rows(t, keep), 0.09, out[keep], lse[keep])
+
+
+def test_nothing_but_cleared_places():
+    t = H.make([1, 3], [700, 200], 8, 2, 128, 128, 64, seed=63)
+    _scale_places(t, [[0.0] * 700, [0.0] * 200])
+    out, lse, bits = H.run(t, 0.09)
+    assert bits == 0 and not out.any()
+    H.check(t, 0.09, out, lse)
