@@ -8,7 +8,8 @@
 // The codes go into the products as they are: four bits with zeros around them are the fp16
 // number u 2^-24, and four bits higher up u 2^-20, so a pair of codes becomes a pair of operands
 // by one AND, without a conversion.  (The tensor core cuts the addends of a sum 24 bits or so below the
-// largest exponent, which for these operands is 2^-14's whatever the code.  K's codes are shifted up by
+// largest exponent, which for these operands is 2^-14's whatever the code: at 2^-14 of the largest weight
+// times scale for V, less than its weight's own rounding.  K's codes are shifted up by
 // two bits for that: a logit is then off by a tenth, at 1% of the time; lse of one position in
 // fp16 1.2e-6 -> 1.4e-7 of its size.)  K's scales are applied to the logits, V's to the weights,
 // both in fp32.  A query row is scaled by a power of two to fp16's upper range first (every bit
@@ -17,9 +18,10 @@
 //
 // Softmax in one pass, base 2: the maximum m only has to be near the row's: O and l are rescaled
 // when it has grown by more than 2^8.  For their product with V weights are held times V's scales
-// relative to a power of two that leaves these below 2^7, so that fp16 holds them to 11 bits
-// down to 2^-21 of the largest.  The power follows the scales as they are, before they are multiplied by it (V
-// may begin with zeros, and what comes next may have any scale), and it only falls.
+// relative to a power of two for each group of 64 columns that leaves these below 2^7, so that fp16
+// holds them to 11 bits down to 2^-20 of the largest.  (With one power for both groups, one whose scales were 2^-24 of
+// the other's lost bits, and at 2^-32 everything.)  The power follows the scales as they are, before they are multiplied
+// by it (V may begin with zeros, and what comes next may have any scale), and it only falls.
 //
 // What bounds it.  Per position and K/V head (D_k + D_v) 17 / 32 bytes have to be read: 136 for
 // 128 + 128, at 45 GB/s for an SM one every 5.7 cycles.  The tensor core has little to do
@@ -530,7 +532,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
       const Item& si = sh->item[k % kItems];
       if (ok) it = {si.row0, si.packed, si.first, si.h, si.len, si.stage, si.stages, si.slot};
       const bool last = it.packed == 0;
-      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], oo[GV][NB][4][4], vinv = 0x1p126f;   // (no scale so far)
+      float qc[GK][NB][2], factor[NB][2], mm[NB][2], l[NB][2], oo[GV][NB][4][4], vinv[GV];
+#pragma unroll
+      for (int g = 0; g < GV; ++g) vinv[g] = 0x1p126f;   // (no scale so far)
       int see[NB][2];
       const uint32_t qf = smem_u32(qs) + k % kItems * kQBytes + lane * 8;
       if (!last) {
@@ -649,21 +653,27 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                   }
                 }
             }
-            float top = -INFINITY, big = 0.f;
+            float top = -INFINITY, big[GV], most = 0.f;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) top = max3(max3(e[t][nb][0], e[t][nb][1], top), e[t][nb][2], e[t][nb][3]);
 #pragma unroll
-              for (int g = 0; g < GV; ++g) big = max3(vs[t][g][0], vs[t][g][1], big);
+            for (int g = 0; g < GV; ++g) {
+              big[g] = max3(vs[0][g][0], vs[0][g][1], fmaxf(vs[1][g][0], vs[1][g][1]));
+              most = fmaxf(most, big[g] * vinv[g]);
             }
-            if (__any_sync(0xffffffffu, first || top > 8.f || big * vinv > 128.f)) {
+            if (__any_sync(0xffffffffu, first || top > 8.f || most > 128.f)) {
               // A row's maximum has grown by more than 2^8, or a scale is above all so far.
-              const uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23;   // 2^(x - 127) <= it
-              const float to = fminf(vinv, __uint_as_float(min(260u - x, 253u) << 23));        // 2^6 of its inverse, about
-              // What O is to be multiplied with: to / vinv, or nothing where that is below 2^-126.
-              const float vf = __uint_as_float((uint32_t)max(__float_as_int(to) - __float_as_int(vinv) + (127 << 23), 0));
-              vinv = to;
+              float vf[GV];
+#pragma unroll
+              for (int g = 0; g < GV; ++g) {
+                const uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(big[g])) >> 23;   // 2^(x - 127) <= it
+                const float from = vinv[g], to = fminf(from, __uint_as_float(min(260u - x, 253u) << 23));   // 2^6 of its inverse, about
+                // What O is to be multiplied with: to / from, or nothing where that is below 2^-126.
+                vf[g] = __uint_as_float((uint32_t)max(__float_as_int(to) - __float_as_int(from) + (127 << 23), 0));
+                vinv[g] = to;
+              }
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 float f[2];
@@ -677,7 +687,6 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
                   f[y] = first ? 1.f : ex2(-m);
                   mm[nb][y] += m;
                   l[nb][y] *= f[y];
-                  f[y] *= vf;
 #pragma unroll
                   for (int t = 0; t < 2; ++t) {
                     e[t][nb][y] -= m;
@@ -690,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
 #pragma unroll
-                      for (int t = 0; t < 4; ++t) oo[g][nb][t][y] *= f[y & 1];
+                      for (int t = 0; t < 4; ++t) oo[g][nb][t][y] *= f[y & 1] * vf[g];
               }
               first = false;
             }
@@ -698,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int g = 0; g < GV; ++g) {
-                vs[t][g][0] *= vinv;
-                vs[t][g][1] *= vinv;
+                vs[t][g][0] *= vinv[g];
+                vs[t][g][1] *= vinv[g];
               }
             float sp[GV][NB][4];       // sums of the weights that go to the groups of V
 #pragma unroll
@@ -769,7 +778,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
           }
       }
       if (consumers_any(!ok || last)) break;
-      const float back = 1.f / vinv;
+      float back[GV];
+#pragma unroll
+      for (int g = 0; g < GV; ++g) back[g] = __uint_as_float((254u << 23) - __float_as_uint(vinv[g]));   // 1 / vinv
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         // The common maximum and sum of row lane % 8, over the warps lane / 8 and 4 + lane / 8.
@@ -786,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float to = __shfl_sync(0xffffffffu, most, 2 * j + x);
-          f[x] = l[nb][x] != 0.f ? ex2(mm[nb][x] - to) * back : 0.f;
+          f[x] = l[nb][x] != 0.f ? ex2(mm[nb][x] - to) : 0.f;
         }
         const float m = __shfl_sync(0xffffffffu, most, warp), sum = __shfl_sync(0xffffffffu, all, warp);   // the row that this warp writes
         const bool any = sum != 0.f;
@@ -799,10 +810,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               float4& y = v[g][w][x];
-              y.x = oo[g][nb][2 * w][x] * 0x1p24f * f[x];
-              y.y = oo[g][nb][2 * w][x + 2] * 0x1p20f * f[x];
-              y.z = oo[g][nb][2 * w + 1][x] * 0x1p24f * f[x];
-              y.w = oo[g][nb][2 * w + 1][x + 2] * 0x1p20f * f[x];
+              const float fb = f[x] * back[g];
+              y.x = oo[g][nb][2 * w][x] * 0x1p24f * fb;
+              y.y = oo[g][nb][2 * w][x + 2] * 0x1p20f * fb;
+              y.z = oo[g][nb][2 * w + 1][x] * 0x1p24f * fb;
+              y.w = oo[g][nb][2 * w + 1][x + 2] * 0x1p20f * fb;
               if (l[nb][x] == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         // The upper four warps hand theirs to the lower four, lane to lane; these lay down

@@ -113,9 +113,13 @@ DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t
  * which a whole prompt's count half) with the pages widened once into the workspace, where that
  * takes at most 8 GB there.
  *
- * Precision: products with K are exact and summed in fp32; the softmax statistics are
- * fp32; a softmax weight is rounded once, to the operands' type or finer, for its product with
- * V; the output once.  Results do not depend on timing.  Range: |q| below 2^115; sums over
+ * Precision: products with K and V are summed in fp32; the softmax statistics are fp32; a softmax
+ * weight is rounded once for its product with V, to the operands' type; the output once.  With up to 64
+ * packed rows a weight is rounded as its product with V's scale, to fp16: to 11 bits from 2^-20 of the
+ * request's largest scale of those 64 columns on, below that by at most 2^-31 of this scale; what a query holds
+ * below 2^-25 of its row's largest value is dropped; and the tensor cores cut the addends of a sum of 16
+ * products at 2^-16 (K) or 2^-14 (V) of the largest query value, or weight, times scale among them.
+ * Results do not depend on timing.  Range: |q| below 2^115; sums over
  * positions of 2^15 |v| below 2^128 (weights are held as up to 2^15 of them).  What lies at positions
  * that no row of a request sees may be anything.  A scale that some rows of a request see has to
  * be finite (with fp16 queries below 2^16), or any output of that request may be NaN.

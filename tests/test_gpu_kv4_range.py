@@ -80,3 +80,41 @@ def test_nothing_but_cleared_places():
     out, lse, bits = H.run(t, 0.09)
     assert bits == 0 and not out.any()
     H.check(t, 0.09, out, lse)
+
+
+@pytest.mark.parametrize("small", [0, 1])
+@pytest.mark.parametrize("e", [10, 20, 24, 32, 60])
+@pytest.mark.parametrize("rows,lens", [([1], [700]), ([1], [5000]), ([4, 2], [300, 900]), ([100], [300])])
+def test_one_group_of_columns_far_below_the_other(rows, lens, e, small):
+    # (columns of V often differ in size for good; the bound takes each group's own largest scale)
+    t = H.make(rows, lens, 8, 2, 128, 128, 64, seed=64 + e)
+    vs = H.parts(t["pages"], 128, 128, 64)[3]
+    vs[:, :, small] = (vs[:, :, small].float() * 2.0 ** -e).bfloat16()
+    out, lse, bits = H.run(t, 0.09)
+    assert bits == 0
+    H.check(t, 0.09, out, lse)
+    ref, _, bound, _ = H.reference(t, 0.09)
+    assert (ref.abs() > bound)[..., 64 * small:64 * small + 64].float().mean() > 0.5   # (the bound tells a lost group)
+
+
+@pytest.mark.parametrize("at", [0, 200])
+@pytest.mark.parametrize("e", [8, 20])
+def test_one_position_far_above_the_others(e, at):
+    import torch
+    # What the header states: sums over 16 positions are cut 2^-14 of the largest weight times scale in them below, each of
+    # their 17 addends.
+    t = H.make([1, 3], [900, 300], 8, 2, 128, 128, 32, seed=65)
+    _scale_places(t, [[2.0 ** e if x == at else 1.0 for x in range(L)] for L in (900, 300)])
+    out, lse, bits = H.run(t, 0.09)
+    ref, _, bound, _ = H.reference(t, 0.09)
+    most = torch.zeros_like(ref)
+    _, _, ks, vs = H.parts(t["pages"], 128, 128, 32)
+    K, _ = H.values(t["pages"], 128, 128, 32)
+    for r, (b, n) in enumerate(zip([0, 1, 1, 1], t["row_len"].tolist())):
+        x = torch.arange(n)
+        page = t["table"][b, x // 32].long()
+        k = K[page, x % 32].repeat_interleave(4, dim=1)
+        s = vs.double()[page, :, :, x % 32].repeat_interleave(4, dim=1)                     # [n, heads, groups]
+        w = torch.softmax(torch.einsum("hd,nhd->nh", t["q"][r].double(), k) * 0.09, dim=0)
+        most[r] = (w[..., None] * s).amax(dim=0).repeat_interleave(64, dim=1)
+    assert bits == 0 and bool(((out.double() - ref).abs() <= bound + 17 * 2.0 ** -14 * most).all())
