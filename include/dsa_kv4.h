@@ -77,8 +77,8 @@ DSA_API dsa_status dsa_kv4_append(const dsa_kv4_cache* c, const dsa_qk_problem* 
  * aligned) get the values that positions[r] of row r's request holds, in bf16, or in fp16 with
  * flags = DSA_FLAG_FP16 (exact in bf16; rounded once in fp16).  row_offsets [B + 1] are the
  * rows of the cache's B requests; R <= 2^31 - 1.  Skipped rows (as above) are left as they
- * were.  In fp16 a scale has to be below 2^16 (a pool written from fp16 has no larger ones).  For
- * prompts that attend over a cached prefix with dsa_dense_attn.
+ * were.  In fp16 a value has to be at most 65504, which is a scale up to 9216 (what was written from
+ * fp16 without norm and rotation is).  For prompts that attend over a cached prefix with dsa_dense_attn.
  */
 DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t* row_offsets, const int32_t* positions,
                                 int32_t flags, uint16_t* k_out, uint16_t* v_out, void* ws, size_t ws_bytes, void* stream);
@@ -122,7 +122,8 @@ DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t
  * Results do not depend on timing.  Range: |q| below 2^115; sums over
  * positions of 2^15 |v| below 2^128 (weights are held as up to 2^15 of them).  What lies at positions
  * that no row of a request sees may be anything.  A scale that some rows of a request see has to
- * be finite (with fp16 queries below 2^16), or any output of that request may be NaN.
+ * be finite, or any output of that request may be NaN.  With fp16 queries the kernels of more than 64 packed
+ * rows take K and V as dsa_kv4_read gives them in fp16: rounded once, and at most 65504.
  */
 typedef struct dsa_kv4_problem {
   int32_t R, H_q, L_max, rows_max;

@@ -1,0 +1,54 @@
+"""The 4-bit cache's writer and reader at the ends of their ranges (dsa_kv4_append, dsa_kv4_read)."""
+import math
+
+import pytest
+
+import kv4_harness as H
+from test_gpu_kv4_cache import _append
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (192, 128)])
+def test_fp16_values_are_rounded_once(dk, dv):
+    # Every scale from 2^-44 to the largest whose sevenfold fp16 holds, with every code.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    ps, hkv = 64, 2
+    scales = torch.tensor([m * 2.0 ** (e - 3) for e in range(-44, 14) for m in range(8, 16)], dtype=torch.float64)
+    scales = torch.cat([scales[scales * 7 <= 65504], torch.zeros(1, dtype=torch.float64)])
+    n = -(-len(scales) // ps)
+    t = H.make([0], [n * ps], hkv, hkv, dk, dv, ps, "fp16", seed=70, spare=0)
+    g = torch.Generator().manual_seed(71)
+    kc, vc, ks, vs = H.parts(t["pages"], dk, dv, ps)
+    at = torch.arange(n * ps) % len(scales)
+    for codes, s in ((kc, ks), (vc, vs)):
+        lo, hi = (torch.randint(1, 16, codes.shape, generator=g, dtype=torch.uint8) for _ in range(2))
+        codes.copy_(lo | hi << 4)
+        s.copy_(scales[at].reshape(n, 1, 1, ps).bfloat16().expand(s.shape))
+    kc[..., :8] = torch.tensor([0x21, 0x43, 0x65, 0x87, 0xA9, 0xCB, 0xED, 0x1F], dtype=torch.uint8)
+    cache = dsa.KV4Cache.from_tensors(pages=t["pages"].cuda(), table=t["table"].cuda(), page_size=ps, D_k=dk, D_v=dv)
+    pos = torch.arange(n * ps, dtype=torch.int32)
+    ko = torch.zeros(n * ps, hkv, dk, dtype=torch.float16, device="cuda")
+    vo = torch.zeros(n * ps, hkv, dv, dtype=torch.float16, device="cuda")
+    ws = dsa.alloc_kv4_workspace()
+    dsa.dsa_kv4_read(cache, H.prefix([n * ps]).cuda(), pos.cuda(), ko, vo, ws)
+    assert dsa.dsa_read_device_status(ws) == 0
+    K, V = H.values(t["pages"], dk, dv, ps)
+    page = t["table"][0, pos.long() // ps].long()
+    for got, want in ((ko, K), (vo, V)):
+        want = want[page, pos.long() % ps].half()        # (eight significant bits: one rounding)
+        assert bool(want.isfinite().all()) and got.cpu().equal(want)
+
+
+def test_fp16_appended_and_read_back_in_the_smallest_steps():
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    g = torch.Generator().manual_seed(72)
+    x = (torch.randint(-40, 41, (64, 2, 64), generator=g).double() * 2.0 ** -24).half()
+    x[:, :, 0] = 5 * 2.0 ** -24
+    a = _append([64], [0], 0, 2, 64, 64, 16, "fp16", rot=0, norm=False, x=(x, x.flip(2)))
+    assert a["cache"]._keep["pages"].cpu().equal(a["want"])
+    ko, vo = (torch.zeros(64, 2, 64, dtype=torch.float16, device="cuda") for _ in range(2))
+    dsa.dsa_kv4_read(a["cache"], a["ro"].cuda(), a["pos"].cuda(), ko, vo, a["ws"])
+    assert ko.cpu().equal(H.held(x).half()) and vo.cpu().equal(H.held(x.flip(2)).half())

@@ -118,3 +118,32 @@ def test_one_position_far_above_the_others(e, at):
         w = torch.softmax(torch.einsum("hd,nhd->nh", t["q"][r].double(), k) * 0.09, dim=0)
         most[r] = (w[..., None] * s).amax(dim=0).repeat_interleave(64, dim=1)
     assert bits == 0 and bool(((out.double() - ref).abs() <= bound + 17 * 2.0 ** -14 * most).all())
+
+
+@pytest.mark.parametrize("rows", [1, 150, 600])
+def test_fp16_keys_and_values_of_tiny_scales(rows, monkeypatch):
+    # The kernels in tiles take K and V as dsa_kv4_read gives them in fp16, rounded once; the other one takes them as they are.
+    import torch
+    t = H.make([rows], [700], 16, 2, 64, 64, 64, "fp16", seed=67)
+    _, _, ks, _ = H.parts(t["pages"], 64, 64, 64)
+    ks.copy_((ks.float() * 2.0 ** -21).bfloat16())             # scales of about 2^-22.5
+    t["q"] = (t["q"].float() * 2.0 ** 11).half()
+    if rows > 1:
+        plain = H.values
+        monkeypatch.setattr(H, "values", lambda *a: [x.half().double() for x in plain(*a)])
+    out, lse, bits = H.run(t, 2.0 ** 7)
+    keep = [r for r in (0, 1, 70, 149, 300, 599) if r < rows]
+    assert bits == 0
+    H.check(_rows(t, keep), 2.0 ** 7, out[keep], lse[keep])
+
+
+@pytest.mark.parametrize("rows", [1, 150, 600])
+def test_fp16_output_of_tiny_values(rows):
+    # All codes 15 and one scale, 1.125 * 2^-22: 31.5 steps of fp16's subnormals, 32 as the values are rounded once.
+    import torch
+    t = H.make([rows], [700], 16, 2, 64, 64, 64, "fp16", seed=68)
+    _, vc, _, vs = H.parts(t["pages"], 64, 64, 64)
+    vc.fill_(0xFF)
+    vs.fill_(1.125 * 2.0 ** -22)
+    out, _, bits = H.run(t, 0.125)
+    assert bits == 0 and bool(((out.double() / 2.0 ** -24 - 31.5).abs() <= 1.0).all())
