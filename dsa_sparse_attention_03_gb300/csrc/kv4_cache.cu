@@ -112,6 +112,9 @@ __device__ __forceinline__ bool open_scale(float top, float e) {
   const float m = top * (1.f / 7.f), border = __uint_as_float((__float_as_uint(m) & ~0xfffffu) | 0x80000u);
   return fabsf(m - border) <= fmaf(m, 0x1p-22f, e * (1.f / 7.f));   // (2^-22: the product's own rounding)
 }
+// A bound of the errors of a head's values, of which `all` is the largest.  A pair's magnitudes before the rotation add up
+// to at most twice the larger one after it.  No bound where a value is NaN: the other groups' are looked at one by one.
+__device__ __forceinline__ float head_error(float all) { return fminf(2.f * kTurnErr * all, INFINITY); }
 // A quotient nearer to a half than that may be rounded wrongly (2^-18: its own and the inverse's
 // roundings, of at most 7.5, and the bound's).
 __device__ __forceinline__ float open_code(float e, float inv) { return 0.5f - 0x1p-18f - e * inv; }
@@ -180,7 +183,7 @@ __device__ __noinline__ Held hold_exactly(const TurnArgs& t, const float2* cs, c
   float top[2] = {0.f, 0.f}, scale[2];
   const float all = group_max<D>(l, four(y), four(y + 4), top[0], top[1]);
   const bool exact = !t.k_weight && t.rot == 0;
-  const float e = exact ? 0.f : 2.f * kTurnErr * all;
+  const float e = exact ? 0.f : head_error(all);
   double most[2] = {0.0, 0.0}, most_of[2] = {0.0, 0.0};
   bool open[2];
 #pragma unroll
@@ -242,10 +245,9 @@ __device__ __forceinline__ bool hold_key(const TurnArgs& t, const float* x, cons
   auto four = [&](const float* v) { return max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))); };
   float top[2] = {0.f, 0.f};
   const float all = group_max<D>(l, four(x), four(x + 4), top[0], top[1]);
-  // A pair's magnitudes before the rotation add up to at most twice the larger one after it.  Columns that
-  // are neither normed nor rotated come as they are.
+  // (columns that are neither normed nor rotated come as they are)
   const bool exact = !t.k_weight && t.rot == 0, turned = t.k_weight || l.f >= 0;
-  const float e = exact ? 0.f : 2.f * kTurnErr * all;
+  const float e = exact ? 0.f : head_error(all);
   bool open = false;
 #pragma unroll
   for (int v = 0; v < 2; ++v) {

@@ -52,3 +52,22 @@ def test_fp16_appended_and_read_back_in_the_smallest_steps():
     ko, vo = (torch.zeros(64, 2, 64, dtype=torch.float16, device="cuda") for _ in range(2))
     dsa.dsa_kv4_read(a["cache"], a["ro"].cuda(), a["pos"].cuda(), ko, vo, a["ws"])
     assert ko.cpu().equal(H.held(x).half()) and vo.cpu().equal(H.held(x.flip(2)).half())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("c", [dict(), dict(adjacent=True)])
+def test_neighbours_of_a_group_that_is_not_finite(bad, c):
+    # The head's other group is rotated: its borders fall where exact arithmetic puts them all the same.
+    import torch
+    g = torch.Generator().manual_seed(73)
+    k, v = (torch.randn(8200, 8, 128, generator=g).bfloat16() for _ in range(2))
+    k[:, :, 100] = bad
+    a = _append([8200], [0], 0, 8, 128, 128, 64, rot=64, norm=False, x=(k, v), **c)
+    assert a["bits"] == 0
+    page, at = a["table"][0, a["pos"].long() // 64].long(), a["pos"].long() % 64
+    got, want = (H.parts(x, 128, 128, 64) for x in (a["cache"]._keep["pages"].cpu(), a["want"]))
+    for i in (0, 2):                                     # codes and scales of K's first group
+        assert bool((got[i][page, :, 0, at] == want[i][page, :, 0, at]).all())
+    for i in (1, 3):
+        assert got[i][page, :, :, at].equal(want[i][page, :, :, at])
+    assert bool(got[2][page, :, 1, at].isnan().all())
