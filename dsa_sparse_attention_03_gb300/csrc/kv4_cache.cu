@@ -107,9 +107,10 @@ struct Held {
   float scale[2];
 };
 
-// Whether fp32 leaves a scale open: the border above its four bits lies within the errors.
+// Whether fp32 leaves a scale open: the border above its four bits lies within the errors.  Below 2^-126 it is the one from which
+// on a scale is 2^-126: 31 / 32 of that, 0x7c0000.
 __device__ __forceinline__ bool open_scale(float top, float e) {
-  const float m = top * (1.f / 7.f), border = __uint_as_float((__float_as_uint(m) & ~0xfffffu) | 0x80000u);
+  const float m = top * (1.f / 7.f), border = __uint_as_float(max((__float_as_uint(m) & ~0xfffffu) | 0x80000u, 0x7c0000u));
   return fabsf(m - border) <= fmaf(m, 0x1p-22f, e * (1.f / 7.f));   // (2^-22: the product's own rounding)
 }
 // A bound of the errors of a head's values, of which `all` is the largest.  A pair's magnitudes before the rotation add up

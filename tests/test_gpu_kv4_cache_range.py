@@ -71,3 +71,27 @@ def test_neighbours_of_a_group_that_is_not_finite(bad, c):
     for i in (1, 3):
         assert got[i][page, :, :, at].equal(want[i][page, :, :, at])
     assert bool(got[2][page, :, 1, at].isnan().all())
+
+
+def test_border_of_the_smallest_scale():
+    # One rotated pair to a key, its larger column next to 7 * 31 / 32 * 2^-126, where a scale of 2^-126 begins: those within
+    # 2^-22 of it out of forty million, on either side.
+    import numpy as np
+    import torch
+    rng = np.random.default_rng(74)
+    border, keep = 7 * 31 / 32 * 2.0 ** -126, []
+    for _ in range(20):
+        u, v = (torch.from_numpy(rng.uniform(-1, 1, 2_000_000) * 2.0 ** -123).bfloat16() for _ in range(2))
+        pos = rng.integers(0, 1 << 15, 2_000_000)
+        a, b = u.double().numpy(), v.double().numpy()
+        c, s = np.cos(pos.astype(np.float64)), np.sin(pos.astype(np.float64))
+        top = np.maximum(np.abs(a * c - b * s), np.abs(b * c + a * s))
+        at = np.nonzero(np.abs(top / border - 1) < 2.0 ** -22)[0]
+        keep += [(u[i].item(), v[i].item(), int(pos[i])) for i in at]
+    n = len(keep)
+    assert n >= 20
+    k = torch.zeros(n, 1, 64, dtype=torch.bfloat16)
+    k[:, 0, 0], k[:, 0, 32] = (torch.tensor([x[i] for x in keep]).bfloat16() for i in (0, 1))
+    # (each key at its own position: a request to a key)
+    a = _append([1] * n, [x[2] for x in keep], 0, 1, 64, 64, 128, norm=False, x=(k, k))
+    assert a["bits"] == 0 and a["cache"]._keep["pages"].cpu().equal(a["want"])
