@@ -158,7 +158,8 @@ __device__ __noinline__ Held hold_exactly(const TurnArgs& t, const float2* cs, c
   unpack4<F16>(live ? load4(x, l.b) : make_uint2(0, 0), y + 4);
   double r = 1.0;
   if (t.k_weight) {
-    // (squares of 11 bits are exact in fp32, and so is what each sum is off by: low holds these)
+    // (squares of 11 bits are exact in fp32, or below 2^-126 off by less than 2^-50 of the mean in its range, and so is
+    // what each sum is off by: low holds these)
     float high = 0.f, low = 0.f;
     auto add = [&](float x) {
       const float sum = high + x, part = sum - high;
@@ -174,7 +175,7 @@ __device__ __noinline__ Held hold_exactly(const TurnArgs& t, const float2* cs, c
       add(x);
     }
     const double s = fma((double)high + (double)low, 1.0 / D, (double)t.eps);   // (D = 192: 1 / D is off by 2^-54 of it)
-    // s r^2 = 1 - e: r / sqrt(1 - e), and e is below 2^-21.
+    // s r^2 = 1 - e: r / sqrt(1 - e) by the binomial series, 1 + e / 2 + 3 e^2 / 8, and e is below 2^-21.
     r = (double)rsqrtf((float)s);
     const double e = fma(-s * r, r, 1.0);
     r = fma(r * e, fma(0.375, e, 0.5), r);

@@ -20,8 +20,8 @@
  * 4.25 bits a value, each off by at most half a scale.  A scale of four significant bits
  * times a code of four is exact in bf16 (and in fp16 in its range), so the values that
  * the cache stands for can be multiplied by the tensor cores without another rounding.
- * Scales and codes are those of exact arithmetic: where fp32 cannot tell on which side of
- * a border a normed and rotated key lies, it is computed again in fp64.  A group that
+ * Scales and codes are those of exact arithmetic, in dsa_rope.h's range: where fp32 cannot tell on which
+ * side of a border a normed and rotated key lies, it is computed again in fp64.  A group that
  * holds a value that is not finite has no finite values afterwards.
  */
 #ifndef DSA_KV4_H

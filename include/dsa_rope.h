@@ -16,7 +16,9 @@
  *
  * Precision: sums, norms and the rotation in fp32, one rounding at the end, to the
  * operands' type.  The angle is reduced exactly: inv_freq is held as a 64-bit fraction of
- * a turn, so a position of 10^6 is rotated as exactly as the first one.
+ * a turn, so a position of 10^6 is rotated as exactly as the first one.  Range: a normed head's
+ * mean x^2 + eps from 2^-100 to 2^119 (outside, fp32 does not hold the sum of squares, and outputs may be 0 or
+ * not finite), and results that the operands' type holds.
  *
  * A row of a negative position is skipped: its outputs are left as they were (padded
  * batches).  A value that is not finite reaches its own head's outputs alone.

@@ -95,3 +95,27 @@ def test_border_of_the_smallest_scale():
     # (each key at its own position: a request to a key)
     a = _append([1] * n, [x[2] for x in keep], 0, 1, 64, 64, 128, norm=False, x=(k, k))
     assert a["bits"] == 0 and a["cache"]._keep["pages"].cpu().equal(a["want"])
+
+
+@pytest.mark.parametrize("e,eps", [(-50, 0.0), (-40, 2.0 ** -90), (59, 0.0), (59, 1e-6)])
+def test_ends_of_the_norms_range(e, eps):
+    # Keys whose mean square is 2^-100 or 2^118: the bytes are exact arithmetic's there too, and the rotated rows within
+    # their bound.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    g = torch.Generator().manual_seed(75)
+    k, v = torch.randn(600, 4, 128, generator=g), torch.randn(600, 4, 128, generator=g)
+    k *= 2.0 ** e / (k * k).mean(dim=-1, keepdim=True).sqrt() * 1.01
+    a = _append([600], [100], 0, 4, 128, 128, 64, x=(k, v), seed=76)
+    a["cache"]._keep["pages"].copy_(a["before"])
+    prob = a["prob"].set(eps=eps)
+    dsa.dsa_kv4_append(a["cache"], prob, None, a["ws"])
+    weight = prob._keep["k_weight"].cpu()
+    y, size = H.turned(a["k"].cpu(), weight, a["pos"], a["freq"], eps=eps)
+    want = a["before"].clone()
+    for r, p in enumerate(a["pos"].tolist()):
+        H.put(want, int(a["table"][0, p // 64]), p % 64, y[r], a["v"][r].cpu().double(), 128, 128, 64)
+    assert dsa.dsa_read_device_status(a["ws"]) == 0 and a["cache"]._keep["pages"].cpu().equal(want)
+    out = torch.zeros(600, 4, 128, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_qk_norm_rope(prob, None, out)
+    assert bool(((out.cpu().double() - y).abs() <= H.turned_bound(y, size, torch.bfloat16)).all())
