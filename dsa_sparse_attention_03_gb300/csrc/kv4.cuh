@@ -70,7 +70,7 @@ struct Kv4Tile {
 // copy pays.  In us, widened by the way and first: a chunk behind 10240 positions of 64 heads over 8, 2048
 // packed rows 97 and 91, 4096 166 and 139, 16384 518 and 405; whole prompts of one K/V head to a query head, 2048
 // tokens (ragged, 192 wide) 285 and 320, 4096 72 and 70, 8192 135 and 114; eight of 1024 tokens and four query heads
-// 74 and 85.
+// 74 and 85.  A compromise: at 2048 rows it pays behind a context and costs for whole prompts, and does not for one of 4096.
 constexpr int kCopyRows = 2304;
 constexpr size_t kCopyBytes = size_t(1) << 33;
 dsa_dense_problem kv4_dense(const dsa_kv4_cache& c, const dsa_kv4_problem& p);

@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) kv4_attn_kernel(con
   pdl_wait();      // (the inputs may only just be written; the status block is cleared)
   pdl_trigger();
   // Units (an item's cost, then its stages, at least one) of all requests: each warp adds up those of a run.  Up to
-  // 32 requests are the loading warp's lanes.
+  // 32 requests are the loading warp's lanes (0.2 to 0.4 us less than by all warps: 32 single tokens over 4096 positions
+  // 40.0 and 40.4; 33 41.2, 64 63.6, 256 204).
   const int per = (a.c.B + kWarps) / (kWarps + 1);
   const bool few = a.c.B <= 32;
   bool bad = false;

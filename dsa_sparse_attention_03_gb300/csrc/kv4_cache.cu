@@ -313,8 +313,10 @@ __device__ __forceinline__ void put_key(const CacheArgs& c, uint8_t* to, int pla
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Few rows: the status block is not cleared by a launch before, but set by one more CTA, which looks every row's
-// page up for itself (32 tokens appended and read back 8.1 -> 7.1 us, called from the host 15.5 -> 11.9; 498 rows
-// read 2.8 -> 2.3 and 9.0 -> 7.3).
+// page up for itself.  us in a graph, by a launch before and by that CTA (called from the host: a launch less, 1.4 us for
+// reads): append of 32 rows 5.1 and 3.8, of 512 requests' tokens 10.1 and 9.7, of 1024 14.4 and 13.5, of 2048 17.1
+// and 21.9; read of 32 rows 3.2 and 2.7, of 512 rows of eight requests 3.4 and 2.9, of 512 requests 3.4 and 4.1 (from the
+// host 7.3 and 6.0), of 1024 4.2 and 7.4.
 constexpr int kOwnRows = 512;
 __device__ __forceinline__ void set_status(const CacheArgs& c, int R, const int32_t* row_offsets, const int32_t* positions,
                                            uint32_t* status) {

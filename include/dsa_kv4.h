@@ -111,7 +111,13 @@ DSA_API dsa_status dsa_kv4_read(const dsa_kv4_cache* c, int32_t R, const int32_t
  * Kernels, by the packed rows of a request, rows_max * G: up to 64 a few rows at a time with the
  * codes as they are, more in tiles of 128 whose K and V are widened to 16 bits, from 2304 on (of
  * which a whole prompt's count half) with the pages widened once into the workspace, where that
- * takes at most 8 GB there.
+ * takes at most 8 GB there: B * L_max positions, whatever the requests' own lengths.  Who has no room for that
+ * declares rows_max below 2304 / G (a 2048-row chunk over 10240 positions of 64 heads over 8 then takes 518 us
+ * instead of 405).
+ * One kernel serves a whole call, so a long chunk and other requests' single tokens are better two calls (31 tokens of up to
+ * 32768 positions beside a 2048-row chunk over 10240: 1317 us in one call, 613 in two, 518 where the chunk's call
+ * has a cache of its own rows of the table): with the tokens' T rows first, one call with R = T and
+ * min(row_offsets, T), one with max(row_offsets, T) and the rows' own L_max and rows_max.
  *
  * Precision: products with K and V are summed in fp32; the softmax statistics are fp32; a softmax
  * weight is rounded once for its product with V, to the operands' type; the output once.  With up to 64

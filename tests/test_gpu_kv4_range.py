@@ -147,3 +147,42 @@ def test_fp16_output_of_tiny_values(rows):
     vs.fill_(1.125 * 2.0 ** -22)
     out, _, bits = H.run(t, 0.125)
     assert bits == 0 and bool(((out.double() / 2.0 ** -24 - 31.5).abs() <= 1.0).all())
+
+
+def test_one_batch_in_two_calls():
+    # Single tokens and a long chunk, as the header advises: the tokens' call ends behind their rows, the chunk's leaves them alone.
+    import torch
+    import dsa_sparse_attention_03_gb300 as dsa
+    rows, lens, T = [1, 1, 0, 1, 400], [700, 30, 5, 1500, 900], 3
+    t = H.make(rows, lens, 16, 2, 128, 128, 64, seed=77)
+    prob = H.problem(t, 0.09)
+    q, ro, rl = (prob._keep[x] for x in ("q", "row_offsets", "row_len"))
+    out = torch.full((403, 16, 128), 77.0, dtype=torch.bfloat16, device="cuda")
+    calls = (dict(q=q[:T], row_offsets=ro.clamp(max=T), row_len=rl[:T]),
+             dict(q=q, row_offsets=ro.clamp(min=T), row_len=rl, L_max=900))
+    for part, kw in zip((out[:T], out), calls):
+        p = dsa.KV4Problem.from_tensors(cache=prob._keep_cache, softmax_scale=0.09, **kw)
+        ws = dsa.alloc_kv4_workspace(p)
+        before = out.clone()
+        dsa.dsa_kv4_attn(p, part, None, ws)
+        # (the chunk's L_max is below a token's length: rows outside row_offsets are not looked at)
+        assert dsa.dsa_read_device_status(ws) == 0
+    assert out[:T].equal(before[:T])
+    keep = [0, 1, 2, 3, 130, 258, 402]
+    H.check(_rows(t, keep), 0.09, out.cpu()[keep], None)
+
+
+def test_no_copy_where_few_rows_are_declared():
+    import dsa_sparse_attention_03_gb300 as dsa
+    t = H.make([600], [900], 16, 2, 128, 128, 32, seed=78)
+    sizes = [dsa.dsa_kv4_workspace_size(H.problem(t, 0.09, rows_max=n)) for n in (600, 2304 // 8 - 1)]
+    assert sizes[0] >= 900 * 2 * 256 * 2 and sizes[1] < sizes[0] - 900 * 2 * 256 * 2 // 2
+
+
+@pytest.mark.parametrize("rows", [1, 200, 600])
+@pytest.mark.parametrize("L_max", [0, 300])
+def test_rows_that_see_nothing_at_all(rows, L_max):
+    t = H.make([rows, 1], [300, 40], 16, 2, 64, 64, 16, seed=79, row_len=[0] * (rows + 1))
+    t["table"][:] = -1
+    out, lse, bits = H.run(t, 0.1, L_max=L_max)
+    assert bits == 0 and not out.any() and bool((lse == -math.inf).all())
