@@ -30,10 +30,10 @@
 // memory for tcgen05 would cost the same extraction, a store and two reads of 16-bit
 // operands; registers are what mma.sync takes and tcgen05 does not.  Measured: one token of 64
 // heads over 8 and 307200 positions 62 us, 5.4 TB/s with the start (3.6 us until the first stage is
-// there), CTAs that get less of HBM than others and end 6 us after the middle one, and the join (3
-// us); twice as many positions take another 50, the copy rate.  32 ragged tokens of up to 32768
-// positions 81 us in pages of 64 (5.2 TB/s), 85.5 in pages of 16, whose copies are 2 KB each.  One
-// token over 4096 positions 10.8 us: a chain of launch, lengths (0.7), the share's place in the batch
+// there), CTAs that get less of HBM than others and end 6 us after the middle one, and the join with the next
+// launch (4.5 us); twice as many positions take another 50, the copy rate.  32 ragged tokens of up to 32768
+// positions 81 us in pages of 64 (5.2 TB/s), 85.3 in pages of 16, whose copies are 2 KB each.  One
+// token over 4096 positions 10.6 us: a chain of launch, lengths (0.7), the share's place in the batch
 // (0.8), table and first pages (1.5), two tiles of 32 positions (1 to 2), the warps' sums and parts
 // (1.2), the next launch (0.7) and the join.
 //

@@ -20,9 +20,9 @@
 // are exact in bf16 (kv4_widen.cuh).
 //
 // Both move each byte once.  Measured: 9601 rows of 8 + 8 heads of 128 appended in 32 us (1.6 TB/s:
-// 22 million warp instructions, half of the issue slots; the quantising of keys, 225 instructions
-// for two heads, is most of it; 5 us are the last heads computed again), a prefix of 10240 positions read in 13 us (4.1 TB/s; a wave of CTAs
-// that look up, load and write in step), 8000 positions of 64 heads of 192 + 128 in 71 us
+// 22.6 million warp instructions, 62% of the issue slots; the quantising of keys, some 230 instructions
+// for two heads, is most of it; 5 us are the last heads computed again), a prefix of 10240 positions read in 12.8 us
+// (4.1 TB/s, in fp16 as well; a wave of CTAs that look up, load and write in step), 8000 positions of 64 heads of 192 + 128 in 71 us
 // (5.9 TB/s).  Prefetching the rows into L2 at the start gained 1 us.
 #include "kv4_widen.cuh"
 #include "rope.cuh"

@@ -16,8 +16,8 @@
 // the pages once into the workspace and the kernel reads that (a 2048-row chunk over 10240
 // positions 518 -> 405 us, 14 of them the copy).
 //
-// A scale has 4 significant bits, so code * scale is exact in bf16 (in fp16 within its range) and the
-// products are those of the values that the cache stands for.
+// A scale has 4 significant bits, so code * scale is exact in bf16 (in fp16 from a scale of 2^-21 on, rounded once
+// below) and the products are those of the values that the cache stands for.
 #include "dense_kernel.cuh"
 
 namespace dsa {

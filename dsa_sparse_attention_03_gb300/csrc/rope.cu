@@ -10,7 +10,7 @@
 // rotation needs no exchange and the norm three to five shuffles.
 //
 // Measured: 9601 rows of 64 + 8 heads of 128 out of a fused projection 62.5 us, 5.7 TB/s (83% of the
-// copy rate; 61% of the issue slots are taken); one row 2.3 us in a graph.
+// copy rate; 67% of the issue slots are taken); one row 2.3 us in a graph.
 #include "rope.cuh"
 
 namespace dsa {
